@@ -19,8 +19,12 @@
  *   - `stream` is a cudaStream_t passed as void*; 0 is the legacy default stream.
  *     Every call only enqueues work on it and returns; nothing synchronises except
  *     kv_cache_check_error and kv_cache_profile_read.
- *   - Dtypes: PKV_F16 / PKV_BF16 / PKV_FP8_E4M3.  q, k, v and out are in the
- *     cache's model dtype (fp16 or bf16); the pool is in its KV dtype.
+ *   - Dtypes: PKV_F16 / PKV_BF16 / PKV_FP8_E4M3 / PKV_INT4.  q, k, v and out are in the
+ *     cache's model dtype (fp16 or bf16); the pool is in its KV dtype.  PKV_INT4 caches hold 4-bit
+ *     codes with a step and an offset per (token, K|V, head) row (see paged_kv_append); they are
+ *     written by the appends and the packed prefill, read by the decode calls without a shared
+ *     prefix, by paged_kv_gather and paged_kv_evict, and moved by block copy and swap.  The cascade
+ *     decode and the prefill over a cached prefix return PKV_EUNSUPPORTED for them.
  *   - Return value: PKV_OK or a negative pkv_status; pkv_last_error() gives a
  *     message for the calling thread's last failure.  Host-side validation fails
  *     before anything is enqueued.  Data that only the device sees (block ids,
@@ -41,7 +45,7 @@ extern "C" {
 
 typedef struct pkv_cache *pkv_cache_t; /* opaque; created by kv_cache_create */
 
-typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
+typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2, PKV_INT4 = 3 } pkv_dtype;
 
 typedef enum {
     PKV_OK = 0,
@@ -62,10 +66,13 @@ typedef enum {
 /* Create a cache: cudaMalloc a pool of num_blocks blocks, each holding K and V of
  * block_size tokens x num_kv_heads heads x head_dim, in kv_dtype (zero-filled).
  * model_dtype is the dtype of q/k/v/out used with this cache; it must equal
- * kv_dtype unless kv_dtype is PKV_FP8_E4M3.  The pool is the "flat device pool of
+ * kv_dtype unless kv_dtype is PKV_FP8_E4M3 or PKV_INT4.  The pool is the "flat device pool of
  * equal blocks" of 2kiu.com section 2.2 / discosf.com section 2.1.  Pool layout
  * (see kv_cache_view): [num_blocks][2 = K,V][num_kv_heads][block_size][head_dim],
- * so one (block, K|V, head) tile is block_size*head_dim contiguous elements.
+ * so one (block, K|V, head) tile is block_size*head_dim contiguous elements.  PKV_INT4:
+ * [num_blocks][num_kv_heads] runs of block_size * (head_dim + 8) bytes, each K codes
+ * [block_size][head_dim / 2], V codes, K (step, offset) [block_size][2], V (step, offset) in the
+ * model dtype; element i of a row is nibble i, the low one of byte i / 2 for even i.
  * On failure *out is untouched. */
 int kv_cache_create(int64_t num_blocks, int block_size, int num_kv_heads, int head_dim, pkv_dtype kv_dtype,
                     pkv_dtype model_dtype, pkv_cache_t *out);
@@ -80,13 +87,16 @@ int kv_cache_destroy(pkv_cache_t cache);
 int kv_cache_set_scales(pkv_cache_t cache, const float *k_scale, const float *v_scale, void *stream);
 
 /* Describe the pool for tests and initialisation: *base = device address of the pool,
- * strides_elems = element strides of the (block, K|V, head, offset, dim) axes,
+ * strides_elems = element strides of the (block, K|V, head, offset, dim) axes (PKV_INT4: of the
+ * 4-bit codes, two elements a byte),
  * *num_bytes = pool size in bytes.  The library keeps ownership. */
 int kv_cache_view(pkv_cache_t cache, void **base, int64_t strides_elems[5], int64_t *num_bytes);
 
 /* Pre-size the decode split-K workspace for up to max_seqs x max_q_heads rows and tables
  * of max_blocks_per_seq entries, so that later decode calls allocate nothing (a batch larger
- * than one launch takes needs only one launch's rows: the launches share the workspace). */
+ * than one launch takes needs only one launch's rows: the launches share the workspace).  PKV_INT4
+ * caches keep a workspace per stream (see paged_decode_attention_mass): the reserved one goes to the
+ * first stream or capture that needs one; reserve once per stream. */
 int kv_cache_reserve(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq);
 
 /* Synchronise the device, return the device error word's bits in *device_code and clear
@@ -119,11 +129,23 @@ int paged_slot_mapping(const int32_t *block_tables, int num_rows, int max_blocks
  * step 2): for each token j with slot = slot_mapping[j] >= 0, write k[j] and v[j]
  * ([num_tokens][num_kv_heads][head_dim], model dtype) into block slot / block_size at
  * offset slot % block_size.  fp16/bf16 caches store the bits unchanged; FP8 caches store
- * E4M3(fp32(x) / scale[head]) (see kv_cache_set_scales).  Negative slots are padding and
+ * E4M3(fp32(x) / scale[head]) (see kv_cache_set_scales).  PKV_INT4 caches store, for each row x of
+ * head_dim elements (one token's K or V of one head), the offset z = min x, the step
+ * s = round((max x - min x) / 15) (fp32 division, rounded to the model dtype, 0 below 2^-126) and the
+ * codes min(15, rint((x - z) / s)) (fp32 subtraction and division, ties to even; 0 where s = 0);
+ * element i reads as s * code_i + z.  A row that holds a NaN or an infinity, or whose range
+ * overflows fp32, reads as NaN.  Negative slots are padding and
  * skipped; slots >= num_blocks*block_size are skipped and set PKV_DEVERR_SLOT.  Two
  * tokens with the same slot in one call: which one lands is unspecified. */
 int paged_kv_append(pkv_cache_t cache, const void *k, const void *v, const int64_t *slot_mapping,
                     int64_t num_tokens, void *stream);
+
+/* Rows read back: for each token j, k[j] and v[j] ([num_tokens][num_kv_heads][head_dim], model
+ * dtype) := K and V at slot_mapping[j]: the bits of a 16-bit cache, code * scale[head] of an FP8
+ * cache, step * code + offset of a PKV_INT4 cache, rounded once to the model dtype.  A negative slot
+ * gives zeros; one >= num_blocks*block_size gives zeros and sets PKV_DEVERR_SLOT. */
+int paged_kv_gather(pkv_cache_t cache, const int64_t *slot_mapping, int64_t num_tokens, void *k, void *v,
+                    void *stream);
 
 /* Slot indexing and paged KV append in one launch: for each token j, slot_j is computed as in
  * paged_slot_mapping from (block_tables, seq_ids[j], positions[j]) and k[j], v[j] are written as in
@@ -146,10 +168,51 @@ int paged_kv_append_at(pkv_cache_t cache, const void *k, const void *v, const in
  * on block placement.  Any num_seqs: a batch larger than one launch takes (1024 sequences, or
  * fewer for the tensor-core kernel of grouped-query heads, whose shared memory holds fewer) runs
  * as consecutive launches of that many sequences on the stream, sharing one workspace sized for
- * a launch.  The workspace grows (cudaMalloc) on demand unless kv_cache_reserve covered the call. */
+ * a launch.  The workspace grows (cudaMalloc) on demand unless kv_cache_reserve covered the call.
+ * PKV_INT4 caches: split boundaries depend on L_s, num_seqs and max_blocks_per_seq; the workspace is
+ * the stream's own (see paged_decode_attention_mass). */
 int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *block_tables, int max_blocks_per_seq,
                            const int32_t *context_lens, int num_seqs, int num_q_heads, float scale, void *out,
                            void *stream);
+
+/* paged_decode_attention that also accumulates each token's attention mass, for eviction:
+ *   attn_mass[s][g][t] := decay * attn_mass[s][g][t] + sum_{h: h / group == g} softmax_t(scale * q[s][h] . K_t)
+ * for t < L_s; the rest of a row is not touched.  attn_mass: fp32 [num_seqs][num_kv_heads][mass_len],
+ * row s belonging to row s of the tables; a token's entry has to be 0 before its first step.  decay in
+ * [0, 1] (1 sums, less lets old mass fade).  Every cache type; out as paged_decode_attention (to its
+ * tolerance, not bit for bit).  A length above mass_len or the tables' tokens sets PKV_DEVERR_LENGTH and
+ * is cut to that.  Two launches (one where every sequence fits a split); the products take the
+ * softmax weights as hi + lo 16-bit pairs, all else is fp32; no atomics, so equal calls give equal bits.
+ * Workspace: fp32 partials and scores (num_q_heads x tokens x 4 bytes per sequence, at most 2 GB a
+ * launch unless one sequence needs more; larger batches run as consecutive launches), one per stream
+ * and one per stream capture, allocated by the first call that needs it or more of it, also during a
+ * capture, and kept until the cache is destroyed: calls on different streams, and captured graphs,
+ * may overlap. */
+int paged_decode_attention_mass(const void *q, pkv_cache_t cache, const int32_t *block_tables,
+                                int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_q_heads,
+                                float scale, float decay, float *attn_mass, int64_t mass_len, void *out,
+                                void *stream);
+
+/* Eviction by attention mass.  For each sequence s and KV head g with L_s > budget tokens: the last
+ * `recent` tokens stay, and of the others the budget - recent of largest attn_mass[s][g][t] (equal
+ * masses: lowest t first; NaN below every number); a sequence of L_s <= budget tokens keeps all.  The
+ * tokens that stay keep their order and are copied (K and V rows of head g, exact bytes) to positions
+ * 0, 1, ... of row s of dst_block_tables; every head keeps its own choice.
+ *   kept[s][g][j]     = position of the j-th token that stays, -1 for j >= new length (int32 [S][Hkv][budget])
+ *   new_lens[s]       = min(L_s, budget)                                             (int32 [S])
+ *   new_mass[s][g][j] = its mass, 0 behind the new length                      (fp32 [S][Hkv][new_mass_len])
+ * attn_mass: fp32 [S][Hkv][mass_len].  1 <= budget, 0 <= recent <= budget; the destination tables and
+ * new_mass rows must hold min(budget, mass_len, tables' tokens) tokens (PKV_EINVAL otherwise).  The
+ * destination blocks must not be blocks of block_tables in the same call, nor appear twice (rows move
+ * in parallel); they are the caller's to allocate, and the old blocks, which are not changed and may be
+ * shared, the caller's to release.  Slots behind a new length are left as they were.  new_mass must not
+ * overlap attn_mass, nor new_lens context_lens (PKV_EINVAL).  A length above mass_len or the tables'
+ * tokens sets PKV_DEVERR_LENGTH and its sequence is skipped (kept -1, new length 0, new mass 0); a bad
+ * block id skips the row and sets PKV_DEVERR_BLOCK_ID.  No workspace. */
+int paged_kv_evict(pkv_cache_t cache, const int32_t *block_tables, int max_blocks_per_seq,
+                   const int32_t *context_lens, int num_seqs, const float *attn_mass, int64_t mass_len, int budget,
+                   int recent, const int32_t *dst_block_tables, int max_dst_blocks_per_seq, int32_t *kept,
+                   int32_t *new_lens, float *new_mass, int64_t new_mass_len, void *stream);
 
 /* paged_decode_attention without any device-memory allocation.  The pages have no counterpart:
  * this entry point exists for callers that cannot let a library allocate, e.g. a serving engine
@@ -207,9 +270,8 @@ int paged_decode_attention_cascade(const void *q, pkv_cache_t cache, const int32
  * whose bounds break these rules is skipped and sets PKV_DEVERR_CU_SEQLENS.  Q.K^T and P.V run on
  * the tensor cores (tcgen05, fp32 accumulation in tensor memory), two 128-row query tiles of one
  * (sequence, head) per work item sharing each 128-key K/V tile; P is rounded to the model dtype for
- * P.V (bf16: a hi + lo pair).  FP8 caches: the attention reads the packed k, v as given, and the
- * cache write is paged_kv_append's (E4M3 of fp32(x) / scale[head], the same bytes), issued as a
- * separate launch before it. */
+ * P.V (bf16: a hi + lo pair).  FP8 and PKV_INT4 caches: the attention reads the packed k, v as given,
+ * and the cache write is paged_kv_append's (the same bytes), issued as a separate launch before it. */
 int packed_prefill_attention(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int num_seqs,
                              int max_seqlen, int64_t total_tokens, const int32_t *block_tables,
                              int max_blocks_per_seq, pkv_cache_t cache, int num_q_heads, float scale, void *out,

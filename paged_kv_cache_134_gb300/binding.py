@@ -17,8 +17,8 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libpagedkv.so")
 
-PKV_F16, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2
-_DT = {"f16": PKV_F16, "bf16": PKV_BF16, "fp8": PKV_FP8_E4M3}
+PKV_F16, PKV_BF16, PKV_FP8_E4M3, PKV_INT4 = 0, 1, 2, 3
+_DT = {"f16": PKV_F16, "bf16": PKV_BF16, "fp8": PKV_FP8_E4M3, "int4": PKV_INT4}
 _TORCH = {PKV_F16: torch.float16, PKV_BF16: torch.bfloat16}
 DEVERR = {1: "block id", 2: "slot", 4: "length", 8: "cu_seqlens", 16: "timeout"}
 
@@ -55,6 +55,10 @@ def lib() -> ctypes.CDLL:
         L.paged_kv_append_at.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i64, vp, vp]
         L.paged_decode_attention.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp]
         L.paged_decode_attention_noalloc.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp]
+        L.paged_kv_gather.argtypes = [vp, vp, i64, vp, vp, vp]
+        L.paged_decode_attention_mass.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, ctypes.c_float, vp,
+                                                  i64, vp, vp]
+        L.paged_kv_evict.argtypes = [vp, vp, i32, vp, i32, vp, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp]
         L.packed_prefill_attention.argtypes = [vp, vp, vp, vp, i32, i32, i64, vp, i32, vp, i32, ctypes.c_float, vp,
                                                vp]
         L.paged_prefill_attention.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, vp, i32, vp, i32, ctypes.c_float, vp,
@@ -114,6 +118,12 @@ def _req(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
 
 
+def _same_device(cache: "KVCache", **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cache.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.device}")
+
+
 class _DevMem:
     """Exposes a raw device range through __cuda_array_interface__ for a zero-copy torch view."""
 
@@ -132,11 +142,12 @@ class KVCache:
         self.num_blocks, self.block_size = int(num_blocks), int(block_size)
         self.num_kv_heads, self.head_dim = int(num_kv_heads), int(head_dim)
         self.kv_dtype = kv_dtype
-        self.model_dtype = model_dtype or (kv_dtype if kv_dtype != "fp8" else "bf16")
+        self.model_dtype = model_dtype or (kv_dtype if kv_dtype not in ("fp8", "int4") else "bf16")
         h = ctypes.c_void_p()
         _check(L.kv_cache_create(self.num_blocks, self.block_size, self.num_kv_heads, self.head_dim,
                                  _DT[kv_dtype], _DT[self.model_dtype], ctypes.byref(h)))
         self._h = h
+        self.device = torch.cuda.current_device()
         self.torch_dtype = _TORCH[_DT[self.model_dtype]]
 
     @property
@@ -166,9 +177,10 @@ class KVCache:
         return raw, [int(x) for x in st]
 
     def pool_elems(self) -> torch.Tensor:
-        """The pool as a flat tensor of raw elements (int16 for 16-bit caches, uint8 for FP8)."""
+        """The pool as a flat tensor of raw elements (int16 for 16-bit caches, uint8 for FP8; the bytes of a
+        4-bit cache)."""
         raw, _ = self.view()
-        return raw if self.kv_dtype == "fp8" else raw.view(torch.int16)
+        return raw if self.kv_dtype in ("fp8", "int4") else raw.view(torch.int16)
 
     def set_scales(self, k_scale: torch.Tensor, v_scale: torch.Tensor):
         _req(k_scale, "k_scale", torch.float32, 1)
@@ -198,6 +210,8 @@ class KVCache:
     @property
     def block_bytes(self) -> int:
         """Bytes of one physical block (K and V of every KV head)."""
+        if self.kv_dtype == "int4":
+            return self.num_kv_heads * self.block_size * (self.head_dim + 8)
         return 2 * self.num_kv_heads * self.block_size * self.head_dim * (1 if self.kv_dtype == "fp8" else 2)
 
     def profile_start(self, kinds=("decode", "prefill", "append", "merge"), every: int = 1):
@@ -268,6 +282,87 @@ def paged_kv_append_at(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_t
                                     block_tables.shape[1], _ptr(seq_ids), _ptr(positions), n, _ptr(slot_mapping),
                                     _stream()))
     return slot_mapping
+
+
+def paged_kv_gather(cache: KVCache, slot_mapping: torch.Tensor, k: Optional[torch.Tensor] = None,
+                    v: Optional[torch.Tensor] = None):
+    """K and V at ``slot_mapping`` as (k, v), each [T, num_kv_heads, head_dim] in the model dtype: the
+    stored values of any cache type (a negative slot gives zeros)."""
+    _req(slot_mapping, "slot_mapping", torch.int64, 1)
+    n = slot_mapping.numel()
+    shape = (n, cache.num_kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=cache.torch_dtype, device=slot_mapping.device) if k is None else k
+    v = torch.empty(shape, dtype=cache.torch_dtype, device=slot_mapping.device) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        _req(t, name, cache.torch_dtype, 3)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+    _same_device(cache, slot_mapping=slot_mapping, k=k, v=v)
+    _check(lib().paged_kv_gather(cache.handle, _ptr(slot_mapping), n, _ptr(k), _ptr(v), _stream()))
+    return k, v
+
+
+def paged_decode_attention_mass(q: torch.Tensor, cache: KVCache, block_tables: torch.Tensor,
+                                context_lens: torch.Tensor, scale: float, attn_mass: torch.Tensor,
+                                decay: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_decode_attention that also adds every token's attention weight, summed over the query heads
+    of its KV head, to ``attn_mass`` (float32 [S, num_kv_heads, T], in place, after multiplying by
+    ``decay``); T must reach every length.  A token's entry starts at 0."""
+    _req(q, "q", cache.torch_dtype, 3)
+    _req(block_tables, "block_tables", torch.int32, 2)
+    _req(context_lens, "context_lens", torch.int32, 1)
+    _req(attn_mass, "attn_mass", torch.float32, 3)
+    S, hq, d = q.shape
+    if d != cache.head_dim or block_tables.shape[0] != S or context_lens.numel() != S:
+        raise ValueError("shape mismatch between q, block_tables and context_lens")
+    if tuple(attn_mass.shape[:2]) != (S, cache.num_kv_heads):
+        raise ValueError(f"attn_mass must be [{S}, {cache.num_kv_heads}, T]")
+    if out is None:
+        out = torch.empty_like(q)
+    _req(out, "out", cache.torch_dtype, 3)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _same_device(cache, q=q, block_tables=block_tables, context_lens=context_lens, attn_mass=attn_mass, out=out)
+    _check(lib().paged_decode_attention_mass(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
+                                             _ptr(context_lens), S, hq, ctypes.c_float(scale), ctypes.c_float(decay),
+                                             _ptr(attn_mass), attn_mass.shape[2], _ptr(out), _stream()))
+    return out
+
+
+def paged_kv_evict(cache: KVCache, block_tables: torch.Tensor, context_lens: torch.Tensor, attn_mass: torch.Tensor,
+                   budget: int, recent: int, dst_block_tables: torch.Tensor, kept: Optional[torch.Tensor] = None,
+                   new_lens: Optional[torch.Tensor] = None, new_mass: Optional[torch.Tensor] = None):
+    """Keep per (sequence, KV head) the last ``recent`` tokens and the ``budget - recent`` others of largest
+    ``attn_mass``, copied in order to the blocks of ``dst_block_tables`` (blocks of no table of this call).
+
+    Returns (kept int32 [S, Hkv, budget]: the positions that stay, -1 behind them; new_lens int32 [S];
+    new_mass float32 [S, Hkv, T']: their mass, 0 behind them, T' = attn_mass's T unless given).  The old
+    blocks are unchanged; the caller releases them."""
+    _req(block_tables, "block_tables", torch.int32, 2)
+    _req(dst_block_tables, "dst_block_tables", torch.int32, 2)
+    _req(context_lens, "context_lens", torch.int32, 1)
+    _req(attn_mass, "attn_mass", torch.float32, 3)
+    S, hkv, budget = context_lens.numel(), cache.num_kv_heads, int(budget)
+    if block_tables.shape[0] != S or dst_block_tables.shape[0] != S or tuple(attn_mass.shape[:2]) != (S, hkv):
+        raise ValueError("shape mismatch between tables, context_lens and attn_mass")
+    if budget < 1:
+        raise ValueError(f"budget {budget} is less than 1")
+    dev = context_lens.device
+    kept = torch.empty((S, hkv, budget), dtype=torch.int32, device=dev) if kept is None else kept
+    new_lens = torch.empty(S, dtype=torch.int32, device=dev) if new_lens is None else new_lens
+    new_mass = torch.empty_like(attn_mass) if new_mass is None else new_mass
+    _req(kept, "kept", torch.int32, 3)
+    _req(new_lens, "new_lens", torch.int32, 1)
+    _req(new_mass, "new_mass", torch.float32, 3)
+    if tuple(kept.shape) != (S, hkv, budget) or new_lens.numel() != S or tuple(new_mass.shape[:2]) != (S, hkv):
+        raise ValueError("kept must be [S, num_kv_heads, budget], new_lens [S], new_mass [S, num_kv_heads, T']")
+    _same_device(cache, block_tables=block_tables, dst_block_tables=dst_block_tables, context_lens=context_lens,
+                 attn_mass=attn_mass, kept=kept, new_lens=new_lens, new_mass=new_mass)
+    _check(lib().paged_kv_evict(cache.handle, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S,
+                                _ptr(attn_mass), attn_mass.shape[2], budget, int(recent), _ptr(dst_block_tables),
+                                dst_block_tables.shape[1], _ptr(kept), _ptr(new_lens), _ptr(new_mass),
+                                new_mass.shape[2], _stream()))
+    return kept, new_lens, new_mass
 
 
 def paged_decode_attention(q: torch.Tensor, cache: KVCache, block_tables: torch.Tensor,

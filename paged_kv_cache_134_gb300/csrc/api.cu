@@ -15,11 +15,32 @@ thread_local char g_msg[512] = "";
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int elem_bytes(pkv_dtype d) { return d == PKV_FP8_E4M3 ? 1 : 2; }
+int elem_bytes(pkv_dtype d) { return d == PKV_INT4 ? 0 : d == PKV_FP8_E4M3 ? 1 : 2; }
 
 bool supported_head_dim(int d) { return d == 64 || d == 128; }
 bool supported_block_size(int b) { return b == 8 || b == 16 || b == 32; }
 bool supported_group(int g) { return g == 1 || g == 2 || g == 4 || g == 8; }
+
+// the argument checks the decode entry points share
+int check_decode(const pkv_cache *c, const void *q, const int32_t *block_tables, int max_blocks_per_seq,
+                 const int32_t *context_lens, int num_q_heads, float scale, const void *out) {
+    if (num_q_heads <= 0 || num_q_heads % c->num_kv_heads)
+        return pkv_fail(PKV_EINVAL, "num_q_heads %d is not a multiple of num_kv_heads %d", num_q_heads,
+                        c->num_kv_heads);
+    if (!supported_group(num_q_heads / c->num_kv_heads))
+        return pkv_fail(PKV_EUNSUPPORTED, "num_q_heads / num_kv_heads = %d not in {1, 2, 4, 8}",
+                        num_q_heads / c->num_kv_heads);
+    if (!q || !out || !context_lens || (!block_tables && max_blocks_per_seq > 0))
+        return pkv_fail(PKV_EINVAL, "NULL pointer");
+    if (!aligned16(q) || !aligned16(out)) return pkv_fail(PKV_EINVAL, "q and out must be 16-byte aligned");
+    if (!(scale == scale)) return pkv_fail(PKV_EINVAL, "scale is NaN");
+    return PKV_OK;
+}
+
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
 
 int check_device(const pkv_cache *c) {
     int dev = -1;
@@ -45,6 +66,58 @@ int ensure_workspace(pkv_cache *c, int64_t floats) {
     return PKV_OK;
 }
 } // namespace
+
+int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, float **ws) {
+    *ws = nullptr;
+    if (floats <= 0) return PKV_OK;
+    const int64_t bytes = floats * (int64_t)sizeof(float);
+    unsigned long long stream = 0, capture = 0;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamGetCaptureInfo(st, &status, &capture);
+    if (e == cudaSuccess && status == cudaStreamCaptureStatusActive) {
+        stream = reinterpret_cast<uintptr_t>(st); // its id cannot be asked for now; the handle lives as long as the capture
+    } else if (e == cudaSuccess) {
+        capture = 0;
+        e = cudaStreamGetId(st, &stream);
+    }
+    if (e != cudaSuccess) return pkv_cuda_fail(e, "stream query");
+    std::lock_guard<std::mutex> lk(c->ws_mu);
+    int64_t most = 0;
+    for (auto &b : c->stream_ws) {
+        if (b.spare || b.stream != stream || b.capture != capture) continue;
+        if (b.bytes >= bytes) {
+            *ws = b.p;
+            return PKV_OK;
+        }
+        most = std::max(most, b.bytes);
+    }
+    for (auto &b : c->stream_ws) {
+        if (!b.spare || b.bytes < bytes) continue;
+        b.spare = false;
+        b.stream = stream;
+        b.capture = capture;
+        *ws = b.p;
+        return PKV_OK;
+    }
+    // at least twice the last one: the buffers left behind add up to less than the one in use
+    pkv_cache::StreamWs b{stream, capture, false, nullptr, std::max(bytes, 2 * most)};
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed; // an allocation is no part of the capture
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    e = cudaMalloc(reinterpret_cast<void **>(&b.p), (size_t)b.bytes);
+    if (e != cudaSuccess && b.bytes > bytes) {
+        cudaGetLastError();
+        b.bytes = bytes;
+        e = cudaMalloc(reinterpret_cast<void **>(&b.p), (size_t)b.bytes);
+    }
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return pkv_fail(PKV_ENOMEM, "decode workspace of %lld bytes: %s", (long long)bytes, cudaGetErrorString(e));
+    }
+    c->stream_ws.push_back(b);
+    *ws = b.p;
+    return PKV_OK;
+}
 
 int pkv_fail(int status, const char *fmt, ...) {
     va_list ap;
@@ -126,9 +199,9 @@ int kv_cache_create(int64_t num_blocks, int block_size, int num_kv_heads, int he
                     pkv_dtype model_dtype, pkv_cache_t *out) {
     if (!out) return pkv_fail(PKV_EINVAL, "out is NULL");
     if (num_blocks <= 0 || num_kv_heads <= 0) return pkv_fail(PKV_EINVAL, "num_blocks and num_kv_heads must be > 0");
-    if (kv_dtype < PKV_F16 || kv_dtype > PKV_FP8_E4M3 || model_dtype < PKV_F16 || model_dtype > PKV_BF16)
+    if (kv_dtype < PKV_F16 || kv_dtype > PKV_INT4 || model_dtype < PKV_F16 || model_dtype > PKV_BF16)
         return pkv_fail(PKV_EINVAL, "bad dtype (kv %d, model %d)", (int)kv_dtype, (int)model_dtype);
-    if (kv_dtype != PKV_FP8_E4M3 && kv_dtype != model_dtype)
+    if (kv_dtype != PKV_FP8_E4M3 && kv_dtype != PKV_INT4 && kv_dtype != model_dtype)
         return pkv_fail(PKV_EINVAL, "a 16-bit cache must use its own dtype as model dtype");
     if (!supported_head_dim(head_dim)) return pkv_fail(PKV_EUNSUPPORTED, "head_dim %d not in {64, 128}", head_dim);
     if (!supported_block_size(block_size))
@@ -146,9 +219,13 @@ int kv_cache_create(int64_t num_blocks, int block_size, int num_kv_heads, int he
     c->head_dim = head_dim;
     c->kv_dtype = kv_dtype;
     c->model_dtype = model_dtype;
-    c->elem_bytes = elem_bytes(kv_dtype);
+    c->elem_bytes = elem_bytes(kv_dtype); // 4-bit caches: 0, their strides are pkv_row_strides'
     c->tile_bytes = (int64_t)block_size * head_dim * c->elem_bytes;
-    c->pool_bytes = num_blocks * 2 * num_kv_heads * c->tile_bytes;
+    {
+        int64_t block, head, v;
+        pkv_row_strides(c, &block, &head, &v);
+        c->pool_bytes = num_blocks * block;
+    }
     e = cudaMalloc(&c->pool, (size_t)c->pool_bytes);
     if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void **>(&c->err), 16);
     if (e == cudaSuccess && kv_dtype == PKV_FP8_E4M3) {
@@ -177,12 +254,10 @@ int kv_cache_create(int64_t num_blocks, int block_size, int num_kv_heads, int he
     }
     if (e != cudaSuccess) {
         const int st = (e == cudaErrorMemoryAllocation) ? PKV_ENOMEM : PKV_ECUDA;
+        const long long bytes = c->pool_bytes;
         cudaGetLastError();
         kv_cache_destroy(c);
-        return pkv_fail(st, "kv_cache_create (%lld bytes): %s", (long long)(num_blocks * 2 * num_kv_heads *
-                                                                              (int64_t)block_size * head_dim *
-                                                                              elem_bytes(kv_dtype)),
-                        cudaGetErrorString(e));
+        return pkv_fail(st, "kv_cache_create (%lld bytes): %s", bytes, cudaGetErrorString(e));
     }
     *out = c;
     return PKV_OK;
@@ -197,6 +272,7 @@ int kv_cache_destroy(pkv_cache_t c) {
     if (c->v_scale) cudaFree(c->v_scale);
     if (c->ws) cudaFree(c->ws);
     if (c->plan) cudaFree(c->plan);
+    for (auto &b : c->stream_ws) cudaFree(b.p);
     for (auto &ev : c->events) {
         cudaEventDestroy(ev.a);
         cudaEventDestroy(ev.b);
@@ -225,9 +301,12 @@ int kv_cache_view(pkv_cache_t c, void **base, int64_t strides_elems[5], int64_t 
     const int64_t tile = (int64_t)c->block_size * c->head_dim;
     if (base) *base = c->pool;
     if (strides_elems) {
-        strides_elems[0] = 2 * c->num_kv_heads * tile;
-        strides_elems[1] = c->num_kv_heads * tile;
-        strides_elems[2] = tile;
+        int64_t block, head, v;
+        pkv_row_strides(c, &block, &head, &v);
+        const bool i4 = c->kv_dtype == PKV_INT4; // elements are nibbles: two a byte
+        strides_elems[0] = i4 ? 2 * block : 2 * c->num_kv_heads * tile;
+        strides_elems[1] = i4 ? 2 * v : c->num_kv_heads * tile;
+        strides_elems[2] = i4 ? 2 * head : tile;
         strides_elems[3] = c->head_dim;
         strides_elems[4] = 1;
     }
@@ -239,6 +318,24 @@ int kv_cache_reserve(pkv_cache_t c, int max_seqs, int max_q_heads, int max_block
     if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
     if (max_seqs < 0 || max_q_heads < 0 || max_blocks_per_seq < 0) return pkv_fail(PKV_EINVAL, "negative size");
     if (int r = check_device(c)) return r;
+    if (c->kv_dtype == PKV_INT4) {
+        const int64_t floats = max_q_heads > 0 && max_seqs > 0
+                                   ? decode_mma_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq)
+                                   : 0;
+        std::lock_guard<std::mutex> lk(c->ws_mu);
+        for (auto &b : c->stream_ws)
+            if (b.spare && b.bytes >= floats * (int64_t)sizeof(float)) return PKV_OK;
+        if (floats == 0) return PKV_OK;
+        pkv_cache::StreamWs b{0, 0, true, nullptr, floats * (int64_t)sizeof(float)};
+        cudaError_t e = cudaMalloc(reinterpret_cast<void **>(&b.p), (size_t)b.bytes);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return pkv_fail(PKV_ENOMEM, "decode workspace of %lld bytes: %s", (long long)b.bytes,
+                            cudaGetErrorString(e));
+        }
+        c->stream_ws.push_back(b);
+        return PKV_OK;
+    }
     const int bps = decode_split_blocks(c);
     const int max_splits = (max_blocks_per_seq + bps - 1) / bps;
     // consecutive launches of one call share the workspace: one launch's rows are enough
@@ -307,6 +404,71 @@ int paged_kv_append_at(pkv_cache_t c, const void *k, const void *v, const int32_
     return PKV_OK;
 }
 
+int paged_kv_gather(pkv_cache_t c, const int64_t *slot_mapping, int64_t num_tokens, void *k, void *v, void *stream) {
+    PKV_RANGE("paged_kv_gather");
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (num_tokens < 0) return pkv_fail(PKV_EINVAL, "num_tokens < 0");
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !slot_mapping) return pkv_fail(PKV_EINVAL, "NULL pointer");
+    if (!aligned16(k) || !aligned16(v)) return pkv_fail(PKV_EINVAL, "k and v must be 16-byte aligned");
+    if (int r = check_device(c)) return r;
+    cudaError_t e = launch_gather(c, slot_mapping, num_tokens, k, v, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return pkv_cuda_fail(e, "gather launch");
+    return PKV_OK;
+}
+
+int paged_decode_attention_mass(const void *q, pkv_cache_t c, const int32_t *block_tables, int max_blocks_per_seq,
+                                const int32_t *context_lens, int num_seqs, int num_q_heads, float scale, float decay,
+                                float *attn_mass, int64_t mass_len, void *out, void *stream) {
+    PKV_RANGE("paged_decode_attention_mass");
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || mass_len < 0) return pkv_fail(PKV_EINVAL, "negative size");
+    if (num_seqs == 0) return PKV_OK;
+    if (int r = check_decode(c, q, block_tables, max_blocks_per_seq, context_lens, num_q_heads, scale, out)) return r;
+    if (!attn_mass && mass_len > 0) return pkv_fail(PKV_EINVAL, "NULL pointer");
+    if (!(decay >= 0.f && decay <= 1.f)) return pkv_fail(PKV_EINVAL, "decay must be in [0, 1]");
+    if (int r = check_device(c)) return r;
+    MmaDecodeLaunch d{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale,
+                      attn_mass, mass_len, decay};
+    return decode_mma_entry(c, d, nullptr, 0, static_cast<cudaStream_t>(stream));
+}
+
+int paged_kv_evict(pkv_cache_t c, const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                   int num_seqs, const float *attn_mass, int64_t mass_len, int budget, int recent,
+                   const int32_t *dst_block_tables, int max_dst_blocks_per_seq, int32_t *kept, int32_t *new_lens,
+                   float *new_mass, int64_t new_mass_len, void *stream) {
+    PKV_RANGE("paged_kv_evict");
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || max_dst_blocks_per_seq < 0 || mass_len < 0 || new_mass_len < 0)
+        return pkv_fail(PKV_EINVAL, "negative size");
+    if (budget < 1) return pkv_fail(PKV_EINVAL, "budget %d is less than 1", budget);
+    if (recent < 0 || recent > budget) return pkv_fail(PKV_EINVAL, "recent %d is not in [0, budget %d]", recent, budget);
+    if (num_seqs == 0) return PKV_OK;
+    const int64_t cap = std::min<int64_t>(mass_len, (int64_t)max_blocks_per_seq * c->block_size);
+    const int64_t most = std::min<int64_t>(cap, budget);
+    if ((int64_t)max_dst_blocks_per_seq * c->block_size < most)
+        return pkv_fail(PKV_EINVAL, "destination tables of %d blocks cannot hold %lld tokens", max_dst_blocks_per_seq,
+                        (long long)most);
+    if (new_mass_len < most)
+        return pkv_fail(PKV_EINVAL, "new_mass rows of %lld cannot hold %lld tokens", (long long)new_mass_len,
+                        (long long)most);
+    if ((int64_t)num_seqs * c->num_kv_heads > 0x7FFFFFFF) return pkv_fail(PKV_EUNSUPPORTED, "too many rows");
+    if (!context_lens || !kept || !new_lens || (most > 0 && (!block_tables || !attn_mass || !dst_block_tables)) ||
+        (!new_mass && new_mass_len > 0))
+        return pkv_fail(PKV_EINVAL, "NULL pointer");
+    const int64_t rows = (int64_t)num_seqs * c->num_kv_heads;
+    if (overlap(attn_mass, rows * mass_len * 4, new_mass, rows * new_mass_len * 4))
+        return pkv_fail(PKV_EINVAL, "new_mass overlaps attn_mass");
+    if (overlap(context_lens, (int64_t)num_seqs * 4, new_lens, (int64_t)num_seqs * 4))
+        return pkv_fail(PKV_EINVAL, "new_lens overlaps context_lens");
+    if (int r = check_device(c)) return r;
+    EvictLaunch v{block_tables, dst_block_tables, context_lens, attn_mass, kept, new_lens, new_mass, mass_len,
+                  new_mass_len, max_blocks_per_seq, max_dst_blocks_per_seq, num_seqs, budget, recent};
+    cudaError_t e = launch_evict(c, v, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return pkv_cuda_fail(e, "eviction launch");
+    return PKV_OK;
+}
+
 int paged_decode_attention(const void *q, pkv_cache_t c, const int32_t *block_tables, int max_blocks_per_seq,
                            const int32_t *context_lens, int num_seqs, int num_q_heads, float scale, void *out,
                            void *stream) {
@@ -314,17 +476,13 @@ int paged_decode_attention(const void *q, pkv_cache_t c, const int32_t *block_ta
     if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
     if (num_seqs < 0 || max_blocks_per_seq < 0) return pkv_fail(PKV_EINVAL, "negative size");
     if (num_seqs == 0) return PKV_OK;
-    if (num_q_heads <= 0 || num_q_heads % c->num_kv_heads)
-        return pkv_fail(PKV_EINVAL, "num_q_heads %d is not a multiple of num_kv_heads %d", num_q_heads,
-                        c->num_kv_heads);
-    if (!supported_group(num_q_heads / c->num_kv_heads))
-        return pkv_fail(PKV_EUNSUPPORTED, "num_q_heads / num_kv_heads = %d not in {1, 2, 4, 8}",
-                        num_q_heads / c->num_kv_heads);
-    if (!q || !out || !context_lens || (!block_tables && max_blocks_per_seq > 0))
-        return pkv_fail(PKV_EINVAL, "NULL pointer");
-    if (!aligned16(q) || !aligned16(out)) return pkv_fail(PKV_EINVAL, "q and out must be 16-byte aligned");
-    if (!(scale == scale)) return pkv_fail(PKV_EINVAL, "scale is NaN");
+    if (int r = check_decode(c, q, block_tables, max_blocks_per_seq, context_lens, num_q_heads, scale, out)) return r;
     if (int r = check_device(c)) return r;
+    if (c->kv_dtype == PKV_INT4) {
+        MmaDecodeLaunch d{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale,
+                          nullptr, 0, 1.f};
+        return decode_mma_entry(c, d, nullptr, 0, static_cast<cudaStream_t>(stream));
+    }
     // a batch larger than one launch takes runs in consecutive launches that share the workspace
     const int per_launch = std::min(num_seqs, decode_seqs_per_launch(c, num_q_heads / c->num_kv_heads));
     DecodeLaunch d;
@@ -397,6 +555,8 @@ int paged_decode_attention_cascade(const void *q, pkv_cache_t c, const int32_t *
     if (shared_prefix_len == 0)
         return paged_decode_attention(q, c, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
                                       scale, out, stream);
+    if (c->kv_dtype == PKV_INT4)
+        return pkv_fail(PKV_EUNSUPPORTED, "the cascade's prefix phase does not read 4-bit caches");
     if (num_seqs < 0 || max_blocks_per_seq < 0) return pkv_fail(PKV_EINVAL, "negative size");
     if (num_seqs == 0) return PKV_OK;
     if ((int64_t)shared_prefix_len > (int64_t)max_blocks_per_seq * c->block_size)
@@ -470,6 +630,8 @@ int paged_prefill_attention(const void *q, const void *k, const void *v, const i
                             float scale, void *out, void *stream) {
     PKV_RANGE("paged_prefill_attention");
     if (!context_lens && num_seqs > 0) return pkv_fail(PKV_EINVAL, "NULL pointer");
+    if (c && c->kv_dtype == PKV_INT4)
+        return pkv_fail(PKV_EUNSUPPORTED, "the prefill over a cached prefix does not read 4-bit caches");
     return prefill_entry(q, k, v, cu_seqlens, context_lens, num_seqs, max_seqlen, total_tokens, block_tables,
                          max_blocks_per_seq, c, num_q_heads, scale, out, stream);
 }

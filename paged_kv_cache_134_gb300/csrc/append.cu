@@ -12,7 +12,11 @@
 // per decode step.  All kernels are launched with programmatic dependent launch: they let the
 // next kernel in the stream start its launch early and wait for their own predecessor before
 // touching global memory.
+//
+// A 4-bit cache's rows are quantised on the way (append4_kernel, below); gather_kernel reads the rows
+// of any cache back in the model's type.
 #include "device_common.cuh"
+#include "int4.cuh"
 #include "pkv_internal.h"
 
 namespace {
@@ -151,6 +155,136 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     }
 }
 
+// 4-bit append.  Per (token, K|V, KV head) row x[0 .. D): z = min x, s = RN((max x - min x) / 15) in the
+// model's type, code = min(15, rint((x - z) / s)); int4.cuh has the layout and the border cases.  D / 8
+// lanes share a row, eight elements each: the extremes meet by xor shuffles (on packed pairs, with the
+// NaN-propagating forms, so a NaN anywhere reaches s), and each lane writes the four bytes of its codes.
+//
+// The quotient has to be the correctly rounded one, so that a code does not hang on how it was computed;
+// an IEEE division per element would double the kernel's arithmetic, so the codes come from a
+// multiplication by 1 / s wherever its error (below 1e-5 at quotients up to 22) cannot move rint, and only
+// the others divide.  Bound by HBM: 4 D bytes read and D + 8 written per token and head.
+template <int MT, int MODE>
+__global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int cpr = a.chunks_per_row, row_chunks = a.hkv * cpr, per_token = 2 * row_chunks;
+    const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
+    const int lt = tpg > 1 ? (int)threadIdx.x / per_token : 0;
+    const int r0 = tpg > 1 ? (int)threadIdx.x - lt * per_token : (int)threadIdx.x;
+    const int rstep = tpg > 1 ? per_token : kAppendThreads;
+    if (lt >= tpg) return;
+    // the lanes that share a row: per_token, rstep and kAppendThreads are multiples of cpr (8 or 16), so
+    // they take every branch below together
+    const unsigned lanes = ((1u << cpr) - 1u) << ((threadIdx.x & 31) & ~(cpr - 1));
+    for (int64_t j = (int64_t)blockIdx.x * tpg + lt; j < a.n; j += (int64_t)gridDim.x * tpg) {
+        const int64_t slot = append_slot<MODE>(a, j);
+        if (MODE != SLOTS_GIVEN && r0 == 0 && a.slots_out) a.slots_out[j] = slot;
+        if (slot < 0) continue;
+        if (slot >= a.num_slots) {
+            if (r0 == 0) set_error(a.err, PKV_DEVERR_SLOT);
+            continue;
+        }
+        const int64_t blk = slot / a.bs;
+        const int off = static_cast<int>(slot - blk * a.bs);
+        const uint4 *ksrc = a.k + j * row_chunks, *vsrc = a.v + j * row_chunks;
+        for (int rb = r0; rb < per_token; rb += kAppendUnroll * rstep) {
+            uint4 src[kAppendUnroll];
+#pragma unroll
+            for (int u = 0; u < kAppendUnroll; ++u) {
+                const int r = rb + u * rstep;
+                if (r < per_token) src[u] = r >= row_chunks ? vsrc[r - row_chunks] : ksrc[r];
+            }
+#pragma unroll
+            for (int u = 0; u < kAppendUnroll; ++u) {
+                const int r = rb + u * rstep;
+                if (r >= per_token) continue;
+                const int kv = r >= row_chunks ? 1 : 0, hc = r - kv * row_chunks, h = hc / cpr, c = hc - h * cpr;
+                const Int4Row row = int4_quantise<MT>(src[u], cpr, lanes);
+                char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, a.d);
+                *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, a.bs, a.d) + c * 4) = row.codes;
+                if (c == 0) *reinterpret_cast<uint32_t *>(tile + int4_params(kv, off, a.bs, a.d)) = row.params;
+            }
+        }
+    }
+}
+
+// Rows read back: token j's K and V at slots[j] in the model's type (a 4- or 8-bit row's values, rounded
+// once; a 16-bit row's bits).  A negative slot gives a row of zeros, one past the pool zeros and
+// PKV_DEVERR_SLOT.  Bound by HBM; the append's assignment of threads to chunks, loads before stores.
+struct GatherArgs {
+    uint4 *k, *v;
+    const int64_t *slots;
+    const char *pool;
+    const float *k_scale, *v_scale;
+    unsigned int *err;
+    int64_t n, num_slots;
+    int hkv, bs, chunks_per_row, d;
+};
+
+template <int KVT, int MT>
+PKV_DEV uint4 gather_chunk(const GatherArgs &a, int64_t blk, int off, int kv, int h, int c) {
+    using M = ModelT<MT>;
+    const int64_t e = ((blk * 2 + kv) * a.hkv + h) * ((int64_t)a.bs * a.d) + (int64_t)off * a.d + c * 8;
+    if constexpr (KVT == PKV_F16) {
+        return reinterpret_cast<const uint4 *>(a.pool)[e / 8];
+    } else {
+        float f[8];
+        if constexpr (KVT == PKV_FP8_E4M3) {
+            cvt8_e4m3(reinterpret_cast<const uint2 *>(a.pool)[e / 8], f);
+            const float sc = (kv ? a.v_scale : a.k_scale)[h];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= sc;
+        } else {
+            const char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, a.d);
+            int4_values<MT>(*reinterpret_cast<const uint32_t *>(tile + int4_codes(kv, off, a.bs, a.d) + c * 4),
+                            *reinterpret_cast<const uint32_t *>(tile + int4_params(kv, off, a.bs, a.d)), f);
+        }
+        return make_uint4(M::pack(f[0], f[1]), M::pack(f[2], f[3]), M::pack(f[4], f[5]), M::pack(f[6], f[7]));
+    }
+}
+
+template <int KVT, int MT>
+__global__ void __launch_bounds__(kAppendThreads) gather_kernel(GatherArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int cpr = a.chunks_per_row, row_chunks = a.hkv * cpr, per_token = 2 * row_chunks;
+    const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
+    const int lt = tpg > 1 ? (int)threadIdx.x / per_token : 0;
+    const int r0 = tpg > 1 ? (int)threadIdx.x - lt * per_token : (int)threadIdx.x;
+    const int rstep = tpg > 1 ? per_token : kAppendThreads;
+    if (lt >= tpg) return;
+    for (int64_t j = (int64_t)blockIdx.x * tpg + lt; j < a.n; j += (int64_t)gridDim.x * tpg) {
+        int64_t slot = a.slots[j];
+        if (slot >= a.num_slots) {
+            if (r0 == 0) set_error(a.err, PKV_DEVERR_SLOT);
+            slot = -1;
+        }
+        const int64_t blk = slot < 0 ? 0 : slot / a.bs;
+        const int off = static_cast<int>(slot - blk * a.bs);
+        for (int rb = r0; rb < per_token; rb += kAppendUnroll * rstep) {
+            uint4 x[kAppendUnroll];
+#pragma unroll
+            for (int u = 0; u < kAppendUnroll; ++u) {
+                const int r = rb + u * rstep;
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (r < per_token && slot >= 0) {
+                    const int kv = r >= row_chunks ? 1 : 0, hc = r - kv * row_chunks, h = hc / cpr;
+                    x[u] = gather_chunk<KVT, MT>(a, blk, off, kv, h, hc - h * cpr);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAppendUnroll; ++u) {
+                const int r = rb + u * rstep;
+                if (r < row_chunks)
+                    a.k[j * row_chunks + r] = x[u];
+                else if (r < per_token)
+                    a.v[j * row_chunks + r - row_chunks] = x[u];
+            }
+        }
+    }
+}
+
 inline int grid_for(int64_t work, int threads, int num_sms) {
     const int64_t blocks = (work + threads - 1) / threads;
     const int64_t cap = (int64_t)num_sms * 16;
@@ -185,7 +319,11 @@ cudaError_t launch_append_t(pkv_cache *c, const AppendArgs &a, cudaStream_t st) 
     const dim3 grid((unsigned)(passes < 1 ? 1 : (passes > cap ? cap : passes)));
     PkvTimer timer(c, PKV_KIND_APPEND, st);
     cudaError_t e;
-    if (c->kv_dtype != PKV_FP8_E4M3)
+    if (c->kv_dtype == PKV_INT4)
+        e = c->model_dtype == PKV_F16
+                ? pdl_launch(append4_kernel<PKV_F16, MODE>, grid, dim3(kAppendThreads), 0, st, a)
+                : pdl_launch(append4_kernel<PKV_BF16, MODE>, grid, dim3(kAppendThreads), 0, st, a);
+    else if (c->kv_dtype != PKV_FP8_E4M3)
         e = pdl_launch(append_kernel<PKV_F16, PKV_F16, MODE>, grid, dim3(kAppendThreads), 0, st, a);
     else if (c->model_dtype == PKV_F16)
         e = pdl_launch(append_kernel<PKV_FP8_E4M3, PKV_F16, MODE>, grid, dim3(kAppendThreads), 0, st, a);
@@ -241,4 +379,36 @@ cudaError_t launch_append_ranges(pkv_cache *c, const void *k, const void *v, con
     a.cu = cu;
     a.ctx = ctx;
     return launch_append_t<SLOTS_RANGES>(c, a, st);
+}
+
+cudaError_t launch_gather(pkv_cache *c, const int64_t *slots, int64_t n, void *k, void *v, cudaStream_t st) {
+    if (n == 0) return cudaSuccess;
+    GatherArgs a{};
+    a.k = static_cast<uint4 *>(k);
+    a.v = static_cast<uint4 *>(v);
+    a.slots = slots;
+    a.pool = static_cast<const char *>(c->pool);
+    a.k_scale = c->k_scale;
+    a.v_scale = c->v_scale;
+    a.err = c->err;
+    a.n = n;
+    a.num_slots = c->num_blocks * c->block_size;
+    a.hkv = c->num_kv_heads;
+    a.bs = c->block_size;
+    a.chunks_per_row = c->head_dim / 8;
+    a.d = c->head_dim;
+    const int per_token = 2 * a.hkv * a.chunks_per_row;
+    const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
+    const int64_t passes = (n + tpg - 1) / tpg, cap = (int64_t)c->num_sms * 8;
+    const dim3 grid((unsigned)(passes > cap ? cap : passes)), block(kAppendThreads);
+    const bool h = c->model_dtype == PKV_F16;
+    PkvTimer timer(c, PKV_KIND_COPY, st);
+    g_pkv_launches++;
+    if (c->kv_dtype == PKV_INT4)
+        return h ? pdl_launch(gather_kernel<PKV_INT4, PKV_F16>, grid, block, 0, st, a)
+                 : pdl_launch(gather_kernel<PKV_INT4, PKV_BF16>, grid, block, 0, st, a);
+    if (c->kv_dtype == PKV_FP8_E4M3)
+        return h ? pdl_launch(gather_kernel<PKV_FP8_E4M3, PKV_F16>, grid, block, 0, st, a)
+                 : pdl_launch(gather_kernel<PKV_FP8_E4M3, PKV_BF16>, grid, block, 0, st, a);
+    return pdl_launch(gather_kernel<PKV_F16, PKV_F16>, grid, block, 0, st, a);
 }

@@ -1,0 +1,119 @@
+// Host side of the matrix-instruction decode (decode_mma.cuh): split size, workspace, launches.
+#include "decode_mma.cuh"
+
+#include <algorithm>
+
+namespace {
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// What one launch of at most `seqs` sequences looks like.
+struct Plan {
+    int64_t cap;    // tokens a sequence may have
+    int split, max_splits, seqs;
+    int64_t floats; // workspace
+};
+
+bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len, Plan *p) {
+    const bool mass = mass_len >= 0;
+    p->cap = (int64_t)max_blocks * c->block_size;
+    if (mass) p->cap = std::min(p->cap, mass_len);
+    // Two units per resident CTA at the table's full width: fewer leave SMs idle at the end, more make
+    // units so short that their fixed costs (q, the warps' join, the partial) show.  At least 64 tokens
+    // (a tile per warp), at most kMaxSplit; more only to keep a row's splits within 1024.  A function of
+    // the call's shapes, never of the lengths: a result does not change with the other sequences' lengths.
+    const int64_t slots = (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
+    const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads;
+    int64_t split = round_up((rows * p->cap + 2 * slots - 1) / (2 * slots), 64);
+    split = std::max<int64_t>(64, std::min<int64_t>(split, pkv_mma::kMaxSplit));
+    split = std::max(split, round_up((p->cap + 1023) / 1024, 64));
+    if (split / c->block_size > 8192) return false; // the split's table entries no longer fit shared memory
+    p->split = (int)split;
+    p->max_splits = (int)((p->cap + split - 1) / split);
+    const int64_t partials = p->max_splits > 1 ? (int64_t)hq * p->max_splits * (c->head_dim + 2) : 0;
+    const int64_t per_seq = partials + (mass ? (int64_t)hq * p->cap : 0);
+    // sequences per launch: at most kMaxSeqs, and at most 2 GB of workspace unless one sequence needs more
+    int64_t n = std::min<int64_t>(num_seqs, pkv_mma::kMaxSeqs);
+    if (per_seq > 0) n = std::max<int64_t>(1, std::min<int64_t>(n, ((int64_t)1 << 29) / per_seq));
+    p->seqs = (int)n;
+    p->floats = n * per_seq;
+    return true;
+}
+
+cudaError_t run(const pkv_cache *c, const pkv_mma::Args &a, bool mass, bool merge, cudaStream_t st) {
+    const int mt = c->model_dtype, D = c->head_dim, sms = c->num_sms;
+    if (!mass) return pkv_mma_int4(a, mt, D, sms, merge, st);
+    if (c->kv_dtype == PKV_INT4) return pkv_mma_int4_mass(a, mt, D, sms, merge, st);
+    if (c->kv_dtype == PKV_FP8_E4M3) return pkv_mma_fp8_mass(a, mt, D, sms, merge, st);
+    return pkv_mma_16bit_mass(a, mt, D, sms, merge, st);
+}
+
+} // namespace
+
+int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks) {
+    Plan p;
+    return plan_for(c, num_seqs, hq, max_blocks, -1, &p) ? p.floats : 0;
+}
+
+int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, float *scratch, int64_t scratch_floats, cudaStream_t st) {
+    Plan p;
+    if (!plan_for(c, d.num_seqs, d.num_q_heads, d.max_blocks, d.mass ? d.mass_len : -1, &p))
+        return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this decode takes", d.max_blocks);
+    float *ws = scratch;
+    if (!scratch) {
+        if (int r = pkv_stream_workspace(c, st, p.floats, &ws)) return r;
+    } else if (p.floats > scratch_floats) {
+        return pkv_fail(PKV_EINVAL,
+                        "no-alloc decode needs %lld bytes of scratch for %d sequences x %d query heads x %d splits; "
+                        "its fixed scratch holds %lld bytes (use fewer sequences per call or paged_decode_attention)",
+                        (long long)(p.floats * 4), p.seqs, d.num_q_heads, p.max_splits, (long long)(scratch_floats * 4));
+    }
+    pkv_mma::Args a;
+    a.pool = static_cast<const char *>(c->pool);
+    a.k_scale = c->k_scale;
+    a.v_scale = c->v_scale;
+    a.err = c->err;
+    a.num_blocks = c->num_blocks;
+    pkv_row_strides(c, &a.blk_stride, &a.head_stride, &a.v_off);
+    a.mass_len = d.mass_len;
+    a.cap = p.cap;
+    a.max_blocks = d.max_blocks;
+    a.hq = d.num_q_heads;
+    a.hkv = c->num_kv_heads;
+    a.group = d.num_q_heads / c->num_kv_heads;
+    a.bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
+    a.split_tokens = p.split;
+    a.max_splits = p.max_splits;
+    a.qk_scale_log2 = d.scale * 1.4426950408889634f;
+    a.decay = d.decay;
+    // a batch larger than one launch takes runs in consecutive launches that share the workspace: each
+    // waits for the one before it
+    for (int s0 = 0; s0 < d.num_seqs; s0 += p.seqs) {
+        const int n = std::min(p.seqs, d.num_seqs - s0);
+        const int64_t rows = (int64_t)n * d.num_q_heads * (p.max_splits > 1 ? p.max_splits : 0);
+        const int64_t row_bytes = (int64_t)d.num_q_heads * c->head_dim * 2;
+        a.q = static_cast<const char *>(d.q) + s0 * row_bytes;
+        a.out = static_cast<char *>(d.out) + s0 * row_bytes;
+        a.tables = d.tables ? d.tables + (int64_t)s0 * d.max_blocks : nullptr;
+        a.lens = d.lens + s0;
+        a.num_seqs = n;
+        a.ws_o = ws;
+        a.ws_ml = ws + rows * c->head_dim;
+        a.ws_x = ws + rows * (c->head_dim + 2);
+        a.mass = d.mass ? d.mass + (int64_t)s0 * c->num_kv_heads * d.mass_len : nullptr;
+        cudaError_t e;
+        {
+            PkvTimer timer(c, PKV_KIND_DECODE, st);
+            g_pkv_launches++;
+            e = run(c, a, d.mass != nullptr, false, st);
+        }
+        if (e != cudaSuccess) return pkv_cuda_fail(e, "decode launch");
+        if (p.max_splits > 1) {
+            PkvTimer timer(c, PKV_KIND_MERGE, st);
+            g_pkv_launches++;
+            e = run(c, a, d.mass != nullptr, true, st);
+        }
+        if (e != cudaSuccess) return pkv_cuda_fail(e, "decode merge launch");
+    }
+    return PKV_OK;
+}

@@ -73,6 +73,20 @@ extern "C" int paged_decode_attention_noalloc(const void *q, pkv_cache_t c, cons
     if (e != cudaSuccess) return pkv_cuda_fail(e, "cudaGetDevice");
     if (dev != c->device) return pkv_fail(PKV_EINVAL, "cache lives on device %d but device %d is current", c->device, dev);
 
+    if (c->kv_dtype == PKV_INT4) {
+        float *scratch;
+        {
+            std::lock_guard<std::mutex> lk(g_scratch_mu);
+            scratch = dev < kMaxDevices ? g_scratch_ptr[dev] : nullptr;
+        }
+        if (!scratch)
+            return pkv_fail(PKV_EINVAL,
+                            "no-alloc decode scratch is not resident on device %d (create a cache there first)", dev);
+        MmaDecodeLaunch m{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale,
+                          nullptr, 0, 1.f};
+        return decode_mma_entry(c, m, scratch, kScratchFloats, static_cast<cudaStream_t>(stream));
+    }
+
     DecodeLaunch d;
     d.q = q;
     d.out = out;

@@ -18,7 +18,7 @@ struct pkv_cache {
     int block_size = 0, num_kv_heads = 0, head_dim = 0;
     pkv_dtype kv_dtype = PKV_F16, model_dtype = PKV_F16;
     int elem_bytes = 2;
-    // pool: [num_blocks][2][Hkv][bs][D] elements
+    // pool: [num_blocks][2][Hkv][bs][D] elements; 4-bit caches: int4.cuh
     void *pool = nullptr;
     int64_t pool_bytes = 0;
     int64_t tile_bytes = 0;   // one (block, K|V, head) tile: bs * D * elem
@@ -32,6 +32,18 @@ struct pkv_cache {
     int *plan = nullptr;
     int64_t plan_bytes = 0;
     int num_sms = 0;
+    // workspaces of the decode of 4-bit caches and of the decode with attention mass, one per stream
+    // (and one per stream capture): work of one stream is ordered, so its calls share one, while
+    // concurrent streams and captured graphs never meet in one.  A buffer that was outgrown stays until
+    // the cache is destroyed, because a captured graph may still use it.
+    struct StreamWs {
+        unsigned long long stream, capture;
+        bool spare; // from kv_cache_reserve, not yet any stream's
+        float *p;
+        int64_t bytes;
+    };
+    std::vector<StreamWs> stream_ws;
+    std::mutex ws_mu;
     // profiling
     bool profiling = false;
     unsigned profile_kinds = 0; // bit (1 << PKV_KIND_*)
@@ -93,6 +105,48 @@ cudaError_t launch_append_at(pkv_cache *c, const void *k, const void *v, const i
 // of sequence i (the tail of a prompt after its cached prefix)
 cudaError_t launch_append_ranges(pkv_cache *c, const void *k, const void *v, const int32_t *tables, int num_seqs,
                                  int max_blocks, const int32_t *cu, const int32_t *ctx, int64_t n, cudaStream_t st);
+
+// rows at slots[i] in the model's type: k, v [n][Hkv][D] (append.cu)
+cudaError_t launch_gather(pkv_cache *c, const int64_t *slots, int64_t n, void *k, void *v, cudaStream_t st);
+
+// bytes between blocks, between a block's KV heads, and from a head's K rows to its V rows
+inline void pkv_row_strides(const pkv_cache *c, int64_t *block, int64_t *head, int64_t *v) {
+    if (c->kv_dtype == PKV_INT4) {
+        *head = (int64_t)c->block_size * (c->head_dim + 8);
+        *block = c->num_kv_heads * *head;
+        *v = (int64_t)c->block_size * c->head_dim / 2;
+    } else {
+        *head = c->tile_bytes;
+        *v = c->num_kv_heads * c->tile_bytes;
+        *block = 2 * *v;
+    }
+}
+
+// decode of 4-bit caches, and decode with attention mass of every cache (decode_mma.cu)
+struct MmaDecodeLaunch {
+    const void *q;
+    void *out;
+    const int32_t *tables, *lens;
+    int max_blocks, num_seqs, num_q_heads;
+    float scale;
+    float *mass; // or NULL
+    int64_t mass_len;
+    float decay;
+};
+// scratch: a fixed workspace of scratch_floats to use instead of the stream's own, or NULL
+int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, float *scratch, int64_t scratch_floats, cudaStream_t st);
+int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks);
+int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, float **ws); // api.cu
+
+struct EvictLaunch {
+    const int32_t *tables, *dst_tables, *lens;
+    const float *mass;
+    int32_t *kept, *new_lens;
+    float *mass_out;
+    int64_t mass_len, mass_out_len;
+    int max_blocks, max_dst_blocks, num_seqs, budget, recent;
+};
+cudaError_t launch_evict(pkv_cache *c, const EvictLaunch &v, cudaStream_t st); // evict.cu
 
 // whole-block copies (blocks.cu): pair i copies block src_ids[i] (or i) of `src` to block
 // dst_ids[i] (or i) of `dst`; both regions are made of blocks of the cache's block size

@@ -262,7 +262,8 @@ cudaError_t launch_prefill(pkv_cache *c, const PrefillLaunch &p, cudaStream_t st
     if (p.total_tokens <= 0) return cudaSuccess;
     const int D = c->head_dim;
     const int mt = c->model_dtype;
-    const bool kv8 = c->kv_dtype == PKV_FP8_E4M3;
+    const bool kv8 = c->kv_dtype == PKV_FP8_E4M3, kv4 = c->kv_dtype == PKV_INT4;
+    if (kv4 && p.ctx) return cudaErrorNotSupported;
     Args a = base_args(c, p.scale);
     a.k = static_cast<const char *>(p.k);
     a.v = static_cast<const char *>(p.v);
@@ -275,7 +276,7 @@ cudaError_t launch_prefill(pkv_cache *c, const PrefillLaunch &p, cudaStream_t st
     a.max_seqlen = p.max_seqlen;
     a.max_blocks = p.max_blocks;
     a.hq = p.num_q_heads;
-    a.write_pool = kv8 ? 0 : 1;
+    a.write_pool = kv8 || kv4 ? 0 : 1;
     // (sequence, pair of query tiles) items: sum_i ceil(n_i / 2 BM) <= T / 2 BM + num_seqs
     const int64_t tiles_max = ((int64_t)p.max_seqlen + BM - 1) / BM;
     a.npairs_max = (int)((tiles_max + 1) / 2);
@@ -298,13 +299,15 @@ cudaError_t launch_prefill(pkv_cache *c, const PrefillLaunch &p, cudaStream_t st
     Maps m;
     if (!make_map(&m.q, p.q, mt, p.total_tokens, (int64_t)p.num_q_heads * D, BM) ||
         !make_map(&m.k, p.k, mt, p.total_tokens, (int64_t)c->num_kv_heads * D, BN) ||
-        !make_map(&m.v, p.v, mt, p.total_tokens, (int64_t)c->num_kv_heads * D, BN) || !pool_map(&m.pool, c) ||
+        !make_map(&m.v, p.v, mt, p.total_tokens, (int64_t)c->num_kv_heads * D, BN) ||
+        // (a 4-bit pool has no rows of elements: the append writes it and no load of the packed mode reads it)
+        !(kv4 ? make_map(&m.pool, p.k, mt, p.total_tokens, (int64_t)c->num_kv_heads * D, BN) : pool_map(&m.pool, c)) ||
         !make_map(&m.out, p.out, mt, p.total_tokens, (int64_t)p.num_q_heads * D, BM))
         return cudaErrorInvalidValue;
-    if (p.ctx || kv8) {
+    if (p.ctx || kv8 || kv4) {
         // A cached prefix: the new tokens' K/V go to their slots first, then attention reads every key
-        // through the block table.  An FP8 cache: the packed prefill's K/V write is the append's
-        // (fp32 division by the head's scale, E4M3 rounding), and the attention reads the packed k, v.
+        // through the block table.  An FP8 or 4-bit cache: the packed prefill's K/V write is the append's
+        // (E4M3 or 4-bit codes), and the attention reads the packed k, v.
         e = launch_append_ranges(c, p.k, p.v, p.tables, p.num_seqs, p.max_blocks, p.cu, p.ctx, p.total_tokens, st);
         if (e != cudaSuccess) return e;
     }
