@@ -70,9 +70,11 @@ typedef enum {
  * equal blocks" of 2kiu.com section 2.2 / discosf.com section 2.1.  Pool layout
  * (see kv_cache_view): [num_blocks][2 = K,V][num_kv_heads][block_size][head_dim],
  * so one (block, K|V, head) tile is block_size*head_dim contiguous elements.  PKV_INT4:
- * [num_blocks][num_kv_heads] runs of block_size * (head_dim + 8) bytes, each K codes
- * [block_size][head_dim / 2], V codes, K (step, offset) [block_size][2], V (step, offset) in the
- * model dtype; element i of a row is nibble i, the low one of byte i / 2 for even i.
+ * [num_blocks][num_kv_heads] runs of block_size * (head_dim + 8) bytes, each one octet of 8 slots
+ * after the other: K codes [8][head_dim / 2], V codes [8][head_dim / 2], K (step, offset) [8][2],
+ * V (step, offset) [8][2] in the model dtype.  Elements 4 i .. 4 i + 3 of a row are the nibbles of its
+ * 16-bit word i, lowest first, the word rotated left by three bits.  V's rows stand in the order 0 2 4 6 1 3 5 7; at head_dim 128 rows 4, 5, 6 and 7
+ * hold their second 32 bytes first.
  * On failure *out is untouched. */
 int kv_cache_create(int64_t num_blocks, int block_size, int num_kv_heads, int head_dim, pkv_dtype kv_dtype,
                     pkv_dtype model_dtype, pkv_cache_t *out);
@@ -87,8 +89,8 @@ int kv_cache_destroy(pkv_cache_t cache);
 int kv_cache_set_scales(pkv_cache_t cache, const float *k_scale, const float *v_scale, void *stream);
 
 /* Describe the pool for tests and initialisation: *base = device address of the pool,
- * strides_elems = element strides of the (block, K|V, head, offset, dim) axes (PKV_INT4: of the
- * 4-bit codes, two elements a byte),
+ * strides_elems = element strides of the (block, K|V, head, offset, dim) axes (PKV_INT4: in
+ * 4-bit codes, two a byte, for block and head; 0 for K|V and offset, see kv_cache_create),
  * *num_bytes = pool size in bytes.  The library keeps ownership. */
 int kv_cache_view(pkv_cache_t cache, void **base, int64_t strides_elems[5], int64_t *num_bytes);
 

@@ -67,10 +67,34 @@ int ensure_workspace(pkv_cache *c, int64_t floats) {
 }
 } // namespace
 
-int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, float **ws) {
-    *ws = nullptr;
+namespace {
+int64_t workspace_counters(const pkv_cache *c) { return (int64_t)1024 * c->num_kv_heads; } // rows of a launch
+
+// A workspace of `bytes` for partials and its zeroed counters, not tied to any stream's work: also while a
+// stream is captured (an allocation is no part of the capture).
+cudaError_t allocate_workspace(const pkv_cache *c, int64_t bytes, float **p) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    const int64_t tail = workspace_counters(c) * (int64_t)sizeof(int);
+    cudaStream_t own = nullptr;
+    cudaError_t e = cudaMalloc(reinterpret_cast<void **>(p), (size_t)(bytes + tail));
+    if (e == cudaSuccess) {
+        e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+        if (e == cudaSuccess) e = cudaMemsetAsync(reinterpret_cast<char *>(*p) + bytes, 0, (size_t)tail, own);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+        if (own) cudaStreamDestroy(own);
+        if (e != cudaSuccess) cudaFree(*p);
+    }
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+} // namespace
+
+int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorkspace *ws) {
+    *ws = PkvWorkspace();
     if (floats <= 0) return PKV_OK;
-    const int64_t bytes = floats * (int64_t)sizeof(float);
+    const int64_t bytes = (floats * (int64_t)sizeof(float) + 255) / 256 * 256;
     unsigned long long stream = 0, capture = 0;
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamGetCaptureInfo(st, &status, &capture);
@@ -81,14 +105,18 @@ int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, float **
         e = cudaStreamGetId(st, &stream);
     }
     if (e != cudaSuccess) return pkv_cuda_fail(e, "stream query");
+    auto use = [&](const pkv_cache::StreamWs &b) {
+        ws->p = b.p;
+        ws->floats = b.bytes / (int64_t)sizeof(float);
+        ws->done = reinterpret_cast<int *>(reinterpret_cast<char *>(b.p) + b.bytes);
+        ws->counters = workspace_counters(c);
+        return PKV_OK;
+    };
     std::lock_guard<std::mutex> lk(c->ws_mu);
     int64_t most = 0;
     for (auto &b : c->stream_ws) {
         if (b.spare || b.stream != stream || b.capture != capture) continue;
-        if (b.bytes >= bytes) {
-            *ws = b.p;
-            return PKV_OK;
-        }
+        if (b.bytes >= bytes) return use(b);
         most = std::max(most, b.bytes);
     }
     for (auto &b : c->stream_ws) {
@@ -96,27 +124,20 @@ int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, float **
         b.spare = false;
         b.stream = stream;
         b.capture = capture;
-        *ws = b.p;
-        return PKV_OK;
+        return use(b);
     }
     // at least twice the last one: the buffers left behind add up to less than the one in use
     pkv_cache::StreamWs b{stream, capture, false, nullptr, std::max(bytes, 2 * most)};
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed; // an allocation is no part of the capture
-    cudaThreadExchangeStreamCaptureMode(&mode);
-    e = cudaMalloc(reinterpret_cast<void **>(&b.p), (size_t)b.bytes);
+    e = allocate_workspace(c, b.bytes, &b.p);
     if (e != cudaSuccess && b.bytes > bytes) {
-        cudaGetLastError();
         b.bytes = bytes;
-        e = cudaMalloc(reinterpret_cast<void **>(&b.p), (size_t)b.bytes);
+        e = allocate_workspace(c, b.bytes, &b.p);
     }
-    cudaThreadExchangeStreamCaptureMode(&mode);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return pkv_fail(PKV_ENOMEM, "decode workspace of %lld bytes: %s", (long long)bytes, cudaGetErrorString(e));
-    }
+    if (e != cudaSuccess)
+        return pkv_fail(e == cudaErrorMemoryAllocation ? PKV_ENOMEM : PKV_ECUDA, "decode workspace of %lld bytes: %s",
+                        (long long)bytes, cudaGetErrorString(e));
     c->stream_ws.push_back(b);
-    *ws = b.p;
-    return PKV_OK;
+    return use(b);
 }
 
 int pkv_fail(int status, const char *fmt, ...) {
@@ -305,9 +326,9 @@ int kv_cache_view(pkv_cache_t c, void **base, int64_t strides_elems[5], int64_t 
         pkv_row_strides(c, &block, &head, &v);
         const bool i4 = c->kv_dtype == PKV_INT4; // elements are nibbles: two a byte
         strides_elems[0] = i4 ? 2 * block : 2 * c->num_kv_heads * tile;
-        strides_elems[1] = i4 ? 2 * v : c->num_kv_heads * tile;
+        strides_elems[1] = i4 ? 0 : c->num_kv_heads * tile;
         strides_elems[2] = i4 ? 2 * head : tile;
-        strides_elems[3] = c->head_dim;
+        strides_elems[3] = i4 ? 0 : c->head_dim;
         strides_elems[4] = 1;
     }
     if (num_bytes) *num_bytes = c->pool_bytes;
@@ -322,17 +343,15 @@ int kv_cache_reserve(pkv_cache_t c, int max_seqs, int max_q_heads, int max_block
         const int64_t floats = max_q_heads > 0 && max_seqs > 0
                                    ? decode_mma_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq)
                                    : 0;
+        if (floats <= 0) return PKV_OK;
+        pkv_cache::StreamWs b{0, 0, true, nullptr, (floats * (int64_t)sizeof(float) + 255) / 256 * 256};
         std::lock_guard<std::mutex> lk(c->ws_mu);
-        for (auto &b : c->stream_ws)
-            if (b.spare && b.bytes >= floats * (int64_t)sizeof(float)) return PKV_OK;
-        if (floats == 0) return PKV_OK;
-        pkv_cache::StreamWs b{0, 0, true, nullptr, floats * (int64_t)sizeof(float)};
-        cudaError_t e = cudaMalloc(reinterpret_cast<void **>(&b.p), (size_t)b.bytes);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return pkv_fail(PKV_ENOMEM, "decode workspace of %lld bytes: %s", (long long)b.bytes,
-                            cudaGetErrorString(e));
-        }
+        for (auto &have : c->stream_ws)
+            if (have.spare && have.bytes >= b.bytes) return PKV_OK;
+        cudaError_t e = allocate_workspace(c, b.bytes, &b.p);
+        if (e != cudaSuccess)
+            return pkv_fail(e == cudaErrorMemoryAllocation ? PKV_ENOMEM : PKV_ECUDA,
+                            "decode workspace of %lld bytes: %s", (long long)b.bytes, cudaGetErrorString(e));
         c->stream_ws.push_back(b);
         return PKV_OK;
     }
@@ -430,7 +449,7 @@ int paged_decode_attention_mass(const void *q, pkv_cache_t c, const int32_t *blo
     if (int r = check_device(c)) return r;
     MmaDecodeLaunch d{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale,
                       attn_mass, mass_len, decay};
-    return decode_mma_entry(c, d, nullptr, 0, static_cast<cudaStream_t>(stream));
+    return decode_mma_entry(c, d, nullptr, static_cast<cudaStream_t>(stream));
 }
 
 int paged_kv_evict(pkv_cache_t c, const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
@@ -480,8 +499,8 @@ int paged_decode_attention(const void *q, pkv_cache_t c, const int32_t *block_ta
     if (int r = check_device(c)) return r;
     if (c->kv_dtype == PKV_INT4) {
         MmaDecodeLaunch d{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale,
-                          nullptr, 0, 1.f};
-        return decode_mma_entry(c, d, nullptr, 0, static_cast<cudaStream_t>(stream));
+                          nullptr, -1, 1.f};
+        return decode_mma_entry(c, d, nullptr, static_cast<cudaStream_t>(stream));
     }
     // a batch larger than one launch takes runs in consecutive launches that share the workspace
     const int per_launch = std::min(num_seqs, decode_seqs_per_launch(c, num_q_heads / c->num_kv_heads));

@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
                 const int kv = r >= row_chunks ? 1 : 0, hc = r - kv * row_chunks, h = hc / cpr, c = hc - h * cpr;
                 const Int4Row row = int4_quantise<MT>(src[u], cpr, lanes);
                 char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, a.d);
-                *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, a.bs, a.d) + c * 4) = row.codes;
-                if (c == 0) *reinterpret_cast<uint32_t *>(tile + int4_params(kv, off, a.bs, a.d)) = row.params;
+                *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, c * 4, a.d)) = row.codes;
+                if (c == 0) *reinterpret_cast<uint32_t *>(tile + int4_params(kv, off, a.d)) = row.params;
             }
         }
     }
@@ -237,8 +237,8 @@ PKV_DEV uint4 gather_chunk(const GatherArgs &a, int64_t blk, int off, int kv, in
             for (int i = 0; i < 8; ++i) f[i] *= sc;
         } else {
             const char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, a.d);
-            int4_values<MT>(*reinterpret_cast<const uint32_t *>(tile + int4_codes(kv, off, a.bs, a.d) + c * 4),
-                            *reinterpret_cast<const uint32_t *>(tile + int4_params(kv, off, a.bs, a.d)), f);
+            int4_values<MT>(*reinterpret_cast<const uint32_t *>(tile + int4_codes(kv, off, c * 4, a.d)),
+                            *reinterpret_cast<const uint32_t *>(tile + int4_params(kv, off, a.d)), f);
         }
         return make_uint4(M::pack(f[0], f[1]), M::pack(f[2], f[3]), M::pack(f[4], f[5]), M::pack(f[6], f[7]));
     }

@@ -1,0 +1,519 @@
+// Decode attention over a 4-bit cache, with or without attention mass.
+//
+// What it computes, for sequence s, query head h of KV head g = h / G, L = context_lens[s]:
+//     x_t = scale * q[s][h] . K_t,   p_t = exp(x_t) / sum_u exp(x_u),   out[s][h] = sum_t p_t V_t
+// and, where asked, mass[s][g][t] := decay * mass[s][g][t] + sum_{h in group g} p[s][h][t].
+// A row stands for K_t = s_t c_t + z_t (c in 0..15, one s and z per row), so
+//     q . K_t = s_t (q . c_t) + z_t sum(q),     sum_t p_t V_t = sum_t (p_t s_t) c_t + sum_t p_t z_t:
+// the matrix products run on the codes themselves; steps and offsets are two scalars per token outside them.
+//
+// What bounds it: the bytes of the cache (68 B per row and head at D = 128).  At the measured 6.78 TB/s an
+// SM gets 24 B = 47 codes per clock, too many to widen one by one: widening through shared memory for
+// tcgen05 operands would write 94 B and read 94 B per clock of its 128, and one fp32 FMA per code would take
+// 47 of the 128 lanes on top of the unpacking.  mma.sync takes its operands from registers, so a code
+// travels global -> shared (bulk copy) -> register once and is widened there.
+//   * Codes as fp16: the stored words (int4.cuh) hold each nibble where an fp16 reads it as c 2^-21 or
+//     c 2^-17, so widening is one AND per two codes and a byte exchange per eight: no bias to subtract.  The
+//     products take such numbers exactly; their sums keep them to 2^-17 of a code step at the largest q
+//     (2^-24 of the exponent that subnormal numbers count as), far below the half step of the codes.  The
+//     powers of two go into q (a sixteenth for odd elements), the score and the accumulator.
+//   * K tile: A operand (16 tokens x D codes), q^T: B operand (D x 8 heads).  V tile: A operand (16 dims x
+//     16 tokens at a time), P^T: B operand (16 tokens x 8 heads).  The order of the summed index is free, so
+//     each thread takes whole pieces of a row as they lie, and q is laid out once per unit in the same
+//     order.  P goes from the first product's layout to the second's by movmatrix.
+//   * The second product takes P as fp16 hi + lo parts (2^-20 relative), so that rounding P does not
+//     show: with up to four heads the lo part uses the four columns of B that are free anyway; with eight it
+//     takes a second product.  One head alone leaves every other column of its thread's two empty.
+//   * p_t s_t is divided by a power of two A >= every s_t seen (A moves with the accumulator like the
+//     running maximum does), so that fp16 holds it whatever the steps' magnitude.
+//   * Queries are scaled by a power of two per head so that their largest element is in [2^10, 2^11): fp16
+//     then holds them (and a sixteenth of them) to 2^-31 of that element or better.
+//   * Four warps share a unit's 32-token tiles (whose is fixed by the tile's number), each with its own ring of tiles, no barrier between
+//     warps inside a unit, and the next unit's first tiles on their way before this one is joined.  A tile is
+//     one run of the pool per block: one lane per block copies it, completion counted on an mbarrier
+//     (bounded waits).  One warp in turn finds the next unit, fetches its table and q and lays q out for
+//     all four.
+//   * The running maximum moves only when a score passes it by 2^8 (the weights stay below 2^8, which hi + lo
+//     holds as well as 1), so the accumulator is rescaled about once a unit.
+//   * Scores, softmax statistics, sums and accumulators are fp32.
+#pragma once
+
+#include <type_traits>
+
+#include "mma_common.cuh"
+
+namespace pkv_mma {
+
+template <int D>
+struct Geo4 {
+    static constexpr int kOct = 8 * (D + 8);  // 8 tokens' K, V, (s, z), as in the pool
+    static constexpr int kTile = 32;          // tokens
+    static constexpr int kBytes = 4 * kOct;
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kCtas = 4; // per SM
+};
+
+// Nibbles 0..3 of each 16-bit half of w -> four fp16 pairs (low half, high half): c 2^-21 for nibbles 0
+// and 2, c 2^-17 for nibbles 1 and 3.  v is w with the bytes of each half exchanged.
+PKV_DEV void widen4(uint32_t w, uint32_t v, uint32_t *h) {
+    h[0] = w & 0x00780078u;
+    h[1] = w & 0x07800780u;
+    h[2] = v & 0x00780078u;
+    h[3] = v & 0x07800780u;
+}
+
+// GC: 1 query head per KV head, 4 (two or four), 8
+template <int D, int MT, int GC, bool MASS>
+__global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(const Args a) {
+    using G_ = Geo4<D>;
+    constexpr int KS = D / 16;             // k steps of the first product = m tiles of the second
+    constexpr int ST = G_::kStages, T = G_::kTile;
+    constexpr int NC = GC == 1 ? 1 : 2;    // columns of a thread that count
+    constexpr int COLS = GC, LD = D + 4;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ Join J;
+    __shared__ int sm_tmp[2 * kWarps];
+    __shared__ uint64_t sm_bars[kWarps * ST];
+    __shared__ Unit sm_unit[2];
+    __shared__ float sm_Q[2][8], sm_SQ[2][8]; // per column: the score's scale, sum(q) times it
+    __shared__ int sm_bad[2];
+    float *oacc = reinterpret_cast<float *>(smem + kWarps * ST * G_::kBytes); // [warp][COLS][LD]
+    uint4 *frags = reinterpret_cast<uint4 *>(oacc + kWarps * COLS * LD);      // two units' q as B operands
+    char *qraw = reinterpret_cast<char *>(frags + 2 * KS / 2 * 32);           // q rows as they lie
+    const int tb_len = a.split_tokens >> a.bs_log2;
+    int *tb = reinterpret_cast<int *>(qraw + COLS * D * 2); // two units' table entries
+    int *full = tb + 2 * tb_len;
+    int *part = full + a.num_seqs + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int G = a.group, bl = a.bs_log2, bs = 1 << bl;
+    char *ring = smem + warp * ST * G_::kBytes;
+    const uint32_t ring_u = smem_u32(ring);
+    uint64_t *bars = sm_bars + warp * ST;
+    uint32_t phase = 0; // of the slot being read, a bit per slot
+    bool alive = true;  // false after a wait ran out: nothing more is copied or waited for
+    if (lane < ST) mbar_init(&bars[lane], 1);
+    fence_mbarrier_init();
+    const uint64_t policy = l2_policy_evict_first();
+    pdl_wait();
+    list_units(a, full, part, sm_tmp);
+    const int nfull = full[a.num_seqs] * a.hkv, nunits = nfull + part[a.num_seqs] * a.hkv;
+    if ((int)blockIdx.x >= nunits) return;
+
+    // Tile `tile` of unit u to slot `slot`, a lane per block: whole octets (what lies behind the sequence's
+    // end is masked later: its codes are numbers, whatever they are).
+    const int lane_t = lane << bl;                       // this lane's block's first token in a tile
+    const uint32_t lane_bytes = (bs >> 3) * G_::kOct;    // bytes of a block's tile part
+    auto issue = [&](const Unit &u, const int *table, int tile, int slot) {
+        const int t = tile * T + lane_t;
+        int b = -1;
+        if (lane_t < T && t < u.n) b = table[t >> bl];
+        const unsigned copies = __ballot_sync(0xffffffffu, b >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&bars[slot], __popc(copies) * lane_bytes);
+        __syncwarp();
+        if (b >= 0)
+            bulk_g2s_hint(ring + slot * G_::kBytes + lane * lane_bytes, a.pool + b * a.blk_stride + u.kvh * a.head_stride,
+                          lane_bytes, &bars[slot], policy);
+    };
+    // One warp's work for a unit of buffer `par`: find it and start its copies ...
+    auto fetch = [&](int ui, int par) {
+        const Unit v = unit_of(a, full, part, nfull, ui);
+        if (lane == 0) sm_unit[par] = v;
+        stage_unit<D>(a, v, tb + par * tb_len, qraw, lane, 32);
+        cp_commit();
+    };
+    // ... and when they have landed check the table and lay out q in the order of the K codes.
+    auto prepare = [&](int par) {
+        cp_wait<0>();
+        __syncwarp();
+        const bool bad = check_table(a, sm_unit[par], tb + par * tb_len, lane, 32);
+        if (__any_sync(0xffffffffu, bad) && lane == 0) sm_bad[par] = 1;
+        else if (lane == 0) sm_bad[par] = 0;
+        const char *q = qraw + (GC == 8 ? g : GC == 1 ? 0 : (g & 3) % G) * D * 2;
+        float x[KS][4];
+        float mx = 0.f, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) { // word w of the thread's quarter row
+            float f[8];
+            cvt8<MT>(*reinterpret_cast<const uint4 *>(q + (t4 * (D / 4) + 8 * w) * 2), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[2 * w + ((i & 3) >> 1)][2 * (i & 1) + (i >> 2)] = f[i]; // pairs (i, i + 4), two pairs a step
+                mx = fmaxf(mx, fabsf(f[i]));
+                sum += f[i];
+            }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int e = (int)(__float_as_uint(mx) >> 23); // biased exponent of the head's largest element
+        const int sh = (e == 0 || e == 255) ? 0 : min(max(10 - (e - 127), -100), 100);
+        const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
+        if (t4 == 0) {
+            sm_Q[par][g] = a.qk_scale_log2 * __uint_as_float((uint32_t)(127 - sh) << 23) * 2097152.f; // 2^21
+            sm_SQ[par][g] = sum * a.qk_scale_log2;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) { // odd nibbles (second pairs) a sixteenth
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = i & 1 ? up * 0.0625f : up;
+                w[i] = ModelT<PKV_F16>::pack(x[k + (i >> 1)][2 * (i & 1)] * f, x[k + (i >> 1)][2 * (i & 1) + 1] * f);
+            }
+            frags[(par * (KS / 2) + k / 2) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    };
+
+    int par = 0; // which of the two buffers is this unit's
+    if (warp == 0) {
+        fetch(blockIdx.x, 0);
+        prepare(0);
+    }
+    __syncthreads();
+    Unit u = sm_unit[0];
+    int *table = tb;
+    bool bad = sm_bad[0] != 0;
+    int turn = 1; // the warp that prepares the next unit, and takes a tile less of this one
+    int slot = 0; // the slot of this warp's next tile
+    int nt = 0;   // this warp's tiles of the unit
+    // Tile i of this warp: the others take one each before the warp whose turn it is gets its first.
+    auto tile_of = [&](int i) {
+        const int r = (warp - turn + kWarps - 1) & (kWarps - 1); // 3: this warp prepares the next unit
+        return r == 3 ? 4 * i + 6 : i == 0 ? r : 4 * i + r - 1;
+    };
+    auto start = [&]() {
+        const int ntiles = (u.n + T - 1) / T, r = (warp - turn + kWarps - 1) & (kWarps - 1);
+        nt = r == 3 ? max(0, ntiles - 3) / 4 : ntiles <= r ? 0 : 1 + max(0, ntiles - r) / 4;
+        if (!alive) return;
+        int to = slot;
+#pragma unroll
+        for (int i = 0; i < ST; ++i) {
+            if (i < nt) issue(u, table, tile_of(i), to);
+            to = to == ST - 1 ? 0 : to + 1;
+        }
+    };
+    start();
+
+    Unit prev = u;        // the last unit, if it still has to be counted
+    bool pending = false;
+    for (int ui = blockIdx.x;;) {
+        int before = 0;
+        if (!MASS && pending && threadIdx.x == 0) before = count_unit(a, prev);
+        const int un = ui + gridDim.x;
+        const bool more = un < nunits;
+        if (warp == turn && more) fetch(un, par ^ 1);
+        uint32_t qf[KS][2];
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+            const uint4 w = frags[(par * (KS / 2) + k / 2) * 32 + lane];
+            qf[k][0] = w.x;
+            qf[k][1] = w.y;
+            qf[k + 1][0] = w.z;
+            qf[k + 1][1] = w.w;
+        }
+        float Q[NC], SQ[NC]; // of columns 2 t4 (and 2 t4 + 1)
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            Q[k] = sm_Q[par][2 * t4 + k];
+            SQ[k] = sm_SQ[par][2 * t4 + k];
+        }
+
+        // reference maxima; the finite ones to subtract; the scores above which they move
+        float m[2] = {-INFINITY, -INFINITY}, mu[2] = {0.f, 0.f}, lim[2] = {-INFINITY, -INFINITY};
+        float l[2] = {0.f, 0.f}, z[2] = {0.f, 0.f};
+        float A = 0.f, invA = 1.f;
+        float acc[KS][4];
+#pragma unroll
+        for (int i = 0; i < KS; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        // the lanes whose columns carry the lo parts (up to four heads: columns 4..7)
+        const uint32_t lo_mask = GC != 8 && t4 >= 2 ? 0xFFFFE000u : 0u;
+
+        for (int i = 0; i < nt; ++i) {
+            if (!mbar_wait(&bars[slot], (phase >> slot) & 1)) {
+                set_error(a.err, PKV_DEVERR_TIMEOUT);
+                alive = false;
+            }
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            phase ^= 1u << slot;
+            const uint32_t tile = ring_u + slot * G_::kBytes;
+            const uint32_t at_k = tile + g * (D / 2) + t4 * (D / 8), at_p = tile + 8 * D + g * 4;
+            const int t0 = tile_of(i) * T;
+            const int left = u.n - t0;
+
+            // ---- scores of tokens g, g + 8, g + 16, g + 24 for the thread's columns
+            float x[4][NC];
+            float vs[4], vz[4]; // V's step and offset
+            auto scores = [&](auto half) {
+                constexpr int hh = decltype(half)::value;
+                constexpr int O0 = 2 * hh * G_::kOct, O1 = O0 + G_::kOct;
+                uint32_t ka[D / 32], kb[D / 32];
+                if constexpr (D == 128) {
+                    lds128<O0>(ka, at_k);
+                    lds128<O1>(kb, at_k);
+                } else {
+                    lds64<O0>(ka, at_k);
+                    lds64<O1>(kb, at_k);
+                }
+                float c[4];
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    uint32_t ha[4], hb[4];
+                    widen4(ka[w], __byte_perm(ka[w], 0, 0x2301), ha);
+                    widen4(kb[w], __byte_perm(kb[w], 0, 0x2301), hb);
+                    if (w == 0)
+                        mma_first<PKV_F16>(c, ha[0], hb[0], ha[1], hb[1], qf[2 * w][0], qf[2 * w][1]);
+                    else
+                        mma<PKV_F16>(c, ha[0], hb[0], ha[1], hb[1], qf[2 * w][0], qf[2 * w][1]);
+                    mma<PKV_F16>(c, ha[2], hb[2], ha[3], hb[3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
+                }
+                const uint32_t kp[2] = {lds32<O0>(at_p), lds32<O1>(at_p)};
+                const uint32_t vp[2] = {lds32<O0 + 32>(at_p), lds32<O1 + 32>(at_p)};
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float s = lo_f(kp[r], MT), o = hi_f(kp[r], MT);
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) x[2 * hh + r][k] = fmaf(c[2 * r + k] * Q[k], s, o * SQ[k]);
+                    vs[2 * hh + r] = lo_f(vp[r], MT);
+                    vz[2 * hh + r] = hi_f(vp[r], MT);
+                }
+            };
+            scores(std::integral_constant<int, 0>());
+            scores(std::integral_constant<int, 1>());
+            if (left < T || bad) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (g + 8 * r >= left || (bad && table[(t0 + g + 8 * r) >> bl] < 0)) {
+#pragma unroll
+                        for (int k = 0; k < NC; ++k) x[r][k] = -INFINITY;
+                        vs[r] = vz[r] = 0.f;
+                    }
+            }
+            if constexpr (MASS) {
+                float *dst = a.ws_x + (((int64_t)u.s * a.hkv + u.kvh) * a.cap + u.t0 + t0 + g) * G;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (g + 8 * r < left) {
+                        if constexpr (GC == 1) {
+                            if (t4 == 0) dst[8 * r] = x[r][0];
+                        } else if (2 * t4 < G) {
+                            *reinterpret_cast<float2 *>(dst + 8 * r * G + 2 * t4) = make_float2(x[r][0], x[r][NC - 1]);
+                        }
+                    }
+            }
+
+            // ---- reference maximum and the divisor of p s (they move rarely: one vote a tile)
+            float n_[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < NC; ++k) n_[k] = fmaxf(fmaxf(x[0][k], x[1][k]), fmaxf(x[2][k], x[3][k]));
+            float ns = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+            bool up = ns > A;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) up = up || n_[k] > lim[k];
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) n_[k] = fmaxf(n_[k], __shfl_xor_sync(0xffffffffu, n_[k], o));
+                    ns = fmaxf(ns, __shfl_xor_sync(0xffffffffu, ns, o));
+                }
+                float f[2] = {1.f, 1.f};
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    n_[k] = fmaxf(n_[k], m[k]);
+                    f[k] = m[k] == n_[k] ? 1.f : fast_exp2(m[k] - n_[k]);
+                    m[k] = n_[k];
+                    mu[k] = m[k] == -INFINITY ? 0.f : m[k];
+                    lim[k] = m[k] + 8.f;
+                    l[k] *= f[k];
+                    z[k] *= f[k];
+                }
+                if (ns > A) { // a power of two twice to four times the largest step (its reciprocal stays normal)
+                    const int e = min(max((int)(__float_as_uint(ns) >> 23) + 2, 2), 252);
+                    const float nA = __uint_as_float((uint32_t)e << 23);
+                    invA = __uint_as_float((uint32_t)(254 - e) << 23);
+                    f[0] *= A * invA;
+                    f[1] *= A * invA;
+                    A = nA;
+                }
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    acc[k][0] *= f[0];
+                    acc[k][1] *= f[1];
+                    acc[k][2] *= f[0];
+                    acc[k][3] *= f[1];
+                }
+            }
+            // ---- P^T as the second product's B operand: hi parts (columns 0..3) and lo parts (4..7), or
+            // for eight heads one after the other
+            uint32_t b[4], bl_[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float w[2] = {0.f, 0.f};
+                const float sv = vs[r] * invA;
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const float p = fast_exp2(x[r][k] - mu[k]);
+                    l[k] += p;
+                    z[k] = fmaf(p, vz[r], z[k]);
+                    w[k] = p * sv;
+                }
+                if constexpr (GC == 8) {
+                    b[r] = movmatrix(pack_rz<PKV_F16>(w[0], w[1]));
+                    bl_[r] = movmatrix(pack_rz<PKV_F16>(w[0] - kept_rz<PKV_F16>(w[0]), w[1] - kept_rz<PKV_F16>(w[1])));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) w[k] -= __uint_as_float(__float_as_uint(w[k]) & lo_mask);
+                    b[r] = movmatrix(pack_rz<PKV_F16>(w[0], w[1]));
+                }
+            }
+
+            // ---- acc[dims][column] += V^T P^T: rows 2 t4, 2 t4 + 1 of each octet (places t4 and t4 + 4), this
+            // thread's D / 8 codes of each
+            const uint32_t at_v = D == 128 ? tile + t4 * 64 + ((g * 8) ^ ((t4 & 2) << 4)) : tile + t4 * 32 + g * 4;
+            auto outputs = [&](auto half) {
+                constexpr int hh = decltype(half)::value;
+                constexpr int W = D / 64, O0 = 2 * hh * G_::kOct + 4 * D, O1 = O0 + G_::kOct, P4 = 4 * (D / 2);
+                uint32_t v[4][W];
+                if constexpr (W == 1) {
+                    v[0][0] = lds32<O0>(at_v);
+                    v[1][0] = lds32<O0 + P4>(at_v);
+                    v[2][0] = lds32<O1>(at_v);
+                    v[3][0] = lds32<O1 + P4>(at_v);
+                } else {
+                    lds64<O0>(v[0], at_v);
+                    lds64<O0 + P4>(v[1], at_v);
+                    lds64<O1>(v[2], at_v);
+                    lds64<O1 + P4>(v[3], at_v);
+                }
+                uint32_t h[2][D / 8]; // token pairs of the two octets: code pairs by dim
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const uint32_t x0 = v[2 * r][w], x1 = v[2 * r + 1][w];
+                        widen4(__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x4501), &h[r][8 * w]);
+                        widen4(__byte_perm(x0, x1, 0x7632), __byte_perm(x0, x1, 0x6723), &h[r][8 * w + 4]);
+                    }
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    mma<PKV_F16>(acc[k], h[0][k], h[0][k + KS], h[1][k], h[1][k + KS], b[2 * hh], b[2 * hh + 1]);
+                    if constexpr (GC == 8)
+                        mma<PKV_F16>(acc[k], h[0][k], h[0][k + KS], h[1][k], h[1][k + KS], bl_[2 * hh], bl_[2 * hh + 1]);
+                }
+            };
+            outputs(std::integral_constant<int, 0>());
+            outputs(std::integral_constant<int, 1>());
+            __syncwarp(); // every lane has read the slot
+            if (i + ST < nt) issue(u, table, tile_of(i + ST), slot);
+            slot = slot == ST - 1 ? 0 : slot + 1;
+        }
+
+        // ---- the next unit's first tiles, then this unit's join
+        if (warp == turn && more) prepare(par ^ 1);
+        turn = turn == kWarps - 1 ? 0 : turn + 1;
+        if (g == 0) {
+#pragma unroll
+            for (int k = 0; k < NC; ++k) J.m[warp][2 * t4 + k] = m[k];
+        }
+        if (!MASS && threadIdx.x == 0) J.last = pending && before == prev.nsplit - 1;
+        __syncthreads();
+        const Unit cur = u;
+        par ^= 1;
+        if (more) {
+            u = sm_unit[par];
+            bad = sm_bad[par] != 0;
+            table = tb + par * tb_len;
+            start();
+        }
+        if constexpr (!MASS) {
+            if (J.last) {
+                __threadfence();
+                join_row<D, MT>(a, prev, J);
+            }
+        }
+        {
+            Weight w[NC];
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                w[k] = warp_weight(J, warp, 2 * t4 + k);
+                l[k] = row_sum(l[k]);
+                z[k] = w[k].w == 0.f ? 0.f : row_sum(z[k]) * w[k].w;
+                if (g == 0) {
+                    J.l[warp][2 * t4 + k] = w[k].w == 0.f ? 0.f : l[k] * w[k].w;
+                    if (warp == 0) J.M[2 * t4 + k] = w[k].M;
+                }
+            }
+            // hi and lo columns together, the codes' powers of two and A, the warp's weight, the offsets
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (NC == 1 && (e & 1)) continue;
+                    float v = acc[k][e];
+                    if constexpr (GC != 8) v += __shfl_xor_sync(0xffffffffu, v, 2);
+                    acc[k][e] = fmaf(v * (k & 1 ? 131072.f : 2097152.f), A * w[e & (NC - 1)].w, z[e & (NC - 1)]);
+                }
+            if (2 * t4 < COLS) { // 16 (or 8) dims from (D / 8) g of each column
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    float *o = oacc + (warp * COLS + 2 * t4 + c) * LD + (D / 8) * g;
+#pragma unroll
+                    for (int k = 0; k < KS; k += 4) {
+                        *reinterpret_cast<float4 *>(o + k) =
+                            make_float4(acc[k][c], acc[k + 1][c], acc[k + 2][c], acc[k + 3][c]);
+                        *reinterpret_cast<float4 *>(o + KS + k) =
+                            make_float4(acc[k][c + 2], acc[k + 1][c + 2], acc[k + 2][c + 2], acc[k + 3][c + 2]);
+                    }
+                }
+            }
+        }
+        join_unit<D, COLS, MT, MASS>(a, cur, J, oacc);
+        prev = cur;
+        pending = !MASS && cur.nsplit > 1 && a.done;
+        if (!more) break;
+        ui = un;
+    }
+    if constexpr (!MASS) {
+        if (pending) {
+            if (threadIdx.x == 0) J.last = count_unit(a, prev) == prev.nsplit - 1;
+            __syncthreads();
+            if (J.last) {
+                __threadfence();
+                join_row<D, MT>(a, prev, J);
+            }
+        }
+    }
+    pdl_trigger();
+}
+
+template <int D, int MT, int GC, bool MASS>
+cudaError_t launch_int4_t(const Args &a, int sms, cudaStream_t st) {
+    using G_ = Geo4<D>;
+    static std::atomic<int> have[64];
+    auto kern = decode_int4_kernel<D, MT, GC, MASS>;
+    const size_t smem = (size_t)kWarps * G_::kStages * G_::kBytes + kWarps * GC * (D + 4) * sizeof(float) +
+                        2 * (D / 32) * 32 * 16 + GC * D * 2 + (2 * (a.num_seqs + 1) + 2 * (a.split_tokens >> a.bs_log2)) * sizeof(int);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), smem, have);
+    if (e != cudaSuccess) return e;
+    return pdl_launch(kern, dim3(grid_of(a, sms * G_::kCtas)), dim3(kThreads), smem, st, a);
+}
+
+template <int MT, bool MASS>
+cudaError_t dispatch_int4(const Args &a, int D, int sms, bool merge, cudaStream_t st) {
+    if (merge) return D == 64 ? launch_merge_t<64, MT, MASS>(a, sms, st) : launch_merge_t<128, MT, MASS>(a, sms, st);
+#define PKV_INT4_CASE(DD, GC)                                                                                          \
+    if (D == DD && (GC == 4 ? a.group == 2 || a.group == 4 : a.group == GC))                                           \
+        return launch_int4_t<DD, MT, GC, MASS>(a, sms, st);
+    PKV_INT4_CASE(64, 1)
+    PKV_INT4_CASE(64, 4)
+    PKV_INT4_CASE(64, 8)
+    PKV_INT4_CASE(128, 1)
+    PKV_INT4_CASE(128, 4)
+    PKV_INT4_CASE(128, 8)
+#undef PKV_INT4_CASE
+    return cudaErrorNotSupported;
+}
+
+} // namespace pkv_mma

@@ -1,9 +1,11 @@
-// Host side of the matrix-instruction decode (decode_mma.cuh): split size, workspace, launches.
-#include "decode_mma.cuh"
+// Host side of the matrix-instruction decodes (decode_int4.cuh, decode_mma.cuh): split size, workspace, launches.
+#include "mma_common.cuh"
 
 #include <algorithm>
 
 namespace {
+
+constexpr int kMaxSplit = 1024; // tokens
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -18,19 +20,22 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     const bool mass = mass_len >= 0;
     p->cap = (int64_t)max_blocks * c->block_size;
     if (mass) p->cap = std::min(p->cap, mass_len);
-    // Two units per resident CTA at the table's full width: fewer leave SMs idle at the end, more make
-    // units so short that their fixed costs (q, the warps' join, the partial) show.  At least 64 tokens
-    // (a tile per warp), at most kMaxSplit; more only to keep a row's splits within 1024.  A function of
-    // the call's shapes, never of the lengths: a result does not change with the other sequences' lengths.
-    const int64_t slots = (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
+    // Two units per resident CTA at the table's full
+    // width: fewer leave SMs idle at the end, more make units so short that their fixed costs (q, the join, the
+    // partial) show.  At least 64 tokens, at most kMaxSplit; more only to keep a row's splits within 1024.  A
+    // function of the call's shapes, never of the lengths: a result does not change with the other sequences'
+    // lengths.
+    const bool i4 = c->kv_dtype == PKV_INT4;
+    const int64_t workers = (int64_t)c->num_sms * (i4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
     const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads;
-    int64_t split = round_up((rows * p->cap + 2 * slots - 1) / (2 * slots), 64);
-    split = std::max<int64_t>(64, std::min<int64_t>(split, pkv_mma::kMaxSplit));
+    int64_t split = round_up((rows * p->cap + 2 * workers - 1) / (2 * workers), 64);
+    split = std::max<int64_t>(64, std::min<int64_t>(split, kMaxSplit));
     split = std::max(split, round_up((p->cap + 1023) / 1024, 64));
-    if (split / c->block_size > 8192) return false; // the split's table entries no longer fit shared memory
+    if (split / c->block_size > (i4 ? 1024 : 8192)) return false; // the split's table entries no longer fit shared memory
     p->split = (int)split;
-    p->max_splits = (int)((p->cap + split - 1) / split);
-    const int64_t partials = p->max_splits > 1 ? (int64_t)hq * p->max_splits * (c->head_dim + 2) : 0;
+    p->max_splits = (int)std::max<int64_t>(1, (p->cap + split - 1) / split);
+    // (with mass a row of one split keeps its (m, l) too)
+    const int64_t partials = p->max_splits > 1 || mass ? (int64_t)hq * p->max_splits * (c->head_dim + 2) : 0;
     const int64_t per_seq = partials + (mass ? (int64_t)hq * p->cap : 0);
     // sequences per launch: at most kMaxSeqs, and at most 2 GB of workspace unless one sequence needs more
     int64_t n = std::min<int64_t>(num_seqs, pkv_mma::kMaxSeqs);
@@ -55,19 +60,24 @@ int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, in
     return plan_for(c, num_seqs, hq, max_blocks, -1, &p) ? p.floats : 0;
 }
 
-int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, float *scratch, int64_t scratch_floats, cudaStream_t st) {
+int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st) {
     Plan p;
-    if (!plan_for(c, d.num_seqs, d.num_q_heads, d.max_blocks, d.mass ? d.mass_len : -1, &p))
+    if (!plan_for(c, d.num_seqs, d.num_q_heads, d.max_blocks, d.mass_len, &p))
         return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this decode takes", d.max_blocks);
-    float *ws = scratch;
-    if (!scratch) {
+    PkvWorkspace ws;
+    if (!fixed) {
         if (int r = pkv_stream_workspace(c, st, p.floats, &ws)) return r;
-    } else if (p.floats > scratch_floats) {
+    } else if (p.floats > fixed->floats) {
         return pkv_fail(PKV_EINVAL,
                         "no-alloc decode needs %lld bytes of scratch for %d sequences x %d query heads x %d splits; "
                         "its fixed scratch holds %lld bytes (use fewer sequences per call or paged_decode_attention)",
-                        (long long)(p.floats * 4), p.seqs, d.num_q_heads, p.max_splits, (long long)(scratch_floats * 4));
+                        (long long)(p.floats * 4), p.seqs, d.num_q_heads, p.max_splits, (long long)(fixed->floats * 4));
+    } else {
+        ws = *fixed;
     }
+    // few splits: the CTA that finishes a row last joins them (no second launch); many: merge_kernel
+    const bool mass = d.mass_len >= 0;
+    const bool join = !mass && p.max_splits <= pkv_mma::kJoinSplits && (int64_t)p.seqs * c->num_kv_heads <= ws.counters;
     pkv_mma::Args a;
     a.pool = static_cast<const char *>(c->pool);
     a.k_scale = c->k_scale;
@@ -81,6 +91,12 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, float *scratch, int
     a.hq = d.num_q_heads;
     a.hkv = c->num_kv_heads;
     a.group = d.num_q_heads / c->num_kv_heads;
+    {
+        int s = 0;
+        while (((int64_t)1 << s) < a.hkv) ++s;
+        a.hkv_shift = 31 + s;
+        a.hkv_magic = (uint32_t)((((uint64_t)1 << a.hkv_shift) + a.hkv - 1) / a.hkv);
+    }
     a.bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
     a.split_tokens = p.split;
     a.max_splits = p.max_splits;
@@ -90,28 +106,29 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, float *scratch, int
     // waits for the one before it
     for (int s0 = 0; s0 < d.num_seqs; s0 += p.seqs) {
         const int n = std::min(p.seqs, d.num_seqs - s0);
-        const int64_t rows = (int64_t)n * d.num_q_heads * (p.max_splits > 1 ? p.max_splits : 0);
+        const int64_t rows = (int64_t)n * d.num_q_heads * (p.max_splits > 1 || mass ? p.max_splits : 0);
         const int64_t row_bytes = (int64_t)d.num_q_heads * c->head_dim * 2;
         a.q = static_cast<const char *>(d.q) + s0 * row_bytes;
         a.out = static_cast<char *>(d.out) + s0 * row_bytes;
         a.tables = d.tables ? d.tables + (int64_t)s0 * d.max_blocks : nullptr;
         a.lens = d.lens + s0;
         a.num_seqs = n;
-        a.ws_o = ws;
-        a.ws_ml = ws + rows * c->head_dim;
-        a.ws_x = ws + rows * (c->head_dim + 2);
-        a.mass = d.mass ? d.mass + (int64_t)s0 * c->num_kv_heads * d.mass_len : nullptr;
+        a.ws_o = ws.p;
+        a.ws_ml = ws.p + rows * c->head_dim;
+        a.ws_x = ws.p + rows * (c->head_dim + 2);
+        a.done = join ? ws.done : nullptr;
+        a.mass = mass ? d.mass + (int64_t)s0 * c->num_kv_heads * d.mass_len : nullptr;
         cudaError_t e;
         {
             PkvTimer timer(c, PKV_KIND_DECODE, st);
             g_pkv_launches++;
-            e = run(c, a, d.mass != nullptr, false, st);
+            e = run(c, a, mass, false, st);
         }
         if (e != cudaSuccess) return pkv_cuda_fail(e, "decode launch");
-        if (p.max_splits > 1) {
+        if (mass || (p.max_splits > 1 && !join)) {
             PkvTimer timer(c, PKV_KIND_MERGE, st);
             g_pkv_launches++;
-            e = run(c, a, d.mass != nullptr, true, st);
+            e = run(c, a, mass, true, st);
         }
         if (e != cudaSuccess) return pkv_cuda_fail(e, "decode merge launch");
     }

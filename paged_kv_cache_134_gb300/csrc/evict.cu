@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
 
 // LPT lanes move one token's K and V rows of one head, 16 bytes each; a 4-bit row's (s, z) words go by
 // the two lanes behind them.
-template <int LPT>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int row_bytes, int par_off) {
+template <int LPT, bool I4>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int row_bytes) {
     pdl_trigger();
     pdl_wait();
     constexpr int kTokens = kMoveThreads / LPT;
@@ -167,13 +167,15 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
     const int32_t *kept = a.kept + row * a.budget;
     const int32_t *src_t = a.tables + (int64_t)s * a.max_blocks, *dst_t = a.dst_tables + (int64_t)s * a.max_dst_blocks;
     const int chunks = row_bytes / 16;
-    const bool code = lane < 2 * chunks, par = par_off && !code && lane < 2 * chunks + 2;
+    const bool code = lane < 2 * chunks, par = I4 && !code && lane < 2 * chunks + 2;
     if (!code && !par) return;
     const int kv = code ? lane / chunks : lane - 2 * chunks;
-    // bytes from a (block, head)'s start to this lane's piece of its row 0, and from row to row
-    const int64_t base = kvh * a.head_stride + (code ? kv * a.v_off + (lane - kv * chunks) * 16
-                                                     : par_off + kv * a.bs * 4);
-    const int step = code ? row_bytes : 4;
+    const int64_t base = kvh * a.head_stride;
+    // bytes from a (block, head)'s start to this lane's piece of row `o`
+    auto piece = [&](int o) -> int64_t {
+        if (!I4) return kv * a.v_off + (int64_t)o * row_bytes + (lane - kv * chunks) * 16;
+        return code ? int4_codes(kv, o, (lane - kv * chunks) * 16, a.d) : int4_params(kv, o, a.d);
+    };
     const int lim = (int)min((int64_t)a.budget, a.cap);
     for (int j0 = blockIdx.y * kTokens * kMoveUnroll; j0 < lim; j0 += gridDim.y * kTokens * kMoveUnroll) {
         const char *from[kMoveUnroll];
@@ -188,8 +190,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
                 if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
                     if (lane == 0) set_error(a.err, PKV_DEVERR_BLOCK_ID);
                 } else {
-                    from[u] = a.pool + sb * a.blk_stride + base + (t % a.bs) * step;
-                    to[u] = a.pool + db * a.blk_stride + base + (j % a.bs) * step;
+                    from[u] = a.pool + sb * a.blk_stride + base + piece(t % a.bs);
+                    to[u] = a.pool + db * a.blk_stride + base + piece(j % a.bs);
                 }
             }
         }
@@ -244,7 +246,6 @@ cudaError_t launch_evict(pkv_cache *c, const EvictLaunch &v, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const bool i4 = c->kv_dtype == PKV_INT4;
     const int row_bytes = i4 ? a.d / 2 : a.d * c->elem_bytes;
-    const int par_off = i4 ? a.bs * a.d : 0;
     const int lanes = 2 * row_bytes / 16 + (i4 ? 2 : 0);
     const int lpt = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
     const int64_t per = (int64_t)(kMoveThreads / lpt) * kMoveUnroll;
@@ -252,7 +253,7 @@ cudaError_t launch_evict(pkv_cache *c, const EvictLaunch &v, cudaStream_t st) {
     const dim3 grid(rows, (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + per - 1) / per, 65535)));
     PkvTimer timer(c, PKV_KIND_COPY, st);
     g_pkv_launches++;
-    if (lpt == 8) return pdl_launch(move_kernel<8>, grid, dim3(kMoveThreads), 0, st, a, row_bytes, par_off);
-    if (lpt == 16) return pdl_launch(move_kernel<16>, grid, dim3(kMoveThreads), 0, st, a, row_bytes, par_off);
-    return pdl_launch(move_kernel<32>, grid, dim3(kMoveThreads), 0, st, a, row_bytes, par_off);
+    auto kern = i4 ? (lpt == 8 ? move_kernel<8, true> : move_kernel<16, true>)
+                   : lpt == 8 ? move_kernel<8, false> : lpt == 16 ? move_kernel<16, false> : move_kernel<32, false>;
+    return pdl_launch(kern, grid, dim3(kMoveThreads), 0, st, a, row_bytes);
 }

@@ -1,10 +1,15 @@
 // The 4-bit cache: layout and arithmetic of its rows.
 //
-// A (block, KV head) is one run of bs * (D + 8) bytes:
-//     K codes [bs][D / 2] | V codes [bs][D / 2] | K (s, z) [bs][2] | V (s, z) [bs][2]
-// so that a head's K and V of a block lie together (a tile of any 8 rows is four aligned runs), and a
-// whole block, scales and all, is one run for block copy and swap.  Element i of a row is nibble i
-// (the low one of byte i / 2 for even i); s and z are in the model's type.
+// A (block, KV head) is one run of bs * (D + 8) bytes, an octet of 8 tokens after the other:
+//     K codes [8][D / 2] | V codes [8][D / 2] | K (s, z) [8][2] | V (s, z) [8][2]
+// so that the K and V of any 8 tokens of a head are one aligned run (one bulk copy brings a 16-token tile
+// of a block), and a whole block, scales and all, is one run for block copy and swap.  s and z are in the
+// model's type.  Elements 4 i .. 4 i + 3 of a row are the nibbles of its 16-bit word i, lowest first, the
+// word rotated left by three bits: a nibble in bits 7..10 or 3..6 of an fp16 reads c 2^-17 or c 2^-21 (fp16
+// numbers are evenly spaced up to bit 10), and exchanging the word's bytes brings the other two there.
+// V's rows stand in the order 0 2 4 6 1 3 5 7, and at D = 128 those of places 2, 3, 6 and 7 with their
+// halves swapped: the attention reads rows 0 2 4 6 (then 1 3 5 7) of 8 bytes each at once, and so finds
+// them in different banks without copying them around.
 //
 // One step and one offset per (token, head) row: they then stand outside both matrix products of the
 // attention (two scalars per token).  z is an element of the row, so the model's type holds it exactly;
@@ -20,8 +25,17 @@
 PKV_DEV int64_t int4_head(int64_t blk, int h, int hkv, int bs, int d) {
     return (blk * hkv + h) * ((int64_t)bs * (d + 8));
 }
-PKV_DEV int int4_codes(int kv, int off, int bs, int d) { return (kv * bs + off) * (d / 2); }
-PKV_DEV int int4_params(int kv, int off, int bs, int d) { return bs * d + (kv * bs + off) * 4; }
+PKV_DEV int int4_place(int r) { return (r >> 1) | ((r & 1) << 2); } // V row r of an octet
+// from a (block, head)'s start: byte `i` (a multiple of 4) of row `off`'s codes, and its (s, z)
+PKV_DEV int int4_codes(int kv, int off, int i, int d) {
+    const int oct = (off >> 3) * 8 * (d + 8), r = off & 7;
+    if (kv == 0) return oct + r * (d / 2) + i;
+    const int p = int4_place(r);
+    return oct + 4 * d + p * (d / 2) + (d == 128 ? i ^ ((p & 2) << 4) : i);
+}
+PKV_DEV int int4_params(int kv, int off, int d) {
+    return (off >> 3) * 8 * (d + 8) + 8 * d + kv * 32 + (off & 7) * 4;
+}
 
 struct Int4Row {
     uint32_t codes;  // this lane's eight
@@ -99,6 +113,7 @@ PKV_DEV Int4Row int4_quantise(const uint4 &src, int cpr, unsigned lanes) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) // the low mantissa bits of y + 1.5 * 2^23 are rint(y)
         r.codes |= (__float_as_uint(__fadd_rn(fminf(y[i], 15.f), 12582912.f)) & 15u) << (4 * i);
+    r.codes = ((r.codes << 3) & 0xFFF8FFF8u) | ((r.codes >> 13) & 0x00070007u);
     return r;
 }
 
@@ -106,6 +121,7 @@ PKV_DEV Int4Row int4_quantise(const uint4 &src, int cpr, unsigned lanes) {
 template <int MT>
 PKV_DEV void int4_values(uint32_t codes, uint32_t params, float *f) {
     const float s = half_of<MT>(params, 0), z = half_of<MT>(params, 1);
+    codes = ((codes >> 3) & 0x1FFF1FFFu) | ((codes << 13) & 0xE000E000u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = fmaf(s, (float)((codes >> (4 * i)) & 15u), z);
 }

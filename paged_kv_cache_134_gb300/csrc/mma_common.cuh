@@ -1,0 +1,515 @@
+// What the matrix-instruction decode kernels share (decode_int4.cuh, decode_mma.cuh): arguments, PTX wrappers,
+// the list of units, the join of a unit's warps and of a row's splits, the attention mass.
+//
+// A unit is (sequence, KV head, split of split_tokens tokens); persistent CTAs of four warps walk the units,
+// whole splits first.  Each warp keeps the running maximum m, the sum l and the accumulator of its tokens;
+// a unit's four are joined through shared memory in warp order.  A row's splits leave fp32 partials
+// (m, l, o): up to kJoinSplits of them are joined by the CTA that finishes the row last (a counter per row
+// that it sets back to 0), in split order, so the result does not depend on which CTA that is; more by
+// merge_kernel, whose CTAs share them out.  With attention mass a second kernel, mass_kernel, walks the same
+// units: it joins the splits and turns the stored scores into weights, which needs the row's final
+// maximum and sum.  (Done by the row's last CTA instead, it kept one CTA busy with a whole row at the end:
+// 246 us against 181 on 32 fp16 sequences of up to 4096 tokens.)
+#pragma once
+
+#include "device_common.cuh"
+#include "int4.cuh"
+#include "pkv_internal.h"
+
+namespace pkv_mma {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxSeqs = 1024;   // sequences of a launch (their unit counts sit in shared memory)
+constexpr int kJoinSplits = 16;  // splits of a row that its last CTA joins itself
+
+struct Args {
+    const void *q;
+    void *out;
+    const char *pool;
+    const float *k_scale, *v_scale; // E4M3 caches
+    const int32_t *tables, *lens;
+    float *ws_o, *ws_ml; // [S * Hq][max_splits][D], [S * Hq][max_splits][2]
+    float *ws_x;         // mass: scores in log2 units, [S * Hkv][cap][G]
+    int *done;           // units finished per row, [S * Hkv], all 0 between launches; NULL: merge_kernel joins
+    float *mass;         // [S][Hkv][mass_len]
+    unsigned int *err;
+    int64_t num_blocks;
+    int64_t blk_stride, head_stride, v_off; // bytes: block, head, V behind K
+    int64_t mass_len, cap;                  // tokens of a mass row; tokens a sequence may have
+    int max_blocks, num_seqs, hq, hkv, group, bs_log2;
+    int split_tokens, max_splits;
+    uint32_t hkv_magic; // x / hkv = x * hkv_magic >> hkv_shift for 0 <= x < 2^31
+    int hkv_shift;
+    float qk_scale_log2; // scale * log2(e)
+    float decay;
+};
+
+// (the offset rides in the instruction: no address to compute)
+template <int OFF = 0>
+PKV_DEV void lds64(uint32_t *w, uint32_t a) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(w[0]), "=r"(w[1]) : "r"(a), "n"(OFF));
+}
+template <int OFF = 0>
+PKV_DEV void lds128(uint32_t *w, uint32_t a) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a), "n"(OFF));
+}
+template <int OFF = 0>
+PKV_DEV uint32_t lds32(uint32_t a) {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(w) : "r"(a), "n"(OFF));
+    return w;
+}
+PKV_DEV void ldmatrix4(uint32_t *w, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a));
+}
+PKV_DEV void ldmatrix4t(uint32_t *w, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a));
+}
+PKV_DEV uint32_t movmatrix(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// c (16 x 8, fp32) += a (16 x 16) b (16 x 8), operands fp16 or bf16
+template <int OT>
+PKV_DEV void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (OT == PKV_F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// c = a b
+template <int OT>
+PKV_DEV void mma_first(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    const float z = 0.f;
+    if constexpr (OT == PKV_F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z));
+}
+// two pairs of E4M3 codes (low 16 bits, high 16 bits) -> two fp16 pairs (exact)
+PKV_DEV void widen8(uint32_t w, uint32_t *h) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(h[0]), "=r"(h[1])
+        : "r"(w));
+}
+PKV_DEV uint32_t bytes_of(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+PKV_DEV float lo_f(uint32_t w, int mt) {
+    return mt == PKV_F16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))) : __uint_as_float(w << 16);
+}
+PKV_DEV float hi_f(uint32_t w, int mt) {
+    return mt == PKV_F16 ? __half2float(__ushort_as_half((unsigned short)(w >> 16))) : __uint_as_float(w & 0xFFFF0000u);
+}
+
+
+template <int OT> // fp32 pair -> 16-bit pair, towards zero
+PKV_DEV uint32_t pack_rz(float lo, float hi) {
+    uint32_t r;
+    if constexpr (OT == PKV_F16)
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// the part of x that pack_rz keeps (of a normal number)
+template <int OT>
+PKV_DEV float kept_rz(float x) {
+    return __uint_as_float(__float_as_uint(x) & (OT == PKV_F16 ? 0xFFFFE000u : 0xFFFF0000u));
+}
+
+PKV_DEV int row_len(const Args &a, int s) {
+    const int L = a.lens[s];
+    return L <= 0 ? 0 : (int64_t)L > a.cap ? (int)a.cap : L;
+}
+
+// mass of tokens [t0, t1) of (sequence, KV head) row `row` from their stored scores, with the row's
+// final maxima and reciprocal sums per head; U tokens' loads at a time
+template <int G, int U>
+PKV_DEV void add_mass_g(const Args &a, int64_t row, int t0, int t1, const float *M, const float *inv) {
+    const float *x = a.ws_x + row * a.cap * G;
+    float *m = a.mass + row * a.mass_len;
+    for (int tb = t0 + threadIdx.x; tb < t1; tb += kThreads * U) {
+        float xs[U][G], old[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int t = tb + i * kThreads;
+            if (t >= t1) continue;
+            const float *src = x + (int64_t)t * G;
+            if constexpr (G == 1) {
+                xs[i][0] = __ldcg(src);
+            } else {
+#pragma unroll
+                for (int h = 0; h < G; h += 2) {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + h));
+                    xs[i][h] = v.x;
+                    xs[i][h + 1] = v.y;
+                }
+            }
+            old[i] = m[t];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int t = tb + i * kThreads;
+            if (t >= t1) continue;
+            float p = 0.f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) p = fmaf(fast_exp2(xs[i][h] - M[h]), inv[h], p);
+            m[t] = fmaf(old[i], a.decay, p);
+        }
+    }
+}
+PKV_DEV void add_mass(const Args &a, int64_t row, int t0, int t1, const float *M, const float *inv) {
+    if (a.group == 1)
+        add_mass_g<1, 8>(a, row, t0, t1, M, inv);
+    else if (a.group == 2)
+        add_mass_g<2, 4>(a, row, t0, t1, M, inv);
+    else if (a.group == 4)
+        add_mass_g<4, 4>(a, row, t0, t1, M, inv);
+    else
+        add_mass_g<8, 2>(a, row, t0, t1, M, inv);
+}
+
+// Block scan of the sequences' unit counts: full[s + 1], part[s + 1] hold the inclusive sums of whole
+// splits and of partial ones (a sequence of length 0 has one partial unit, which writes its zero row).
+PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
+    const int S = a.num_seqs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int cf = 0, cp = 0; // sums of the sequences before this pass
+    if (threadIdx.x == 0) full[0] = part[0] = 0;
+    for (int s0 = 0; s0 < S; s0 += kThreads) {
+        const int s = s0 + threadIdx.x;
+        int f = 0, p = 0;
+        if (s < S) {
+            const int L = row_len(a, s);
+            if (blockIdx.x == 0 && (int64_t)a.lens[s] > a.cap) set_error(a.err, PKV_DEVERR_LENGTH);
+            f = L / a.split_tokens;
+            p = (L % a.split_tokens != 0 || L == 0) ? 1 : 0;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int vf = __shfl_up_sync(0xffffffffu, f, o), vp = __shfl_up_sync(0xffffffffu, p, o);
+            if (lane >= o) f += vf, p += vp;
+        }
+        if (lane == 31) tmp[warp] = f, tmp[kWarps + warp] = p;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) f += tmp[w], p += tmp[kWarps + w];
+        }
+        f += cf;
+        p += cp;
+        if (s < S) full[s + 1] = f, part[s + 1] = p;
+        for (int w = 0; w < kWarps; ++w) cf += tmp[w], cp += tmp[kWarps + w];
+        __syncthreads();
+    }
+}
+
+// Largest i in [0, n) with pref[i] <= k (pref[0] = 0 <= k, non-decreasing, n <= 1024): a warp looks at 32 places at once.
+PKV_DEV int find_row(const int *pref, int n, int k) {
+    const int lane = threadIdx.x & 31, stride = (n + 31) >> 5;
+    const int at = lane * stride;
+    const int block = __popc(__ballot_sync(0xffffffffu, at < n && pref[at] <= k)) - 1;
+    const int i = block * stride + lane;
+    return block * stride + __popc(__ballot_sync(0xffffffffu, lane < stride && i < n && pref[i] <= k)) - 1;
+}
+
+struct Unit {
+    int s, kvh, j, L, nsplit;
+    int t0, n; // first token, tokens
+};
+
+// Unit u of the list (all lanes of a warp together, u the same for all).
+PKV_DEV Unit unit_of(const Args &a, const int *full, const int *part, int nfull, int u) {
+    Unit r;
+    const bool whole = u < nfull;
+    const int v = whole ? u : u - nfull;
+    const int k = (int)(((uint64_t)(uint32_t)v * a.hkv_magic) >> a.hkv_shift); // v / hkv
+    r.kvh = v - k * a.hkv;
+    r.s = find_row(whole ? full : part, a.num_seqs, k);
+    r.j = whole ? k - full[r.s] : full[r.s + 1] - full[r.s];
+    r.L = row_len(a, r.s);
+    r.nsplit = (full[r.s + 1] - full[r.s]) + (part[r.s + 1] - part[r.s]);
+    r.t0 = r.j * a.split_tokens;
+    r.n = min(r.L - r.t0, a.split_tokens);
+    return r;
+}
+
+// What a unit needs besides its tiles: its table entries and its q rows (group x D, as they lie).
+// They are copied to shared memory a unit ahead.
+PKV_DEV int blocks_of(const Args &a, const Unit &u) { return (u.n + (1 << a.bs_log2) - 1) >> a.bs_log2; }
+
+// Checks entries that have landed: an id that is no block becomes -1.  Returns whether this thread met one.
+// i0, step: this thread's share
+PKV_DEV bool check_table(const Args &a, const Unit &u, int *tb, int i0, int step) {
+    bool bad = false;
+    const int nblk = blocks_of(a, u);
+    for (int i = i0; i < nblk; i += step) {
+        const int b = tb[i];
+        if (b < 0 || b >= a.num_blocks) {
+            set_error(a.err, PKV_DEVERR_BLOCK_ID);
+            bad = true;
+            tb[i] = -1;
+        }
+    }
+    return bad;
+}
+
+PKV_DEV void cp16(uint32_t dst, const char *src, int bytes) { // bytes < 16: zeros behind them
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+PKV_DEV void cp4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+PKV_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+PKV_DEV void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// issue only: the caller commits and waits
+template <int D>
+PKV_DEV void stage_unit(const Args &a, const Unit &u, int *tb, char *qs, int i0, int step) {
+    const int nblk = blocks_of(a, u);
+    const int32_t *row = a.tables + (int64_t)u.s * a.max_blocks + (u.t0 >> a.bs_log2);
+    for (int i = i0; i < nblk; i += step) cp4(smem_u32(tb + i), row + i);
+    const char *q = static_cast<const char *>(a.q) + ((int64_t)u.s * a.hq + u.kvh * a.group) * (D * 2);
+    for (int i = i0; i < a.group * (D / 8); i += step) cp16(smem_u32(qs) + i * 16, q + i * 16, 16);
+}
+
+struct Join {
+    float m[kWarps][8], l[kWarps][8]; // per warp and column
+    float M[8], inv[8];
+    float wj[8][kJoinSplits];
+    int last;
+};
+
+PKV_DEV float weight_of(float m, float M) { return m == -INFINITY ? 0.f : m == M ? 1.f : fast_exp2(m - M); }
+
+// Row (s, kvh)'s splits: maxima, reciprocal sums (M, inv) and the splits' weights w[h * ldw + j] per head.
+// One warp per head; the caller synchronises.
+PKV_DEV void split_weights(const Args &a, int s, int kvh, int nsplit, float *w, int ldw, float *M, float *inv) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int h = warp; h < a.group; h += blockDim.x / 32) {
+        const float2 *ml =
+            reinterpret_cast<const float2 *>(a.ws_ml) + ((int64_t)s * a.hq + kvh * a.group + h) * a.max_splits;
+        float Mx = -INFINITY, den = 0.f;
+        for (int j = lane; j < nsplit; j += 32) Mx = fmaxf(Mx, __ldcg(ml + j).x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
+        for (int j = lane; j < nsplit; j += 32) {
+            const float2 v = __ldcg(ml + j);
+            const float f = weight_of(v.x, Mx);
+            w[h * ldw + j] = f;
+            if (f != 0.f) den = fmaf(f, v.y, den);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        if (lane == 0) {
+            M[h] = Mx == -INFINITY ? 0.f : Mx;
+            inv[h] = den == 0.f ? 0.f : 1.f / den;
+        }
+    }
+}
+
+// The end of a unit, in three steps.  1: each warp stores its columns' maxima (store_max); barrier.  2: it takes
+// its weight 2^(m - max over the warps) per column and stores its sum, offsets' sum and accumulator already
+// weighted.  3 (join_unit): barrier, the four warps' values added in warp order; leaves a barrier behind.
+struct Weight {
+    float M, w; // the unit's maximum of the column, this warp's weight
+};
+PKV_DEV Weight warp_weight(const Join &J, int warp, int column) {
+    Weight r;
+    r.M = fmaxf(fmaxf(J.m[0][column], J.m[1][column]), fmaxf(J.m[2][column], J.m[3][column]));
+    r.w = weight_of(J.m[warp][column], r.M);
+    return r;
+}
+
+// MASS: the unit's (m, l) is kept for mass_kernel even where the row is one unit.
+template <int D, int COLS, int MT, bool MASS>
+PKV_DEV void join_unit(const Args &a, const Unit &u, Join &J, const float *oacc) {
+    using M_ = ModelT<MT>;
+    constexpr int LD = D + 4;
+    const int G = a.group;
+    __syncthreads();
+    for (int e = threadIdx.x; e < G * D; e += kThreads) {
+        const int h = e / D, d = e % D;
+        const float *o = oacc + h * LD + d;
+        const float num = ((o[0] + o[COLS * LD]) + o[2 * COLS * LD]) + o[3 * COLS * LD];
+        const float den = ((J.l[0][h] + J.l[1][h]) + J.l[2][h]) + J.l[3][h];
+        const int64_t row = (int64_t)u.s * a.hq + u.kvh * G + h;
+        if ((MASS || u.nsplit > 1) && d == 0)
+            reinterpret_cast<float2 *>(a.ws_ml)[row * a.max_splits + u.j] = make_float2(J.M[h], den);
+        if (u.nsplit > 1)
+            a.ws_o[(row * a.max_splits + u.j) * D + d] = num;
+        else
+            static_cast<typename M_::T *>(a.out)[row * D + d] = M_::from_f(den == 0.f ? 0.f : num * (1.f / den));
+    }
+    __syncthreads();
+}
+
+// A finished unit is counted when the next one starts (its partials have landed by then, and the counter's answer
+// comes while that one runs).  Thread 0; after the barrier join_unit leaves.
+PKV_DEV int count_unit(const Args &a, const Unit &u) {
+    __threadfence(); // the unit's partials before its count
+    const int before = atomicAdd(a.done + (int64_t)u.s * a.hkv + u.kvh, 1);
+    return before;
+}
+
+// The row whose last unit u was: joins its splits.  All threads; starts and leaves with a barrier.
+template <int D, int MT>
+PKV_DEV void join_row(const Args &a, const Unit &u, Join &J) {
+    using M_ = ModelT<MT>;
+    const int G = a.group;
+    const int64_t row = (int64_t)u.s * a.hkv + u.kvh;
+    if (threadIdx.x == 0) a.done[row] = 0;
+    split_weights(a, u.s, u.kvh, u.nsplit, &J.wj[0][0], kJoinSplits, J.M, J.inv);
+    __syncthreads();
+    for (int e = threadIdx.x; e < G * D; e += kThreads) {
+        const int h = e / D, d = e % D;
+        const int64_t r = (int64_t)u.s * a.hq + u.kvh * G + h;
+        const float *o = a.ws_o + r * a.max_splits * D + d;
+        float num = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < u.nsplit; ++j) {
+            const float v = __ldcg(o + (int64_t)j * D);
+            if (J.wj[h][j] != 0.f) num = fmaf(J.wj[h][j], v, num);
+        }
+        static_cast<typename M_::T *>(a.out)[r * D + d] = M_::from_f(num * J.inv[h]);
+    }
+    __syncthreads();
+}
+
+// sum over the lanes that share a column (the token rows)
+PKV_DEV float row_sum(float x) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Outputs e0, e0 + step, ... (runs of 32 dims of a head) of row (s, kvh) from its splits: each of the W warps adds
+// every W-th split in order, their sums are joined in warp order.
+template <int D, int MT, int W>
+PKV_DEV void join_outputs(const Args &a, int s, int kvh, int nsplit, const float *wj, const float *inv, float (*sum)[32],
+                          int e0, int step) {
+    using M = ModelT<MT>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (; e0 < a.group * D; e0 += step) {
+        const int h = e0 / D, d = e0 % D + lane;
+        const int64_t r = (int64_t)s * a.hq + kvh * a.group + h;
+        const float *o = a.ws_o + r * a.max_splits * D + d;
+        const float *w = wj + h * a.max_splits;
+        float num = 0.f;
+#pragma unroll 8
+        for (int j = warp; j < nsplit; j += W) {
+            const float v = o[(int64_t)j * D];
+            if (w[j] != 0.f) num = fmaf(w[j], v, num);
+        }
+        sum[warp][lane] = num;
+        __syncthreads();
+        if (warp == 0) {
+            num = sum[0][lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) num += sum[w][lane];
+            static_cast<typename M::T *>(a.out)[r * D + d] = M::from_f(num * inv[h]);
+        }
+        __syncthreads();
+    }
+}
+
+// Joins the splits of a row: block (row, y) takes every gridDim.y-th run of 32 outputs.  Rows come here with more
+// than kJoinSplits splits: sixteen warps keep enough loads in flight.
+constexpr int kMergeWarps = 16;
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
+    __shared__ float sm_M[8], sm_inv[8], sum[kMergeWarps][32];
+    extern __shared__ float wj[]; // [G][max_splits]
+    pdl_wait();
+    const int row = blockIdx.x, s = row / a.hkv, kvh = row - s * a.hkv;
+    const int nsplit = (row_len(a, s) + a.split_tokens - 1) / a.split_tokens;
+    if (nsplit <= 1) return;
+    split_weights(a, s, kvh, nsplit, wj, a.max_splits, sm_M, sm_inv);
+    __syncthreads();
+    join_outputs<D, MT, kMergeWarps>(a, s, kvh, nsplit, wj, sm_inv, sum, blockIdx.y * 32, gridDim.y * 32);
+}
+
+// After a decode that stored its scores: for every unit the mass of its tokens, and its share of the row's outputs
+// where the row has several splits.  Persistent, the decode's list of units.
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads) mass_kernel(const Args a) {
+    __shared__ float sm_M[8], sm_inv[8], sum[kWarps][32];
+    __shared__ int sm_tmp[2 * kWarps];
+    extern __shared__ float wj[]; // [G][max_splits], then the list of units
+    int *full = reinterpret_cast<int *>(wj + a.group * a.max_splits), *part = full + a.num_seqs + 1;
+    pdl_wait();
+    list_units(a, full, part, sm_tmp);
+    const int nfull = full[a.num_seqs] * a.hkv, nunits = nfull + part[a.num_seqs] * a.hkv;
+    for (int ui = blockIdx.x; ui < nunits; ui += gridDim.x) {
+        const Unit u = unit_of(a, full, part, nfull, ui);
+        if (u.n <= 0) continue; // an empty sequence
+        split_weights(a, u.s, u.kvh, u.nsplit, wj, a.max_splits, sm_M, sm_inv);
+        __syncthreads();
+        add_mass(a, (int64_t)u.s * a.hkv + u.kvh, u.t0, u.t0 + u.n, sm_M, sm_inv);
+        if (u.nsplit > 1)
+            join_outputs<D, MT, kWarps>(a, u.s, u.kvh, u.nsplit, wj, sm_inv, sum, u.j * 32, u.nsplit * 32);
+        __syncthreads();
+    }
+}
+
+// cudaFuncSetAttribute once per kernel, device and size
+inline cudaError_t allow_smem(const void *kern, size_t smem, std::atomic<int> *have) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && have[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && dev < 64) have[dev].store((int)smem, std::memory_order_relaxed);
+    return e;
+}
+
+inline unsigned grid_of(const Args &a, int slots) {
+    const int64_t units = (int64_t)a.num_seqs * a.hkv * (a.max_splits > 0 ? a.max_splits : 1);
+    return (unsigned)(units < slots ? units : slots);
+}
+
+// the launch after the decode: merge_kernel, or mass_kernel
+template <int D, int MT, bool MASS>
+cudaError_t launch_merge_t(const Args &a, int sms, cudaStream_t st) {
+    const size_t smem = (size_t)a.group * a.max_splits * sizeof(float);
+    if constexpr (MASS) {
+        return pdl_launch(mass_kernel<D, MT>, dim3(grid_of(a, 8 * sms)), dim3(kThreads),
+                          smem + 2 * (a.num_seqs + 1) * sizeof(int), st, a);
+    } else {
+        return pdl_launch(merge_kernel<D, MT>, dim3((unsigned)(a.num_seqs * a.hkv), a.group * D / 32),
+                          dim3(kMergeWarps * 32),
+                          smem, st, a);
+    }
+}
+
+} // namespace pkv_mma
+
+cudaError_t pkv_mma_int4(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_mma_int4_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_mma_fp8_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_mma_16bit_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);

@@ -21,12 +21,16 @@
 // 16 MiB of fp32 partials, held by every device on which a cache was created until the process exits.
 constexpr int64_t kScratchFloats = int64_t(4) << 20;
 static __device__ __align__(256) float g_decode_scratch[kScratchFloats];
+// the 4-bit decode's counters of finished units (zero between launches; 32768 rows, more join in a second launch)
+constexpr int64_t kScratchCounters = 32768;
+static __device__ int g_decode_done[kScratchCounters];
 
 namespace {
 
 constexpr int kMaxDevices = 256;
 std::mutex g_scratch_mu;
 float *g_scratch_ptr[kMaxDevices] = {};
+int *g_done_ptr[kMaxDevices] = {};
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -38,8 +42,9 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // no-alloc call can use it.
 int pkv_noalloc_scratch_prepare(int device) {
     if (device < 0 || device >= kMaxDevices) return pkv_fail(PKV_EUNSUPPORTED, "device index %d out of range", device);
-    void *p = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_decode_scratch);
+    void *p = nullptr, *done = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&p, g_decode_scratch);
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(&done, g_decode_done);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return pkv_fail(e == cudaErrorMemoryAllocation ? PKV_ENOMEM : PKV_ECUDA,
@@ -48,6 +53,7 @@ int pkv_noalloc_scratch_prepare(int device) {
     }
     std::lock_guard<std::mutex> lk(g_scratch_mu);
     g_scratch_ptr[device] = static_cast<float *>(p);
+    g_done_ptr[device] = static_cast<int *>(done);
     return PKV_OK;
 }
 
@@ -74,17 +80,17 @@ extern "C" int paged_decode_attention_noalloc(const void *q, pkv_cache_t c, cons
     if (dev != c->device) return pkv_fail(PKV_EINVAL, "cache lives on device %d but device %d is current", c->device, dev);
 
     if (c->kv_dtype == PKV_INT4) {
-        float *scratch;
-        {
+        PkvWorkspace scratch;
+        if (dev < kMaxDevices) {
             std::lock_guard<std::mutex> lk(g_scratch_mu);
-            scratch = dev < kMaxDevices ? g_scratch_ptr[dev] : nullptr;
+            scratch = PkvWorkspace{g_scratch_ptr[dev], kScratchFloats, g_done_ptr[dev], kScratchCounters};
         }
-        if (!scratch)
+        if (!scratch.p)
             return pkv_fail(PKV_EINVAL,
                             "no-alloc decode scratch is not resident on device %d (create a cache there first)", dev);
         MmaDecodeLaunch m{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale,
-                          nullptr, 0, 1.f};
-        return decode_mma_entry(c, m, scratch, kScratchFloats, static_cast<cudaStream_t>(stream));
+                          nullptr, -1, 1.f};
+        return decode_mma_entry(c, m, &scratch, static_cast<cudaStream_t>(stream));
     }
 
     DecodeLaunch d;

@@ -40,7 +40,7 @@ struct pkv_cache {
         unsigned long long stream, capture;
         bool spare; // from kv_cache_reserve, not yet any stream's
         float *p;
-        int64_t bytes;
+        int64_t bytes; // of partials; the counters of finished units lie behind them
     };
     std::vector<StreamWs> stream_ws;
     std::mutex ws_mu;
@@ -114,7 +114,7 @@ inline void pkv_row_strides(const pkv_cache *c, int64_t *block, int64_t *head, i
     if (c->kv_dtype == PKV_INT4) {
         *head = (int64_t)c->block_size * (c->head_dim + 8);
         *block = c->num_kv_heads * *head;
-        *v = (int64_t)c->block_size * c->head_dim / 2;
+        *v = 0; // K and V of 8 tokens lie together
     } else {
         *head = c->tile_bytes;
         *v = c->num_kv_heads * c->tile_bytes;
@@ -129,14 +129,20 @@ struct MmaDecodeLaunch {
     const int32_t *tables, *lens;
     int max_blocks, num_seqs, num_q_heads;
     float scale;
-    float *mass; // or NULL
-    int64_t mass_len;
+    float *mass;
+    int64_t mass_len; // -1: no mass
     float decay;
 };
-// scratch: a fixed workspace of scratch_floats to use instead of the stream's own, or NULL
-int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, float *scratch, int64_t scratch_floats, cudaStream_t st);
+struct PkvWorkspace {
+    float *p = nullptr;
+    int64_t floats = 0;
+    int *done = nullptr; // counters, all 0 whenever no launch uses them
+    int64_t counters = 0;
+};
+// fixed: a workspace to use instead of the stream's own, or NULL
+int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st);
 int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks);
-int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, float **ws); // api.cu
+int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorkspace *ws); // api.cu
 
 struct EvictLaunch {
     const int32_t *tables, *dst_tables, *lens;

@@ -54,6 +54,15 @@ def attention(q, k, v, scale):
     return np.einsum("ht,thd->hd", p, vv), p, np.einsum("ht,thd->hd", p, np.abs(vv)), big
 
 
+def code_alignment(d, q, step, scale):
+    """What the 4-bit products lose: a code enters as a subnormal number, whose product with q is kept to 2^-17 of a code
+    step times the head's largest |q| (half the elements; 2^-21 the other half).  Bound of a score's error, for a
+    softmax weight twice that; q [Hq, D], step [L, Hkv] float64."""
+    if step.size == 0:
+        return 0.0
+    return 2 * scale * float(np.abs(q).max() * step.max()) * d * (2.0 ** -18 + 2.0 ** -22)
+
+
 def relative_weight_error(big):
     """Bound on a softmax weight's relative error.
 

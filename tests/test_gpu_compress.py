@@ -76,6 +76,19 @@ class Setup:
                 out.append(R.to64(x))
         return out
 
+    def bounds(self, s, big):
+        """(relative error of sequence s's softmax weights, error of a unit-weight sum of its V rows)."""
+        rel = R.relative_weight_error(big)
+        if self.kv == "bf16":
+            rel += 2.0 ** -14                              # weights as bf16 hi + lo, each cut off
+        if self.kv != "int4" or not self.lens[s]:
+            return rel, 0.0
+        step = [R.quantise4(R.to64(x[self.rows(s)]), self.model)[1] for x in (self.k, self.v)]
+        rel += R.code_alignment(self.d, R.to64(self.q[s]), step[0], self.scale)
+        # V: in a product of 16 tokens each keeps its code to 2^-17 of a step at the largest weight: 16 of them
+        # lose at most 2^-13 of a step per unit of weight
+        return rel, 2.0 ** -13 * float(step[1].max())
+
     def rows(self, s):
         a = sum(self.lens[:s])
         return slice(a, a + self.lens[s])
@@ -91,8 +104,8 @@ def check_attention(x, out, mass=None, old=None, decay=1.0):
     q, got = R.to64(x.q), R.to64(out)
     for s, n in enumerate(x.lens):
         ref, p, pv, big = R.attention(q[s], k[x.rows(s)], v[x.rows(s)], x.scale)
-        rel = R.relative_weight_error(big) + (2.0 ** -15 if x.kv == "bf16" else 0)
-        tol = R.HALF_STEP[x.model] * np.abs(ref) * 1.001 + rel * pv + 2.0 ** -24
+        rel, cut = x.bounds(s, big)
+        tol = R.HALF_STEP[x.model] * np.abs(ref) * 1.001 + rel * pv + cut + 2.0 ** -24
         err = np.abs(got[s] - ref)
         assert np.all(err <= tol), f"sequence {s} (L {n}): {err.max():.3e}, {(err / tol).max():.2f} of its bound"
         if mass is None:
@@ -100,21 +113,39 @@ def check_attention(x, out, mass=None, old=None, decay=1.0):
         m, before = R.to64(mass[s]), R.to64(old[s])
         add = p.reshape(x.hkv, x.hq // x.hkv, n).sum(1)
         want = before[:, :n] * decay + add
-        bound = R.relative_weight_error(big) * add + 2.0 ** -22 * np.abs(want)
+        bound = rel * add + 2.0 ** -22 * np.abs(want)
         assert np.all(np.abs(m[:, :n] - want) <= bound), f"mass of sequence {s}"
         assert np.array_equal(m[:, n:], before[:, n:]), f"mass behind sequence {s} changed"
 
 
 # ------------------------------------------------------------------------------------------ 4-bit rows
 
+V_ORDER = [0, 2, 4, 6, 1, 3, 5, 7]   # V rows of an octet by place
+
+
+def int4_rows(raw, hkv, bs, d):
+    """Bytes [NB, ...] of a 4-bit pool -> (code bytes [NB, Hkv, 2, bs, D / 2], parameter bytes [NB, Hkv, 2, bs, 4])."""
+    nb = raw.shape[0]
+    o = raw.reshape(nb, hkv, bs // 8, 8 * (d + 8))
+    k = o[..., :4 * d].reshape(nb, hkv, bs // 8, 8, d // 2)
+    placed = o[..., 4 * d:8 * d].reshape(nb, hkv, bs // 8, 8, d // 2)
+    v = np.empty_like(placed)
+    for place, row in enumerate(V_ORDER):
+        r = placed[:, :, :, place]
+        v[:, :, :, row] = np.roll(r, 32, axis=-1) if d == 128 and place & 2 else r
+    par = o[..., 8 * d:].reshape(nb, hkv, bs // 8, 2, 8, 4).transpose(0, 1, 3, 2, 4, 5).reshape(nb, hkv, 2, bs, 4)
+    return np.stack([k, v], 2).reshape(nb, hkv, 2, bs, d // 2), par
+
+
 def int4_parts(cache, model):
     """(codes [NB, Hkv, 2, bs, D], step, low [NB, Hkv, 2, bs] as raw int16) of a 4-bit pool."""
-    nb, hkv, bs, d = cache.num_blocks, cache.num_kv_heads, cache.block_size, cache.head_dim
-    raw = cache.view()[0].cpu().numpy().reshape(nb, hkv, bs * (d + 8))
-    c = raw[:, :, :bs * d].reshape(nb, hkv, 2, bs, d // 2)
-    codes = np.stack([c & 15, c >> 4], -1).reshape(nb, hkv, 2, bs, d)
-    par = np.ascontiguousarray(raw[:, :, bs * d:]).view(np.int16).reshape(nb, hkv, 2, bs, 2)
-    return codes, par[..., 0], par[..., 1]
+    c, par = int4_rows(cache.view()[0].cpu().numpy().reshape(cache.num_blocks, -1), cache.num_kv_heads,
+                       cache.block_size, cache.head_dim)
+    par = np.ascontiguousarray(par).view(np.int16)
+    w = np.ascontiguousarray(c).view(np.uint16)             # four codes a word, rotated left by three bits
+    w = (w >> 3) | (w << 13)
+    codes = np.stack([(w >> (4 * i)) & 15 for i in range(4)], -1).astype(np.uint8)
+    return codes.reshape(*c.shape[:-1], -1), par[..., 0], par[..., 1]
 
 
 def model_bits(x, model):
@@ -355,7 +386,8 @@ def test_int4_values_of_any_magnitude(step):
     k, v = x.stored()
     for s in range(2):
         ref, _, pv, big = R.attention(R.to64(x.q[s]), k[x.rows(s)], v[x.rows(s)], x.scale)
-        tol = R.HALF_STEP[model] * np.abs(ref) * 1.001 + R.relative_weight_error(big) * pv
+        rel, cut = x.bounds(s, big)
+        tol = R.HALF_STEP[model] * np.abs(ref) * 1.001 + rel * pv + cut
         assert np.all(np.abs(R.to64(out[s]) - ref) <= tol)
     assert x.close() == 0
 
@@ -393,7 +425,8 @@ def test_bad_blocks_and_lengths_are_reported_and_their_tokens_left_out(kv):
     for s, gone in ((0, range(32, 48)), (1, range(48, 64))):
         stay = [i for i in range(x.lens[s]) if i not in gone]
         ref, p, pv, big = R.attention(R.to64(x.q[s]), k[x.rows(s)][stay], v[x.rows(s)][stay], x.scale)
-        tol = R.HALF_STEP["f16" if kv != "fp8" else x.model] * np.abs(ref) * 1.001 + R.relative_weight_error(big) * pv
+        rel, cut = x.bounds(s, big)
+        tol = R.HALF_STEP[x.model] * np.abs(ref) * 1.001 + rel * pv + cut
         assert np.all(np.abs(R.to64(out[s]) - ref) <= tol)
         assert not mass[s][:, list(gone)].any()
     # a length past the tables or the mass rows is cut to them
@@ -476,9 +509,8 @@ def test_evict(kv, model, hkv, d, bs, budget, recent):
         for slot in tail:
             b, o = divmod(slot, bs)
             if kv == "int4":
-                blk = raw[b].reshape(hkv, bs * (d + 8))
-                assert (blk[:, :bs * d].reshape(hkv, 2, bs, -1)[:, :, o] == 255).all()
-                assert (blk[:, bs * d:].reshape(hkv, 2, bs, 4)[:, :, o] == 255).all()
+                codes, par = int4_rows(raw[b:b + 1], hkv, bs, d)
+                assert (codes[:, :, :, o] == 255).all() and (par[:, :, :, o] == 255).all()
             else:
                 assert (raw[b].reshape(2, hkv, bs, -1)[:, :, o] == 255).all()
     assert x.close() == 0
@@ -547,8 +579,8 @@ def test_decode_evict_and_decode_on(kv, model):
         kk, vv = [np.concatenate([np.stack([a[base + hk[s, h, :n], h] for h in range(2)], 1), b[s:s + 1]])
                   for a, b in ((k, new[0]), (v, new[1]))]
         ref, p, pv, big = R.attention(R.to64(x.q[s]), kk, vv, x.scale)
-        rel = R.relative_weight_error(big) + (2.0 ** -15 if kv == "bf16" else 0)
-        tol = R.HALF_STEP[model] * np.abs(ref) * 1.001 + rel * pv
+        rel, cut = x.bounds(s, big)
+        tol = R.HALF_STEP[model] * np.abs(ref) * 1.001 + 1.5 * (rel * pv + cut)  # (the new token's step besides)
         assert np.all(np.abs(R.to64(out[s]) - ref) <= tol)
         # the new token started from the zero behind the compacted mass
         got = R.to64(mass2[s, :, n])
@@ -686,6 +718,19 @@ def test_refusals():
     # what a refused call leaves behind works
     check_attention(x, P.paged_decode_attention(x.q, c, x.tables, x.context, x.scale))
     assert x.close() == 0
+
+
+def test_no_room_for_any_token():
+    """Mass rows or tables of no tokens: every length is cut to 0 and reported, outputs are zero rows."""
+    x = Setup([5, 0], hq=2, hkv=2, kv="f16", model="f16", seed=1)
+    out = P.paged_decode_attention_mass(x.q, x.cache, x.tables, x.context, x.scale, torch.zeros(2, 2, 0, device="cuda"))
+    assert not out.any() and x.cache.check_error() == 4
+    none = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    out = P.paged_decode_attention_mass(x.q, x.cache, none, x.context, x.scale, torch.zeros(2, 2, 9, device="cuda"))
+    assert not out.any() and x.cache.check_error() == 4
+    kept, lens, new = P.paged_kv_evict(x.cache, none, x.context, torch.zeros(2, 2, 9, device="cuda"), 3, 1, none)
+    assert (kept == -1).all() and not lens.any() and not new.any() and x.cache.check_error() == 4
+    x.cache.close()
 
 
 def test_empty_batches():
