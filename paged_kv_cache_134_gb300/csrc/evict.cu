@@ -6,12 +6,18 @@
 // sequence of at most B tokens is copied whole.  Attention does not depend on the order of keys whose
 // positions are already in them, so a head may keep tokens of its own choice.
 //
-// select_kernel: one CTA per row finds the (B - R)-th largest mass by radix selection (four passes of
-// 8-bit digits over keys whose unsigned order is the masses' order, histogram in shared memory), then
-// writes the kept positions in order: each warp owns a run of positions, counts, and after a scan over
-// the warps places its own.  The row is read from L2 after the first pass.
-// move_kernel: the gather.  Bound by HBM: row_bytes read and written per kept token, K|V and head.
-// Sources and destinations are different blocks, so rows move in any order.
+// One launch: a cluster of 1 to 8 CTAs per row selects, then moves.
+//   * Selection.  Each CTA keeps its stretch of the row's keys (numbers whose unsigned order is the masses') in shared
+//     memory, and the (B - R)-th largest is found by three passes of a radix selection (digits of 11, 11 and
+//     10 bits, histograms in shared memory, summed over the cluster's); up to 512 candidates are ranked by comparing
+//     all with all instead, which takes one pass.  Each warp owns a run of positions, counts what stays, and after
+//     a scan over warps and CTAs writes its kept positions in order.
+//   * Moving.  The kept tokens are shared out evenly over the cluster, 512 at a time: each thread looks up one
+//     token's source and destination slot a chunk ahead, so that a row's copy waits for nothing but its own bytes;
+//     a warp then moves eight tokens' rows at once (K and V, 16 bytes a lane, all loaded before the first is
+//     stored).  Sources and destinations are different blocks, so rows move in any order.
+// Bound by HBM: row_bytes read and written per kept token, K|V and head.  One CTA a row while there are rows for
+// every SM, so that the rows that still select run beside those that move already; a cluster where rows are few.
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -20,10 +26,12 @@
 
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 4;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kAllPairs = 512;      // candidates that are ranked by comparing all with all
+constexpr int kMaxKeys = 24 * 1024; // keys of a CTA in shared memory; longer stretches are read again
+constexpr int kMoveUnroll = 8;
 
 struct EvictArgs {
     char *pool;
@@ -34,7 +42,9 @@ struct EvictArgs {
     unsigned int *err;
     int64_t num_blocks, mass_len, mass_out_len, cap;
     int64_t blk_stride, head_stride, v_off;
-    int max_blocks, max_dst_blocks, hkv, bs, d, budget, recent;
+    int max_blocks, max_dst_blocks, hkv, bs_log2, d, budget, recent;
+    int cluster, keys; // CTAs of a row; keys of a CTA that fit its shared memory
+    int row_bytes;
 };
 
 // masses as unsigned numbers of the same order; NaN below every number, -0 as 0
@@ -44,16 +54,50 @@ PKV_DEV uint32_t order_key(float x) {
     return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) {
-    __shared__ int hist[256];
-    __shared__ int wsum[2][kSelWarps];
+PKV_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// mass of an order key (-0 comes back as 0, any NaN as one NaN)
+PKV_DEV float key_mass(uint32_t k) {
+    return k == 0u ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
+}
+// what stands at the place of `p` in the shared memory of the cluster's CTA `rank` (no compiler barrier, so that several
+// are under way at once; the cluster barriers are ones)
+PKV_DEV uint32_t peer_at(const void *p, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+PKV_DEV int peer_word(const void *p, int rank) {
+    int v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_at(p, rank)));
+    return v;
+}
+PKV_DEV int4 peer_int4(const void *p, int rank) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(peer_at(p, rank)));
+    return v;
+}
+
+// LPT lanes move one token's K and V rows of one head, 16 bytes each; a 4-bit row's (s, z) words go by the two
+// lanes behind them.  CL: the row has a cluster.
+template <int LPT, bool I4, bool CL>
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
+    extern __shared__ uint32_t keys[];
+    __shared__ __align__(16) int hist[2][kBins];
+    __shared__ int wsum[2][kWarps];
+    __shared__ int sums[2]; // this CTA's larger and equal keys
     __shared__ uint32_t s_prefix;
     __shared__ int s_left;
-    pdl_trigger();
-    pdl_wait();
-    const int64_t row = blockIdx.x;
+    const int C = CL ? a.cluster : 1;
+    const int64_t row = CL ? blockIdx.x / C : blockIdx.x;
+    const int rank = CL ? (int)(blockIdx.x - row * C) : 0;
     const int s = (int)(row / a.hkv), kvh = (int)(row - (int64_t)s * a.hkv);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_trigger();
+    pdl_wait();
     int L = max(a.lens[s], 0);
     if (L > a.cap) {
         if (tid == 0) set_error(a.err, PKV_DEVERR_LENGTH);
@@ -63,152 +107,230 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     int32_t *kept = a.kept + row * a.budget;
     float *mo = a.mass_out + row * a.mass_out_len;
     const int len = min(L, a.budget);
-    if (tid == 0 && kvh == 0) a.new_lens[s] = len;
+    if (tid == 0 && rank == 0 && kvh == 0) a.new_lens[s] = len;
     const int n = L > a.budget ? L - a.recent : 0; // candidates
     const int k = a.budget - a.recent;             // how many of them stay
 
     if (n > 0 && k > 0) {
-        uint32_t prefix = 0; // the threshold's digits found so far
-        int left = k;        // its rank among the keys that share them
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
+        // this CTA's stretch [b, b + cnt)
+        const int stretch = CL ? ((n + C - 1) / C + 31) & ~31 : n;
+        const int b = min(rank * stretch, n), cnt = min(stretch, n - b);
+        const bool held = stretch <= a.keys;
+        if (held) {
+#pragma unroll 8
+            for (int i = tid; i < cnt; i += kThreads) keys[i] = order_key(m[b + i]);
+        }
+        auto key_at = [&](int i) { return held ? keys[i] : order_key(m[b + i]); };
+        uint32_t prefix = 0; // the threshold; `left` of the keys equal to it stay, the first ones
+        int left = k;
+        if (!CL && n <= kAllPairs && held) {
             __syncthreads();
-            for (int t0 = 0; t0 < n; t0 += kSelThreads) {
-                const int t = t0 + tid;
-                uint32_t key = 0;
-                bool in = t < n;
-                if (in) {
-                    key = order_key(m[t]);
-                    in = shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8));
+            if (tid < n) {
+                const uint32_t mine = keys[tid];
+                int larger = 0, same = 0; // same: equal ones before
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t o = keys[i];
+                    larger += o > mine;
+                    same += o == mine && i < tid;
                 }
-                // one addition per digit and warp: most keys of a pass share a few digits
-                const int digit = in ? (int)((key >> shift) & 255u) : 256;
-                const unsigned same = __match_any_sync(0xffffffffu, digit);
-                if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+                if (larger + same == k - 1) s_prefix = mine, s_left = same + 1;
             }
             __syncthreads();
-            if (warp == 0) { // the digit whose suffix sum first reaches `left`
-                int c[8], sum = 0;
+            prefix = s_prefix;
+            left = s_left;
+        } else {
+            for (int pass = 0; pass < 3; ++pass) {
+                const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
+                int *h = hist[pass & 1];
+                for (int i = tid; i < kBins; i += kThreads) h[i] = 0;
+                __syncthreads();
+                for (int i = tid; i < cnt; i += kThreads) {
+                    const uint32_t key = key_at(i);
+                    // (the digits above: all 32 bits shifted out in the first pass)
+                    if (pass == 0 || (key >> (pass == 1 ? 21 : 10)) == (prefix >> (pass == 1 ? 21 : 10)))
+                        atomicAdd(&h[(key >> shift) & (bins - 1)], 1);
+                }
+                if (CL)
+                    cluster_sync();
+                else
+                    __syncthreads();
+                // four digits a thread, the largest first; the thread whose sum reaches `left` has the digit
+                const int d0 = kBins - 4 - tid * 4;
+                int4 v = make_int4(0, 0, 0, 0);
+                if (CL) {
+                    int4 part[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) c[i] = hist[255 - (lane * 8 + i)], sum += c[i];
+                    for (int r = 0; r < 8; ++r) part[r] = r < C ? peer_int4(&h[d0], r) : make_int4(0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        v.x += part[r].x, v.y += part[r].y, v.z += part[r].z, v.w += part[r].w;
+                } else {
+                    v = *reinterpret_cast<const int4 *>(&h[d0]);
+                }
+                const int c[4] = {v.w, v.z, v.y, v.x};
+                const int sum = (c[0] + c[1]) + (c[2] + c[3]);
                 int before = sum;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, before, o);
                     if (lane >= o) before += v;
                 }
-                before -= sum; // keys of larger digits, before this lane's eight
+                if (lane == 31) wsum[0][warp] = before;
+                __syncthreads();
+                for (int w = 0; w < warp; ++w) before += wsum[0][w];
+                before -= sum; // keys of larger digits
                 if (before < left && left <= before + sum) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         if (before < left && left <= before + c[i]) {
-                            s_prefix = prefix | ((uint32_t)(255 - (lane * 8 + i)) << shift);
+                            s_prefix = prefix | ((uint32_t)(kBins - 1 - (tid * 4 + i)) << shift);
                             s_left = left - before;
                         }
                         before += c[i];
                     }
                 }
+                __syncthreads();
+                prefix = s_prefix;
+                left = s_left;
             }
-            __syncthreads();
-            prefix = s_prefix;
-            left = s_left;
         }
-        // prefix: the threshold; `left` of the keys equal to it stay, the first ones
-        const int seg = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
-        const int b = min(warp * seg, n), e = min(b + seg, n);
+        // ---- each warp's run of the stretch: larger and equal keys, their sums before it, then the positions
+        const int run = ((cnt + kWarps - 1) / kWarps + 31) & ~31;
+        const int rb = min(warp * run, cnt), re = min(rb + run, cnt);
         int gt = 0, eq = 0;
-        for (int t0 = b; t0 < e; t0 += 32) {
-            const int t = t0 + lane;
-            const uint32_t key = t < e ? order_key(m[t]) : 0u;
-            gt += __popc(__ballot_sync(0xffffffffu, t < e && key > prefix));
-            eq += __popc(__ballot_sync(0xffffffffu, t < e && key == prefix));
+        for (int i0 = rb; i0 < re; i0 += 32) {
+            const int i = i0 + lane;
+            const uint32_t key = i < re ? key_at(i) : 0u;
+            gt += __popc(__ballot_sync(0xffffffffu, i < re && key > prefix));
+            eq += __popc(__ballot_sync(0xffffffffu, i < re && key == prefix));
         }
+        __syncthreads(); // wsum has been read
         if (lane == 0) wsum[0][warp] = gt, wsum[1][warp] = eq;
         __syncthreads();
-        int at = 0, eqb = 0; // larger keys and equal keys before this warp's run
+        int at = 0, eqb = 0; // larger and equal keys before this warp's run
         for (int w = 0; w < warp; ++w) at += wsum[0][w], eqb += wsum[1][w];
+        if (CL) {
+            if (tid == kThreads - 1) sums[0] = at + gt, sums[1] = eqb + eq;
+            cluster_sync();
+            for (int r = 0; r < rank; ++r) at += peer_word(&sums[0], r), eqb += peer_word(&sums[1], r);
+        }
         at += min(eqb, left);
-        for (int t0 = b; t0 < e; t0 += 32) {
-            const int t = t0 + lane;
-            const float v = t < e ? m[t] : 0.f;
-            const uint32_t key = t < e ? order_key(v) : 0u;
-            const unsigned be = __ballot_sync(0xffffffffu, t < e && key == prefix);
-            const bool stay = t < e && (key > prefix || (key == prefix && eqb + __popc(be & ((1u << lane) - 1)) < left));
-            const unsigned bs_ = __ballot_sync(0xffffffffu, stay);
+        for (int i0 = rb; i0 < re; i0 += 32) {
+            const int i = i0 + lane;
+            const uint32_t key = i < re ? key_at(i) : 0u;
+            const unsigned be = __ballot_sync(0xffffffffu, i < re && key == prefix);
+            const bool stay =
+                i < re && (key > prefix || (key == prefix && eqb + __popc(be & ((1u << lane) - 1)) < left));
+            const unsigned st = __ballot_sync(0xffffffffu, stay);
             if (stay) {
-                const int p = at + __popc(bs_ & ((1u << lane) - 1));
-                kept[p] = t;
-                mo[p] = v;
+                const int p = at + __popc(st & ((1u << lane) - 1));
+                kept[p] = b + i;
+                mo[p] = key_mass(key);
             }
-            at += __popc(bs_);
+            at += __popc(st);
             eqb += __popc(be);
         }
     }
-    // the recent tokens (or a short sequence whole), then what lies behind
+    // ---- the recent tokens (or a short sequence whole), then what lies behind
     const int first = n > 0 ? k : 0, from = n > 0 ? n - k : 0;
-    for (int p = first + tid; p < len; p += kSelThreads) {
+    const int t0 = rank * kThreads + tid, step = C * kThreads;
+    for (int p = first + t0; p < len; p += step) {
         kept[p] = p + from;
         mo[p] = m[p + from];
     }
-    for (int p = len + tid; p < a.budget; p += kSelThreads) kept[p] = -1;
-    for (int64_t p = len + tid; p < a.mass_out_len; p += kSelThreads) mo[p] = 0.f;
-}
+    for (int p = len + t0; p < a.budget; p += step) kept[p] = -1;
+    for (int64_t p = len + t0; p < a.mass_out_len; p += step) mo[p] = 0.f;
 
-// LPT lanes move one token's K and V rows of one head, 16 bytes each; a 4-bit row's (s, z) words go by
-// the two lanes behind them.
-template <int LPT, bool I4>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int row_bytes) {
-    pdl_trigger();
-    pdl_wait();
-    constexpr int kTokens = kMoveThreads / LPT;
-    const int64_t row = blockIdx.x;
-    const int s = (int)(row / a.hkv), kvh = (int)(row - (int64_t)s * a.hkv);
-    const int lane = threadIdx.x % LPT, grp = threadIdx.x / LPT;
-    const int32_t *kept = a.kept + row * a.budget;
+    // ---- move: every CTA of the row sees all kept positions, and nobody's shared memory is read any more
+    if (CL)
+        cluster_sync();
+    else
+        __syncthreads();
+    constexpr int kGroups = kThreads / LPT;
+    __shared__ uint2 slots[2][kThreads]; // source and destination slot of a chunk's tokens; none: -1
+    const int part = lane % LPT, grp = tid / LPT;
     const int32_t *src_t = a.tables + (int64_t)s * a.max_blocks, *dst_t = a.dst_tables + (int64_t)s * a.max_dst_blocks;
-    const int chunks = row_bytes / 16;
-    const bool code = lane < 2 * chunks, par = I4 && !code && lane < 2 * chunks + 2;
-    if (!code && !par) return;
-    const int kv = code ? lane / chunks : lane - 2 * chunks;
-    const int64_t base = kvh * a.head_stride;
-    // bytes from a (block, head)'s start to this lane's piece of row `o`
-    auto piece = [&](int o) -> int64_t {
-        if (!I4) return kv * a.v_off + (int64_t)o * row_bytes + (lane - kv * chunks) * 16;
-        return code ? int4_codes(kv, o, (lane - kv * chunks) * 16, a.d) : int4_params(kv, o, a.d);
+    const int chunks = a.row_bytes / 16, bs = 1 << a.bs_log2;
+    const bool code = part < 2 * chunks, par = I4 && !code && part < 2 * chunks + 2;
+    const int kv = code ? part / chunks : part - 2 * chunks, in_row = (part - kv * chunks) * 16;
+    char *head = a.pool + kvh * a.head_stride + (I4 ? 0 : kv * a.v_off + in_row);
+    // this lane's piece of a slot's row
+    auto place = [&](uint32_t slot) -> char * {
+        const uint32_t o = slot & (bs - 1);
+        char *p = head + (int64_t)(slot >> a.bs_log2) * a.blk_stride;
+        if constexpr (!I4) return p + o * a.row_bytes;
+        return p + (code ? int4_codes(kv, o, in_row, a.d) : int4_params(kv, o, a.d));
     };
-    const int lim = (int)min((int64_t)a.budget, a.cap);
-    for (int j0 = blockIdx.y * kTokens * kMoveUnroll; j0 < lim; j0 += gridDim.y * kTokens * kMoveUnroll) {
-        const char *from[kMoveUnroll];
-        char *to[kMoveUnroll];
+    auto look_up = [&](int j) {
+        uint2 r = make_uint2(~0u, ~0u);
+        if (j >= len) return r;
+        const int t = kept[j];
+        const int sb = src_t[t >> a.bs_log2], db = dst_t[j >> a.bs_log2];
+        if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks)
+            set_error(a.err, PKV_DEVERR_BLOCK_ID);
+        else
+            r = make_uint2(((uint32_t)sb << a.bs_log2) + (t & (bs - 1)), ((uint32_t)db << a.bs_log2) + (j & (bs - 1)));
+        return r;
+    };
+    slots[0][tid] = look_up(rank * kThreads + tid);
+    __syncthreads();
+    for (int j0 = rank * kThreads, buf = 0; j0 < len; j0 += C * kThreads, buf ^= 1) {
+        const uint2 next = look_up(j0 + C * kThreads + tid);
+        const int here = min(kThreads, len - j0);
+        if (code || par) {
+            for (int i0 = grp; i0 < here; i0 += kGroups * kMoveUnroll) {
+                uint2 sl[kMoveUnroll];
+                uint4 x[kMoveUnroll];
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            const int j = j0 + u * kTokens + grp;
-            const int t = j < lim ? kept[j] : -1;
-            from[u] = nullptr;
-            if (t >= 0) {
-                const int sb = src_t[t / a.bs], db = dst_t[j / a.bs];
-                if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
-                    if (lane == 0) set_error(a.err, PKV_DEVERR_BLOCK_ID);
-                } else {
-                    from[u] = a.pool + sb * a.blk_stride + base + piece(t % a.bs);
-                    to[u] = a.pool + db * a.blk_stride + base + piece(j % a.bs);
+                for (int u = 0; u < kMoveUnroll; ++u) {
+                    const int i = i0 + u * kGroups;
+                    sl[u] = i < here ? slots[buf][i] : make_uint2(~0u, ~0u);
+                    if (sl[u].x == ~0u) continue;
+                    if (code)
+                        x[u] = __ldcs(reinterpret_cast<const uint4 *>(place(sl[u].x)));
+                    else
+                        x[u].x = *reinterpret_cast<const uint32_t *>(place(sl[u].x));
+                }
+#pragma unroll
+                for (int u = 0; u < kMoveUnroll; ++u) {
+                    if (sl[u].x == ~0u) continue;
+                    if (code)
+                        *reinterpret_cast<uint4 *>(place(sl[u].y)) = x[u];
+                    else
+                        *reinterpret_cast<uint32_t *>(place(sl[u].y)) = x[u].x;
                 }
             }
         }
-        if (code) {
-            uint4 x[kMoveUnroll];
-#pragma unroll
-            for (int u = 0; u < kMoveUnroll; ++u)
-                if (from[u]) x[u] = __ldcs(reinterpret_cast<const uint4 *>(from[u]));
-#pragma unroll
-            for (int u = 0; u < kMoveUnroll; ++u)
-                if (from[u]) *reinterpret_cast<uint4 *>(to[u]) = x[u];
-        } else {
-#pragma unroll
-            for (int u = 0; u < kMoveUnroll; ++u)
-                if (from[u]) *reinterpret_cast<uint32_t *>(to[u]) = *reinterpret_cast<const uint32_t *>(from[u]);
-        }
+        slots[buf ^ 1][tid] = next;
+        __syncthreads();
     }
+}
+
+template <int LPT, bool I4, bool CL>
+cudaError_t launch_t(const EvictArgs &a, unsigned rows, cudaStream_t st) {
+    auto kern = evict_kernel<LPT, I4, CL>;
+    const size_t smem = a.keys * sizeof(uint32_t);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * (int)sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(rows * a.cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int LPT, bool I4>
+cudaError_t launch_lpt(const EvictArgs &a, unsigned rows, cudaStream_t st) {
+    return a.cluster > 1 ? launch_t<LPT, I4, true>(a, rows, st) : launch_t<LPT, I4, false>(a, rows, st);
 }
 
 } // namespace
@@ -232,28 +354,22 @@ cudaError_t launch_evict(pkv_cache *c, const EvictLaunch &v, cudaStream_t st) {
     a.max_blocks = v.max_blocks;
     a.max_dst_blocks = v.max_dst_blocks;
     a.hkv = c->num_kv_heads;
-    a.bs = c->block_size;
+    a.bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
     a.d = c->head_dim;
     a.budget = v.budget;
     a.recent = v.recent;
-    const unsigned rows = (unsigned)v.num_seqs * (unsigned)a.hkv;
-    cudaError_t e;
-    {
-        PkvTimer timer(c, PKV_KIND_COPY, st);
-        g_pkv_launches++;
-        e = pdl_launch(select_kernel, dim3(rows), dim3(kSelThreads), 0, st, a);
-    }
-    if (e != cudaSuccess) return e;
     const bool i4 = c->kv_dtype == PKV_INT4;
-    const int row_bytes = i4 ? a.d / 2 : a.d * c->elem_bytes;
-    const int lanes = 2 * row_bytes / 16 + (i4 ? 2 : 0);
-    const int lpt = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
-    const int64_t per = (int64_t)(kMoveThreads / lpt) * kMoveUnroll;
-    const int64_t most = std::min<int64_t>(a.budget, a.cap);
-    const dim3 grid(rows, (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + per - 1) / per, 65535)));
+    a.row_bytes = i4 ? a.d / 2 : a.d * c->elem_bytes;
+    const unsigned rows = (unsigned)v.num_seqs * (unsigned)a.hkv;
+    // a CTA per row, or a cluster while that leaves SMs without one and gives each CTA 2048 positions or more
+    a.cluster = 1;
+    while (a.cluster < 8 && (int64_t)rows * a.cluster * 2 <= c->num_sms && a.cap / (2 * a.cluster) >= 2048) a.cluster *= 2;
+    const int64_t stretch = ((a.cap + a.cluster - 1) / a.cluster + 31) / 32 * 32;
+    a.keys = (int)std::min<int64_t>(stretch, kMaxKeys);
+    const int lanes = 2 * a.row_bytes / 16 + (i4 ? 2 : 0);
     PkvTimer timer(c, PKV_KIND_COPY, st);
     g_pkv_launches++;
-    auto kern = i4 ? (lpt == 8 ? move_kernel<8, true> : move_kernel<16, true>)
-                   : lpt == 8 ? move_kernel<8, false> : lpt == 16 ? move_kernel<16, false> : move_kernel<32, false>;
-    return pdl_launch(kern, grid, dim3(kMoveThreads), 0, st, a, row_bytes);
+    if (i4) return lanes <= 8 ? launch_lpt<8, true>(a, rows, st) : launch_lpt<16, true>(a, rows, st);
+    if (lanes <= 8) return launch_lpt<8, false>(a, rows, st);
+    return lanes <= 16 ? launch_lpt<16, false>(a, rows, st) : launch_lpt<32, false>(a, rows, st);
 }
