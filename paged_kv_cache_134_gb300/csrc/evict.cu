@@ -8,9 +8,10 @@
 //
 // One launch: a cluster of 1 to 8 CTAs per row selects, then moves.
 //   * Selection.  Each CTA keeps its stretch of the row's keys (numbers whose unsigned order is the masses') in shared
-//     memory, and the (B - R)-th largest is found by three passes of a radix selection (digits of 11, 11 and
-//     10 bits, histograms in shared memory, summed over the cluster's); up to 512 candidates are ranked by comparing
-//     all with all instead, which takes one pass.  Each warp owns a run of positions, counts what stays, and after
+//     memory, and the (B - R)-th largest is found by four passes of a radix selection (digits of 8 bits,
+//     histograms in shared memory, summed over the cluster's: 11-bit digits take a pass less, but made the CTAs
+//     spend 34 us on one another's histograms, 16 rows of 131071 positions, where these take 22 in all); up to 512 candidates
+//     are ranked by comparing all with all instead, which takes one pass.  Each warp owns a run of positions, counts what stays, and after
 //     a scan over warps and CTAs writes its kept positions in order.
 //   * Moving.  The kept tokens are shared out evenly over the cluster, 512 at a time: each thread looks up one
 //     token's source and destination slot a chunk ahead, so that a row's copy waits for nothing but its own bytes;
@@ -28,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 constexpr int kAllPairs = 512;      // candidates that are ranked by comparing all with all
 constexpr int kMaxKeys = 24 * 1024; // keys of a CTA in shared memory; longer stretches are read again
 constexpr int kMoveUnroll = 8;
@@ -73,20 +74,12 @@ PKV_DEV int peer_word(const void *p, int rank) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_at(p, rank)));
     return v;
 }
-PKV_DEV int4 peer_int4(const void *p, int rank) {
-    int4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(peer_at(p, rank)));
-    return v;
-}
-
 // LPT lanes move one token's K and V rows of one head, 16 bytes each; a 4-bit row's (s, z) words go by the two
 // lanes behind them.  CL: the row has a cluster.
 template <int LPT, bool I4, bool CL>
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
-    extern __shared__ uint32_t keys[];
-    __shared__ __align__(16) int hist[2][kBins];
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ int hist[2][kBins];
     __shared__ int wsum[2][kWarps];
     __shared__ int sums[2]; // this CTA's larger and equal keys
     __shared__ uint32_t s_prefix;
@@ -116,14 +109,36 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
         const int stretch = CL ? ((n + C - 1) / C + 31) & ~31 : n;
         const int b = min(rank * stretch, n), cnt = min(stretch, n - b);
         const bool held = stretch <= a.keys;
-        if (held) {
-#pragma unroll 8
-            for (int i = tid; i < cnt; i += kThreads) keys[i] = order_key(m[b + i]);
+        const bool pairs = !CL && n <= kAllPairs && held;
+        if (!pairs) { // the first pass's histogram is taken while the keys come in
+            if (tid < kBins) hist[0][tid] = 0;
+            __syncthreads();
         }
-        auto key_at = [&](int i) { return held ? keys[i] : order_key(m[b + i]); };
+        constexpr int kLoad = 8;
+        for (int i0 = tid; i0 < cnt; i0 += kLoad * kThreads) {
+            float v[kLoad];
+#pragma unroll
+            for (int u = 0; u < kLoad; ++u)
+                if (i0 + u * kThreads < cnt) v[u] = m[b + i0 + u * kThreads];
+#pragma unroll
+            for (int u = 0; u < kLoad; ++u) {
+                const int i = i0 + u * kThreads;
+                if (i >= cnt) break;
+                const uint32_t key = order_key(v[u]);
+                if (held) keys[i] = key;
+                if (!pairs) atomicAdd(&hist[0][key >> 24], 1);
+            }
+        }
+        // keys i .. i + 3 (i a multiple of 4; what lies behind the stretch is not meant)
+        auto four = [&](int i) {
+            if (held) return *reinterpret_cast<const uint4 *>(keys + i);
+            const float *p = m + b + i;
+            return make_uint4(order_key(p[0]), i + 1 < cnt ? order_key(p[1]) : 0u, i + 2 < cnt ? order_key(p[2]) : 0u,
+                              i + 3 < cnt ? order_key(p[3]) : 0u);
+        };
         uint32_t prefix = 0; // the threshold; `left` of the keys equal to it stay, the first ones
         int left = k;
-        if (!CL && n <= kAllPairs && held) {
+        if (pairs) {
             __syncthreads();
             if (tid < n) {
                 const uint32_t mine = keys[tid];
@@ -139,37 +154,41 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
             prefix = s_prefix;
             left = s_left;
         } else {
-            for (int pass = 0; pass < 3; ++pass) {
-                const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
+            for (int pass = 0; pass < 4; ++pass) {
+                const int shift = 24 - 8 * pass;
                 int *h = hist[pass & 1];
-                for (int i = tid; i < kBins; i += kThreads) h[i] = 0;
-                __syncthreads();
-                for (int i = tid; i < cnt; i += kThreads) {
-                    const uint32_t key = key_at(i);
-                    // (the digits above: all 32 bits shifted out in the first pass)
-                    if (pass == 0 || (key >> (pass == 1 ? 21 : 10)) == (prefix >> (pass == 1 ? 21 : 10)))
-                        atomicAdd(&h[(key >> shift) & (bins - 1)], 1);
+                if (pass > 0) {
+                    if (tid < kBins) h[tid] = 0;
+                    __syncthreads();
+                    const uint32_t found = prefix >> (shift + 8);
+                    for (int i = tid * 4; i < cnt; i += 4 * kThreads) {
+                        const uint4 q = four(i);
+                        const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (i + u < cnt && (k4[u] >> (shift + 8)) == found)
+                                atomicAdd(&h[(k4[u] >> shift) & (kBins - 1)], 1);
+                    }
                 }
                 if (CL)
                     cluster_sync();
                 else
                     __syncthreads();
-                // four digits a thread, the largest first; the thread whose sum reaches `left` has the digit
-                const int d0 = kBins - 4 - tid * 4;
-                int4 v = make_int4(0, 0, 0, 0);
-                if (CL) {
-                    int4 part[8];
+                // a digit a thread, the largest first; the thread whose sum reaches `left` has the digit
+                int c = 0;
+                if (tid < kBins) {
+                    const int *d = &h[kBins - 1 - tid];
+                    if (CL) {
+                        int part[8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) part[r] = r < C ? peer_int4(&h[d0], r) : make_int4(0, 0, 0, 0);
+                        for (int r = 0; r < 8; ++r) part[r] = r < C ? peer_word(d, r) : 0;
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        v.x += part[r].x, v.y += part[r].y, v.z += part[r].z, v.w += part[r].w;
-                } else {
-                    v = *reinterpret_cast<const int4 *>(&h[d0]);
+                        for (int r = 0; r < 8; ++r) c += part[r];
+                    } else {
+                        c = *d;
+                    }
                 }
-                const int c[4] = {v.w, v.z, v.y, v.x};
-                const int sum = (c[0] + c[1]) + (c[2] + c[3]);
-                int before = sum;
+                int before = c;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, before, o);
@@ -178,16 +197,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
                 if (lane == 31) wsum[0][warp] = before;
                 __syncthreads();
                 for (int w = 0; w < warp; ++w) before += wsum[0][w];
-                before -= sum; // keys of larger digits
-                if (before < left && left <= before + sum) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (before < left && left <= before + c[i]) {
-                            s_prefix = prefix | ((uint32_t)(kBins - 1 - (tid * 4 + i)) << shift);
-                            s_left = left - before;
-                        }
-                        before += c[i];
-                    }
+                before -= c; // keys of larger digits
+                if (before < left && left <= before + c) {
+                    s_prefix = prefix | ((uint32_t)(kBins - 1 - tid) << shift);
+                    s_left = left - before;
                 }
                 __syncthreads();
                 prefix = s_prefix;
@@ -195,15 +208,20 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
             }
         }
         // ---- each warp's run of the stretch: larger and equal keys, their sums before it, then the positions
-        const int run = ((cnt + kWarps - 1) / kWarps + 31) & ~31;
+        const int run = ((cnt + kWarps - 1) / kWarps + 127) & ~127;
         const int rb = min(warp * run, cnt), re = min(rb + run, cnt);
         int gt = 0, eq = 0;
-        for (int i0 = rb; i0 < re; i0 += 32) {
-            const int i = i0 + lane;
-            const uint32_t key = i < re ? key_at(i) : 0u;
-            gt += __popc(__ballot_sync(0xffffffffu, i < re && key > prefix));
-            eq += __popc(__ballot_sync(0xffffffffu, i < re && key == prefix));
+        for (int i = rb + lane * 4; i < re; i += 128) {
+            const uint4 q = four(i);
+            const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                gt += i + u < re && k4[u] > prefix;
+                eq += i + u < re && k4[u] == prefix;
+            }
         }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        eq = __reduce_add_sync(0xffffffffu, eq);
         __syncthreads(); // wsum has been read
         if (lane == 0) wsum[0][warp] = gt, wsum[1][warp] = eq;
         __syncthreads();
@@ -215,20 +233,38 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
             for (int r = 0; r < rank; ++r) at += peer_word(&sums[0], r), eqb += peer_word(&sums[1], r);
         }
         at += min(eqb, left);
-        for (int i0 = rb; i0 < re; i0 += 32) {
-            const int i = i0 + lane;
-            const uint32_t key = i < re ? key_at(i) : 0u;
-            const unsigned be = __ballot_sync(0xffffffffu, i < re && key == prefix);
-            const bool stay =
-                i < re && (key > prefix || (key == prefix && eqb + __popc(be & ((1u << lane) - 1)) < left));
-            const unsigned st = __ballot_sync(0xffffffffu, stay);
-            if (stay) {
-                const int p = at + __popc(st & ((1u << lane) - 1));
-                kept[p] = b + i;
-                mo[p] = key_mass(key);
+        for (int i0 = rb; i0 < re; i0 += 128) {
+            const int i = i0 + lane * 4;
+            const uint4 q = i < re ? four(i) : make_uint4(0, 0, 0, 0);
+            const uint32_t k4[4] = {q.x, q.y, q.z, q.w};
+            int g = 0, e = 0; // this lane's larger and equal keys
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                g += i + u < re && k4[u] > prefix;
+                e += i + u < re && k4[u] == prefix;
             }
-            at += __popc(st);
-            eqb += __popc(be);
+            int both = g | (e << 16); // summed over the lanes before, and over all
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, both, o);
+                if (lane >= o) both += v;
+            }
+            const int all = __shfl_sync(0xffffffffu, both, 31);
+            int e_at = eqb + (both >> 16) - e;
+            // equal keys take a place while fewer than `left` of them have
+            int p = at + (both & 0xFFFF) - g + min(e_at, left) - min(eqb, left);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool in = i + u < re, same = in && k4[u] == prefix;
+                if (in && (k4[u] > prefix || (same && e_at < left))) {
+                    kept[p] = b + i + u;
+                    mo[p] = key_mass(k4[u]);
+                    ++p;
+                }
+                e_at += same;
+            }
+            at += (all & 0xFFFF) + min(eqb + (all >> 16), left) - min(eqb, left);
+            eqb += all >> 16;
         }
     }
     // ---- the recent tokens (or a short sequence whole), then what lies behind
@@ -239,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
         mo[p] = m[p + from];
     }
     for (int p = len + t0; p < a.budget; p += step) kept[p] = -1;
+#pragma unroll 4
     for (int64_t p = len + t0; p < a.mass_out_len; p += step) mo[p] = 0.f;
 
     // ---- move: every CTA of the row sees all kept positions, and nobody's shared memory is read any more
@@ -261,21 +298,28 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
         if constexpr (!I4) return p + o * a.row_bytes;
         return p + (code ? int4_codes(kv, o, in_row, a.d) : int4_params(kv, o, a.d));
     };
-    auto look_up = [&](int j) {
-        uint2 r = make_uint2(~0u, ~0u);
-        if (j >= len) return r;
-        const int t = kept[j];
-        const int sb = src_t[t >> a.bs_log2], db = dst_t[j >> a.bs_log2];
-        if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks)
-            set_error(a.err, PKV_DEVERR_BLOCK_ID);
-        else
-            r = make_uint2(((uint32_t)sb << a.bs_log2) + (t & (bs - 1)), ((uint32_t)db << a.bs_log2) + (j & (bs - 1)));
-        return r;
+    // a chunk's tokens, a thread each: the position two chunks ahead, its blocks one chunk ahead
+    const int stride = C * kThreads, mine = rank * kThreads + tid;
+    auto kept_at = [&](int j) { return j < len ? kept[j] : -1; };
+    auto blocks_at = [&](int j, int t) {
+        return t < 0 ? make_int2(0, 0) : make_int2(src_t[t >> a.bs_log2], dst_t[j >> a.bs_log2]);
     };
-    slots[0][tid] = look_up(rank * kThreads + tid);
+    auto slots_of = [&](int j, int t, int2 b) {
+        if (t < 0) return make_uint2(~0u, ~0u);
+        if (b.x < 0 || b.x >= a.num_blocks || b.y < 0 || b.y >= a.num_blocks) {
+            set_error(a.err, PKV_DEVERR_BLOCK_ID);
+            return make_uint2(~0u, ~0u);
+        }
+        return make_uint2(((uint32_t)b.x << a.bs_log2) + (t & (bs - 1)), ((uint32_t)b.y << a.bs_log2) + (j & (bs - 1)));
+    };
+    int t1 = kept_at(mine), t2 = kept_at(mine + stride);
+    slots[0][tid] = slots_of(mine, t1, blocks_at(mine, t1));
     __syncthreads();
-    for (int j0 = rank * kThreads, buf = 0; j0 < len; j0 += C * kThreads, buf ^= 1) {
-        const uint2 next = look_up(j0 + C * kThreads + tid);
+    for (int j0 = rank * kThreads, buf = 0; j0 < len; j0 += stride, buf ^= 1) {
+        t1 = t2;
+        const int j1 = j0 + stride + tid;
+        const int2 b1 = blocks_at(j1, t1);
+        t2 = kept_at(j1 + stride);
         const int here = min(kThreads, len - j0);
         if (code || par) {
             for (int i0 = grp; i0 < here; i0 += kGroups * kMoveUnroll) {
@@ -301,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
                 }
             }
         }
-        slots[buf ^ 1][tid] = next;
+        slots[buf ^ 1][tid] = slots_of(j1, t1, b1);
         __syncthreads();
     }
 }
@@ -361,7 +405,8 @@ cudaError_t launch_evict(pkv_cache *c, const EvictLaunch &v, cudaStream_t st) {
     const bool i4 = c->kv_dtype == PKV_INT4;
     a.row_bytes = i4 ? a.d / 2 : a.d * c->elem_bytes;
     const unsigned rows = (unsigned)v.num_seqs * (unsigned)a.hkv;
-    // a CTA per row, or a cluster while that leaves SMs without one and gives each CTA 2048 positions or more
+    // a CTA per row, or a cluster while there are SMs for its CTAs and each gets 2048 positions or more (16 rows
+    // of 131071 positions: 59 us with clusters of 8, 63 with 16, whose barriers take longer)
     a.cluster = 1;
     while (a.cluster < 8 && (int64_t)rows * a.cluster * 2 <= c->num_sms && a.cap / (2 * a.cluster) >= 2048) a.cluster *= 2;
     const int64_t stretch = ((a.cap + a.cluster - 1) / a.cluster + 31) / 32 * 32;
