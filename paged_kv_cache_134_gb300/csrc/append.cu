@@ -52,7 +52,7 @@ struct AppendArgs {
     int64_t n, num_slots;
     int hkv, bs, chunks_per_row; // chunks_per_row = D / 8
     int64_t tile_elems;          // bs * D
-    int d;
+    int d, bs_log2;
 };
 
 // KVT: 0 = 16-bit cache (bit copy), 2 = E4M3 cache; MT = model dtype for the E4M3 path;
@@ -156,27 +156,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 }
 
 // 4-bit append.  Per (token, K|V, KV head) row x[0 .. D): z = min x, s = RN((max x - min x) / 15) in the
-// model's type, code = min(15, rint((x - z) / s)); int4.cuh has the layout and the border cases.  D / 8
-// lanes share a row, eight elements each: the extremes meet by xor shuffles (on packed pairs, with the
-// NaN-propagating forms, so a NaN anywhere reaches s), and each lane writes the four bytes of its codes.
-//
-// The quotient has to be the correctly rounded one, so that a code does not hang on how it was computed;
-// an IEEE division per element would double the kernel's arithmetic, so the codes come from a
-// multiplication by 1 / s wherever its error (below 1e-5 at quotients up to 22) cannot move rint, and only
-// the others divide.  Bound by HBM: 4 D bytes read and D + 8 written per token and head.
-template <int MT, int MODE>
+// model's type, code = min(15, rint((x - z) / s)); int4.cuh has the layout and the border cases.  D / 16 lanes
+// share a row, sixteen elements each (two 16-byte loads): the extremes meet by xor shuffles in the NaN-propagating
+// forms, so a NaN anywhere reaches s, and each lane writes the eight bytes of its codes.  With eight elements a
+// lane the row's own work (range, step, reciprocal) cost as much as the codes.  Bound by HBM (4 D bytes read and
+// D + 8 written per token and head) once the arithmetic is out of the way; fp32 pairs halve its instructions.
+constexpr int kAppend4Unroll = 1; // (two: 80 registers, 60 us against 55 for 5256 tokens x 32 heads written and read back)
+
+template <int D, int MT, int MODE>
 __global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
     pdl_trigger();
     pdl_wait();
-    const int cpr = a.chunks_per_row, row_chunks = a.hkv * cpr, per_token = 2 * row_chunks;
+    constexpr int per_row = D / 16;
+    const int side = a.hkv * per_row, per_token = 2 * side;
     const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
     const int lt = tpg > 1 ? (int)threadIdx.x / per_token : 0;
     const int r0 = tpg > 1 ? (int)threadIdx.x - lt * per_token : (int)threadIdx.x;
     const int rstep = tpg > 1 ? per_token : kAppendThreads;
     if (lt >= tpg) return;
-    // the lanes that share a row: per_token, rstep and kAppendThreads are multiples of cpr (8 or 16), so
-    // they take every branch below together
-    const unsigned lanes = ((1u << cpr) - 1u) << ((threadIdx.x & 31) & ~(cpr - 1));
+    // the lanes that share a row: per_token, rstep and kAppendThreads are multiples of per_row (8 or 4), so they
+    // take every branch below together
+    const unsigned lanes = ((1u << per_row) - 1u) << ((threadIdx.x & 31) & ~(per_row - 1));
     for (int64_t j = (int64_t)blockIdx.x * tpg + lt; j < a.n; j += (int64_t)gridDim.x * tpg) {
         const int64_t slot = append_slot<MODE>(a, j);
         if (MODE != SLOTS_GIVEN && r0 == 0 && a.slots_out) a.slots_out[j] = slot;
@@ -185,25 +185,28 @@ __global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
             if (r0 == 0) set_error(a.err, PKV_DEVERR_SLOT);
             continue;
         }
-        const int64_t blk = slot / a.bs;
-        const int off = static_cast<int>(slot - blk * a.bs);
-        const uint4 *ksrc = a.k + j * row_chunks, *vsrc = a.v + j * row_chunks;
-        for (int rb = r0; rb < per_token; rb += kAppendUnroll * rstep) {
-            uint4 src[kAppendUnroll];
+        const int64_t blk = slot >> a.bs_log2;
+        const int off = static_cast<int>(slot) & (a.bs - 1);
+        const uint4 *ksrc = a.k + j * side * 2, *vsrc = a.v + j * side * 2;
+        for (int rb = r0; rb < per_token; rb += kAppend4Unroll * rstep) {
+            uint4 src[kAppend4Unroll][2];
 #pragma unroll
-            for (int u = 0; u < kAppendUnroll; ++u) {
-                const int r = rb + u * rstep;
-                if (r < per_token) src[u] = r >= row_chunks ? vsrc[r - row_chunks] : ksrc[r];
-            }
-#pragma unroll
-            for (int u = 0; u < kAppendUnroll; ++u) {
+            for (int u = 0; u < kAppend4Unroll; ++u) {
                 const int r = rb + u * rstep;
                 if (r >= per_token) continue;
-                const int kv = r >= row_chunks ? 1 : 0, hc = r - kv * row_chunks, h = hc / cpr, c = hc - h * cpr;
-                const Int4Row row = int4_quantise<MT>(src[u], cpr, lanes);
-                char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, a.d);
-                *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, c * 4, a.d)) = row.codes;
-                if (c == 0) *reinterpret_cast<uint32_t *>(tile + int4_params(kv, off, a.d)) = row.params;
+                const uint4 *p = (r >= side ? vsrc - side * 2 : ksrc) + r * 2;
+                src[u][0] = __ldcs(p);
+                src[u][1] = __ldcs(p + 1);
+            }
+#pragma unroll
+            for (int u = 0; u < kAppend4Unroll; ++u) {
+                const int r = rb + u * rstep;
+                if (r >= per_token) continue;
+                const int kv = r >= side ? 1 : 0, hc = r - kv * side, h = hc / per_row, c = hc - h * per_row;
+                const Int4Row row = int4_quantise<MT>(src[u], per_row, lanes);
+                char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, D);
+                *reinterpret_cast<uint2 *>(tile + int4_codes(kv, off, c * 8, D)) = row.codes;
+                if (c == 0) *reinterpret_cast<uint32_t *>(tile + int4_params(kv, off, D)) = row.params;
             }
         }
     }
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
 
 // Rows read back: token j's K and V at slots[j] in the model's type (a 4- or 8-bit row's values, rounded
 // once; a 16-bit row's bits).  A negative slot gives a row of zeros, one past the pool zeros and
-// PKV_DEVERR_SLOT.  Bound by HBM; the append's assignment of threads to chunks, loads before stores.
+// PKV_DEVERR_SLOT.  Bound by HBM; sixteen elements a thread, loads before stores.
 struct GatherArgs {
     uint4 *k, *v;
     const int64_t *slots;
@@ -219,36 +222,18 @@ struct GatherArgs {
     const float *k_scale, *v_scale;
     unsigned int *err;
     int64_t n, num_slots;
-    int hkv, bs, chunks_per_row, d;
+    int hkv, bs_log2;
 };
+constexpr int kGatherUnroll = 2;
 
-template <int KVT, int MT>
-PKV_DEV uint4 gather_chunk(const GatherArgs &a, int64_t blk, int off, int kv, int h, int c) {
-    using M = ModelT<MT>;
-    const int64_t e = ((blk * 2 + kv) * a.hkv + h) * ((int64_t)a.bs * a.d) + (int64_t)off * a.d + c * 8;
-    if constexpr (KVT == PKV_F16) {
-        return reinterpret_cast<const uint4 *>(a.pool)[e / 8];
-    } else {
-        float f[8];
-        if constexpr (KVT == PKV_FP8_E4M3) {
-            cvt8_e4m3(reinterpret_cast<const uint2 *>(a.pool)[e / 8], f);
-            const float sc = (kv ? a.v_scale : a.k_scale)[h];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= sc;
-        } else {
-            const char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, a.d);
-            int4_values<MT>(*reinterpret_cast<const uint32_t *>(tile + int4_codes(kv, off, c * 4, a.d)),
-                            *reinterpret_cast<const uint32_t *>(tile + int4_params(kv, off, a.d)), f);
-        }
-        return make_uint4(M::pack(f[0], f[1]), M::pack(f[2], f[3]), M::pack(f[4], f[5]), M::pack(f[6], f[7]));
-    }
-}
-
-template <int KVT, int MT>
+template <int D, int KVT, int MT>
 __global__ void __launch_bounds__(kAppendThreads) gather_kernel(GatherArgs a) {
+    using M = ModelT<MT>;
     pdl_trigger();
     pdl_wait();
-    const int cpr = a.chunks_per_row, row_chunks = a.hkv * cpr, per_token = 2 * row_chunks;
+    constexpr int per_row = D / 16;
+    constexpr int kWords = KVT == PKV_INT4 ? 2 : KVT == PKV_FP8_E4M3 ? 4 : 8; // of sixteen stored elements
+    const int side = a.hkv * per_row, per_token = 2 * side, bs = 1 << a.bs_log2;
     const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
     const int lt = tpg > 1 ? (int)threadIdx.x / per_token : 0;
     const int r0 = tpg > 1 ? (int)threadIdx.x - lt * per_token : (int)threadIdx.x;
@@ -260,26 +245,59 @@ __global__ void __launch_bounds__(kAppendThreads) gather_kernel(GatherArgs a) {
             if (r0 == 0) set_error(a.err, PKV_DEVERR_SLOT);
             slot = -1;
         }
-        const int64_t blk = slot < 0 ? 0 : slot / a.bs;
-        const int off = static_cast<int>(slot - blk * a.bs);
-        for (int rb = r0; rb < per_token; rb += kAppendUnroll * rstep) {
-            uint4 x[kAppendUnroll];
+        const int64_t blk = slot < 0 ? 0 : slot >> a.bs_log2;
+        const int off = slot < 0 ? 0 : static_cast<int>(slot) & (bs - 1);
+        for (int rb = r0; rb < per_token; rb += kGatherUnroll * rstep) {
+            uint32_t x[kGatherUnroll][kWords], par[kGatherUnroll];
 #pragma unroll
-            for (int u = 0; u < kAppendUnroll; ++u) {
+            for (int u = 0; u < kGatherUnroll; ++u) {
                 const int r = rb + u * rstep;
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (r < per_token && slot >= 0) {
-                    const int kv = r >= row_chunks ? 1 : 0, hc = r - kv * row_chunks, h = hc / cpr;
-                    x[u] = gather_chunk<KVT, MT>(a, blk, off, kv, h, hc - h * cpr);
+                if (r >= per_token || slot < 0) continue;
+                const int kv = r >= side ? 1 : 0, hc = r - kv * side, h = hc / per_row, c = hc - h * per_row;
+                if constexpr (KVT == PKV_INT4) {
+                    const char *tile = a.pool + int4_head(blk, h, a.hkv, bs, D);
+                    const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(tile + int4_codes(kv, off, c * 8, D)));
+                    x[u][0] = w.x;
+                    x[u][1] = w.y;
+                    par[u] = *reinterpret_cast<const uint32_t *>(tile + int4_params(kv, off, D));
+                } else {
+                    const char *p = a.pool + ((((blk * 2 + kv) * a.hkv + h) << a.bs_log2) + off) * (D * kWords / 4) +
+                                    c * kWords * 4;
+#pragma unroll
+                    for (int i = 0; i < kWords; i += 4) {
+                        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p) + i / 4);
+                        x[u][i] = w.x;
+                        x[u][i + 1] = w.y;
+                        x[u][i + 2] = w.z;
+                        x[u][i + 3] = w.w;
+                    }
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kAppendUnroll; ++u) {
+            for (int u = 0; u < kGatherUnroll; ++u) {
                 const int r = rb + u * rstep;
-                if (r < row_chunks)
-                    a.k[j * row_chunks + r] = x[u];
-                else if (r < per_token)
-                    a.v[j * row_chunks + r - row_chunks] = x[u];
+                if (r >= per_token) continue;
+                const int kv = r >= side ? 1 : 0, hc = r - kv * side;
+                uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (slot >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (KVT == PKV_INT4) {
+                            o[i] = int4_values<MT>(x[u][i], par[u]);
+                        } else if constexpr (KVT == PKV_FP8_E4M3) {
+                            const float sc = (kv ? a.v_scale : a.k_scale)[hc / per_row];
+                            float f[8];
+                            cvt8_e4m3(make_uint2(x[u][2 * i], x[u][2 * i + 1]), f);
+                            o[i] = make_uint4(M::pack(f[0] * sc, f[1] * sc), M::pack(f[2] * sc, f[3] * sc),
+                                              M::pack(f[4] * sc, f[5] * sc), M::pack(f[6] * sc, f[7] * sc));
+                        } else {
+                            o[i] = make_uint4(x[u][4 * i], x[u][4 * i + 1], x[u][4 * i + 2], x[u][4 * i + 3]);
+                        }
+                    }
+                }
+                uint4 *dst = (kv ? a.v : a.k) + (j * side + hc) * 2;
+                dst[0] = o[0];
+                dst[1] = o[1];
             }
         }
     }
@@ -306,6 +324,7 @@ AppendArgs base_args(pkv_cache *c, const void *k, const void *v, int64_t n) {
     a.chunks_per_row = c->head_dim / 8;
     a.tile_elems = (int64_t)c->block_size * c->head_dim;
     a.d = c->head_dim;
+    a.bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
     return a;
 }
 
@@ -315,15 +334,18 @@ cudaError_t launch_append_t(pkv_cache *c, const AppendArgs &a, cudaStream_t st) 
     const int per_token = 2 * a.hkv * a.chunks_per_row;
     const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
     const int64_t passes = (a.n + tpg - 1) / tpg;
-    const int64_t cap = (int64_t)c->num_sms * 8;
+    // (4-bit: more and shorter CTAs, so that the last ones of a prompt leave fewer SMs idle)
+    const int64_t cap = (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? 32 : 8);
     const dim3 grid((unsigned)(passes < 1 ? 1 : (passes > cap ? cap : passes)));
     PkvTimer timer(c, PKV_KIND_APPEND, st);
     cudaError_t e;
-    if (c->kv_dtype == PKV_INT4)
-        e = c->model_dtype == PKV_F16
-                ? pdl_launch(append4_kernel<PKV_F16, MODE>, grid, dim3(kAppendThreads), 0, st, a)
-                : pdl_launch(append4_kernel<PKV_BF16, MODE>, grid, dim3(kAppendThreads), 0, st, a);
-    else if (c->kv_dtype != PKV_FP8_E4M3)
+    if (c->kv_dtype == PKV_INT4) {
+        auto kern = c->head_dim == 64
+                        ? (c->model_dtype == PKV_F16 ? append4_kernel<64, PKV_F16, MODE> : append4_kernel<64, PKV_BF16, MODE>)
+                        : (c->model_dtype == PKV_F16 ? append4_kernel<128, PKV_F16, MODE>
+                                                     : append4_kernel<128, PKV_BF16, MODE>);
+        e = pdl_launch(kern, grid, dim3(kAppendThreads), 0, st, a);
+    } else if (c->kv_dtype != PKV_FP8_E4M3)
         e = pdl_launch(append_kernel<PKV_F16, PKV_F16, MODE>, grid, dim3(kAppendThreads), 0, st, a);
     else if (c->model_dtype == PKV_F16)
         e = pdl_launch(append_kernel<PKV_FP8_E4M3, PKV_F16, MODE>, grid, dim3(kAppendThreads), 0, st, a);
@@ -394,21 +416,23 @@ cudaError_t launch_gather(pkv_cache *c, const int64_t *slots, int64_t n, void *k
     a.n = n;
     a.num_slots = c->num_blocks * c->block_size;
     a.hkv = c->num_kv_heads;
-    a.bs = c->block_size;
-    a.chunks_per_row = c->head_dim / 8;
-    a.d = c->head_dim;
-    const int per_token = 2 * a.hkv * a.chunks_per_row;
+    a.bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
+    const int per_token = 2 * a.hkv * (c->head_dim / 16);
     const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
-    const int64_t passes = (n + tpg - 1) / tpg, cap = (int64_t)c->num_sms * 8;
+    const int64_t passes = (n + tpg - 1) / tpg, cap = (int64_t)c->num_sms * 32;
     const dim3 grid((unsigned)(passes > cap ? cap : passes)), block(kAppendThreads);
-    const bool h = c->model_dtype == PKV_F16;
+    const bool d64 = c->head_dim == 64, h = c->model_dtype == PKV_F16;
     PkvTimer timer(c, PKV_KIND_COPY, st);
     g_pkv_launches++;
-    if (c->kv_dtype == PKV_INT4)
-        return h ? pdl_launch(gather_kernel<PKV_INT4, PKV_F16>, grid, block, 0, st, a)
-                 : pdl_launch(gather_kernel<PKV_INT4, PKV_BF16>, grid, block, 0, st, a);
-    if (c->kv_dtype == PKV_FP8_E4M3)
-        return h ? pdl_launch(gather_kernel<PKV_FP8_E4M3, PKV_F16>, grid, block, 0, st, a)
-                 : pdl_launch(gather_kernel<PKV_FP8_E4M3, PKV_BF16>, grid, block, 0, st, a);
-    return pdl_launch(gather_kernel<PKV_F16, PKV_F16>, grid, block, 0, st, a);
+    if (c->kv_dtype == PKV_INT4) {
+        auto kern = d64 ? (h ? gather_kernel<64, PKV_INT4, PKV_F16> : gather_kernel<64, PKV_INT4, PKV_BF16>)
+                        : (h ? gather_kernel<128, PKV_INT4, PKV_F16> : gather_kernel<128, PKV_INT4, PKV_BF16>);
+        return pdl_launch(kern, grid, block, 0, st, a);
+    }
+    if (c->kv_dtype == PKV_FP8_E4M3) {
+        auto kern = d64 ? (h ? gather_kernel<64, PKV_FP8_E4M3, PKV_F16> : gather_kernel<64, PKV_FP8_E4M3, PKV_BF16>)
+                        : (h ? gather_kernel<128, PKV_FP8_E4M3, PKV_F16> : gather_kernel<128, PKV_FP8_E4M3, PKV_BF16>);
+        return pdl_launch(kern, grid, block, 0, st, a);
+    }
+    return pdl_launch(d64 ? gather_kernel<64, PKV_F16, PKV_F16> : gather_kernel<128, PKV_F16, PKV_F16>, grid, block, 0, st, a);
 }

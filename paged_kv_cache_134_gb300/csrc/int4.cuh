@@ -38,7 +38,7 @@ PKV_DEV int int4_params(int kv, int off, int d) {
 }
 
 struct Int4Row {
-    uint32_t codes;  // this lane's eight
+    uint2 codes;     // this lane's sixteen
     uint32_t params; // s in the low half, z in the high half (the same on every lane of the row)
 };
 
@@ -68,60 +68,108 @@ PKV_DEV float half_of(uint32_t w, int i) {
         return __uint_as_float(i ? w & 0xFFFF0000u : w << 16);
 }
 
-// Eight elements of a row that the `cpr` lanes of `lanes` hold together.
+// Sixteen elements of a row that the `per_row` lanes of `lanes` hold together.  Codes come from a multiplication by
+// 1 / s; the quotient has to be the correctly rounded one, so that a code does not hang on how it was computed, so
+// lanes with a product within 2e-5 of a half (its error is below 1e-5 at quotients up to 22) divide instead, as do
+// rows whose largest quotient passes 15.4 (a step that the model's type holds to few bits), which are cut at 15.
 template <int MT>
-PKV_DEV Int4Row int4_quantise(const uint4 &src, int cpr, unsigned lanes) {
+PKV_DEV Int4Row int4_quantise(const uint4 (&src)[2], int per_row, unsigned lanes) {
     using M = ModelT<MT>;
-    uint32_t lo = min2_nan<MT>(min2_nan<MT>(src.x, src.y), min2_nan<MT>(src.z, src.w));
-    uint32_t hi = max2_nan<MT>(max2_nan<MT>(src.x, src.y), max2_nan<MT>(src.z, src.w));
-    for (int o = 1; o < cpr; o <<= 1) {
-        lo = min2_nan<MT>(lo, __shfl_xor_sync(lanes, lo, o));
-        hi = max2_nan<MT>(hi, __shfl_xor_sync(lanes, hi, o));
-    }
+    uint32_t lo = min2_nan<MT>(min2_nan<MT>(min2_nan<MT>(src[0].x, src[0].y), min2_nan<MT>(src[0].z, src[0].w)),
+                               min2_nan<MT>(min2_nan<MT>(src[1].x, src[1].y), min2_nan<MT>(src[1].z, src[1].w)));
+    uint32_t hi = max2_nan<MT>(max2_nan<MT>(max2_nan<MT>(src[0].x, src[0].y), max2_nan<MT>(src[0].z, src[0].w)),
+                               max2_nan<MT>(max2_nan<MT>(src[1].x, src[1].y), max2_nan<MT>(src[1].z, src[1].w)));
+    // the pair's least and largest as one word: two shuffles a step would carry two words
     lo = min2_nan<MT>(lo, __byte_perm(lo, lo, 0x1032));
     hi = max2_nan<MT>(hi, __byte_perm(hi, hi, 0x1032));
-    const float z = half_of<MT>(lo, 0), range = __fsub_rn(half_of<MT>(hi, 0), z);
+    uint32_t both = __byte_perm(lo, hi, 0x5410); // least low, largest high
+    for (int o = 1; o < per_row; o <<= 1) {
+        const uint32_t other = __shfl_xor_sync(lanes, both, o);
+        both = __byte_perm(min2_nan<MT>(both, other), max2_nan<MT>(both, other), 0x7610);
+    }
+    const float z = half_of<MT>(both, 0), range = __fsub_rn(half_of<MT>(both, 1), z);
     Int4Row r;
+    r.codes = make_uint2(0, 0);
     if (!(range < INFINITY)) { // NaN or overflow; an infinity in the row makes the range one or the other
-        r.codes = 0;
         r.params = MT == PKV_F16 ? 0x7E007E00u : 0x7FC07FC0u;
         return r;
     }
     const uint32_t s16 = M::pack(__fdiv_rn(range, 15.f), 0.f) & 0xFFFFu;
     float s = half_of<MT>(s16, 0);
     if (s < 1.17549435e-38f) s = 0.f; // 2^-126
-    r.params = (s == 0.f ? 0u : s16) | (lo << 16);
-    r.codes = 0;
+    r.params = (s == 0.f ? 0u : s16) | (both << 16);
     if (s == 0.f) return r;
-    float f[8];
-    cvt8<MT>(src, f);
     const float inv = __frcp_rn(s);
-    bool near_tie = false;
-    float y[8];
+    const float2 inv2 = make_float2(inv, inv), minus_z = make_float2(-z, -z), zero = make_float2(0.f, 0.f),
+                 big = make_float2(12582912.f, 12582912.f), minus_big = make_float2(-12582912.f, -12582912.f),
+                 minus1 = make_float2(-1.f, -1.f);
+    bool slow = __fmul_rn(range, inv) > 15.4f;
+    float t[16]; // codes
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = __fsub_rn(f[i], z);
-        y[i] = __fmul_rn(d, inv);
-        const float t = __fsub_rn(__fadd_rn(y[i], 12582912.f), 12582912.f); // rint
-        near_tie |= fabsf(y[i] - t) > 0.4999f;
-        f[i] = d;
+    for (int u = 0; u < 2; ++u) {
+        float f[8];
+        cvt8<MT>(src[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float2 y = fma2(add2(make_float2(f[i], f[i + 1]), minus_z), inv2, zero);
+            const float2 n = add2(add2(y, big), minus_big); // rint
+            const float2 e = fma2(n, minus1, y);
+            slow |= fabsf(e.x) > 0.49998f || fabsf(e.y) > 0.49998f;
+            t[8 * u + i] = n.x;
+            t[8 * u + i + 1] = n.y;
+        }
     }
-    if (near_tie) {
+    if (slow) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(f[i], s);
+        for (int u = 0; u < 2; ++u) {
+            float f[8];
+            cvt8<MT>(src[u], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) { // (mostly one element: a test each, a division where it is needed)
+                const float d = __fsub_rn(f[i], z), n = t[8 * u + i];
+                if (fabsf(__fmul_rn(d, inv) - n) > 0.49998f || n > 15.f) t[8 * u + i] = fminf(rintf(__fdiv_rn(d, s)), 15.f);
+            }
+        }
     }
+    uint32_t w[4]; // four codes as a number below 2^16, in the low bits of 2^23 + it
 #pragma unroll
-    for (int i = 0; i < 8; ++i) // the low mantissa bits of y + 1.5 * 2^23 are rint(y)
-        r.codes |= (__float_as_uint(__fadd_rn(fminf(y[i], 15.f), 12582912.f)) & 15u) << (4 * i);
-    r.codes = ((r.codes << 3) & 0xFFF8FFF8u) | ((r.codes >> 13) & 0x00070007u);
+    for (int i = 0; i < 4; ++i)
+        w[i] = __float_as_uint(fmaf(fmaf(fmaf(t[4 * i + 3], 16.f, t[4 * i + 2]), 16.f, t[4 * i + 1]), 16.f, t[4 * i]) + 8388608.f);
+    auto rotate = [](uint32_t c) { return ((c << 3) & 0xFFF8FFF8u) | ((c >> 13) & 0x00070007u); };
+    r.codes = make_uint2(rotate(__byte_perm(w[0], w[1], 0x5410)), rotate(__byte_perm(w[2], w[3], 0x5410)));
     return r;
 }
 
-// values of eight codes (exact in fp32 but for the one rounding of the sum)
 template <int MT>
-PKV_DEV void int4_values(uint32_t codes, uint32_t params, float *f) {
-    const float s = half_of<MT>(params, 0), z = half_of<MT>(params, 1);
-    codes = ((codes >> 3) & 0x1FFF1FFFu) | ((codes << 13) & 0xE000E000u);
+PKV_DEV uint32_t pair_add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (MT == PKV_F16)
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <int MT>
+PKV_DEV uint32_t pair_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    if constexpr (MT == PKV_F16)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// The values s c + z of eight codes in the model's type, rounded once: a code in the low bits of 1024 (fp16) or 128
+// (bf16), that number taken off, a fused multiply-add.
+template <int MT>
+PKV_DEV uint4 int4_values(uint32_t codes, uint32_t params) {
+    constexpr uint32_t kBase = MT == PKV_F16 ? 0x64006400u : 0x43004300u, kMinus = kBase | 0x80008000u;
+    const uint32_t s = __byte_perm(params, 0, 0x1010), z = __byte_perm(params, 0, 0x3232);
+    const uint32_t c = ((codes >> 3) & 0x1FFF1FFFu) | ((codes << 13) & 0xE000E000u);
+    uint32_t v[4]; // elements (i, i + 4)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf(s, (float)((codes >> (4 * i)) & 15u), z);
+    for (int i = 0; i < 4; ++i)
+        v[i] = pair_fma<MT>(pair_add<MT>(((c >> (4 * i)) & 0x000F000Fu) | kBase, kMinus), s, z);
+    return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                      __byte_perm(v[2], v[3], 0x7632));
 }
