@@ -35,6 +35,8 @@ class PagedKVError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load the CUDA library (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -92,20 +94,27 @@ class _Profile(ctypes.Structure):
 
 
 def _check(status: int):
-    if status != 0:
+    if status:
         raise PagedKVError(status, lib().pkv_last_error().decode(errors="replace"))
 
 
-def _stream(stream=None) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream=None) -> int:
+    """The stream's handle: the current stream's of the current device by default.
+
+    (Raw handles and plain ints: building torch.cuda.Stream and ctypes objects took several of a small
+    call's microseconds.)"""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return t.data_ptr() if t is not None else None
 
 
 def _req(t: torch.Tensor, name: str, dtype=None, ndim=None):
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -118,10 +127,11 @@ def _req(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
 
 
-def _same_device(cache: "KVCache", **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device.index != cache.device:
-            raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.device}")
+def _same_device(cache: "KVCache", *tensors):
+    dev = cache.device
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the cache on cuda:{dev}")
 
 
 class _DevMem:
@@ -253,7 +263,7 @@ def paged_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slot_mappi
     _req(v, "v", cache.torch_dtype, 3)
     _req(slot_mapping, "slot_mapping", torch.int64, 1)
     n = k.shape[0]
-    if tuple(k.shape) != (n, cache.num_kv_heads, cache.head_dim) or k.shape != v.shape:
+    if k.shape != (n, cache.num_kv_heads, cache.head_dim) or k.shape != v.shape:
         raise ValueError(f"k/v must be [T, {cache.num_kv_heads}, {cache.head_dim}]")
     if slot_mapping.numel() != n:
         raise ValueError("slot_mapping length != number of tokens")
@@ -270,7 +280,7 @@ def paged_kv_append_at(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_t
     _req(seq_ids, "seq_ids", torch.int32, 1)
     _req(positions, "positions", torch.int32, 1)
     n = k.shape[0]
-    if tuple(k.shape) != (n, cache.num_kv_heads, cache.head_dim) or k.shape != v.shape:
+    if k.shape != (n, cache.num_kv_heads, cache.head_dim) or k.shape != v.shape:
         raise ValueError(f"k/v must be [T, {cache.num_kv_heads}, {cache.head_dim}]")
     if seq_ids.numel() != n or positions.numel() != n:
         raise ValueError("seq_ids/positions length != number of tokens")
@@ -291,13 +301,13 @@ def paged_kv_gather(cache: KVCache, slot_mapping: torch.Tensor, k: Optional[torc
     _req(slot_mapping, "slot_mapping", torch.int64, 1)
     n = slot_mapping.numel()
     shape = (n, cache.num_kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=cache.torch_dtype, device=slot_mapping.device) if k is None else k
-    v = torch.empty(shape, dtype=cache.torch_dtype, device=slot_mapping.device) if v is None else v
+    k = slot_mapping.new_empty(shape, dtype=cache.torch_dtype) if k is None else k
+    v = torch.empty_like(k) if v is None else v
     for name, t in (("k", k), ("v", v)):
         _req(t, name, cache.torch_dtype, 3)
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}")
-    _same_device(cache, slot_mapping=slot_mapping, k=k, v=v)
+    _same_device(cache, slot_mapping, k, v)
     _check(lib().paged_kv_gather(cache.handle, _ptr(slot_mapping), n, _ptr(k), _ptr(v), _stream()))
     return k, v
 
@@ -315,16 +325,16 @@ def paged_decode_attention_mass(q: torch.Tensor, cache: KVCache, block_tables: t
     S, hq, d = q.shape
     if d != cache.head_dim or block_tables.shape[0] != S or context_lens.numel() != S:
         raise ValueError("shape mismatch between q, block_tables and context_lens")
-    if tuple(attn_mass.shape[:2]) != (S, cache.num_kv_heads):
+    if attn_mass.shape[:2] != (S, cache.num_kv_heads):
         raise ValueError(f"attn_mass must be [{S}, {cache.num_kv_heads}, T]")
     if out is None:
         out = torch.empty_like(q)
     _req(out, "out", cache.torch_dtype, 3)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    _same_device(cache, q=q, block_tables=block_tables, context_lens=context_lens, attn_mass=attn_mass, out=out)
+    _same_device(cache, q, block_tables, context_lens, attn_mass, out)
     _check(lib().paged_decode_attention_mass(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
-                                             _ptr(context_lens), S, hq, ctypes.c_float(scale), ctypes.c_float(decay),
+                                             _ptr(context_lens), S, hq, float(scale), float(decay),
                                              _ptr(attn_mass), attn_mass.shape[2], _ptr(out), _stream()))
     return out
 
@@ -343,21 +353,19 @@ def paged_kv_evict(cache: KVCache, block_tables: torch.Tensor, context_lens: tor
     _req(context_lens, "context_lens", torch.int32, 1)
     _req(attn_mass, "attn_mass", torch.float32, 3)
     S, hkv, budget = context_lens.numel(), cache.num_kv_heads, int(budget)
-    if block_tables.shape[0] != S or dst_block_tables.shape[0] != S or tuple(attn_mass.shape[:2]) != (S, hkv):
+    if block_tables.shape[0] != S or dst_block_tables.shape[0] != S or attn_mass.shape[:2] != (S, hkv):
         raise ValueError("shape mismatch between tables, context_lens and attn_mass")
     if budget < 1:
         raise ValueError(f"budget {budget} is less than 1")
-    dev = context_lens.device
-    kept = torch.empty((S, hkv, budget), dtype=torch.int32, device=dev) if kept is None else kept
-    new_lens = torch.empty(S, dtype=torch.int32, device=dev) if new_lens is None else new_lens
+    kept = context_lens.new_empty((S, hkv, budget)) if kept is None else kept
+    new_lens = torch.empty_like(context_lens) if new_lens is None else new_lens
     new_mass = torch.empty_like(attn_mass) if new_mass is None else new_mass
     _req(kept, "kept", torch.int32, 3)
     _req(new_lens, "new_lens", torch.int32, 1)
     _req(new_mass, "new_mass", torch.float32, 3)
-    if tuple(kept.shape) != (S, hkv, budget) or new_lens.numel() != S or tuple(new_mass.shape[:2]) != (S, hkv):
+    if kept.shape != (S, hkv, budget) or new_lens.numel() != S or new_mass.shape[:2] != (S, hkv):
         raise ValueError("kept must be [S, num_kv_heads, budget], new_lens [S], new_mass [S, num_kv_heads, T']")
-    _same_device(cache, block_tables=block_tables, dst_block_tables=dst_block_tables, context_lens=context_lens,
-                 attn_mass=attn_mass, kept=kept, new_lens=new_lens, new_mass=new_mass)
+    _same_device(cache, block_tables, dst_block_tables, context_lens, attn_mass, kept, new_lens, new_mass)
     _check(lib().paged_kv_evict(cache.handle, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S,
                                 _ptr(attn_mass), attn_mass.shape[2], budget, int(recent), _ptr(dst_block_tables),
                                 dst_block_tables.shape[1], _ptr(kept), _ptr(new_lens), _ptr(new_mass),
@@ -378,7 +386,7 @@ def paged_decode_attention(q: torch.Tensor, cache: KVCache, block_tables: torch.
         out = torch.empty_like(q)
     _req(out, "out", cache.torch_dtype, 3)
     _check(lib().paged_decode_attention(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
-                                        _ptr(context_lens), S, hq, ctypes.c_float(scale), _ptr(out), _stream()))
+                                        _ptr(context_lens), S, hq, float(scale), _ptr(out), _stream()))
     return out
 
 
@@ -397,7 +405,7 @@ def paged_decode_attention_cascade(q: torch.Tensor, cache: KVCache, block_tables
     _req(out, "out", cache.torch_dtype, 3)
     _check(lib().paged_decode_attention_cascade(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
                                                 _ptr(context_lens), S, hq, int(shared_prefix_len),
-                                                ctypes.c_float(scale), _ptr(out), _stream()))
+                                                float(scale), _ptr(out), _stream()))
     return out
 
 
@@ -417,7 +425,7 @@ def paged_decode_attention_noalloc(q: torch.Tensor, cache: KVCache, block_tables
     if d != cache.head_dim or block_tables.shape[0] != S or context_lens.numel() != S or out.shape != q.shape:
         raise ValueError("shape mismatch between q, out, block_tables and context_lens")
     _check(lib().paged_decode_attention_noalloc(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
-                                                _ptr(context_lens), S, hq, ctypes.c_float(scale), _ptr(out),
+                                                _ptr(context_lens), S, hq, float(scale), _ptr(out),
                                                 _stream()))
     return out
 
@@ -440,7 +448,7 @@ def packed_prefill_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     _req(out, "out", cache.torch_dtype, 3)
     _check(lib().packed_prefill_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), nseq, int(max_seqlen), T,
                                           _ptr(block_tables), block_tables.shape[1], cache.handle, hq,
-                                          ctypes.c_float(scale), _ptr(out), _stream()))
+                                          float(scale), _ptr(out), _stream()))
     return out
 
 
@@ -504,7 +512,7 @@ def paged_prefill_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, c
     _req(out, "out", cache.torch_dtype, 3)
     _check(lib().paged_prefill_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(context_lens), nseq,
                                          int(max_seqlen), T, _ptr(block_tables), block_tables.shape[1], cache.handle,
-                                         hq, ctypes.c_float(scale), _ptr(out), _stream()))
+                                         hq, float(scale), _ptr(out), _stream()))
     return out
 
 

@@ -477,17 +477,6 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(const Args a) {
     }
 }
 
-// cudaFuncSetAttribute once per kernel, device and size
-inline cudaError_t allow_smem(const void *kern, size_t smem, std::atomic<int> *have) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64 && have[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && dev < 64) have[dev].store((int)smem, std::memory_order_relaxed);
-    return e;
-}
-
 inline unsigned grid_of(const Args &a, int slots) {
     const int64_t units = (int64_t)a.num_seqs * a.hkv * (a.max_splits > 0 ? a.max_splits : 1);
     return (unsigned)(units < slots ? units : slots);

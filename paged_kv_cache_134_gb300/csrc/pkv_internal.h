@@ -92,6 +92,17 @@ cudaError_t pdl_launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
+// cudaFuncSetAttribute once per kernel, device and size
+inline cudaError_t pkv_allow_smem(const void *kern, size_t smem, std::atomic<int> *have) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && have[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && dev < 64) have[dev].store((int)smem, std::memory_order_relaxed);
+    return e;
+}
+
 // launchers (one per translation unit); return cudaError_t of the launch
 cudaError_t launch_slot_mapping(const int32_t *tables, int rows, int max_blocks, const int32_t *seq_ids,
                                 const int32_t *positions, int64_t n, int bs, int64_t *out, cudaStream_t st);
