@@ -299,15 +299,19 @@ def paged_kv_gather(cache: KVCache, slot_mapping: torch.Tensor, k: Optional[torc
     """K and V at ``slot_mapping`` as (k, v), each [T, num_kv_heads, head_dim] in the model dtype: the
     stored values of any cache type (a negative slot gives zeros)."""
     _req(slot_mapping, "slot_mapping", torch.int64, 1)
+    _same_device(cache, slot_mapping)
     n = slot_mapping.numel()
     shape = (n, cache.num_kv_heads, cache.head_dim)
-    k = slot_mapping.new_empty(shape, dtype=cache.torch_dtype) if k is None else k
-    v = torch.empty_like(k) if v is None else v
     for name, t in (("k", k), ("v", v)):
-        _req(t, name, cache.torch_dtype, 3)
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}")
-    _same_device(cache, slot_mapping, k, v)
+        if t is not None:
+            _req(t, name, cache.torch_dtype, 3)
+            _same_device(cache, t)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+    if k is None:
+        k = slot_mapping.new_empty(shape, dtype=cache.torch_dtype)
+    if v is None:
+        v = torch.empty_like(k)
     _check(lib().paged_kv_gather(cache.handle, _ptr(slot_mapping), n, _ptr(k), _ptr(v), _stream()))
     return k, v
 
@@ -325,17 +329,20 @@ def paged_decode_attention_mass(q: torch.Tensor, cache: KVCache, block_tables: t
     S, hq, d = q.shape
     if d != cache.head_dim or block_tables.shape[0] != S or context_lens.numel() != S:
         raise ValueError("shape mismatch between q, block_tables and context_lens")
-    if attn_mass.shape[:2] != (S, cache.num_kv_heads):
+    rows, heads, mass_len = attn_mass.shape
+    if rows != S or heads != cache.num_kv_heads:
         raise ValueError(f"attn_mass must be [{S}, {cache.num_kv_heads}, T]")
+    _same_device(cache, q, block_tables, context_lens, attn_mass)
     if out is None:
         out = torch.empty_like(q)
-    _req(out, "out", cache.torch_dtype, 3)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    _same_device(cache, q, block_tables, context_lens, attn_mass, out)
+    else:
+        _req(out, "out", cache.torch_dtype, 3)
+        _same_device(cache, out)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
     _check(lib().paged_decode_attention_mass(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
                                              _ptr(context_lens), S, hq, float(scale), float(decay),
-                                             _ptr(attn_mass), attn_mass.shape[2], _ptr(out), _stream()))
+                                             _ptr(attn_mass), mass_len, _ptr(out), _stream()))
     return out
 
 
@@ -353,21 +360,27 @@ def paged_kv_evict(cache: KVCache, block_tables: torch.Tensor, context_lens: tor
     _req(context_lens, "context_lens", torch.int32, 1)
     _req(attn_mass, "attn_mass", torch.float32, 3)
     S, hkv, budget = context_lens.numel(), cache.num_kv_heads, int(budget)
-    if block_tables.shape[0] != S or dst_block_tables.shape[0] != S or attn_mass.shape[:2] != (S, hkv):
+    rows, heads, mass_len = attn_mass.shape
+    if block_tables.shape[0] != S or dst_block_tables.shape[0] != S or rows != S or heads != hkv:
         raise ValueError("shape mismatch between tables, context_lens and attn_mass")
     if budget < 1:
         raise ValueError(f"budget {budget} is less than 1")
-    kept = context_lens.new_empty((S, hkv, budget)) if kept is None else kept
-    new_lens = torch.empty_like(context_lens) if new_lens is None else new_lens
-    new_mass = torch.empty_like(attn_mass) if new_mass is None else new_mass
-    _req(kept, "kept", torch.int32, 3)
-    _req(new_lens, "new_lens", torch.int32, 1)
-    _req(new_mass, "new_mass", torch.float32, 3)
-    if kept.shape != (S, hkv, budget) or new_lens.numel() != S or new_mass.shape[:2] != (S, hkv):
-        raise ValueError("kept must be [S, num_kv_heads, budget], new_lens [S], new_mass [S, num_kv_heads, T']")
-    _same_device(cache, block_tables, dst_block_tables, context_lens, attn_mass, kept, new_lens, new_mass)
+    _same_device(cache, block_tables, dst_block_tables, context_lens, attn_mass)
+    for name, t, dtype, ndim in (("kept", kept, torch.int32, 3), ("new_lens", new_lens, torch.int32, 1),
+                                 ("new_mass", new_mass, torch.float32, 3)):
+        if t is not None:
+            _req(t, name, dtype, ndim)
+            _same_device(cache, t)
+            if t.shape[:2] != ((S,) if ndim == 1 else (S, hkv)) or (t is kept and t.shape[2] != budget):
+                raise ValueError("kept must be [S, num_kv_heads, budget], new_lens [S], new_mass [S, num_kv_heads, T']")
+    if kept is None:
+        kept = context_lens.new_empty((S, hkv, budget))
+    if new_lens is None:
+        new_lens = torch.empty_like(context_lens)
+    if new_mass is None:
+        new_mass = torch.empty_like(attn_mass)
     _check(lib().paged_kv_evict(cache.handle, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S,
-                                _ptr(attn_mass), attn_mass.shape[2], budget, int(recent), _ptr(dst_block_tables),
+                                _ptr(attn_mass), mass_len, budget, int(recent), _ptr(dst_block_tables),
                                 dst_block_tables.shape[1], _ptr(kept), _ptr(new_lens), _ptr(new_mass),
                                 new_mass.shape[2], _stream()))
     return kept, new_lens, new_mass
@@ -384,7 +397,8 @@ def paged_decode_attention(q: torch.Tensor, cache: KVCache, block_tables: torch.
         raise ValueError("shape mismatch between q, block_tables and context_lens")
     if out is None:
         out = torch.empty_like(q)
-    _req(out, "out", cache.torch_dtype, 3)
+    else:
+        _req(out, "out", cache.torch_dtype, 3)
     _check(lib().paged_decode_attention(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
                                         _ptr(context_lens), S, hq, float(scale), _ptr(out), _stream()))
     return out
