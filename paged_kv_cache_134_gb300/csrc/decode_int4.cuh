@@ -99,20 +99,21 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
     const int nfull = full[a.num_seqs] * a.hkv, nunits = nfull + part[a.num_seqs] * a.hkv;
     if ((int)blockIdx.x >= nunits) return;
 
-    // Tile `tile` of unit u to slot `slot`, a lane per block: whole octets (what lies behind the sequence's
-    // end is masked later: its codes are numbers, whatever they are).
+    // Tile `tile` of a unit (its tokens n, its table, its head's place in the pool) to slot `slot`, a lane per block:
+    // whole octets (what lies behind the sequence's end is masked later: its codes are numbers, whatever they are).
     const int lane_t = lane << bl;                       // this lane's block's first token in a tile
     const uint32_t lane_bytes = (bs >> 3) * G_::kOct;    // bytes of a block's tile part
-    auto issue = [&](const Unit &u, const int *table, int tile, int slot) {
+    const uint32_t lane_dst = lane * lane_bytes, blk_stride = (uint32_t)a.blk_stride;
+    auto issue = [&](int n, const int *table, const char *head, int tile, int slot) {
         const int t = tile * T + lane_t;
         int b = -1;
-        if (lane_t < T && t < u.n) b = table[t >> bl];
+        if (lane_t < T && t < n) b = table[t >> bl];
         const unsigned copies = __ballot_sync(0xffffffffu, b >= 0);
         if (lane == 0) mbar_arrive_expect_tx(&bars[slot], __popc(copies) * lane_bytes);
         __syncwarp();
         if (b >= 0)
-            bulk_g2s_hint(ring + slot * G_::kBytes + lane * lane_bytes, a.pool + b * a.blk_stride + u.kvh * a.head_stride,
-                          lane_bytes, &bars[slot], policy);
+            bulk_g2s_hint(ring + slot * G_::kBytes + lane_dst, head + (uint64_t)(uint32_t)b * blk_stride, lane_bytes,
+                          &bars[slot], policy);
     };
     // One warp's work for a unit of buffer `par`: find it and start its copies ...
     auto fetch = [&](int ui, int par) {
@@ -177,19 +178,21 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
     int turn = 1; // the warp that prepares the next unit, and takes a tile less of this one
     int slot = 0; // the slot of this warp's next tile
     int nt = 0;   // this warp's tiles of the unit
-    // Tile i of this warp: the others take one each before the warp whose turn it is gets its first.
-    auto tile_of = [&](int i) {
-        const int r = (warp - turn + kWarps - 1) & (kWarps - 1); // 3: this warp prepares the next unit
-        return r == 3 ? 4 * i + 6 : i == 0 ? r : 4 * i + r - 1;
-    };
+    // Tile i of this warp: the others take one each before the warp whose turn it is gets its first, so it is
+    // 4 i + tile0, and one more for the others' first.
+    int tile0 = 0;
+    const char *head = nullptr;
+    auto tile_of = [&](int i) { return 4 * i + tile0 + (i == 0 && tile0 < 6); };
     auto start = [&]() {
-        const int ntiles = (u.n + T - 1) / T, r = (warp - turn + kWarps - 1) & (kWarps - 1);
+        const int ntiles = (u.n + T - 1) / T, r = (warp - turn + kWarps - 1) & (kWarps - 1); // 3: this warp's turn
         nt = r == 3 ? max(0, ntiles - 3) / 4 : ntiles <= r ? 0 : 1 + max(0, ntiles - r) / 4;
+        tile0 = r == 3 ? 6 : r - 1;
+        head = a.pool + u.kvh * a.head_stride;
         if (!alive) return;
         int to = slot;
 #pragma unroll
         for (int i = 0; i < ST; ++i) {
-            if (i < nt) issue(u, table, tile_of(i), to);
+            if (i < nt) issue(u.n, table, head, tile_of(i), to);
             to = to == ST - 1 ? 0 : to + 1;
         }
     };
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
         const uint32_t lo_mask = GC != 8 && t4 >= 2 ? 0xFFFFE000u : 0u;
 
         for (int i = 0; i < nt; ++i) {
-            if (!mbar_wait(&bars[slot], (phase >> slot) & 1)) {
+            if (alive && !mbar_wait(&bars[slot], (phase >> slot) & 1)) {
                 set_error(a.err, PKV_DEVERR_TIMEOUT);
                 alive = false;
             }
@@ -337,12 +340,14 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                     f[1] *= A * invA;
                     A = nA;
                 }
+                if (i > 0) { // (nothing is summed before the first tile)
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    acc[k][0] *= f[0];
-                    acc[k][1] *= f[1];
-                    acc[k][2] *= f[0];
-                    acc[k][3] *= f[1];
+                    for (int k = 0; k < KS; ++k) {
+                        acc[k][0] *= f[0];
+                        acc[k][1] *= f[1];
+                        acc[k][2] *= f[0];
+                        acc[k][3] *= f[1];
+                    }
                 }
             }
             // ---- P^T as the second product's B operand: hi parts (columns 0..3) and lo parts (4..7), or
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
             outputs(std::integral_constant<int, 0>());
             outputs(std::integral_constant<int, 1>());
             __syncwarp(); // every lane has read the slot
-            if (i + ST < nt) issue(u, table, tile_of(i + ST), slot);
+            if (i + ST < nt) issue(u.n, table, head, 4 * (i + ST) + tile0, slot);
             slot = slot == ST - 1 ? 0 : slot + 1;
         }
 
@@ -442,10 +447,12 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                 z[k] = w[k].w == 0.f ? 0.f : row_sum(z[k]) * w[k].w;
                 if (g == 0) {
                     J.l[warp][2 * t4 + k] = w[k].w == 0.f ? 0.f : l[k] * w[k].w;
+                    J.z[warp][2 * t4 + k] = z[k];
                     if (warp == 0) J.M[2 * t4 + k] = w[k].M;
                 }
+                w[k].w *= A;
             }
-            // hi and lo columns together, the codes' powers of two and A, the warp's weight, the offsets
+            // hi and lo columns together; A and the warp's weight
 #pragma unroll
             for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                     if (NC == 1 && (e & 1)) continue;
                     float v = acc[k][e];
                     if constexpr (GC != 8) v += __shfl_xor_sync(0xffffffffu, v, 2);
-                    acc[k][e] = fmaf(v * (k & 1 ? 131072.f : 2097152.f), A * w[e & (NC - 1)].w, z[e & (NC - 1)]);
+                    acc[k][e] = v * w[e & (NC - 1)].w;
                 }
             if (2 * t4 < COLS) { // 16 (or 8) dims from (D / 8) g of each column
 #pragma unroll
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                 }
             }
         }
-        join_unit<D, COLS, MT, MASS>(a, cur, J, oacc);
+        join_unit<D, COLS, MT, MASS, true>(a, cur, J, oacc);
         prev = cur;
         pending = !MASS && cur.nsplit > 1 && a.done;
         if (!more) break;

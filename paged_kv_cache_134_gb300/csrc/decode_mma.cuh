@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
                 }
             }
         }
-        join_unit<D, COLS, MT, true>(a, cur, J, oacc);
+        join_unit<D, COLS, MT, true, false>(a, cur, J, oacc);
         if (!more) break;
         ui = un;
     }

@@ -298,7 +298,7 @@ PKV_DEV void stage_unit(const Args &a, const Unit &u, int *tb, char *qs, int i0,
 }
 
 struct Join {
-    float m[kWarps][8], l[kWarps][8]; // per warp and column
+    float m[kWarps][8], l[kWarps][8], z[kWarps][8]; // per warp and column
     float M[8], inv[8];
     float wj[8][kJoinSplits];
     int last;
@@ -345,25 +345,39 @@ PKV_DEV Weight warp_weight(const Join &J, int warp, int column) {
     return r;
 }
 
-// MASS: the unit's (m, l) is kept for mass_kernel even where the row is one unit.
-template <int D, int COLS, int MT, bool MASS>
+// MASS: the unit's (m, l) is kept for mass_kernel even where the row is one unit.  I4: the accumulators are of
+// codes that read 2^-21 (even elements) and 2^-17, without the offsets' sum.
+template <int D, int COLS, int MT, bool MASS, bool I4>
 PKV_DEV void join_unit(const Args &a, const Unit &u, Join &J, const float *oacc) {
     using M_ = ModelT<MT>;
     constexpr int LD = D + 4;
     const int G = a.group;
     __syncthreads();
-    for (int e = threadIdx.x; e < G * D; e += kThreads) {
-        const int h = e / D, d = e % D;
+    for (int e = threadIdx.x; e < G * (D / 4); e += kThreads) {
+        const int h = e / (D / 4), d = e % (D / 4) * 4;
         const float *o = oacc + h * LD + d;
-        const float num = ((o[0] + o[COLS * LD]) + o[2 * COLS * LD]) + o[3 * COLS * LD];
+        float4 v[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v[w] = *reinterpret_cast<const float4 *>(o + w * COLS * LD);
+        float n[4] = {((v[0].x + v[1].x) + v[2].x) + v[3].x, ((v[0].y + v[1].y) + v[2].y) + v[3].y,
+                      ((v[0].z + v[1].z) + v[2].z) + v[3].z, ((v[0].w + v[1].w) + v[2].w) + v[3].w};
         const float den = ((J.l[0][h] + J.l[1][h]) + J.l[2][h]) + J.l[3][h];
+        if constexpr (I4) {
+            const float z = ((J.z[0][h] + J.z[1][h]) + J.z[2][h]) + J.z[3][h];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n[i] = fmaf(n[i], i & 1 ? 131072.f : 2097152.f, z);
+        }
         const int64_t row = (int64_t)u.s * a.hq + u.kvh * G + h;
         if ((MASS || u.nsplit > 1) && d == 0)
             reinterpret_cast<float2 *>(a.ws_ml)[row * a.max_splits + u.j] = make_float2(J.M[h], den);
-        if (u.nsplit > 1)
-            a.ws_o[(row * a.max_splits + u.j) * D + d] = num;
-        else
-            static_cast<typename M_::T *>(a.out)[row * D + d] = M_::from_f(den == 0.f ? 0.f : num * (1.f / den));
+        if (u.nsplit > 1) {
+            *reinterpret_cast<float4 *>(a.ws_o + (row * a.max_splits + u.j) * D + d) = make_float4(n[0], n[1], n[2], n[3]);
+        } else {
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            *reinterpret_cast<uint2 *>(static_cast<char *>(a.out) + (row * D + d) * 2) =
+                den == 0.f ? make_uint2(0u, 0u)
+                           : make_uint2(M_::pack(n[0] * inv, n[1] * inv), M_::pack(n[2] * inv, n[3] * inv));
+        }
     }
     __syncthreads();
 }
@@ -385,17 +399,25 @@ PKV_DEV void join_row(const Args &a, const Unit &u, Join &J) {
     if (threadIdx.x == 0) a.done[row] = 0;
     split_weights(a, u.s, u.kvh, u.nsplit, &J.wj[0][0], kJoinSplits, J.M, J.inv);
     __syncthreads();
-    for (int e = threadIdx.x; e < G * D; e += kThreads) {
-        const int h = e / D, d = e % D;
+    for (int e = threadIdx.x; e < G * (D / 4); e += kThreads) {
+        const int h = e / (D / 4), d = e % (D / 4) * 4;
         const int64_t r = (int64_t)u.s * a.hq + u.kvh * G + h;
         const float *o = a.ws_o + r * a.max_splits * D + d;
-        float num = 0.f;
+        float4 n = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int j = 0; j < u.nsplit; ++j) {
-            const float v = __ldcg(o + (int64_t)j * D);
-            if (J.wj[h][j] != 0.f) num = fmaf(J.wj[h][j], v, num);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + (int64_t)j * D));
+            const float w = J.wj[h][j];
+            if (w != 0.f) {
+                n.x = fmaf(w, v.x, n.x);
+                n.y = fmaf(w, v.y, n.y);
+                n.z = fmaf(w, v.z, n.z);
+                n.w = fmaf(w, v.w, n.w);
+            }
         }
-        static_cast<typename M_::T *>(a.out)[r * D + d] = M_::from_f(num * J.inv[h]);
+        const float inv = J.inv[h];
+        *reinterpret_cast<uint2 *>(static_cast<char *>(a.out) + (r * D + d) * 2) =
+            make_uint2(M_::pack(n.x * inv, n.y * inv), M_::pack(n.z * inv, n.w * inv));
     }
     __syncthreads();
 }
