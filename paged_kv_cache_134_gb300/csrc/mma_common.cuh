@@ -145,53 +145,6 @@ PKV_DEV int row_len(const Args &a, int s) {
     return L <= 0 ? 0 : (int64_t)L > a.cap ? (int)a.cap : L;
 }
 
-// mass of tokens [t0, t1) of (sequence, KV head) row `row` from their stored scores, with the row's
-// final maxima and reciprocal sums per head; U tokens' loads at a time
-template <int G, int U>
-PKV_DEV void add_mass_g(const Args &a, int64_t row, int t0, int t1, const float *M, const float *inv) {
-    const float *x = a.ws_x + row * a.cap * G;
-    float *m = a.mass + row * a.mass_len;
-    for (int tb = t0 + threadIdx.x; tb < t1; tb += kThreads * U) {
-        float xs[U][G], old[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int t = tb + i * kThreads;
-            if (t >= t1) continue;
-            const float *src = x + (int64_t)t * G;
-            if constexpr (G == 1) {
-                xs[i][0] = __ldcg(src);
-            } else {
-#pragma unroll
-                for (int h = 0; h < G; h += 2) {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + h));
-                    xs[i][h] = v.x;
-                    xs[i][h + 1] = v.y;
-                }
-            }
-            old[i] = m[t];
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int t = tb + i * kThreads;
-            if (t >= t1) continue;
-            float p = 0.f;
-#pragma unroll
-            for (int h = 0; h < G; ++h) p = fmaf(fast_exp2(xs[i][h] - M[h]), inv[h], p);
-            m[t] = fmaf(old[i], a.decay, p);
-        }
-    }
-}
-PKV_DEV void add_mass(const Args &a, int64_t row, int t0, int t1, const float *M, const float *inv) {
-    if (a.group == 1)
-        add_mass_g<1, 8>(a, row, t0, t1, M, inv);
-    else if (a.group == 2)
-        add_mass_g<2, 4>(a, row, t0, t1, M, inv);
-    else if (a.group == 4)
-        add_mass_g<4, 4>(a, row, t0, t1, M, inv);
-    else
-        add_mass_g<8, 2>(a, row, t0, t1, M, inv);
-}
-
 // Block scan of the sequences' unit counts: full[s + 1], part[s + 1] hold the inclusive sums of whole
 // splits and of partial ones (a sequence of length 0 has one partial unit, which writes its zero row).
 PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
@@ -313,12 +266,14 @@ PKV_DEV void split_weights(const Args &a, int s, int kvh, int nsplit, float *w, 
     for (int h = warp; h < a.group; h += blockDim.x / 32) {
         const float2 *ml =
             reinterpret_cast<const float2 *>(a.ws_ml) + ((int64_t)s * a.hq + kvh * a.group + h) * a.max_splits;
-        float Mx = -INFINITY, den = 0.f;
-        for (int j = lane; j < nsplit; j += 32) Mx = fmaxf(Mx, __ldcg(ml + j).x);
+        const float2 none = make_float2(-INFINITY, 0.f);
+        float2 v = lane < nsplit ? __ldcg(ml + lane) : none;
+        float Mx = v.x, den = 0.f;
+        for (int j = lane + 32; j < nsplit; j += 32) Mx = fmaxf(Mx, __ldcg(ml + j).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
         for (int j = lane; j < nsplit; j += 32) {
-            const float2 v = __ldcg(ml + j);
+            if (j >= 32) v = __ldcg(ml + j);
             const float f = weight_of(v.x, Mx);
             w[h * ldw + j] = f;
             if (f != 0.f) den = fmaf(f, v.y, den);
@@ -429,21 +384,32 @@ PKV_DEV float row_sum(float x) {
     return x;
 }
 
-// Outputs e0, e0 + step, ... (runs of 32 dims of a head) of row (s, kvh) from its splits: each of the W warps adds
-// every W-th split in order, their sums are joined in warp order.
-template <int D, int MT, int W>
-PKV_DEV void join_outputs(const Args &a, int s, int kvh, int nsplit, const float *wj, const float *inv, float (*sum)[32],
-                          int e0, int step) {
+// Joins the splits of a row: block (row, y) takes every gridDim.y-th run of 32 outputs; each warp adds every
+// kMergeWarps-th split in order, their sums are joined in warp order.  Rows come here with more than kJoinSplits
+// splits: sixteen warps keep enough loads in flight.
+constexpr int kMergeWarps = 16;
+constexpr int kMassCtas = 8;
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
     using M = ModelT<MT>;
+    __shared__ float sm_M[8], sm_inv[8], sum[kMergeWarps][32];
+    extern __shared__ float wj[]; // [G][max_splits]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (; e0 < a.group * D; e0 += step) {
+    pdl_wait();
+    const int row = blockIdx.x, s = row / a.hkv, kvh = row - s * a.hkv;
+    const int nsplit = (row_len(a, s) + a.split_tokens - 1) / a.split_tokens;
+    if (nsplit <= 1) return;
+    split_weights(a, s, kvh, nsplit, wj, a.max_splits, sm_M, sm_inv);
+    __syncthreads();
+    for (int e0 = blockIdx.y * 32; e0 < a.group * D; e0 += gridDim.y * 32) {
         const int h = e0 / D, d = e0 % D + lane;
         const int64_t r = (int64_t)s * a.hq + kvh * a.group + h;
         const float *o = a.ws_o + r * a.max_splits * D + d;
         const float *w = wj + h * a.max_splits;
         float num = 0.f;
 #pragma unroll 8
-        for (int j = warp; j < nsplit; j += W) {
+        for (int j = warp; j < nsplit; j += kMergeWarps) {
             const float v = o[(int64_t)j * D];
             if (w[j] != 0.f) num = fmaf(w[j], v, num);
         }
@@ -452,51 +418,136 @@ PKV_DEV void join_outputs(const Args &a, int s, int kvh, int nsplit, const float
         if (warp == 0) {
             num = sum[0][lane];
 #pragma unroll
-            for (int w = 1; w < W; ++w) num += sum[w][lane];
-            static_cast<typename M::T *>(a.out)[r * D + d] = M::from_f(num * inv[h]);
+            for (int w = 1; w < kMergeWarps; ++w) num += sum[w][lane];
+            static_cast<typename M::T *>(a.out)[r * D + d] = M::from_f(num * sm_inv[h]);
         }
         __syncthreads();
     }
 }
 
-// Joins the splits of a row: block (row, y) takes every gridDim.y-th run of 32 outputs.  Rows come here with more
-// than kJoinSplits splits: sixteen warps keep enough loads in flight.
-constexpr int kMergeWarps = 16;
-
-template <int D, int MT>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
-    __shared__ float sm_M[8], sm_inv[8], sum[kMergeWarps][32];
-    extern __shared__ float wj[]; // [G][max_splits]
-    pdl_wait();
-    const int row = blockIdx.x, s = row / a.hkv, kvh = row - s * a.hkv;
-    const int nsplit = (row_len(a, s) + a.split_tokens - 1) / a.split_tokens;
-    if (nsplit <= 1) return;
-    split_weights(a, s, kvh, nsplit, wj, a.max_splits, sm_M, sm_inv);
-    __syncthreads();
-    join_outputs<D, MT, kMergeWarps>(a, s, kvh, nsplit, wj, sm_inv, sum, blockIdx.y * 32, gridDim.y * 32);
-}
-
 // After a decode that stored its scores: for every unit the mass of its tokens, and its share of the row's outputs
 // where the row has several splits.  Persistent, the decode's list of units.
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads) mass_kernel(const Args a) {
-    __shared__ float sm_M[8], sm_inv[8], sum[kWarps][32];
-    __shared__ int sm_tmp[2 * kWarps];
-    extern __shared__ float wj[]; // [G][max_splits], then the list of units
-    int *full = reinterpret_cast<int *>(wj + a.group * a.max_splits), *part = full + a.num_seqs + 1;
-    pdl_wait();
-    list_units(a, full, part, sm_tmp);
+struct MassShared {
+    float M[8], inv[8];
+    float4 part[kThreads];
+    int tmp[2 * kWarps];
+};
+
+// G heads, U tokens a thread at a time; a unit's first scores are on their way while the row's splits are weighed.
+template <int D, int MT, int G, int U>
+PKV_DEV void mass_units(const Args &a, MassShared &sm, float *wj, const int *full, const int *part) {
+    using M_ = ModelT<MT>;
     const int nfull = full[a.num_seqs] * a.hkv, nunits = nfull + part[a.num_seqs] * a.hkv;
     for (int ui = blockIdx.x; ui < nunits; ui += gridDim.x) {
         const Unit u = unit_of(a, full, part, nfull, ui);
         if (u.n <= 0) continue; // an empty sequence
-        split_weights(a, u.s, u.kvh, u.nsplit, wj, a.max_splits, sm_M, sm_inv);
+        const int64_t row = (int64_t)u.s * a.hkv + u.kvh;
+        const float *x = a.ws_x + (row * a.cap + u.t0) * G;
+        float *m = a.mass + row * a.mass_len + u.t0;
+        float xs[U][G], old[U];
+        auto load = [&](int tb) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int t = tb + i * kThreads;
+                if (t >= u.n) continue;
+                const float *src = x + (int64_t)t * G;
+                if constexpr (G == 1) {
+                    xs[i][0] = __ldcg(src);
+                } else if constexpr (G == 2) {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                    xs[i][0] = v.x;
+                    xs[i][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int h = 0; h < G; h += 4) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + h));
+                        xs[i][h] = v.x;
+                        xs[i][h + 1] = v.y;
+                        xs[i][h + 2] = v.z;
+                        xs[i][h + 3] = v.w;
+                    }
+                }
+                old[i] = m[t];
+            }
+        };
+        load(threadIdx.x);
+        split_weights(a, u.s, u.kvh, u.nsplit, wj, a.max_splits, sm.M, sm.inv);
         __syncthreads();
-        add_mass(a, (int64_t)u.s * a.hkv + u.kvh, u.t0, u.t0 + u.n, sm_M, sm_inv);
-        if (u.nsplit > 1)
-            join_outputs<D, MT, kWarps>(a, u.s, u.kvh, u.nsplit, wj, sm_inv, sum, u.j * 32, u.nsplit * 32);
+        float M[G], inv[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) M[h] = sm.M[h], inv[h] = sm.inv[h];
+        for (int tb = threadIdx.x; tb < u.n; tb += kThreads * U) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int t = tb + i * kThreads;
+                if (t >= u.n) continue;
+                float p = 0.f;
+#pragma unroll
+                for (int h = 0; h < G; ++h) p = fmaf(fast_exp2(xs[i][h] - M[h]), inv[h], p);
+                m[t] = fmaf(old[i], a.decay, p);
+            }
+            load(tb + kThreads * U);
+        }
+        if (u.nsplit > 1) {
+            // the unit's share: c runs of four outputs, at most one a thread.  K threads a run take every K-th
+            // split, their sums are added in order.
+            constexpr int V = G * D / 4;
+            const int i0 = V * u.j / u.nsplit, c = V * (u.j + 1) / u.nsplit - i0;
+            if (c > 0) {
+                const int K = min(kThreads / c, u.nsplit), k = threadIdx.x / c, i = i0 + threadIdx.x - k * c;
+                const int h = i / (D / 4), d = i % (D / 4) * 4;
+                const int64_t r = (int64_t)u.s * a.hq + u.kvh * G + h;
+                if (k < K) {
+                    const float *o = a.ws_o + r * a.max_splits * D + d, *w = wj + h * a.max_splits;
+                    float4 n = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int j = k; j < u.nsplit; j += K) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + (int64_t)j * D));
+                        if (w[j] != 0.f) {
+                            n.x = fmaf(w[j], v.x, n.x);
+                            n.y = fmaf(w[j], v.y, n.y);
+                            n.z = fmaf(w[j], v.z, n.z);
+                            n.w = fmaf(w[j], v.w, n.w);
+                        }
+                    }
+                    sm.part[threadIdx.x] = n;
+                }
+                __syncthreads();
+                if (k == 0) {
+                    float4 n = sm.part[threadIdx.x];
+                    for (int q = 1; q < K; ++q) {
+                        const float4 v = sm.part[q * c + threadIdx.x];
+                        n.x += v.x;
+                        n.y += v.y;
+                        n.z += v.z;
+                        n.w += v.w;
+                    }
+                    const float f = sm.inv[h];
+                    *reinterpret_cast<uint2 *>(static_cast<char *>(a.out) + (r * D + d) * 2) =
+                        make_uint2(M_::pack(n.x * f, n.y * f), M_::pack(n.z * f, n.w * f));
+                }
+            }
+        }
         __syncthreads();
     }
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, kMassCtas) mass_kernel(const Args a) {
+    __shared__ MassShared sm;
+    extern __shared__ float wj[]; // [G][max_splits], then the list of units
+    int *full = reinterpret_cast<int *>(wj + a.group * a.max_splits), *part = full + a.num_seqs + 1;
+    // (the lengths were complete before the decode began, so the list need not wait for its end)
+    list_units(a, full, part, sm.tmp);
+    pdl_wait();
+    if (a.group == 1)
+        mass_units<D, MT, 1, 8>(a, sm, wj, full, part);
+    else if (a.group == 2)
+        mass_units<D, MT, 2, 4>(a, sm, wj, full, part);
+    else if (a.group == 4)
+        mass_units<D, MT, 4, 4>(a, sm, wj, full, part);
+    else
+        mass_units<D, MT, 8, 2>(a, sm, wj, full, part);
 }
 
 inline unsigned grid_of(const Args &a, int slots) {
@@ -509,7 +560,7 @@ template <int D, int MT, bool MASS>
 cudaError_t launch_merge_t(const Args &a, int sms, cudaStream_t st) {
     const size_t smem = (size_t)a.group * a.max_splits * sizeof(float);
     if constexpr (MASS) {
-        return pdl_launch(mass_kernel<D, MT>, dim3(grid_of(a, 8 * sms)), dim3(kThreads),
+        return pdl_launch(mass_kernel<D, MT>, dim3(grid_of(a, kMassCtas * sms)), dim3(kThreads),
                           smem + 2 * (a.num_seqs + 1) * sizeof(int), st, a);
     } else {
         return pdl_launch(merge_kernel<D, MT>, dim3((unsigned)(a.num_seqs * a.hkv), a.group * D / 32),
