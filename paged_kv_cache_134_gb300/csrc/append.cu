@@ -194,9 +194,10 @@ __global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
             for (int u = 0; u < kAppend4Unroll; ++u) {
                 const int r = rb + u * rstep;
                 if (r >= per_token) continue;
-                const uint4 *p = (r >= side ? vsrc - side * 2 : ksrc) + r * 2;
+                // (row r / per_row of K and V; elements 8 c .. and D / 2 + 8 c .., so that lanes lie side by side)
+                const uint4 *p = (r >= side ? vsrc - side * 2 : ksrc) + r / per_row * (2 * per_row) + r % per_row;
                 src[u][0] = __ldcs(p);
-                src[u][1] = __ldcs(p + 1);
+                src[u][1] = __ldcs(p + per_row);
             }
 #pragma unroll
             for (int u = 0; u < kAppend4Unroll; ++u) {
@@ -205,7 +206,8 @@ __global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
                 const int kv = r >= side ? 1 : 0, hc = r - kv * side, h = hc / per_row, c = hc - h * per_row;
                 const Int4Row row = int4_quantise<MT>(src[u], per_row, lanes);
                 char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, D);
-                *reinterpret_cast<uint2 *>(tile + int4_codes(kv, off, c * 8, D)) = row.codes;
+                *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, c * 4, D)) = row.codes.x;
+                *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, D / 4 + c * 4, D)) = row.codes.y;
                 if (c == 0) *reinterpret_cast<uint32_t *>(tile + int4_params(kv, off, D)) = row.params;
             }
         }
@@ -256,20 +258,25 @@ __global__ void __launch_bounds__(kAppendThreads) gather_kernel(GatherArgs a) {
                 const int kv = r >= side ? 1 : 0, hc = r - kv * side, h = hc / per_row, c = hc - h * per_row;
                 if constexpr (KVT == PKV_INT4) {
                     const char *tile = a.pool + int4_head(blk, h, a.hkv, bs, D);
-                    const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(tile + int4_codes(kv, off, c * 8, D)));
-                    x[u][0] = w.x;
-                    x[u][1] = w.y;
+                    x[u][0] = __ldcs(reinterpret_cast<const uint32_t *>(tile + int4_codes(kv, off, c * 4, D)));
+                    x[u][1] = __ldcs(reinterpret_cast<const uint32_t *>(tile + int4_codes(kv, off, D / 4 + c * 4, D)));
                     par[u] = *reinterpret_cast<const uint32_t *>(tile + int4_params(kv, off, D));
                 } else {
                     const char *p = a.pool + ((((blk * 2 + kv) * a.hkv + h) << a.bs_log2) + off) * (D * kWords / 4) +
-                                    c * kWords * 4;
+                                    c * kWords * 2;
 #pragma unroll
-                    for (int i = 0; i < kWords; i += 4) {
-                        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p) + i / 4);
-                        x[u][i] = w.x;
-                        x[u][i + 1] = w.y;
-                        x[u][i + 2] = w.z;
-                        x[u][i + 3] = w.w;
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (KVT == PKV_FP8_E4M3) {
+                            const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p + i * (D / 2)));
+                            x[u][2 * i] = w.x;
+                            x[u][2 * i + 1] = w.y;
+                        } else {
+                            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p + i * D));
+                            x[u][4 * i] = w.x;
+                            x[u][4 * i + 1] = w.y;
+                            x[u][4 * i + 2] = w.z;
+                            x[u][4 * i + 3] = w.w;
+                        }
                     }
                 }
             }
@@ -295,9 +302,9 @@ __global__ void __launch_bounds__(kAppendThreads) gather_kernel(GatherArgs a) {
                         }
                     }
                 }
-                uint4 *dst = (kv ? a.v : a.k) + (j * side + hc) * 2;
+                uint4 *dst = (kv ? a.v : a.k) + j * side * 2 + hc / per_row * (2 * per_row) + hc % per_row;
                 dst[0] = o[0];
-                dst[1] = o[1];
+                dst[per_row] = o[1];
             }
         }
     }

@@ -38,7 +38,7 @@ PKV_DEV int int4_params(int kv, int off, int d) {
 }
 
 struct Int4Row {
-    uint2 codes;     // this lane's sixteen
+    uint2 codes;     // of this lane's two runs of eight
     uint32_t params; // s in the low half, z in the high half (the same on every lane of the row)
 };
 
@@ -68,10 +68,14 @@ PKV_DEV float half_of(uint32_t w, int i) {
         return __uint_as_float(i ? w & 0xFFFF0000u : w << 16);
 }
 
-// Sixteen elements of a row that the `per_row` lanes of `lanes` hold together.  Codes come from a multiplication by
-// 1 / s; the quotient has to be the correctly rounded one, so that a code does not hang on how it was computed, so
-// lanes with a product within 2e-5 of a half (its error is below 1e-5 at quotients up to 22) divide instead, as do
-// rows whose largest quotient passes 15.4 (a step that the model's type holds to few bits), which are cut at 15.
+// Sixteen elements of a row that the `per_row` lanes of `lanes` hold together (which sixteen is the caller's choice).
+// Codes come from quotients d / s rounded as a division rounds them, so that a code does not hang on how it was
+// computed.  They are q = d i, i an approximate 1 / s, corrected once by the remainder, q + (d - q s) i (Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor, 1990): d - q s is exact, as s
+// has at most 11 bits and q is off by a few units, and the sum is off by less than 2^-44 before it is rounded,
+// while a quotient of 24 by 11 bits that is no float lies 2^-37 or more from a place where rounding turns.
+// Rows with a step below 2^-90, whose remainders would be subnormal, divide; so do rows whose largest quotient passes 15.4
+// (a step that the model's type holds to few bits), which are cut at 15.  The step is found the same way.
 template <int MT>
 PKV_DEV Int4Row int4_quantise(const uint4 (&src)[2], int per_row, unsigned lanes) {
     using M = ModelT<MT>;
@@ -94,47 +98,52 @@ PKV_DEV Int4Row int4_quantise(const uint4 (&src)[2], int per_row, unsigned lanes
         r.params = MT == PKV_F16 ? 0x7E007E00u : 0x7FC07FC0u;
         return r;
     }
-    const uint32_t s16 = M::pack(__fdiv_rn(range, 15.f), 0.f) & 0xFFFFu;
+    constexpr float kTiny = 8.0779357e-28f; // 2^-90
+    float step = range * (1.f / 15.f);
+    step = range < kTiny ? __fdiv_rn(range, 15.f) : fmaf(fmaf(step, -15.f, range), 1.f / 15.f, step);
+    const uint32_t s16 = M::pack(step, 0.f) & 0xFFFFu;
     float s = half_of<MT>(s16, 0);
     if (s < 1.17549435e-38f) s = 0.f; // 2^-126
     r.params = (s == 0.f ? 0u : s16) | (both << 16);
     if (s == 0.f) return r;
-    const float inv = __frcp_rn(s);
-    const float2 inv2 = make_float2(inv, inv), minus_z = make_float2(-z, -z), zero = make_float2(0.f, 0.f),
-                 big = make_float2(12582912.f, 12582912.f), minus_big = make_float2(-12582912.f, -12582912.f),
-                 minus1 = make_float2(-1.f, -1.f);
-    bool slow = __fmul_rn(range, inv) > 15.4f;
-    float t[16]; // codes
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        float f[8];
-        cvt8<MT>(src[u], f);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const float2 y = fma2(add2(make_float2(f[i], f[i + 1]), minus_z), inv2, zero);
-            const float2 n = add2(add2(y, big), minus_big); // rint
-            const float2 e = fma2(n, minus1, y);
-            slow |= fabsf(e.x) > 0.49998f || fabsf(e.y) > 0.49998f;
-            t[8 * u + i] = n.x;
-            t[8 * u + i + 1] = n.y;
-        }
-    }
-    if (slow) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s)); // (2^-126 <= s < 2^125: neither end is flushed)
+    const float2 inv2 = make_float2(inv, inv), minus_z = make_float2(-z, -z), minus_s = make_float2(-s, -s),
+                 zero = make_float2(0.f, 0.f), big = make_float2(12582912.f, 12582912.f);
+    uint32_t w[4]; // four codes in the low 16 bits
+    if (s < kTiny || range * inv > 15.4f) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             float f[8];
             cvt8<MT>(src[u], f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) { // (mostly one element: a test each, a division where it is needed)
-                const float d = __fsub_rn(f[i], z), n = t[8 * u + i];
-                if (fabsf(__fmul_rn(d, inv) - n) > 0.49998f || n > 15.f) t[8 * u + i] = fminf(rintf(__fdiv_rn(d, s)), 15.f);
+            for (int i = 0; i < 2; ++i) {
+                w[2 * u + i] = 0;
+#pragma unroll
+                for (int e = 3; e >= 0; --e)
+                    w[2 * u + i] = w[2 * u + i] * 16 + (uint32_t)fminf(rintf(__fdiv_rn(__fsub_rn(f[4 * i + e], z), s)), 15.f);
             }
         }
-    }
-    uint32_t w[4]; // four codes as a number below 2^16, in the low bits of 2^23 + it
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __float_as_uint(fmaf(fmaf(fmaf(t[4 * i + 3], 16.f, t[4 * i + 2]), 16.f, t[4 * i + 1]), 16.f, t[4 * i]) + 8388608.f);
+        for (int u = 0; u < 2; ++u) {
+            float f[8];
+            cvt8<MT>(src[u], f);
+            uint32_t t[8]; // codes in the low bits of 2^23 + 2^22 + them: the bits above drop out below
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float2 d = add2(make_float2(f[i], f[i + 1]), minus_z);
+                float2 q = fma2(d, inv2, zero);
+                q = fma2(fma2(q, minus_s, d), inv2, q);
+                q = add2(q, big);
+                t[i] = __float_as_uint(q.x);
+                t[i + 1] = __float_as_uint(q.y);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[2 * u + i] = ((t[4 * i + 3] * 16 + t[4 * i + 2]) * 16 + t[4 * i + 1]) * 16 + t[4 * i];
+        }
+    }
     auto rotate = [](uint32_t c) { return ((c << 3) & 0xFFF8FFF8u) | ((c >> 13) & 0x00070007u); };
     r.codes = make_uint2(rotate(__byte_perm(w[0], w[1], 0x5410)), rotate(__byte_perm(w[2], w[3], 0x5410)));
     return r;
