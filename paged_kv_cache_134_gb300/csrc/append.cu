@@ -341,8 +341,8 @@ cudaError_t launch_append_t(pkv_cache *c, const AppendArgs &a, cudaStream_t st) 
     const int per_token = 2 * a.hkv * a.chunks_per_row;
     const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
     const int64_t passes = (a.n + tpg - 1) / tpg;
-    // (4-bit: more and shorter CTAs, so that the last ones of a prompt leave fewer SMs idle)
-    const int64_t cap = (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? 32 : 8);
+    // (4-bit: two for each that fits, so that the last ones of a prompt leave fewer SMs idle)
+    const int64_t cap = (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? 12 : 8);
     const dim3 grid((unsigned)(passes < 1 ? 1 : (passes > cap ? cap : passes)));
     PkvTimer timer(c, PKV_KIND_APPEND, st);
     cudaError_t e;
@@ -426,7 +426,7 @@ cudaError_t launch_gather(pkv_cache *c, const int64_t *slots, int64_t n, void *k
     a.bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
     const int per_token = 2 * a.hkv * (c->head_dim / 16);
     const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
-    const int64_t passes = (n + tpg - 1) / tpg, cap = (int64_t)c->num_sms * 32;
+    const int64_t passes = (n + tpg - 1) / tpg, cap = (int64_t)c->num_sms * 12;
     const dim3 grid((unsigned)(passes > cap ? cap : passes)), block(kAppendThreads);
     const bool d64 = c->head_dim == 64, h = c->model_dtype == PKV_F16;
     PkvTimer timer(c, PKV_KIND_COPY, st);
