@@ -73,8 +73,8 @@ typedef enum {
  * [num_blocks][num_kv_heads] runs of block_size * (head_dim + 8) bytes, each one octet of 8 slots
  * after the other: K codes [8][head_dim / 2], V codes [8][head_dim / 2], K (step, offset) [8][2],
  * V (step, offset) [8][2] in the model dtype.  Elements 4 i .. 4 i + 3 of a row are the nibbles of its
- * 16-bit word i, lowest first, the word rotated left by three bits.  V's rows stand in the order 0 2 4 6 1 3 5 7; at head_dim 128 rows 4, 5, 6 and 7
- * hold their second 32 bytes first.
+ * 16-bit word i, lowest first, the word rotated left by three bits.  V's rows stand in the order
+ * 0 2 4 6 1 3 5 7; at head_dim 128 rows 4, 5, 6 and 7 hold their second 32 bytes first.
  * On failure *out is untouched. */
 int kv_cache_create(int64_t num_blocks, int block_size, int num_kv_heads, int head_dim, pkv_dtype kv_dtype,
                     pkv_dtype model_dtype, pkv_cache_t *out);
@@ -183,8 +183,8 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
  * row s belonging to row s of the tables; a token's entry has to be 0 before its first step.  decay in
  * [0, 1] (1 sums, less lets old mass fade).  Every cache type; out as paged_decode_attention (to its
  * tolerance, not bit for bit).  A length above mass_len or the tables' tokens sets PKV_DEVERR_LENGTH and
- * is cut to that.  Two launches (one where every sequence fits a split); the products take the
- * softmax weights as hi + lo 16-bit pairs, all else is fp32; no atomics, so equal calls give equal bits.
+ * is cut to that.  Two launches, the second for the mass; the products take the softmax weights as
+ * hi + lo 16-bit pairs, all else is fp32; sums run in a fixed order, so equal calls give equal bits.
  * Workspace: fp32 partials and scores (num_q_heads x tokens x 4 bytes per sequence, at most 2 GB a
  * launch unless one sequence needs more; larger batches run as consecutive launches), one per stream
  * and one per stream capture, allocated by the first call that needs it or more of it, also during a
@@ -210,7 +210,7 @@ int paged_decode_attention_mass(const void *q, pkv_cache_t cache, const int32_t 
  * shared, the caller's to release.  Slots behind a new length are left as they were.  new_mass must not
  * overlap attn_mass, nor new_lens context_lens (PKV_EINVAL).  A length above mass_len or the tables'
  * tokens sets PKV_DEVERR_LENGTH and its sequence is skipped (kept -1, new length 0, new mass 0); a bad
- * block id skips the row and sets PKV_DEVERR_BLOCK_ID.  No workspace. */
+ * block id skips the row and sets PKV_DEVERR_BLOCK_ID.  At most 2^30 tokens.  No workspace. */
 int paged_kv_evict(pkv_cache_t cache, const int32_t *block_tables, int max_blocks_per_seq,
                    const int32_t *context_lens, int num_seqs, const float *attn_mass, int64_t mass_len, int budget,
                    int recent, const int32_t *dst_block_tables, int max_dst_blocks_per_seq, int32_t *kept,

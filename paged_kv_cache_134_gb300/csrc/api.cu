@@ -68,6 +68,16 @@ int ensure_workspace(pkv_cache *c, int64_t floats) {
 } // namespace
 
 namespace {
+// (an exception must not leave a C entry point)
+bool room_for_one_more(std::vector<pkv_cache::StreamWs> &v) {
+    try {
+        v.reserve(v.size() + 1);
+    } catch (...) {
+        return false;
+    }
+    return true;
+}
+
 int64_t workspace_counters(const pkv_cache *c) { return (int64_t)1024 * c->num_kv_heads; } // rows of a launch
 
 // A workspace of `bytes` for partials and its zeroed counters, not tied to any stream's work: also while a
@@ -126,6 +136,7 @@ int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorks
         b.capture = capture;
         return use(b);
     }
+    if (!room_for_one_more(c->stream_ws)) return pkv_fail(PKV_ENOMEM, "out of host memory");
     // at least twice the last one: the buffers left behind add up to less than the one in use
     pkv_cache::StreamWs b{stream, capture, false, nullptr, std::max(bytes, 2 * most)};
     e = allocate_workspace(c, b.bytes, &b.p);
@@ -348,6 +359,7 @@ int kv_cache_reserve(pkv_cache_t c, int max_seqs, int max_q_heads, int max_block
         std::lock_guard<std::mutex> lk(c->ws_mu);
         for (auto &have : c->stream_ws)
             if (have.spare && have.bytes >= b.bytes) return PKV_OK;
+        if (!room_for_one_more(c->stream_ws)) return pkv_fail(PKV_ENOMEM, "out of host memory");
         cudaError_t e = allocate_workspace(c, b.bytes, &b.p);
         if (e != cudaSuccess)
             return pkv_fail(e == cudaErrorMemoryAllocation ? PKV_ENOMEM : PKV_ECUDA,
@@ -465,6 +477,8 @@ int paged_kv_evict(pkv_cache_t c, const int32_t *block_tables, int max_blocks_pe
     if (num_seqs == 0) return PKV_OK;
     const int64_t cap = std::min<int64_t>(mass_len, (int64_t)max_blocks_per_seq * c->block_size);
     const int64_t most = std::min<int64_t>(cap, budget);
+    if (cap > 1 << 30 || budget > 1 << 30)
+        return pkv_fail(PKV_EUNSUPPORTED, "sequences and budgets of more than 2^30 tokens");
     if ((int64_t)max_dst_blocks_per_seq * c->block_size < most)
         return pkv_fail(PKV_EINVAL, "destination tables of %d blocks cannot hold %lld tokens", max_dst_blocks_per_seq,
                         (long long)most);

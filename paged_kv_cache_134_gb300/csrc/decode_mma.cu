@@ -85,6 +85,8 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace 
     a.err = c->err;
     a.num_blocks = c->num_blocks;
     pkv_row_strides(c, &a.blk_stride, &a.head_stride, &a.v_off);
+    if (a.blk_stride > 0xFFFFFFFFll)
+        return pkv_fail(PKV_EUNSUPPORTED, "blocks of %lld bytes are larger than this decode takes", (long long)a.blk_stride);
     a.mass_len = d.mass_len;
     a.cap = p.cap;
     a.max_blocks = d.max_blocks;
@@ -103,7 +105,9 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace 
     a.qk_scale_log2 = d.scale * 1.4426950408889634f;
     a.decay = d.decay;
     // a batch larger than one launch takes runs in consecutive launches that share the workspace: each
-    // waits for the one before it
+    // waits for the one before it.  Another host thread's call on this stream may use the same workspace: no launch of
+    // its own comes between this call's.
+    std::lock_guard<std::mutex> lk(c->ws_mu);
     for (int s0 = 0; s0 < d.num_seqs; s0 += p.seqs) {
         const int n = std::min(p.seqs, d.num_seqs - s0);
         const int64_t rows = (int64_t)n * d.num_q_heads * (p.max_splits > 1 || mass ? p.max_splits : 0);

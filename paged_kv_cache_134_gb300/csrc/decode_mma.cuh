@@ -394,12 +394,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
 template <int D, int KV, int MT, bool G8>
 cudaError_t launch_mass_t(const Args &a, int sms, cudaStream_t st) {
     using G_ = Geo<D, KV, G8>;
-    static std::atomic<int> have[64];
+    static std::atomic<bool> have[64];
     auto kern = decode_mass_kernel<D, KV, MT, G8>;
     constexpr int cols = G8 ? 8 : 4;
     const size_t smem = (size_t)kWarps * G_::kStages * G_::kBytes + kWarps * cols * (D + 4) * sizeof(float) +
                         2 * cols * D * 2 + (2 * (a.num_seqs + 1) + 2 * (a.split_tokens >> a.bs_log2)) * sizeof(int);
-    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), smem, have);
+    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have);
     if (e != cudaSuccess) return e;
     return pdl_launch(kern, dim3(grid_of(a, sms * G_::kCtas)), dim3(kThreads), smem, st, a);
 }

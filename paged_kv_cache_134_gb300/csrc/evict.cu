@@ -354,8 +354,8 @@ template <int LPT, bool I4, bool CL>
 cudaError_t launch_t(const EvictArgs &a, unsigned rows, cudaStream_t st) {
     auto kern = evict_kernel<LPT, I4, CL>;
     const size_t smem = a.keys * sizeof(uint32_t);
-    static std::atomic<int> have[64];
-    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), smem, have);
+    static std::atomic<bool> have[64];
+    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * a.cluster);

@@ -92,14 +92,19 @@ cudaError_t pdl_launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// cudaFuncSetAttribute once per kernel, device and size
-inline cudaError_t pkv_allow_smem(const void *kern, size_t smem, std::atomic<int> *have) {
-    int dev = 0;
+// All the dynamic shared memory a block may have, allowed once per kernel and device (always the same value, so that two
+// host threads cannot leave the smaller of two).
+inline cudaError_t pkv_allow_smem(const void *kern, std::atomic<bool> *have) {
+    int dev = 0, most = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 64 && have[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && dev < 64) have[dev].store((int)smem, std::memory_order_relaxed);
+    if (dev < 64 && have[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, kern);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)f.sharedSizeBytes);
+    if (e == cudaSuccess && dev < 64) have[dev].store(true, std::memory_order_relaxed);
     return e;
 }
 

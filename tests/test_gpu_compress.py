@@ -5,6 +5,7 @@ Every pool is filled with 0xFF first: a read of a slot that no token owns shows 
 and moved rows are compared exactly; attention within half a step of the output type plus what
 compress_ref.relative_weight_error derives for the weights."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -216,6 +217,30 @@ def test_int4_append_stores_the_definition_bit_for_bit(model, hkv, d, bs):
     z, _ = P.paged_kv_gather(cache, far)
     assert not z.any() and torch.equal(saved, cache.view()[0]) and not torch.equal(saved, before)
     assert cache.check_error() == 2
+    cache.close()
+
+
+@pytest.mark.parametrize("model", ["f16", "bf16"])
+def test_int4_codes_are_those_of_divisions(model):
+    """Codes next to and at ties, over every magnitude of the step: the quotients are not divisions in the kernel."""
+    n, hkv, d = 512, 4, 128
+    g = torch.Generator().manual_seed(9)
+    lo, hi = (-20, 12) if model == "f16" else (-120, 120)
+    scale = torch.exp2(torch.randint(lo, hi, (n, hkv, 1), generator=g).double())
+    steps = torch.randint(1, 64, (n, hkv, 1), generator=g)           # quarter steps of a whole number
+    x = torch.randint(0, 61, (n, hkv, d), generator=g) * steps / 256.0 * scale
+    x[..., 0], x[..., 1] = 0.0, 15.0 * steps[..., 0] / 64.0 * scale[..., 0]
+    x[n // 2:] += torch.randn(n // 2, hkv, 1, generator=g) * scale[n // 2:]   # rounded: next to the ties
+    x = x.to(TORCH[model]).cuda()
+    cache = P.KVCache(n // 16, 16, hkv, d, kv_dtype="int4", model_dtype=model)
+    P.paged_kv_append(cache, x, x.flip(0), torch.arange(n, device="cuda"))
+    codes, step, _ = int4_parts(cache, model)
+    for kv, rows in enumerate((x, x.flip(0))):
+        c, s, _ = R.quantise4(R.to64(rows), model)
+        got = codes[:, :, kv].transpose(0, 2, 1, 3).reshape(n, hkv, d)
+        assert np.array_equal(step[:, :, kv].transpose(0, 2, 1).reshape(n, hkv), model_bits(s, model))
+        assert np.array_equal(got, c)
+    assert cache.check_error() == 0
     cache.close()
 
 
@@ -659,6 +684,33 @@ def test_two_streams_and_two_graphs_of_one_cache_at_once(kv):
     assert x.close() == 0
 
 
+def test_two_host_threads_on_one_stream():
+    """A call is two launches over the stream's workspace: another thread's do not come between them."""
+    x = Setup([3000, 2000, 1500, 700], hq=8, hkv=2, kv="int4", model="f16", seed=18)
+    parts = [dict(q=x.q[i:i + 2].contiguous(), t=x.tables[i:i + 2].contiguous(), n=x.context[i:i + 2].contiguous(),
+                  m=torch.zeros(2, 2, 3000, device="cuda")) for i in (0, 2)]
+
+    def call(p, out):
+        P.paged_decode_attention_mass(p["q"], x.cache, p["t"], p["n"], x.scale, p["m"], decay=0.0, out=out)
+
+    want = []
+    for p in parts:
+        out = torch.empty_like(p["q"])
+        call(p, out)
+        want.append((out, p["m"].clone()))
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(p["q"]) for _ in range(200)] for p in parts]
+    threads = [threading.Thread(target=lambda p=p, o=o: [call(p, out) for out in o]) for p, o in zip(parts, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for p, o, (out, m) in zip(parts, outs, want):
+        assert all(torch.equal(got, out) for got in o) and torch.equal(p["m"], m)
+    assert x.close() == 0
+
+
 def test_reserved_workspace_leaves_no_allocation_to_the_call():
     x = Setup([3000, 50], hq=8, hkv=2, model="bf16", seed=16)
     P.paged_decode_attention_noalloc(x.q, x.cache, x.tables, x.context, x.scale, torch.empty_like(x.q))  # loads code
@@ -715,6 +767,11 @@ def test_refusals():
         with pytest.raises((ValueError, TypeError, P.PagedKVError)):
             call()
             pytest.fail(f"call {i} went through")
+    kept, lens, new = P.paged_kv_evict(c, x.tables, x.context, mass, 16, 2, dst)
+    long = P.binding.lib().paged_kv_evict(c.handle, x.tables.data_ptr(), 1 << 30, x.context.data_ptr(), 2, mass.data_ptr(),
+                                          1 << 31, 16, 2, dst.data_ptr(), dst.shape[1], kept.data_ptr(), lens.data_ptr(),
+                                          new.data_ptr(), new.shape[2], None)
+    assert long == -4
     # what a refused call leaves behind works
     check_attention(x, P.paged_decode_attention(x.q, c, x.tables, x.context, x.scale))
     assert x.close() == 0
