@@ -363,8 +363,8 @@ def paged_kv_evict(cache: KVCache, block_tables: torch.Tensor, context_lens: tor
     rows, heads, mass_len = attn_mass.shape
     if block_tables.shape[0] != S or dst_block_tables.shape[0] != S or rows != S or heads != hkv:
         raise ValueError("shape mismatch between tables, context_lens and attn_mass")
-    if budget < 1:
-        raise ValueError(f"budget {budget} is less than 1")
+    if not 0 <= recent <= budget or not 1 <= budget <= 1 << 30:
+        raise ValueError(f"recent {recent} and budget {budget}: 0 <= recent <= budget, 1 <= budget <= 2^30")
     _same_device(cache, block_tables, dst_block_tables, context_lens, attn_mass)
     for name, t, dtype, ndim in (("kept", kept, torch.int32, 3), ("new_lens", new_lens, torch.int32, 1),
                                  ("new_mass", new_mass, torch.float32, 3)):

@@ -757,6 +757,8 @@ def test_refusals():
         lambda: P.paged_kv_evict(c, x.tables, x.context, mass, 0, 0, dst),
         lambda: P.paged_kv_evict(c, x.tables, x.context, mass, 16, 17, dst),
         lambda: P.paged_kv_evict(c, x.tables, x.context, mass, 16, -1, dst),
+        lambda: P.paged_kv_evict(c, x.tables, x.context, mass, 16, (1 << 32) + 2, dst),
+        lambda: P.paged_kv_evict(c, x.tables, x.context, mass, (1 << 32) + 16, 2, dst),
         lambda: P.paged_kv_evict(c, x.tables, x.context, mass, 30, 2, dst),               # destination too narrow
         lambda: P.paged_kv_evict(c, x.tables, x.context, mass, 16, 2, dst, new_mass=mass),
         lambda: P.paged_kv_evict(c, x.tables, x.context, mass, 16, 2, dst, new_lens=x.context),
