@@ -127,11 +127,15 @@ def _req(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
 
 
-def _same_device(cache: "KVCache", *tensors):
-    dev = cache.device
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the cache on cuda:{dev}")
+def _take(cache: "KVCache", t: torch.Tensor, name: str, dtype, ndim: int) -> int:
+    """The address of a checked tensor on the cache's device."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.get_device() == cache.device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _req(t, name, dtype, ndim)
+    if t.get_device() != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.device}")
+    return t.data_ptr()
 
 
 class _DevMem:
@@ -298,21 +302,19 @@ def paged_kv_gather(cache: KVCache, slot_mapping: torch.Tensor, k: Optional[torc
                     v: Optional[torch.Tensor] = None):
     """K and V at ``slot_mapping`` as (k, v), each [T, num_kv_heads, head_dim] in the model dtype: the
     stored values of any cache type (a negative slot gives zeros)."""
-    _req(slot_mapping, "slot_mapping", torch.int64, 1)
-    _same_device(cache, slot_mapping)
-    n = slot_mapping.numel()
+    slots = _take(cache, slot_mapping, "slot_mapping", torch.int64, 1)
+    n = slot_mapping.shape[0]
     shape = (n, cache.num_kv_heads, cache.head_dim)
     for name, t in (("k", k), ("v", v)):
         if t is not None:
-            _req(t, name, cache.torch_dtype, 3)
-            _same_device(cache, t)
+            _take(cache, t, name, cache.torch_dtype, 3)
             if t.shape != shape:
                 raise ValueError(f"{name} must be {list(shape)}")
     if k is None:
         k = slot_mapping.new_empty(shape, dtype=cache.torch_dtype)
     if v is None:
         v = torch.empty_like(k)
-    _check(lib().paged_kv_gather(cache.handle, _ptr(slot_mapping), n, _ptr(k), _ptr(v), _stream()))
+    _check(lib().paged_kv_gather(cache.handle, slots, n, k.data_ptr(), v.data_ptr(), _stream()))
     return k, v
 
 
@@ -322,27 +324,25 @@ def paged_decode_attention_mass(q: torch.Tensor, cache: KVCache, block_tables: t
     """paged_decode_attention that also adds every token's attention weight, summed over the query heads
     of its KV head, to ``attn_mass`` (float32 [S, num_kv_heads, T], in place, after multiplying by
     ``decay``); T must reach every length.  A token's entry starts at 0."""
-    _req(q, "q", cache.torch_dtype, 3)
-    _req(block_tables, "block_tables", torch.int32, 2)
-    _req(context_lens, "context_lens", torch.int32, 1)
-    _req(attn_mass, "attn_mass", torch.float32, 3)
+    qp = _take(cache, q, "q", cache.torch_dtype, 3)
+    tables = _take(cache, block_tables, "block_tables", torch.int32, 2)
+    lens = _take(cache, context_lens, "context_lens", torch.int32, 1)
+    mass = _take(cache, attn_mass, "attn_mass", torch.float32, 3)
     S, hq, d = q.shape
-    if d != cache.head_dim or block_tables.shape[0] != S or context_lens.numel() != S:
+    table_rows, width = block_tables.shape
+    if d != cache.head_dim or table_rows != S or context_lens.shape[0] != S:
         raise ValueError("shape mismatch between q, block_tables and context_lens")
     rows, heads, mass_len = attn_mass.shape
     if rows != S or heads != cache.num_kv_heads:
         raise ValueError(f"attn_mass must be [{S}, {cache.num_kv_heads}, T]")
-    _same_device(cache, q, block_tables, context_lens, attn_mass)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _req(out, "out", cache.torch_dtype, 3)
-        _same_device(cache, out)
+        _take(cache, out, "out", cache.torch_dtype, 3)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    _check(lib().paged_decode_attention_mass(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
-                                             _ptr(context_lens), S, hq, float(scale), float(decay),
-                                             _ptr(attn_mass), mass_len, _ptr(out), _stream()))
+    _check(lib().paged_decode_attention_mass(qp, cache.handle, tables, width, lens, S, hq, float(scale), float(decay),
+                                             mass, mass_len, out.data_ptr(), _stream()))
     return out
 
 
@@ -355,34 +355,39 @@ def paged_kv_evict(cache: KVCache, block_tables: torch.Tensor, context_lens: tor
     Returns (kept int32 [S, Hkv, budget]: the positions that stay, -1 behind them; new_lens int32 [S];
     new_mass float32 [S, Hkv, T']: their mass, 0 behind them, T' = attn_mass's T unless given).  The old
     blocks are unchanged; the caller releases them."""
-    _req(block_tables, "block_tables", torch.int32, 2)
-    _req(dst_block_tables, "dst_block_tables", torch.int32, 2)
-    _req(context_lens, "context_lens", torch.int32, 1)
-    _req(attn_mass, "attn_mass", torch.float32, 3)
-    S, hkv, budget = context_lens.numel(), cache.num_kv_heads, int(budget)
+    tables = _take(cache, block_tables, "block_tables", torch.int32, 2)
+    dst = _take(cache, dst_block_tables, "dst_block_tables", torch.int32, 2)
+    lens = _take(cache, context_lens, "context_lens", torch.int32, 1)
+    mass = _take(cache, attn_mass, "attn_mass", torch.float32, 3)
+    S, hkv, budget, recent = context_lens.shape[0], cache.num_kv_heads, int(budget), int(recent)
+    table_rows, width = block_tables.shape
+    dst_rows, dst_width = dst_block_tables.shape
     rows, heads, mass_len = attn_mass.shape
-    if block_tables.shape[0] != S or dst_block_tables.shape[0] != S or rows != S or heads != hkv:
+    if not table_rows == dst_rows == rows == S or heads != hkv:
         raise ValueError("shape mismatch between tables, context_lens and attn_mass")
     if not 0 <= recent <= budget or not 1 <= budget <= 1 << 30:
         raise ValueError(f"recent {recent} and budget {budget}: 0 <= recent <= budget, 1 <= budget <= 2^30")
-    _same_device(cache, block_tables, dst_block_tables, context_lens, attn_mass)
-    for name, t, dtype, ndim in (("kept", kept, torch.int32, 3), ("new_lens", new_lens, torch.int32, 1),
-                                 ("new_mass", new_mass, torch.float32, 3)):
-        if t is not None:
-            _req(t, name, dtype, ndim)
-            _same_device(cache, t)
-            if t.shape[:2] != ((S,) if ndim == 1 else (S, hkv)) or (t is kept and t.shape[2] != budget):
-                raise ValueError("kept must be [S, num_kv_heads, budget], new_lens [S], new_mass [S, num_kv_heads, T']")
     if kept is None:
         kept = context_lens.new_empty((S, hkv, budget))
+    else:
+        _take(cache, kept, "kept", torch.int32, 3)
+        if kept.shape != (S, hkv, budget):
+            raise ValueError(f"kept must be {[S, hkv, budget]}")
     if new_lens is None:
         new_lens = torch.empty_like(context_lens)
+    else:
+        _take(cache, new_lens, "new_lens", torch.int32, 1)
+        if new_lens.shape[0] != S:
+            raise ValueError(f"new_lens must be {[S]}")
     if new_mass is None:
         new_mass = torch.empty_like(attn_mass)
-    _check(lib().paged_kv_evict(cache.handle, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S,
-                                _ptr(attn_mass), mass_len, budget, int(recent), _ptr(dst_block_tables),
-                                dst_block_tables.shape[1], _ptr(kept), _ptr(new_lens), _ptr(new_mass),
-                                new_mass.shape[2], _stream()))
+    else:
+        _take(cache, new_mass, "new_mass", torch.float32, 3)
+        if new_mass.shape[:2] != (S, hkv):
+            raise ValueError(f"new_mass must be [{S}, {hkv}, T']")
+    _check(lib().paged_kv_evict(cache.handle, tables, width, lens, S, mass, mass_len, budget, recent, dst, dst_width,
+                                kept.data_ptr(), new_lens.data_ptr(), new_mass.data_ptr(), new_mass.shape[2],
+                                _stream()))
     return kept, new_lens, new_mass
 
 
