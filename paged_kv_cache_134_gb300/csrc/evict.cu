@@ -6,19 +6,23 @@
 // sequence of at most B tokens is copied whole.  Attention does not depend on the order of keys whose
 // positions are already in them, so a head may keep tokens of its own choice.
 //
-// One launch: a cluster of 1 to 8 CTAs per row selects, then moves.
-//   * Selection.  Each CTA keeps its stretch of the row's keys (numbers whose unsigned order is the masses') in shared
-//     memory, and the (B - R)-th largest is found by four passes of a radix selection (digits of 8 bits,
-//     histograms in shared memory, summed over the cluster's: 11-bit digits take a pass less, but made the CTAs
-//     spend 34 us on one another's histograms, 16 rows of 131071 positions, where these take 22 in all); up to 512 candidates
-//     are ranked by comparing all with all instead, which takes one pass.  Each warp owns a run of positions, counts what stays, and after
-//     a scan over warps and CTAs writes its kept positions in order.
-//   * Moving.  The kept tokens are shared out evenly over the cluster, 512 at a time: each thread looks up one
-//     token's source and destination slot a chunk ahead, so that a row's copy waits for nothing but its own bytes;
-//     a warp then moves eight tokens' rows at once (K and V, 16 bytes a lane, all loaded before the first is
-//     stored).  Sources and destinations are different blocks, so rows move in any order.
-// Bound by HBM: row_bytes read and written per kept token, K|V and head.  One CTA a row while there are rows for
-// every SM, so that the rows that still select run beside those that move already; a cluster where rows are few.
+// While there is a row for every SM, one CTA takes a row: it selects, then moves, and rows that still select run
+// beside rows that move already.  Few long rows: a cluster of 2 to 8 CTAs selects a row's tokens, and a second
+// launch spreads the copies evenly over all SMs (clusters do not land evenly: two CTAs on one SM, none on
+// another; two sequences of 131071 tokens x 8 heads cut to 8191: 56 us, 60 with the clusters copying themselves).
+//   * Selection.  Each CTA keeps its stretch of the row's keys (numbers whose unsigned order is the masses') in
+//     shared memory, and the (B - R)-th largest is found by four passes of a radix selection (digits of 8 bits,
+//     histograms in shared memory, summed over the cluster's: 11-bit digits take a pass less, but made the
+//     CTAs spend 34 us on one another's histograms, 16 rows of 131071 positions, where these take 24 in all);
+//     up to 512 candidates are ranked by comparing all with all instead, which takes one pass.  Each warp owns
+//     a run of positions, counts what stays, and after a scan over warps and CTAs writes its kept positions in
+//     order.  Bound by latency: sweeps over 16384 keys a CTA and the barriers between them.
+//   * Moving.  A row's kept tokens are shared out evenly over its CTAs, 512 at a time: each thread looks up one
+//     token's source and destination slot a chunk ahead, so that a row's copy waits for nothing but its own
+//     bytes; a warp then moves four tokens' rows at once (K and V, 16 bytes a lane, all loaded before the first
+//     is stored; eight at once spill: 164 us against 159 below).  Sources and destinations are different
+//     blocks, so rows move in any order.  Bound by HBM: row_bytes read and written per kept token, K|V and
+//     head.  1024 rows of up to 4096 fp16 tokens, D = 128, cut to 1024: 973 MB in 159 us, 6.1 TB/s.
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -32,7 +36,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 256;
 constexpr int kAllPairs = 512;      // candidates that are ranked by comparing all with all
 constexpr int kMaxKeys = 24 * 1024; // keys of a CTA in shared memory; longer stretches are read again
-constexpr int kMoveUnroll = 8;
+constexpr int kMoveUnroll = 4;
 
 struct EvictArgs {
     char *pool;
@@ -44,7 +48,7 @@ struct EvictArgs {
     int64_t num_blocks, mass_len, mass_out_len, cap;
     int64_t blk_stride, head_stride, v_off;
     int max_blocks, max_dst_blocks, hkv, bs_log2, d, budget, recent;
-    int cluster, keys; // CTAs of a row; keys of a CTA that fit its shared memory
+    int ctas, keys; // CTAs of a row; keys of a CTA that fit its shared memory
     int row_bytes;
 };
 
@@ -74,28 +78,25 @@ PKV_DEV int peer_word(const void *p, int rank) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_at(p, rank)));
     return v;
 }
-// LPT lanes move one token's K and V rows of one head, 16 bytes each; a 4-bit row's (s, z) words go by the two
-// lanes behind them.  CL: the row has a cluster.
-template <int LPT, bool I4, bool CL>
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
+// tokens of sequence s; one that does not fit is skipped
+PKV_DEV int length_of(const EvictArgs &a, int s) {
+    const int L = max(a.lens[s], 0);
+    if (L <= a.cap) return L;
+    if (threadIdx.x == 0) set_error(a.err, PKV_DEVERR_LENGTH);
+    return 0;
+}
+
+// What stays of row `row` (L tokens of sequence s, KV head kvh), its mass and what lies behind, by CTA `rank`
+// of the row's C (a cluster if CL).
+template <bool CL>
+PKV_DEV void select_row(const EvictArgs &a, int64_t row, int s, int kvh, int L, int rank, int C) {
     extern __shared__ __align__(16) uint32_t keys[];
     __shared__ int hist[2][kBins];
     __shared__ int wsum[2][kWarps];
     __shared__ int sums[2]; // this CTA's larger and equal keys
     __shared__ uint32_t s_prefix;
     __shared__ int s_left;
-    const int C = CL ? a.cluster : 1;
-    const int64_t row = CL ? blockIdx.x / C : blockIdx.x;
-    const int rank = CL ? (int)(blockIdx.x - row * C) : 0;
-    const int s = (int)(row / a.hkv), kvh = (int)(row - (int64_t)s * a.hkv);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_trigger();
-    pdl_wait();
-    int L = max(a.lens[s], 0);
-    if (L > a.cap) {
-        if (tid == 0) set_error(a.err, PKV_DEVERR_LENGTH);
-        L = 0; // the sequence is skipped
-    }
     const float *m = a.mass + row * a.mass_len;
     int32_t *kept = a.kept + row * a.budget;
     float *mo = a.mass_out + row * a.mass_out_len;
@@ -277,12 +278,15 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
     for (int p = len + t0; p < a.budget; p += step) kept[p] = -1;
 #pragma unroll 4
     for (int64_t p = len + t0; p < a.mass_out_len; p += step) mo[p] = 0.f;
+}
 
-    // ---- move: every CTA of the row sees all kept positions, and nobody's shared memory is read any more
-    if (CL)
-        cluster_sync();
-    else
-        __syncthreads();
+// Moves the `len` tokens of row `row` that stay, CTA `rank` of C a C-th of them.  LPT lanes move one token's
+// K and V rows of one head, 16 bytes each; a 4-bit row's (s, z) words go by the two lanes behind them.
+template <int LPT, bool I4>
+PKV_DEV void move_row(const EvictArgs &a, int64_t row, int s, int kvh, int len, int rank, int C) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int32_t *kept = a.kept + row * a.budget;
+    const int per = (len + C - 1) / C, end = min(len, (rank + 1) * per);
     constexpr int kGroups = kThreads / LPT;
     __shared__ uint2 slots[2][kThreads]; // source and destination slot of a chunk's tokens; none: -1
     const int part = lane % LPT, grp = tid / LPT;
@@ -299,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
         return p + (code ? int4_codes(kv, o, in_row, a.d) : int4_params(kv, o, a.d));
     };
     // a chunk's tokens, a thread each: the position two chunks ahead, its blocks one chunk ahead
-    const int stride = C * kThreads, mine = rank * kThreads + tid;
-    auto kept_at = [&](int j) { return j < len ? kept[j] : -1; };
+    const int mine = rank * per + tid;
+    auto kept_at = [&](int j) { return j < end ? kept[j] : -1; };
     auto blocks_at = [&](int j, int t) {
         return t < 0 ? make_int2(0, 0) : make_int2(src_t[t >> a.bs_log2], dst_t[j >> a.bs_log2]);
     };
@@ -312,15 +316,15 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
         }
         return make_uint2(((uint32_t)b.x << a.bs_log2) + (t & (bs - 1)), ((uint32_t)b.y << a.bs_log2) + (j & (bs - 1)));
     };
-    int t1 = kept_at(mine), t2 = kept_at(mine + stride);
+    int t1 = kept_at(mine), t2 = kept_at(mine + kThreads);
     slots[0][tid] = slots_of(mine, t1, blocks_at(mine, t1));
     __syncthreads();
-    for (int j0 = rank * kThreads, buf = 0; j0 < len; j0 += stride, buf ^= 1) {
+    for (int j0 = rank * per, buf = 0; j0 < end; j0 += kThreads, buf ^= 1) {
         t1 = t2;
-        const int j1 = j0 + stride + tid;
+        const int j1 = j0 + kThreads + tid;
         const int2 b1 = blocks_at(j1, t1);
-        t2 = kept_at(j1 + stride);
-        const int here = min(kThreads, len - j0);
+        t2 = kept_at(j1 + kThreads);
+        const int here = min(kThreads, end - j0);
         if (code || par) {
             for (int i0 = grp; i0 < here; i0 += kGroups * kMoveUnroll) {
                 uint2 sl[kMoveUnroll];
@@ -350,15 +354,47 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
     }
 }
 
-template <int LPT, bool I4, bool CL>
-cudaError_t launch_t(const EvictArgs &a, unsigned rows, cudaStream_t st) {
-    auto kern = evict_kernel<LPT, I4, CL>;
+template <int LPT, bool I4>
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int s = blockIdx.x / a.hkv, kvh = blockIdx.x - s * a.hkv, L = length_of(a, s);
+    select_row<false>(a, blockIdx.x, s, kvh, L, 0, 1);
+    __syncthreads();
+    move_row<LPT, I4>(a, blockIdx.x, s, kvh, min(L, a.budget), 0, 1);
+}
+
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int row = blockIdx.x / a.ctas, s = row / a.hkv;
+    select_row<true>(a, row, s, row - s * a.hkv, length_of(a, s), blockIdx.x - row * a.ctas, a.ctas);
+    cluster_sync(); // nobody leaves while its sums are read
+}
+
+template <int LPT, bool I4>
+__global__ void __launch_bounds__(kThreads, 2) move_kernel(const EvictArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int row = blockIdx.x / a.ctas, s = row / a.hkv;
+    move_row<LPT, I4>(a, row, s, row - s * a.hkv, min(length_of(a, s), a.budget), blockIdx.x - row * a.ctas, a.ctas);
+}
+
+template <int LPT, bool I4>
+cudaError_t launch_t(EvictArgs a, unsigned rows, int sms, cudaStream_t st) {
     const size_t smem = a.keys * sizeof(uint32_t);
-    static std::atomic<bool> have[64];
-    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have);
+    static std::atomic<bool> have[2][64];
+    if (a.ctas == 1) {
+        auto kern = evict_kernel<LPT, I4>;
+        cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have[0]);
+        if (e != cudaSuccess) return e;
+        g_pkv_launches++;
+        return pdl_launch(kern, dim3(rows), dim3(kThreads), smem, st, a);
+    }
+    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(select_kernel), have[1]);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(rows * a.cluster);
+    cfg.gridDim = dim3(rows * a.ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -366,16 +402,16 @@ cudaError_t launch_t(const EvictArgs &a, unsigned rows, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.x = a.ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CL ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
-}
-
-template <int LPT, bool I4>
-cudaError_t launch_lpt(const EvictArgs &a, unsigned rows, cudaStream_t st) {
-    return a.cluster > 1 ? launch_t<LPT, I4, true>(a, rows, st) : launch_t<LPT, I4, false>(a, rows, st);
+    cfg.numAttrs = 2;
+    g_pkv_launches++;
+    e = cudaLaunchKernelEx(&cfg, select_kernel, a);
+    if (e != cudaSuccess) return e;
+    a.ctas = (2 * sms + rows - 1) / rows;
+    g_pkv_launches++;
+    return pdl_launch(move_kernel<LPT, I4>, dim3(rows * a.ctas), dim3(kThreads), 0, st, a);
 }
 
 } // namespace
@@ -407,15 +443,15 @@ cudaError_t launch_evict(pkv_cache *c, const EvictLaunch &v, cudaStream_t st) {
     a.row_bytes = i4 ? a.d / 2 : a.d * c->elem_bytes;
     const unsigned rows = (unsigned)v.num_seqs * (unsigned)a.hkv;
     // a CTA per row, or a cluster while there are SMs for its CTAs and each gets 2048 positions or more (16 rows
-    // of 131071 positions: 59 us with clusters of 8, 63 with 16, whose barriers take longer)
-    a.cluster = 1;
-    while (a.cluster < 8 && (int64_t)rows * a.cluster * 2 <= c->num_sms && a.cap / (2 * a.cluster) >= 2048) a.cluster *= 2;
-    const int64_t stretch = ((a.cap + a.cluster - 1) / a.cluster + 31) / 32 * 32;
+    // of 131071 positions: clusters of 16 took 4 us more than clusters of 8, their barriers take longer)
+    a.ctas = 1;
+    while (a.ctas < 8 && (int64_t)rows * a.ctas * 2 <= c->num_sms && a.cap / (2 * a.ctas) >= 2048) a.ctas *= 2;
+    const int64_t stretch = ((a.cap + a.ctas - 1) / a.ctas + 31) / 32 * 32;
     a.keys = (int)std::min<int64_t>(stretch, kMaxKeys);
     const int lanes = 2 * a.row_bytes / 16 + (i4 ? 2 : 0);
     PkvTimer timer(c, PKV_KIND_COPY, st);
-    g_pkv_launches++;
-    if (i4) return lanes <= 8 ? launch_lpt<8, true>(a, rows, st) : launch_lpt<16, true>(a, rows, st);
-    if (lanes <= 8) return launch_lpt<8, false>(a, rows, st);
-    return lanes <= 16 ? launch_lpt<16, false>(a, rows, st) : launch_lpt<32, false>(a, rows, st);
+    const int sms = c->num_sms;
+    if (i4) return lanes <= 8 ? launch_t<8, true>(a, rows, sms, st) : launch_t<16, true>(a, rows, sms, st);
+    if (lanes <= 8) return launch_t<8, false>(a, rows, sms, st);
+    return lanes <= 16 ? launch_t<16, false>(a, rows, sms, st) : launch_t<32, false>(a, rows, sms, st);
 }

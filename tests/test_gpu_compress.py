@@ -555,6 +555,31 @@ def test_evict_long_rows_and_given_outputs():
     assert x.close() == 0
 
 
+@pytest.mark.parametrize("kv,model,hkv,d,bs", EVICT)
+@pytest.mark.parametrize("budget,recent", [(7, 0), (700, 64), (4999, 4999)])
+def test_evict_few_rows_of_very_different_lengths(kv, model, hkv, d, bs, budget, recent):
+    """Rows that several CTAs share: long, one behind the budget, at it, one token, none; masses with NaN, infinities,
+    zeros of both signs and runs of ties."""
+    x = Setup([9003, budget + 1, budget, 1, 0], hq=hkv, hkv=hkv, d=d, kv=kv, model=model, bs=bs, seed=21,
+              extra=5 * ((5000 + bs) // bs + 1))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    mass = torch.rand(5, hkv, 9003, generator=g, device="cuda").pow(6)
+    mass[0, :, 100:4000:7] = float("nan")
+    mass[0, :, 5000:5100] = float("inf")
+    mass[0, :, 6000:6500] = 0.0
+    mass[0, :, 6500:7000] = -0.0
+    mass[0, :, 7000:8000] = 0.5
+    dst = dst_tables(x, budget)
+    kept, lens, new = P.paged_kv_evict(x.cache, x.tables, x.context, mass, budget, recent, dst)
+    check_evicted(x, kept, lens, dst, mass, budget, recent, new)
+    far = x.context.clone()
+    far[0] = 9004
+    kept, lens, new = P.paged_kv_evict(x.cache, x.tables, far, mass, budget, recent, dst)
+    assert x.cache.check_error() == 4
+    assert lens.tolist() == [0, budget, budget, 1, 0] and (kept[0] == -1).all() and not new[0].any()
+    x.cache.close()
+
+
 def test_evict_reports_bad_blocks_and_lengths():
     x = Setup([40, 40, 40], hq=1, hkv=1, d=64, extra=20, seed=1)
     mass = torch.rand(3, 1, 40, device="cuda")
