@@ -168,17 +168,17 @@ PKV_DEV uint32_t pair_fma(uint32_t a, uint32_t b, uint32_t c) {
     return r;
 }
 
-// The values s c + z of eight codes in the model's type, rounded once: a code in the low bits of 1024 (fp16) or 128
-// (bf16), that number taken off, a fused multiply-add.
+// The values s c + z of eight codes in the model's type, rounded once: a code in bits 3..6 of 128 (fp16) or 16 (bf16),
+// where those bits count ones, that number taken off, a fused multiply-add.
 template <int MT>
 PKV_DEV uint4 int4_values(uint32_t codes, uint32_t params) {
-    constexpr uint32_t kBase = MT == PKV_F16 ? 0x64006400u : 0x43004300u, kMinus = kBase | 0x80008000u;
+    constexpr uint32_t kBase = MT == PKV_F16 ? 0x58005800u : 0x41804180u, kMinus = kBase | 0x80008000u;
     const uint32_t s = __byte_perm(params, 0, 0x1010), z = __byte_perm(params, 0, 0x3232);
-    const uint32_t c = ((codes >> 3) & 0x1FFF1FFFu) | ((codes << 13) & 0xE000E000u);
+    const uint32_t other = __byte_perm(codes, 0, 0x2301); // nibbles 2 and 3 where 0 and 1 are
+    const uint32_t at3[4] = {codes, codes >> 4, other, other >> 4};
     uint32_t v[4]; // elements (i, i + 4)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = pair_fma<MT>(pair_add<MT>(((c >> (4 * i)) & 0x000F000Fu) | kBase, kMinus), s, z);
+    for (int i = 0; i < 4; ++i) v[i] = pair_fma<MT>(pair_add<MT>((at3[i] & 0x00780078u) | kBase, kMinus), s, z);
     return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
                       __byte_perm(v[2], v[3], 0x7632));
 }
