@@ -157,11 +157,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 
 // 4-bit append.  Per (token, K|V, KV head) row x[0 .. D): z = min x, s = RN((max x - min x) / 15) in the
 // model's type, code = min(15, rint((x - z) / s)); int4.cuh has the layout and the border cases.  D / 16 lanes
-// share a row, sixteen elements each (two 16-byte loads): the extremes meet by xor shuffles in the NaN-propagating
-// forms, so a NaN anywhere reaches s, and each lane writes the eight bytes of its codes.  With eight elements a
-// lane the row's own work (range, step, reciprocal) cost as much as the codes.  Bound by HBM (4 D bytes read and
-// D + 8 written per token and head) once the arithmetic is out of the way; fp32 pairs halve its instructions.
-constexpr int kAppend4Unroll = 1; // (two: 80 registers, 60 us against 55 for 5256 tokens x 32 heads written and read back)
+// share a row, sixteen elements each (a 16-byte load from each half of the row, so that lanes lie side by side): the
+// extremes meet by xor shuffles in the NaN-propagating forms, so a NaN anywhere reaches s, and each lane writes the four
+// bytes of its codes in either half.  Bound by HBM (4 D bytes read and D + 8 written per token and head) and the
+// ALU alike, 243 instructions a warp for sixteen elements a lane: with eight a lane the row's own work (range, step,
+// reciprocal) cost as much as the codes, and reading tokens ahead into shared memory only added instructions.
+// 5256 tokens x 32 heads, D = 128, written and read back: 43 us, 218 MB, 5.0 TB/s.
+constexpr int kAppend4Ctas = 12; // of an SM, twice what fits: each takes several tokens (32: 44.1 us above, 6: 46.1)
 
 template <int D, int MT, int MODE>
 __global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
@@ -188,35 +190,23 @@ __global__ void __launch_bounds__(kAppendThreads) append4_kernel(AppendArgs a) {
         const int64_t blk = slot >> a.bs_log2;
         const int off = static_cast<int>(slot) & (a.bs - 1);
         const uint4 *ksrc = a.k + j * side * 2, *vsrc = a.v + j * side * 2;
-        for (int rb = r0; rb < per_token; rb += kAppend4Unroll * rstep) {
-            uint4 src[kAppend4Unroll][2];
-#pragma unroll
-            for (int u = 0; u < kAppend4Unroll; ++u) {
-                const int r = rb + u * rstep;
-                if (r >= per_token) continue;
-                // (row r / per_row of K and V; elements 8 c .. and D / 2 + 8 c .., so that lanes lie side by side)
-                const uint4 *p = (r >= side ? vsrc - side * 2 : ksrc) + r / per_row * (2 * per_row) + r % per_row;
-                src[u][0] = __ldcs(p);
-                src[u][1] = __ldcs(p + per_row);
-            }
-#pragma unroll
-            for (int u = 0; u < kAppend4Unroll; ++u) {
-                const int r = rb + u * rstep;
-                if (r >= per_token) continue;
-                const int kv = r >= side ? 1 : 0, hc = r - kv * side, h = hc / per_row, c = hc - h * per_row;
-                const Int4Row row = int4_quantise<MT>(src[u], per_row, lanes);
-                char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, D);
-                *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, c * 4, D)) = row.codes.x;
-                *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, D / 4 + c * 4, D)) = row.codes.y;
-                if (c == 0) *reinterpret_cast<uint32_t *>(tile + int4_params(kv, off, D)) = row.params;
-            }
+        for (int r = r0; r < per_token; r += rstep) {
+            const uint4 *p = (r >= side ? vsrc - side * 2 : ksrc) + r / per_row * (2 * per_row) + r % per_row;
+            const uint4 src[2] = {__ldcs(p), __ldcs(p + per_row)};
+            const int kv = r >= side ? 1 : 0, hc = r - kv * side, h = hc / per_row, c = hc - h * per_row;
+            const Int4Row row = int4_quantise<MT>(src, per_row, lanes);
+            char *tile = a.pool + int4_head(blk, h, a.hkv, a.bs, D);
+            *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, c * 4, D)) = row.codes.x;
+            *reinterpret_cast<uint32_t *>(tile + int4_codes(kv, off, D / 4 + c * 4, D)) = row.codes.y;
+            if (c == 0) *reinterpret_cast<uint32_t *>(tile + int4_params(kv, off, D)) = row.params;
         }
     }
 }
 
 // Rows read back: token j's K and V at slots[j] in the model's type (a 4- or 8-bit row's values, rounded
 // once; a 16-bit row's bits).  A negative slot gives a row of zeros, one past the pool zeros and
-// PKV_DEVERR_SLOT.  Bound by HBM; sixteen elements a thread, loads before stores.
+// PKV_DEVERR_SLOT.  Bound by HBM; sixteen elements a thread, half of them from either half of a row so that lanes lie side
+// by side, two rows' loads before their stores (one: as fast for 4-bit rows; four: 45.4 us for 43.3 above).
 struct GatherArgs {
     uint4 *k, *v;
     const int64_t *slots;
@@ -226,7 +216,7 @@ struct GatherArgs {
     int64_t n, num_slots;
     int hkv, bs_log2;
 };
-constexpr int kGatherUnroll = 2;
+constexpr int kGatherUnroll = 2, kGatherCtas = 12; // CTAs of an SM, as kAppend4Ctas
 
 template <int D, int KVT, int MT>
 __global__ void __launch_bounds__(kAppendThreads) gather_kernel(GatherArgs a) {
@@ -341,8 +331,7 @@ cudaError_t launch_append_t(pkv_cache *c, const AppendArgs &a, cudaStream_t st) 
     const int per_token = 2 * a.hkv * a.chunks_per_row;
     const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
     const int64_t passes = (a.n + tpg - 1) / tpg;
-    // (4-bit: two for each that fits, so that the last ones of a prompt leave fewer SMs idle)
-    const int64_t cap = (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? 12 : 8);
+    const int64_t cap = (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? kAppend4Ctas : 8);
     const dim3 grid((unsigned)(passes < 1 ? 1 : (passes > cap ? cap : passes)));
     PkvTimer timer(c, PKV_KIND_APPEND, st);
     cudaError_t e;
@@ -426,7 +415,7 @@ cudaError_t launch_gather(pkv_cache *c, const int64_t *slots, int64_t n, void *k
     a.bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
     const int per_token = 2 * a.hkv * (c->head_dim / 16);
     const int tpg = per_token >= kAppendThreads ? 1 : kAppendThreads / per_token;
-    const int64_t passes = (n + tpg - 1) / tpg, cap = (int64_t)c->num_sms * 12;
+    const int64_t passes = (n + tpg - 1) / tpg, cap = (int64_t)c->num_sms * kGatherCtas;
     const dim3 grid((unsigned)(passes > cap ? cap : passes)), block(kAppendThreads);
     const bool d64 = c->head_dim == 64, h = c->model_dtype == PKV_F16;
     PkvTimer timer(c, PKV_KIND_COPY, st);

@@ -28,14 +28,19 @@
 //     running maximum does), so that fp16 holds it whatever the steps' magnitude.
 //   * Queries are scaled by a power of two per head so that their largest element is in [2^10, 2^11): fp16
 //     then holds them (and a sixteenth of them) to 2^-31 of that element or better.
-//   * Four warps share a unit's 32-token tiles (whose is fixed by the tile's number), each with its own ring of tiles, no barrier between
-//     warps inside a unit, and the next unit's first tiles on their way before this one is joined.  A tile is
-//     one run of the pool per block: one lane per block copies it, completion counted on an mbarrier
-//     (bounded waits).  One warp in turn finds the next unit, fetches its table and q and lays q out for
-//     all four.
+//   * Four warps share a unit's 32-token tiles (whose is fixed by the tile's number), each with its own ring of
+//     tiles, no barrier between warps inside a unit, and the next unit's first tiles on their way before this one
+//     is joined.  A tile is one run of the pool per block: one lane per block copies it, completion counted
+//     on an mbarrier (bounded waits).  One warp in turn finds the next unit, fetches its table and q and lays q
+//     out for all four, and takes a tile less.
 //   * The running maximum moves only when a score passes it by 2^8 (the weights stay below 2^8, which hi + lo
 //     holds as well as 1), so the accumulator is rescaled about once a unit.
 //   * Scores, softmax statistics, sums and accumulators are fp32.
+//
+// Measured: 32 sequences of up to 4096 tokens, 32 heads (7B batch), 268 MB in 58 us, 4.6 TB/s; 256 ragged ones of up to
+// 8192, four heads to a KV head, 237 MB in 60 us, 3.9 TB/s; one of 131071 tokens, 143 MB in 38 us.  Copies alone take 48 us
+// of the first, arithmetic on data in L2 56: four warps a scheduler, as many as 128 registers allow, hide the two and
+// the dependent chain of a tile behind one another only in part.
 #pragma once
 
 #include <type_traits>
@@ -49,8 +54,9 @@ struct Geo4 {
     static constexpr int kOct = 8 * (D + 8);  // 8 tokens' K, V, (s, z), as in the pool
     static constexpr int kTile = 32;          // tokens
     static constexpr int kBytes = 4 * kOct;
+    // four CTAs per SM, two tiles of 4 KB a warp on their way: with three CTAs of three the 7B batch below takes 62 us
     static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int kCtas = 4; // per SM
+    static constexpr int kCtas = 4;
 };
 
 // Nibbles 0..3 of each 16-bit half of w -> four fp16 pairs (low half, high half): c 2^-21 for nibbles 0

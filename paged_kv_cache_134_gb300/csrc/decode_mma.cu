@@ -20,11 +20,12 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     const bool mass = mass_len >= 0;
     p->cap = (int64_t)max_blocks * c->block_size;
     if (mass) p->cap = std::min(p->cap, mass_len);
-    // Two units per resident CTA at the table's full
-    // width: fewer leave SMs idle at the end, more make units so short that their fixed costs (q, the join, the
-    // partial) show.  At least 64 tokens, at most kMaxSplit; more only to keep a row's splits within 1024.  A
-    // function of the call's shapes, never of the lengths: a result does not change with the other sequences'
-    // lengths.
+    // Two units per resident CTA at the table's full width: fewer leave SMs idle at the end, more make units so
+    // short that their fixed costs (q, the join, the partial) show (one 4-bit sequence of 131071 tokens: 38 us, with
+    // four 43).  At least 64 tokens, at most kMaxSplit (4-bit, 32 sequences of up to 4096 tokens and 256 of up to
+    // 8192: 512 took 9 and 15 us more than 1024; 2048 took 2 and 14 more); more only to keep a row's splits within
+    // 1024.  A function of the call's shapes, never of the lengths: a result does not change with the other
+    // sequences' lengths.
     const bool i4 = c->kv_dtype == PKV_INT4;
     const int64_t workers = (int64_t)c->num_sms * (i4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
     const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads;
