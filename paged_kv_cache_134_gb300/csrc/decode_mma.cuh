@@ -400,7 +400,7 @@ cudaError_t launch_mass_t(const Args &a, int sms, cudaStream_t st) {
     auto kern = decode_mass_kernel<D, KV, MT, G8>;
     constexpr int cols = G8 ? 8 : 4;
     const size_t smem = (size_t)kWarps * G_::kStages * G_::kBytes + kWarps * cols * (D + 4) * sizeof(float) +
-                        2 * cols * D * 2 + (2 * (a.num_seqs + 1) + 2 * (a.split_tokens >> a.bs_log2)) * sizeof(int);
+                        2 * cols * D * 2 + (3 * (a.num_seqs + 1) + 2 * (a.split_tokens >> a.bs_log2)) * sizeof(int);
     cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have);
     if (e != cudaSuccess) return e;
     return pdl_launch(kern, dim3(grid_of(a, sms * G_::kCtas)), dim3(kThreads), smem, st, a);

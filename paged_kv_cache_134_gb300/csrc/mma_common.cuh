@@ -146,9 +146,11 @@ PKV_DEV int row_len(const Args &a, int s) {
 }
 
 // Block scan of the sequences' unit counts: full[s + 1], part[s + 1] hold the inclusive sums of whole
-// splits and of partial ones (a sequence of length 0 has one partial unit, which writes its zero row).
+// splits and of partial ones (a sequence of length 0 has one partial unit, which writes its zero row); the lengths lie
+// behind part.
 PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
     const int S = a.num_seqs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int *len = part + S + 1;
     int cf = 0, cp = 0; // sums of the sequences before this pass
     if (threadIdx.x == 0) full[0] = part[0] = 0;
     for (int s0 = 0; s0 < S; s0 += kThreads) {
@@ -157,6 +159,7 @@ PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
         if (s < S) {
             const int L = row_len(a, s);
             if (blockIdx.x == 0 && (int64_t)a.lens[s] > a.cap) set_error(a.err, PKV_DEVERR_LENGTH);
+            len[s] = L;
             f = L / a.split_tokens;
             p = (L % a.split_tokens != 0 || L == 0) ? 1 : 0;
         }
@@ -188,7 +191,7 @@ PKV_DEV int find_row(const int *pref, int n, int k) {
 }
 
 struct Unit {
-    int s, kvh, j, L, nsplit;
+    int s, kvh, j, nsplit;
     int t0, n; // first token, tokens
 };
 
@@ -201,10 +204,10 @@ PKV_DEV Unit unit_of(const Args &a, const int *full, const int *part, int nfull,
     r.kvh = v - k * a.hkv;
     r.s = find_row(whole ? full : part, a.num_seqs, k);
     r.j = whole ? k - full[r.s] : full[r.s + 1] - full[r.s];
-    r.L = row_len(a, r.s);
+    const int L = part[a.num_seqs + 1 + r.s];
     r.nsplit = (full[r.s + 1] - full[r.s]) + (part[r.s + 1] - part[r.s]);
     r.t0 = r.j * a.split_tokens;
-    r.n = min(r.L - r.t0, a.split_tokens);
+    r.n = min(L - r.t0, a.split_tokens);
     return r;
 }
 
@@ -563,7 +566,7 @@ cudaError_t launch_merge_t(const Args &a, int sms, cudaStream_t st) {
     const size_t smem = (size_t)a.group * a.max_splits * sizeof(float);
     if constexpr (MASS) {
         return pdl_launch(mass_kernel<D, MT>, dim3(grid_of(a, kMassCtas * sms)), dim3(kThreads),
-                          smem + 2 * (a.num_seqs + 1) * sizeof(int), st, a);
+                          smem + 3 * (a.num_seqs + 1) * sizeof(int), st, a);
     } else {
         return pdl_launch(merge_kernel<D, MT>, dim3((unsigned)(a.num_seqs * a.hkv), a.group * D / 32),
                           dim3(kMergeWarps * 32),
