@@ -18,7 +18,8 @@ LIB = os.path.join(LIBDIR, "libpagedkv.so")
 
 SOURCES = ["api.cu", "append.cu", "decode.cu", "decode_f16.cu", "decode_bf16.cu", "decode_fp8_f16.cu",
            "decode_fp8_bf16.cu", "decode_tc.cu", "decode_mma.cu", "decode_mma_int4.cu",
-           "decode_mma_int4_mass.cu", "decode_mma_fp8_mass.cu", "decode_mma_16bit_mass.cu", "evict.cu",
+           "decode_mma_int4_mass.cu", "decode_mma_fp8_mass.cu", "decode_mma_16bit_mass.cu",
+           "decode_short.cu", "decode_short_fp8.cu", "decode_short_int4.cu", "evict.cu",
            "prefill.cu", "prefill_packed.cu", "prefill_paged.cu",
            "prefill_cascade.cu", "noalloc.cu", "blocks.cu", "selftest.cu",
            "prefix_cache.cpp"]

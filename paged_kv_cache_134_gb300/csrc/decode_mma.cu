@@ -14,21 +14,34 @@ struct Plan {
     int64_t cap;    // tokens a sequence may have
     int split, max_splits, seqs;
     int64_t floats; // workspace
+    bool is_short;  // a warp a row
 };
 
 bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len, Plan *p) {
     const bool mass = mass_len >= 0;
     p->cap = (int64_t)max_blocks * c->block_size;
     if (mass) p->cap = std::min(p->cap, mass_len);
+    const bool i4 = c->kv_dtype == PKV_INT4;
+    const int64_t workers = (int64_t)c->num_sms * (i4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
+    const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads;
+    // Short rows by a warp each, where two of three speak for it: the mass (which saves a launch), up to four heads (a
+    // warp's work), more rows than CTAs.  4-bit, D = 128: 8 rows of four heads and 16 tokens, 5.4 us with mass
+    // (units: 8.0), 5.7 without (5.1); 256 rows of eight heads and 32 tokens, 15.7 us with mass (9.4); many rows see
+    // decode_short.cuh.
+    p->is_short = p->cap <= pkv_mma::kShortTokens &&
+                  (int)mass + (hq / c->num_kv_heads <= 4) + (rows > workers) >= 2;
+    if (p->is_short) {
+        p->split = p->max_splits = 1;
+        p->seqs = (int)std::min<int64_t>(num_seqs, 0x7FFFFFFF / c->num_kv_heads);
+        p->floats = 0;
+        return true;
+    }
     // Two units per resident CTA at the table's full width: fewer leave SMs idle at the end, more make units so
     // short that their fixed costs (q, the join, the partial) show (one 4-bit sequence of 131071 tokens: 38 us, with
     // four 43).  At least 64 tokens, at most kMaxSplit (4-bit, 32 sequences of up to 4096 tokens and 256 of up to
     // 8192: 512 took 9 and 15 us more than 1024; 2048 took 2 and 14 more); more only to keep a row's splits within
     // 1024.  A function of the call's shapes, never of the lengths: a result does not change with the other
     // sequences' lengths.
-    const bool i4 = c->kv_dtype == PKV_INT4;
-    const int64_t workers = (int64_t)c->num_sms * (i4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
-    const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads;
     int64_t split = round_up((rows * p->cap + 2 * workers - 1) / (2 * workers), 64);
     split = std::max<int64_t>(64, std::min<int64_t>(split, kMaxSplit));
     split = std::max(split, round_up((p->cap + 1023) / 1024, 64));
@@ -44,6 +57,12 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     p->seqs = (int)n;
     p->floats = n * per_seq;
     return true;
+}
+
+cudaError_t run_short(const pkv_cache *c, const pkv_mma::Args &a, cudaStream_t st) {
+    const int mt = c->model_dtype, D = c->head_dim;
+    if (c->kv_dtype == PKV_INT4) return pkv_short_int4(a, mt, D, st);
+    return c->kv_dtype == PKV_FP8_E4M3 ? pkv_short_fp8(a, mt, D, st) : pkv_short_16bit(a, mt, D, st);
 }
 
 cudaError_t run(const pkv_cache *c, const pkv_mma::Args &a, bool mass, bool merge, cudaStream_t st) {
@@ -127,10 +146,10 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace 
         {
             PkvTimer timer(c, PKV_KIND_DECODE, st);
             g_pkv_launches++;
-            e = run(c, a, mass, false, st);
+            e = p.is_short ? run_short(c, a, st) : run(c, a, mass, false, st);
         }
         if (e != cudaSuccess) return pkv_cuda_fail(e, "decode launch");
-        if (mass || (p.max_splits > 1 && !join)) {
+        if (!p.is_short && (mass || (p.max_splits > 1 && !join))) {
             PkvTimer timer(c, PKV_KIND_MERGE, st);
             g_pkv_launches++;
             e = run(c, a, mass, true, st);

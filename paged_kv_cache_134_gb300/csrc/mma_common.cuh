@@ -21,6 +21,7 @@ namespace pkv_mma {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSeqs = 1024;   // sequences of a launch (their unit counts sit in shared memory)
+constexpr int kShortTokens = 32; // tokens of a row that one warp may take whole (decode_short.cuh): a lane each
 constexpr int kJoinSplits = 16;  // splits of a row that its last CTA joins itself
 
 struct Args {
@@ -580,3 +581,6 @@ cudaError_t pkv_mma_int4(const pkv_mma::Args &, int mt, int D, int sms, bool mer
 cudaError_t pkv_mma_int4_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_fp8_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_16bit_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_short_int4(const pkv_mma::Args &, int mt, int D, cudaStream_t);
+cudaError_t pkv_short_fp8(const pkv_mma::Args &, int mt, int D, cudaStream_t);
+cudaError_t pkv_short_16bit(const pkv_mma::Args &, int mt, int D, cudaStream_t);

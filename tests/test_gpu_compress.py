@@ -363,6 +363,53 @@ def test_decode_with_attention_mass(kv, model, hq, hkv, d, bs):
     assert x.close() == 0
 
 
+SHORT = [0, 1, 2, 7, 8, 9, 16, 17, 31, 32, 32, 5]
+
+
+@pytest.mark.parametrize("kv,model", [("int4", "f16"), ("int4", "bf16"), ("fp8", "f16"), ("fp8", "bf16"), ("f16", "f16"),
+                                      ("bf16", "bf16")])
+@pytest.mark.parametrize("group,hkv,d,bs", [(1, 3, 128, 8), (2, 2, 64, 16), (4, 1, 128, 32), (4, 2, 64, 8), (8, 2, 128, 16)])
+def test_mass_of_short_rows(kv, model, group, hkv, d, bs):
+    """Tables of at most 32 tokens: a warp takes a row (of eight heads only where the rows are many)."""
+    x = Setup(SHORT * (18 if group == 8 else 1), hq=group * hkv, hkv=hkv, d=d, bs=bs, kv=kv, model=model, seed=group)
+    if group == 8 and kv != "f16":
+        assert len(x.lens) * hkv < 608  # few rows here; many below
+    mass = torch.rand(len(x.lens), hkv, 33, device="cuda")
+    old = mass.clone()
+    out = P.paged_decode_attention_mass(x.q, x.cache, x.tables, x.context, x.scale, mass, decay=0.5)
+    check_attention(x, out, mass, old, 0.5)
+    again = old.clone()
+    assert torch.equal(out, P.paged_decode_attention_mass(x.q, x.cache, x.tables, x.context, x.scale, again, decay=0.5))
+    assert torch.equal(mass, again)
+    assert x.close() == 0
+
+
+@pytest.mark.parametrize("group,d,bs", [(1, 128, 16), (4, 64, 8), (8, 128, 8)])
+@pytest.mark.parametrize("kv", ["int4", "fp8", "f16"])
+def test_many_short_rows(kv, group, d, bs):
+    x = Setup([(7 * i) % 33 for i in range(170)], hq=4 * group, hkv=4, d=d, bs=bs, kv=kv, model="f16", seed=3)
+    mass = torch.zeros(170, 4, 32, device="cuda")
+    out = P.paged_decode_attention_mass(x.q, x.cache, x.tables, x.context, x.scale, mass)
+    check_attention(x, out, mass, torch.zeros_like(mass))
+    if kv == "int4":
+        check_attention(x, P.paged_decode_attention(x.q, x.cache, x.tables, x.context, x.scale))
+    # bad blocks and lengths: reported, their tokens left out
+    t = x.tables.clone()
+    t[32, 0] = -3
+    t[19, 0] = x.nb
+    far = x.context.clone()
+    far[64] = 1000
+    out = P.paged_decode_attention_mass(x.q, x.cache, t, far, x.scale, mass)
+    assert x.cache.check_error() == 5
+    k, v = x.stored()
+    for s in (19, 32):
+        stay = list(range(min(bs, x.lens[s]), x.lens[s]))
+        ref, _, pv, big = R.attention(R.to64(x.q[s]), k[x.rows(s)][stay], v[x.rows(s)][stay], x.scale)
+        rel, cut = x.bounds(s, big)
+        assert np.all(np.abs(R.to64(out[s]) - ref) <= R.HALF_STEP["f16"] * np.abs(ref) * 1.001 + rel * pv + cut + 2.0 ** -24)
+    x.cache.close()
+
+
 @pytest.mark.parametrize("kv", ["bf16", "int4"])
 def test_mass_of_long_rows(kv):
     x = Setup([4001, 5, 0, 1600], hq=8, hkv=2, kv=kv, model="bf16", seed=9)
