@@ -184,15 +184,22 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
     int turn = 1; // the warp that prepares the next unit, and takes a tile less of this one
     int slot = 0; // the slot of this warp's next tile
     int nt = 0;   // this warp's tiles of the unit
-    // Tile i of this warp: the others take one each before the warp whose turn it is gets its first, so it is
-    // 4 i + tile0, and one more for the others' first.
-    int tile0 = 0;
+    // Tile i of this warp: where there is a next unit the others take one each before the warp whose turn it is gets
+    // its first, so it is 4 i + tile0, and one more for the others' first.
+    int tile0 = 0, first = 0;
     const char *head = nullptr;
-    auto tile_of = [&](int i) { return 4 * i + tile0 + (i == 0 && tile0 < 6); };
-    auto start = [&]() {
+    auto tile_of = [&](int i) { return 4 * i + tile0 + (i == 0 ? first : 0); };
+    auto start = [&](bool last) {
         const int ntiles = (u.n + T - 1) / T, r = (warp - turn + kWarps - 1) & (kWarps - 1); // 3: this warp's turn
-        nt = r == 3 ? max(0, ntiles - 3) / 4 : ntiles <= r ? 0 : 1 + max(0, ntiles - r) / 4;
-        tile0 = r == 3 ? 6 : r - 1;
+        if (last) {
+            nt = max(0, ntiles + 3 - warp) / 4;
+            tile0 = warp;
+            first = 0;
+        } else {
+            nt = r == 3 ? max(0, ntiles - 3) / 4 : ntiles <= r ? 0 : 1 + max(0, ntiles - r) / 4;
+            tile0 = r == 3 ? 6 : r - 1;
+            first = r != 3;
+        }
         head = a.pool + u.kvh * a.head_stride;
         if (!alive) return;
         int to = slot;
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
             to = to == ST - 1 ? 0 : to + 1;
         }
     };
-    start();
+    start((int)(blockIdx.x + gridDim.x) >= nunits);
 
     Unit prev = u;        // the last unit, if it still has to be counted
     bool pending = false;
@@ -436,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
             u = sm_unit[par];
             bad = sm_bad[par] != 0;
             table = tb + par * tb_len;
-            start();
+            start(un + (int)gridDim.x >= nunits);
         }
         if constexpr (!MASS) {
             if (J.last) {

@@ -9,6 +9,11 @@ constexpr int kMaxSplit = 1024; // tokens
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
+// resident CTAs of the kernels of units
+int64_t workers_of(const pkv_cache *c) {
+    return (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
+}
+
 // What one launch of at most `seqs` sequences looks like.
 struct Plan {
     int64_t cap;    // tokens a sequence may have
@@ -22,7 +27,7 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     p->cap = (int64_t)max_blocks * c->block_size;
     if (mass) p->cap = std::min(p->cap, mass_len);
     const bool i4 = c->kv_dtype == PKV_INT4;
-    const int64_t workers = (int64_t)c->num_sms * (i4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
+    const int64_t workers = workers_of(c);
     const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads;
     // Short rows by a warp each, where two of three speak for it: the mass (which saves a launch), up to four heads (a
     // warp's work), more rows than CTAs.  4-bit, D = 128: 8 rows of four heads and 16 tokens, 5.4 us with mass
@@ -36,14 +41,33 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
         p->floats = 0;
         return true;
     }
-    // Two units per resident CTA at the table's full width: fewer leave SMs idle at the end, more make units so
-    // short that their fixed costs (q, the join, the partial) show (one 4-bit sequence of 131071 tokens: 38 us, with
-    // four 43).  At least 64 tokens, at most kMaxSplit (4-bit, 32 sequences of up to 4096 tokens and 256 of up to
-    // 8192: 512 took 9 and 15 us more than 1024; 2048 took 2 and 14 more); more only to keep a row's splits within
-    // 1024.  A function of the call's shapes, never of the lengths: a result does not change with the other
-    // sequences' lengths.
-    int64_t split = round_up((rows * p->cap + 2 * workers - 1) / (2 * workers), 64);
-    split = std::max<int64_t>(64, std::min<int64_t>(split, kMaxSplit));
+    // Tokens of a split, a function of the call's shapes, never of the lengths (a result does not change with the other
+    // sequences' lengths).  More than four waves of the largest: those, which have the least fixed costs (4-bit, 32
+    // sequences of up to 4096 tokens and 256 of up to 8192: 58 and 60 us; 864 takes 3 more of both, 512 9 and 15).
+    // Else the one with the least time at the table's full width by a model of it: waves of units, each of
+    // so many rounds of the warps' tiles and a fixed part, and what joins the splits.  4-bit: rounds of 2.1 us, 1.2 a
+    // unit, 3 for the last CTA's join, 5 for a merge launch; where a CTA has several units one warp prepares the next and
+    // takes a tile less.  (Against two units per CTA, at least 64 tokens, over a hundred batches of 1 to 256
+    // sequences: 0.5 to 1.1 of the time, 6 % less on average; one sequence of 131071 tokens 38.0 -> 37.1 us.)
+    const int tile = i4 ? 32 : 16, round = 4 * tile;
+    int64_t split = kMaxSplit;
+    if (rows * ((p->cap + kMaxSplit - 1) / kMaxSplit) <= 4 * workers) {
+        double least = 0.;
+        for (int64_t k = i4 ? 1 : 2; k <= 2 * kMaxSplit / round; k += i4 ? 1 : 2) { // whole rounds, or a tile less
+            const int64_t t = (k + 1) / 2 * round - (k % 2 ? tile : 0);
+            const int64_t splits = std::max<int64_t>(1, (p->cap + t - 1) / t), units = rows * splits;
+            if (units > 2 * workers + rows) continue; // (keeps the workspace within decode_mma_workspace_floats)
+            const int64_t tiles = (std::min(t, p->cap) + tile - 1) / tile;
+            const int64_t rounds = i4 && units > workers ? 1 + tiles / 4 : (tiles + 3) / 4;
+            const double join = mass || splits == 1 ? 0. : splits <= pkv_mma::kJoinSplits ? 3. : 5.;
+            const double time = (double)((units + workers - 1) / workers) * ((i4 ? 2.1 : 1.1) * rounds + (i4 ? 1.2 : 3.)) + join;
+            if (least == 0. || time < least) {
+                least = time;
+                split = t;
+            }
+            if (splits == 1) break;
+        }
+    }
     split = std::max(split, round_up((p->cap + 1023) / 1024, 64));
     if (split / c->block_size > (i4 ? 1024 : 8192)) return false; // the split's table entries no longer fit shared memory
     p->split = (int)split;
@@ -76,8 +100,13 @@ cudaError_t run(const pkv_cache *c, const pkv_mma::Args &a, bool mass, bool merg
 } // namespace
 
 int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks) {
-    Plan p;
-    return plan_for(c, num_seqs, hq, max_blocks, -1, &p) ? p.floats : 0;
+    // the most that any call of at most these sizes asks for: its units are at most two waves and one more a row, or
+    // those of the largest split
+    const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads, group = hq / c->num_kv_heads;
+    const int64_t cap = (int64_t)max_blocks * c->block_size;
+    const int64_t units = std::max(rows * ((cap + kMaxSplit - 1) / kMaxSplit), 2 * workers_of(c) + rows);
+    const int64_t row = std::max<int64_t>(group, 1) * (c->head_dim + 2);
+    return std::min(units * row, std::max<int64_t>((int64_t)1 << 29, 1024 * row * c->num_kv_heads));
 }
 
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st) {

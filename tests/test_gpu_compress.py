@@ -797,6 +797,32 @@ def test_reserved_workspace_leaves_no_allocation_to_the_call():
     assert x.close() == 0
 
 
+def test_reserved_workspace_covers_smaller_calls():
+    """No call of fewer sequences, heads or blocks than reserved asks for more than what was reserved."""
+    width, seqs = 700, 160
+    tables = torch.zeros(seqs, width, dtype=torch.int32, device="cuda")
+    lens = torch.ones(seqs, dtype=torch.int32, device="cuda")
+    q = torch.randn(seqs, 16, 128, device="cuda").bfloat16()
+
+    def taken():  # device memory that torch does not hold
+        torch.cuda.synchronize()
+        return -torch.cuda.mem_get_info()[0] - torch.cuda.memory_reserved()
+
+    for reserved in (False, True):  # (the first cache's calls load the code)
+        x = Setup([1], hq=4, hkv=2, d=128, model="bf16", bs=8, extra=0)
+        if reserved:
+            x.cache.reserve(seqs, 16, width)
+        before = taken()
+        for n in (160, 1, 2, 3, 7, 20, 41, 80, 101):
+            for w in (700, 5, 17, 33, 62, 130, 333, 512):
+                for hq in (16, 2, 4):
+                    P.paged_decode_attention(q[:n, :hq].contiguous(), x.cache, tables[:n, :w].contiguous(),
+                                             lens[:n].contiguous(), 1.0)
+        grown = taken() - before
+        assert grown == 0 if reserved else grown > 0
+        assert x.close() == 0
+
+
 # ------------------------------------------------------------------------------------------ refusals
 
 def test_refusals():
