@@ -6,15 +6,15 @@
 // sequence of at most B tokens is copied whole.  Attention does not depend on the order of keys whose
 // positions are already in them, so a head may keep tokens of its own choice.
 //
-// While there is a row for every SM, one CTA takes a row: it selects, then moves, and rows that still select run
-// beside rows that move already.  Few long rows: a cluster of 2 to 8 CTAs selects a row's tokens, and a second
-// launch spreads the copies evenly over all SMs (clusters do not land evenly: two CTAs on one SM, none on
+// While there is a row for every SM, or a row keeps few tokens, one CTA takes a row: it selects, then moves, and rows
+// that still select run beside rows that move already.  Few long rows: a CTA, or a cluster of 2 to 8, selects a
+// row's tokens, and a second launch spreads the copies evenly over all SMs (clusters do not land evenly: two CTAs on one SM, none on
 // another; two sequences of 131071 tokens x 8 heads cut to 8191: 56 us, 60 with the clusters copying themselves).
 //   * Selection.  Each CTA keeps its stretch of the row's keys (numbers whose unsigned order is the masses') in
 //     shared memory, and the (B - R)-th largest is found by four passes of a radix selection (digits of 8 bits,
 //     histograms in shared memory, summed over the cluster's: 11-bit digits take a pass less, but made the
 //     CTAs spend 34 us on one another's histograms, 16 rows of 131071 positions, where these take 24 in all);
-//     up to 512 candidates are ranked by comparing all with all instead, which takes one pass.  Each warp owns
+//     up to 160 candidates are ranked by comparing all with all instead, which takes one pass.  Each warp owns
 //     a run of positions, counts what stays, and after a scan over warps and CTAs writes its kept positions in
 //     order.  Bound by latency: sweeps over 16384 keys a CTA and the barriers between them.
 //   * Moving.  A row's kept tokens are shared out evenly over its CTAs, 512 at a time: each thread looks up one
@@ -34,7 +34,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 256;
-constexpr int kAllPairs = 512;      // candidates that are ranked by comparing all with all
+// candidates that are ranked by comparing all with all (132 of them: 6.3 us, by digits 6.9; 263: 9.8 and 7.7)
+constexpr int kAllPairs = 160;
 constexpr int kMaxKeys = 24 * 1024; // keys of a CTA in shared memory; longer stretches are read again
 constexpr int kMoveUnroll = 4;
 
@@ -140,14 +141,17 @@ PKV_DEV void select_row(const EvictArgs &a, int64_t row, int s, int kvh, int L, 
         uint32_t prefix = 0; // the threshold; `left` of the keys equal to it stay, the first ones
         int left = k;
         if (pairs) {
+            if (tid >= n && tid < ((n + 3) & ~3)) keys[tid] = 0u; // (not larger than any)
             __syncthreads();
             if (tid < n) {
                 const uint32_t mine = keys[tid];
                 int larger = 0, same = 0; // same: equal ones before
-                for (int i = 0; i < n; ++i) {
-                    const uint32_t o = keys[i];
-                    larger += o > mine;
-                    same += o == mine && i < tid;
+#pragma unroll 4
+                for (int i = 0; i < n; i += 4) {
+                    const uint4 o = *reinterpret_cast<const uint4 *>(keys + i);
+                    larger += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+                    same += (o.x == mine && i < tid) + (o.y == mine && i + 1 < tid) + (o.z == mine && i + 2 < tid) +
+                            (o.w == mine && i + 3 < tid);
                 }
                 if (larger + same == k - 1) s_prefix = mine, s_left = same + 1;
             }
@@ -364,12 +368,13 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs a) {
     move_row<LPT, I4>(a, blockIdx.x, s, kvh, min(L, a.budget), 0, 1);
 }
 
+template <bool CL>
 __global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a) {
     pdl_trigger();
     pdl_wait();
-    const int row = blockIdx.x / a.ctas, s = row / a.hkv;
-    select_row<true>(a, row, s, row - s * a.hkv, length_of(a, s), blockIdx.x - row * a.ctas, a.ctas);
-    cluster_sync(); // nobody leaves while its sums are read
+    const int row = CL ? blockIdx.x / a.ctas : blockIdx.x, s = row / a.hkv;
+    select_row<CL>(a, row, s, row - s * a.hkv, length_of(a, s), blockIdx.x - row * a.ctas, a.ctas);
+    if (CL) cluster_sync(); // nobody leaves while its sums are read
 }
 
 template <int LPT, bool I4>
@@ -380,19 +385,13 @@ __global__ void __launch_bounds__(kThreads, 2) move_kernel(const EvictArgs a) {
     move_row<LPT, I4>(a, row, s, row - s * a.hkv, min(length_of(a, s), a.budget), blockIdx.x - row * a.ctas, a.ctas);
 }
 
-template <int LPT, bool I4>
-cudaError_t launch_t(EvictArgs a, unsigned rows, int sms, cudaStream_t st) {
-    const size_t smem = a.keys * sizeof(uint32_t);
-    static std::atomic<bool> have[2][64];
-    if (a.ctas == 1) {
-        auto kern = evict_kernel<LPT, I4>;
-        cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have[0]);
-        if (e != cudaSuccess) return e;
-        g_pkv_launches++;
-        return pdl_launch(kern, dim3(rows), dim3(kThreads), smem, st, a);
-    }
-    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(select_kernel), have[1]);
+template <bool CL>
+cudaError_t launch_select(const EvictArgs &a, unsigned rows, size_t smem, cudaStream_t st) {
+    static std::atomic<bool> have[64];
+    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(select_kernel<CL>), have);
     if (e != cudaSuccess) return e;
+    g_pkv_launches++;
+    if constexpr (!CL) return pdl_launch(select_kernel<CL>, dim3(rows), dim3(kThreads), smem, st, a);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * a.ctas);
     cfg.blockDim = dim3(kThreads);
@@ -406,8 +405,21 @@ cudaError_t launch_t(EvictArgs a, unsigned rows, int sms, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    g_pkv_launches++;
-    e = cudaLaunchKernelEx(&cfg, select_kernel, a);
+    return cudaLaunchKernelEx(&cfg, select_kernel<CL>, a);
+}
+
+template <int LPT, bool I4>
+cudaError_t launch_t(EvictArgs a, unsigned rows, bool apart, int sms, cudaStream_t st) {
+    const size_t smem = a.keys * sizeof(uint32_t);
+    if (!apart) {
+        static std::atomic<bool> have[64];
+        auto kern = evict_kernel<LPT, I4>;
+        cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have);
+        if (e != cudaSuccess) return e;
+        g_pkv_launches++;
+        return pdl_launch(kern, dim3(rows), dim3(kThreads), smem, st, a);
+    }
+    cudaError_t e = a.ctas > 1 ? launch_select<true>(a, rows, smem, st) : launch_select<false>(a, rows, smem, st);
     if (e != cudaSuccess) return e;
     a.ctas = (2 * sms + rows - 1) / rows;
     g_pkv_launches++;
@@ -451,7 +463,10 @@ cudaError_t launch_evict(pkv_cache *c, const EvictLaunch &v, cudaStream_t st) {
     const int lanes = 2 * a.row_bytes / 16 + (i4 ? 2 : 0);
     PkvTimer timer(c, PKV_KIND_COPY, st);
     const int sms = c->num_sms;
-    if (i4) return lanes <= 8 ? launch_t<8, true>(a, rows, sms, st) : launch_t<16, true>(a, rows, sms, st);
-    if (lanes <= 8) return launch_t<8, false>(a, rows, sms, st);
-    return lanes <= 16 ? launch_t<16, false>(a, rows, sms, st) : launch_t<32, false>(a, rows, sms, st);
+    // Few rows that keep many tokens: the copies apart (8 rows that keep 600 bf16 tokens, D = 128: 8.6 us against 13.2; 128
+    // rows that keep 1500 4-bit tokens 26.5 against 34; but 128 that keep 300, 14 against 13)
+    const bool apart = a.ctas > 1 || (rows < (unsigned)sms && std::min<int64_t>(a.cap, a.budget) > 384 + 4 * (int64_t)rows);
+    if (i4) return lanes <= 8 ? launch_t<8, true>(a, rows, apart, sms, st) : launch_t<16, true>(a, rows, apart, sms, st);
+    if (lanes <= 8) return launch_t<8, false>(a, rows, apart, sms, st);
+    return lanes <= 16 ? launch_t<16, false>(a, rows, apart, sms, st) : launch_t<32, false>(a, rows, apart, sms, st);
 }
