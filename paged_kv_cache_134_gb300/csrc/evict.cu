@@ -6,9 +6,9 @@
 // sequence of at most B tokens is copied whole.  Attention does not depend on the order of keys whose
 // positions are already in them, so a head may keep tokens of its own choice.
 //
-// While there is a row for every SM, or a row keeps few tokens, one CTA takes a row: it selects, then moves, and rows
-// that still select run beside rows that move already.  Few long rows: a CTA, or a cluster of 2 to 8, selects a
-// row's tokens, and a second launch spreads the copies evenly over all SMs (clusters do not land evenly: two CTAs on one SM, none on
+// Rows that keep few tokens for their number: one CTA takes a row; it selects, then moves, and rows that still
+// select run beside rows that move already.  Else a CTA, or a cluster of 2 to 8 where rows are few and long, selects a
+// row's tokens, and a second launch spreads the copies over all SMs (clusters do not land evenly: two CTAs on one SM, none on
 // another; two sequences of 131071 tokens x 8 heads cut to 8191: 56 us, 60 with the clusters copying themselves).
 //   * Selection.  Each CTA keeps its stretch of the row's keys (numbers whose unsigned order is the masses') in
 //     shared memory, and the (B - R)-th largest is found by four passes of a radix selection (digits of 8 bits,
@@ -421,7 +421,8 @@ cudaError_t launch_t(EvictArgs a, unsigned rows, bool apart, int sms, cudaStream
     }
     cudaError_t e = a.ctas > 1 ? launch_select<true>(a, rows, smem, st) : launch_select<false>(a, rows, smem, st);
     if (e != cudaSuccess) return e;
-    a.ctas = (2 * sms + rows - 1) / rows;
+    // two for each SM, and no more than 512 tokens for one
+    a.ctas = (int)std::max<int64_t>((2 * sms + rows - 1) / rows, (std::min<int64_t>(a.cap, a.budget) + kThreads - 1) / kThreads);
     g_pkv_launches++;
     return pdl_launch(move_kernel<LPT, I4>, dim3(rows * a.ctas), dim3(kThreads), 0, st, a);
 }
@@ -463,9 +464,10 @@ cudaError_t launch_evict(pkv_cache *c, const EvictLaunch &v, cudaStream_t st) {
     const int lanes = 2 * a.row_bytes / 16 + (i4 ? 2 : 0);
     PkvTimer timer(c, PKV_KIND_COPY, st);
     const int sms = c->num_sms;
-    // Few rows that keep many tokens: the copies apart (8 rows that keep 600 bf16 tokens, D = 128: 8.6 us against 13.2; 128
-    // rows that keep 1500 4-bit tokens 26.5 against 34; but 128 that keep 300, 14 against 13)
-    const bool apart = a.ctas > 1 || (rows < (unsigned)sms && std::min<int64_t>(a.cap, a.budget) > 384 + 4 * (int64_t)rows);
+    // Rows that keep many tokens for their number: the copies apart (8 rows that keep 600 bf16 tokens, D = 128:
+    // 8.6 us against 13.2; 152 rows of very different lengths that keep up to 4566, 40 against 85; but 128 that
+    // keep 300, 14 against 13, and 256 that keep 2000, 76 against 73)
+    const bool apart = a.ctas > 1 || std::min<int64_t>(a.cap, a.budget) > 384 + 4 * (int64_t)rows;
     if (i4) return lanes <= 8 ? launch_t<8, true>(a, rows, apart, sms, st) : launch_t<16, true>(a, rows, apart, sms, st);
     if (lanes <= 8) return launch_t<8, false>(a, rows, apart, sms, st);
     return lanes <= 16 ? launch_t<16, false>(a, rows, apart, sms, st) : launch_t<32, false>(a, rows, apart, sms, st);
