@@ -183,8 +183,9 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
  * row s belonging to row s of the tables; a token's entry has to be 0 before its first step.  decay in
  * [0, 1] (1 sums, less lets old mass fade).  Every cache type; out as paged_decode_attention (to its
  * tolerance, not bit for bit).  A length above mass_len or the tables' tokens sets PKV_DEVERR_LENGTH and
- * is cut to that.  Two launches, the second for the mass; the products take the softmax weights as
- * hi + lo 16-bit pairs, all else is fp32; sums run in a fixed order, so equal calls give equal bits.
+ * is cut to that.  Two launches, the second for the mass (one where no sequence can have more than 32
+ * tokens); the products take the softmax weights as hi + lo 16-bit pairs, all else is fp32; sums run in
+ * a fixed order, so equal calls give equal bits.
  * Workspace: fp32 partials and scores (num_q_heads x tokens x 4 bytes per sequence, at most 2 GB a
  * launch unless one sequence needs more; larger batches run as consecutive launches), one per stream
  * and one per stream capture, allocated by the first call that needs it or more of it, also during a

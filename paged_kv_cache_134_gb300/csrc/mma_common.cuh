@@ -1,4 +1,5 @@
-// What the matrix-instruction decode kernels share (decode_int4.cuh, decode_mma.cuh): arguments, PTX wrappers,
+// What the decode kernels of 4-bit caches and of the attention mass share (decode_int4.cuh, decode_mma.cuh, and for
+// rows of a few tokens decode_short.cuh): arguments, PTX wrappers,
 // the list of units, the join of a unit's warps and of a row's splits, the attention mass.
 //
 // A unit is (sequence, KV head, split of split_tokens tokens); persistent CTAs of four warps walk the units,
