@@ -130,7 +130,10 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
         const bool more = un < nunits;
         Unit next = u;
         int *next_tb = tbuf + (par ^ 1) * tb_len;
-        if (more) next = unit_of(a, full, part, nfull, un);
+        if (more) { // its needs ride in this unit's first group: they have landed with the last tile
+            next = unit_of(a, full, part, nfull, un);
+            stage_unit<D>(a, next, next_tb, qbuf + (par ^ 1) * COLS * D * 2, threadIdx.x, kThreads);
+        }
         const int n = u.n, s = u.s, kvh = u.kvh;
         // ---- q in the order of the K codes; per head: the score scale
         uint32_t qf[KS][2];
@@ -197,8 +200,6 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
             {
                 const int ahead = i + ST - 1;
                 if (ahead < nt) issue(warp + ahead * kWarps, slot == 0 ? ST - 1 : slot - 1);
-                // the next unit's needs ride in the first tile's group: they have landed with the last tile
-                if (i == 0 && more) stage_unit<D>(a, next, next_tb, qbuf + (par ^ 1) * COLS * D * 2, threadIdx.x, kThreads);
                 cp_commit();
             }
             const uint32_t tile = ring_u + slot * G_::kBytes;
@@ -339,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
                 for (int k = 0; k < KS; ++k) product(k, h[0][k], h[0][k + KS], h[1][k], h[1][k + KS]);
             }
         }
-        if (nt == 0 && more) stage_unit<D>(a, next, next_tb, qbuf + (par ^ 1) * COLS * D * 2, threadIdx.x, kThreads);
         cp_commit();
         cp_wait<0>();
 
@@ -348,9 +348,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
             J.m[warp][2 * t4] = m0;
             J.m[warp][2 * t4 + 1] = m1;
         }
-        __syncthreads();
         const Unit cur = u;
-        bad = __syncthreads_or(more && check_table(a, next, next_tb, threadIdx.x, kThreads));
+        bad = __syncthreads_or(more && check_table(a, next, next_tb, threadIdx.x, kThreads)); // (each its own copies)
         u = next;
         tb = next_tb;
         par ^= 1;
