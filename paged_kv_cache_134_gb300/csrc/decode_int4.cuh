@@ -517,7 +517,7 @@ cudaError_t launch_int4_t(const Args &a, int sms, cudaStream_t st) {
                         2 * (D / 32) * 32 * 16 + GC * D * 2 + (3 * (a.num_seqs + 1) + 2 * (a.split_tokens >> a.bs_log2)) * sizeof(int);
     cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have);
     if (e != cudaSuccess) return e;
-    return pdl_launch(kern, dim3(grid_of(a, sms * G_::kCtas)), dim3(kThreads), smem, st, a);
+    return pdl_launch(kern, dim3(grid_of(a, sms * ctas_of(G_::kCtas, smem))), dim3(kThreads), smem, st, a);
 }
 
 template <int MT, bool MASS>

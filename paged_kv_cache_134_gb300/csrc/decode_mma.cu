@@ -10,8 +10,9 @@ constexpr int kMaxSplit = 1024; // tokens
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // resident CTAs of the kernels of units
-int64_t workers_of(const pkv_cache *c) {
-    return (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? 4 : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
+int64_t workers_of(const pkv_cache *c, int group) {
+    const bool few = c->head_dim == 128 && group == 8; // their accumulators leave room for three
+    return (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? (few ? 3 : 4) : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
 }
 
 // What one launch of at most `seqs` sequences looks like.
@@ -27,8 +28,10 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     p->cap = (int64_t)max_blocks * c->block_size;
     if (mass) p->cap = std::min(p->cap, mass_len);
     const bool i4 = c->kv_dtype == PKV_INT4;
-    const int64_t workers = workers_of(c);
-    const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads;
+    const int64_t workers = workers_of(c, hq / c->num_kv_heads);
+    // sequences of a launch: over 16-bit caches the list of more would leave room for one CTA an SM instead of two
+    const int most = i4 || c->kv_dtype == PKV_FP8_E4M3 ? pkv_mma::kMaxSeqs : 384;
+    const int64_t rows = (int64_t)std::min(num_seqs, most) * c->num_kv_heads;
     // Short rows by a warp each, where two of three speak for it: the mass (which saves a launch), up to four heads (a
     // warp's work), more rows than CTAs.  4-bit, D = 128: 8 rows of four heads and 16 tokens, 5.4 us with mass
     // (units: 8.0), 5.7 without (5.1); 256 rows of eight heads and 32 tokens, 15.7 us with mass (9.4); many rows see
@@ -75,8 +78,8 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     // (with mass a row of one split keeps its (m, l) too)
     const int64_t partials = p->max_splits > 1 || mass ? (int64_t)hq * p->max_splits * (c->head_dim + 2) : 0;
     const int64_t per_seq = partials + (mass ? (int64_t)hq * p->cap : 0);
-    // sequences per launch: at most kMaxSeqs, and at most 2 GB of workspace unless one sequence needs more
-    int64_t n = std::min<int64_t>(num_seqs, pkv_mma::kMaxSeqs);
+    // ... and at most 2 GB of workspace unless one sequence needs more
+    int64_t n = std::min(num_seqs, most);
     if (per_seq > 0) n = std::max<int64_t>(1, std::min<int64_t>(n, ((int64_t)1 << 29) / per_seq));
     p->seqs = (int)n;
     p->floats = n * per_seq;
@@ -104,7 +107,7 @@ int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, in
     // those of the largest split
     const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads, group = hq / c->num_kv_heads;
     const int64_t cap = (int64_t)max_blocks * c->block_size;
-    const int64_t units = std::max(rows * ((cap + kMaxSplit - 1) / kMaxSplit), 2 * workers_of(c) + rows);
+    const int64_t units = std::max(rows * ((cap + kMaxSplit - 1) / kMaxSplit), 2 * workers_of(c, 1) + rows);
     const int64_t row = std::max<int64_t>(group, 1) * (c->head_dim + 2);
     return std::min(units * row, std::max<int64_t>((int64_t)1 << 29, 1024 * row * c->num_kv_heads));
 }

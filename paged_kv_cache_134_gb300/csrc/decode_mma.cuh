@@ -29,8 +29,8 @@ struct Geo {
     static constexpr int kChunks = kRow / 16;
     static constexpr int kV = kTile * kRow;                       // V codes behind K's
     static constexpr int kBytes = 2 * kTile * kRow;
-    static constexpr int kStages = kBits == 8 ? 4 : G8 ? 2 : 3;
-    static constexpr int kCtas = kBits == 8 ? 3 : 2; // per SM
+    static constexpr int kStages = kBits == 8 ? (D == 128 ? 3 : 4) : G8 ? 2 : 3;
+    static constexpr int kCtas = kBits == 8 ? 3 : 2; // per SM, as many as fit beside these rings
 };
 
 // Where 16-byte piece c of row r sits in a tile, chosen so that the reads below touch every bank once.
@@ -402,7 +402,7 @@ cudaError_t launch_mass_t(const Args &a, int sms, cudaStream_t st) {
                         2 * cols * D * 2 + (3 * (a.num_seqs + 1) + 2 * (a.split_tokens >> a.bs_log2)) * sizeof(int);
     cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have);
     if (e != cudaSuccess) return e;
-    return pdl_launch(kern, dim3(grid_of(a, sms * G_::kCtas)), dim3(kThreads), smem, st, a);
+    return pdl_launch(kern, dim3(grid_of(a, sms * ctas_of(G_::kCtas, smem))), dim3(kThreads), smem, st, a);
 }
 
 // one cache type's kernels (one translation unit each)

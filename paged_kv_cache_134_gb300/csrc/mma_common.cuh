@@ -557,6 +557,13 @@ __global__ void __launch_bounds__(kThreads, kMassCtas) mass_kernel(const Args a)
         mass_units<D, MT, 8, 2>(a, sm, wj, full, part);
 }
 
+// Resident CTAs per SM: `want`, or what the shared memory holds (228 KB an SM; a CTA has up to 1.5 KB of its own and 1 KB
+// of the system's besides).  A CTA more would wait for a whole walk over the units to end.
+inline int ctas_of(int want, size_t smem) {
+    const int fit = (int)(233472 / (smem + 2560));
+    return fit < 1 ? 1 : fit < want ? fit : want;
+}
+
 inline unsigned grid_of(const Args &a, int slots) {
     const int64_t units = (int64_t)a.num_seqs * a.hkv * (a.max_splits > 0 ? a.max_splits : 1);
     return (unsigned)(units < slots ? units : slots);
