@@ -330,6 +330,28 @@ def test_int4_decode_long_rows_in_many_splits(hq, hkv, lens):
     assert x.close() == 0
 
 
+@pytest.mark.parametrize("hq,hkv,lens,pad", [(8, 8, [9001, 40], 0), (16, 2, [3000] * 5 + [0, 1], 0), (4, 4, [33, 7, 0, 64], 600)])
+def test_int4_decode_without_allocation_captured(hq, hkv, lens, pad):
+    """The fixed scratch: joined by a merge launch, by the last CTA, and single units under wide tables; twice in a graph."""
+    x = Setup(lens, hq=hq, hkv=hkv, model="f16", seed=12)
+    t = torch.nn.functional.pad(x.tables, (0, pad), value=-1).contiguous()
+    want = P.paged_decode_attention(x.q, x.cache, t, x.context, x.scale)
+    check_attention(x, want)
+    outs = [torch.zeros_like(x.q) for _ in range(2)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for o in outs:
+            P.paged_decode_attention_noalloc(x.q, x.cache, t, x.context, x.scale, o)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+    assert x.close() == 0
+
+
 def test_int4_decode_does_not_depend_on_placement_or_on_other_lengths():
     a = Setup([700, 45, 200], seed=3)
     b = Setup([700, 45, 200], seed=3, spread=False)
