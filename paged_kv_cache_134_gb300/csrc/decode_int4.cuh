@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
         float acc[KS][4];
 #pragma unroll
         for (int i = 0; i < KS; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        // the lanes whose columns carry the lo parts (up to four heads: columns 4..7)
-        const uint32_t lo_mask = GC != 8 && t4 >= 2 ? 0xFFFFE000u : 0u;
+        // 1 on the lanes whose columns carry the lo parts (up to four heads: columns 4..7)
+        const float lo_part = GC != 8 && t4 >= 2 ? 1.f : 0.f;
 
         for (int i = 0; i < nt; ++i) {
             if (alive && !mbar_wait(&bars[slot], (phase >> slot) & 1)) {
@@ -363,8 +363,10 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                     }
                 }
             }
-            // ---- P^T as the second product's B operand: hi parts (columns 0..3) and lo parts (4..7), or
-            // for eight heads one after the other
+            // ---- P^T as the second product's B operand: minus the hi parts (columns 0..3) and the lo parts (4..7), or
+            // for eight heads hi and lo one after the other.  hi is w cut to 11 bits; the rest, which is exact, is rounded
+            // to nearest: cut as well, every weight would be low, and over zero-mean rows, whose sums of codes and of
+            // offsets cancel, 131071 tokens' outputs were off by 3e-4.
             uint32_t b[4], bl_[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -379,11 +381,12 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                 }
                 if constexpr (GC == 8) {
                     b[r] = movmatrix(pack_rz<PKV_F16>(w[0], w[1]));
-                    bl_[r] = movmatrix(pack_rz<PKV_F16>(w[0] - kept_rz<PKV_F16>(w[0]), w[1] - kept_rz<PKV_F16>(w[1])));
+                    bl_[r] = movmatrix(
+                        ModelT<PKV_F16>::pack(w[0] - kept_rz<PKV_F16>(w[0]), w[1] - kept_rz<PKV_F16>(w[1])));
                 } else {
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) w[k] -= __uint_as_float(__float_as_uint(w[k]) & lo_mask);
-                    b[r] = movmatrix(pack_rz<PKV_F16>(w[0], w[1]));
+                    for (int k = 0; k < NC; ++k) w[k] = fmaf(w[k], lo_part, -kept_rz<PKV_F16>(w[k]));
+                    b[r] = movmatrix(ModelT<PKV_F16>::pack(w[0], w[1]));
                 }
             }
 
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                 for (int e = 0; e < 4; ++e) {
                     if (NC == 1 && (e & 1)) continue;
                     float v = acc[k][e];
-                    if constexpr (GC != 8) v += __shfl_xor_sync(0xffffffffu, v, 2);
+                    if constexpr (GC != 8) v = __shfl_xor_sync(0xffffffffu, v, 2) - v;
                     acc[k][e] = v * w[e & (NC - 1)].w;
                 }
             if (2 * t4 < COLS) { // 16 (or 8) dims from (D / 8) g of each column

@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
 
         float m0 = -INFINITY, m1 = -INFINITY, mu0 = 0.f, mu1 = 0.f; // running maxima; the finite ones to subtract
         float l0 = 0.f, l1 = 0.f;
+        const float lo_part = !G8 && t4 >= 2 ? 1.f : 0.f; // on the lanes whose columns carry the lo parts
         float acc[KS][4];
 #pragma unroll
         for (int i = 0; i < KS; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -287,18 +288,18 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
             p[3] = fast_exp2(x[3] - mu1);
             l0 += p[0] + p[2];
             l1 += p[1] + p[3];
-            // ---- P^T as the second product's B operand, hi and lo parts
+            // ---- P^T as the second product's B operand: hi parts (cut) and lo parts (the rest, rounded to nearest)
             uint32_t b[2], lo[2] = {0, 0};
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float w0 = p[2 * r], w1 = p[2 * r + 1];
                 if constexpr (G8) {
                     b[r] = movmatrix(pack_rz<OT>(w0, w1));
-                    lo[r] = movmatrix(pack_rz<OT>(w0 - kept_rz<OT>(w0), w1 - kept_rz<OT>(w1)));
-                } else { // columns 4..7 repeat the heads of columns 0..3: they carry the lo parts
-                    w0 -= t4 >= 2 ? kept_rz<OT>(w0) : 0.f;
-                    w1 -= t4 >= 2 ? kept_rz<OT>(w1) : 0.f;
-                    b[r] = movmatrix(pack_rz<OT>(w0, w1));
+                    lo[r] = movmatrix(O::pack(w0 - kept_rz<OT>(w0), w1 - kept_rz<OT>(w1)));
+                } else { // columns 4..7 repeat the heads of columns 0..3: they carry the lo parts, 0..3 minus the hi parts
+                    w0 = fmaf(w0, lo_part, -kept_rz<OT>(w0));
+                    w1 = fmaf(w1, lo_part, -kept_rz<OT>(w1));
+                    b[r] = movmatrix(O::pack(w0, w1));
                 }
             }
 
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
                 const int d1 = G_::kBits == 16 ? d0 + 8 : d0 + KS;
                 if constexpr (!G8) { // hi and lo columns together
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[k][e] += __shfl_xor_sync(0xffffffffu, acc[k][e], 2);
+                    for (int e = 0; e < 4; ++e) acc[k][e] = __shfl_xor_sync(0xffffffffu, acc[k][e], 2) - acc[k][e];
                 }
                 if (2 * t4 < COLS) {
                     o0[d0] = acc[k][0] * f0;

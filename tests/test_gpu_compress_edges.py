@@ -1,0 +1,64 @@
+"""GPU tests of the 4-bit cache and the decode with attention mass where they can lose precision, drop a NaN or keep
+state between calls: against 64-bit references, with bounds derived beside them."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import compress_ref as R
+import paged_kv_cache_134_gb300 as P
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+TORCH = R.TORCH
+
+
+def fill(k, v, kv, model, bs=16, lens=None, k_scale=None, v_scale=None):
+    """A cache of the sequences' rows k, v [N, Hkv, D] (fp32) one after the other: (cache, tables, lengths)."""
+    lens = [k.shape[0]] if lens is None else lens
+    need = [(n + bs - 1) // bs for n in lens]
+    cache = P.KVCache(max(1, sum(need)), bs, k.shape[1], k.shape[2], kv_dtype=kv, model_dtype=model)
+    cache.view()[0].fill_(255)
+    if kv == "fp8":
+        one = torch.ones(k.shape[1], device="cuda")
+        cache.set_scales(one if k_scale is None else k_scale, one if v_scale is None else v_scale)
+    t = torch.full((len(lens), max(1, max(need))), -1, dtype=torch.int32)
+    at, slots = 0, []
+    for i, n in enumerate(need):
+        t[i, :n] = torch.arange(at, at + n, dtype=torch.int32)
+        slots.append(torch.arange(lens[i]) + at * bs)
+        at += n
+    P.paged_kv_append(cache, k.to(TORCH[model]).contiguous(), v.to(TORCH[model]).contiguous(),
+                      torch.cat(slots).cuda())
+    return cache, t.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------------------------------ precision
+
+@pytest.mark.parametrize("model", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv", [(32, 32), (64, 16), (64, 8)])
+def test_int4_weights_are_not_cut_to_one_side(model, hq, hkv):
+    """Rows whose elements 0..63 hold code 8 and read as exactly 0 (offset -8 s): what the output has there is what the
+    weights of the codes' sum lost against those of the offsets' sum.
+
+    Bound of the mean over heads, in units of 8 s.  128 tokens, a 32-token tile a warp: two matrix instructions a
+    warp and column, each at most 2^-23 of its sum: 2^-22.  Weights rounded to nearest are off by at most 2^-22 of
+    themselves, or 2^-25 of a weight that is at least 2^-3 of the largest where the lo part is subnormal; with
+    fp32 sums of eight terms (2^-24 each at most) these have no preferred sign: the mean over 32 or more heads of
+    128 tokens stays below 6.5 (odds of 10^-9, Hoeffding) * 2^-21 / sqrt(32 * 128) < 2^-24."""
+    L, d, s = 128, 128, 64.0
+    g = torch.Generator(device="cuda").manual_seed(3)
+    codes = torch.randint(0, 16, (L, hkv, d), generator=g, device="cuda").float()
+    codes[..., :64], codes[..., 64], codes[..., 65] = 8, 0, 15
+    k = torch.randn(L, hkv, d, generator=g, device="cuda")
+    cache, tables, lens = fill(k, (codes - 8) * s, "int4", model)
+    q = torch.randn(1, hq, d, generator=g, device="cuda").to(TORCH[model])
+    out = P.paged_decode_attention(q, cache, tables, lens, 1 / math.sqrt(d))
+    off = R.to64(out[0, :, :64]) / (8 * s)
+    assert abs(off.mean()) <= 2.0 ** -22 + 2.0 ** -24, off.mean()
+    assert cache.check_error() == 0
+    cache.close()
