@@ -33,8 +33,12 @@
 //     is joined.  A tile is one run of the pool per block: one lane per block copies it, completion counted
 //     on an mbarrier (bounded waits).  One warp in turn finds the next unit, fetches its table and q and lays q
 //     out for all four, and takes a tile less.
-//   * The running maximum moves only when a score passes it by 2^8 (the weights stay below 2^8, which hi + lo
-//     holds as well as 1), so the accumulator is rescaled about once a unit.
+//   * Two references a column.  The weights p stand against m, a running maximum of the scores that moves only when
+//     a score passes it by 2^8.  The products p s that go into the second product are multiplied by F, a power of two
+//     that puts the largest so far between 2^4 and 2^15: hi + lo hold them to 2^-22 of themselves or 2^-29 of the
+//     largest, whatever tokens of great weight and small range, or of great range and no weight, stand among them
+//     (F from the largest step alone: one token of e^-20 of the weight and 1024 times the range cost the others
+//     1e-2 of the output).  Both move about once a unit (m by 2^4, F from 2^8: 62.7 us for the 61.6 of 256 ragged rows).
 //   * Scores, softmax statistics, sums and accumulators are fp32.
 //
 // Measured: 32 sequences of up to 4096 tokens, 32 heads (7B batch), 268 MB in 58 us, 4.6 TB/s; 256 ragged ones of up to
@@ -67,6 +71,9 @@ PKV_DEV void widen4(uint32_t w, uint32_t v, uint32_t *h) {
     h[2] = v & 0x00780078u;
     h[3] = v & 0x07800780u;
 }
+
+PKV_DEV int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; } // of a positive number
+PKV_DEV float power_of_two(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + e) << 23); } // e < 128
 
 // GC: 1 query head per KV head, 4 (two or four), 8
 template <int D, int MT, int GC, bool MASS>
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
         // reference maxima; the finite ones to subtract; the scores above which they move
         float m[2] = {-INFINITY, -INFINITY}, mu[2] = {0.f, 0.f}, lim[2] = {-INFINITY, -INFINITY};
         float l[2] = {0.f, 0.f}, z[2] = {0.f, 0.f};
-        float A = 0.f, invA = 1.f;
+        float F[2] = {1.f, 1.f}, lim_s = 0.f; // of the products; the step above which they may pass 2^15
         float acc[KS][4];
 #pragma unroll
         for (int i = 0; i < KS; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -319,39 +326,56 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                     }
             }
 
-            // ---- reference maximum and the divisor of p s (they move rarely: one vote a tile)
+            // ---- references: one vote a tile, on its largest scores and its largest step
             float n_[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int k = 0; k < NC; ++k) n_[k] = fmaxf(fmaxf(x[0][k], x[1][k]), fmaxf(x[2][k], x[3][k]));
             float ns = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-            bool up = ns > A;
+            bool up = ns > lim_s;
 #pragma unroll
             for (int k = 0; k < NC; ++k) up = up || n_[k] > lim[k];
             if (__any_sync(0xffffffffu, up)) {
+                float most[2] = {0.f, 0.f}; // the tile's largest product
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
 #pragma unroll
                     for (int k = 0; k < NC; ++k) n_[k] = fmaxf(n_[k], __shfl_xor_sync(0xffffffffu, n_[k], o));
                     ns = fmaxf(ns, __shfl_xor_sync(0xffffffffu, ns, o));
                 }
-                float f[2] = {1.f, 1.f};
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
                     n_[k] = fmaxf(n_[k], m[k]);
-                    f[k] = m[k] == n_[k] ? 1.f : fast_exp2(m[k] - n_[k]);
-                    m[k] = n_[k];
-                    mu[k] = m[k] == -INFINITY ? 0.f : m[k];
-                    lim[k] = m[k] + 8.f;
-                    l[k] *= f[k];
-                    z[k] *= f[k];
+                    mu[k] = n_[k] == -INFINITY ? 0.f : n_[k];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) most[k] = fmaxf(most[k], fast_exp2(x[r][k] - mu[k]) * vs[r]);
                 }
-                if (ns > A) { // a power of two twice to four times the largest step (its reciprocal stays normal)
-                    const int e = min(max((int)(__float_as_uint(ns) >> 23) + 2, 2), 252);
-                    const float nA = __uint_as_float((uint32_t)e << 23);
-                    invA = __uint_as_float((uint32_t)(254 - e) << 23);
-                    f[0] *= A * invA;
-                    f[1] *= A * invA;
-                    A = nA;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) most[k] = fmaxf(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
+                }
+                float f[2] = {1.f, 1.f}; // of the accumulator
+                lim_s = INFINITY;
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const float d = m[k] == n_[k] ? 0.f : fminf(n_[k] - m[k], 300.f), whole = floorf(d);
+                    const float back = fast_exp2(-d);
+                    l[k] *= back;
+                    z[k] *= back;
+                    // F against the new m, but for the fraction of the move, and what the tile asks for
+                    const int e = exponent(F[k]) + (int)whole, q = exponent(most[k]);
+                    int to = min(4 - q, 100);
+                    if (m[k] != -INFINITY) {
+                        to = e > 100 || e + q >= 15 ? min(to, e) : e;
+                        f[k] = fast_exp2(whole - d) * power_of_two(to - e);
+                    }
+                    const int room = min(0, 125 - exponent(ns) - to); // F times any step stays finite
+                    to += room;
+                    f[k] *= power_of_two(room);
+                    F[k] = power_of_two(to);
+                    m[k] = n_[k];
+                    lim[k] = m[k] + 8.f;
+                    lim_s = fminf(lim_s, power_of_two(7 - to)); // of p <= 2^8
                 }
                 if (i > 0) { // (nothing is summed before the first tile)
 #pragma unroll
@@ -371,13 +395,12 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float w[2] = {0.f, 0.f};
-                const float sv = vs[r] * invA;
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
                     const float p = fast_exp2(x[r][k] - mu[k]);
                     l[k] += p;
                     z[k] = fmaf(p, vz[r], z[k]);
-                    w[k] = p * sv;
+                    w[k] = p * (F[k] * vs[r]);
                 }
                 if constexpr (GC == 8) {
                     b[r] = movmatrix(pack_rz<PKV_F16>(w[0], w[1]));
@@ -466,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                     J.z[warp][2 * t4 + k] = z[k];
                     if (warp == 0) J.M[2 * t4 + k] = w[k].M;
                 }
-                w[k].w *= A;
+                w[k].w *= power_of_two(-exponent(F[k]));
             }
-            // hi and lo columns together; A and the warp's weight
+            // hi and lo columns together; F and the warp's weight
 #pragma unroll
             for (int k = 0; k < KS; ++k)
 #pragma unroll

@@ -62,3 +62,60 @@ def test_int4_weights_are_not_cut_to_one_side(model, hq, hkv):
     assert abs(off.mean()) <= 2.0 ** -22 + 2.0 ** -24, off.mean()
     assert cache.check_error() == 0
     cache.close()
+
+
+def outlier(L, hq, hkv, d, at, shift, gain, seed, channel):
+    """fp32 (q, k, v) of one sequence whose token `at` scores `shift` beside the others' scores of about 1, with a V row
+    `gain` times as large.  The score comes from one large channel, or from all of them."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = torch.randn(L, hkv, d, generator=g, device="cuda")
+    v = torch.randn(L, hkv, d, generator=g, device="cuda")
+    q = torch.randn(1, hq, d, generator=g, device="cuda")
+    if channel:
+        q[..., 0], k[..., 0] = 8.0, 0.0
+        k[at] *= 0.01
+        k[at, :, 0] = shift * math.sqrt(d) / 8.0
+    else:
+        sign = torch.where(torch.rand(d, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+        q = sign + 0.1 * q
+        k[at] = shift / math.sqrt(d) * sign
+    v[at] *= gain
+    return q, k, v
+
+
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (16, 2)])
+@pytest.mark.parametrize("channel", [True, False])
+@pytest.mark.parametrize("L,at,shift,gain", [
+    (256, 5, -20.0, 64.0), (256, 5, -20.0, 1024.0), (1000, 900, -20.0, 1024.0),   # no weight, a great range
+    (5000, 3, 16.0, 1.0 / 64), (5000, 3, 16.0, 1.0), (5000, 4990, 16.0, 1.0 / 64),  # nearly all the weight
+    (700, 3, -60.0, 3000.0), (700, 3, 40.0, 1e-3),
+    (700, 3, -60.0, 30000.0)])                             # past the type: the row reads as NaN, and so does the output
+def test_int4_a_token_of_another_magnitude_leaves_the_others_their_weights(L, at, shift, gain, channel, hq, hkv, mass):
+    """Bound: half a step of the output, the weights' relative error, and what the codes lose in a product of 16 tokens,
+    2^-17 of a step of the largest p s among them: over all groups of 16 at most 16 * 2^-17 sum(p s).  A product p s is
+    kept to 2^-22 of itself or 2^-29 of the largest of its warp's tokens of a split, 256 of them: together, times codes of
+    at most 15, 15 * 2^-21 sum(p s)."""
+    d, model = 128, "f16"
+    q, k, v = outlier(L, hq, hkv, d, at, shift, gain, L + hq, channel)
+    q = q.to(TORCH[model])
+    cache, tables, lens = fill(k, v, "int4", model)
+    scale = 1 / math.sqrt(d)
+    k64, v64 = (R.values4(*R.quantise4(R.to64(x.to(TORCH[model])), model)) for x in (k, v))
+    steps = [R.quantise4(R.to64(x.to(TORCH[model])), model)[1] for x in (k, v)]
+    m = torch.zeros(1, hkv, L, device="cuda")
+    out = (P.paged_decode_attention_mass(q, cache, tables, lens, scale, m) if mass
+           else P.paged_decode_attention(q, cache, tables, lens, scale))
+    ref, p, pv, big = R.attention(R.to64(q[0]), k64, v64, scale)
+    rel = R.relative_weight_error(big) + R.code_alignment(d, R.to64(q[0]), steps[0], scale)
+    ps = np.einsum("ht,th->h", p, np.repeat(steps[1], hq // hkv, 1))[:, None]
+    tol = R.HALF_STEP[model] * np.abs(ref) * 1.001 + rel * pv + (2.0 ** -13 + 15 * 2.0 ** -21) * ps + 2.0 ** -24
+    err = np.abs(R.to64(out[0]) - ref)
+    nan = np.isnan(ref)
+    assert np.array_equal(np.isnan(R.to64(out[0])), nan)
+    assert np.all(err[~nan] <= tol[~nan]), (err / tol)[~nan].max()
+    if mass:
+        want = p.reshape(hkv, hq // hkv, L).sum(1)
+        assert np.all(np.abs(R.to64(m[0]) - want) <= rel * want + 2.0 ** -24)
+    assert cache.check_error() == 0
+    cache.close()
