@@ -7,9 +7,11 @@
 // mostly still in L2 when they are read) are kept until the row's last split is done.  Bound by the bytes of
 // the cache.  K tile: A operand of mma.sync (16 tokens x D), q^T: B operand (D x 8 heads); V tile: A
 // operand (16 dims x 16 tokens at a time, read transposed), P^T: B operand.  P goes from the first product's
-// layout to the second's by movmatrix, as hi + lo parts (2^-20 relative for fp16 operands, 2^-14 for bf16):
+// layout to the second's by movmatrix, as hi + lo parts (2^-22 relative for fp16 operands, 2^-16 for bf16):
 // with up to four heads the lo part uses the four columns of B that are free anyway, with eight it takes a
-// second product.  E4M3 codes widen to fp16 in registers; bf16 queries are then scaled by a power of two
+// second product.  For fp16 operands the largest weight so far stands at 2^14, so that weights down to 2^-28 of it
+// stay normal numbers and smaller ones lose 2^-39 of it at most (at 1, 20000 tokens beside one of e^16 times their
+// weight lost 4e-4 of their sum).  E4M3 codes widen to fp16 in registers; bf16 queries are then scaled by a power of two
 // per head so that their largest element is in [2^10, 2^11).  Each warp has its own ring of 16-token tiles,
 // filled by cp.async and swizzled on the way (no barrier between warps, no wait that could hang).
 //
@@ -58,6 +60,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
     using O = ModelT<OT>;
     constexpr int KS = D / 16; // k steps of the first product = m tiles of the second
     constexpr int ST = G_::kStages;
+    constexpr float kUp = OT == PKV_F16 ? 14.f : 0.f; // log2 of the largest weight
     extern __shared__ __align__(128) char smem[];
     __shared__ Join J;
     __shared__ int sm_tmp[2 * kWarps];
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
             qs1 = __shfl_sync(0xffffffffu, qs, 8 * t4 + 4);
         }
 
-        float m0 = -INFINITY, m1 = -INFINITY, mu0 = 0.f, mu1 = 0.f; // running maxima; the finite ones to subtract
+        float m0 = -INFINITY, m1 = -INFINITY, mu0 = 0.f, mu1 = 0.f; // running maxima; the finite numbers to subtract
         float l0 = 0.f, l1 = 0.f;
         const float lo_part = !G8 && t4 >= 2 ? 1.f : 0.f; // on the lanes whose columns carry the lo parts
         float acc[KS][4];
@@ -269,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
                 const float f0 = m0 == n0 ? 1.f : fast_exp2(m0 - n0), f1 = m1 == n1 ? 1.f : fast_exp2(m1 - n1);
                 m0 = n0;
                 m1 = n1;
-                mu0 = m0 == -INFINITY ? 0.f : m0;
-                mu1 = m1 == -INFINITY ? 0.f : m1;
+                mu0 = m0 == -INFINITY ? 0.f : m0 - kUp;
+                mu1 = m1 == -INFINITY ? 0.f : m1 - kUp;
                 l0 *= f0;
                 l1 *= f1;
 #pragma unroll
@@ -346,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
 
         // ---- the next unit's first tiles, then this unit's join
         if (g == 0) {
-            J.m[warp][2 * t4] = m0;
-            J.m[warp][2 * t4 + 1] = m1;
+            J.m[warp][2 * t4] = m0 - kUp;
+            J.m[warp][2 * t4 + 1] = m1 - kUp;
         }
         const Unit cur = u;
         bad = __syncthreads_or(more && check_table(a, next, next_tb, threadIdx.x, kThreads)); // (each its own copies)

@@ -119,3 +119,36 @@ def test_int4_a_token_of_another_magnitude_leaves_the_others_their_weights(L, at
         assert np.all(np.abs(R.to64(m[0]) - want) <= rel * want + 2.0 ** -24)
     assert cache.check_error() == 0
     cache.close()
+
+
+@pytest.mark.parametrize("kv,model", [("f16", "f16"), ("bf16", "bf16"), ("fp8", "f16"), ("fp8", "bf16")])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (16, 2)])
+@pytest.mark.parametrize("shift,at", [(12.0, 3), (16.0, 3), (18.0, 3), (20.0, 19990)])
+def test_mass_decode_keeps_small_weights_beside_a_dominant_one(kv, model, hq, hkv, shift, at):
+    """One token of zeros takes nearly all the weight: the output is the other 19999 tokens' share.
+
+    Bound: half a step of the output; a score of at most 16 fp32 roundings of 2^-23 of sum |q||k| scale, in a weight twice
+    that; 2^-19 for exp2 and the sums; 2^-15 for weights as bf16 pairs (2^-22 as fp16 pairs), and 2^-39 of the
+    largest weight for each that is no normal fp16 number."""
+    L, d = 20000, 128
+    q, k, v = outlier(L, hq, hkv, d, at, shift, 1.0, hq, False)
+    v = 1000.0 + 100.0 * v
+    v[at] = 0.0
+    q, k, v = (x.to(TORCH[model]) for x in (q, k, v))
+    scales = [(x.float().abs().amax(dim=(0, 2)) / 448).contiguous() for x in (k, v)]
+    cache, tables, lens = fill(k, v, kv, model, k_scale=scales[0], v_scale=scales[1])
+    scale = 1 / math.sqrt(d)
+    m = torch.zeros(1, hkv, L, device="cuda")
+    out = P.paged_decode_attention_mass(q, cache, tables, lens, scale, m)
+    if kv == "fp8":
+        k, v = ((x.float() / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).double() * s[:, None].double()
+                for x, s in zip((k, v), scales))
+    ref, p, pv, big = R.attention(R.to64(q[0]), R.to64(k), R.to64(v), scale)
+    rel = 2 * 16 * 2.0 ** -23 * big + 2.0 ** -19 + (2.0 ** -15 if kv == "bf16" else 0.0)
+    tol = R.HALF_STEP[model] * np.abs(ref) * 1.001 + rel * pv + L * 2.0 ** -39 * float(v.double().abs().max()) + 2.0 ** -24
+    err = np.abs(R.to64(out[0]) - ref)
+    assert np.all(err <= tol), (err / tol).max()
+    want = p.reshape(hkv, hq // hkv, L).sum(1)
+    assert np.all(np.abs(R.to64(m[0]) - want) <= rel * want + 2.0 ** -60)
+    assert cache.check_error() == 0
+    cache.close()
