@@ -483,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
             for (int k = 0; k < NC; ++k) {
                 w[k] = warp_weight(J, warp, 2 * t4 + k);
                 l[k] = row_sum(l[k]);
-                z[k] = w[k].w == 0.f ? 0.f : row_sum(z[k]) * w[k].w;
+                z[k] = row_sum(z[k]); // (all lanes: the columns' weights differ)
+                z[k] = w[k].w == 0.f ? 0.f : z[k] * w[k].w;
                 if (g == 0) {
                     J.l[warp][2 * t4 + k] = w[k].w == 0.f ? 0.f : l[k] * w[k].w;
                     J.z[warp][2 * t4 + k] = z[k];

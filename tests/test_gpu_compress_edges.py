@@ -152,3 +152,29 @@ def test_mass_decode_keeps_small_weights_beside_a_dominant_one(kv, model, hq, hk
     assert np.all(np.abs(R.to64(m[0]) - want) <= rel * want + 2.0 ** -60)
     assert cache.check_error() == 0
     cache.close()
+
+
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (4, 1, 128), (8, 1, 64), (8, 1, 128)])
+@pytest.mark.parametrize("L,at", [(128, 3), (700, 690), (2500, 5)])
+def test_int4_a_warp_without_weight_in_one_head_only(hq, hkv, d, L, at, mass):
+    """One head has a token 250 above the others, so that every other warp's weight in that head alone is 0."""
+    g = torch.Generator(device="cuda").manual_seed(hq)
+    k, v = torch.randn(2, L, hkv, d, generator=g, device="cuda")
+    q = torch.randn(1, hq, d, generator=g, device="cuda")
+    q[..., 0], k[..., 0] = 0.0, 0.0
+    q[:, 1, 0], k[at, :, 0] = 50.0, 5.0 * math.sqrt(d)
+    q, k, v = (x.half() for x in (q, k, v))
+    cache, tables, lens = fill(k, v, "int4", "f16")
+    scale = 1 / math.sqrt(d)
+    m = torch.zeros(1, hkv, L, device="cuda")
+    out = (P.paged_decode_attention_mass(q, cache, tables, lens, scale, m) if mass
+           else P.paged_decode_attention(q, cache, tables, lens, scale))
+    quantised = [R.quantise4(R.to64(x), "f16") for x in (k, v)]
+    ref, p, pv, big = R.attention(R.to64(q[0]), *(R.values4(*x) for x in quantised), scale)
+    rel = R.relative_weight_error(big) + R.code_alignment(d, R.to64(q[0]), quantised[0][1], scale)
+    tol = R.HALF_STEP["f16"] * np.abs(ref) * 1.001 + rel * pv + 2.0 ** -13 * float(quantised[1][1].max()) + 2.0 ** -24
+    assert np.all(np.abs(R.to64(out[0]) - ref) <= tol)
+    assert abs(p[1, at] - 1) < 1e-6 and p[0, at] < 0.5
+    assert cache.check_error() == 0
+    cache.close()
