@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                     F[k] = power_of_two(to);
                     m[k] = n_[k];
                     lim[k] = m[k] + 8.f;
-                    lim_s = fminf(lim_s, power_of_two(7 - to)); // of p <= 2^8
+                    if (m[k] != -INFINITY) lim_s = fminf(lim_s, power_of_two(7 - to)); // of p <= 2^8
                 }
                 if (i > 0) { // (nothing is summed before the first tile)
 #pragma unroll
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
                 z[k] = row_sum(z[k]); // (all lanes: the columns' weights differ)
                 z[k] = w[k].w == 0.f ? 0.f : z[k] * w[k].w;
                 if (g == 0) {
-                    J.l[warp][2 * t4 + k] = w[k].w == 0.f ? 0.f : l[k] * w[k].w;
+                    J.l[warp][2 * t4 + k] = l[k] * w[k].w; // (a NaN comes through a weight of 0)
                     J.z[warp][2 * t4 + k] = z[k];
                     if (warp == 0) J.M[2 * t4 + k] = w[k].M;
                 }

@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
             l0 = row_sum(l0);
             l1 = row_sum(l1);
             if (g == 0) {
-                J.l[warp][2 * t4] = w0.w == 0.f ? 0.f : l0 * w0.w;
-                J.l[warp][2 * t4 + 1] = w1.w == 0.f ? 0.f : l1 * w1.w;
+                J.l[warp][2 * t4] = l0 * w0.w; // (a NaN comes through a weight of 0)
+                J.l[warp][2 * t4 + 1] = l1 * w1.w;
                 if (warp == 0) {
                     J.M[2 * t4] = w0.M;
                     J.M[2 * t4 + 1] = w1.M;

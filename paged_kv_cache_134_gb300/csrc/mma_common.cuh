@@ -262,6 +262,8 @@ struct Join {
     int last;
 };
 
+// The running maxima pass over NaN, so what saw nothing else keeps -inf and weighs 0: its sums are NaN, and are multiplied
+// by their weight whatever that is, so that a row with a NaN score (or a NaN in V) comes out NaN however it was split.
 PKV_DEV float weight_of(float m, float M) { return m == -INFINITY ? 0.f : m == M ? 1.f : fast_exp2(m - M); }
 
 // Row (s, kvh)'s splits: maxima, reciprocal sums (M, inv) and the splits' weights w[h * ldw + j] per head.
@@ -281,7 +283,7 @@ PKV_DEV void split_weights(const Args &a, int s, int kvh, int nsplit, float *w, 
             if (j >= 32) v = __ldcg(ml + j);
             const float f = weight_of(v.x, Mx);
             w[h * ldw + j] = f;
-            if (f != 0.f) den = fmaf(f, v.y, den);
+            den = fmaf(f, v.y, den);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -368,12 +370,10 @@ PKV_DEV void join_row(const Args &a, const Unit &u, Join &J) {
         for (int j = 0; j < u.nsplit; ++j) {
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + (int64_t)j * D));
             const float w = J.wj[h][j];
-            if (w != 0.f) {
-                n.x = fmaf(w, v.x, n.x);
-                n.y = fmaf(w, v.y, n.y);
-                n.z = fmaf(w, v.z, n.z);
-                n.w = fmaf(w, v.w, n.w);
-            }
+            n.x = fmaf(w, v.x, n.x);
+            n.y = fmaf(w, v.y, n.y);
+            n.z = fmaf(w, v.z, n.z);
+            n.w = fmaf(w, v.w, n.w);
         }
         const float inv = J.inv[h];
         *reinterpret_cast<uint2 *>(static_cast<char *>(a.out) + (r * D + d) * 2) =
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
 #pragma unroll 8
         for (int j = warp; j < nsplit; j += kMergeWarps) {
             const float v = o[(int64_t)j * D];
-            if (w[j] != 0.f) num = fmaf(w[j], v, num);
+            num = fmaf(w[j], v, num);
         }
         sum[warp][lane] = num;
         __syncthreads();
@@ -510,12 +510,10 @@ PKV_DEV void mass_units(const Args &a, MassShared &sm, float *wj, const int *ful
 #pragma unroll 4
                     for (int j = k; j < u.nsplit; j += K) {
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(o + (int64_t)j * D));
-                        if (w[j] != 0.f) {
-                            n.x = fmaf(w[j], v.x, n.x);
-                            n.y = fmaf(w[j], v.y, n.y);
-                            n.z = fmaf(w[j], v.z, n.z);
-                            n.w = fmaf(w[j], v.w, n.w);
-                        }
+                        n.x = fmaf(w[j], v.x, n.x);
+                        n.y = fmaf(w[j], v.y, n.y);
+                        n.z = fmaf(w[j], v.z, n.z);
+                        n.w = fmaf(w[j], v.w, n.w);
                     }
                     sm.part[threadIdx.x] = n;
                 }

@@ -178,3 +178,60 @@ def test_int4_a_warp_without_weight_in_one_head_only(hq, hkv, d, L, at, mass):
     assert abs(p[1, at] - 1) < 1e-6 and p[0, at] < 0.5
     assert cache.check_error() == 0
     cache.close()
+
+
+# ------------------------------------------------------------------------------------------ NaN
+
+# one token behind every multiple that a split may have, and rows that one warp takes
+NAN_LENS = [1, 33, 65, 97, 129, 193, 225, 257, 353, 385, 449, 481, 513, 609, 641, 769, 897, 961, 1025, 2049]
+
+
+@pytest.mark.parametrize("kv,model", [("int4", "f16"), ("int4", "bf16"), ("fp8", "f16"), ("fp8", "bf16"), ("f16", "f16"),
+                                      ("bf16", "bf16")])
+@pytest.mark.parametrize("hq,hkv", [(3, 3), (8, 2), (16, 2)])
+@pytest.mark.parametrize("lens", [NAN_LENS, [2049], [1], [40] * 200, [1, 2, 31, 32, 7], [20] * 400],
+                         ids=["ragged", "long", "one", "many", "short", "manyshort"])
+@pytest.mark.parametrize("where", ["query", "key", "value", "far value"])
+def test_nan_reaches_the_output_however_a_row_is_split(kv, model, hq, hkv, lens, where):
+    """A NaN in a query, in the last token's key, in its value, and in the value of a last token that has no weight (a
+    score of -2^11): output and mass are NaN where the formula's are, and nowhere else."""
+    d, n = 64, sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(len(lens))
+    k, v = torch.randn(2, n, hkv, d, generator=g, device="cuda")
+    q = torch.randn(len(lens), hq, d, generator=g, device="cuda")
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    last = torch.tensor(lens).cumsum(0) - 1
+    if where == "query":
+        q[:, -1, 5] = float("nan")
+    elif where == "key":
+        k[last, 0, 3] = float("nan")
+    else:
+        v[last, 0, 3] = float("nan")
+        if where == "far value":
+            k[last, :, 0] = -256.0
+    q, k, v = (x.to(TORCH[model]) for x in (q, k, v))
+    cache, tables, context = fill(k, v, kv, model, lens=lens)
+    mass = torch.zeros(len(lens), hkv, max(lens), device="cuda")
+    outs = [P.paged_decode_attention_mass(q, cache, tables, context, 1.0, mass)]
+    if kv == "int4":
+        outs.append(P.paged_decode_attention(q, cache, tables, context, 1.0))
+        outs.append(torch.empty_like(q))
+        P.paged_decode_attention_noalloc(q, cache, tables, context, 1.0, outs[-1])
+    nan = torch.zeros(q.shape, dtype=torch.bool, device="cuda").view(len(lens), hkv, -1, d)
+    bad_mass = torch.zeros(mass.shape, dtype=torch.bool, device="cuda")
+    inside = torch.arange(max(lens), device="cuda") < context[:, None]
+    if where == "query":
+        nan[:, -1, -1] = True
+        bad_mass[:, -1] = inside
+    elif where == "key":
+        nan[:, 0] = True
+        bad_mass[:, 0] = inside
+    elif kv == "int4":
+        nan[:, 0] = True                                   # the whole row reads as NaN
+    else:
+        nan[:, 0, :, 3] = True
+    for out in outs:
+        assert torch.equal(out.isnan(), nan.view_as(out)) and torch.isfinite(out[~nan.view_as(out)]).all()
+    assert torch.equal(mass.isnan(), bad_mass) and torch.isfinite(mass[~bad_mass]).all()
+    assert cache.check_error() == 0
+    cache.close()
