@@ -28,11 +28,11 @@
 //     running maximum does), so that fp16 holds it whatever the steps' magnitude.
 //   * Queries are scaled by a power of two per head so that their largest element is in [2^10, 2^11): fp16
 //     then holds them (and a sixteenth of them) to 2^-31 of that element or better.
-//   * Four warps share a unit's 32-token tiles (whose is fixed by the tile's number), each with its own ring of
-//     tiles, no barrier between warps inside a unit, and the next unit's first tiles on their way before this one
+//   * Four warps share a unit's 32-token tiles (which of a unit's four sums a tile goes to depends on its number and the
+//     call's shapes alone, and so do the bits of a row: not on the other sequences), each with its own ring of tiles, no barrier between warps inside a unit, and the next unit's first tiles on their way before this one
 //     is joined.  A tile is one run of the pool per block: one lane per block copies it, completion counted
 //     on an mbarrier (bounded waits).  One warp in turn finds the next unit, fetches its table and q and lays q
-//     out for all four, and takes a tile less.
+//     out for all four.
 //   * Two references a column.  The weights p stand against m, a running maximum of the scores that moves only when
 //     a score passes it by 2^8.  The products p s that go into the second product are multiplied by F, a power of two
 //     that puts the largest so far between 2^4 and 2^15: hi + lo hold them to 2^-22 of themselves or 2^-29 of the
@@ -188,17 +188,23 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
     Unit u = sm_unit[0];
     int *table = tb;
     bool bad = sm_bad[0] != 0;
-    int turn = 1; // the warp that prepares the next unit, and takes a tile less of this one
+    int turn = 1; // the warp that prepares the next unit
     int slot = 0; // the slot of this warp's next tile
     int nt = 0;   // this warp's tiles of the unit
-    // Tile i of this warp: where there is a next unit the others take one each before the warp whose turn it is gets
-    // its first, so it is 4 i + tile0, and one more for the others' first.
+    // Whose tiles.  Evenly, tile 4 i + warp, where no CTA has two units, and with mass or eight heads (256 ragged
+    // sequences with mass 71.9 us, 64 of eight heads 41.8).  Else the warp whose turn it is to prepare gets a tile less: the
+    // others take one each before it gets its first, by their place behind it (73.9 and 42.6; but 256 ragged ones without
+    // mass 61.1 for 62.1, 8192 rows of up to 500 tokens 80.7 for 83.1).  Also in a CTA's last unit, which prepares nothing:
+    // the four sums are kept by that place (role), so that they do not depend on which warp's turn it was.
+    const bool even = MASS || GC == 8 || (int64_t)gridDim.x == (int64_t)a.num_seqs * a.hkv * a.max_splits;
+    int role = 0;
     int tile0 = 0, first = 0;
     const char *head = nullptr;
     auto tile_of = [&](int i) { return 4 * i + tile0 + (i == 0 ? first : 0); };
-    auto start = [&](bool last) {
+    auto start = [&]() {
         const int ntiles = (u.n + T - 1) / T, r = (warp - turn + kWarps - 1) & (kWarps - 1); // 3: this warp's turn
-        if (last) {
+        role = even ? warp : r;
+        if (even) {
             nt = max(0, ntiles + 3 - warp) / 4;
             tile0 = warp;
             first = 0;
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
             to = to == ST - 1 ? 0 : to + 1;
         }
     };
-    start((int)(blockIdx.x + gridDim.x) >= nunits);
+    start();
 
     Unit prev = u;        // the last unit, if it still has to be counted
     bool pending = false;
@@ -459,17 +465,18 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
         turn = turn == kWarps - 1 ? 0 : turn + 1;
         if (g == 0) {
 #pragma unroll
-            for (int k = 0; k < NC; ++k) J.m[warp][2 * t4 + k] = m[k];
+            for (int k = 0; k < NC; ++k) J.m[role][2 * t4 + k] = m[k];
         }
         if (!MASS && threadIdx.x == 0) J.last = pending && before == prev.nsplit - 1;
         __syncthreads();
         const Unit cur = u;
+        const int me = role;
         par ^= 1;
         if (more) {
             u = sm_unit[par];
             bad = sm_bad[par] != 0;
             table = tb + par * tb_len;
-            start(un + (int)gridDim.x >= nunits);
+            start();
         }
         if constexpr (!MASS) {
             if (J.last) {
@@ -481,13 +488,13 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
             Weight w[NC];
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
-                w[k] = warp_weight(J, warp, 2 * t4 + k);
+                w[k] = warp_weight(J, me, 2 * t4 + k);
                 l[k] = row_sum(l[k]);
                 z[k] = row_sum(z[k]); // (all lanes: the columns' weights differ)
                 z[k] = w[k].w == 0.f ? 0.f : z[k] * w[k].w;
                 if (g == 0) {
-                    J.l[warp][2 * t4 + k] = l[k] * w[k].w; // (a NaN comes through a weight of 0)
-                    J.z[warp][2 * t4 + k] = z[k];
+                    J.l[me][2 * t4 + k] = l[k] * w[k].w; // (a NaN comes through a weight of 0)
+                    J.z[me][2 * t4 + k] = z[k];
                     if (warp == 0) J.M[2 * t4 + k] = w[k].M;
                 }
                 w[k].w *= power_of_two(-exponent(F[k]));
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
             if (2 * t4 < COLS) { // 16 (or 8) dims from (D / 8) g of each column
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    float *o = oacc + (warp * COLS + 2 * t4 + c) * LD + (D / 8) * g;
+                    float *o = oacc + (me * COLS + 2 * t4 + c) * LD + (D / 8) * g;
 #pragma unroll
                     for (int k = 0; k < KS; k += 4) {
                         *reinterpret_cast<float4 *>(o + k) =

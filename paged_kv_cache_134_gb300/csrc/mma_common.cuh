@@ -4,7 +4,7 @@
 //
 // A unit is (sequence, KV head, split of split_tokens tokens); persistent CTAs of four warps walk the units,
 // whole splits first.  Each warp keeps the running maximum m, the sum l and the accumulator of its tokens;
-// a unit's four are joined through shared memory in warp order.  A row's splits leave fp32 partials
+// a unit's four are joined through shared memory in a fixed order.  A row's splits leave fp32 partials
 // (m, l, o): up to kJoinSplits of them are joined by the CTA that finishes the row last (a counter per row
 // that it sets back to 0), in split order, so the result does not depend on which CTA that is; more by
 // merge_kernel, whose CTAs share them out.  With attention mass a second kernel, mass_kernel, walks the same
@@ -296,7 +296,7 @@ PKV_DEV void split_weights(const Args &a, int s, int kvh, int nsplit, float *w, 
 
 // The end of a unit, in three steps.  1: each warp stores its columns' maxima (store_max); barrier.  2: it takes
 // its weight 2^(m - max over the warps) per column and stores its sum, offsets' sum and accumulator already
-// weighted.  3 (join_unit): barrier, the four warps' values added in warp order; leaves a barrier behind.
+// weighted.  3 (join_unit): barrier, the four warps' values added in a fixed order; leaves a barrier behind.
 struct Weight {
     float M, w; // the unit's maximum of the column, this warp's weight
 };

@@ -235,3 +235,34 @@ def test_nan_reaches_the_output_however_a_row_is_split(kv, model, hq, hkv, lens,
     assert torch.equal(mass.isnan(), bad_mass) and torch.isfinite(mass[~bad_mass]).all()
     assert cache.check_error() == 0
     cache.close()
+
+
+# ------------------------------------------------------------------------------------------ other sequences, other calls
+
+@pytest.mark.parametrize("kv,model", [("int4", "f16"), ("int4", "bf16"), ("fp8", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("hq,hkv,d,most,seqs", [(32, 32, 64, 200, 120), (32, 8, 128, 300, 200), (16, 4, 64, 900, 160),
+                                                (64, 8, 128, 300, 200), (8, 8, 128, 1500, 130)])
+def test_a_row_does_not_depend_on_the_other_sequences_lengths(kv, model, hq, hkv, d, most, seqs):
+    """Several units a CTA: the other rows' lengths decide which CTA, and which of its warps, a row meets."""
+    g = torch.Generator(device="cuda").manual_seed(hq + most)
+    lens = torch.randint(1, most + 1, (seqs,), generator=torch.Generator().manual_seed(1)).tolist()
+    lens[0] = most
+    n = sum(lens)
+    k, v = torch.randn(2, n, hkv, d, generator=g, device="cuda").to(TORCH[model])
+    q = torch.randn(seqs, hq, d, generator=g, device="cuda").to(TORCH[model])
+    cache, tables, context = fill(k, v, kv, model, lens=lens, k_scale=torch.full((hkv,), 0.02, device="cuda"),
+                                  v_scale=torch.full((hkv,), 0.02, device="cuda"))
+    keep = torch.arange(0, seqs, 3, device="cuda")
+    runs = []
+    for i in range(3):
+        now = context if i == 0 else (context // (4 * i)).int()
+        now[keep] = context[keep]
+        mass = torch.zeros(seqs, hkv, most, device="cuda")
+        out = [P.paged_decode_attention_mass(q, cache, tables, now, d ** -0.5, mass)[keep], mass[keep]]
+        if kv == "int4":
+            out.append(P.paged_decode_attention(q, cache, tables, now, d ** -0.5)[keep])
+        runs.append(out)
+    for out in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out, runs[0]))
+    assert cache.check_error() == 0
+    cache.close()
