@@ -190,7 +190,8 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
  * launch unless one sequence needs more; larger batches run as consecutive launches), one per stream
  * and one per stream capture, allocated by the first call that needs it or more of it, also during a
  * capture, and kept until the cache is destroyed: calls on different streams, and captured graphs,
- * may overlap. */
+ * may overlap.  Executables instantiated from one capture share its workspace: they must not run at the
+ * same time. */
 int paged_decode_attention_mass(const void *q, pkv_cache_t cache, const int32_t *block_tables,
                                 int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_q_heads,
                                 float scale, float decay, float *attn_mass, int64_t mass_len, void *out,
@@ -233,10 +234,13 @@ int paged_kv_evict(pkv_cache_t cache, const int32_t *block_tables, int max_block
  * A call whose partials for one launch do not fit (n x Hq x ceil(max_blocks_per_seq / split
  * blocks) x (D + 2) floats > 16 MiB, n = min(num_seqs, sequences per launch); with the default
  * 256-token splits, e.g., 32 sequences x 32 heads x 4096-token tables need 9 MB) returns PKV_EINVAL
- * with the sizes in pkv_last_error().  Every call shares the array: calls whose work can overlap
+ * with the sizes in pkv_last_error().  PKV_INT4 caches: rows of several splits take (D + 2) floats a split,
+ * and the splits are those of paged_decode_attention: at most max(2 * 608 + n x Hkv, n x Hkv x ceil(table
+ * tokens / 1024)) x (Hq / Hkv) x (D + 2) floats for a launch of n sequences on 152 SMs.
+ * Every call shares the array: calls whose work can overlap
  * on the GPU (different streams, or different host threads) race on it and must be serialised by
  * the caller.  Nothing in the array has to start at zero; each call writes every partial before it
- * reads it. */
+ * reads it, and clears the counters it joins by: what such a race damages ends with the calls in it. */
 int paged_decode_attention_noalloc(const void *q, pkv_cache_t cache, const int32_t *block_tables,
                                    int max_blocks_per_seq, const int32_t *context_lens, int num_seqs,
                                    int num_q_heads, float scale, void *out, void *stream);

@@ -120,6 +120,7 @@ int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorks
         ws->floats = b.bytes / (int64_t)sizeof(float);
         ws->done = reinterpret_cast<int *>(reinterpret_cast<char *>(b.p) + b.bytes);
         ws->counters = workspace_counters(c);
+        ws->clear = capture != 0;
         return PKV_OK;
     };
     std::lock_guard<std::mutex> lk(c->ws_mu);

@@ -21,7 +21,7 @@
 // 16 MiB of fp32 partials, held by every device on which a cache was created until the process exits.
 constexpr int64_t kScratchFloats = int64_t(4) << 20;
 static __device__ __align__(256) float g_decode_scratch[kScratchFloats];
-// the 4-bit decode's counters of finished units (zero between launches; 32768 rows, more join in a second launch)
+// the 4-bit decode's counters of finished units (cleared by every call that counts; 32768 rows, more join in a second launch)
 constexpr int64_t kScratchCounters = 32768;
 static __device__ int g_decode_done[kScratchCounters];
 
@@ -83,7 +83,7 @@ extern "C" int paged_decode_attention_noalloc(const void *q, pkv_cache_t c, cons
         PkvWorkspace scratch;
         if (dev < kMaxDevices) {
             std::lock_guard<std::mutex> lk(g_scratch_mu);
-            scratch = PkvWorkspace{g_scratch_ptr[dev], kScratchFloats, g_done_ptr[dev], kScratchCounters};
+            scratch = PkvWorkspace{g_scratch_ptr[dev], kScratchFloats, g_done_ptr[dev], kScratchCounters, true};
         }
         if (!scratch.p)
             return pkv_fail(PKV_EINVAL,

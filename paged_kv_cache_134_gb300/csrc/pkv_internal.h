@@ -154,6 +154,7 @@ struct PkvWorkspace {
     int64_t floats = 0;
     int *done = nullptr; // counters, all 0 whenever no launch uses them
     int64_t counters = 0;
+    bool clear = false; // ... unless launches met: to be cleared first
 };
 // fixed: a workspace to use instead of the stream's own, or NULL
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st);

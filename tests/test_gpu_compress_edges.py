@@ -266,3 +266,34 @@ def test_a_row_does_not_depend_on_the_other_sequences_lengths(kv, model, hq, hkv
         assert all(torch.equal(a, b) for a, b in zip(out, runs[0]))
     assert cache.check_error() == 0
     cache.close()
+
+
+@pytest.mark.parametrize("seqs,hkv,eager", [(6, 2, 2),     # many splits: joined by a second launch, without counters
+                                            (40, 8, 1)])   # at most 16: by the row's last CTA
+def test_int4_counters_are_cleared_where_calls_may_have_met(seqs, hkv, eager):
+    """The counters that a row's last CTA joins by: a call on the library's fixed scratch, and a captured one, clear them first
+    (a launch more), so that nothing an earlier call left there matters; a stream's own workspace is its calls' alone."""
+    lens, hq, d = [3000] * (seqs - 1) + [1], 16, 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = torch.randn(2, sum(lens), hkv, d, generator=g, device="cuda")
+    q = torch.randn(len(lens), hq, d, generator=g, device="cuda").half()
+    cache, tables, context = fill(k, v, "int4", "f16", lens=lens)
+    outs = [torch.empty_like(q) for _ in range(3)]
+
+    def launches(call):
+        before = P.kernel_launches()
+        call()
+        return P.kernel_launches() - before
+
+    assert launches(lambda: P.paged_decode_attention(q, cache, tables, context, 0.1, out=outs[0])) == eager
+    assert launches(lambda: P.paged_decode_attention_noalloc(q, cache, tables, context, 0.1, outs[1])) == 2
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        assert launches(lambda: P.paged_decode_attention(q, cache, tables, context, 0.1, out=outs[2])) == 2
+    for _ in range(3):
+        outs[2].zero_()
+        graph.replay()
+        assert torch.equal(outs[2], outs[0]) and torch.equal(outs[1], outs[0])
+    assert cache.check_error() == 0
+    cache.close()
