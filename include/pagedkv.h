@@ -97,8 +97,8 @@ int kv_cache_view(pkv_cache_t cache, void **base, int64_t strides_elems[5], int6
 /* Pre-size the decode split-K workspace for up to max_seqs x max_q_heads rows and tables
  * of max_blocks_per_seq entries, so that later decode calls allocate nothing (a batch larger
  * than one launch takes needs only one launch's rows: the launches share the workspace).  PKV_INT4
- * caches keep a workspace per stream (see paged_decode_attention_mass): the reserved one goes to the
- * first stream or capture that needs one; reserve once per stream. */
+ * caches keep a workspace per stream (see paged_decode_attention_mass): each call here adds one, which
+ * goes to the first stream or capture that needs one; reserve once per stream and per capture. */
 int kv_cache_reserve(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq);
 
 /* Synchronise the device, return the device error word's bits in *device_code and clear

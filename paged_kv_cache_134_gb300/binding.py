@@ -204,6 +204,8 @@ class KVCache:
         _check(lib().kv_cache_set_scales(self.handle, _ptr(k_scale), _ptr(v_scale), _stream()))
 
     def reserve(self, max_seqs: int, max_q_heads: int, max_blocks_per_seq: int):
+        """Allocate the decode's workspace for calls of at most these sizes (4-bit caches: one more workspace a call,
+        for one stream or stream capture)."""
         _check(lib().kv_cache_reserve(self.handle, int(max_seqs), int(max_q_heads), int(max_blocks_per_seq)))
 
     def check_error(self) -> int:

@@ -358,8 +358,6 @@ int kv_cache_reserve(pkv_cache_t c, int max_seqs, int max_q_heads, int max_block
         if (floats <= 0) return PKV_OK;
         pkv_cache::StreamWs b{0, 0, true, nullptr, (floats * (int64_t)sizeof(float) + 255) / 256 * 256};
         std::lock_guard<std::mutex> lk(c->ws_mu);
-        for (auto &have : c->stream_ws)
-            if (have.spare && have.bytes >= b.bytes) return PKV_OK;
         if (!room_for_one_more(c->stream_ws)) return pkv_fail(PKV_ENOMEM, "out of host memory");
         cudaError_t e = allocate_workspace(c, b.bytes, &b.p);
         if (e != cudaSuccess)

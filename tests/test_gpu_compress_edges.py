@@ -297,3 +297,50 @@ def test_int4_counters_are_cleared_where_calls_may_have_met(seqs, hkv, eager):
         assert torch.equal(outs[2], outs[0]) and torch.equal(outs[1], outs[0])
     assert cache.check_error() == 0
     cache.close()
+
+
+# ------------------------------------------------------------------------------------------ workspaces
+
+def device_memory_taken():
+    """Device memory in use that torch does not hold."""
+    torch.cuda.synchronize()
+    free, total = torch.cuda.mem_get_info()
+    return total - free - torch.cuda.memory_reserved()
+
+
+def ragged_decode(lens, kv="int4", hq=16, hkv=8, d=128, seed=5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k, v = torch.randn(2, sum(lens), hkv, d, generator=g, device="cuda").half()
+    q = torch.randn(len(lens), hq, d, generator=g, device="cuda").half()
+    return (q, *fill(k, v, kv, "f16", lens=lens, k_scale=torch.full((hkv,), 0.02, device="cuda"),
+                     v_scale=torch.full((hkv,), 0.02, device="cuda")))
+
+
+def test_every_reserve_adds_a_workspace():
+    """Two streams and a capture after three reserves: none of their calls allocates."""
+    q, cache, tables, context = ragged_decode([3000] * 39 + [1])
+    want = torch.empty_like(q)
+    P.paged_decode_attention_noalloc(q, cache, tables, context, 0.1, want)   # loads the kernels
+    outs = [torch.empty_like(q) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                                            # (what a capture allocates for itself)
+        outs[0].fill_(0)
+    del graph
+    for _ in range(3):
+        cache.reserve(40, 16, tables.shape[1])
+    before = device_memory_taken()
+    for s, out in zip(streams, outs):
+        with torch.cuda.stream(s):
+            P.paged_decode_attention(q, cache, tables, context, 0.1, out=out)
+    assert device_memory_taken() == before
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        P.paged_decode_attention(q, cache, tables, context, 0.1, out=outs[2])
+    after = device_memory_taken()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert after - before < 1 << 20          # (a graph's own nodes; a workspace of these sizes takes 2 MB)
+    assert all(torch.equal(out, want) for out in outs)
+    assert cache.check_error() == 0
+    cache.close()
