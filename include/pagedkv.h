@@ -101,6 +101,13 @@ int kv_cache_view(pkv_cache_t cache, void **base, int64_t strides_elems[5], int6
  * goes to the first stream or capture that needs one; reserve once per stream and per capture. */
 int kv_cache_reserve(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq);
 
+/* Add a workspace for paged_decode_attention_mass calls (any cache type) of at most max_seqs sequences,
+ * max_q_heads query heads, tables of max_blocks_per_seq entries and mass rows of max_mass_len tokens.
+ * It goes to the first stream or capture that needs one, whose later calls of these sizes then allocate
+ * nothing; call once per stream and per capture. */
+int kv_cache_reserve_mass(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq,
+                          int64_t max_mass_len);
+
 /* Synchronise the device, return the device error word's bits in *device_code and clear
  * it.  Returns PKV_EDEVICE when any bit was set, PKV_OK otherwise. */
 int kv_cache_check_error(pkv_cache_t cache, int *device_code);

@@ -50,6 +50,7 @@ def lib() -> ctypes.CDLL:
         L.kv_cache_set_scales.argtypes = [vp, vp, vp, vp]
         L.kv_cache_view.argtypes = [vp, ctypes.POINTER(vp), ctypes.POINTER(i64), ctypes.POINTER(i64)]
         L.kv_cache_reserve.argtypes = [vp, i32, i32, i32]
+        L.kv_cache_reserve_mass.argtypes = [vp, i32, i32, i32, i64]
         L.kv_cache_check_error.argtypes = [vp, ctypes.POINTER(i32)]
         L.pkv_last_error.restype = ctypes.c_char_p
         L.paged_slot_mapping.argtypes = [vp, i32, i32, vp, vp, i64, i32, vp, vp]
@@ -207,6 +208,12 @@ class KVCache:
         """Allocate the decode's workspace for calls of at most these sizes (4-bit caches: one more workspace a call,
         for one stream or stream capture)."""
         _check(lib().kv_cache_reserve(self.handle, int(max_seqs), int(max_q_heads), int(max_blocks_per_seq)))
+
+    def reserve_mass(self, max_seqs: int, max_q_heads: int, max_blocks_per_seq: int, max_mass_len: int):
+        """Allocate a workspace for paged_decode_attention_mass calls of at most these sizes (any cache type), for one
+        stream or stream capture."""
+        _check(lib().kv_cache_reserve_mass(self.handle, int(max_seqs), int(max_q_heads), int(max_blocks_per_seq),
+                                           int(max_mass_len)))
 
     def check_error(self) -> int:
         """Synchronise and return (and clear) the device error bits; 0 when clean."""

@@ -99,6 +99,20 @@ cudaError_t allocate_workspace(const pkv_cache *c, int64_t bytes, float **p) {
     if (e != cudaSuccess) cudaGetLastError();
     return e;
 }
+
+// One more workspace for the first stream or capture that needs one of at most its size.
+int add_spare(pkv_cache *c, int64_t floats) {
+    if (floats <= 0) return PKV_OK;
+    pkv_cache::StreamWs b{0, 0, true, nullptr, (floats * (int64_t)sizeof(float) + 255) / 256 * 256};
+    std::lock_guard<std::mutex> lk(c->ws_mu);
+    if (!room_for_one_more(c->stream_ws)) return pkv_fail(PKV_ENOMEM, "out of host memory");
+    cudaError_t e = allocate_workspace(c, b.bytes, &b.p);
+    if (e != cudaSuccess)
+        return pkv_fail(e == cudaErrorMemoryAllocation ? PKV_ENOMEM : PKV_ECUDA, "decode workspace of %lld bytes: %s",
+                        (long long)b.bytes, cudaGetErrorString(e));
+    c->stream_ws.push_back(b);
+    return PKV_OK;
+}
 } // namespace
 
 int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorkspace *ws) {
@@ -351,21 +365,8 @@ int kv_cache_reserve(pkv_cache_t c, int max_seqs, int max_q_heads, int max_block
     if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
     if (max_seqs < 0 || max_q_heads < 0 || max_blocks_per_seq < 0) return pkv_fail(PKV_EINVAL, "negative size");
     if (int r = check_device(c)) return r;
-    if (c->kv_dtype == PKV_INT4) {
-        const int64_t floats = max_q_heads > 0 && max_seqs > 0
-                                   ? decode_mma_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq)
-                                   : 0;
-        if (floats <= 0) return PKV_OK;
-        pkv_cache::StreamWs b{0, 0, true, nullptr, (floats * (int64_t)sizeof(float) + 255) / 256 * 256};
-        std::lock_guard<std::mutex> lk(c->ws_mu);
-        if (!room_for_one_more(c->stream_ws)) return pkv_fail(PKV_ENOMEM, "out of host memory");
-        cudaError_t e = allocate_workspace(c, b.bytes, &b.p);
-        if (e != cudaSuccess)
-            return pkv_fail(e == cudaErrorMemoryAllocation ? PKV_ENOMEM : PKV_ECUDA,
-                            "decode workspace of %lld bytes: %s", (long long)b.bytes, cudaGetErrorString(e));
-        c->stream_ws.push_back(b);
-        return PKV_OK;
-    }
+    if (c->kv_dtype == PKV_INT4)
+        return add_spare(c, decode_mma_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq, -1));
     const int bps = decode_split_blocks(c);
     const int max_splits = (max_blocks_per_seq + bps - 1) / bps;
     // consecutive launches of one call share the workspace: one launch's rows are enough
@@ -373,6 +374,14 @@ int kv_cache_reserve(pkv_cache_t c, int max_seqs, int max_q_heads, int max_block
     if (max_q_heads > 0 && max_q_heads % c->num_kv_heads == 0 && supported_group(max_q_heads / c->num_kv_heads))
         rows = std::min(rows, decode_seqs_per_launch(c, max_q_heads / c->num_kv_heads));
     return ensure_workspace(c, decode_workspace_floats(c, rows, max_q_heads, max_splits));
+}
+
+int kv_cache_reserve_mass(pkv_cache_t c, int max_seqs, int max_q_heads, int max_blocks_per_seq, int64_t max_mass_len) {
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (max_seqs < 0 || max_q_heads < 0 || max_blocks_per_seq < 0 || max_mass_len < 0)
+        return pkv_fail(PKV_EINVAL, "negative size");
+    if (int r = check_device(c)) return r;
+    return add_spare(c, decode_mma_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq, max_mass_len));
 }
 
 int kv_cache_check_error(pkv_cache_t c, int *device_code) {

@@ -15,6 +15,11 @@ int64_t workers_of(const pkv_cache *c, int group) {
     return (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? (few ? 3 : 4) : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
 }
 
+// sequences of a launch: over 16-bit caches the list of more would leave room for one CTA an SM instead of two
+int most_seqs(const pkv_cache *c) {
+    return c->kv_dtype == PKV_INT4 || c->kv_dtype == PKV_FP8_E4M3 ? pkv_mma::kMaxSeqs : 384;
+}
+
 // What one launch of at most `seqs` sequences looks like.
 struct Plan {
     int64_t cap;    // tokens a sequence may have
@@ -29,8 +34,7 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     if (mass) p->cap = std::min(p->cap, mass_len);
     const bool i4 = c->kv_dtype == PKV_INT4;
     const int64_t workers = workers_of(c, hq / c->num_kv_heads);
-    // sequences of a launch: over 16-bit caches the list of more would leave room for one CTA an SM instead of two
-    const int most = i4 || c->kv_dtype == PKV_FP8_E4M3 ? pkv_mma::kMaxSeqs : 384;
+    const int most = most_seqs(c);
     const int64_t rows = (int64_t)std::min(num_seqs, most) * c->num_kv_heads;
     // Short rows by a warp each, where two of three speak for it: the mass (which saves a launch), up to four heads (a
     // warp's work), more rows than CTAs.  4-bit, D = 128: 8 rows of four heads and 16 tokens, 5.4 us with mass
@@ -109,14 +113,20 @@ cudaError_t run(const pkv_cache *c, const pkv_mma::Args &a, bool mass, bool merg
 
 } // namespace
 
-int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks) {
-    // the most that any call of at most these sizes asks for: its units are at most two waves and one more a row, or
-    // those of the largest split
-    const int64_t rows = (int64_t)std::min(num_seqs, pkv_mma::kMaxSeqs) * c->num_kv_heads, group = hq / c->num_kv_heads;
-    const int64_t cap = (int64_t)max_blocks * c->block_size;
+int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len) {
+    // units of one launch: at most two waves and one more a row, or those of the largest split; with mass the scores
+    // besides.  2 GB, unless one sequence (of at most 1024 splits) needs more.
+    if (num_seqs <= 0 || hq <= 0) return 0;
+    const int64_t seqs = std::min(num_seqs, most_seqs(c)), rows = seqs * c->num_kv_heads;
+    int64_t cap = (int64_t)max_blocks * c->block_size, scores = 0; // of a sequence
+    if (mass_len >= 0) {
+        cap = std::min(cap, mass_len);
+        scores = hq * cap;
+    }
     const int64_t units = std::max(rows * ((cap + kMaxSplit - 1) / kMaxSplit), 2 * workers_of(c, 1) + rows);
-    const int64_t row = std::max<int64_t>(group, 1) * (c->head_dim + 2);
-    return std::min(units * row, std::max<int64_t>((int64_t)1 << 29, 1024 * row * c->num_kv_heads));
+    const int64_t row = std::max<int64_t>(hq / c->num_kv_heads, 1) * (c->head_dim + 2);
+    return std::min(units * row + seqs * scores,
+                    std::max<int64_t>((int64_t)1 << 29, 1024 * row * c->num_kv_heads + scores));
 }
 
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st) {

@@ -158,7 +158,8 @@ struct PkvWorkspace {
 };
 // fixed: a workspace to use instead of the stream's own, or NULL
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st);
-int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks); // 4-bit, without mass
+// the most that a call of at most these sizes asks for (mass_len -1: without mass)
+int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len);
 int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorkspace *ws); // api.cu
 
 struct EvictLaunch {

@@ -344,3 +344,44 @@ def test_every_reserve_adds_a_workspace():
     assert all(torch.equal(out, want) for out in outs)
     assert cache.check_error() == 0
     cache.close()
+
+
+@pytest.mark.parametrize("kv", ["f16", "fp8", "int4"])
+def test_reserved_mass_workspace_covers_smaller_calls(kv):
+    """No mass call of at most the reserved sizes allocates, whichever way its rows are split."""
+    seqs, width, hkv, d, bs = 450, 700, 2, 128, 8
+    q = torch.randn(seqs, 16, d, device="cuda").half()
+    tables = torch.zeros(seqs, width, dtype=torch.int32, device="cuda")
+    lens = torch.ones(seqs, dtype=torch.int32, device="cuda")
+    mass = torch.zeros(seqs * hkv * width * bs, device="cuda")
+    for reserved in (False, True):                         # (the first cache's calls load the kernels)
+        cache = P.KVCache(1, bs, hkv, d, kv_dtype=kv, model_dtype="f16")
+        if reserved:
+            cache.reserve_mass(seqs, 16, width, width * bs)
+        before = device_memory_taken()
+        for n in (450, 1, 2, 3, 20, 101, 390):
+            for w in (700, 5, 17, 62, 333, 512):
+                for hq in (16, 2, 4):
+                    for t in (w * bs, w * bs // 3):
+                        P.paged_decode_attention_mass(q[:n, :hq].contiguous(), cache, tables[:n, :w].contiguous(),
+                                                      lens[:n].contiguous(), 1.0,
+                                                      mass[: n * hkv * t].view(n, hkv, t))
+        grown = device_memory_taken() - before
+        assert grown == 0 if reserved else grown > 0
+        assert cache.check_error() == 0
+        cache.close()
+
+
+def test_reserved_mass_workspace_is_used():
+    q, cache, tables, context = ragged_decode([3000] * 7 + [1], kv="f16", hq=8, hkv=2)
+    mass = [torch.zeros(8, 2, 3000, device="cuda") for _ in range(2)]
+    want = P.paged_decode_attention_mass(q, cache, tables, context, 0.1, mass[0])
+    cache.reserve_mass(8, 8, tables.shape[1], 3000)
+    before = device_memory_taken()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        out = P.paged_decode_attention_mass(q, cache, tables, context, 0.1, mass[1])
+    assert device_memory_taken() == before
+    assert torch.equal(out, want) and torch.equal(mass[0], mass[1])
+    assert P.binding.lib().kv_cache_reserve_mass(cache.handle, -1, 8, 1, 1) == -1
+    assert cache.check_error() == 0
+    cache.close()
