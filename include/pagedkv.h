@@ -108,6 +108,11 @@ int kv_cache_reserve(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_b
 int kv_cache_reserve_mass(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq,
                           int64_t max_mass_len);
 
+/* Synchronise the device and free the workspaces of all streams, whether reserved or grown on demand; with
+ * graphs != 0 also those of all captures, whose graphs must not be launched again.  Later calls allocate
+ * anew.  Not to be called while a stream is being captured. */
+int kv_cache_release_workspaces(pkv_cache_t cache, int graphs);
+
 /* Synchronise the device, return the device error word's bits in *device_code and clear
  * it.  Returns PKV_EDEVICE when any bit was set, PKV_OK otherwise. */
 int kv_cache_check_error(pkv_cache_t cache, int *device_code);
@@ -196,8 +201,8 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
  * Workspace: fp32 partials and scores (num_q_heads x tokens x 4 bytes per sequence, at most 2 GB a
  * launch unless one sequence needs more; larger batches run as consecutive launches), one per stream
  * and one per stream capture, allocated by the first call that needs it or more of it, also during a
- * capture, and kept until the cache is destroyed: calls on different streams, and captured graphs,
- * may overlap.  Executables instantiated from one capture share its workspace: they must not run at the
+ * capture, and kept until kv_cache_release_workspaces or the cache's end (a stream's that was outgrown is freed
+ * at once, which waits for the stream): calls on different streams, and captured graphs, may overlap.  Executables instantiated from one capture share its workspace: they must not run at the
  * same time. */
 int paged_decode_attention_mass(const void *q, pkv_cache_t cache, const int32_t *block_tables,
                                 int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_q_heads,

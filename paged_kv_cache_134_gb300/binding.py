@@ -51,6 +51,7 @@ def lib() -> ctypes.CDLL:
         L.kv_cache_view.argtypes = [vp, ctypes.POINTER(vp), ctypes.POINTER(i64), ctypes.POINTER(i64)]
         L.kv_cache_reserve.argtypes = [vp, i32, i32, i32]
         L.kv_cache_reserve_mass.argtypes = [vp, i32, i32, i32, i64]
+        L.kv_cache_release_workspaces.argtypes = [vp, i32]
         L.kv_cache_check_error.argtypes = [vp, ctypes.POINTER(i32)]
         L.pkv_last_error.restype = ctypes.c_char_p
         L.paged_slot_mapping.argtypes = [vp, i32, i32, vp, vp, i64, i32, vp, vp]
@@ -214,6 +215,11 @@ class KVCache:
         stream or stream capture."""
         _check(lib().kv_cache_reserve_mass(self.handle, int(max_seqs), int(max_q_heads), int(max_blocks_per_seq),
                                            int(max_mass_len)))
+
+    def release_workspaces(self, graphs: bool = False):
+        """Synchronise and free the decode workspaces of every stream; with ``graphs`` also those of stream captures,
+        whose graphs must not be replayed again."""
+        _check(lib().kv_cache_release_workspaces(self.handle, int(graphs)))
 
     def check_error(self) -> int:
         """Synchronise and return (and clear) the device error bits; 0 when clean."""

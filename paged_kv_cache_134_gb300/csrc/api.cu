@@ -80,11 +80,17 @@ bool room_for_one_more(std::vector<pkv_cache::StreamWs> &v) {
 
 int64_t workspace_counters(const pkv_cache *c) { return (int64_t)1024 * c->num_kv_heads; } // rows of a launch
 
-// A workspace of `bytes` for partials and its zeroed counters, not tied to any stream's work: also while a
-// stream is captured (an allocation is no part of the capture).
-cudaError_t allocate_workspace(const pkv_cache *c, int64_t bytes, float **p) {
+// Allocating and freeing are no part of a capture that this thread, or another, may be in.
+struct RelaxedCapture {
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    cudaThreadExchangeStreamCaptureMode(&mode);
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// A workspace of `bytes` for partials and its zeroed counters, not tied to any stream's work: also while a
+// stream is captured.
+cudaError_t allocate_workspace(const pkv_cache *c, int64_t bytes, float **p) {
+    RelaxedCapture relaxed;
     const int64_t tail = workspace_counters(c) * (int64_t)sizeof(int);
     cudaStream_t own = nullptr;
     cudaError_t e = cudaMalloc(reinterpret_cast<void **>(p), (size_t)(bytes + tail));
@@ -95,7 +101,6 @@ cudaError_t allocate_workspace(const pkv_cache *c, int64_t bytes, float **p) {
         if (own) cudaStreamDestroy(own);
         if (e != cudaSuccess) cudaFree(*p);
     }
-    cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) cudaGetLastError();
     return e;
 }
@@ -137,23 +142,42 @@ int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorks
         ws->clear = capture != 0;
         return PKV_OK;
     };
-    std::lock_guard<std::mutex> lk(c->ws_mu);
+    auto &all = c->stream_ws;
+    auto mine = [&](const pkv_cache::StreamWs &b) { return !b.spare && b.stream == stream && b.capture == capture; };
     int64_t most = 0;
-    for (auto &b : c->stream_ws) {
-        if (b.spare || b.stream != stream || b.capture != capture) continue;
+    for (auto &b : all) {
+        if (!mine(b)) continue;
         if (b.bytes >= bytes) return use(b);
         most = std::max(most, b.bytes);
     }
-    for (auto &b : c->stream_ws) {
+    // A spare one, or a new one.  What it replaces stays where it belongs to a capture (the graph's earlier nodes use it);
+    // else it is freed once the stream's work, which alone uses it, is done.
+    auto replace = [&](const pkv_cache::StreamWs &by) {
+        if (capture || !most) return;
+        RelaxedCapture relaxed;
+        if (cudaStreamSynchronize(st) != cudaSuccess) {
+            cudaGetLastError(); // (it stays for kv_cache_release_workspaces)
+            return;
+        }
+        for (auto &b : all) {
+            if (!mine(b) || b.p == by.p) continue;
+            cudaFree(b.p);
+            b.p = nullptr;
+        }
+        all.erase(std::remove_if(all.begin(), all.end(), [](const pkv_cache::StreamWs &b) { return !b.p; }), all.end());
+    };
+    for (auto &b : all) {
         if (!b.spare || b.bytes < bytes) continue;
         b.spare = false;
         b.stream = stream;
         b.capture = capture;
-        return use(b);
+        const pkv_cache::StreamWs taken = b;
+        replace(taken);
+        return use(taken);
     }
-    if (!room_for_one_more(c->stream_ws)) return pkv_fail(PKV_ENOMEM, "out of host memory");
-    // at least twice the last one: the buffers left behind add up to less than the one in use
-    pkv_cache::StreamWs b{stream, capture, false, nullptr, std::max(bytes, 2 * most)};
+    if (!room_for_one_more(all)) return pkv_fail(PKV_ENOMEM, "out of host memory");
+    // half as much again as the last one, so that growing step by step is rare and what a capture outgrew stays little
+    pkv_cache::StreamWs b{stream, capture, false, nullptr, std::max(bytes, (most + most / 2) / 256 * 256)};
     e = allocate_workspace(c, b.bytes, &b.p);
     if (e != cudaSuccess && b.bytes > bytes) {
         b.bytes = bytes;
@@ -162,7 +186,8 @@ int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorks
     if (e != cudaSuccess)
         return pkv_fail(e == cudaErrorMemoryAllocation ? PKV_ENOMEM : PKV_ECUDA, "decode workspace of %lld bytes: %s",
                         (long long)bytes, cudaGetErrorString(e));
-    c->stream_ws.push_back(b);
+    all.push_back(b);
+    replace(b);
     return use(b);
 }
 
@@ -382,6 +407,22 @@ int kv_cache_reserve_mass(pkv_cache_t c, int max_seqs, int max_q_heads, int max_
         return pkv_fail(PKV_EINVAL, "negative size");
     if (int r = check_device(c)) return r;
     return add_spare(c, decode_mma_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq, max_mass_len));
+}
+
+int kv_cache_release_workspaces(pkv_cache_t c, int graphs) {
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (int r = check_device(c)) return r;
+    std::lock_guard<std::mutex> lk(c->ws_mu);
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return pkv_cuda_fail(e, "cudaDeviceSynchronize");
+    for (auto &b : c->stream_ws) {
+        if (b.capture && !graphs) continue;
+        cudaFree(b.p);
+        b.p = nullptr;
+    }
+    auto &all = c->stream_ws;
+    all.erase(std::remove_if(all.begin(), all.end(), [](const pkv_cache::StreamWs &b) { return !b.p; }), all.end());
+    return PKV_OK;
 }
 
 int kv_cache_check_error(pkv_cache_t c, int *device_code) {

@@ -133,6 +133,10 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace 
     Plan p;
     if (!plan_for(c, d.num_seqs, d.num_q_heads, d.max_blocks, d.mass_len, &p))
         return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this decode takes", d.max_blocks);
+    // a batch larger than one launch takes runs in consecutive launches that share the workspace: each
+    // waits for the one before it.  Another host thread's call on this stream may use the same workspace, or replace
+    // it: none of its own launches comes between this call's.
+    std::lock_guard<std::mutex> lk(c->ws_mu);
     PkvWorkspace ws;
     if (!fixed) {
         if (int r = pkv_stream_workspace(c, st, p.floats, &ws)) return r;
@@ -173,10 +177,6 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace 
     a.max_splits = p.max_splits;
     a.qk_scale_log2 = d.scale * 1.4426950408889634f;
     a.decay = d.decay;
-    // a batch larger than one launch takes runs in consecutive launches that share the workspace: each
-    // waits for the one before it.  Another host thread's call on this stream may use the same workspace: no launch of
-    // its own comes between this call's.
-    std::lock_guard<std::mutex> lk(c->ws_mu);
     for (int s0 = 0; s0 < d.num_seqs; s0 += p.seqs) {
         const int n = std::min(p.seqs, d.num_seqs - s0);
         const int64_t rows = (int64_t)n * d.num_q_heads * (p.max_splits > 1 || mass ? p.max_splits : 0);

@@ -34,8 +34,8 @@ struct pkv_cache {
     int num_sms = 0;
     // workspaces of the decode of 4-bit caches and of the decode with attention mass, one per stream
     // (and one per stream capture): work of one stream is ordered, so its calls share one, while
-    // concurrent streams and captured graphs never meet in one.  A buffer that was outgrown stays until
-    // the cache is destroyed, because a captured graph may still use it.
+    // concurrent streams and captured graphs never meet in one.  A capture's outgrown buffer stays, because its graph's
+    // earlier nodes use it.
     struct StreamWs {
         unsigned long long stream, capture;
         bool spare; // from kv_cache_reserve, not yet any stream's
@@ -160,7 +160,9 @@ struct PkvWorkspace {
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st);
 // the most that a call of at most these sizes asks for (mass_len -1: without mass)
 int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len);
-int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorkspace *ws); // api.cu
+// The caller holds ws_mu until it has launched what uses the workspace (another thread's call on the stream may replace
+// it) (api.cu).
+int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorkspace *ws);
 
 struct EvictLaunch {
     const int32_t *tables, *dst_tables, *lens;

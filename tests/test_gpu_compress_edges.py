@@ -1,6 +1,7 @@
 """GPU tests of the 4-bit cache and the decode with attention mass where they can lose precision, drop a NaN or keep
 state between calls: against 64-bit references, with bounds derived beside them."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -383,5 +384,81 @@ def test_reserved_mass_workspace_is_used():
     assert device_memory_taken() == before
     assert torch.equal(out, want) and torch.equal(mass[0], mass[1])
     assert P.binding.lib().kv_cache_reserve_mass(cache.handle, -1, 8, 1, 1) == -1
+    assert cache.check_error() == 0
+    cache.close()
+
+
+@pytest.mark.parametrize("kv", ["int4", "f16"])
+def test_workspaces_do_not_pile_up(kv):
+    """A stream keeps one workspace however often it was outgrown, and those of streams and captures are given back."""
+    q, cache, tables, context = ragged_decode([3000] * 64, kv=kv, hq=8, hkv=2)
+    mass = torch.zeros(64, 2, 3000, device="cuda")
+    out = torch.empty_like(q)
+
+    def call(n):
+        P.paged_decode_attention_mass(q[:n], cache, tables[:n], context[:n], 0.1, mass[:n], out=out[:n], decay=0.0)
+
+    call(64)
+    want = (out.clone(), mass.clone())
+    torch.cuda.synchronize()
+    cache.release_workspaces()
+    empty = device_memory_taken()
+    call(64)
+    one = device_memory_taken() - empty
+    assert one >= 6 << 20                                  # the scores of 64 x 8 x 3000 alone
+    cache.release_workspaces()
+    assert device_memory_taken() == empty
+    for n in range(1, 65, 3):                              # outgrown 21 times
+        call(n)
+    call(64)
+    assert device_memory_taken() - empty <= 2 * one
+    assert all(torch.equal(a, b) for a, b in zip((out, mass), want))
+    graphs = []
+    for _ in range(3):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(5)
+            call(64)
+        graphs.append(g)
+    cache.release_workspaces()                             # leaves the graphs theirs
+    out.zero_(), mass.fill_(2.0)
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((out, mass), want))
+    held = device_memory_taken() - empty
+    graphs.clear()
+    del g
+    cache.release_workspaces(graphs=True)
+    assert device_memory_taken() - empty <= held - 3 * one
+    call(64)                                               # and the cache goes on
+    assert all(torch.equal(a, b) for a, b in zip((out, mass), want))
+    assert cache.check_error() == 0
+    cache.close()
+
+
+def test_two_host_threads_grow_one_streams_workspace():
+    """A call that replaces the stream's workspace does not take it from another thread's call that has yet to launch."""
+    q, cache, tables, context = ragged_decode([2000] * 24, hq=8, hkv=2)
+    want = P.paged_decode_attention(q, cache, tables, context, 0.1)
+    sizes = [[1, 3, 7, 15, 24], [2, 5, 9, 18, 24]]
+    first = {n: P.paged_decode_attention(q[:n], cache, tables[:n], context[:n], 0.1) for s in sizes for n in s}
+    outs = [[torch.empty_like(q[:n]) for n in s * 10] for s in sizes]
+    torch.cuda.synchronize()
+    cache.release_workspaces()
+
+    def run(sizes, outs):
+        for n, out in zip(sizes * 10, outs):
+            P.paged_decode_attention(q[:n], cache, tables[:n], context[:n], 0.1, out=out)
+
+    threads = [threading.Thread(target=run, args=a) for a in zip(sizes, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for s, out in zip(sizes, outs):
+        assert all(torch.equal(o, first[n]) for n, o in zip(s * 10, out))
+    assert torch.equal(first[24], want)
     assert cache.check_error() == 0
     cache.close()
