@@ -29,13 +29,13 @@ def new_cache(w_like, num_blocks, block_size, hkv, d, kv_dtype, model_dtype, k_s
         cache.set_scales(dev(k_scale), dev(v_scale))
     bits = W.NAN_BITS[kv_dtype]
     pool = cache.pool_elems()
-    pool.fill_(bits if kv_dtype == "fp8" else int(np.array([bits], np.uint16).view(np.int16)[0]))
+    pool.fill_(bits if kv_dtype in ("fp8", "int4") else int(np.array([bits], np.uint16).view(np.int16)[0]))
     return cache
 
 
 def pool_numpy(cache) -> np.ndarray:
     p = cache.pool_elems().cpu().numpy()
-    return p if cache.kv_dtype == "fp8" else p.view(np.uint16)
+    return p if cache.kv_dtype in ("fp8", "int4") else p.view(np.uint16)
 
 
 def fill_cache(cache, w):

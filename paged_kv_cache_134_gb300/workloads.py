@@ -44,11 +44,17 @@ import numpy as np
 import torch
 
 # dtype names used throughout (the C ABI uses the same order)
-F16, BF16, FP8 = "f16", "bf16", "fp8"
-DTYPE_CODE = {F16: 0, BF16: 1, FP8: 2}
+F16, BF16, FP8, INT4 = "f16", "bf16", "fp8", "int4"
+DTYPE_CODE = {F16: 0, BF16: 1, FP8: 2, INT4: 3}
 ELEM_BYTES = {F16: 2, BF16: 2, FP8: 1}
-# quiet-NaN bit patterns used to poison every cache slot that no token owns
-NAN_BITS = {F16: 0x7E00, BF16: 0x7FC0, FP8: 0x7F}
+# quiet-NaN bit patterns used to poison every cache slot that no token owns (4-bit caches: every byte, so that the
+# rows' steps and offsets are NaN)
+NAN_BITS = {F16: 0x7E00, BF16: 0x7FC0, FP8: 0x7F, INT4: 0xFF}
+
+
+def kv_row_bytes(kv_dtype: str, head_dim: int) -> int:
+    """Bytes the cache holds for one token's K or V of one head (4-bit: codes, step and offset)."""
+    return head_dim // 2 + 4 if kv_dtype == INT4 else head_dim * ELEM_BYTES[kv_dtype]
 
 
 class PoolExhausted(RuntimeError):
@@ -177,8 +183,8 @@ class DecodeWorkload:
         return int(self.block_tables.shape[1])
 
     def kv_read_bytes(self) -> int:
-        """Algorithmic K+V bytes one decode pass reads: sum(L+1) * Hkv * D * elt * 2."""
-        return int(self.decode_lens.sum()) * self.num_kv_heads * self.head_dim * ELEM_BYTES[self.kv_dtype] * 2
+        """Algorithmic K+V bytes one decode pass reads: sum(L+1) * Hkv * row bytes * 2."""
+        return int(self.decode_lens.sum()) * self.num_kv_heads * kv_row_bytes(self.kv_dtype, self.head_dim) * 2
 
 
 @dataclasses.dataclass
@@ -537,7 +543,7 @@ def stress(bs: int = 16, kv_dtype: str = BF16, seed: int = 1005, num_seqs: int =
 def small_decode(name, lens, *, hq, hkv, d, bs, kv_dtype=F16, model_dtype=None, seed=7,
                  num_blocks=None, pool_factor=1.5, placement_seed=None) -> DecodeWorkload:
     """Arbitrary small decode case for edge-case tests."""
-    md = model_dtype or (kv_dtype if kv_dtype != FP8 else BF16)
+    md = model_dtype or (kv_dtype if kv_dtype not in (FP8, INT4) else BF16)
     return _decode_from_lens(name, lens, hq=hq, hkv=hkv, d=d, bs=bs, kv_dtype=kv_dtype,
                              model_dtype=md, seed=seed, num_blocks=num_blocks, pool_factor=pool_factor,
                              placement_seed=placement_seed)

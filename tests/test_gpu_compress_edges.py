@@ -9,6 +9,7 @@ import torch
 
 import compress_ref as R
 import paged_kv_cache_134_gb300 as P
+from paged_kv_cache_134_gb300 import runner, workloads as W
 
 pytestmark = pytest.mark.gpu
 
@@ -462,3 +463,39 @@ def test_two_host_threads_grow_one_streams_workspace():
     assert torch.equal(first[24], want)
     assert cache.check_error() == 0
     cache.close()
+
+
+# ------------------------------------------------------------------------------------------ step helpers
+
+@pytest.mark.parametrize("model", ["f16", "bf16"])
+@pytest.mark.parametrize("fused", [True, False])
+def test_the_decode_step_takes_a_4_bit_cache(model, fused):
+    w = W.small_decode("int4", [0, 1, 37, 300], hq=8, hkv=2, d=128, bs=16, kv_dtype="int4", model_dtype=model)
+    got = runner.run_decode(w, fused=fused)
+    assert got["err"] == 0 and got["pool"].dtype == np.uint8
+    assert got["pool"].size == w.num_blocks * 2 * 16 * (128 + 8)
+    q = R.to64(runner.dev(w.q, TORCH[model]))
+    for s in range(4):
+        k, v = (R.to64(runner.dev(x, TORCH[model])) for x in W.logical_kv(w, s))
+        (ck, sk, lk), (cv, sv, lv) = R.quantise4(k, model), R.quantise4(v, model)
+        scale = float(w.scale)
+        ref, _, pv, big = R.attention(q[s], R.values4(ck, sk, lk), R.values4(cv, sv, lv), scale)
+        rel = R.relative_weight_error(big) + R.code_alignment(128, q[s], sk, scale)
+        tol = R.HALF_STEP[model] * np.abs(ref) * 1.001 + rel * pv + 2.0 ** -13 * float(sv.max()) + 2.0 ** -24
+        assert np.all(np.abs(got["out"][s] - ref) <= tol)
+
+
+def test_the_prefill_step_takes_a_4_bit_cache():
+    w = W.prefill(lengths=[5, 40, 1], heads=4, kv_heads=2, d=64, dtype="f16", kv_dtype="int4")
+    plain = W.prefill(lengths=[5, 40, 1], heads=4, kv_heads=2, d=64, dtype="f16")
+    got, want = runner.run_prefill(w, keep_cache=True), runner.run_prefill(plain)
+    assert got["err"] == 0 and np.array_equal(got["out"], want["out"])   # the attention reads the packed k and v
+    pos = np.concatenate([np.arange(n) for n in w.lengths])
+    seq = np.repeat(np.arange(3), w.lengths)
+    slots = torch.from_numpy(w.block_tables[seq, pos // 16].astype(np.int64) * 16 + pos % 16).cuda()
+    k, v = P.paged_kv_gather(got["cache"], slots)
+    for x, back in ((w.k, k), (w.v, v)):
+        x = runner.dev(x, torch.float16)
+        want = torch.from_numpy(R.values4(*R.quantise4(R.to64(x), "f16")).astype(np.float32)).half()
+        assert torch.equal(back.cpu(), want)
+    got["cache"].close()

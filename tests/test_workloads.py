@@ -129,3 +129,11 @@ def test_fp8_scales_cover_amax():
     w = W.stress(bs=16, kv_dtype="fp8", num_seqs=6)
     k = np.abs(W.bits_to_float(np.concatenate([w.fill_k, w.new_k]), "bf16")).max(axis=(0, 2))
     assert np.all(k / w.k_scale <= 448.0 * (1 + 1e-6))
+
+
+def test_int4_workloads_count_codes_steps_and_offsets():
+    w = W.small_decode("i4", [3, 20], hq=4, hkv=2, d=128, bs=16, kv_dtype="int4")
+    assert w.model_dtype == "bf16" and w.k_scale is None
+    assert w.kv_read_bytes() == (4 + 21) * 2 * 2 * 68
+    assert W.kv_row_bytes("int4", 64) == 36 and W.kv_row_bytes("fp8", 64) == 64 and W.kv_row_bytes("f16", 64) == 128
+    assert W.small_decode("f", [3], hq=1, hkv=1, d=64, bs=8).kv_read_bytes() == 4 * 2 * 128
