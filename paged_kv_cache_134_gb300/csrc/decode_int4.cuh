@@ -53,14 +53,16 @@
 
 namespace pkv_mma {
 
-template <int D>
+template <int D, int GC>
 struct Geo4 {
     static constexpr int kOct = 8 * (D + 8);  // 8 tokens' K, V, (s, z), as in the pool
     static constexpr int kTile = 32;          // tokens
     static constexpr int kBytes = 4 * kOct;
-    // four CTAs per SM, two tiles of 4 KB a warp on their way: with three CTAs of three the 7B batch below takes 62 us
+    // four CTAs per SM, two tiles of 4 KB a warp on their way: with three CTAs of three the 7B batch below takes 62 us.
+    // With eight heads the four warps' accumulators leave shared memory for three, and so 168 registers a thread (64
+    // sequences of eight heads a group: 41.1 us; held to 128 registers, which spill, 43.5).
     static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int kCtas = 4;
+    static constexpr int kCtas = D == 128 && GC == 8 ? 3 : 4;
 };
 
 // Nibbles 0..3 of each 16-bit half of w -> four fp16 pairs (low half, high half): c 2^-21 for nibbles 0
@@ -77,8 +79,8 @@ PKV_DEV float power_of_two(int e) { return e < -126 ? 0.f : __uint_as_float((uin
 
 // GC: 1 query head per KV head, 4 (two or four), 8
 template <int D, int MT, int GC, bool MASS>
-__global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(const Args a) {
-    using G_ = Geo4<D>;
+__global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kernel(const Args a) {
+    using G_ = Geo4<D, GC>;
     constexpr int KS = D / 16;             // k steps of the first product = m tiles of the second
     constexpr int ST = G_::kStages, T = G_::kTile;
     constexpr int NC = GC == 1 ? 1 : 2;    // columns of a thread that count
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D>::kCtas) decode_int4_kernel(c
 
 template <int D, int MT, int GC, bool MASS>
 cudaError_t launch_int4_t(const Args &a, int sms, cudaStream_t st) {
-    using G_ = Geo4<D>;
+    using G_ = Geo4<D, GC>;
     static std::atomic<bool> have[64];
     auto kern = decode_int4_kernel<D, MT, GC, MASS>;
     const size_t smem = (size_t)kWarps * G_::kStages * G_::kBytes + kWarps * GC * (D + 4) * sizeof(float) +

@@ -11,7 +11,7 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // resident CTAs of the kernels of units
 int64_t workers_of(const pkv_cache *c, int group) {
-    const bool few = c->head_dim == 128 && group == 8; // their accumulators leave room for three
+    const bool few = c->head_dim == 128 && group == 8; // Geo4::kCtas
     return (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? (few ? 3 : 4) : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
 }
 
