@@ -261,12 +261,18 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
         const float lo_part = GC != 8 && t4 >= 2 ? 1.f : 0.f;
 
         for (int i = 0; i < nt; ++i) {
+            const bool was_alive = alive;
             if (alive && !mbar_wait(&bars[slot], (phase >> slot) & 1)) {
                 set_error(a.err, PKV_DEVERR_TIMEOUT);
                 alive = false;
             }
             alive = __all_sync(0xffffffffu, alive);
-            if (!alive) break;
+            if (!alive) {
+                if (was_alive) // this warp's copies still on their way: its CTA must not end before them
+                    for (int j = 0, at = slot; j < ST && i + j < nt; ++j, at = at == ST - 1 ? 0 : at + 1)
+                        mbar_wait(&bars[at], (phase >> at) & 1);
+                break;
+            }
             phase ^= 1u << slot;
             const uint32_t tile = ring_u + slot * G_::kBytes;
             const uint32_t at_k = tile + g * (D / 2) + t4 * (D / 8), at_p = tile + 8 * D + g * 4;
