@@ -344,8 +344,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
             float n_[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int k = 0; k < NC; ++k) n_[k] = fmaxf(fmaxf(x[0][k], x[1][k]), fmaxf(x[2][k], x[3][k]));
-            float ns = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-            bool up = ns > lim_s;
+            bool up = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])) > lim_s;
 #pragma unroll
             for (int k = 0; k < NC; ++k) up = up || n_[k] > lim[k];
             if (__any_sync(0xffffffffu, up)) {
@@ -354,7 +353,6 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
                 for (int o = 4; o < 32; o <<= 1) {
 #pragma unroll
                     for (int k = 0; k < NC; ++k) n_[k] = fmaxf(n_[k], __shfl_xor_sync(0xffffffffu, n_[k], o));
-                    ns = fmaxf(ns, __shfl_xor_sync(0xffffffffu, ns, o));
                 }
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
@@ -383,9 +381,6 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
                         to = e > 100 || e + q >= 15 ? min(to, e) : e;
                         f[k] = fast_exp2(whole - d) * power_of_two(to - e);
                     }
-                    const int room = min(0, 125 - exponent(ns) - to); // F times any step stays finite
-                    to += room;
-                    f[k] *= power_of_two(room);
                     F[k] = power_of_two(to);
                     m[k] = n_[k];
                     lim[k] = m[k] + 8.f;
@@ -414,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
                     const float p = fast_exp2(x[r][k] - mu[k]);
                     l[k] += p;
                     z[k] = fmaf(p, vz[r], z[k]);
-                    w[k] = p * (F[k] * vs[r]);
+                    w[k] = p * F[k] * vs[r]; // (in this order: F times a step may overflow where p is 0)
                 }
                 if constexpr (GC == 8) {
                     b[r] = movmatrix(pack_rz<PKV_F16>(w[0], w[1]));

@@ -499,3 +499,29 @@ def test_the_prefill_step_takes_a_4_bit_cache():
         want = torch.from_numpy(R.values4(*R.quantise4(R.to64(x), "f16")).astype(np.float32)).half()
         assert torch.equal(back.cpu(), want)
     got["cache"].close()
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (16, 2)])
+@pytest.mark.parametrize("at", [40, 5])
+def test_int4_a_great_range_without_any_weight(hq, hkv, at):
+    """All the weight on a token of range 2^-80; the others, of range 2^80, have none (scores 400 below): the output is
+    that token's row, to half a step and 2^-12 of a step (the codes' products)."""
+    L, d, model = 300, 128, "bf16"
+    g = torch.Generator(device="cuda").manual_seed(at)
+    k, v = torch.randn(2, L, hkv, d, generator=g, device="cuda")
+    q = torch.randn(1, hq, d, generator=g, device="cuda")
+    q[..., 0], k[..., 0] = 50.0, 0.0
+    k[at, :, 0] = 8.0
+    v *= torch.where(torch.arange(L, device="cuda") == at, 2.0 ** -80, 2.0 ** 80)[:, None, None]
+    q = q.to(TORCH[model])
+    cache, tables, lens = fill(k, v, "int4", model)
+    quantised = R.quantise4(R.to64(v.to(TORCH[model])), model)
+    want, step = np.repeat(R.values4(*quantised)[at], hq // hkv, 0), np.repeat(quantised[1][at], hq // hkv, 0)[:, None]
+    tol = (R.HALF_STEP[model] * np.abs(want) + 2.0 ** -12 * step) * 1.001
+    m = torch.zeros(1, hkv, L, device="cuda")
+    for out in (P.paged_decode_attention(q, cache, tables, lens, 1.0),
+                P.paged_decode_attention_mass(q, cache, tables, lens, 1.0, m)):
+        assert np.all(np.abs(R.to64(out[0]) - want) <= tol)
+    assert torch.equal(m[0, :, at], torch.full((hkv,), hq / hkv, device="cuda"))
+    assert cache.check_error() == 0
+    cache.close()
