@@ -150,13 +150,16 @@ int paged_slot_mapping(const int32_t *block_tables, int num_rows, int max_blocks
  * element i reads as s * code_i + z.  A row that holds a NaN or an infinity, or whose range
  * overflows fp32, reads as NaN.  Negative slots are padding and
  * skipped; slots >= num_blocks*block_size are skipped and set PKV_DEVERR_SLOT.  Two
- * tokens with the same slot in one call: which one lands is unspecified. */
+ * tokens with the same slot in one call: which one lands is unspecified, 16 bytes by 16 bytes (a 4-bit
+ * row may hold one's codes with the other's step and offset). */
 int paged_kv_append(pkv_cache_t cache, const void *k, const void *v, const int64_t *slot_mapping,
                     int64_t num_tokens, void *stream);
 
 /* Rows read back: for each token j, k[j] and v[j] ([num_tokens][num_kv_heads][head_dim], model
  * dtype) := K and V at slot_mapping[j]: the bits of a 16-bit cache, code * scale[head] of an FP8
- * cache, step * code + offset of a PKV_INT4 cache, rounded once to the model dtype.  A negative slot
+ * cache, step * code + offset of a PKV_INT4 cache, rounded once to the model dtype (an fp16 row that spans
+ * nearly all of the type may so read as infinity at its top, where the rounded step reaches past it; the
+ * decode reads it unrounded).  A negative slot
  * gives zeros; one >= num_blocks*block_size gives zeros and sets PKV_DEVERR_SLOT. */
 int paged_kv_gather(pkv_cache_t cache, const int64_t *slot_mapping, int64_t num_tokens, void *k, void *v,
                     void *stream);
@@ -183,8 +186,9 @@ int paged_kv_append_at(pkv_cache_t cache, const void *k, const void *v, const in
  * fewer for the tensor-core kernel of grouped-query heads, whose shared memory holds fewer) runs
  * as consecutive launches of that many sequences on the stream, sharing one workspace sized for
  * a launch.  The workspace grows (cudaMalloc) on demand unless kv_cache_reserve covered the call.
- * PKV_INT4 caches: split boundaries depend on L_s, num_seqs and max_blocks_per_seq; the workspace is
- * the stream's own (see paged_decode_attention_mass). */
+ * PKV_INT4 caches: split boundaries depend on L_s, num_seqs and max_blocks_per_seq (so a row's bits do not
+ * depend on the other lengths); NaN as in paged_decode_attention_mass; the workspace is the stream's own
+ * (see there). */
 int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *block_tables, int max_blocks_per_seq,
                            const int32_t *context_lens, int num_seqs, int num_q_heads, float scale, void *out,
                            void *stream);
@@ -195,7 +199,9 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
  * row s belonging to row s of the tables; a token's entry has to be 0 before its first step.  decay in
  * [0, 1] (1 sums, less lets old mass fade).  Every cache type; out as paged_decode_attention (to its
  * tolerance, not bit for bit).  A length above mass_len or the tables' tokens sets PKV_DEVERR_LENGTH and
- * is cut to that.  Two launches, the second for the mass (one where no sequence can have more than 32
+ * is cut to that.  A NaN in q or in a K row makes the head's output and its group's mass row NaN, one in V
+ * the output where its row has it (a 4-bit row: everywhere); an infinity in V gives an infinity or NaN; a row
+ * of which no token has a score above -infinity gives zeros.  Two launches, the second for the mass (one where no sequence can have more than 32
  * tokens); the products take the softmax weights as hi + lo 16-bit pairs, all else is fp32; sums run in
  * a fixed order, so equal calls give equal bits.
  * Workspace: fp32 partials and scores (num_q_heads x tokens x 4 bytes per sequence, at most 2 GB a

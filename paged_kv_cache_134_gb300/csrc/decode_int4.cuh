@@ -41,10 +41,10 @@
 //     1e-2 of the output).  Both move about once a unit (m by 2^4, F from 2^8: 62.7 us for the 61.6 of 256 ragged rows).
 //   * Scores, softmax statistics, sums and accumulators are fp32.
 //
-// Measured: 32 sequences of up to 4096 tokens, 32 heads (7B batch), 268 MB in 58 us, 4.6 TB/s; 256 ragged ones of up to
-// 8192, four heads to a KV head, 237 MB in 60 us, 3.9 TB/s; one of 131071 tokens, 143 MB in 38 us.  Copies alone take 48 us
-// of the first, arithmetic on data in L2 56: four warps a scheduler, as many as 128 registers allow, hide the two and
-// the dependent chain of a tile behind one another only in part.
+// Measured: 32 sequences of up to 4096 tokens, 32 heads (7B batch), 268 MB in 59 us, 4.5 TB/s; 256 ragged ones of up to
+// 8192, four heads to a KV head, 237 MB in 61 us, 3.9 TB/s; one of 131071 tokens, 143 MB in 37 us; 64 of up to 4096, eight
+// heads to a KV head, 40 us.  Copies alone take 48 us of the first, arithmetic on data in L2 nearly all of it: four warps a
+// scheduler, as many as 128 registers allow, hide the two and the dependent chain of a tile behind one another only in part.
 #pragma once
 
 #include <type_traits>

@@ -50,7 +50,7 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     }
     // Tokens of a split, a function of the call's shapes, never of the lengths (a result does not change with the other
     // sequences' lengths).  More than four waves of the largest: those, which have the least fixed costs (4-bit, 32
-    // sequences of up to 4096 tokens and 256 of up to 8192: 58 and 60 us; 864 takes 3 more of both, 512 9 and 15).
+    // sequences of up to 4096 tokens and 256 of up to 8192: 59 and 61 us; 864 takes 3 more of both, 512 9 and 15).
     // Else the one with the least time at the table's full width by a model of it: waves of units, each of
     // so many rounds of the warps' tiles and a fixed part, and what joins the splits.  4-bit: rounds of 2.1 us, 1.2 a
     // unit, 3 for the last CTA's join, 5 for a merge launch; where a CTA has several units one warp prepares the next and

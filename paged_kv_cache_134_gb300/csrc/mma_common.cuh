@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
 // After a decode that stored its scores: for every unit the mass of its tokens, and its share of the row's outputs
 // where the row has several splits.  Persistent, the decode's list of units.  Bound by latency (the scores are mostly in L2):
 // a unit waits once for its scores and the row's statistics together.  256 ragged sequences, 1.6 M (token, KV head)
-// pairs of four heads: 15 us behind the decode's 60; a CTA needs 64 registers, more of them an SM were no faster.
+// pairs of four heads: 13 us behind the decode's 61; a CTA needs 64 registers, more of them an SM were no faster.
 struct MassShared {
     float M[8], inv[8];
     float4 part[kThreads];

@@ -525,3 +525,46 @@ def test_int4_a_great_range_without_any_weight(hq, hkv, at):
     assert torch.equal(m[0, :, at], torch.full((hkv,), hq / hkv, device="cuda"))
     assert cache.check_error() == 0
     cache.close()
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (16, 2)])
+@pytest.mark.parametrize("lens", [[1, 5, 32], [1, 40, 700, 2100]], ids=["short", "long"])
+def test_infinities_in_a_16_bit_cache(kv, hq, hkv, lens):
+    """A score of -infinity takes no weight, a row of nothing else is zeros; +infinity gives NaN; an infinity in V something
+    that is not finite, in its element alone."""
+    d, n = 64, sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k, v = torch.randn(2, n, hkv, d, generator=g, device="cuda")
+    q = torch.randn(len(lens), hq, d, generator=g, device="cuda").to(TORCH[kv])
+    q[..., 0] = 1.0
+    inf, last = float("inf"), torch.tensor(lens).cumsum(0) - 1
+    for where in ("low", "all low", "high", "value"):
+        kk, vv = k.clone(), v.clone()
+        if where == "low":
+            kk[last[1:], :, 0] = -inf                      # (the row of one token keeps it)
+        elif where == "all low":
+            kk[..., 0] = -inf
+        elif where == "high":
+            kk[last, :, 0] = inf
+        else:
+            vv[last, :, 3] = inf
+        cache, tables, context = fill(kk, vv, kv, kv, lens=lens)
+        mass = torch.full((len(lens), hkv, max(lens)), 0.5, device="cuda")
+        out = P.paged_decode_attention_mass(q, cache, tables, context, 0.1, mass).float()
+        inside = (torch.arange(max(lens), device="cuda") < context[:, None])[:, None].expand_as(mass)
+        if where == "low":
+            assert torch.isfinite(out).all() and torch.isfinite(mass).all()
+            end = mass[torch.arange(1, len(lens)), :, torch.tensor(lens[1:]) - 1]
+            assert torch.equal(end, torch.full_like(end, 0.5))
+            total = (mass - 0.5).sum(-1)
+            assert torch.allclose(total, torch.full_like(total, hq / hkv), rtol=1e-3)
+        elif where == "all low":
+            assert not out.any() and torch.equal(mass, torch.full_like(mass, 0.5))
+        elif where == "high":
+            assert out.isnan().all() and torch.equal(mass.isnan(), inside)
+        else:
+            assert not torch.isfinite(out[..., 3]).any() and torch.isfinite(mass).all()
+            assert torch.isfinite(torch.cat([out[..., :3], out[..., 4:]], -1)).all()
+        assert cache.check_error() == 0
+        cache.close()
