@@ -201,15 +201,15 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
  * tolerance, not bit for bit).  A length above mass_len or the tables' tokens sets PKV_DEVERR_LENGTH and
  * is cut to that.  A NaN in q or in a K row makes the head's output and its group's mass row NaN, one in V
  * the output where its row has it (a 4-bit row: everywhere); an infinity in V gives an infinity or NaN; a row
- * of which no token has a score above -infinity gives zeros.  Two launches, the second for the mass (one where no sequence can have more than 32
- * tokens); the products take the softmax weights as hi + lo 16-bit pairs, all else is fp32; sums run in
+ * of which no token has a score above -infinity gives zeros.  Two launches, the second for the mass (one
+ * where no sequence can have more than 32 tokens); the products take the softmax weights as hi + lo 16-bit pairs, all else is fp32; sums run in
  * a fixed order, so equal calls give equal bits.
  * Workspace: fp32 partials and scores (num_q_heads x tokens x 4 bytes per sequence, at most 2 GB a
  * launch unless one sequence needs more; larger batches run as consecutive launches), one per stream
  * and one per stream capture, allocated by the first call that needs it or more of it, also during a
  * capture, and kept until kv_cache_release_workspaces or the cache's end (a stream's that was outgrown is freed
- * at once, which waits for the stream): calls on different streams, and captured graphs, may overlap.  Executables instantiated from one capture share its workspace: they must not run at the
- * same time. */
+ * at once, which waits for the stream): calls on different streams, and captured graphs, may overlap.
+ * Executables instantiated from one capture share its workspace: they must not run at the same time. */
 int paged_decode_attention_mass(const void *q, pkv_cache_t cache, const int32_t *block_tables,
                                 int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_q_heads,
                                 float scale, float decay, float *attn_mass, int64_t mass_len, void *out,

@@ -21,18 +21,17 @@
 //     16 tokens at a time), P^T: B operand (16 tokens x 8 heads).  The order of the summed index is free, so
 //     each thread takes whole pieces of a row as they lie, and q is laid out once per unit in the same
 //     order.  P goes from the first product's layout to the second's by movmatrix.
-//   * The second product takes P as fp16 hi + lo parts (2^-20 relative), so that rounding P does not
+//   * The second product takes P as fp16 hi + lo parts (2^-22 relative), so that rounding P does not
 //     show: with up to four heads the lo part uses the four columns of B that are free anyway; with eight it
 //     takes a second product.  One head alone leaves every other column of its thread's two empty.
-//   * p_t s_t is divided by a power of two A >= every s_t seen (A moves with the accumulator like the
-//     running maximum does), so that fp16 holds it whatever the steps' magnitude.
 //   * Queries are scaled by a power of two per head so that their largest element is in [2^10, 2^11): fp16
 //     then holds them (and a sixteenth of them) to 2^-31 of that element or better.
-//   * Four warps share a unit's 32-token tiles (which of a unit's four sums a tile goes to depends on its number and the
-//     call's shapes alone, and so do the bits of a row: not on the other sequences), each with its own ring of tiles, no barrier between warps inside a unit, and the next unit's first tiles on their way before this one
-//     is joined.  A tile is one run of the pool per block: one lane per block copies it, completion counted
-//     on an mbarrier (bounded waits).  One warp in turn finds the next unit, fetches its table and q and lays q
-//     out for all four.
+//   * Four warps share a unit's 32-token tiles, each with its own ring of tiles, no barrier between warps inside a
+//     unit, and the next unit's first tiles on their way before this one is joined.  Which of the unit's four sums
+//     a tile goes to depends on its number and the call's shapes alone, and so do the bits of a row: not on the other
+//     sequences.  A tile is one run of the pool per block: one lane per block copies it, completion counted on an
+//     mbarrier (bounded waits).  One warp in turn finds the next unit, fetches its table and q and lays q out for
+//     all four.
 //   * Two references a column.  The weights p stand against m, a running maximum of the scores that moves only when
 //     a score passes it by 2^8.  The products p s that go into the second product are multiplied by F, a power of two
 //     that puts the largest so far between 2^4 and 2^15: hi + lo hold them to 2^-22 of themselves or 2^-29 of the
@@ -371,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
                     const float d = m[k] == n_[k] ? 0.f : fminf(n_[k] - m[k], 300.f), whole = floorf(d);
-                    const float back = fast_exp2(-d);
+                    const float part = fast_exp2(whole - d), back = part * power_of_two(-(int)whole);
                     l[k] *= back;
                     z[k] *= back;
                     // F against the new m, but for the fraction of the move, and what the tile asks for
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
                     int to = min(4 - q, 100);
                     if (m[k] != -INFINITY) {
                         to = e > 100 || e + q >= 15 ? min(to, e) : e;
-                        f[k] = fast_exp2(whole - d) * power_of_two(to - e);
+                        f[k] = part * power_of_two(to - e);
                     }
                     F[k] = power_of_two(to);
                     m[k] = n_[k];
@@ -398,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
             }
             // ---- P^T as the second product's B operand: minus the hi parts (columns 0..3) and the lo parts (4..7), or
             // for eight heads hi and lo one after the other.  hi is w cut to 11 bits; the rest, which is exact, is rounded
-            // to nearest: cut as well, every weight would be low, and over zero-mean rows, whose sums of codes and of
-            // offsets cancel, 131071 tokens' outputs were off by 3e-4.
+            // to nearest: cut as well, every weight would be low, and over zero-mean rows the sums of codes and of
+            // offsets cancel (131071 tokens: 1.2e-3 of the bf16 output off an fp32 sum, for 5e-4).
             uint32_t b[4], bl_[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
