@@ -108,9 +108,10 @@ int kv_cache_reserve(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_b
 int kv_cache_reserve_mass(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq,
                           int64_t max_mass_len);
 
-/* Synchronise the device and free the workspaces of all streams, whether reserved or grown on demand; with
- * graphs != 0 also those of all captures, whose graphs must not be launched again.  Later calls allocate
- * anew.  Not to be called while a stream is being captured. */
+/* Synchronise the device and free the workspaces that paged_decode_attention_mass and the decode of
+ * PKV_INT4 caches keep for streams, whether reserved or grown on demand; with graphs != 0 also those of
+ * captures, whose graphs must not be launched again.  Later calls allocate anew.  Not to be called while a
+ * stream is being captured. */
 int kv_cache_release_workspaces(pkv_cache_t cache, int graphs);
 
 /* Synchronise the device, return the device error word's bits in *device_code and clear

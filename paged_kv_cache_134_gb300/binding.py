@@ -217,8 +217,8 @@ class KVCache:
                                            int(max_mass_len)))
 
     def release_workspaces(self, graphs: bool = False):
-        """Synchronise and free the decode workspaces of every stream; with ``graphs`` also those of stream captures,
-        whose graphs must not be replayed again."""
+        """Synchronise and free the workspaces that the mass decode and the decode of 4-bit caches keep for streams; with
+        ``graphs`` also those of stream captures, whose graphs must not be replayed again."""
         _check(lib().kv_cache_release_workspaces(self.handle, int(graphs)))
 
     def check_error(self) -> int:

@@ -166,12 +166,14 @@ int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorks
         }
         all.erase(std::remove_if(all.begin(), all.end(), [](const pkv_cache::StreamWs &b) { return !b.p; }), all.end());
     };
-    for (auto &b : all) {
-        if (!b.spare || b.bytes < bytes) continue;
-        b.spare = false;
-        b.stream = stream;
-        b.capture = capture;
-        const pkv_cache::StreamWs taken = b;
+    pkv_cache::StreamWs *fit = nullptr; // the smallest: a decode leaves a larger one to the mass call it was reserved for
+    for (auto &b : all)
+        if (b.spare && b.bytes >= bytes && (!fit || b.bytes < fit->bytes)) fit = &b;
+    if (fit) {
+        fit->spare = false;
+        fit->stream = stream;
+        fit->capture = capture;
+        const pkv_cache::StreamWs taken = *fit;
         replace(taken);
         return use(taken);
     }

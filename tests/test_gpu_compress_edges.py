@@ -568,3 +568,25 @@ def test_infinities_in_a_16_bit_cache(kv, hq, hkv, lens):
             assert torch.isfinite(torch.cat([out[..., :3], out[..., 4:]], -1)).all()
         assert cache.check_error() == 0
         cache.close()
+
+
+@pytest.mark.parametrize("mass_first", [True, False])
+def test_a_decode_leaves_the_larger_workspace_to_the_mass_call(mass_first):
+    q, cache, tables, context = ragged_decode([3000] * 39 + [1])
+    mass = torch.zeros(40, 8, 3000, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(2)]
+    P.paged_decode_attention(q, cache, tables, context, 0.1, out=outs[0])            # loads the kernels
+    P.paged_decode_attention_mass(q, cache, tables, context, 0.1, mass, out=outs[1])
+    cache.release_workspaces()
+    reserve = [lambda: cache.reserve(40, 16, tables.shape[1]), lambda: cache.reserve_mass(40, 16, tables.shape[1], 3000)]
+    for i in (1, 0) if mass_first else (0, 1):
+        reserve[i]()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    before = device_memory_taken()
+    with torch.cuda.stream(streams[0]):
+        P.paged_decode_attention(q, cache, tables, context, 0.1, out=outs[0])
+    with torch.cuda.stream(streams[1]):
+        P.paged_decode_attention_mass(q, cache, tables, context, 0.1, mass, out=outs[1])
+    assert device_memory_taken() == before
+    assert cache.check_error() == 0
+    cache.close()
