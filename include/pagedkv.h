@@ -174,6 +174,34 @@ int paged_kv_append_at(pkv_cache_t cache, const void *k, const void *v, const in
                        int max_blocks_per_seq, const int32_t *seq_ids, const int32_t *positions, int64_t num_tokens,
                        int64_t *slot_mapping, void *stream);
 
+/* Rotary position embedding: element pairs of the first rotary_dim elements of a head, (i, i + rotary_dim / 2)
+ * or, interleaved, (2 i, 2 i + 1), turned by position * inv_freq[i] radians; cosine and sine times gain (1,
+ * or the temperature that scaling for long contexts brings).  rotary_dim: a multiple of 16, 16 .. head_dim.
+ * inv_freq is a HOST array of rotary_dim / 2 finite numbers, read before the call returns. */
+typedef struct {
+    int rotary_dim;
+    int interleaved;
+    float gain;
+    const double *inv_freq;
+} pkv_rotary_t;
+
+/* paged_kv_append_at for the rows as the projections leave them: for each token j, q and k head rows are normed
+ * (x * rsqrt(mean(x^2) + eps) * weight, where the weight, [head_dim] in the model dtype, is not NULL), rotated, and
+ * rounded once to the model dtype; fp32 in between, angles exact to 2^-25 of a turn at every position.  q goes to q_out;
+ * k and v to the slot of (block_tables, seq_ids[j], positions[j]) as paged_kv_append stores the rounded rows.
+ * rotary_positions, when not NULL, are the positions of the rotation (after paged_kv_evict a token's place in the cache
+ * and its position differ); may be negative.  A token without a slot is not stored, but its q_out is written.
+ * q: [num_tokens][num_q_heads][head_dim], k, v: [num_tokens][num_kv_heads][head_dim], model dtype, tokens the
+ * given strides (elements, multiples of 8) apart, heads contiguous: slices of one projection's output.  q_out may be
+ * q itself with the same stride, and must not overlap the inputs otherwise.  num_q_heads 0 (q, q_out NULL): k and v alone.
+ * slot_mapping, when not NULL, receives the slots.  Slots twice in one call: as for paged_kv_append. */
+int paged_kv_append_rotary(pkv_cache_t cache, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, int num_q_heads, const int32_t *block_tables, int num_rows,
+                           int max_blocks_per_seq, const int32_t *seq_ids, const int32_t *positions,
+                           const int32_t *rotary_positions, int64_t num_tokens, const pkv_rotary_t *rotary,
+                           const void *q_weight, const void *k_weight, float eps, void *q_out, int64_t q_out_stride,
+                           int64_t *slot_mapping, void *stream);
+
 /* Paged decode attention (2kiu.com section 2.3: walk the block table, mask the tail
  * block by the true length; section 3.3: prefix blocks are read per sequence):
  *   out[s][h] = sum_{t < L_s} softmax_t(scale * q[s][h] . K_t) V_t,  L_s = context_lens[s],

@@ -14,6 +14,8 @@ from typing import Optional
 
 import torch
 
+from .rotary import Rotary
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libpagedkv.so")
 
@@ -57,6 +59,8 @@ def lib() -> ctypes.CDLL:
         L.paged_slot_mapping.argtypes = [vp, i32, i32, vp, vp, i64, i32, vp, vp]
         L.paged_kv_append.argtypes = [vp, vp, vp, vp, i64, vp]
         L.paged_kv_append_at.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i64, vp, vp]
+        L.paged_kv_append_rotary.argtypes = [vp, vp, i64, vp, i64, vp, i64, i32, vp, i32, i32, vp, vp, vp, i64, vp, vp, vp,
+                                             ctypes.c_float, vp, i64, vp, vp]
         L.paged_decode_attention.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp]
         L.paged_decode_attention_noalloc.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp]
         L.paged_kv_gather.argtypes = [vp, vp, i64, vp, vp, vp]
@@ -311,6 +315,80 @@ def paged_kv_append_at(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_t
                                     block_tables.shape[1], _ptr(seq_ids), _ptr(positions), n, _ptr(slot_mapping),
                                     _stream()))
     return slot_mapping
+
+
+def _take_rows(cache: "KVCache", t: torch.Tensor, name: str, heads: Optional[int], n: Optional[int]):
+    """Address and token stride (elements) of [T, heads, head_dim] rows whose tokens may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.get_device() != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.device}")
+    if t.dtype != cache.torch_dtype:
+        raise TypeError(f"{name} must be {cache.torch_dtype}, got {t.dtype}")
+    d = cache.head_dim
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) or \
+            (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be [{'T' if n is None else n}, {'H' if heads is None else heads}, {d}], got "
+                         f"{list(t.shape)}")
+    stride, head, elem = t.stride()
+    if elem != 1 or (t.shape[1] > 1 and head != d):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if t.shape[0] <= 1:
+        return t.data_ptr(), t.shape[1] * d
+    return t.data_ptr(), stride
+
+
+def paged_kv_append_rotary(cache: KVCache, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                           block_tables: torch.Tensor, seq_ids: torch.Tensor, positions: torch.Tensor, rotary: Rotary,
+                           q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                           eps: float = 1e-6, rotary_positions: Optional[torch.Tensor] = None,
+                           slot_mapping: Optional[torch.Tensor] = None,
+                           q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """paged_kv_append_at of rows as the projections leave them: q and k normed per head (where a weight is given),
+    rotated, k and v written to their slots, q returned.
+
+    q, k and v may be slices of one [T, (Hq + 2 Hkv) * D] projection (tokens apart, heads contiguous).
+    ``rotary_positions`` (int32 [T]) where the rotation's position is not the place in the cache; ``q_out`` may be
+    ``q``.  ``q`` None: k and v alone (returns None)."""
+    n = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else None
+    kp, ks = _take_rows(cache, k, "k", cache.num_kv_heads, None)
+    vp, vs = _take_rows(cache, v, "v", cache.num_kv_heads, n)
+    tables = _take(cache, block_tables, "block_tables", torch.int32, 2)
+    seqs = _take(cache, seq_ids, "seq_ids", torch.int32, 1)
+    pos = _take(cache, positions, "positions", torch.int32, 1)
+    if seq_ids.shape[0] != n or positions.shape[0] != n:
+        raise ValueError("seq_ids/positions length != number of tokens")
+    if not isinstance(rotary, Rotary):
+        raise TypeError("rotary must be a Rotary")
+    angles = None
+    if rotary_positions is not None:
+        angles = _take(cache, rotary_positions, "rotary_positions", torch.int32, 1)
+        if rotary_positions.shape[0] != n:
+            raise ValueError("rotary_positions length != number of tokens")
+    slots = None
+    if slot_mapping is not None:
+        slots = _take(cache, slot_mapping, "slot_mapping", torch.int64, 1)
+        if slot_mapping.shape[0] != n:
+            raise ValueError("slot_mapping length != number of tokens")
+    weights = []
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        weights.append(None if w is None else _take(cache, w, name, cache.torch_dtype, 1))
+        if w is not None and w.shape[0] != cache.head_dim:
+            raise ValueError(f"{name} must be [{cache.head_dim}]")
+    if q is None:
+        if q_out is not None or q_weight is not None:
+            raise ValueError("q_out and q_weight need q")
+        qp, qs, hq, op, os_ = None, 0, 0, None, 0
+    else:
+        qp, qs = _take_rows(cache, q, "q", None, n)
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = q.new_empty((n, hq, cache.head_dim))
+        op, os_ = _take_rows(cache, q_out, "q_out", hq, n)
+    _check(lib().paged_kv_append_rotary(cache.handle, qp, qs, kp, ks, vp, vs, hq, tables, block_tables.shape[0],
+                                        block_tables.shape[1], seqs, pos, angles, n, rotary._ref, weights[0],
+                                        weights[1], float(eps), op, os_, slots, _stream()))
+    return q_out
 
 
 def paged_kv_gather(cache: KVCache, slot_mapping: torch.Tensor, k: Optional[torch.Tensor] = None,

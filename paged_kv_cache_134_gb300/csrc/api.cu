@@ -1,7 +1,8 @@
 // C ABI of the library: handle management, host-side validation, launches, error
 // reporting and profiling.  Every computation happens in the kernels of append.cu,
-// decode*.cu, prefill.cu and blocks.cu.
+// decode*.cu, rotary.cu, prefill.cu and blocks.cu.
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -482,6 +483,45 @@ int paged_kv_append_at(pkv_cache_t c, const void *k, const void *v, const int32_
     if (int r = check_device(c)) return r;
     cudaError_t e = launch_append_at(c, k, v, block_tables, num_rows, max_blocks_per_seq, seq_ids, positions,
                                      num_tokens, slot_mapping, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return pkv_cuda_fail(e, "append launch");
+    return PKV_OK;
+}
+
+int paged_kv_append_rotary(pkv_cache_t c, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, int num_q_heads, const int32_t *block_tables, int num_rows,
+                           int max_blocks_per_seq, const int32_t *seq_ids, const int32_t *positions,
+                           const int32_t *rotary_positions, int64_t num_tokens, const pkv_rotary_t *rotary,
+                           const void *q_weight, const void *k_weight, float eps, void *q_out, int64_t q_out_stride,
+                           int64_t *slot_mapping, void *stream) {
+    PKV_RANGE("paged_kv_append_rotary");
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (num_tokens < 0 || num_rows < 0 || max_blocks_per_seq < 0 || num_q_heads < 0)
+        return pkv_fail(PKV_EINVAL, "negative size");
+    if (num_q_heads > 4096 || c->num_kv_heads > 4096) return pkv_fail(PKV_EUNSUPPORTED, "more than 4096 heads");
+    if (!rotary || !rotary->inv_freq) return pkv_fail(PKV_EINVAL, "rotary is NULL");
+    if (rotary->rotary_dim < 16 || rotary->rotary_dim > c->head_dim || rotary->rotary_dim % 16)
+        return pkv_fail(PKV_EUNSUPPORTED, "rotary_dim %d is not a multiple of 16 in [16, head_dim %d]",
+                        rotary->rotary_dim, c->head_dim);
+    if (!std::isfinite(rotary->gain)) return pkv_fail(PKV_EINVAL, "gain is not finite");
+    for (int i = 0; i < rotary->rotary_dim / 2; ++i)
+        if (!std::isfinite(rotary->inv_freq[i])) return pkv_fail(PKV_EINVAL, "inv_freq[%d] is not finite", i);
+    if (!(eps >= 0.f)) return pkv_fail(PKV_EINVAL, "eps must be >= 0");
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !seq_ids || !positions || (!block_tables && num_rows > 0 && max_blocks_per_seq > 0) ||
+        (num_q_heads > 0 && (!q || !q_out)))
+        return pkv_fail(PKV_EINVAL, "NULL pointer");
+    if (!aligned16(k) || !aligned16(v) || (num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out))) ||
+        !aligned16(q_weight) || !aligned16(k_weight))
+        return pkv_fail(PKV_EINVAL, "q, k, v, q_out and the weights must be 16-byte aligned");
+    if ((k_stride | v_stride) % 8 || (num_q_heads > 0 && (q_stride | q_out_stride) % 8))
+        return pkv_fail(PKV_EINVAL, "strides must be multiples of 8 elements");
+    if (num_q_heads > 0 && num_tokens > 1 && q_out_stride < (int64_t)num_q_heads * c->head_dim)
+        return pkv_fail(PKV_EINVAL, "q_out rows overlap");
+    if (int r = check_device(c)) return r;
+    RotaryLaunch r{q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, num_q_heads, block_tables, num_rows,
+                   max_blocks_per_seq, seq_ids, positions, rotary_positions, num_tokens, rotary,
+                   num_q_heads > 0 ? q_weight : nullptr, k_weight, eps, slot_mapping};
+    cudaError_t e = launch_append_rotary(c, r, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return pkv_cuda_fail(e, "append launch");
     return PKV_OK;
 }

@@ -21,14 +21,6 @@
 
 namespace {
 
-PKV_DEV int64_t slot_of(const int32_t *__restrict__ tables, int rows, int max_blocks, int s, int p, int bs) {
-    if (s < 0 || s >= rows || p < 0) return -1;
-    const int lb = p / bs;
-    if (lb >= max_blocks) return -1;
-    const int b = tables[(int64_t)s * max_blocks + lb];
-    return b < 0 ? -1 : (int64_t)b * bs + p % bs;
-}
-
 __global__ void slot_mapping_kernel(const int32_t *__restrict__ tables, int rows, int max_blocks,
                                     const int32_t *__restrict__ seq_ids, const int32_t *__restrict__ positions,
                                     int64_t n, int bs, int64_t *__restrict__ out) {

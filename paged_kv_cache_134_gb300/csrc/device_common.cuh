@@ -34,6 +34,15 @@ PKV_DEV void set_error(unsigned int *err, unsigned int bits) {
     if (err) atomicOr(err, bits);
 }
 
+// the slot of position p of table row s, -1 where there is none
+PKV_DEV int64_t slot_of(const int32_t *__restrict__ tables, int rows, int max_blocks, int s, int p, int bs) {
+    if (s < 0 || s >= rows || p < 0) return -1;
+    const int lb = p / bs;
+    if (lb >= max_blocks) return -1;
+    const int b = tables[(int64_t)s * max_blocks + lb];
+    return b < 0 ? -1 : (int64_t)b * bs + p % bs;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 PKV_DEV void mbar_init(uint64_t *bar, uint32_t count) {

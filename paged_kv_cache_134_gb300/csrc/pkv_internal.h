@@ -125,6 +125,23 @@ cudaError_t launch_append_ranges(pkv_cache *c, const void *k, const void *v, con
 // rows at slots[i] in the model's type: k, v [n][Hkv][D] (append.cu)
 cudaError_t launch_gather(pkv_cache *c, const int64_t *slots, int64_t n, void *k, void *v, cudaStream_t st);
 
+// rotation, norms and append of new tokens (rotary.cu); strides in elements
+struct RotaryLaunch {
+    const void *q, *k, *v;
+    void *q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    int num_q_heads;
+    const int32_t *tables;
+    int rows, max_blocks;
+    const int32_t *seq_ids, *positions, *rotary_positions;
+    int64_t n;
+    const pkv_rotary_t *rotary;
+    const void *q_weight, *k_weight;
+    float eps;
+    int64_t *slots_out;
+};
+cudaError_t launch_append_rotary(pkv_cache *c, const RotaryLaunch &r, cudaStream_t st);
+
 // bytes between blocks, between a block's KV heads, and from a head's K rows to its V rows
 inline void pkv_row_strides(const pkv_cache *c, int64_t *block, int64_t *head, int64_t *v) {
     if (c->kv_dtype == PKV_INT4) {
