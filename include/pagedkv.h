@@ -222,6 +222,16 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
                            const int32_t *context_lens, int num_seqs, int num_q_heads, float scale, void *out,
                            void *stream);
 
+/* paged_decode_attention under a sliding window with sinks: of the L_s tokens the query sees the last `window`
+ * (t >= L_s - window) and the first `sinks` (t < sinks), window >= 1, sinks >= 0; blocks that hold none of them
+ * are not read, and their table entries may be -1.  A window that reaches the sinks, or the first token, is
+ * paged_decode_attention to its tolerance.  Lengths above the tables' tokens are cut to them and set PKV_DEVERR_LENGTH.
+ * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4).  Split boundaries depend on L_s, window, sinks, num_seqs
+ * and max_blocks_per_seq.  Workspace: as for paged_decode_attention_mass, one per stream and per capture. */
+int paged_decode_attention_window(const void *q, pkv_cache_t cache, const int32_t *block_tables,
+                                  int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_q_heads,
+                                  float scale, int window, int sinks, void *out, void *stream);
+
 /* paged_decode_attention that also accumulates each token's attention mass, for eviction:
  *   attn_mass[s][g][t] := decay * attn_mass[s][g][t] + sum_{h: h / group == g} softmax_t(scale * q[s][h] . K_t)
  * for t < L_s; the rest of a row is not touched.  attn_mass: fp32 [num_seqs][num_kv_heads][mass_len],

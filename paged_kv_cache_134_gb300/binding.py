@@ -63,6 +63,7 @@ def lib() -> ctypes.CDLL:
                                              ctypes.c_float, vp, i64, vp, vp]
         L.paged_decode_attention.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp]
         L.paged_decode_attention_noalloc.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp]
+        L.paged_decode_attention_window.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, i32, i32, vp, vp]
         L.paged_kv_gather.argtypes = [vp, vp, i64, vp, vp, vp]
         L.paged_decode_attention_mass.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, ctypes.c_float, vp,
                                                   i64, vp, vp]
@@ -500,6 +501,37 @@ def paged_decode_attention(q: torch.Tensor, cache: KVCache, block_tables: torch.
     _check(lib().paged_decode_attention(_ptr(q), cache.handle, _ptr(block_tables), block_tables.shape[1],
                                         _ptr(context_lens), S, hq, float(scale), _ptr(out), _stream()))
     return out
+
+
+def paged_decode_attention_window(q: torch.Tensor, cache: KVCache, block_tables: torch.Tensor,
+                                  context_lens: torch.Tensor, scale: float, window: int, sinks: int = 0,
+                                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_decode_attention over the last ``window`` tokens of each sequence and its first ``sinks``; blocks that
+    hold none of them are not read."""
+    qp = _take(cache, q, "q", cache.torch_dtype, 3)
+    tables = _take(cache, block_tables, "block_tables", torch.int32, 2)
+    lens = _take(cache, context_lens, "context_lens", torch.int32, 1)
+    S, hq, d = q.shape
+    rows, width = block_tables.shape
+    if d != cache.head_dim or rows != S or context_lens.shape[0] != S:
+        raise ValueError("shape mismatch between q, block_tables and context_lens")
+    window, sinks = _window(window, sinks, 1)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _take(cache, out, "out", cache.torch_dtype, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    _check(lib().paged_decode_attention_window(qp, cache.handle, tables, width, lens, S, hq, float(scale), window, sinks,
+                                               out.data_ptr(), _stream()))
+    return out
+
+
+def _window(window, sinks, least):
+    window, sinks = int(window), int(sinks)
+    if window < least or sinks < 0 or (window == 0 and sinks):
+        raise ValueError(f"window {window} and sinks {sinks}: window >= {least}, sinks >= 0 and 0 without a window")
+    return min(window, 2 ** 31 - 1), min(sinks, 2 ** 31 - 1)
 
 
 def paged_decode_attention_cascade(q: torch.Tensor, cache: KVCache, block_tables: torch.Tensor,

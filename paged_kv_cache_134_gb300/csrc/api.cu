@@ -208,7 +208,7 @@ int pkv_cuda_fail(cudaError_t e, const char *what) {
 
 cudaError_t launch_decode_chunked(pkv_cache *c, DecodeLaunch d, cudaStream_t st) {
     const int G = d.num_q_heads / c->num_kv_heads;
-    const int per = decode_seqs_per_launch(c, G);
+    const int per = decode_seqs_per_launch(c, G, d.window > 0);
     const int total = d.num_seqs;
     const int64_t row_bytes = (int64_t)d.num_q_heads * c->head_dim * 2; // q and out rows, 16-bit model dtype
     const char *q0 = static_cast<const char *>(d.q);
@@ -625,6 +625,44 @@ int paged_decode_attention(const void *q, pkv_cache_t c, const int32_t *block_ta
     d.ws_o = ws ? c->ws : nullptr;
     d.ws_ml = nullptr;
     cudaError_t e = launch_decode_chunked(c, d, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return pkv_cuda_fail(e, "decode launch");
+    return PKV_OK;
+}
+
+int paged_decode_attention_window(const void *q, pkv_cache_t c, const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *context_lens, int num_seqs, int num_q_heads, float scale, int window,
+                                  int sinks, void *out, void *stream) {
+    PKV_RANGE("paged_decode_attention_window");
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (num_seqs < 0 || max_blocks_per_seq < 0) return pkv_fail(PKV_EINVAL, "negative size");
+    if (window < 1 || sinks < 0) return pkv_fail(PKV_EINVAL, "window %d and sinks %d: window >= 1, sinks >= 0", window, sinks);
+    if (c->kv_dtype == PKV_INT4) return pkv_fail(PKV_EUNSUPPORTED, "the windowed decode does not read 4-bit caches");
+    if (num_seqs == 0) return PKV_OK;
+    if (int r = check_decode(c, q, block_tables, max_blocks_per_seq, context_lens, num_q_heads, scale, out)) return r;
+    if (int r = check_device(c)) return r;
+    const int G = num_q_heads / c->num_kv_heads;
+    const int per_launch = std::min(num_seqs, decode_seqs_per_launch(c, G, true));
+    DecodeLaunch d;
+    d.q = q;
+    d.out = out;
+    d.tables = block_tables;
+    d.lens = context_lens;
+    d.max_blocks = max_blocks_per_seq;
+    d.num_seqs = num_seqs;
+    d.num_q_heads = num_q_heads;
+    d.scale = scale;
+    d.window = window;
+    d.sinks = std::min(sinks, 1 << 30); // (a block's rounding stays within 32 bits)
+    const int64_t seen = window_seen_blocks(c, max_blocks_per_seq, window, d.sinks);
+    d.split_blocks = window_split_blocks(c, G, per_launch, seen);
+    d.max_splits = (int)((seen + d.split_blocks - 1) / d.split_blocks);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    std::lock_guard<std::mutex> lk(c->ws_mu);
+    PkvWorkspace ws;
+    if (int r = pkv_stream_workspace(c, st, decode_workspace_floats(c, per_launch, num_q_heads, d.max_splits), &ws)) return r;
+    d.ws_o = ws.p;
+    d.ws_ml = nullptr;
+    cudaError_t e = launch_decode_chunked(c, d, st);
     if (e != cudaSuccess) return pkv_cuda_fail(e, "decode launch");
     return PKV_OK;
 }

@@ -1,4 +1,5 @@
 // Host side of the paged decode: split size, stage count, grid, workspace, launches.
+#include <algorithm>
 #include <cstdlib>
 
 #include "decode_impl.cuh"
@@ -18,7 +19,15 @@ int ctas_per_sm() { return env_int("PAGEDKV_DECODE_CTAS", 4); }
 using DecodeFn = cudaError_t (*)(const pkv_decode::Args &, int, int, int, size_t, cudaStream_t, bool);
 using OccFn = int (*)(int, int, size_t);
 
-void pick(const pkv_cache *c, DecodeFn *fn, OccFn *occ) {
+void pick(const pkv_cache *c, bool window, DecodeFn *fn, OccFn *occ) {
+    if (window) {
+        const bool f8 = c->kv_dtype == PKV_FP8_E4M3, h = c->model_dtype == PKV_F16;
+        *fn = f8 ? (h ? pkv_decode_window_fp8_f16 : pkv_decode_window_fp8_bf16)
+                 : (h ? pkv_decode_window_f16 : pkv_decode_window_bf16);
+        *occ = f8 ? (h ? pkv_decode_window_occupancy_fp8_f16 : pkv_decode_window_occupancy_fp8_bf16)
+                  : (h ? pkv_decode_window_occupancy_f16 : pkv_decode_window_occupancy_bf16);
+        return;
+    }
     if (c->kv_dtype == PKV_F16) {
         *fn = pkv_decode_f16;
         *occ = pkv_decode_occupancy_f16;
@@ -59,14 +68,29 @@ int cascade_suffix_split_blocks(const pkv_cache *c) {
     return b > 0 ? b : 1;
 }
 
-int decode_seqs_per_launch(const pkv_cache *c, int G) {
+int decode_seqs_per_launch(const pkv_cache *c, int G, bool window) {
     // Both decode kernels keep a per-sequence unit table (3 ints a sequence) in shared memory: the
     // CUDA-core kernel takes up to kMaxSeqs sequences a launch; the tensor-core kernel, whose stage
     // rings fill nearly all of shared memory, fewer (the largest multiple of 64 that still fits).
     int n = pkv_decode::kMaxSeqs;
-    if (pkv_decode_tc_eligible(c, G, 64))
-        while (n > 64 && !pkv_decode_tc_eligible(c, G, n)) n -= 64;
+    if (pkv_decode_tc_eligible(c, G, 64, window))
+        while (n > 64 && !pkv_decode_tc_eligible(c, G, n, window)) n -= 64;
     return n;
+}
+
+int64_t window_seen_blocks(const pkv_cache *c, int max_blocks, int window, int sinks) {
+    const int64_t bs = c->block_size, w = ((int64_t)window - 1 + bs - 1) / bs + 1, s = ((int64_t)sinks + bs - 1) / bs;
+    return std::min<int64_t>(max_blocks, w + s);
+}
+
+int window_split_blocks(const pkv_cache *c, int G, int num_seqs, int64_t seen_blocks) {
+    // The splits of the plain decode, but of equal size: under a window most sequences show the same number of
+    // blocks, and a last split of a block or two would cost a unit of its own.
+    const bool tc = pkv_decode_tc_eligible(c, G, num_seqs, true);
+    const int want = tc ? (c->kv_dtype == PKV_FP8_E4M3 ? 1024 : 512) : 256;
+    const int64_t per = std::max(1, want / c->block_size);
+    const int64_t k = std::max<int64_t>(1, (seen_blocks + per / 2) / per);
+    return (int)std::max<int64_t>(1, (seen_blocks + k - 1) / k);
 }
 
 int64_t decode_workspace_floats(const pkv_cache *c, int num_seqs, int num_q_heads, int max_splits) {
@@ -114,12 +138,14 @@ cudaError_t launch_decode(pkv_cache *c, const DecodeLaunch &d, cudaStream_t st) 
     a.qk_scale_log2 = d.scale * 1.4426950408889634f;
     a.start_block = d.start_block;
     a.slot0 = d.slot0;
+    a.window = d.window;
+    a.sinks = d.sinks;
 
     DecodeFn fn;
     OccFn occ;
-    pick(c, &fn, &occ);
+    pick(c, d.window > 0, &fn, &occ);
     cudaError_t e;
-    if (pkv_decode_tc_eligible(c, G, d.num_seqs)) {
+    if (pkv_decode_tc_eligible(c, G, d.num_seqs, d.window > 0)) {
         a.nstages = 0;
         // longer splits than the CUDA-core kernel's: a unit then spans several 128-token MMA steps,
         // which spreads the per-unit work (Q load, epilogue, partial write) over more bytes; the
@@ -129,7 +155,7 @@ cudaError_t launch_decode(pkv_cache *c, const DecodeLaunch &d, cudaStream_t st) 
         // ~5 % faster than 512-token ones for E4M3 and ~4 % slower for bf16)
         const int tc_default = c->kv_dtype == PKV_FP8_E4M3 ? 1024 : 512;
         const int tc_blocks = env_int("PAGEDKV_SPLIT_TOKENS_TC", tc_default) / c->block_size;
-        if (tc_blocks > a.split_blocks) a.split_blocks = tc_blocks;
+        if (tc_blocks > a.split_blocks && d.window == 0) a.split_blocks = tc_blocks;
         {
             PkvTimer timer(c, PKV_KIND_DECODE, st);
             e = pkv_decode_tc_launch(c, a, d.q, G, st);

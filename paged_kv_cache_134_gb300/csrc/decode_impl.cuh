@@ -68,7 +68,29 @@ struct Args {
     // attention another kernel computed into workspace slots [0, slot0); this kernel then covers the
     // blocks from start_block on and writes its splits from slot slot0 on (both 0 otherwise)
     int start_block = 0, slot0 = 0;
+    // sliding window (WIN kernels): the last `window` tokens and the first `sinks` ones are attended to
+    int window = 0, sinks = 0;
 };
+
+// What a sequence of L tokens shows to a query at its end under a window with sinks: the blocks that hold a visible token,
+// taken one after the other ("seen" order: the sinks' blocks, then the window's), as if the sequence were
+// `len` tokens long.  Seen block i is logical block i, or i + skip from block `from` on.  Of the seen tokens only
+// [lo, hi) are not visible: the rest of the sinks' last block and what lies before the window in its first.
+// Every seen block holds a visible token.
+struct Reach {
+    int len, from, skip, lo, hi;
+};
+PKV_DEV Reach reach_of(int L, int window, int sinks, int bs) {
+    const int first = L - window; // (L >= 0, window >= 1)
+    if (first <= sinks) return {L, 0, 0, 0, 0};
+    const int from = (sinks + bs - 1) / bs, skip = max(first / bs - from, 0);
+    return {L - skip * bs, from, skip, sinks, first - skip * bs};
+}
+// a length cut to what the table's row can name
+PKV_DEV int length_in(const Args &a, int s) {
+    const int64_t most = (int64_t)a.max_blocks * a.bs;
+    return (int)max((int64_t)0, min((int64_t)a.lens[s], most));
+}
 
 template <int KVT>
 PKV_DEV void load8(const char *p, float *f) {
@@ -144,10 +166,12 @@ PKV_DEV void loadN(const char *p, float *f) {
 }
 
 // One tile of `bs` tokens, `valid` of them real, for this lane's query head.
-template <int D, int G, int KVT>
+// WIN: tokens [lo, hi) of the tile are not attended to.
+template <int D, int G, int KVT, bool WIN>
 PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
                           const float (&qf)[Lanes<D, G>::DL], float &m, float &l, float (&acc)[Lanes<D, G>::DL],
-                          int lane) {
+                          int lane, int lo, int hi) {
+    auto live = [&](int t) { return t < valid && !(WIN && t >= lo && t < hi); };
     using LY = Lanes<D, G>;
     constexpr int DL = LY::DL, LH = LY::LH, LT = LY::LT, TPP = LY::TPP, MAXP = LY::MAXP;
     constexpr int EB = (KVT == PKV_FP8_E4M3) ? 1 : 2;
@@ -156,6 +180,7 @@ PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
     const int npc = ch / TPP;
     for (int c0 = 0; c0 < bs; c0 += ch) {
         if (c0 >= valid) break;
+        if (WIN && c0 >= lo && c0 + ch <= hi) continue;
         float sc[MAXP];
 #pragma unroll
         for (int p = 0; p < MAXP; ++p) {
@@ -178,7 +203,7 @@ PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
                 float v = sc[p];
 #pragma unroll
                 for (int o = LH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                sc[p] = (c0 + p * TPP + tg) < valid ? v : -INFINITY;
+                sc[p] = live(c0 + p * TPP + tg) ? v : -INFINITY;
             }
         }
         float mx = -INFINITY;
@@ -205,7 +230,7 @@ PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
         for (int p = 0; p < MAXP; ++p) {
             if (p < npc) {
                 const int t = c0 + p * TPP + tg;
-                if (t < valid) {
+                if (live(t)) {
                     float vf[DL];
                     loadN<KVT, DL>(vs + (t * D + sub * DL) * EB, vf);
 #pragma unroll
@@ -223,9 +248,10 @@ PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
 // lanes by a reduce-scatter: after log2 steps every lane holds the full score of one pass, so the
 // softmax of a head costs one exp2 per lane, and each pass's weight is then fetched back by a
 // shuffle from the lane that owns it.
-template <int D, int G, int KVT>
+template <int D, int G, int KVT, bool WIN>
 PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, const float (&qf)[G][8],
-                             float (&m)[G], float (&l)[G], float (&acc)[G][8], int lane) {
+                             float (&m)[G], float (&l)[G], float (&acc)[G][8], int lane, int lo, int hi) {
+    auto live = [&](int t) { return t < valid && !(WIN && t >= lo && t < hi); };
     constexpr int LPT = D / 8;     // lanes per token
     constexpr int TPP = 32 / LPT;  // tokens per pass
     constexpr int MAXP = 16 / TPP; // passes per 16-token chunk (8 for D=128, 4 for D=64)
@@ -242,6 +268,7 @@ PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, 
     const int npc = ch / TPP;
     for (int c0 = 0; c0 < bs; c0 += ch) {
         if (c0 >= valid) break;
+        if (WIN && c0 >= lo && c0 + ch <= hi) continue;
         float part[G][MAXP];
 #pragma unroll
         for (int p = 0; p < MAXP; ++p) {
@@ -280,7 +307,7 @@ PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, 
             float v = part[g][0];
 #pragma unroll
             for (int o = (1 << DUP) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            sc[g] = (c0 + mypass * TPP + grp) < valid ? v : -INFINITY;
+            sc[g] = live(c0 + mypass * TPP + grp) ? v : -INFINITY;
         }
         // online softmax per head; the chunk's scores are spread one per lane
 #pragma unroll
@@ -305,7 +332,7 @@ PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, 
                 float w[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g) w[g] = __shfl_sync(0xffffffffu, sc[g], src);
-                if (t < valid) {
+                if (live(t)) {
                     float vf[8];
                     load8<KVT>(vs + (t * D + sub * 8) * EB, vf);
 #pragma unroll
@@ -321,8 +348,10 @@ PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, 
 // Unit list, built by the whole CTA into shared memory: per sequence its block count nb[s], and
 // prefix counts of full splits (pf) and of partial tail splits (pp, 0 or 1 per sequence), so that
 // unit u resolves to (sequence, KV head, split) with two binary searches (unit_info).  Sequences
-// longer than the table allows are clamped and reported.
-PKV_DEV void build_unit_list(const Args &a, int *pf, int *pp, int *nb, int warp, int lane) {
+// longer than the table allows are clamped and reported.  WIN: the blocks in sight (see Reach); `ln`, when given,
+// receives the lengths.
+template <bool WIN = false>
+PKV_DEV void build_unit_list(const Args &a, int *pf, int *pp, int *nb, int warp, int lane, int *ln = nullptr) {
     const int S = a.num_seqs, bps = a.split_blocks;
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
         const int L = a.lens[s];
@@ -330,6 +359,11 @@ PKV_DEV void build_unit_list(const Args &a, int *pf, int *pp, int *nb, int warp,
         if (n > a.max_blocks) {
             if (blockIdx.x == 0) set_error(a.err, PKV_DEVERR_LENGTH);
             n = a.max_blocks;
+        }
+        if constexpr (WIN) {
+            const int cut = length_in(a, s);
+            if (ln) ln[s] = cut;
+            n = (reach_of(cut, a.window, a.sinks, a.bs).len + a.bs - 1) / a.bs;
         }
         nb[s] = n;
         const int m = n > a.start_block ? n - a.start_block : 0; // blocks this kernel covers
@@ -377,7 +411,7 @@ PKV_DEV bool wait_at_least(const int *x, int n, const int *abort_flag) {
     return true;
 }
 
-template <int D, int G, int MT, int KVT>
+template <int D, int G, int MT, int KVT, bool WIN = false>
 __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
     using M = ModelT<MT>;
     using T = typename M::T;
@@ -411,7 +445,11 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
     // it may launch now and take the SMs this grid's CTAs leave
     if (a.slot0 > 0) pdl_trigger();
     const int bps = a.split_blocks;
-    build_unit_list(a, pf, pp, nb, warp, lane);
+    build_unit_list<WIN>(a, pf, pp, nb, warp, lane);
+    auto reach = [&](int s) -> Reach {
+        if constexpr (WIN) return reach_of(length_in(a, s), a.window, a.sinks, a.bs);
+        return {a.lens[s], 0, 0, 0, 0};
+    };
     const int U = (pf[S] + pp[S]) * a.hkv;
     const int ST = a.sub_tokens, spb = a.bs / a.sub_tokens; // stage tokens, stages per block
 
@@ -422,13 +460,16 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
         bool ok = true;
         for (int u = blockIdx.x; u < U && ok; u += gridDim.x) {
             const Unit un = unit_info(u, pf, pp, nb, S, a.hkv, bps, a.start_block);
+            Reach rc{};
+            if constexpr (WIN) rc = reach(un.s);
             const int32_t *trow = a.tables + (int64_t)un.s * a.max_blocks + un.blk0;
             const char *head_base = a.pool + (int64_t)un.kvh * a.tile_bytes;
             // stages of this unit: spb per block, less the parts wholly past the sequence's end
-            const int nt = spb > 1 ? min(un.ntiles * spb, (a.lens[un.s] - un.blk0 * a.bs + ST - 1) / ST) : un.ntiles;
+            const int nt = spb > 1 ? min(un.ntiles * spb, ((WIN ? rc.len : a.lens[un.s]) - un.blk0 * a.bs + ST - 1) / ST) : un.ntiles;
             for (int i0 = 0; i0 < un.ntiles && ok; i0 += 32) {
                 const int cnt = min(32, un.ntiles - i0);
-                const int myb = lane < cnt ? trow[i0 + lane] : 0;
+                const int at = i0 + lane + (WIN && un.blk0 + i0 + lane >= rc.from ? rc.skip : 0);
+                const int myb = lane < cnt ? trow[at] : 0;
                 for (int i = 0; i < cnt && ok; ++i) {
                     const int b = __shfl_sync(0xffffffffu, myb, i);
                     for (int h = 0, k = (i0 + i) * spb; h < spb && k < nt; ++h, ++k) {
@@ -482,7 +523,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
     int nu = 0; // this CTA's units so far
     for (int u = blockIdx.x; u < U; u += gridDim.x, ++nu) {
         const Unit un = unit_info(u, pf, pp, nb, S, a.hkv, bps, a.start_block);
-        const int L = a.lens[un.s];
+        const Reach rc = reach(un.s);
+        const int L = rc.len;
         float qs = a.qk_scale_log2;
         if constexpr (KVT == PKV_FP8_E4M3) qs *= a.k_scale[un.kvh];
         float qf[GS][DL];
@@ -520,10 +562,11 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
             if (!flags[stage]) {
                 const char *ks = ring + (size_t)stage * 2 * a.sub_bytes;
                 const int valid = min(ST, L - un.blk0 * a.bs - i * ST);
+                const int lo = rc.lo - un.blk0 * a.bs - i * ST, hi = rc.hi - un.blk0 * a.bs - i * ST;
                 if constexpr (G == 1)
-                    process_tile<D, 1, KVT>(ks, ks + a.sub_bytes, ST, valid, qf[0], m[0], l[0], acc[0], lane);
+                    process_tile<D, 1, KVT, WIN>(ks, ks + a.sub_bytes, ST, valid, qf[0], m[0], l[0], acc[0], lane, lo, hi);
                 else
-                    process_tile_tp<D, G, KVT>(ks, ks + a.sub_bytes, ST, valid, qf, m, l, acc, lane);
+                    process_tile_tp<D, G, KVT, WIN>(ks, ks + a.sub_bytes, ST, valid, qf, m, l, acc, lane, lo, hi);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[stage]);
@@ -625,7 +668,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
 // max M from all splits' (m, l), then accumulates the splits j = warp, warp + 4, ... (lane = D/32
 // dims, vector loads; the first 16 splits' loads go out with those of the maxima); the four warp
 // sums are added in warp order through shared memory, so the result is deterministic.
-template <int D, int MT>
+template <int D, int MT, bool WIN = false>
 __global__ void __launch_bounds__(128) merge_kernel(const Args a) {
     using M = ModelT<MT>;
     using T = typename M::T;
@@ -638,7 +681,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const Args a) {
     pdl_wait();
     const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = row / a.hq;
-    const int L = a.lens[s];
+    const int L = WIN ? reach_of(length_in(a, s), a.window, a.sinks, a.bs).len : a.lens[s];
     int n = L > 0 ? (L + a.bs - 1) / a.bs : 0;
     if (n > a.max_blocks) n = a.max_blocks;
     if (a.slot0 > 0 && L < a.start_block * a.bs) {
@@ -723,26 +766,26 @@ inline size_t smem_bytes(int D, int G, int nst, int stage_part_bytes, int S) {
            (size_t)(3 * S + 2) * 4;
 }
 
-template <int D, int G, int MT, int KVT>
+template <int D, int G, int MT, int KVT, bool WIN>
 cudaError_t launch_t(const Args &a, int grid, size_t smem, cudaStream_t st) {
-    auto kern = decode_kernel<D, G, MT, KVT>;
+    auto kern = decode_kernel<D, G, MT, KVT, WIN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return pdl_launch(kern, dim3(grid), dim3(kThreads), smem, st, a);
 }
 
-template <int D, int MT>
+template <int D, int MT, bool WIN>
 cudaError_t launch_merge_t(const Args &a, cudaStream_t st) {
     const int rows = a.num_seqs * a.hq;
     if (rows == 0) return cudaSuccess;
-    return pdl_launch(merge_kernel<D, MT>, dim3(rows), dim3(128), 0, st, a);
+    return pdl_launch(merge_kernel<D, MT, WIN>, dim3(rows), dim3(128), 0, st, a);
 }
 
 // Dispatch over head_dim and group size for one (model dtype, KV dtype) pair.
-template <int MT, int KVT>
+template <int MT, int KVT, bool WIN = false>
 cudaError_t dispatch(const Args &a, int D, int G, int grid, size_t smem, cudaStream_t st, bool merge) {
 #define PKV_CASE(DD, GG)                                                                                               \
-    if (D == DD && G == GG) return merge ? launch_merge_t<DD, MT>(a, st) : launch_t<DD, GG, MT, KVT>(a, grid, smem, st);
+    if (D == DD && G == GG) return merge ? launch_merge_t<DD, MT, WIN>(a, st) : launch_t<DD, GG, MT, KVT, WIN>(a, grid, smem, st);
     PKV_CASE(64, 1)
     PKV_CASE(64, 2)
     PKV_CASE(64, 4)
@@ -755,18 +798,18 @@ cudaError_t dispatch(const Args &a, int D, int G, int grid, size_t smem, cudaStr
     return cudaErrorInvalidValue;
 }
 
-template <int D, int G, int MT, int KVT>
+template <int D, int G, int MT, int KVT, bool WIN>
 int occupancy(size_t smem) {
     int n = 0;
-    cudaFuncSetAttribute(decode_kernel<D, G, MT, KVT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, MT, KVT>, kThreads, smem);
+    cudaFuncSetAttribute(decode_kernel<D, G, MT, KVT, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, MT, KVT, WIN>, kThreads, smem);
     return n;
 }
 
-template <int MT, int KVT>
+template <int MT, int KVT, bool WIN = false>
 int occupancy_dispatch(int D, int G, size_t smem) {
 #define PKV_CASE(DD, GG)                                                                                               \
-    if (D == DD && G == GG) return occupancy<DD, GG, MT, KVT>(smem);
+    if (D == DD && G == GG) return occupancy<DD, GG, MT, KVT, WIN>(smem);
     PKV_CASE(64, 1)
     PKV_CASE(64, 2)
     PKV_CASE(64, 4)
@@ -792,3 +835,14 @@ int pkv_decode_occupancy_f16(int D, int G, size_t smem);
 int pkv_decode_occupancy_bf16(int D, int G, size_t smem);
 int pkv_decode_occupancy_fp8_f16(int D, int G, size_t smem);
 int pkv_decode_occupancy_fp8_bf16(int D, int G, size_t smem);
+// the same with a sliding window and sinks (decode_window_*.cu)
+cudaError_t pkv_decode_window_f16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t, bool merge);
+cudaError_t pkv_decode_window_bf16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t, bool merge);
+cudaError_t pkv_decode_window_fp8_f16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t,
+                                      bool merge);
+cudaError_t pkv_decode_window_fp8_bf16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t,
+                                       bool merge);
+int pkv_decode_window_occupancy_f16(int D, int G, size_t smem);
+int pkv_decode_window_occupancy_bf16(int D, int G, size_t smem);
+int pkv_decode_window_occupancy_fp8_f16(int D, int G, size_t smem);
+int pkv_decode_window_occupancy_fp8_bf16(int D, int G, size_t smem);
