@@ -108,8 +108,13 @@ int kv_cache_reserve(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_b
 int kv_cache_reserve_mass(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq,
                           int64_t max_mass_len);
 
-/* Synchronise the device and free the workspaces that paged_decode_attention_mass and the decode of
- * PKV_INT4 caches keep for streams, whether reserved or grown on demand; with graphs != 0 also those of
+/* Add a workspace for paged_chunk_attention calls of at most max_seqs sequences, max_tokens new tokens in all,
+ * max_seqlen of one sequence, max_q_heads query heads and tables of max_blocks_per_seq entries, as above. */
+int kv_cache_reserve_chunk(pkv_cache_t cache, int max_seqs, int64_t max_tokens, int max_seqlen, int max_q_heads,
+                           int max_blocks_per_seq);
+
+/* Synchronise the device and free the workspaces that paged_decode_attention_mass, paged_decode_attention_window,
+ * paged_chunk_attention and the decode of PKV_INT4 caches keep for streams, whether reserved or grown on demand; with graphs != 0 also those of
  * captures, whose graphs must not be launched again.  Later calls allocate anew.  Not to be called while a
  * stream is being captured. */
 int kv_cache_release_workspaces(pkv_cache_t cache, int graphs);
@@ -361,6 +366,27 @@ int paged_prefill_attention(const void *q, const void *k, const void *v, const i
                             const int32_t *context_lens, int num_seqs, int max_seqlen, int64_t total_tokens,
                             const int32_t *block_tables, int max_blocks_per_seq, pkv_cache_t cache, int num_q_heads,
                             float scale, void *out, void *stream);
+
+/* Attention of a chunk of new tokens over the cache: drafted tokens to be checked, a piece of a prompt, single
+ * tokens, in any mix.  Sequence i holds L_i = context_lens[i] tokens in its blocks, the new ones included (append them
+ * first: paged_kv_append_at, paged_kv_append_rotary); rows [cu_seqlens[i], cu_seqlens[i+1]) of q, n_i of them, are the
+ * queries of its last n_i tokens.  Row r sits at position p = L_i - n_i + r:
+ *   out[cu_i + r][h] = sum_t softmax_t(scale * q[cu_i + r][h] . K_t[g]) V_t[g],
+ *   t <= p, and with window > 0 also t > p - window or t < sinks (window 0: no window, sinks 0),
+ * g = h / group.  A row that sees nothing (p < 0) is zero.  q, out: [total_tokens][num_q_heads][head_dim], not
+ * overlapping; rows behind cu_seqlens[num_seqs] are left as they were.  Blocks that no row of a tile (128 / group tokens) sees are
+ * not read.  scale finite and > 0.  cu_seqlens as for packed_prefill_attention; L_i above the tables' tokens sets
+ * PKV_DEVERR_LENGTH.  The rows of a sequence with such numbers are left as they were.
+ * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4), arithmetic as in paged_prefill_attention, whose results for the
+ * same rows agree to its tolerance.  The query heads of a KV head share its keys, which are cut into splits where the
+ * rows are few: boundaries depend on L_i, n_i, num_seqs, total_tokens, max_seqlen, max_blocks_per_seq, window and
+ * sinks.  A NaN or infinity in V reaches the rows of its sequence whose tile of rows sees that token, also the earlier ones among
+ * them; one in K only the rows that see it.  Three launches (two where no row's keys are split).  Workspace: as
+ * for paged_decode_attention_mass, one per stream and per capture. */
+int paged_chunk_attention(const void *q, pkv_cache_t cache, const int32_t *block_tables, int max_blocks_per_seq,
+                          const int32_t *context_lens, const int32_t *cu_seqlens, int num_seqs, int max_seqlen,
+                          int64_t total_tokens, int num_q_heads, float scale, int window, int sinks, void *out,
+                          void *stream);
 
 /* Block copy for copy-on-write (2kiu.com section 2.2: copy-on-write of prefix blocks shared by
  * beam search or parallel sampling; section 4.3 step 3: a shared block is never rewritten in

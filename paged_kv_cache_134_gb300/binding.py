@@ -53,6 +53,7 @@ def lib() -> ctypes.CDLL:
         L.kv_cache_view.argtypes = [vp, ctypes.POINTER(vp), ctypes.POINTER(i64), ctypes.POINTER(i64)]
         L.kv_cache_reserve.argtypes = [vp, i32, i32, i32]
         L.kv_cache_reserve_mass.argtypes = [vp, i32, i32, i32, i64]
+        L.kv_cache_reserve_chunk.argtypes = [vp, i32, i64, i32, i32, i32]
         L.kv_cache_release_workspaces.argtypes = [vp, i32]
         L.kv_cache_check_error.argtypes = [vp, ctypes.POINTER(i32)]
         L.pkv_last_error.restype = ctypes.c_char_p
@@ -68,6 +69,7 @@ def lib() -> ctypes.CDLL:
         L.paged_decode_attention_mass.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, ctypes.c_float, vp,
                                                   i64, vp, vp]
         L.paged_kv_evict.argtypes = [vp, vp, i32, vp, i32, vp, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp]
+        L.paged_chunk_attention.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i64, i32, ctypes.c_float, i32, i32, vp, vp]
         L.packed_prefill_attention.argtypes = [vp, vp, vp, vp, i32, i32, i64, vp, i32, vp, i32, ctypes.c_float, vp,
                                                vp]
         L.paged_prefill_attention.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, vp, i32, vp, i32, ctypes.c_float, vp,
@@ -220,6 +222,11 @@ class KVCache:
         stream or stream capture."""
         _check(lib().kv_cache_reserve_mass(self.handle, int(max_seqs), int(max_q_heads), int(max_blocks_per_seq),
                                            int(max_mass_len)))
+
+    def reserve_chunk(self, max_seqs: int, max_tokens: int, max_seqlen: int, max_q_heads: int, max_blocks_per_seq: int):
+        """Allocate a workspace for paged_chunk_attention calls of at most these sizes, for one stream or stream capture."""
+        _check(lib().kv_cache_reserve_chunk(self.handle, int(max_seqs), int(max_tokens), int(max_seqlen),
+                                            int(max_q_heads), int(max_blocks_per_seq)))
 
     def release_workspaces(self, graphs: bool = False):
         """Synchronise and free the workspaces that the mass decode and the decode of 4-bit caches keep for streams; with
@@ -593,6 +600,36 @@ def packed_prefill_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     _check(lib().packed_prefill_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), nseq, int(max_seqlen), T,
                                           _ptr(block_tables), block_tables.shape[1], cache.handle, hq,
                                           float(scale), _ptr(out), _stream()))
+    return out
+
+
+def paged_chunk_attention(q: torch.Tensor, cache: KVCache, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                          cu_seqlens: torch.Tensor, max_seqlen: int, scale: float, window: int = 0, sinks: int = 0,
+                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of the last tokens of each sequence over everything the cache holds of it.
+
+    Sequence i holds ``context_lens[i]`` tokens, its new ones included (append them first); its rows
+    [cu_seqlens[i], cu_seqlens[i + 1]) of q are the queries of the last of them.  Causal; with ``window`` > 0 a query sees the
+    last ``window`` tokens up to its own and the first ``sinks``.  Any mix of single tokens, drafted tokens and
+    pieces of prompts; ``max_seqlen`` is at least the longest piece."""
+    qp = _take(cache, q, "q", cache.torch_dtype, 3)
+    tables = _take(cache, block_tables, "block_tables", torch.int32, 2)
+    lens = _take(cache, context_lens, "context_lens", torch.int32, 1)
+    cu = _take(cache, cu_seqlens, "cu_seqlens", torch.int32, 1)
+    T, hq, d = q.shape
+    rows, width = block_tables.shape
+    nseq = context_lens.shape[0]
+    if d != cache.head_dim or rows != nseq or cu_seqlens.shape[0] != nseq + 1:
+        raise ValueError("shape mismatch between q, block_tables, context_lens and cu_seqlens")
+    window, sinks = _window(window, sinks, 0)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _take(cache, out, "out", cache.torch_dtype, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    _check(lib().paged_chunk_attention(qp, cache.handle, tables, width, lens, cu, nseq, int(max_seqlen), T, hq,
+                                       float(scale), window, sinks, out.data_ptr(), _stream()))
     return out
 
 

@@ -412,6 +412,18 @@ int kv_cache_reserve_mass(pkv_cache_t c, int max_seqs, int max_q_heads, int max_
     return add_spare(c, decode_mma_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq, max_mass_len));
 }
 
+int kv_cache_reserve_chunk(pkv_cache_t c, int max_seqs, int64_t max_tokens, int max_seqlen, int max_q_heads,
+                           int max_blocks_per_seq) {
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (max_seqs < 0 || max_tokens < 0 || max_seqlen < 0 || max_q_heads < 0 || max_blocks_per_seq < 0)
+        return pkv_fail(PKV_EINVAL, "negative size");
+    if (max_q_heads % c->num_kv_heads || (max_q_heads > 0 && !supported_group(max_q_heads / c->num_kv_heads)))
+        return pkv_fail(PKV_EUNSUPPORTED, "num_q_heads / num_kv_heads not in {1, 2, 4, 8}");
+    if (int r = check_device(c)) return r;
+    if (!max_seqs || !max_tokens || !max_seqlen || !max_q_heads) return PKV_OK;
+    return add_spare(c, chunk_workspace_floats(c, max_seqs, max_tokens, max_seqlen, max_q_heads, max_blocks_per_seq));
+}
+
 int kv_cache_release_workspaces(pkv_cache_t c, int graphs) {
     if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
     if (int r = check_device(c)) return r;
@@ -665,6 +677,30 @@ int paged_decode_attention_window(const void *q, pkv_cache_t c, const int32_t *b
     cudaError_t e = launch_decode_chunked(c, d, st);
     if (e != cudaSuccess) return pkv_cuda_fail(e, "decode launch");
     return PKV_OK;
+}
+
+int paged_chunk_attention(const void *q, pkv_cache_t c, const int32_t *block_tables, int max_blocks_per_seq,
+                          const int32_t *context_lens, const int32_t *cu_seqlens, int num_seqs, int max_seqlen,
+                          int64_t total_tokens, int num_q_heads, float scale, int window, int sinks, void *out,
+                          void *stream) {
+    PKV_RANGE("paged_chunk_attention");
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (num_seqs < 0 || max_seqlen < 0 || max_blocks_per_seq < 0 || total_tokens < 0)
+        return pkv_fail(PKV_EINVAL, "negative size");
+    if (window < 0 || sinks < 0 || (window == 0 && sinks > 0))
+        return pkv_fail(PKV_EINVAL, "window %d and sinks %d: window >= 0 (0: none), sinks >= 0 and 0 without a window",
+                        window, sinks);
+    if (c->kv_dtype == PKV_INT4) return pkv_fail(PKV_EUNSUPPORTED, "the chunk attention does not read 4-bit caches");
+    if (!(scale > 0.f) || !std::isfinite(scale)) return pkv_fail(PKV_EINVAL, "scale must be finite and > 0");
+    if (num_seqs == 0 || max_seqlen == 0 || total_tokens == 0) return PKV_OK;
+    if (int r = check_decode(c, q, block_tables, max_blocks_per_seq, context_lens, num_q_heads, scale, out)) return r;
+    if (!cu_seqlens) return pkv_fail(PKV_EINVAL, "NULL pointer");
+    if (overlap(q, total_tokens * num_q_heads * c->head_dim * 2, out, total_tokens * num_q_heads * c->head_dim * 2))
+        return pkv_fail(PKV_EINVAL, "out overlaps q");
+    if (int r = check_device(c)) return r;
+    ChunkLaunch p{q, out, block_tables, context_lens, cu_seqlens, max_blocks_per_seq, num_seqs, max_seqlen,
+                  total_tokens, num_q_heads, window, std::min(sinks, 1 << 30), scale};
+    return chunk_entry(c, p, static_cast<cudaStream_t>(stream));
 }
 
 static int prefill_entry(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,

@@ -281,6 +281,19 @@ struct PrefillLaunch {
 };
 cudaError_t launch_prefill(pkv_cache *c, const PrefillLaunch &p, cudaStream_t st);
 
+// attention of the last tokens of each sequence over its cache (prefill.cu)
+struct ChunkLaunch {
+    const void *q;
+    void *out;
+    const int32_t *tables, *lens, *cu;
+    int max_blocks, num_seqs, max_seqlen;
+    int64_t total_tokens;
+    int num_q_heads, window, sinks;
+    float scale;
+};
+int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st);
+int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens, int max_seqlen, int hq, int max_blocks);
+
 // Tiled-TMA map of a row-major fp16/bf16 matrix [rows][cols]: box = 64 columns x box_rows rows,
 // 128-byte swizzle, out-of-range elements read as zero (prefill.cu).
 bool pkv_tmap_2d(CUtensorMap *m, const void *base, int mt, int64_t rows, int64_t cols, int box_rows);

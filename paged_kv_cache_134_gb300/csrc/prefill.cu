@@ -102,6 +102,132 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
     }
 }
 
+// The work list of chunk and stream mode: every (sequence, row tile or pair of them, split or pair of them), heaviest first as
+// above.  A warp takes a sequence, its lanes the row tiles (long chunks have hundreds).
+template <bool STREAM>
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Args a) {
+    extern __shared__ int sh[];
+    const int R = a.cost_bins;
+    int *hist = sh, *cnt = sh + R, *warp_sums = sh + 2 * R;
+    pdl_trigger();
+    pdl_wait();
+    for (int x = threadIdx.x; x < R; x += kPlanThreads) hist[x] = cnt[x] = 0;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int4 *list = reinterpret_cast<int4 *>(a.plan + 4);
+    // row tiles of sequence i (stream) or pairs of them (chunk); 0 where its numbers make no sense, which is reported once
+    auto groups = [&](int i, bool report) -> int {
+        const int st = a.cu[i], en = a.cu[i + 1];
+        if (st < 0 || en < st || en > a.total_tokens || en - st > a.max_seqlen) {
+            if (report && lane == 0) set_error(a.err, PKV_DEVERR_CU_SEQLENS);
+            return 0;
+        }
+        if (en > st && (int64_t)a.lens[i] > (int64_t)a.max_blocks * a.bs) {
+            if (report && lane == 0) set_error(a.err, PKV_DEVERR_LENGTH);
+            return 0;
+        }
+        const int per = (STREAM ? 1 : 2) * (BM >> a.lg_group);
+        return (en - st + per - 1) / per;
+    };
+    auto visit = [&](bool report, auto &&entry) {
+        for (int i = warp; i < a.num_seqs; i += kPlanThreads / 32) {
+            const int n = groups(i, report);
+            for (int g = lane; g < n; g += 32) {
+                ChunkItem it = chunk_item<STREAM>(a, i, g, 0, 0);
+                const int ns = max(it.ns[0], it.ns[1]);
+                const int items = max(1, STREAM ? (ns + 1) / 2 : ns);
+                for (int k = 0; k < items; ++k) {
+                    if (k > 0) it = chunk_item<STREAM>(a, i, g, k, 0);
+                    entry(i, g, k, min(it.t[0].n + it.t[1].n, R - 1));
+                }
+            }
+        }
+    };
+    visit(true, [&](int, int, int, int c) { atomicAdd(&hist[c], 1); });
+    __syncthreads();
+    cta_inclusive_scan(hist, R, warp_sums);
+    const int total = hist[R - 1];
+    visit(false, [&](int i, int g, int k, int c) {
+        const int pos = total - hist[c] + atomicAdd(&cnt[c], 1);
+        if (pos < a.plan_cap) list[pos] = make_int4(i, g, k, 0);
+    });
+    if (threadIdx.x == 0) {
+        if (total > a.plan_cap) set_error(a.err, PKV_DEVERR_CU_SEQLENS); // rows that overlap: the list is cut short
+        a.plan[0] = (int)min((int64_t)total, a.plan_cap);
+        a.plan[1] = 0;
+    }
+}
+
+// The rows of a chunk whose keys went in several splits: partials joined by their maxima, one warp a (token, head) row.
+template <int D, int MT, bool STREAM>
+__global__ void __launch_bounds__(128) chunk_merge_kernel(const Args a) {
+    using M = ModelT<MT>;
+    constexpr int PER = D / 32;
+    pdl_wait();
+    const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int tok = blockIdx.x;
+    if (h >= a.hq) return;
+    // the sequence of the token: the last one that starts at or before it (the whole warp searches)
+    int lo = 0, hi = a.num_seqs;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+        const unsigned le = __ballot_sync(0xffffffffu, i < hi && a.cu[i] <= tok);
+        if (!le) return; // (starts that do not ascend)
+        lo += (31 - __clz(le)) * step;
+        hi = min(hi, lo + step);
+    }
+    const int st = a.cu[lo], en = a.cu[lo + 1];
+    if (tok < st || tok >= en || st < 0 || en > a.total_tokens || en - st > a.max_seqlen ||
+        (int64_t)a.lens[lo] > (int64_t)a.max_blocks * a.bs)
+        return;
+    const int tile = (tok - st) / (BM >> a.lg_group);
+    const ChunkItem it = chunk_item<STREAM>(a, lo, STREAM ? tile : tile / 2, 0, 0);
+    const int n = STREAM ? it.ns[0] : chunk_splits(it, tile & 1);
+    if (n <= 1) return;
+    const int64_t base = ((int64_t)tok * a.hq + h) * a.max_splits;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + base;
+    float top = -INFINITY;
+    for (int j = lane; j < n; j += 32) {
+        const float2 v = ml[j];
+        if (v.y != 0.f) top = fmaxf(top, v.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float num[PER], den = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) num[e] = 0.f;
+    constexpr int U = 4; // splits whose loads go out together
+    for (int j0 = 0; j0 < n; j0 += U) {
+        float2 w[U];
+        float v[U][PER];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            w[u] = make_float2(0.f, 0.f);
+            if (j0 + u >= n) continue;
+            w[u] = ml[j0 + u];
+            const float *src = a.ws_o + (base + j0 + u) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(src + e);
+                v[u][e] = x.x;
+                v[u][e + 1] = x.y;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (w[u].y == 0.f) continue; // no key of this split in sight (a NaN is a sum like any other)
+            const float f = fast_exp2(w[u].x - top);
+            den = fmaf(f, w[u].y, den);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) num[e] = fmaf(f, v[u][e], num[e]);
+        }
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<typename M::T *>(a.out) + ((int64_t)tok * a.hq + h) * D) + lane * (PER / 2);
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) o[e / 2] = M::pack(num[e] * inv, num[e + 1] * inv);
+}
+
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -134,6 +260,21 @@ bool make_map(CUtensorMap *m, const void *base, int mt, int64_t rows, int64_t co
                                    : mt == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const CUresult r = enc(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// q or out [T][Hq][D] as tiles of 128 (token, head of a group) rows: box = 64 dims x G heads x 128 / G tokens
+bool make_group_map(CUtensorMap *m, const void *base, int mt, int64_t tokens, int hq, int D, int G) {
+    EncodeFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)hq, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)hq * D * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(BM / G)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType dt = mt == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult r = enc(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
@@ -385,4 +526,119 @@ cudaError_t launch_cascade_prefix(pkv_cache *c, const CascadePrefixLaunch &p, cu
             : dispatch<MODE_CASCADE, false>(D, mt, m, a, pairs * p.num_q_heads, c->num_sms, st);
     g_pkv_launches++;
     return e;
+}
+
+// ---------------------------------------------------------------- chunks of new tokens over the cache
+
+namespace {
+using namespace pkv_prefill;
+
+// How a call of these sizes is cut: row tiles, key tiles of a split, splits of a row at most, items at most.
+struct ChunkShape {
+    bool stream;
+    int split_steps, max_splits;
+    int64_t groups, items; // (sequence, row tile or pair) at most; times the splits of each
+    int64_t floats(const pkv_cache *c, int64_t tokens, int hq) const {
+        const int64_t list = (4 + 4 * items + 63) / 64 * 64;
+        return list + (max_splits > 1 ? tokens * hq * max_splits * (c->head_dim + 2) : 0);
+    }
+};
+
+ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max_seqlen, int hq, int max_blocks, int window,
+                       int sinks) {
+    ChunkShape s;
+    const int G = hq / c->num_kv_heads, bs = c->block_size;
+    const int per = BM / G; // tokens of a row tile
+    // one row tile: its keys as two streams; more: tiles in pairs that share their keys
+    s.stream = max_seqlen <= per;
+    const int group = s.stream ? per : 2 * per;
+    s.groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + group - 1) / group), tokens / group + num_seqs);
+    int64_t keys = (int64_t)max_blocks * bs;
+    if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + std::min(max_seqlen, group) + sinks + 2 * bs);
+    const int64_t steps = std::max<int64_t>(1, (keys + BN - 1) / BN);
+    // splits of at most kMost key tiles, shorter where the items would not fill the SMs, but no shorter than kLeast
+    constexpr int64_t kLeast = 4, kMost = 32;
+    const int64_t share = (s.groups * c->num_kv_heads * steps + c->num_sms - 1) / c->num_sms;
+    s.split_steps = (int)std::min(kMost, std::max(kLeast, s.stream ? (share + 1) / 2 : share));
+    s.max_splits = (int)((steps + s.split_steps - 1) / s.split_steps);
+    if (s.stream) s.max_splits = steps <= 2 ? 1 : (int)(2 * ((steps + 2 * s.split_steps - 1) / (2 * s.split_steps)));
+    s.items = s.groups * (s.stream ? (s.max_splits + 1) / 2 : s.max_splits);
+    return s;
+}
+
+template <bool STREAM>
+cudaError_t launch_chunk_t(pkv_cache *c, const Args &a, const Maps &m, int64_t ctas, cudaStream_t st) {
+    const int D = c->head_dim, mt = c->model_dtype, smem = (2 * a.cost_bins + 32) * (int)sizeof(int);
+    static std::atomic<bool> allowed[64] = {};
+    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(chunk_plan_kernel<STREAM>), allowed);
+    if (e != cudaSuccess) return e;
+    e = pdl_launch(chunk_plan_kernel<STREAM>, dim3(1), dim3(kPlanThreads), smem, st, a);
+    g_pkv_launches++;
+    if (e != cudaSuccess) return e;
+    constexpr int MODE = STREAM ? MODE_STREAM : MODE_CHUNK;
+    e = c->kv_dtype == PKV_FP8_E4M3 ? dispatch<MODE, true>(D, mt, m, a, ctas, c->num_sms, st)
+                                    : dispatch<MODE, false>(D, mt, m, a, ctas, c->num_sms, st);
+    g_pkv_launches++;
+    if (e != cudaSuccess || a.max_splits <= 1) return e;
+    const dim3 grid((unsigned)a.total_tokens, (unsigned)((a.hq + 3) / 4));
+    auto merge = D == 128 ? (mt == PKV_F16 ? chunk_merge_kernel<128, PKV_F16, STREAM> : chunk_merge_kernel<128, PKV_BF16, STREAM>)
+                          : (mt == PKV_F16 ? chunk_merge_kernel<64, PKV_F16, STREAM> : chunk_merge_kernel<64, PKV_BF16, STREAM>);
+    e = pdl_launch(merge, grid, dim3(128), 0, st, a);
+    g_pkv_launches++;
+    return e;
+}
+} // namespace
+
+int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens, int max_seqlen, int hq, int max_blocks) {
+    // A call of fewer rows may be cut into more splits: what chunk_shape can make of any sizes up to these.  Splits are
+    // at most steps / 32 + 3, or as many more as fill the SMs: 2 SMs / (row tiles KV heads) of them, so that rows times
+    // those stay below 2 SMs tiles of 256 rows.
+    const int64_t steps = ((int64_t)max_blocks * c->block_size + BN - 1) / BN, splits = steps / 32 + 3;
+    const int64_t rows = tokens * hq;
+    const int64_t partials = rows * splits + std::min<int64_t>(rows * (steps / 4 + 2), 2 * 256 * (int64_t)c->num_sms);
+    const int64_t groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + 15) / 16), tokens / 16 + num_seqs);
+    const int64_t items = groups * splits + std::min<int64_t>(groups * (steps / 4 + 2), 2 * (int64_t)c->num_sms);
+    return (4 + 4 * items + 63) / 64 * 64 + partials * (c->head_dim + 2);
+}
+
+int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
+    const int hq = p.num_q_heads, D = c->head_dim, mt = c->model_dtype;
+    const ChunkShape s = chunk_shape(c, p.num_seqs, p.total_tokens, p.max_seqlen, hq, p.max_blocks, p.window, p.sinks);
+    if (s.items * c->num_kv_heads > 0x7FFFFFFF || p.total_tokens > 0x7FFFFFFF)
+        return pkv_fail(PKV_EUNSUPPORTED, "too many rows for one call");
+    const int64_t pool_rows = c->num_blocks * 2 * c->num_kv_heads * c->block_size;
+    if (pool_rows > 0x7FFFFFFFLL) return pkv_fail(PKV_EUNSUPPORTED, "pools of more than 2^31 - 1 rows");
+    Args a = base_args(c, p.scale);
+    a.out = p.out;
+    a.cu = p.cu;
+    a.tables = p.tables;
+    a.lens = p.lens;
+    a.total_tokens = p.total_tokens;
+    a.num_seqs = p.num_seqs;
+    a.max_seqlen = p.max_seqlen;
+    a.max_blocks = p.max_blocks;
+    a.hq = hq;
+    a.window = p.window;
+    a.sinks = p.sinks;
+    a.lg_group = lg2(hq / c->num_kv_heads);
+    a.split_steps = s.split_steps;
+    a.max_splits = s.max_splits;
+    a.plan_cap = s.items;
+    a.cost_bins = 2 * std::max(s.split_steps, 1) + 2;
+    Maps m;
+    if (!make_group_map(&m.q, p.q, mt, p.total_tokens, hq, D, hq / c->num_kv_heads) ||
+        !make_group_map(&m.out, p.out, mt, p.total_tokens, hq, D, hq / c->num_kv_heads) || !pool_map(&m.pool, c))
+        return pkv_fail(PKV_ECUDA, "tensor map");
+    m.k = m.v = m.pool;
+    std::lock_guard<std::mutex> lk(c->ws_mu);
+    PkvWorkspace ws;
+    if (int r = pkv_stream_workspace(c, st, s.floats(c, p.total_tokens, hq), &ws)) return r;
+    a.plan = reinterpret_cast<int *>(ws.p);
+    a.ws_o = ws.p + (4 + 4 * s.items + 63) / 64 * 64;
+    a.ws_ml = a.ws_o + p.total_tokens * hq * s.max_splits * D;
+    PkvTimer timer(c, PKV_KIND_PREFILL, st);
+    const int64_t ctas = s.items * c->num_kv_heads;
+    const cudaError_t e = s.stream ? launch_chunk_t<true>(c, a, m, ctas, st) : launch_chunk_t<false>(c, a, m, ctas, st);
+    if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
+    return PKV_OK;
 }

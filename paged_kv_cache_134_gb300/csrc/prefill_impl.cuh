@@ -12,6 +12,9 @@
 // rows sit at positions ctx[i] + r and every key is read from the pool through the block table.  In
 // cascade mode the queries are the decode queries of a batch (one row per sequence) and the keys are
 // a prefix shared by every table (section 3.3), cut into splits whose fp32 partials a merge combines.
+// In chunk and stream mode (paged_chunk_attention) the last n_i of a sequence's L_i cached tokens are its queries, the
+// group's query heads of a token lie side by side in a tile's rows (a KV head's keys are read once for all of them), the
+// keys may be cut into splits, and a window with sinks may hide keys: see ChunkItem.
 //
 // Design (one persistent CTA per SM, items taken from an atomic counter, heaviest first):
 //  * An item is two 128-row query tiles A and B.  Packed and paged modes: consecutive tiles of one
@@ -40,6 +43,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "tcgen05.cuh"
 #include "pkv_internal.h"
 
@@ -52,7 +57,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f; // log2 units
 constexpr int kCodeOff = 16384;  // E4M3 codes of a stage: row r at stage + kCodeOff + r * D
 
-enum { MODE_PACKED = 0, MODE_PAGED = 1, MODE_CASCADE = 2 };
+enum { MODE_PACKED = 0, MODE_PAGED = 1, MODE_CASCADE = 2, MODE_CHUNK = 3, MODE_STREAM = 4 };
 
 struct Args {
     const char *k, *v;  // packed [T][Hkv][D] (packed mode)
@@ -73,6 +78,10 @@ struct Args {
     // leaves an fp32 partial (m, l, unnormalised o) in workspace slot split
     float *ws_o = nullptr, *ws_ml = nullptr;
     int max_splits = 0, prefix_tokens = 0, split_tokens = 0, nps = 0;
+    // chunk and stream mode: tokens of each sequence, the new ones included; the last `window` keys (0: all) and the first
+    // `sinks` are attended to; log2 of the query heads per KV head; key tiles of a split, about
+    const int32_t *lens = nullptr;
+    int window = 0, sinks = 0, lg_group = 0, split_steps = 0;
 };
 
 // TMA descriptors of one launch: q (and out) as [rows][Hq * D] with 64-column boxes of BM rows; packed
@@ -233,6 +242,81 @@ PKV_DEV Item decode_item(const Args &a, int seq, int pr, int h) {
     return it;
 }
 
+// Chunk mode: two row tiles A and B of one (sequence, KV head) over the same keys, one split of them.  Stream mode: one row tile
+// over two neighbouring splits, for chunks of few rows, whose keys then pass through two chains of products at a time.
+// Row r of a tile is token q0 + r / G, query head h G + r % G.  Keys are counted in "seen" order: the blocks
+// that a row of the item can see, one after the other, as if nothing lay between (seen block i is logical block i, or
+// i + skip from block `from` on).  Of them [lo, hi) are hidden from every row (the rest of the sinks' last block, and what
+// lies before the first row's window); what else a row does not see is masked.
+// How the keys are cut depends on the sequence's own lengths and the call's sizes, not on the other sequences.
+struct ChunkItem : Item {
+    int from, skip, lo, hi;
+    int split;  // chunk: the split; stream: the pair of splits
+    int ns[2];  // splits of each tile's keys (1: the tile's rows are final)
+    bool zero;  // rows without keys: written as zeros by the first split's item
+};
+
+// key tiles of a split, of n in all: n / ceil(n / split_steps); stream mode: an even number of splits, unless the tiles are
+// too few to be worth a merge
+template <bool STREAM>
+PKV_DEV int steps_per_split(const Args &a, int n) {
+    if (STREAM) {
+        if (n <= 2) return 2;
+        const int k = 2 * ((n + 2 * a.split_steps - 1) / (2 * a.split_steps));
+        return (n + k - 1) / k;
+    }
+    const int k = (n + a.split_steps - 1) / a.split_steps;
+    return k > 1 ? (n + k - 1) / k : max(n, 1);
+}
+
+template <bool STREAM>
+PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
+    ChunkItem it;
+    it.seq = seq;
+    it.pr = pr;
+    it.h = h;
+    it.split = split;
+    if (seq < 0) return it;
+    const int per_tile = BM >> a.lg_group; // tokens
+    it.start = a.cu[seq];
+    it.n = a.cu[seq + 1] - it.start;
+    it.trow = seq;
+    const int before = max(a.lens[seq], 0) - it.n; // position of the first new token (negative: those rows see nothing)
+    const int tok0 = (STREAM ? pr : 2 * pr) * per_tile;
+    const int low = a.window > 0 ? max(before + tok0 - a.window + 1, 0) : 0; // first key of the first row's window
+    it.from = it.skip = it.lo = it.hi = 0;
+    if (low > a.sinks) {
+        it.from = (a.sinks + a.bs - 1) >> a.lg_bs;
+        it.skip = max((low >> a.lg_bs) - it.from, 0);
+        it.lo = a.sinks;
+        it.hi = low - (it.skip << a.lg_bs);
+    }
+    int end[2], n[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        Tile &x = it.t[t];
+        x.q0 = tok0 + (STREAM ? 0 : t * per_tile);
+        x.qlast = min(x.q0 + per_tile, it.n) - 1;
+        x.qpos0 = before + x.q0;
+        end[t] = x.q0 < it.n ? max(before + x.qlast + 1 - (it.skip << a.lg_bs), 0) : 0;
+        n[t] = (end[t] + BN - 1) / BN;
+    }
+    const int most = max(n[0], n[1]), per = steps_per_split<STREAM>(a, most);
+    it.zero = false;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        Tile &x = it.t[t];
+        const int j0 = (STREAM ? 2 * split + t : split) * per;
+        x.k0 = j0 * BN;
+        x.n = min(max(n[t] - j0, 0), per);
+        // (chunk: one end for both tiles, whose loads they share)
+        x.kend = min(STREAM ? end[t] : max(end[0], end[1]), x.k0 + per * BN);
+        it.ns[t] = (n[t] + per - 1) / per;
+    }
+    it.zero = split == 0;
+    return it;
+}
+
 // K (or V) ring index of key step j of tile t, counted from the item's first tile.  Packed and paged
 // modes share one key tile per step; cascade mode has one per tile and step.
 template <bool SHARED>
@@ -267,13 +351,20 @@ PKV_DEV void ring_entry(const Item &it, int e, int &t, int &j) {
     }
 }
 
+PKV_DEV int chunk_splits(const ChunkItem &it, int t) { return t ? it.ns[1] : it.ns[0]; }
+PKV_DEV int chunk_splits(const Item &, int) { return 1; }
+
 template <int D, int MT, int MODE, bool KV8>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Maps maps, const Args a) {
     const CUtensorMap &tq = maps.q, &tk = maps.k, &tv = maps.v, &tp = maps.pool, &to = maps.out;
     using L = Layout<D, KV8>;
     constexpr bool PAGED = MODE != MODE_PACKED;    // keys from the pool through the block table
     constexpr bool CASCADE = MODE == MODE_CASCADE; // no causal mask, fp32 split partials out
-    constexpr bool SHARED = !CASCADE;              // both tiles use the same key tiles
+    constexpr bool STREAM = MODE == MODE_STREAM;
+    constexpr bool CHUNKED = MODE == MODE_CHUNK || STREAM;
+    constexpr bool ONE_Q = CASCADE || STREAM;      // one Q tile, two key streams
+    constexpr bool SHARED = !ONE_Q;                // both tiles use the same key tiles
+    using It = std::conditional_t<CHUNKED, ChunkItem, Item>;
     constexpr bool WRITER = MODE == MODE_PACKED;   // the loaders write the item's K/V rows into the pool
     constexpr int NP = MT == PKV_BF16 ? 2 : 1;     // P parts (bf16: hi + lo)
     constexpr int EB = KV8 ? 1 : 2;                // pool bytes per element
@@ -318,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(q_full + s, 1);
-            mbar_init(q_empty + s, CASCADE ? 2 : 1); // cascade: one Q tile, read by both MMA warps
+            mbar_init(q_empty + s, ONE_Q ? 2 : 1); // cascade, stream: one Q tile, read by both MMA warps
             mbar_init(s_full + s, 1);
             mbar_init(p_full + s, 4); // one arrival per softmax warp
             mbar_init(o_full + s, 1);
@@ -360,24 +451,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if constexpr (!CASCADE) pdl_wait();
 
     const int G = a.hq / a.hkv;
+    auto make_item = [&](int seq, int pr, int h, int split) -> It {
+        (void)split;
+        if constexpr (CHUNKED)
+            return chunk_item<STREAM>(a, seq, pr, split, h);
+        else
+            return decode_item(a, seq, pr, h);
+    };
+    auto kv_head = [&](const It &it) -> int { return CHUNKED ? it.h : it.h / G; };
     auto fail = [&]() {
         set_error(a.err, PKV_DEVERR_TIMEOUT);
         *abort_flag = 1;
     };
     // the item in ring slot n % 4, once the scheduler has published it
-    auto take_item = [&](int n, bool &ok) -> Item {
+    auto take_item = [&](int n, bool &ok) -> It {
         const int sl = n & (kItemSlots - 1);
         ok = mbar_wait_hint(item_full + sl, (n / kItemSlots) & 1);
-        if (!ok) return decode_item(a, -1, 0, 0);
-        return decode_item(a, item_slot[sl].x, item_slot[sl].y, item_slot[sl].z);
+        if (!ok) return make_item(-1, 0, 0, 0);
+        return make_item(item_slot[sl].x, item_slot[sl].y, item_slot[sl].z, CHUNKED ? item_slot[sl].w : 0);
     };
     // the item's keys of ring entry e: key step j of tile t (packed / paged: one tile serves both)
     // (tiles are selected, not indexed, so that the item stays in registers)
-    auto key_base = [&](const Item &it, int e, int &t, int &j) -> int {
+    auto key_base = [&](const It &it, int e, int &t, int &j) -> int {
         ring_entry<SHARED>(it, e, t, j);
         return (t ? it.t[1].k0 : it.t[0].k0) + j * BN;
     };
-    auto key_end = [&](const Item &it, int t) -> int {
+    auto key_end = [&](const It &it, int t) -> int {
         return (SHARED || t == 0) ? it.t[0].kend : it.t[1].kend;
     };
 
@@ -477,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             if (lane == 0) mbar_arrive(ready + st);
             return true;
         };
-        const int total = a.plan[0] * a.hq;
+        const int total = a.plan[0] * (CHUNKED ? a.hkv : a.hq);
         int64_t g = 0;      // tiles issued so far (all items)
         int nq[2] = {0, 0}; // Q loads per buffer so far (warp 0)
         int64_t pend = -1;  // FP8: the issued tile still to widen
@@ -495,12 +594,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         };
         bool ok = true;
         // the scheduler (warp 0): take item m from the work list and publish it in ring slot m % 4
-        auto publish = [&](int m, bool &pok) -> Item {
+        auto publish = [&](int m, bool &pok) -> It {
             const int sl = m & (kItemSlots - 1);
             pok = true;
             if (m >= kItemSlots) pok = __all_sync(0xffffffffu, mbar_wait_hint(item_empty + sl, ((m / kItemSlots) - 1) & 1));
             int4 raw = make_int4(-1, 0, 0, 0);
-            if (!pok) return decode_item(a, -1, 0, 0);
+            if (!pok) return make_item(-1, 0, 0, 0);
             if (lane == 0) {
                 const int idx = *abort_flag ? total : atomicAdd(a.plan + 1, 1);
                 if (idx < total) {
@@ -508,6 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         const int pair = idx / a.hq; // (tile of sequences, split pair)
                         const int npr = (a.nps + 1) / 2;
                         raw = make_int4(pair / npr, pair % npr, idx % a.hq, 0);
+                    } else if constexpr (CHUNKED) {
+                        const int4 e = reinterpret_cast<const int4 *>(a.plan + 4)[idx / a.hkv];
+                        raw = make_int4(e.x, e.y, idx % a.hkv, e.z);
                     } else {
                         const int2 sq = reinterpret_cast<const int2 *>(a.plan + 4)[idx / a.hq];
                         raw = make_int4(sq.x, sq.y, idx % a.hq, 0);
@@ -516,15 +618,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 item_slot[sl].x = raw.x;
                 item_slot[sl].y = raw.y;
                 item_slot[sl].z = raw.z;
+                if constexpr (CHUNKED) item_slot[sl].w = raw.w;
                 mbar_arrive(item_full + sl);
             }
             raw.x = __shfl_sync(0xffffffffu, raw.x, 0);
             raw.y = __shfl_sync(0xffffffffu, raw.y, 0);
             raw.z = __shfl_sync(0xffffffffu, raw.z, 0);
-            return decode_item(a, raw.x, raw.y, raw.z);
+            if constexpr (CHUNKED) raw.w = __shfl_sync(0xffffffffu, raw.w, 0);
+            return make_item(raw.x, raw.y, raw.z, raw.w);
         };
         for (int n = 0; ok; ++n) {
-            Item it;
+            It it;
             if (!isK && !widen_pending()) ok = false; // before waiting for the next item
             if (!ok) break;
             if (isK) {
@@ -538,9 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     // staged in L2 now, they then arrive from L2
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        if (CASCADE ? b == 1 : it.t[b].n == 0) continue;
+                        if (ONE_Q ? b == 1 : it.t[b].n == 0) continue;
 #pragma unroll
-                        for (int c = 0; c < D / 64; ++c) tc::tma_prefetch_2d(&tq, it.h * D + c * 64, it.start + it.t[b].q0);
+                        for (int c = 0; c < D / 64; ++c) {
+                            if constexpr (CHUNKED)
+                                tc::tma_prefetch_3d(&tq, c * 64, it.h * G, it.start + it.t[b].q0);
+                            else
+                                tc::tma_prefetch_2d(&tq, it.h * D + c * 64, it.start + it.t[b].q0);
+                        }
                     }
                 }
             } else {
@@ -549,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 if (!ok) break;
             }
             if (it.seq < 0) break;
-            const int kvh = it.h / G;
+            const int kvh = kv_head(it);
             if (isK && !widen_pending()) ok = false; // before the Q loads wait for their buffers
             if (!ok) {
                 if (lane == 0) fail();
@@ -562,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // of each tile then finds both operands in place.
             // query row of each buffer's tile, -1: nothing to load
             const int qrow0 = it.t[0].n > 0 ? it.start + it.t[0].q0 : -1;
-            const int qrow1 = !CASCADE && it.t[1].n > 0 ? it.start + it.t[1].q0 : -1;
+            const int qrow1 = !ONE_Q && it.t[1].n > 0 ? it.start + it.t[1].q0 : -1;
             const int qcol = it.h * D;
             int qnext = 0; // next Q buffer to load
             auto issue_q = [&](int upto) {
@@ -575,9 +684,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         if (w) {
                             mbar_arrive_expect_tx(q_full + b, L::Q_TILE);
 #pragma unroll
-                            for (int c = 0; c < D / 64; ++c)
-                                tc::tma_load_2d(smem + L::Q + b * L::Q_TILE + c * BM * 128, &tq, qcol + c * 64, row,
-                                                q_full + b);
+                            for (int c = 0; c < D / 64; ++c) {
+                                uint8_t *dst = smem + L::Q + b * L::Q_TILE + c * BM * 128;
+                                if constexpr (CHUNKED)
+                                    tc::tma_load_3d(dst, &tq, c * 64, it.h * G, row, q_full + b);
+                                else
+                                    tc::tma_load_2d(dst, &tq, qcol + c * 64, row, q_full + b);
+                            }
                         } else {
                             fail();
                         }
@@ -602,8 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 int t, j;
                 const int kb = key_base(it, e, t, j);
                 const int lb = (kb >> a.lg_bs) + lane;
+                int at = lb;
+                if constexpr (CHUNKED) at += lb >= it.from ? it.skip : 0;
                 return (lane < (BN >> a.lg_bs) && (lb << a.lg_bs) < key_end(it, t))
-                           ? a.tables[(int64_t)it.trow * a.max_blocks + lb]
+                           ? a.tables[(int64_t)it.trow * a.max_blocks + at]
                            : -1;
             };
             int nxt = PAGED && ne > 0 ? entry(0) : -1;
@@ -629,7 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     const bool good = has && b >= 0 && b < a.num_blocks;
                     if (!isK && has && !good) set_error(a.err, PKV_DEVERR_BLOCK_ID);
                     // K: every usable block whole (rows past the end are masked); V: only full blocks
-                    const bool full_blk = good && (isK || ((lb + 1) << a.lg_bs) <= send);
+                    bool full_blk = good && (isK || ((lb + 1) << a.lg_bs) <= send);
+                    if constexpr (CHUNKED) // (a block with tokens that no row sees: its other V rows one by one)
+                        full_blk = full_blk && (isK || (lb << a.lg_bs) >= it.hi || ((lb + 1) << a.lg_bs) <= it.lo);
                     const unsigned fullmask = __ballot_sync(0xffffffffu, full_blk);
                     if (lane == 0) mbar_expect_tx(full + st, (uint32_t)__popc(fullmask) * (uint32_t)(a.bs * D * EB));
                     __syncwarp();
@@ -651,7 +768,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             const int bl = __shfl_sync(0xffffffffu, good ? b : -1, l);
                             if ((fullmask >> l) & 1u) continue;
                             uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                            if (bl >= 0 && kbase + r < send)
+                            bool held = bl >= 0 && kbase + r < send;
+                            if constexpr (CHUNKED) held = held && !(kbase + r >= it.lo && kbase + r < it.hi);
+                            if (held)
                                 x = *reinterpret_cast<const uint4 *>(
                                     a.pool + ((((int64_t)bl * 2 + 1) * a.hkv + kvh) * a.tile_elems +
                                               (int64_t)(r - (l << a.lg_bs)) * D) * EB + cc * 16);
@@ -738,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
         };
         for (int n = 0; ok; ++n) {
-            const Item it = take_item(n, ok);
+            const It it = take_item(n, ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || it.seq < 0) break;
             const int nt = t ? it.t[1].n : it.t[0].n;
@@ -747,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // without waiting for their loads
             const int n_other = t ? it.t[0].n : it.t[1].n;
             const int ne = ring_count<SHARED>(it);
-            const int qb = CASCADE ? 0 : t;
+            const int qb = ONE_Q ? 0 : t;
             // ring entries of the item this warp has passed (cascade: the other tile's are skipped)
             int ke = 0, ve = 0;
             auto owner = [&](int e) -> int {
@@ -785,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 if (j == nt - 1) {
                     // cascade: the last S of the tile has read Q (other modes: the epilogue, which stages
                     // the tile's output in the Q buffer, frees it)
-                    if constexpr (CASCADE) tc::commit_warp(q_empty + qb);
+                    if constexpr (ONE_Q) tc::commit_warp(q_empty + qb);
                     qph ^= 1u;
                 }
             };
@@ -853,8 +972,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 // the other tile's remaining entries
                 for (; ke < ne; ++ke) adv(kst, kph, NKS);
                 for (; ve < ne; ++ve) adv(vst, vph, NVS);
-                if (nt == 0 && ok) {
-                    // cascade: no split for this tile; its share of the Q buffer once Q has landed
+                if (nt == 0 && ok && (CASCADE || it.t[0].n > 0)) {
+                    // cascade, stream: no split for this tile; its share of the Q buffer once Q has landed
                     ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full + qb, qph));
                     if (ok && lane == 0) mbar_arrive(q_empty + qb);
                     qph ^= 1u;
@@ -897,15 +1016,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             return false;
         };
         for (int n = 0; ok; ++n) {
-            const Item it = take_item(n, ok);
+            const It it = take_item(n, ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || it.seq < 0) break;
             const Tile x = t ? it.t[1] : it.t[0];
             const int n0 = it.t[0].n, n1 = it.t[1].n;
             if (x.n > 0) {
-                const int kvh = it.h / G;
+                const int kvh = kv_head(it);
                 const float sl = KV8 ? a.scale_log2 * a.k_scale[kvh] : a.scale_log2;
-                const int qpos = x.qpos0 + r; // absolute position of this row (causal modes)
+                const int qpos = x.qpos0 + (CHUNKED ? r >> a.lg_group : r); // absolute position of this row (causal modes)
                 float m_use = -INFINITY, l = 0.f;
                 for (int j = 0; j < x.n && ok; ++j) {
                     // (spinning: S complete is on the critical path; a suspended wait wakes later)
@@ -926,6 +1045,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 #pragma unroll
                             for (int c = 0; c < BN; ++c)
                                 if (c >= lim) sr[c] = 0xFF800000u; // -inf
+                        }
+                    } else if constexpr (CHUNKED) {
+                        // seen key kbase + c is at most this row's position up to c = upto - 1, inside its window from
+                        // c = since on, a sink below c = first; only tiles on either edge of some row's sight
+                        const int hidden = it.skip << a.lg_bs; // tokens between the sinks' blocks and the window's
+                        const int plast = x.qpos0 + x.qlast - x.q0; // position of the tile's last row
+                        const bool late = kbase + BN - 1 + hidden > x.qpos0;
+                        const bool early = a.window > 0 && plast - a.window + 1 - hidden > kbase;
+                        const int upto = qpos + 1 - hidden - kbase;
+                        if (early) {
+                            const int since = max(qpos - a.window + 1, 0) - hidden - kbase;
+                            const int first = min(a.sinks, qpos + 1) - kbase;
+#pragma unroll
+                            for (int c = 0; c < BN; ++c)
+                                if ((c >= upto || c < since) && c >= first) sr[c] = 0xFF800000u; // -inf
+                        } else if (late) {
+#pragma unroll
+                            for (int c = 0; c < BN; ++c)
+                                if (c >= upto) sr[c] = 0xFF800000u; // -inf
                         }
                     } else if (kbase + BN - 1 > x.qpos0) {
                         // causal mask, only on tiles that reach past the tile's first query row
@@ -1029,15 +1167,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                                                  __uint_as_float(o[4 * e + 2]) * vs, __uint_as_float(o[4 * e + 3]) * vs);
                     }
                     if (valid) reinterpret_cast<float2 *>(a.ws_ml)[idx] = make_float2(m_use, l);
+                } else if (CHUNKED && chunk_splits(it, t) > 1) {
+                    if constexpr (CHUNKED) {
+                        // fp32 partial of one of several splits, as in cascade mode; the Q buffer is not used
+                        const int tok = x.q0 + (r >> a.lg_group);
+                        const int split = STREAM ? 2 * it.split + t : it.split;
+                        const int64_t idx =
+                            ((int64_t)(it.start + tok) * a.hq + it.h * G + (r & (G - 1))) * a.max_splits + split;
+                        uint32_t o[D];
+#pragma unroll
+                        for (int cc = 0; cc < D / 32; ++cc) tc::ld32(tO + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[cc * 32]));
+                        tc::wait_ld();
+                        if (!ONE_Q && (warp & 3) == 0 && lane == 0) mbar_arrive(q_empty + t);
+                        if (tok <= x.qlast) {
+                            float4 *dst = reinterpret_cast<float4 *>(a.ws_o + idx * D);
+#pragma unroll
+                            for (int e = 0; e < D / 4; ++e)
+                                dst[e] = make_float4(__uint_as_float(o[4 * e]) * vs, __uint_as_float(o[4 * e + 1]) * vs,
+                                                     __uint_as_float(o[4 * e + 2]) * vs, __uint_as_float(o[4 * e + 3]) * vs);
+                            reinterpret_cast<float2 *>(a.ws_ml)[idx] = make_float2(m_use, l);
+                        }
+                    }
                 } else {
-                    const int row = x.q0 + r;
-                    const float inv = vs / l;
+                    // (chunk and stream mode: rows are (token, head) pairs, and one may see no key)
+                    const int row = CHUNKED ? x.q0 + (r >> a.lg_group) : x.q0 + r;
+                    const int tile_rows = CHUNKED ? BM >> a.lg_group : BM;
+                    const float inv = CHUNKED && l == 0.f ? 0.f : vs / l;
                     uint32_t o[D]; // the whole row in one tensor-memory round trip
 #pragma unroll
                     for (int cc = 0; cc < D / 32; ++cc) tc::ld32(tO + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[cc * 32]));
                     tc::wait_ld();
                     const bool lead = (warp & 3) == 0 && lane == 0;
-                    if (x.q0 + BM <= it.n) {
+                    if (!STREAM && x.q0 + tile_rows <= it.n) {
                         // a whole tile of the sequence's rows: staged in this tile's Q buffer (free, since the
                         // tile's last S has completed) in the Q tile's own 128-byte swizzled layout, then one TMA
                         // store per 64 columns writes coalesced rows; the buffer goes back to the Q loader once
@@ -1060,8 +1221,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                             // the four warps' rows are staged (bounded wait: a warp that gave up never arrives)
                             if (mbar_wait(epi + t, nepi & 1)) {
 #pragma unroll
-                                for (int h = 0; h < D / 64; ++h)
-                                    tc::tma_store_2d(&to, it.h * D + h * 64, it.start + x.q0, stage + h * BM * 128);
+                                for (int h = 0; h < D / 64; ++h) {
+                                    if constexpr (CHUNKED)
+                                        tc::tma_store_3d(&to, h * 64, it.h * G, it.start + x.q0, stage + h * BM * 128);
+                                    else
+                                        tc::tma_store_2d(&to, it.h * D + h * 64, it.start + x.q0, stage + h * BM * 128);
+                                }
                                 tc::bulk_commit();
                                 tc::bulk_wait_read_all();
                                 mbar_arrive(q_empty + t);
@@ -1074,9 +1239,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     } else {
                         // the sequence's last, partial tile: row by row, so that no row of the next sequence is
                         // written; the Q buffer is not used here and is free already
-                        if (lead) mbar_arrive(q_empty + t);
+                        if (!STREAM && lead) mbar_arrive(q_empty + t);
                         if (row < it.n) {
-                            T *orow = static_cast<T *>(a.out) + ((int64_t)(it.start + row) * a.hq + it.h) * D;
+                            const int head = CHUNKED ? it.h * G + (r & (G - 1)) : it.h;
+                            T *orow = static_cast<T *>(a.out) + ((int64_t)(it.start + row) * a.hq + head) * D;
 #pragma unroll
                             for (int cc = 0; cc < D / 8; ++cc) {
                                 uint32_t w[4];
@@ -1092,6 +1258,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_free + t); // O has been read out; the tile's next first P V may overwrite it
+            } else if constexpr (CHUNKED) {
+                // rows that see no key at all
+                const int tok = x.q0 + (r >> a.lg_group);
+                if (it.zero && chunk_splits(it, t) == 0 && tok <= x.qlast && !(STREAM && t == 1)) {
+                    using T = typename ModelT<MT>::T;
+                    uint4 *orow = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) +
+                                                            ((int64_t)(it.start + tok) * a.hq + it.h * G + (r & (G - 1))) * D);
+#pragma unroll
+                    for (int cc = 0; cc < D / 8; ++cc) orow[cc] = make_uint4(0u, 0u, 0u, 0u);
+                }
             }
             steps0 += n0;
             steps1 += n1;
@@ -1140,5 +1316,9 @@ PKV_ATTN_EXTERN(MODE_PAGED, false)
 PKV_ATTN_EXTERN(MODE_PAGED, true)
 PKV_ATTN_EXTERN(MODE_CASCADE, false)
 PKV_ATTN_EXTERN(MODE_CASCADE, true)
+PKV_ATTN_EXTERN(MODE_CHUNK, false)
+PKV_ATTN_EXTERN(MODE_CHUNK, true)
+PKV_ATTN_EXTERN(MODE_STREAM, false)
+PKV_ATTN_EXTERN(MODE_STREAM, true)
 
 } // namespace pkv_prefill
