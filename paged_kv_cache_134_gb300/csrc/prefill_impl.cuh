@@ -96,15 +96,20 @@ struct Maps {
 // and are widened into the 16-bit layout of the same stage: for D = 128 the codes are the upper half
 // of the stage, which each row's widening thread reads whole before it writes it; for D = 64 they
 // follow the 16 KB tile.
-template <int D, bool KV8>
+//
+// ONE_Q (cascade, stream): one Q tile, and the rings in halves, one per key stream (tile t has stages t, t + 2): a
+// stage's barriers then see every phase waited for by one issuer.  (In one ring for both streams, an issuer would come
+// back to a stage after two of its phases, and find the one before the other stream's, whose parity is the same,
+// complete where its own tile is still on its way.)
+template <int D, bool KV8, bool ONE_Q = false>
 struct Layout {
-    static constexpr int NKS = D == 128 ? 3 : 4; // K stages (a K stage frees once S of both tiles is done)
-    static constexpr int NVS = D == 128 ? 2 : 3; // V stages (a V stage frees after P V of both tiles)
+    static constexpr int NKS = D == 128 && !ONE_Q ? 3 : 4; // K stages (a K stage frees once S of both tiles is done)
+    static constexpr int NVS = D == 128 ? 2 : (ONE_Q ? 4 : 3); // V stages (a V stage frees after P V of both tiles)
     static constexpr int Q_TILE = BM * D * 2;
     static constexpr int TILE = BN * D * 2;
     static constexpr int STAGE = (KV8 && D == 64) ? TILE + BN * D : TILE;
     static constexpr int Q = 0;
-    static constexpr int K0 = Q + 2 * Q_TILE;
+    static constexpr int K0 = Q + (ONE_Q ? 1 : 2) * Q_TILE;
     static constexpr int V0 = K0 + NKS * STAGE;
     static constexpr int BAR = V0 + NVS * STAGE;
     static constexpr int NBARS = 4 + 4 + 2 + 2 + 4 * NKS + 4 * NVS + 2 + 2 + 2 + 2 + 2 + 2;
@@ -317,18 +322,8 @@ PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
     return it;
 }
 
-// K (or V) ring index of key step j of tile t, counted from the item's first tile.  Packed and paged
-// modes share one key tile per step; cascade mode has one per tile and step.
-template <bool SHARED>
-PKV_DEV int ring_index(const Item &it, int j, int t) {
-    if constexpr (SHARED) {
-        return j;
-    } else {
-        const int mn = min(it.t[0].n, it.t[1].n);
-        const int before = 2 * min(j, mn) + max(0, j - mn);
-        return before + ((t == 1 && j < it.t[0].n) ? 1 : 0);
-    }
-}
+// Loads of K (or V) tiles of an item, in their order.  Packed, paged and chunk modes share one key tile per step; cascade
+// and stream mode have one per tile and step.
 template <bool SHARED>
 PKV_DEV int ring_count(const Item &it) {
     return SHARED ? max(it.t[0].n, it.t[1].n) : it.t[0].n + it.t[1].n;
@@ -357,7 +352,7 @@ PKV_DEV int chunk_splits(const Item &, int) { return 1; }
 template <int D, int MT, int MODE, bool KV8>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Maps maps, const Args a) {
     const CUtensorMap &tq = maps.q, &tk = maps.k, &tv = maps.v, &tp = maps.pool, &to = maps.out;
-    using L = Layout<D, KV8>;
+    using L = Layout<D, KV8, MODE == MODE_CASCADE || MODE == MODE_STREAM>;
     constexpr bool PAGED = MODE != MODE_PACKED;    // keys from the pool through the block table
     constexpr bool CASCADE = MODE == MODE_CASCADE; // no causal mask, fp32 split partials out
     constexpr bool STREAM = MODE == MODE_STREAM;
@@ -565,10 +560,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 wj[st] = -1;
             }
         };
-        // FP8: widen ring entry gw (landed), then release it to the MMAs
-        auto widen = [&](int64_t gw) -> bool {
-            const int st = (int)(gw % ns);
-            if (!__all_sync(0xffffffffu, mbar_wait_hint(full + st, (uint32_t)((gw / ns) & 1)))) return false;
+        // The stage of the next load of tile t, and how often it was filled before: stages taken in turn, by all loads or
+        // (ONE_Q) by those of each key stream; `g` counts all loads issued, `gt` those of each stream.
+        int64_t g = 0;
+        int gt[2] = {0, 0};
+        auto next_stage = [&](int t, int &st, int &round) {
+            if constexpr (ONE_Q) {
+                const int c = t ? gt[1] : gt[0];
+                st = t + 2 * (c % (ns / 2));
+                round = c / (ns / 2);
+            } else {
+                st = (int)(g % ns);
+                round = (int)(g / ns);
+            }
+        };
+        // FP8: widen the tile in stage st (landed), then release it to the MMAs
+        auto widen = [&](int st, uint32_t parity) -> bool {
+            if (!__all_sync(0xffffffffu, mbar_wait_hint(full + st, parity))) return false;
             uint8_t *stage = ring + st * L::STAGE;
             for (int r = lane; r < BN; r += 32) widen_row<D, MT>(stage, r);
             fence_proxy_async_smem(); // the MMAs read the widened tile through the async proxy
@@ -577,15 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             return true;
         };
         const int total = a.plan[0] * (CHUNKED ? a.hkv : a.hq);
-        int64_t g = 0;      // tiles issued so far (all items)
         int nq[2] = {0, 0}; // Q loads per buffer so far (warp 0)
-        int64_t pend = -1;  // FP8: the issued tile still to widen
+        int pend = -1;      // FP8: the issued tile still to widen: its stage, and its phase's parity in bit 8
         // FP8: widen the pending tile; done before this warp can block on anything an MMA of that tile
         // may be holding up (the next tile's stage, the next item, the next item's Q buffer)
         auto widen_pending = [&]() -> bool {
             if constexpr (KV8) {
                 if (pend >= 0) {
-                    const bool w = widen(pend);
+                    const bool w = widen(pend & 0xFF, (uint32_t)pend >> 8);
                     pend = -1;
                     return w;
                 }
@@ -722,11 +729,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                            : -1;
             };
             int nxt = PAGED && ne > 0 ? entry(0) : -1;
-            int issued = 0;
             for (int e = 0; e < ne && ok; ++e) {
-                const int64_t gg = g + e;
-                const int st = (int)(gg % ns);
-                const int64_t round = gg / ns;
+                int tile = 0, step = 0, st, round;
+                if constexpr (ONE_Q) ring_entry<SHARED>(it, e, tile, step);
+                next_stage(tile, st, round);
                 // FP8: the previous tile is widened first (an MMA waits for it), then this one loads
                 if (!widen_pending()) ok = false;
                 flush_write(st); // the stage's previous tile leaves for the pool before the refill
@@ -803,12 +809,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         wpar[st] = (int)(round & 1);
                     }
                 }
-                issued = e + 1;
-                if constexpr (KV8) pend = gg;
+                ++g;
+                if constexpr (ONE_Q) ++(tile ? gt[1] : gt[0]);
+                if constexpr (KV8) pend = st | (round & 1) << 8;
                 if (isK && e < 2) issue_q(e); // Q_A after K tile 0, Q_B after K tile 1
             }
             if (isK) issue_q(1); // items of fewer than two key tiles
-            g += issued; // tiles issued so far, all items
             if (!isK && lane == 0) mbar_arrive(item_empty + (n & (kItemSlots - 1)));
             if (!ok) {
                 if (lane == 0) fail();
@@ -823,8 +829,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         if constexpr (WRITER) tc::bulk_wait_all();
         // the last loads must land before this CTA's shared memory goes away
         if (lane == 0) {
-            for (int64_t gg = g > ns ? g - ns : 0; gg < g; ++gg)
-                if (!mbar_wait_hint(full + gg % ns, (gg / ns) & 1)) set_error(a.err, PKV_DEVERR_TIMEOUT);
+            if constexpr (ONE_Q) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    for (int c = max(gt[t] - ns / 2, 0); c < gt[t]; ++c)
+                        if (!mbar_wait_hint(full + t + 2 * (c % (ns / 2)), (c / (ns / 2)) & 1)) set_error(a.err, PKV_DEVERR_TIMEOUT);
+            } else {
+                for (int64_t gg = g > ns ? g - ns : 0; gg < g; ++gg)
+                    if (!mbar_wait_hint(full + gg % ns, (gg / ns) & 1)) set_error(a.err, PKV_DEVERR_TIMEOUT);
+            }
             if (isK)
                 for (int b = 0; b < 2; ++b)
                     if (nq[b] >= 1 && !mbar_wait_hint(q_full + b, (nq[b] - 1) & 1)) set_error(a.err, PKV_DEVERR_TIMEOUT);
@@ -846,7 +859,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const uint64_t dV = tc::smem_desc(smem_u32(smem + L::V0), BN * 128, 1024);
         const uint32_t tS = tmem + (uint32_t)(t * BN), tO = tmem + (uint32_t)(2 * BN + t * D);
         bool any_mma = false, ok = true;
-        // ring cursors: the stage of the K (V) entry to look at next and the parity of its phase
+        // ring cursors: the stage of the K (V) entry to look at next and the parity of its phase (ONE_Q: of the tile's own
+        // half of the ring)
+        constexpr int KN = ONE_Q ? NKS / 2 : NKS, VN = ONE_Q ? NVS / 2 : NVS;
+        auto stage = [&](uint32_t st) -> uint32_t { return ONE_Q ? (uint32_t)t + 2 * st : st; };
         uint32_t kst = 0, kph = 0, vst = 0, vph = 0;
         uint32_t pph = 0, oph = 0, qph = 0; // phase parities of this tile's barriers
         bool o_used = false;
@@ -861,32 +877,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || it.seq < 0) break;
             const int nt = t ? it.t[1].n : it.t[0].n;
-            // shared modes: key entries j >= n_other are read by this tile alone, which then gives the
-            // stage's release for both tiles (two commits), so the other tile's issuer skips them
-            // without waiting for their loads
-            const int n_other = t ? it.t[0].n : it.t[1].n;
             const int ne = ring_count<SHARED>(it);
             const int qb = ONE_Q ? 0 : t;
-            // ring entries of the item this warp has passed (cascade: the other tile's are skipped)
-            int ke = 0, ve = 0;
-            auto owner = [&](int e) -> int {
-                int tt, jj;
-                ring_entry<SHARED>(it, e, tt, jj);
-                return tt;
-            };
-            // move a cursor to this tile's next entry (cascade: over the other tile's entries)
-            auto skip_others = [&](int &pos, uint32_t &st, uint32_t &ph, int nstage) {
-                if (!SHARED) {
-                    while (pos < ne && owner(pos) != t) {
-                        adv(st, ph, nstage);
-                        ++pos;
-                    }
-                }
-            };
             // S(j) = Q K^T into the tile's S columns (its MMAs only; the caller commits)
             auto mmas_s = [&]() {
                 const uint64_t a0 = dQ + (uint64_t)((qb * L::Q_TILE) >> 4);
-                const uint64_t b0 = dK + (uint64_t)(kst * (L::STAGE >> 4));
+                const uint64_t b0 = dK + (uint64_t)(stage(kst) * (L::STAGE >> 4));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const int c = k >> 2, kk = k & 3;
@@ -897,10 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // after S(j): S complete, this warp's share of the K stage, and Q after the tile's last S
             auto commit_s = [&](int j) {
                 tc::commit_warp(s_full + t);
-                tc::commit_warp(k_empty + kst); // this warp's share of the K stage
-                if (SHARED && j >= n_other) tc::commit_warp(k_empty + kst); // and the other tile's
-                adv(kst, kph, NKS);
-                ++ke;
+                tc::commit_warp(k_empty + stage(kst)); // this warp's share of the K stage
+                adv(kst, kph, KN);
                 if (j == nt - 1) {
                     // cascade: the last S of the tile has read Q (other modes: the epilogue, which stages
                     // the tile's output in the Q buffer, frees it)
@@ -910,8 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             };
             // S(0): Q and the first K tile
             auto first_s = [&]() -> bool {
-                skip_others(ke, kst, kph, NKS);
-                if (!__all_sync(0xffffffffu, mbar_wait(k_ready + kst, kph) && mbar_wait(q_full + qb, qph))) return false;
+                if (!__all_sync(0xffffffffu, mbar_wait(k_ready + stage(kst), kph) && mbar_wait(q_full + qb, qph))) return false;
                 tc::fence_after_sync();
                 any_mma = true;
                 mmas_s();
@@ -922,21 +915,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             // P is read from tensor memory where the softmax left it (over S), and S(j + 1) overwrites
             // those columns only after P V(j) has read them (one thread's MMAs complete in order).
             auto step = [&](int j) -> bool {
-                skip_others(ve, vst, vph, NVS);
                 const bool more = j + 1 < nt;
                 // the next K tile is normally in place already; checked first, so that nothing but the
                 // softmax is waited for between the two groups
-                if (more) {
-                    skip_others(ke, kst, kph, NKS);
-                    if (!__all_sync(0xffffffffu, mbar_wait(k_ready + kst, kph))) return false;
-                }
-                bool w = mbar_wait(v_ready + vst, vph) && mbar_wait(p_full + t, pph);
+                if (more && !__all_sync(0xffffffffu, mbar_wait(k_ready + stage(kst), kph))) return false;
+                bool w = mbar_wait(v_ready + stage(vst), vph) && mbar_wait(p_full + t, pph);
                 // the previous item's epilogue of this tile has read O out of tensor memory
                 if (j == 0 && o_used) w = w && mbar_wait(o_free + t, oph ^ 1u);
                 if (!__all_sync(0xffffffffu, w)) return false;
                 pph ^= 1u;
                 tc::fence_after_sync();
-                const uint64_t b0 = dV + (uint64_t)(vst * (L::STAGE >> 4));
+                const uint64_t b0 = dV + (uint64_t)(stage(vst) * (L::STAGE >> 4));
 #pragma unroll
                 for (int part = 0; part < NP; ++part)
 #pragma unroll
@@ -946,10 +935,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 // the V stage share goes out before S(j + 1) is issued (a commit covers every earlier MMA of
                 // this thread, so issued later it would hold the stage until S(j + 1) completes too); the
                 // P V MMAs queued ahead keep the pipe busy meanwhile
-                tc::commit_warp(v_empty + vst); // this warp's share of the V stage
-                if (SHARED && j >= n_other) tc::commit_warp(v_empty + vst); // and the other tile's
-                adv(vst, vph, NVS);
-                ++ve;
+                tc::commit_warp(v_empty + stage(vst)); // this warp's share of the V stage
+                adv(vst, vph, VN);
                 if (more) mmas_s();
                 if (!more) {
                     tc::commit_warp(o_full + t); // the tile's O is complete once this commit arrives
@@ -963,15 +950,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             if (nt > 0) ok = first_s();
             for (int j = 0; j < nt && ok; ++j) ok = step(j);
             if constexpr (SHARED) {
-                // key tiles only the other tile reads: released by that tile (see n_other)
-                for (; ke < ne; ++ke, ++ve) {
-                    adv(kst, kph, NKS);
-                    adv(vst, vph, NVS);
+                // Key tiles that only the other tile reads: this warp's share of their release, once they have landed.  (Passed
+                // over without a wait, or released by the other tile's issuer for both, this warp could come to a stage
+                // two of its phases ahead, and find the phase of the same parity before it complete.)
+                for (int e = nt; e < ne && ok; ++e) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_hint(k_ready + kst, kph));
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(k_empty + kst);
+                    adv(kst, kph, KN);
+                    ok = __all_sync(0xffffffffu, mbar_wait_hint(v_ready + vst, vph));
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(v_empty + vst);
+                    adv(vst, vph, VN);
                 }
             } else {
-                // the other tile's remaining entries
-                for (; ke < ne; ++ke) adv(kst, kph, NKS);
-                for (; ve < ne; ++ve) adv(vst, vph, NVS);
                 if (nt == 0 && ok && (CASCADE || it.t[0].n > 0)) {
                     // cascade, stream: no split for this tile; its share of the Q buffer once Q has landed
                     ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full + qb, qph));
@@ -1293,7 +1285,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 template <int D, int MT, int MODE, bool KV8>
 cudaError_t launch_attn(const Maps &m, const Args &a, int64_t max_ctas, int num_sms, cudaStream_t st) {
     auto kern = attn_kernel<D, MT, MODE, KV8>;
-    const int smem = Layout<D, KV8>::TOTAL;
+    const int smem = Layout<D, KV8, MODE == MODE_CASCADE || MODE == MODE_STREAM>::TOTAL;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = std::min<int64_t>(max_ctas, (int64_t)num_sms);

@@ -281,3 +281,22 @@ def test_a_conversation_as_it_runs(kv, model, norm):
         R.check(out.double().cpu().numpy(), ref, model, p, terms)
         at = e
     assert at == total and cache.check_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,kv,model,longest", [
+    (16, 8, 128, 16, "fp8", "bf16", 4), (8, 8, 128, 16, "f16", "f16", 5), (16, 8, 64, 8, "fp8", "f16", 3), (16, 8, 64, 16, "bf16", "bf16", 8),
+    (16, 8, 128, 16, "fp8", "bf16", 150), (8, 8, 128, 8, "bf16", "bf16", 200), (16, 8, 64, 32, "fp8", "f16", 90),
+    (8, 8, 64, 16, "f16", "f16", 300)])
+def test_many_items_of_unequal_lengths(hq, hkv, d, bs, kv, model, longest):
+    """Several items a CTA, the tiles of an item of one to a dozen key tiles each, some absent: stages of the rings change
+    hands at every boundary in another order."""
+    g = np.random.default_rng(longest)
+    lens = [int(min(1500, np.exp(g.normal(np.log(300), 1)))) + 1 for _ in range(190)] + [0, 1, 2]
+    new = [int(min(n, 1 + longest * g.random() ** 2)) for n in lens]
+    x = Setup(lens, hq, hkv, d, bs, kv, model)
+    got = run(x, new, most=longest)
+    cu, q, _ = chunks(x, new)
+    first = P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, longest, 0.1)
+    assert got.shape == first.shape
+    for _ in range(6):
+        assert torch.equal(first, P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, longest, 0.1))
