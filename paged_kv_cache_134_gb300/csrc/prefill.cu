@@ -115,27 +115,12 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Args a) 
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int4 *list = reinterpret_cast<int4 *>(a.plan + 4);
-    // row tiles of sequence i (stream) or pairs of them (chunk); 0 where its numbers make no sense, which is reported once
-    auto groups = [&](int i, bool report) -> int {
-        const int st = a.cu[i], en = a.cu[i + 1];
-        if (st < 0 || en < st || en > a.total_tokens || en - st > a.max_seqlen) {
-            if (report && lane == 0) set_error(a.err, PKV_DEVERR_CU_SEQLENS);
-            return 0;
-        }
-        if (en > st && (int64_t)a.lens[i] > (int64_t)a.max_blocks * a.bs) {
-            if (report && lane == 0) set_error(a.err, PKV_DEVERR_LENGTH);
-            return 0;
-        }
-        const int per = (STREAM ? 1 : 2) * (BM >> a.lg_group);
-        return (en - st + per - 1) / per;
-    };
     auto visit = [&](bool report, auto &&entry) {
         for (int i = warp; i < a.num_seqs; i += kPlanThreads / 32) {
-            const int n = groups(i, report);
+            const int n = chunk_groups<STREAM>(a, i, report && lane == 0);
             for (int g = lane; g < n; g += 32) {
                 ChunkItem it = chunk_item<STREAM>(a, i, g, 0, 0);
-                const int ns = max(it.ns[0], it.ns[1]);
-                const int items = max(1, STREAM ? (ns + 1) / 2 : ns);
+                const int items = chunk_parts<STREAM>(it);
                 for (int k = 0; k < items; ++k) {
                     if (k > 0) it = chunk_item<STREAM>(a, i, g, k, 0);
                     entry(i, g, k, min(it.t[0].n + it.t[1].n, R - 1));
@@ -538,6 +523,13 @@ struct ChunkShape {
     bool stream;
     int split_steps, max_splits;
     int64_t groups, items; // (sequence, row tile or pair) at most; times the splits of each
+    int max_groups, max_parts; // of a sequence; of a group's keys
+    // Few items: no list and no launch for it (one sequence of 2047 tokens: 16 us for 23).  Many: heaviest first from a list
+    // (32 sequences of up to 4096 tokens, 32 heads, by turns: 224 us for 205).
+    bool direct(const pkv_cache *c, int num_seqs) const { return rect(c, num_seqs) <= 2 * (int64_t)c->num_sms; }
+    int64_t rect(const pkv_cache *c, int num_seqs) const {
+        return (int64_t)num_seqs * max_groups * max_parts * c->num_kv_heads;
+    }
     int64_t floats(const pkv_cache *c, int64_t tokens, int hq) const {
         const int64_t list = (4 + 4 * items + 63) / 64 * 64;
         return list + (max_splits > 1 ? tokens * hq * max_splits * (c->head_dim + 2) : 0);
@@ -556,25 +548,32 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
     int64_t keys = (int64_t)max_blocks * bs;
     if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + std::min(max_seqlen, group) + sinks + 2 * bs);
     const int64_t steps = std::max<int64_t>(1, (keys + BN - 1) / BN);
-    // splits of at most kMost key tiles, shorter where the items would not fill the SMs, but no shorter than kLeast
-    constexpr int64_t kLeast = 4, kMost = 32;
+    // splits of at most kMost key tiles, shorter where the items would not fill the SMs
+    // (one sequence of 2047 tokens, 56 rows: 16 us with one tile a split, 20 with two, 25 with four; 512 tokens after
+    // 131071: 1.11 ms with 32 tiles at most, 1.24 with 16, 1.16 with 64)
+    constexpr int64_t kLeast = 1, kMost = 32;
     const int64_t share = (s.groups * c->num_kv_heads * steps + c->num_sms - 1) / c->num_sms;
     s.split_steps = (int)std::min(kMost, std::max(kLeast, s.stream ? (share + 1) / 2 : share));
     s.max_splits = (int)((steps + s.split_steps - 1) / s.split_steps);
     if (s.stream) s.max_splits = steps <= 2 ? 1 : (int)(2 * ((steps + 2 * s.split_steps - 1) / (2 * s.split_steps)));
-    s.items = s.groups * (s.stream ? (s.max_splits + 1) / 2 : s.max_splits);
+    s.max_groups = (max_seqlen + group - 1) / group;
+    s.max_parts = s.stream ? (s.max_splits + 1) / 2 : s.max_splits;
+    s.items = s.groups * s.max_parts;
     return s;
 }
 
 template <bool STREAM>
 cudaError_t launch_chunk_t(pkv_cache *c, const Args &a, const Maps &m, int64_t ctas, cudaStream_t st) {
     const int D = c->head_dim, mt = c->model_dtype, smem = (2 * a.cost_bins + 32) * (int)sizeof(int);
-    static std::atomic<bool> allowed[64] = {};
-    cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(chunk_plan_kernel<STREAM>), allowed);
-    if (e != cudaSuccess) return e;
-    e = pdl_launch(chunk_plan_kernel<STREAM>, dim3(1), dim3(kPlanThreads), smem, st, a);
-    g_pkv_launches++;
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    if (a.plan) {
+        static std::atomic<bool> allowed[64] = {};
+        e = pkv_allow_smem(reinterpret_cast<const void *>(chunk_plan_kernel<STREAM>), allowed);
+        if (e != cudaSuccess) return e;
+        e = pdl_launch(chunk_plan_kernel<STREAM>, dim3(1), dim3(kPlanThreads), smem, st, a);
+        g_pkv_launches++;
+        if (e != cudaSuccess) return e;
+    }
     constexpr int MODE = STREAM ? MODE_STREAM : MODE_CHUNK;
     e = c->kv_dtype == PKV_FP8_E4M3 ? dispatch<MODE, true>(D, mt, m, a, ctas, c->num_sms, st)
                                     : dispatch<MODE, false>(D, mt, m, a, ctas, c->num_sms, st);
@@ -627,17 +626,24 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     a.cost_bins = 2 * std::max(s.split_steps, 1) + 2;
     Maps m;
     if (!make_group_map(&m.q, p.q, mt, p.total_tokens, hq, D, hq / c->num_kv_heads) ||
-        !make_group_map(&m.out, p.out, mt, p.total_tokens, hq, D, hq / c->num_kv_heads) || !pool_map(&m.pool, c))
+        !make_group_map(&m.out, p.out, mt, p.total_tokens, hq, D, hq / c->num_kv_heads) || !(D == 128 && c->kv_dtype != PKV_FP8_E4M3 ? pkv_tmap_rows128_grouped(&m.pool, c->pool, mt, pool_rows, c->block_size)
+                                                  : pool_map(&m.pool, c)))
         return pkv_fail(PKV_ECUDA, "tensor map");
     m.k = m.v = m.pool;
     std::lock_guard<std::mutex> lk(c->ws_mu);
     PkvWorkspace ws;
     if (int r = pkv_stream_workspace(c, st, s.floats(c, p.total_tokens, hq), &ws)) return r;
-    a.plan = reinterpret_cast<int *>(ws.p);
+    const bool direct = s.direct(c, p.num_seqs);
+    a.plan = direct ? nullptr : reinterpret_cast<int *>(ws.p);
+    if (direct) {
+        a.max_groups = s.max_groups;
+        a.max_parts = s.max_parts;
+        a.rect = (int)s.rect(c, p.num_seqs);
+    }
     a.ws_o = ws.p + (4 + 4 * s.items + 63) / 64 * 64;
     a.ws_ml = a.ws_o + p.total_tokens * hq * s.max_splits * D;
     PkvTimer timer(c, PKV_KIND_PREFILL, st);
-    const int64_t ctas = s.items * c->num_kv_heads;
+    const int64_t ctas = direct ? a.rect : s.items * c->num_kv_heads;
     const cudaError_t e = s.stream ? launch_chunk_t<true>(c, a, m, ctas, st) : launch_chunk_t<false>(c, a, m, ctas, st);
     if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
     return PKV_OK;

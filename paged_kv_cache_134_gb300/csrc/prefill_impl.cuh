@@ -82,6 +82,9 @@ struct Args {
     // `sinks` are attended to; log2 of the query heads per KV head; key tiles of a split, about
     const int32_t *lens = nullptr;
     int window = 0, sinks = 0, lg_group = 0, split_steps = 0;
+    // without a list (plan NULL): row tiles (or pairs) of a sequence and splits (or pairs) of their keys, at most, and
+    // sequences x those x KV heads
+    int max_groups = 0, max_parts = 0, rect = 0;
 };
 
 // TMA descriptors of one launch: q (and out) as [rows][Hq * D] with 64-column boxes of BM rows; packed
@@ -169,6 +172,95 @@ PKV_DEV void widen_row(uint8_t *stage, int r) {
                 make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
         }
     }
+}
+
+// E4M3 caches in chunk and stream mode: four more warps widen the codes, so that the loads of the next tiles are on their way
+// meanwhile (a loader that widened its own tiles, one row after another, took 16000 cycles for a pair of tiles that
+// HBM brings in 2900).  Codes land in rings of their own, row r at r * D; the 16-bit tiles are fp16 whatever the model's type
+// (exact; P then is one fp16 and not a pair), and a bf16 q is brought into fp16's range by a power of two for each
+// row, which is left behind the layout for the softmax.
+template <int D, bool ONE_Q>
+struct CodeLayout {
+    static constexpr int NKS = D == 128 ? 2 : ONE_Q ? 4 : 3, NVS = NKS; // fp16 tiles
+    static constexpr int NCS = D == 128 ? (ONE_Q ? 2 : 1) : 3;         // code stages, of K and of V
+    static constexpr int Q_TILE = BM * D * 2;
+    static constexpr int TILE = BN * D * 2, STAGE = TILE, CODE = BN * D;
+    static constexpr int Q = 0;
+    static constexpr int K0 = Q + (ONE_Q ? 1 : 2) * Q_TILE;
+    static constexpr int V0 = K0 + NKS * STAGE;
+    static constexpr int C0 = V0 + NVS * STAGE; // K codes, then V codes
+    static constexpr int BAR = C0 + 2 * NCS * CODE;
+    static constexpr int NBARS = 4 + 4 + 2 + 2 + 4 * NKS + 4 * NVS + 2 + 2 + 2 + 2 + 2 + 2 + 2;
+    static constexpr int MISC = BAR + (NBARS * 8 + 15) / 16 * 16;
+    static constexpr int TOTAL = MISC + 16 + 64;
+    static_assert(NCS <= NKS && NCS <= NVS, "their barriers share the arrays");
+};
+template <int D, int MODE, bool KV8>
+using LayoutOf = std::conditional_t<KV8 && (MODE == MODE_CHUNK || MODE == MODE_STREAM),
+                                    CodeLayout<D, MODE == MODE_STREAM>,
+                                    Layout<D, KV8, MODE == MODE_CASCADE || MODE == MODE_STREAM>>;
+template <int D, int MODE, bool KV8>
+constexpr int smem_total() {
+    constexpr bool chunked = MODE == MODE_CHUNK || MODE == MODE_STREAM;
+    constexpr int n = LayoutOf<D, MODE, KV8>::TOTAL + (chunked && KV8 ? 4 * BM : 0);
+    static_assert(n + 1024 <= 232448, "shared memory");
+    return n;
+}
+template <int MODE, bool KV8>
+constexpr int threads_of() {
+    return KV8 && (MODE == MODE_CHUNK || MODE == MODE_STREAM) ? kThreads + 128 : kThreads;
+}
+
+// row r of a tile of E4M3 codes -> fp16 in the 128-byte-swizzled layout (lanes take the row's sixteens in turn, so that
+// neither the reads nor the writes of eight lanes meet in a bank)
+template <int D>
+PKV_DEV void widen_codes(const uint8_t *codes, uint8_t *tile, int r) {
+    constexpr int NC = D / 16;
+#pragma unroll 2
+    for (int i = 0; i < NC; ++i) {
+        const int c = (i + r) & (NC - 1);
+        const uint4 w = *reinterpret_cast<const uint4 *>(codes + r * D + c * 16);
+        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            o[2 * e] = widen2<PKV_F16>(in[e] & 0xFFFFu);
+            o[2 * e + 1] = widen2<PKV_F16>(in[e] >> 16);
+        }
+        uint8_t *row = tile + (c >> 2) * (BN * 128) + r * 128;
+        const int u = 2 * (c & 3);
+        *reinterpret_cast<uint4 *>(row + ((u ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(row + (((u + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// row r of a bf16 Q tile (128-byte swizzled) -> fp16 in place, times 2^-e; returns e.  The row's largest element comes to
+// [2^14, 2^15); one that is smaller by 2^31 or more loses bits.
+template <int D>
+PKV_DEV int q_to_f16(uint8_t *tile, int r) {
+    uint8_t *row = tile + r * 128;
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(row + (i >> 3) * (BM * 128) + (((i & 7) ^ (r & 7)) << 4));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFF0000u, (w[e] << 16) & 0x7FFF0000u));
+    }
+    const int e = top == 0 ? 0 : max((int)(top >> 23) - 127, -100) - 14;
+    const float f = __uint_as_float((uint32_t)(127 - e) << 23); // 2^-e, -114 <= -e <= 114
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        uint4 *at = reinterpret_cast<uint4 *>(row + (i >> 3) * (BM * 128) + (((i & 7) ^ (r & 7)) << 4));
+        const uint4 x = *at;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = pack2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f, PKV_F16);
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return e;
 }
 
 // query tiles of sequence i (0 for a malformed cu_seqlens entry or context length, which is reported)
@@ -322,6 +414,42 @@ PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
     return it;
 }
 
+// row tiles of sequence i (stream) or pairs of them (chunk); 0 where its numbers make no sense
+template <bool STREAM>
+PKV_DEV int chunk_groups(const Args &a, int i, bool report) {
+    const int st = a.cu[i], en = a.cu[i + 1];
+    if (st < 0 || en < st || en > a.total_tokens || en - st > a.max_seqlen) {
+        if (report) set_error(a.err, PKV_DEVERR_CU_SEQLENS);
+        return 0;
+    }
+    if (en > st && (int64_t)a.lens[i] > (int64_t)a.max_blocks * a.bs) {
+        if (report) set_error(a.err, PKV_DEVERR_LENGTH);
+        return 0;
+    }
+    const int per = (STREAM ? 1 : 2) * (BM >> a.lg_group);
+    return (en - st + per - 1) / per;
+}
+// items of a group: at least the one that writes the rows without keys
+template <bool STREAM>
+PKV_DEV int chunk_parts(const ChunkItem &it) {
+    const int ns = max(it.ns[0], it.ns[1]);
+    return max(1, STREAM ? (ns + 1) / 2 : ns);
+}
+// the next item of this CTA among all that the call's sizes allow, from `at` on: (sequence, group, KV head, part), -1 behind
+// the last
+template <bool STREAM>
+PKV_DEV int4 direct_item(const Args &a, int &at) {
+    for (; at < a.rect; at += gridDim.x) {
+        const int h = at % a.hkv, r = at / a.hkv, part = r % a.max_parts, g = r / a.max_parts % a.max_groups;
+        const int seq = r / a.max_parts / a.max_groups;
+        if (g >= chunk_groups<STREAM>(a, seq, h == 0 && part == 0 && g == 0)) continue;
+        if (part > 0 && part >= chunk_parts<STREAM>(chunk_item<STREAM>(a, seq, g, 0, 0))) continue;
+        at += gridDim.x;
+        return make_int4(seq, g, h, part);
+    }
+    return make_int4(-1, 0, 0, 0);
+}
+
 // Loads of K (or V) tiles of an item, in their order.  Packed, paged and chunk modes share one key tile per step; cascade
 // and stream mode have one per tile and step.
 template <bool SHARED>
@@ -346,22 +474,31 @@ PKV_DEV void ring_entry(const Item &it, int e, int &t, int &j) {
     }
 }
 
+// bits 0 .. n - 1
+PKV_DEV uint32_t ones_below(int n) { return n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u; }
+
 PKV_DEV int chunk_splits(const ChunkItem &it, int t) { return t ? it.ns[1] : it.ns[0]; }
 PKV_DEV int chunk_splits(const Item &, int) { return 1; }
 
 template <int D, int MT, int MODE, bool KV8>
-__global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Maps maps, const Args a) {
+__global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const __grid_constant__ Maps maps, const Args a) {
     const CUtensorMap &tq = maps.q, &tk = maps.k, &tv = maps.v, &tp = maps.pool, &to = maps.out;
-    using L = Layout<D, KV8, MODE == MODE_CASCADE || MODE == MODE_STREAM>;
+    using L = LayoutOf<D, MODE, KV8>;
     constexpr bool PAGED = MODE != MODE_PACKED;    // keys from the pool through the block table
     constexpr bool CASCADE = MODE == MODE_CASCADE; // no causal mask, fp32 split partials out
     constexpr bool STREAM = MODE == MODE_STREAM;
     constexpr bool CHUNKED = MODE == MODE_CHUNK || STREAM;
     constexpr bool ONE_Q = CASCADE || STREAM;      // one Q tile, two key streams
     constexpr bool SHARED = !ONE_Q;                // both tiles use the same key tiles
+    // K and V tiles of chunk and stream mode at D = 128, 16-bit caches: one box a block brings both halves of its rows, as
+    // [8 rows][half][8 rows][128 bytes]; else one box for each half, as [half][128 rows][128 bytes].  (A loader's warp needs
+    // some 100 cycles for each box; with two a block, short chunks were bound by their loaders.)
+    constexpr bool GROUPED = CHUNKED && D == 128 && !KV8;
     using It = std::conditional_t<CHUNKED, ChunkItem, Item>;
     constexpr bool WRITER = MODE == MODE_PACKED;   // the loaders write the item's K/V rows into the pool
-    constexpr int NP = MT == PKV_BF16 ? 2 : 1;     // P parts (bf16: hi + lo)
+    constexpr bool CODES = KV8 && (MODE == MODE_CHUNK || MODE == MODE_STREAM); // widened by warps of their own (CodeLayout)
+    constexpr int OT = CODES ? (int)PKV_F16 : MT;  // the products' operands
+    constexpr int NP = OT == PKV_BF16 ? 2 : 1;     // P parts (bf16: hi + lo)
     constexpr int EB = KV8 ? 1 : 2;                // pool bytes per element
     constexpr int NKS = L::NKS, NVS = L::NVS;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -380,6 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     uint64_t *s_full = v_spare + NVS, *p_full = s_full + 2, *o_full = p_full + 2, *o_free = o_full + 2;
     uint64_t *fin = o_free + 2;
     uint64_t *epi = fin + 2; // a tile's output rows are staged (one arrival per softmax warp)
+    uint64_t *qc_full = epi + 2; // CODES: a Q tile as fp16
+    uint64_t *q_ready = CODES && MT == PKV_BF16 ? qc_full : q_full;
+    int8_t *q_exp = reinterpret_cast<int8_t *>(smem + L::TOTAL); // CODES: [2 Q tiles][2 tiles][BM] exponents of q's rows
+    (void)qc_full;
+    (void)q_exp;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC + 4);
     // exp phases the softmax of each tile has finished, counted per warp (4 per key step), monotonic
@@ -392,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     uint64_t *v_ready = KV8 ? vc_full : v_full;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // item consumers: V loader, the two MMA issuers, eight softmax warps
-    constexpr int kItemConsumers = 11;
+    // item consumers: V loader, the two MMA issuers, eight softmax warps (and four that widen)
+    constexpr int kItemConsumers = CODES ? 15 : 11;
     // a K or V stage frees once every MMA warp whose tile reads it has released it (both tiles read
     // the shared key tiles of packed and paged modes; each cascade tile has key tiles of its own)
     constexpr int kStageReleasers = SHARED ? 2 : 1;
@@ -413,12 +555,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         for (int s = 0; s < NKS; ++s) {
             mbar_init(k_full + s, 1);
             mbar_init(k_empty + s, kStageReleasers);
-            mbar_init(kc_full + s, 1);
+            mbar_init(kc_full + s, CODES ? 4 : 1);
+            if constexpr (CODES) mbar_init(k_spare + s, 4); // codes read (one arrival per warp that widens)
         }
         for (int s = 0; s < NVS; ++s) {
             mbar_init(v_full + s, 1);
             mbar_init(v_empty + s, kStageReleasers);
-            mbar_init(vc_full + s, 1);
+            mbar_init(vc_full + s, CODES ? 4 : 1);
+            if constexpr (CODES) mbar_init(v_spare + s, 4);
+        }
+        if constexpr (CODES) {
+            mbar_init(qc_full, 4);
+            mbar_init(qc_full + 1, 4);
         }
         mbar_init(fin, 1);
         mbar_init(fin + 1, 1);
@@ -475,7 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         return (SHARED || t == 0) ? it.t[0].kend : it.t[1].kend;
     };
 
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if constexpr (CODES) { // 128 x (80 + 2 x 176 + 80) = 512 x 128 registers
+        if (warp < 4 || warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    } else {
+        if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    }
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------------- loaders
         // Warp 0: the scheduler (lane 0), Q loads and K loads; warp 2: V loads.  Packed mode: lane 0
@@ -493,10 +645,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const bool isK = warp == 0;
         constexpr int NS = 0; // (stage counts differ per ring; see ns below)
         (void)NS;
-        const int ns = isK ? NKS : NVS;
-        uint8_t *const ring = smem + (isK ? L::K0 : L::V0);
+        int ns = isK ? NKS : NVS, stage_bytes = L::STAGE, code_off = kCodeOff;
+        uint8_t *ring = smem + (isK ? L::K0 : L::V0);
         uint64_t *const full = isK ? k_full : v_full;
-        uint64_t *const empty = isK ? k_empty : v_empty;
+        uint64_t *empty = isK ? k_empty : v_empty;
+        if constexpr (CODES) { // codes, in their own stages
+            ns = L::NCS;
+            stage_bytes = L::CODE;
+            code_off = 0;
+            ring = smem + L::C0 + (isK ? 0 : L::NCS * L::CODE);
+            empty = isK ? k_spare : v_spare;
+        }
         uint64_t *const ready = isK ? kc_full : vc_full; // E4M3: widened
         const int kvsel = isK ? 0 : 1;                   // K or V half of a pool block
         constexpr int CPR = D * EB / 16;                  // 16-byte chunks per pool row
@@ -565,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         int64_t g = 0;
         int gt[2] = {0, 0};
         auto next_stage = [&](int t, int &st, int &round) {
-            if constexpr (ONE_Q) {
+            if constexpr (ONE_Q && !CODES) {
                 const int c = t ? gt[1] : gt[0];
                 st = t + 2 * (c % (ns / 2));
                 round = c / (ns / 2);
@@ -584,13 +743,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             if (lane == 0) mbar_arrive(ready + st);
             return true;
         };
-        const int total = a.plan[0] * (CHUNKED ? a.hkv : a.hq);
+        const bool direct = CHUNKED && a.plan == nullptr; // few items: no list, every CTA looks for its own
+        const int total = direct ? a.rect : a.plan[0] * (CHUNKED ? a.hkv : a.hq);
+        int next_direct = blockIdx.x;
+        (void)next_direct;
         int nq[2] = {0, 0}; // Q loads per buffer so far (warp 0)
         int pend = -1;      // FP8: the issued tile still to widen: its stage, and its phase's parity in bit 8
         // FP8: widen the pending tile; done before this warp can block on anything an MMA of that tile
         // may be holding up (the next tile's stage, the next item, the next item's Q buffer)
         auto widen_pending = [&]() -> bool {
-            if constexpr (KV8) {
+            if constexpr (KV8 && !CODES) {
                 if (pend >= 0) {
                     const bool w = widen(pend & 0xFF, (uint32_t)pend >> 8);
                     pend = -1;
@@ -608,7 +770,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             int4 raw = make_int4(-1, 0, 0, 0);
             if (!pok) return make_item(-1, 0, 0, 0);
             if (lane == 0) {
-                const int idx = *abort_flag ? total : atomicAdd(a.plan + 1, 1);
+                int idx = total;
+                if (direct) {
+                    if constexpr (CHUNKED) {
+                        if (!*abort_flag) raw = direct_item<STREAM>(a, next_direct);
+                    }
+                } else if (!*abort_flag) {
+                    idx = atomicAdd(a.plan + 1, 1);
+                }
                 if (idx < total) {
                     if constexpr (CASCADE) {
                         const int pair = idx / a.hq; // (tile of sequences, split pair)
@@ -738,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 flush_write(st); // the stage's previous tile leaves for the pool before the refill
                 if (ok && round >= 1) ok = __all_sync(0xffffffffu, mbar_wait_hint(empty + st, (round - 1) & 1));
                 if (!ok || __any_sync(0xffffffffu, *abort_flag != 0)) break;
-                uint8_t *stage = ring + st * L::STAGE;
+                uint8_t *stage = ring + st * stage_bytes;
                 if constexpr (PAGED) {
                     int t, j;
                     const int kbase = key_base(it, e, t, j), send = key_end(it, t);
@@ -759,12 +928,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     if (full_blk) {
                         const int y = ((b * 2 + kvsel) * a.hkv + kvh) << a.lg_bs;
                         if constexpr (KV8) {
-                            tc::tma_load_2d(stage + kCodeOff + (lane << a.lg_bs) * D, &tp, 0, y, full + st);
+                            tc::tma_load_2d(stage + code_off + (lane << a.lg_bs) * D, &tp, 0, y, full + st);
                         } else {
 #pragma unroll
-                            for (int c = 0; c < D / 64; ++c)
+                            for (int c = 0; c < (GROUPED ? 0 : D / 64); ++c)
                                 tc::tma_load_2d(stage + c * BN * 128 + ((lane << a.lg_bs) * 128), &tp, c * 64, y,
                                                 full + st);
+                            if constexpr (GROUPED)
+                                tc::tma_load_4d(stage + (lane << a.lg_bs) * 256, &tp, 0, 0, 0, y >> 3, full + st);
                         }
                     }
                     const unsigned allmask = nbt == 32 ? 0xffffffffu : (1u << nbt) - 1u;
@@ -781,10 +952,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                                     a.pool + ((((int64_t)bl * 2 + 1) * a.hkv + kvh) * a.tile_elems +
                                               (int64_t)(r - (l << a.lg_bs)) * D) * EB + cc * 16);
                             if constexpr (KV8) {
-                                *reinterpret_cast<uint4 *>(stage + kCodeOff + r * D + cc * 16) = x;
+                                *reinterpret_cast<uint4 *>(stage + code_off + r * D + cc * 16) = x;
                             } else {
                                 const int c2 = cc >> 3, u = cc & 7;
-                                *reinterpret_cast<uint4 *>(stage + c2 * BN * 128 + r * 128 + ((u ^ (r & 7)) << 4)) = x;
+                                uint8_t *at = GROUPED ? stage + (r >> 3) * 2048 + c2 * 1024 + (r & 7) * 128
+                                                      : stage + c2 * BN * 128 + r * 128;
+                                *reinterpret_cast<uint4 *>(at + ((u ^ (r & 7)) << 4)) = x;
                             }
                         }
                         if constexpr (!KV8) fence_proxy_async_smem(); // the plain stores are read by the MMA
@@ -810,8 +983,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     }
                 }
                 ++g;
-                if constexpr (ONE_Q) ++(tile ? gt[1] : gt[0]);
-                if constexpr (KV8) pend = st | (round & 1) << 8;
+                if constexpr (ONE_Q && !CODES) ++(tile ? gt[1] : gt[0]);
+                if constexpr (KV8 && !CODES) pend = st | (round & 1) << 8;
                 if (isK && e < 2) issue_q(e); // Q_A after K tile 0, Q_B after K tile 1
             }
             if (isK) issue_q(1); // items of fewer than two key tiles
@@ -829,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         if constexpr (WRITER) tc::bulk_wait_all();
         // the last loads must land before this CTA's shared memory goes away
         if (lane == 0) {
-            if constexpr (ONE_Q) {
+            if constexpr (ONE_Q && !CODES) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     for (int c = max(gt[t] - ns / 2, 0); c < gt[t]; ++c)
@@ -850,13 +1023,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         // columns only after P V(j) has read P from them.  Two issuers keep the tensor pipe's queue fed
         // while either waits for its softmax.  Commits track the issuing thread's own MMAs.
         const int t = warp == 1 ? 0 : 1;
-        constexpr uint32_t IQK = tc::idesc_f16(MT == PKV_BF16 ? 1u : 0u, 0u, BM, BN);
-        constexpr uint32_t IPV = tc::idesc_f16(MT == PKV_BF16 ? 1u : 0u, 1u, BM, D);
+        constexpr uint32_t IQK = tc::idesc_f16(OT == PKV_BF16 ? 1u : 0u, 0u, BM, BN);
+        constexpr uint32_t IPV = tc::idesc_f16(OT == PKV_BF16 ? 1u : 0u, 1u, BM, D);
         // one descriptor per operand layout; the address field counts 16-byte units, so a tile at byte
         // offset `off` from the base is the base descriptor plus off / 16
         const uint64_t dQ = tc::smem_desc(smem_u32(smem + L::Q), 16, 1024);
-        const uint64_t dK = tc::smem_desc(smem_u32(smem + L::K0), 16, 1024);
-        const uint64_t dV = tc::smem_desc(smem_u32(smem + L::V0), BN * 128, 1024);
+        const uint64_t dK = tc::smem_desc(smem_u32(smem + L::K0), 16, GROUPED ? 2048 : 1024);
+        const uint64_t dV = GROUPED ? tc::smem_desc(smem_u32(smem + L::V0), 1024, 2048)
+                                    : tc::smem_desc(smem_u32(smem + L::V0), BN * 128, 1024);
+        constexpr int kHalf = GROUPED ? 1024 : BN * 128, kKeys16 = GROUPED ? 4096 : 2048; // bytes between halves; of 16 keys
         const uint32_t tS = tmem + (uint32_t)(t * BN), tO = tmem + (uint32_t)(2 * BN + t * D);
         bool any_mma = false, ok = true;
         // ring cursors: the stage of the K (V) entry to look at next and the parity of its phase (ONE_Q: of the tile's own
@@ -887,7 +1062,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 for (int k = 0; k < D / 16; ++k) {
                     const int c = k >> 2, kk = k & 3;
                     tc::mma_f16_warp(tS, a0 + (uint64_t)((c * BM * 128 + kk * 32) >> 4),
-                                     b0 + (uint64_t)((c * BN * 128 + kk * 32) >> 4), IQK, k > 0 ? 1u : 0u);
+                                     b0 + (uint64_t)((c * kHalf + kk * 32) >> 4), IQK, k > 0 ? 1u : 0u);
                 }
             };
             // after S(j): S complete, this warp's share of the K stage, and Q after the tile's last S
@@ -904,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             };
             // S(0): Q and the first K tile
             auto first_s = [&]() -> bool {
-                if (!__all_sync(0xffffffffu, mbar_wait(k_ready + stage(kst), kph) && mbar_wait(q_full + qb, qph))) return false;
+                if (!__all_sync(0xffffffffu, mbar_wait(k_ready + stage(kst), kph) && mbar_wait(q_ready + qb, qph))) return false;
                 tc::fence_after_sync();
                 any_mma = true;
                 mmas_s();
@@ -930,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                 for (int part = 0; part < NP; ++part)
 #pragma unroll
                     for (int k = 0; k < BN / 16; ++k)
-                        tc::mma_f16_ts_warp(tO, tS + (uint32_t)(part * (BN / 2) + k * 8), b0 + (uint64_t)((k * 2048) >> 4),
+                        tc::mma_f16_ts_warp(tO, tS + (uint32_t)(part * (BN / 2) + k * 8), b0 + (uint64_t)((k * kKeys16) >> 4),
                                             IPV, (j > 0 || k > 0 || part > 0) ? 1u : 0u);
                 // the V stage share goes out before S(j + 1) is issued (a commit covers every earlier MMA of
                 // this thread, so issued later it would hold the stage until S(j + 1) completes too); the
@@ -966,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             } else {
                 if (nt == 0 && ok && (CASCADE || it.t[0].n > 0)) {
                     // cascade, stream: no split for this tile; its share of the Q buffer once Q has landed
-                    ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full + qb, qph));
+                    ok = __all_sync(0xffffffffu, mbar_wait_hint(q_ready + qb, qph));
                     if (ok && lane == 0) mbar_arrive(q_empty + qb);
                     qph ^= 1u;
                 }
@@ -981,8 +1156,82 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             tc::commit_warp(fin + t);
             if (!__all_sync(0xffffffffu, mbar_wait_hint(fin + t, 0)) && lane == 0) set_error(a.err, PKV_DEVERR_TIMEOUT);
         }
+    } else if (CODES && warp >= 12) {
+        // ---------------------------------------------------------------- widening (warps 12-15)
+        // Thread r owns row r of every tile, K or V, in the loaders' order, K one tile ahead of V (a V tile waits for the
+        // products with the one before it, the next K tile only for its own stage), and of every bf16 Q tile.
+        if constexpr (CODES) {
+            const int r = (warp - 12) * 32 + lane;
+            bool ok = true;
+            uint32_t g[2] = {0, 0};                     // K, V tiles widened
+            uint32_t gt[2][2] = {{0, 0}, {0, 0}};       // stream: those of each key stream
+            uint32_t nq[2] = {0, 0};                    // Q tiles
+            auto widen = [&](auto which, int t) -> bool {
+                constexpr int kv = decltype(which)::value;
+                uint64_t *const land = kv ? v_full : k_full, *const read = kv ? v_spare : k_spare;
+                uint64_t *const free = kv ? v_empty : k_empty, *const done = kv ? vc_full : kc_full;
+                uint32_t st, round;
+                if constexpr (ONE_Q) {
+                    const uint32_t c = t ? gt[kv][1]++ : gt[kv][0]++;
+                    st = t + 2 * (c % (NKS / 2));
+                    round = c / (NKS / 2);
+                } else {
+                    st = g[kv] % NKS;
+                    round = g[kv] / NKS;
+                }
+                const uint32_t cs = g[kv] % L::NCS;
+                bool w = mbar_wait_hint(land + cs, (g[kv] / L::NCS) & 1u);
+                ++g[kv];
+                if (w && round > 0) w = mbar_wait_hint(free + st, (round - 1) & 1u);
+                if (!__all_sync(0xffffffffu, w)) return false;
+                widen_codes<D>(smem + L::C0 + (kv * L::NCS + cs) * L::CODE, smem + (kv ? L::V0 : L::K0) + st * L::STAGE, r);
+                fence_proxy_async_smem(); // the MMAs read the tile through the async proxy
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(read + cs);
+                    mbar_arrive(done + st);
+                }
+                return true;
+            };
+            auto convert_q = [&](int b) -> bool {
+                if constexpr (MT == PKV_BF16) {
+                    const uint32_t n = b ? nq[1]++ : nq[0]++;
+                    if (!__all_sync(0xffffffffu, mbar_wait_hint(q_full + b, n & 1u))) return false;
+                    q_exp[((n & 1) * 2 + b) * BM + r] = (int8_t)q_to_f16<D>(smem + L::Q + b * L::Q_TILE, r);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(qc_full + b);
+                }
+                return true;
+            };
+            for (int n = 0; ok; ++n) {
+                int n0, n1;
+                {
+                    const It it = take_item(n, ok);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok || it.seq < 0) break;
+                    n0 = it.t[0].n;
+                    n1 = it.t[1].n;
+                }
+                const int ne = SHARED ? max(n0, n1) : n0 + n1, both = 2 * min(n0, n1);
+                auto tile_of = [&](int e) -> int { return SHARED ? 0 : e < both ? e & 1 : n0 > n1 ? 0 : 1; };
+                // step -1: K tile 0 and Q_A; step e: K tile e + 1, (step 0: Q_B), V tile e
+                for (int e = -1; e < ne && ok; ++e) {
+                    if (e + 1 < ne) ok = widen(std::integral_constant<int, 0>(), tile_of(e + 1));
+                    if (ok && (e == -1 ? n0 > 0 : !ONE_Q && e == 0 && n1 > 0)) ok = convert_q(e + 1);
+                    if (ok && e >= 0) ok = widen(std::integral_constant<int, 1>(), tile_of(e));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(item_empty + (n & (kItemSlots - 1)));
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            }
+            if (!ok && lane == 0) fail();
+        }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if constexpr (CODES)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---------------------------------------------------------------- softmax, one thread per row
         const int t = (warp - 4) >> 2;          // tile A (warps 4-7) or B (warps 8-11)
         const int r = (warp & 3) * 32 + lane;   // query row of the tile = tensor-memory lane
@@ -990,7 +1239,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const uint32_t tS = tmem + lane_off + (uint32_t)(t * BN);
         const uint32_t tO = tmem + lane_off + (uint32_t)(2 * BN + t * D);
         bool ok = true;
-        int ns = 0, no = 0, nepi = 0;
+        int ns = 0, no = 0, nepi = 0, q_seen = 0; // q_seen: Q tiles of this tile's buffer in earlier items
+        (void)q_seen;
         int steps0 = 0, steps1 = 0; // key steps of tiles A and B in earlier items
         // The two tiles' softmaxes take turns on the exponentials (they share the SMSPs and their
         // transcendental units; run together, each takes twice as long and the MMAs of both tiles
@@ -1015,7 +1265,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const int n0 = it.t[0].n, n1 = it.t[1].n;
             if (x.n > 0) {
                 const int kvh = kv_head(it);
-                const float sl = KV8 ? a.scale_log2 * a.k_scale[kvh] : a.scale_log2;
+                float sl = KV8 ? a.scale_log2 * a.k_scale[kvh] : a.scale_log2;
                 const int qpos = x.qpos0 + (CHUNKED ? r >> a.lg_group : r); // absolute position of this row (causal modes)
                 float m_use = -INFINITY, l = 0.f;
                 for (int j = 0; j < x.n && ok; ++j) {
@@ -1024,6 +1274,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                     if (!ok) break;
                     ++ns;
                     tc::fence_after_sync();
+                    if constexpr (CODES && MT == PKV_BF16) {
+                        // q's power of two: S is complete, so the row is converted; the next but one Q tile, which
+                        // writes this slot again, waits for the next one's S, and that for this row's P
+                        if (j == 0) sl *= exp2f((float)q_exp[((q_seen & 1) * 2 + (ONE_Q ? 0 : t)) * BM + r]);
+                    }
                     uint32_t sr[BN];
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c)
@@ -1045,17 +1300,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                         const int plast = x.qpos0 + x.qlast - x.q0; // position of the tile's last row
                         const bool late = kbase + BN - 1 + hidden > x.qpos0;
                         const bool early = a.window > 0 && plast - a.window + 1 - hidden > kbase;
-                        const int upto = qpos + 1 - hidden - kbase;
-                        if (early) {
-                            const int since = max(qpos - a.window + 1, 0) - hidden - kbase;
+                        if (late || early) {
+                            const int upto = qpos + 1 - hidden - kbase;
+                            const int since = a.window > 0 ? qpos - a.window + 1 - hidden - kbase : 0;
                             const int first = min(a.sinks, qpos + 1) - kbase;
+                            // (a word of seen keys at a time: tested one by one against three bounds they cost 70 registers)
 #pragma unroll
-                            for (int c = 0; c < BN; ++c)
-                                if ((c >= upto || c < since) && c >= first) sr[c] = 0xFF800000u; // -inf
-                        } else if (late) {
+                            for (int w = 0; w < BN / 32; ++w) {
+                                const uint32_t in = (ones_below(upto - 32 * w) & ~ones_below(since - 32 * w)) | ones_below(first - 32 * w);
 #pragma unroll
-                            for (int c = 0; c < BN; ++c)
-                                if (c >= upto) sr[c] = 0xFF800000u; // -inf
+                                for (int c = 0; c < 32; ++c)
+                                    if (!(in & (1u << c))) sr[32 * w + c] = 0xFF800000u; // -inf
+                            }
                         }
                     } else if (kbase + BN - 1 > x.qpos0) {
                         // causal mask, only on tiles that reach past the tile's first query row
@@ -1113,10 +1369,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
                                 fma2(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), sc2, nb2);
                             const float p0 = fast_exp2(xx.x), p1 = fast_exp2(xx.y);
                             rs = add2(rs, make_float2(p0, p1));
-                            phi[c] = pack2(p0, p1, MT);
+                            phi[c] = pack2(p0, p1, OT);
                             if constexpr (NP == 2) // remainders after bf16 rounding, themselves rounded to bf16
                                 plo[c] = pack2(p0 - __uint_as_float(phi[c] << 16),
-                                               p1 - __uint_as_float(phi[c] & 0xFFFF0000u), MT);
+                                               p1 - __uint_as_float(phi[c] & 0xFFFF0000u), OT);
                         }
                         if constexpr (NP == 2) {
                             tc::stn<8>(tS + q * 8, phi);
@@ -1263,6 +1519,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
             steps0 += n0;
             steps1 += n1;
+            if (CODES && (ONE_Q ? n0 : x.n) > 0) ++q_seen;
             __syncwarp();
             if (lane == 0) mbar_arrive(item_empty + (n & (kItemSlots - 1)));
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
@@ -1285,11 +1542,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 template <int D, int MT, int MODE, bool KV8>
 cudaError_t launch_attn(const Maps &m, const Args &a, int64_t max_ctas, int num_sms, cudaStream_t st) {
     auto kern = attn_kernel<D, MT, MODE, KV8>;
-    const int smem = Layout<D, KV8, MODE == MODE_CASCADE || MODE == MODE_STREAM>::TOTAL;
+    const int smem = smem_total<D, MODE, KV8>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = std::min<int64_t>(max_ctas, (int64_t)num_sms);
-    return pdl_launch(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, m, a);
+    return pdl_launch(kern, dim3((unsigned)grid), dim3(threads_of<MODE, KV8>()), smem, st, m, a);
 }
 
 #define PKV_ATTN_EXTERN(MODE, KV8)                                                                                     \
