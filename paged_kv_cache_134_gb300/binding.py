@@ -327,13 +327,19 @@ def paged_kv_append_at(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_t
 
 def _take_rows(cache: "KVCache", t: torch.Tensor, name: str, heads: Optional[int], n: Optional[int]):
     """Address and token stride (elements) of [T, heads, head_dim] rows whose tokens may lie apart."""
+    d = cache.head_dim
+    if type(t) is torch.Tensor and t.dtype is cache.torch_dtype and t.get_device() == cache.device:
+        shape = t.shape
+        if len(shape) == 3 and shape[2] == d and (heads is None or shape[1] == heads) and (n is None or shape[0] == n):
+            stride, head, elem = t.stride()
+            if elem == 1 and head == d and shape[0] > 1:
+                return t.data_ptr(), stride
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.get_device() != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.device}")
     if t.dtype != cache.torch_dtype:
         raise TypeError(f"{name} must be {cache.torch_dtype}, got {t.dtype}")
-    d = cache.head_dim
     if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) or \
             (n is not None and t.shape[0] != n):
         raise ValueError(f"{name} must be [{'T' if n is None else n}, {'H' if heads is None else heads}, {d}], got "
@@ -391,7 +397,7 @@ def paged_kv_append_rotary(cache: KVCache, q: Optional[torch.Tensor], k: torch.T
         qp, qs = _take_rows(cache, q, "q", None, n)
         hq = q.shape[1]
         if q_out is None:
-            q_out = q.new_empty((n, hq, cache.head_dim))
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op, os_ = _take_rows(cache, q_out, "q_out", hq, n)
     _check(lib().paged_kv_append_rotary(cache.handle, qp, qs, kp, ks, vp, vs, hq, tables, block_tables.shape[0],
                                         block_tables.shape[1], seqs, pos, angles, n, rotary._ref, weights[0],

@@ -84,13 +84,31 @@ int64_t window_seen_blocks(const pkv_cache *c, int max_blocks, int window, int s
 }
 
 int window_split_blocks(const pkv_cache *c, int G, int num_seqs, int64_t seen_blocks) {
-    // The splits of the plain decode, but of equal size: under a window most sequences show the same number of
-    // blocks, and a last split of a block or two would cost a unit of its own.
-    const bool tc = pkv_decode_tc_eligible(c, G, num_seqs, true);
-    const int want = tc ? (c->kv_dtype == PKV_FP8_E4M3 ? 1024 : 512) : 256;
-    const int64_t per = std::max(1, want / c->block_size);
-    const int64_t k = std::max<int64_t>(1, (seen_blocks + per / 2) / per);
-    return (int)std::max<int64_t>(1, (seen_blocks + k - 1) / k);
+    const int bs = c->block_size;
+    if (!pkv_decode_tc_eligible(c, G, num_seqs, true)) {
+        // about the splits of the plain decode, of equal size (a last one of a block or two would be a unit like any other);
+        // nothing is cut that is not longer than two of them, as a short call's second launch costs more than it saves
+        const int64_t per = std::max(1, 256 / bs);
+        const int64_t k = seen_blocks <= 2 * per ? 1 : (seen_blocks + per / 2) / per;
+        return (int)std::max<int64_t>(1, (seen_blocks + k - 1) / k);
+    }
+    // Under a window most sequences show the same number of blocks, so that units of work come in equal sizes and rounds
+    // over the SMs show: of the splits of whole steps of 128 tokens, the one whose rounds take the fewest steps, a unit's own
+    // cost counted as 0.7 of a step and the merge's launch as two.  (Four sequences under 8192 + 64 tokens, 32/8 heads: 16
+    // splits of 17 blocks, 4 rounds of 5 steps, 36.2 us; 4 splits, one round of 17 steps, 30.7 us.)
+    const int64_t step = 128 / bs, steps = std::max<int64_t>(1, (seen_blocks + step - 1) / step);
+    const int64_t rows = (int64_t)num_seqs * c->num_kv_heads;
+    int64_t best = steps;
+    double least = 1e300;
+    for (int64_t k = 1; k <= std::min<int64_t>(steps, 128); ++k) {
+        const int64_t s = (steps + k - 1) / k, units = rows * ((steps + s - 1) / s);
+        const double cost = (double)((units + c->num_sms - 1) / c->num_sms) * ((double)s + 0.7) + (k > 1 ? 2.0 : 0.0);
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return (int)std::max<int64_t>(1, std::min(best * step, seen_blocks));
 }
 
 int64_t decode_workspace_floats(const pkv_cache *c, int num_seqs, int num_q_heads, int max_splits) {
@@ -161,7 +179,7 @@ cudaError_t launch_decode(pkv_cache *c, const DecodeLaunch &d, cudaStream_t st) 
             e = pkv_decode_tc_launch(c, a, d.q, G, st);
             g_pkv_launches++;
         }
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || (d.window > 0 && d.max_splits <= 1)) return e;
         if ((e = launch_prefix_between(c, d, st)) != cudaSuccess) return e;
         PkvTimer timer(c, PKV_KIND_MERGE, st);
         e = fn(a, c->head_dim, G, 0, 0, st, true);
@@ -195,7 +213,8 @@ cudaError_t launch_decode(pkv_cache *c, const DecodeLaunch &d, cudaStream_t st) 
         e = fn(a, c->head_dim, G, grid, smem, st, false);
         g_pkv_launches++;
     }
-    if (e != cudaSuccess) return e;
+    // (a window that needs no split needs no merge: its kernels write the rows without tokens, too)
+    if (e != cudaSuccess || (d.window > 0 && d.max_splits <= 1)) return e;
     if ((e = launch_prefix_between(c, d, st)) != cudaSuccess) return e;
     {
         PkvTimer timer(c, PKV_KIND_MERGE, st);

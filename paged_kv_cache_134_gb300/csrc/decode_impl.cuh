@@ -399,6 +399,15 @@ PKV_DEV void build_unit_list(const Args &a, int *pf, int *pp, int *nb, int warp,
     __syncthreads();
 }
 
+// WIN, no split anywhere (no merge follows): rows of sequences without tokens, by `n` threads of each CTA
+template <typename T, int D>
+PKV_DEV void zero_empty_rows(const Args &a, const int *nb, int i, int n) {
+    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x)
+        if (nb[s] == 0)
+            for (int e = i; e < a.hq * D / 8; e += n)
+                reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + (int64_t)s * a.hq * D)[e] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // wait (bounded) until a shared-memory counter reaches n or the CTA aborts; false after the limit
 PKV_DEV bool wait_at_least(const int *x, int n, const int *abort_flag) {
     const volatile int *v = x;
@@ -521,6 +530,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
     const int sub = lane % LH, gl = (G == 1) ? 0 : 0, tg = lane / LT;
     uint32_t tau = 0;
     int nu = 0; // this CTA's units so far
+    if constexpr (WIN)
+        if (a.max_splits <= 1) zero_empty_rows<T, D>(a, nb, threadIdx.x, NCW * 32);
     for (int u = blockIdx.x; u < U; u += gridDim.x, ++nu) {
         const Unit un = unit_info(u, pf, pp, nb, S, a.hkv, bps, a.start_block);
         const Reach rc = reach(un.s);

@@ -876,6 +876,8 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
         const uint32_t lane_off = static_cast<uint32_t>(lw * 32) << 16;
         bool ok = true;
         int nu = 0;
+        if constexpr (WIN)
+            if (a.max_splits <= 1) pkv_decode::zero_empty_rows<T, D>(a, nb, r, 128);
         for (int u = blockIdx.x; u < U && ok; u += gridDim.x, ++nu) {
             Unit un;
             int te;

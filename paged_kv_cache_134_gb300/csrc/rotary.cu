@@ -30,7 +30,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4; // of a pass: 4 x 64 frequencies, one a thread
-constexpr int kUnroll = 2;    // rows whose loads go out before any of them is worked on
+constexpr int kUnroll = 3;    // rows whose loads go out before any of them is worked on
+
+// CTAs of an SM that fit together (64 registers a thread) and are launched.  5256 tokens of 32/32 heads, 8188 of 32/8 with
+// norms: 46.4 and 40.8 us; one to three CTAs of the registers asked for 51.7 and 49.2, five 47.0 and 45.6 (spills), one or
+// two rows at a time 47.3 and 43.9, 48.0 and 40.7.
+constexpr int kCtas = 4, kGridCtas = 8;
 
 struct RotaryArgs {
     const char *q, *k, *v; // token j's row at j * stride bytes
@@ -53,7 +58,7 @@ struct RotaryArgs {
 };
 
 template <int D, int KVT, int MT, bool NORM, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     using M = ModelT<MT>;
     constexpr int LPR = D / 16, RPI = kThreads / LPR; // lanes a row, rows the CTA takes at once
     __shared__ float4 turn[2][kMaxTokens][4][8];      // [buffer][token][two of a lane's eight pairs][lane]: cos, sin twice
@@ -67,18 +72,13 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const int run0 = (INTERLEAVED || !turns) ? 2 * c : c, run1 = (INTERLEAVED || !turns) ? 2 * c + 1 : c + turned;
     pdl_trigger();
     pdl_wait();
-    float wq[16], wk[16];
+    uint4 wq[2], wk[2]; // this lane's weights (as stored: widened they would take 32 registers)
     if constexpr (NORM) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) wq[i] = wk[i] = 1.f;
-        if (a.wq) {
-            cvt8<MT>(static_cast<const uint4 *>(a.wq)[run0], wq);
-            cvt8<MT>(static_cast<const uint4 *>(a.wq)[run1], wq + 8);
-        }
-        if (a.wk) {
-            cvt8<MT>(static_cast<const uint4 *>(a.wk)[run0], wk);
-            cvt8<MT>(static_cast<const uint4 *>(a.wk)[run1], wk + 8);
-        }
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        wq[0] = a.wq ? static_cast<const uint4 *>(a.wq)[run0] : none;
+        wq[1] = a.wq ? static_cast<const uint4 *>(a.wq)[run1] : none;
+        wk[0] = a.wk ? static_cast<const uint4 *>(a.wk)[run0] : none;
+        wk[1] = a.wk ? static_cast<const uint4 *>(a.wk)[run1] : none;
     }
     auto load_pos = [&](int64_t base) { // the position that this thread's angle is of
         const int64_t j = base + my_token;
@@ -155,7 +155,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                     if (hk < 0 ? a.wq != nullptr : a.wk != nullptr) {
                         const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) f[i] = f[i] * inv * (hk < 0 ? wq[i] : wk[i]);
+                        for (int i = 0; i < 2; ++i) {
+                            float w[8];
+                            cvt8<MT>(hk < 0 ? wq[i] : wk[i], w);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[8 * i + e] = f[8 * i + e] * inv * w[e];
+                        }
                     }
                 }
                 if (!live[u]) continue;
@@ -282,8 +287,8 @@ cudaError_t launch_append_rotary(pkv_cache *c, const RotaryLaunch &r, cudaStream
     // few tokens: one a pass, its rows over several CTAs; many: up to four a pass, the cosines of the next pass found
     // while this one's rows are on their way
     const int rows_at_once = kThreads / (c->head_dim / 16);
-    a.tb = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxTokens, r.n / (c->num_sms * 4)));
-    const int64_t passes = (r.n + a.tb - 1) / a.tb, cap = (int64_t)c->num_sms * 4;
+    a.tb = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxTokens, r.n / (c->num_sms * 2)));
+    const int64_t passes = (r.n + a.tb - 1) / a.tb, cap = (int64_t)c->num_sms * kGridCtas;
     const unsigned gx = (unsigned)std::min(passes, cap);
     const unsigned gy = (unsigned)std::max<int64_t>(1, std::min<int64_t>((a.per_token * a.tb + rows_at_once - 1) / rows_at_once, cap / gx));
     const dim3 grid(gx, gy);
