@@ -1,0 +1,6 @@
+// Instantiations of the two-pipeline attention of chunks (chunk_stream.cuh): 16-bit caches, at most 64 rows.
+#include "chunk_stream.cuh"
+
+namespace pkv_prefill {
+PKV_STREAM_INSTANTIATE(false, true)
+} // namespace pkv_prefill

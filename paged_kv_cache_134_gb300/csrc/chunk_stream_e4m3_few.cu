@@ -1,0 +1,6 @@
+// Instantiations of the two-pipeline attention of chunks (chunk_stream.cuh): E4M3 caches, at most 64 rows.
+#include "chunk_stream.cuh"
+
+namespace pkv_prefill {
+PKV_STREAM_INSTANTIATE(true, true)
+} // namespace pkv_prefill

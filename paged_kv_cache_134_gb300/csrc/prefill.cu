@@ -6,7 +6,7 @@
 #include <cstdlib>
 #include <mutex>
 
-#include "prefill_impl.cuh"
+#include "chunk_stream.cuh"
 
 namespace pkv_prefill {
 
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
     }
 }
 
-// The work list of chunk and stream mode: every (sequence, row tile or pair of them, split or pair of them), heaviest first as
-// above.  A warp takes a sequence, its lanes the row tiles (long chunks have hundreds).
+// The work list of a chunk call: every (sequence, row tile or pair of them, split), heaviest first as above.  A warp takes a
+// sequence, its lanes the row tiles (long chunks have hundreds).
 template <bool STREAM>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Args a) {
     extern __shared__ int sh[];
@@ -117,13 +117,19 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Args a) 
     int4 *list = reinterpret_cast<int4 *>(a.plan + 4);
     auto visit = [&](bool report, auto &&entry) {
         for (int i = warp; i < a.num_seqs; i += kPlanThreads / 32) {
-            const int n = chunk_groups<STREAM>(a, i, report && lane == 0);
+            const int n = chunk_groups<!STREAM>(a, i, report && lane == 0);
             for (int g = lane; g < n; g += 32) {
-                ChunkItem it = chunk_item<STREAM>(a, i, g, 0, 0);
-                const int items = chunk_parts<STREAM>(it);
-                for (int k = 0; k < items; ++k) {
-                    if (k > 0) it = chunk_item<STREAM>(a, i, g, k, 0);
-                    entry(i, g, k, min(it.t[0].n + it.t[1].n, R - 1));
+                // (splits are of equal size but for the last one)
+                const int parts = STREAM ? max(1, stream_unit(a, i, g, 0, 0).nsplit) : chunk_parts(chunk_item(a, i, g, 0, 0));
+                for (int k = 0; k < parts; ++k) {
+                    int cost;
+                    if constexpr (STREAM) {
+                        cost = stream_unit(a, i, g, k, 0).n;
+                    } else {
+                        const ChunkItem it = chunk_item(a, i, g, k, 0);
+                        cost = it.t[0].n + it.t[1].n;
+                    }
+                    entry(i, g, k, min(cost, R - 1));
                 }
             }
         }
@@ -166,8 +172,7 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const Args a) {
         (int64_t)a.lens[lo] > (int64_t)a.max_blocks * a.bs)
         return;
     const int tile = (tok - st) / (BM >> a.lg_group);
-    const ChunkItem it = chunk_item<STREAM>(a, lo, STREAM ? tile : tile / 2, 0, 0);
-    const int n = STREAM ? it.ns[0] : chunk_splits(it, tile & 1);
+    const int n = STREAM ? stream_unit(a, lo, tile, 0, 0).nsplit : chunk_splits(chunk_item(a, lo, tile / 2, 0, 0), tile & 1);
     if (n <= 1) return;
     const int64_t base = ((int64_t)tok * a.hq + h) * a.max_splits;
     const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + base;
@@ -250,13 +255,13 @@ bool make_map(CUtensorMap *m, const void *base, int mt, int64_t rows, int64_t co
     return r == CUDA_SUCCESS;
 }
 
-// q or out [T][Hq][D] as tiles of 128 (token, head of a group) rows: box = 64 dims x G heads x 128 / G tokens
-bool make_group_map(CUtensorMap *m, const void *base, int mt, int64_t tokens, int hq, int D, int G) {
+// q or out [T][Hq][D] as tiles of 128 (or `rows`) (token, head of a group) rows: box = 64 dims x G heads x rows / G tokens
+bool make_group_map(CUtensorMap *m, const void *base, int mt, int64_t tokens, int hq, int D, int G, int rows = BM) {
     EncodeFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)hq, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)hq * D * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(BM / G)};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(rows / G)};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUtensorMapDataType dt = mt == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const CUresult r = enc(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -294,6 +299,15 @@ bool pool_map(CUtensorMap *m, const pkv_cache *c) {
     if (c->kv_dtype == PKV_FP8_E4M3) return make_code_map(m, c->pool, pool_rows, c->head_dim, c->block_size);
     return make_map(m, c->pool, c->model_dtype, pool_rows, c->head_dim, c->block_size);
 }
+
+template <>
+cudaError_t launch_stream_any<false, true>(int, int, const CUtensorMap &, const CUtensorMap &, const Args &, int, cudaStream_t);
+template <>
+cudaError_t launch_stream_any<false, false>(int, int, const CUtensorMap &, const CUtensorMap &, const Args &, int, cudaStream_t);
+template <>
+cudaError_t launch_stream_any<true, true>(int, int, const CUtensorMap &, const CUtensorMap &, const Args &, int, cudaStream_t);
+template <>
+cudaError_t launch_stream_any<true, false>(int, int, const CUtensorMap &, const CUtensorMap &, const Args &, int, cudaStream_t);
 
 template <int MODE, bool KV8>
 cudaError_t dispatch(int D, int mt, const Maps &m, const Args &a, int64_t max_ctas, int num_sms, cudaStream_t st) {
@@ -523,12 +537,12 @@ struct ChunkShape {
     bool stream;
     int split_steps, max_splits;
     int64_t groups, items; // (sequence, row tile or pair) at most; times the splits of each
-    int max_groups, max_parts; // of a sequence; of a group's keys
+    int max_groups;        // of a sequence
     // Few items: no list and no launch for it (one sequence of 2047 tokens: 16 us for 23).  Many: heaviest first from a list
     // (32 sequences of up to 4096 tokens, 32 heads, by turns: 224 us for 205).
     bool direct(const pkv_cache *c, int num_seqs) const { return rect(c, num_seqs) <= 2 * (int64_t)c->num_sms; }
     int64_t rect(const pkv_cache *c, int num_seqs) const {
-        return (int64_t)num_seqs * max_groups * max_parts * c->num_kv_heads;
+        return (int64_t)num_seqs * max_groups * max_splits * c->num_kv_heads;
     }
     int64_t floats(const pkv_cache *c, int64_t tokens, int hq) const {
         const int64_t list = (4 + 4 * items + 63) / 64 * 64;
@@ -541,7 +555,7 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
     ChunkShape s;
     const int G = hq / c->num_kv_heads, bs = c->block_size;
     const int per = BM / G; // tokens of a row tile
-    // one row tile: its keys as two streams; more: tiles in pairs that share their keys
+    // one row tile: units by themselves, two at a time on an SM (chunk_stream.cuh); more: tiles in pairs that share their keys
     s.stream = max_seqlen <= per;
     const int group = s.stream ? per : 2 * per;
     s.groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + group - 1) / group), tokens / group + num_seqs);
@@ -552,13 +566,12 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
     // (one sequence of 2047 tokens, 56 rows: 16 us with one tile a split, 20 with two, 25 with four; 512 tokens after
     // 131071: 1.11 ms with 32 tiles at most, 1.24 with 16, 1.16 with 64)
     constexpr int64_t kLeast = 1, kMost = 32;
-    const int64_t share = (s.groups * c->num_kv_heads * steps + c->num_sms - 1) / c->num_sms;
-    s.split_steps = (int)std::min(kMost, std::max(kLeast, s.stream ? (share + 1) / 2 : share));
+    const int64_t places = (int64_t)c->num_sms * (s.stream ? 2 : 1);
+    const int64_t share = (s.groups * c->num_kv_heads * steps + places - 1) / places;
+    s.split_steps = (int)std::min(kMost, std::max(kLeast, share));
     s.max_splits = (int)((steps + s.split_steps - 1) / s.split_steps);
-    if (s.stream) s.max_splits = steps <= 2 ? 1 : (int)(2 * ((steps + 2 * s.split_steps - 1) / (2 * s.split_steps)));
     s.max_groups = (max_seqlen + group - 1) / group;
-    s.max_parts = s.stream ? (s.max_splits + 1) / 2 : s.max_splits;
-    s.items = s.groups * s.max_parts;
+    s.items = s.groups * s.max_splits;
     return s;
 }
 
@@ -574,9 +587,18 @@ cudaError_t launch_chunk_t(pkv_cache *c, const Args &a, const Maps &m, int64_t c
         g_pkv_launches++;
         if (e != cudaSuccess) return e;
     }
-    constexpr int MODE = STREAM ? MODE_STREAM : MODE_CHUNK;
-    e = c->kv_dtype == PKV_FP8_E4M3 ? dispatch<MODE, true>(D, mt, m, a, ctas, c->num_sms, st)
-                                    : dispatch<MODE, false>(D, mt, m, a, ctas, c->num_sms, st);
+    const bool kv8 = c->kv_dtype == PKV_FP8_E4M3;
+    if constexpr (STREAM) {
+        const bool few = (a.max_seqlen << a.lg_group) <= 64;
+        const int grid = (int)std::min<int64_t>(ctas, c->num_sms);
+        e = kv8 ? (few ? launch_stream_any<true, true>(D, mt, m.q, m.pool, a, grid, st)
+                       : launch_stream_any<true, false>(D, mt, m.q, m.pool, a, grid, st))
+                : (few ? launch_stream_any<false, true>(D, mt, m.q, m.pool, a, grid, st)
+                       : launch_stream_any<false, false>(D, mt, m.q, m.pool, a, grid, st));
+    } else {
+        e = kv8 ? dispatch<MODE_CHUNK, true>(D, mt, m, a, ctas, c->num_sms, st)
+                : dispatch<MODE_CHUNK, false>(D, mt, m, a, ctas, c->num_sms, st);
+    }
     g_pkv_launches++;
     if (e != cudaSuccess || a.max_splits <= 1) return e;
     const dim3 grid((unsigned)a.total_tokens, (unsigned)((a.hq + 3) / 4));
@@ -594,9 +616,9 @@ int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens,
     // those stay below 2 SMs tiles of 256 rows.
     const int64_t steps = ((int64_t)max_blocks * c->block_size + BN - 1) / BN, splits = steps / 32 + 3;
     const int64_t rows = tokens * hq;
-    const int64_t partials = rows * splits + std::min<int64_t>(rows * (steps / 4 + 2), 2 * 256 * (int64_t)c->num_sms);
+    const int64_t partials = rows * splits + std::min<int64_t>(rows * steps, 2 * 256 * (int64_t)c->num_sms);
     const int64_t groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + 15) / 16), tokens / 16 + num_seqs);
-    const int64_t items = groups * splits + std::min<int64_t>(groups * (steps / 4 + 2), 2 * (int64_t)c->num_sms);
+    const int64_t items = groups * splits + std::min<int64_t>(groups * steps, 2 * (int64_t)c->num_sms);
     return (4 + 4 * items + 63) / 64 * 64 + partials * (c->head_dim + 2);
 }
 
@@ -625,8 +647,9 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     a.plan_cap = s.items;
     a.cost_bins = 2 * std::max(s.split_steps, 1) + 2;
     Maps m;
-    if (!make_group_map(&m.q, p.q, mt, p.total_tokens, hq, D, hq / c->num_kv_heads) ||
-        !make_group_map(&m.out, p.out, mt, p.total_tokens, hq, D, hq / c->num_kv_heads) || !(D == 128 && c->kv_dtype != PKV_FP8_E4M3 ? pkv_tmap_rows128_grouped(&m.pool, c->pool, mt, pool_rows, c->block_size)
+    const int G = hq / c->num_kv_heads, tile = s.stream && p.max_seqlen * G <= 64 ? 64 : BM;
+    if (!make_group_map(&m.q, p.q, mt, p.total_tokens, hq, D, G, tile) ||
+        !make_group_map(&m.out, p.out, mt, p.total_tokens, hq, D, G) || !(D == 128 && c->kv_dtype != PKV_FP8_E4M3 ? pkv_tmap_rows128_grouped(&m.pool, c->pool, mt, pool_rows, c->block_size)
                                                   : pool_map(&m.pool, c)))
         return pkv_fail(PKV_ECUDA, "tensor map");
     m.k = m.v = m.pool;
@@ -637,7 +660,7 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     a.plan = direct ? nullptr : reinterpret_cast<int *>(ws.p);
     if (direct) {
         a.max_groups = s.max_groups;
-        a.max_parts = s.max_parts;
+        a.max_parts = s.max_splits;
         a.rect = (int)s.rect(c, p.num_seqs);
     }
     a.ws_o = ws.p + (4 + 4 * s.items + 63) / 64 * 64;

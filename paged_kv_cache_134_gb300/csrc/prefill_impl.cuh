@@ -12,7 +12,7 @@
 // rows sit at positions ctx[i] + r and every key is read from the pool through the block table.  In
 // cascade mode the queries are the decode queries of a batch (one row per sequence) and the keys are
 // a prefix shared by every table (section 3.3), cut into splits whose fp32 partials a merge combines.
-// In chunk and stream mode (paged_chunk_attention) the last n_i of a sequence's L_i cached tokens are its queries, the
+// In chunk mode (paged_chunk_attention, pieces of prompts) the last n_i of a sequence's L_i cached tokens are its queries, the
 // group's query heads of a token lie side by side in a tile's rows (a KV head's keys are read once for all of them), the
 // keys may be cut into splits, and a window with sinks may hide keys: see ChunkItem.
 //
@@ -57,7 +57,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f; // log2 units
 constexpr int kCodeOff = 16384;  // E4M3 codes of a stage: row r at stage + kCodeOff + r * D
 
-enum { MODE_PACKED = 0, MODE_PAGED = 1, MODE_CASCADE = 2, MODE_CHUNK = 3, MODE_STREAM = 4 };
+enum { MODE_PACKED = 0, MODE_PAGED = 1, MODE_CASCADE = 2, MODE_CHUNK = 3 };
 
 struct Args {
     const char *k, *v;  // packed [T][Hkv][D] (packed mode)
@@ -78,7 +78,7 @@ struct Args {
     // leaves an fp32 partial (m, l, unnormalised o) in workspace slot split
     float *ws_o = nullptr, *ws_ml = nullptr;
     int max_splits = 0, prefix_tokens = 0, split_tokens = 0, nps = 0;
-    // chunk and stream mode: tokens of each sequence, the new ones included; the last `window` keys (0: all) and the first
+    // chunk mode and chunk_stream.cuh: tokens of each sequence, the new ones included; the last `window` keys (0: all) and the first
     // `sinks` are attended to; log2 of the query heads per KV head; key tiles of a split, about
     const int32_t *lens = nullptr;
     int window = 0, sinks = 0, lg_group = 0, split_steps = 0;
@@ -100,7 +100,7 @@ struct Maps {
 // of the stage, which each row's widening thread reads whole before it writes it; for D = 64 they
 // follow the 16 KB tile.
 //
-// ONE_Q (cascade, stream): one Q tile, and the rings in halves, one per key stream (tile t has stages t, t + 2): a
+// ONE_Q (cascade): one Q tile, and the rings in halves, one per key stream (tile t has stages t, t + 2): a
 // stage's barriers then see every phase waited for by one issuer.  (In one ring for both streams, an issuer would come
 // back to a stage after two of its phases, and find the one before the other stream's, whose parity is the same,
 // complete where its own tile is still on its way.)
@@ -174,19 +174,19 @@ PKV_DEV void widen_row(uint8_t *stage, int r) {
     }
 }
 
-// E4M3 caches in chunk and stream mode: four more warps widen the codes, so that the loads of the next tiles are on their way
+// E4M3 caches in chunk mode: four more warps widen the codes, so that the loads of the next tiles are on their way
 // meanwhile (a loader that widened its own tiles, one row after another, took 16000 cycles for a pair of tiles that
 // HBM brings in 2900).  Codes land in rings of their own, row r at r * D; the 16-bit tiles are fp16 whatever the model's type
 // (exact; P then is one fp16 and not a pair), and a bf16 q is brought into fp16's range by a power of two for each
 // row, which is left behind the layout for the softmax.
-template <int D, bool ONE_Q>
+template <int D>
 struct CodeLayout {
-    static constexpr int NKS = D == 128 ? 2 : ONE_Q ? 4 : 3, NVS = NKS; // fp16 tiles
-    static constexpr int NCS = D == 128 ? (ONE_Q ? 2 : 1) : 3;         // code stages, of K and of V
+    static constexpr int NKS = D == 128 ? 2 : 3, NVS = NKS; // fp16 tiles
+    static constexpr int NCS = D == 128 ? 1 : 3;            // code stages, of K and of V
     static constexpr int Q_TILE = BM * D * 2;
     static constexpr int TILE = BN * D * 2, STAGE = TILE, CODE = BN * D;
     static constexpr int Q = 0;
-    static constexpr int K0 = Q + (ONE_Q ? 1 : 2) * Q_TILE;
+    static constexpr int K0 = Q + 2 * Q_TILE;
     static constexpr int V0 = K0 + NKS * STAGE;
     static constexpr int C0 = V0 + NVS * STAGE; // K codes, then V codes
     static constexpr int BAR = C0 + 2 * NCS * CODE;
@@ -196,19 +196,16 @@ struct CodeLayout {
     static_assert(NCS <= NKS && NCS <= NVS, "their barriers share the arrays");
 };
 template <int D, int MODE, bool KV8>
-using LayoutOf = std::conditional_t<KV8 && (MODE == MODE_CHUNK || MODE == MODE_STREAM),
-                                    CodeLayout<D, MODE == MODE_STREAM>,
-                                    Layout<D, KV8, MODE == MODE_CASCADE || MODE == MODE_STREAM>>;
+using LayoutOf = std::conditional_t<KV8 && MODE == MODE_CHUNK, CodeLayout<D>, Layout<D, KV8, MODE == MODE_CASCADE>>;
 template <int D, int MODE, bool KV8>
 constexpr int smem_total() {
-    constexpr bool chunked = MODE == MODE_CHUNK || MODE == MODE_STREAM;
-    constexpr int n = LayoutOf<D, MODE, KV8>::TOTAL + (chunked && KV8 ? 4 * BM : 0);
+    constexpr int n = LayoutOf<D, MODE, KV8>::TOTAL + (MODE == MODE_CHUNK && KV8 ? 4 * BM : 0);
     static_assert(n + 1024 <= 232448, "shared memory");
     return n;
 }
 template <int MODE, bool KV8>
 constexpr int threads_of() {
-    return KV8 && (MODE == MODE_CHUNK || MODE == MODE_STREAM) ? kThreads + 128 : kThreads;
+    return KV8 && MODE == MODE_CHUNK ? kThreads + 128 : kThreads;
 }
 
 // row r of a tile of E4M3 codes -> fp16 in the 128-byte-swizzled layout (lanes take the row's sixteens in turn, so that
@@ -339,34 +336,24 @@ PKV_DEV Item decode_item(const Args &a, int seq, int pr, int h) {
     return it;
 }
 
-// Chunk mode: two row tiles A and B of one (sequence, KV head) over the same keys, one split of them.  Stream mode: one row tile
-// over two neighbouring splits, for chunks of few rows, whose keys then pass through two chains of products at a time.
-// Row r of a tile is token q0 + r / G, query head h G + r % G.  Keys are counted in "seen" order: the blocks
+// Chunk mode: two row tiles A and B of one (sequence, KV head) over the same keys, one split of them.  Row r of a tile is token q0 + r / G, query head h G + r % G.  Keys are counted in "seen" order: the blocks
 // that a row of the item can see, one after the other, as if nothing lay between (seen block i is logical block i, or
 // i + skip from block `from` on).  Of them [lo, hi) are hidden from every row (the rest of the sinks' last block, and what
 // lies before the first row's window); what else a row does not see is masked.
 // How the keys are cut depends on the sequence's own lengths and the call's sizes, not on the other sequences.
 struct ChunkItem : Item {
     int from, skip, lo, hi;
-    int split;  // chunk: the split; stream: the pair of splits
+    int split;
     int ns[2];  // splits of each tile's keys (1: the tile's rows are final)
     bool zero;  // rows without keys: written as zeros by the first split's item
 };
 
-// key tiles of a split, of n in all: n / ceil(n / split_steps); stream mode: an even number of splits, unless the tiles are
-// too few to be worth a merge
-template <bool STREAM>
+// key tiles of a split, of n in all: splits of equal size
 PKV_DEV int steps_per_split(const Args &a, int n) {
-    if (STREAM) {
-        if (n <= 2) return 2;
-        const int k = 2 * ((n + 2 * a.split_steps - 1) / (2 * a.split_steps));
-        return (n + k - 1) / k;
-    }
     const int k = (n + a.split_steps - 1) / a.split_steps;
     return k > 1 ? (n + k - 1) / k : max(n, 1);
 }
 
-template <bool STREAM>
 PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
     ChunkItem it;
     it.seq = seq;
@@ -379,7 +366,7 @@ PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
     it.n = a.cu[seq + 1] - it.start;
     it.trow = seq;
     const int before = max(a.lens[seq], 0) - it.n; // position of the first new token (negative: those rows see nothing)
-    const int tok0 = (STREAM ? pr : 2 * pr) * per_tile;
+    const int tok0 = 2 * pr * per_tile;
     const int low = a.window > 0 ? max(before + tok0 - a.window + 1, 0) : 0; // first key of the first row's window
     it.from = it.skip = it.lo = it.hi = 0;
     if (low > a.sinks) {
@@ -392,30 +379,27 @@ PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         Tile &x = it.t[t];
-        x.q0 = tok0 + (STREAM ? 0 : t * per_tile);
+        x.q0 = tok0 + t * per_tile;
         x.qlast = min(x.q0 + per_tile, it.n) - 1;
         x.qpos0 = before + x.q0;
         end[t] = x.q0 < it.n ? max(before + x.qlast + 1 - (it.skip << a.lg_bs), 0) : 0;
         n[t] = (end[t] + BN - 1) / BN;
     }
-    const int most = max(n[0], n[1]), per = steps_per_split<STREAM>(a, most);
-    it.zero = false;
+    const int per = steps_per_split(a, max(n[0], n[1]));
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         Tile &x = it.t[t];
-        const int j0 = (STREAM ? 2 * split + t : split) * per;
-        x.k0 = j0 * BN;
-        x.n = min(max(n[t] - j0, 0), per);
-        // (chunk: one end for both tiles, whose loads they share)
-        x.kend = min(STREAM ? end[t] : max(end[0], end[1]), x.k0 + per * BN);
+        x.k0 = split * per * BN;
+        x.n = min(max(n[t] - split * per, 0), per);
+        x.kend = min(max(end[0], end[1]), x.k0 + per * BN); // (one end for both tiles, whose loads they share)
         it.ns[t] = (n[t] + per - 1) / per;
     }
     it.zero = split == 0;
     return it;
 }
 
-// row tiles of sequence i (stream) or pairs of them (chunk); 0 where its numbers make no sense
-template <bool STREAM>
+// row tiles of sequence i, or (PAIRS) pairs of them; 0 where its numbers make no sense
+template <bool PAIRS>
 PKV_DEV int chunk_groups(const Args &a, int i, bool report) {
     const int st = a.cu[i], en = a.cu[i + 1];
     if (st < 0 || en < st || en > a.total_tokens || en - st > a.max_seqlen) {
@@ -426,24 +410,19 @@ PKV_DEV int chunk_groups(const Args &a, int i, bool report) {
         if (report) set_error(a.err, PKV_DEVERR_LENGTH);
         return 0;
     }
-    const int per = (STREAM ? 1 : 2) * (BM >> a.lg_group);
+    const int per = (PAIRS ? 2 : 1) * (BM >> a.lg_group);
     return (en - st + per - 1) / per;
 }
 // items of a group: at least the one that writes the rows without keys
-template <bool STREAM>
-PKV_DEV int chunk_parts(const ChunkItem &it) {
-    const int ns = max(it.ns[0], it.ns[1]);
-    return max(1, STREAM ? (ns + 1) / 2 : ns);
-}
+PKV_DEV int chunk_parts(const ChunkItem &it) { return max(1, max(it.ns[0], it.ns[1])); }
 // the next item of this CTA among all that the call's sizes allow, from `at` on: (sequence, group, KV head, part), -1 behind
 // the last
-template <bool STREAM>
 PKV_DEV int4 direct_item(const Args &a, int &at) {
     for (; at < a.rect; at += gridDim.x) {
         const int h = at % a.hkv, r = at / a.hkv, part = r % a.max_parts, g = r / a.max_parts % a.max_groups;
         const int seq = r / a.max_parts / a.max_groups;
-        if (g >= chunk_groups<STREAM>(a, seq, h == 0 && part == 0 && g == 0)) continue;
-        if (part > 0 && part >= chunk_parts<STREAM>(chunk_item<STREAM>(a, seq, g, 0, 0))) continue;
+        if (g >= chunk_groups<true>(a, seq, h == 0 && part == 0 && g == 0)) continue;
+        if (part > 0 && part >= chunk_parts(chunk_item(a, seq, g, 0, 0))) continue;
         at += gridDim.x;
         return make_int4(seq, g, h, part);
     }
@@ -451,7 +430,7 @@ PKV_DEV int4 direct_item(const Args &a, int &at) {
 }
 
 // Loads of K (or V) tiles of an item, in their order.  Packed, paged and chunk modes share one key tile per step; cascade
-// and stream mode have one per tile and step.
+// mode has one per tile and step.
 template <bool SHARED>
 PKV_DEV int ring_count(const Item &it) {
     return SHARED ? max(it.t[0].n, it.t[1].n) : it.t[0].n + it.t[1].n;
@@ -486,17 +465,16 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
     using L = LayoutOf<D, MODE, KV8>;
     constexpr bool PAGED = MODE != MODE_PACKED;    // keys from the pool through the block table
     constexpr bool CASCADE = MODE == MODE_CASCADE; // no causal mask, fp32 split partials out
-    constexpr bool STREAM = MODE == MODE_STREAM;
-    constexpr bool CHUNKED = MODE == MODE_CHUNK || STREAM;
-    constexpr bool ONE_Q = CASCADE || STREAM;      // one Q tile, two key streams
+    constexpr bool CHUNKED = MODE == MODE_CHUNK;
+    constexpr bool ONE_Q = CASCADE;                // one Q tile, two key streams
     constexpr bool SHARED = !ONE_Q;                // both tiles use the same key tiles
-    // K and V tiles of chunk and stream mode at D = 128, 16-bit caches: one box a block brings both halves of its rows, as
+    // K and V tiles of chunk mode at D = 128, 16-bit caches: one box a block brings both halves of its rows, as
     // [8 rows][half][8 rows][128 bytes]; else one box for each half, as [half][128 rows][128 bytes].  (A loader's warp needs
     // some 100 cycles for each box; with two a block, short chunks were bound by their loaders.)
     constexpr bool GROUPED = CHUNKED && D == 128 && !KV8;
     using It = std::conditional_t<CHUNKED, ChunkItem, Item>;
     constexpr bool WRITER = MODE == MODE_PACKED;   // the loaders write the item's K/V rows into the pool
-    constexpr bool CODES = KV8 && (MODE == MODE_CHUNK || MODE == MODE_STREAM); // widened by warps of their own (CodeLayout)
+    constexpr bool CODES = KV8 && CHUNKED;         // widened by warps of their own (CodeLayout)
     constexpr int OT = CODES ? (int)PKV_F16 : MT;  // the products' operands
     constexpr int NP = OT == PKV_BF16 ? 2 : 1;     // P parts (bf16: hi + lo)
     constexpr int EB = KV8 ? 1 : 2;                // pool bytes per element
@@ -546,7 +524,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(q_full + s, 1);
-            mbar_init(q_empty + s, ONE_Q ? 2 : 1); // cascade, stream: one Q tile, read by both MMA warps
+            mbar_init(q_empty + s, ONE_Q ? 2 : 1); // cascade: one Q tile, read by both MMA warps
             mbar_init(s_full + s, 1);
             mbar_init(p_full + s, 4); // one arrival per softmax warp
             mbar_init(o_full + s, 1);
@@ -597,7 +575,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
     auto make_item = [&](int seq, int pr, int h, int split) -> It {
         (void)split;
         if constexpr (CHUNKED)
-            return chunk_item<STREAM>(a, seq, pr, split, h);
+            return chunk_item(a, seq, pr, split, h);
         else
             return decode_item(a, seq, pr, h);
     };
@@ -724,7 +702,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
         int64_t g = 0;
         int gt[2] = {0, 0};
         auto next_stage = [&](int t, int &st, int &round) {
-            if constexpr (ONE_Q && !CODES) {
+            if constexpr (ONE_Q) {
                 const int c = t ? gt[1] : gt[0];
                 st = t + 2 * (c % (ns / 2));
                 round = c / (ns / 2);
@@ -773,7 +751,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                 int idx = total;
                 if (direct) {
                     if constexpr (CHUNKED) {
-                        if (!*abort_flag) raw = direct_item<STREAM>(a, next_direct);
+                        if (!*abort_flag) raw = direct_item(a, next_direct);
                     }
                 } else if (!*abort_flag) {
                     idx = atomicAdd(a.plan + 1, 1);
@@ -983,7 +961,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                     }
                 }
                 ++g;
-                if constexpr (ONE_Q && !CODES) ++(tile ? gt[1] : gt[0]);
+                if constexpr (ONE_Q) ++(tile ? gt[1] : gt[0]);
                 if constexpr (KV8 && !CODES) pend = st | (round & 1) << 8;
                 if (isK && e < 2) issue_q(e); // Q_A after K tile 0, Q_B after K tile 1
             }
@@ -1002,7 +980,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
         if constexpr (WRITER) tc::bulk_wait_all();
         // the last loads must land before this CTA's shared memory goes away
         if (lane == 0) {
-            if constexpr (ONE_Q && !CODES) {
+            if constexpr (ONE_Q) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     for (int c = max(gt[t] - ns / 2, 0); c < gt[t]; ++c)
@@ -1139,8 +1117,8 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                     adv(vst, vph, VN);
                 }
             } else {
-                if (nt == 0 && ok && (CASCADE || it.t[0].n > 0)) {
-                    // cascade, stream: no split for this tile; its share of the Q buffer once Q has landed
+                if (nt == 0 && ok) {
+                    // cascade: no split for this tile; its share of the Q buffer once Q has landed
                     ok = __all_sync(0xffffffffu, mbar_wait_hint(q_ready + qb, qph));
                     if (ok && lane == 0) mbar_arrive(q_empty + qb);
                     qph ^= 1u;
@@ -1158,27 +1136,18 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
         }
     } else if (CODES && warp >= 12) {
         // ---------------------------------------------------------------- widening (warps 12-15)
-        // Thread r owns row r of every tile, K or V, in the loaders' order, K one tile ahead of V (a V tile waits for the
-        // products with the one before it, the next K tile only for its own stage), and of every bf16 Q tile.
+        // Thread r owns row r of every tile, K or V, K one tile ahead of V (a V tile waits for the products with the one
+        // before it, the next K tile only for its own stage), and of every bf16 Q tile.
         if constexpr (CODES) {
             const int r = (warp - 12) * 32 + lane;
             bool ok = true;
-            uint32_t g[2] = {0, 0};                     // K, V tiles widened
-            uint32_t gt[2][2] = {{0, 0}, {0, 0}};       // stream: those of each key stream
-            uint32_t nq[2] = {0, 0};                    // Q tiles
-            auto widen = [&](auto which, int t) -> bool {
+            uint32_t g[2] = {0, 0};  // K, V tiles widened
+            uint32_t nq[2] = {0, 0}; // Q tiles
+            auto widen = [&](auto which) -> bool {
                 constexpr int kv = decltype(which)::value;
                 uint64_t *const land = kv ? v_full : k_full, *const read = kv ? v_spare : k_spare;
                 uint64_t *const free = kv ? v_empty : k_empty, *const done = kv ? vc_full : kc_full;
-                uint32_t st, round;
-                if constexpr (ONE_Q) {
-                    const uint32_t c = t ? gt[kv][1]++ : gt[kv][0]++;
-                    st = t + 2 * (c % (NKS / 2));
-                    round = c / (NKS / 2);
-                } else {
-                    st = g[kv] % NKS;
-                    round = g[kv] / NKS;
-                }
+                const uint32_t st = g[kv] % NKS, round = g[kv] / NKS;
                 const uint32_t cs = g[kv] % L::NCS;
                 bool w = mbar_wait_hint(land + cs, (g[kv] / L::NCS) & 1u);
                 ++g[kv];
@@ -1213,13 +1182,12 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                     n0 = it.t[0].n;
                     n1 = it.t[1].n;
                 }
-                const int ne = SHARED ? max(n0, n1) : n0 + n1, both = 2 * min(n0, n1);
-                auto tile_of = [&](int e) -> int { return SHARED ? 0 : e < both ? e & 1 : n0 > n1 ? 0 : 1; };
+                const int ne = max(n0, n1);
                 // step -1: K tile 0 and Q_A; step e: K tile e + 1, (step 0: Q_B), V tile e
                 for (int e = -1; e < ne && ok; ++e) {
-                    if (e + 1 < ne) ok = widen(std::integral_constant<int, 0>(), tile_of(e + 1));
-                    if (ok && (e == -1 ? n0 > 0 : !ONE_Q && e == 0 && n1 > 0)) ok = convert_q(e + 1);
-                    if (ok && e >= 0) ok = widen(std::integral_constant<int, 1>(), tile_of(e));
+                    if (e + 1 < ne) ok = widen(std::integral_constant<int, 0>());
+                    if (ok && (e == -1 ? n0 > 0 : e == 0 && n1 > 0)) ok = convert_q(e + 1);
+                    if (ok && e >= 0) ok = widen(std::integral_constant<int, 1>());
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(item_empty + (n & (kItemSlots - 1)));
@@ -1277,7 +1245,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                     if constexpr (CODES && MT == PKV_BF16) {
                         // q's power of two: S is complete, so the row is converted; the next but one Q tile, which
                         // writes this slot again, waits for the next one's S, and that for this row's P
-                        if (j == 0) sl *= exp2f((float)q_exp[((q_seen & 1) * 2 + (ONE_Q ? 0 : t)) * BM + r]);
+                        if (j == 0) sl *= exp2f((float)q_exp[((q_seen & 1) * 2 + t) * BM + r]);
                     }
                     uint32_t sr[BN];
 #pragma unroll
@@ -1419,14 +1387,13 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                     if constexpr (CHUNKED) {
                         // fp32 partial of one of several splits, as in cascade mode; the Q buffer is not used
                         const int tok = x.q0 + (r >> a.lg_group);
-                        const int split = STREAM ? 2 * it.split + t : it.split;
                         const int64_t idx =
-                            ((int64_t)(it.start + tok) * a.hq + it.h * G + (r & (G - 1))) * a.max_splits + split;
+                            ((int64_t)(it.start + tok) * a.hq + it.h * G + (r & (G - 1))) * a.max_splits + it.split;
                         uint32_t o[D];
 #pragma unroll
                         for (int cc = 0; cc < D / 32; ++cc) tc::ld32(tO + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[cc * 32]));
                         tc::wait_ld();
-                        if (!ONE_Q && (warp & 3) == 0 && lane == 0) mbar_arrive(q_empty + t);
+                        if ((warp & 3) == 0 && lane == 0) mbar_arrive(q_empty + t);
                         if (tok <= x.qlast) {
                             float4 *dst = reinterpret_cast<float4 *>(a.ws_o + idx * D);
 #pragma unroll
@@ -1437,7 +1404,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                         }
                     }
                 } else {
-                    // (chunk and stream mode: rows are (token, head) pairs, and one may see no key)
+                    // (chunk mode: rows are (token, head) pairs, and one may see no key)
                     const int row = CHUNKED ? x.q0 + (r >> a.lg_group) : x.q0 + r;
                     const int tile_rows = CHUNKED ? BM >> a.lg_group : BM;
                     const float inv = CHUNKED && l == 0.f ? 0.f : vs / l;
@@ -1446,7 +1413,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                     for (int cc = 0; cc < D / 32; ++cc) tc::ld32(tO + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[cc * 32]));
                     tc::wait_ld();
                     const bool lead = (warp & 3) == 0 && lane == 0;
-                    if (!STREAM && x.q0 + tile_rows <= it.n) {
+                    if (x.q0 + tile_rows <= it.n) {
                         // a whole tile of the sequence's rows: staged in this tile's Q buffer (free, since the
                         // tile's last S has completed) in the Q tile's own 128-byte swizzled layout, then one TMA
                         // store per 64 columns writes coalesced rows; the buffer goes back to the Q loader once
@@ -1487,7 +1454,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                     } else {
                         // the sequence's last, partial tile: row by row, so that no row of the next sequence is
                         // written; the Q buffer is not used here and is free already
-                        if (!STREAM && lead) mbar_arrive(q_empty + t);
+                        if (lead) mbar_arrive(q_empty + t);
                         if (row < it.n) {
                             const int head = CHUNKED ? it.h * G + (r & (G - 1)) : it.h;
                             T *orow = static_cast<T *>(a.out) + ((int64_t)(it.start + row) * a.hq + head) * D;
@@ -1509,7 +1476,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
             } else if constexpr (CHUNKED) {
                 // rows that see no key at all
                 const int tok = x.q0 + (r >> a.lg_group);
-                if (it.zero && chunk_splits(it, t) == 0 && tok <= x.qlast && !(STREAM && t == 1)) {
+                if (it.zero && chunk_splits(it, t) == 0 && tok <= x.qlast) {
                     using T = typename ModelT<MT>::T;
                     uint4 *orow = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) +
                                                             ((int64_t)(it.start + tok) * a.hq + it.h * G + (r & (G - 1))) * D);
@@ -1519,7 +1486,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
             }
             steps0 += n0;
             steps1 += n1;
-            if (CODES && (ONE_Q ? n0 : x.n) > 0) ++q_seen;
+            if (CODES && x.n > 0) ++q_seen;
             __syncwarp();
             if (lane == 0) mbar_arrive(item_empty + (n & (kItemSlots - 1)));
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
@@ -1567,7 +1534,5 @@ PKV_ATTN_EXTERN(MODE_CASCADE, false)
 PKV_ATTN_EXTERN(MODE_CASCADE, true)
 PKV_ATTN_EXTERN(MODE_CHUNK, false)
 PKV_ATTN_EXTERN(MODE_CHUNK, true)
-PKV_ATTN_EXTERN(MODE_STREAM, false)
-PKV_ATTN_EXTERN(MODE_STREAM, true)
 
 } // namespace pkv_prefill
