@@ -15,11 +15,15 @@
 //
 // FEW (at most 64 rows, half a tile): both pipelines' rows lie in one Q tile, 0..63 and 64..127, and each multiplies all of
 // it (the other's rows come out as garbage that nobody reads).  Their softmax warps then sit on different quarters of
-// tensor memory, hence of the SM, and do not compete for the exponentials; warps without rows only pass the barriers on.
-// The room goes to a second K stage.
+// tensor memory, hence of the SM, and do not compete for the exponentials; of the four of a pipeline two have no rows and end,
+// or widen codes.  The room goes to a third stage.
 //
-// E4M3 caches: codes land in a ring of their own, K and V in turn, and two more warps a pipeline widen them to fp16 (see
-// CodeLayout); a bf16 q is scaled into fp16 by the same warps.
+// K and V tiles take turns in one ring, K(0), V(0), K(1), ...: with three stages V(j + 1) loads once S(j) is done and K(j + 2)
+// once P V(j) is, each about a step before it is needed.  (Rings of two for K and one for V: V(j + 1) could only follow
+// P V(j), and its way from HBM was in the chain of every step.)
+//
+// E4M3 caches: codes land in a ring of their own, K and V in turn, and two more warps a pipeline (FEW: four) widen them to
+// fp16 (see CodeLayout); a bf16 q is scaled into fp16 by the same warps.
 //
 // The loader works a unit out once and publishes it, while the unit before is being loaded, in a ring of four.
 // Every wait is bounded; a timeout sets PKV_DEVERR_TIMEOUT and the CTA winds down.
@@ -31,21 +35,22 @@ namespace pkv_prefill {
 
 template <int D, bool KV8, bool FEW>
 struct StreamLayout {
-    static constexpr int KN = !KV8 && FEW ? 2 : 1;                     // K stages of a pipeline (V: one)
+    static constexpr int NS = !KV8 && FEW ? 3 : 2;                     // stages of a pipeline, K and V in turn
     static constexpr int NC = KV8 ? (D == 64 ? 4 : FEW ? 2 : 1) : 0;   // code stages of a pipeline, K and V in turn
     static constexpr int Q_TILE = BM * D * 2, TILE = BN * D * 2, CODE = BN * D;
     static constexpr int NQ = FEW ? 1 : 2;
     static constexpr int Q = 0;
-    static constexpr int K0 = Q + NQ * Q_TILE;           // [pipeline][stage]
-    static constexpr int V0 = K0 + 2 * KN * TILE;        // [pipeline]
-    static constexpr int C0 = V0 + 2 * TILE;             // [pipeline][stage]
+    static constexpr int T0 = Q + NQ * Q_TILE;           // [pipeline][stage]
+    static constexpr int C0 = T0 + 2 * NS * TILE;        // [pipeline][stage]
     static constexpr int UNITS = C0 + 2 * NC * CODE;     // [pipeline][kUnitSlots] StreamUnit
     static constexpr int kUnitSlots = 4;
     static constexpr int EXP = UNITS + 2 * kUnitSlots * 64; // [pipeline][2 Q tiles][BM] exponents of q's rows (int8)
     static constexpr int BAR = EXP + (KV8 ? 2 * 2 * BM : 0);
-    // a pipeline's barriers: units full, empty; Q full, empty, as fp16; K full, empty; V full, empty; codes landed, read;
-    // S full, P full, O full, O free; end
-    static constexpr int NBARS = 2 * kUnitSlots + 3 + 2 * KN + 2 + 2 * (NC ? NC : 1) + 4 + 1;
+    // a pipeline's barriers: units full, empty; Q full, empty, as fp16; tiles full, empty; codes landed, read; S full, P
+    // full, O full, O free; end
+    static constexpr int NBARS = 2 * kUnitSlots + 3 + 2 * NS + 2 * (NC ? NC : 1) + 4 + 1;
+    static constexpr int kSoftmax = FEW ? 2 : 4;             // softmax warps of a pipeline
+    static constexpr int kWiden = KV8 ? (FEW ? 4 : 2) : 0;   // warps that widen
     static constexpr int MISC = BAR + 2 * NBARS * 8; // tensor-memory address, abort flag
     static constexpr int TOTAL = MISC + 16;
     static_assert(TOTAL + 1024 <= 232448, "shared memory");
@@ -130,19 +135,20 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
     constexpr int EB = KV8 ? 1 : 2;              // pool bytes per element
     constexpr bool GROUPED = D == 128 && !KV8;   // one box a block, [8 rows][half][8 rows][128 bytes] (see attn_kernel)
     constexpr bool SCALE_Q = KV8 && MT == PKV_BF16;
-    constexpr int KN = L::KN, NC = L::NC, NU = L::kUnitSlots;
+    constexpr int NS = L::NS, NC = L::NC, NU = L::kUnitSlots;
     constexpr int kRows = FEW ? 64 : 128;        // rows of a pipeline in the Q tile
     extern __shared__ __align__(1024) uint8_t smem[];
 
     pdl_trigger();
     if (smem_u32(smem) & 1023u) return; // the swizzled tiles need 1024-byte alignment (always true)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // loaders 0 and 2, issuers 1 and 3, softmax 4-7 and 8-11, widening 12-13 and 14-15
+    // loaders 0 and 2, issuers 1 and 3, softmax 4-7 and 8-11 (FEW: 4-5 and 10-11), widening 12-13 and 14-15 (FEW: and 6-7, 8-9)
     const int pipe = warp < 4 ? warp >> 1 : warp < 12 ? (warp - 4) >> 2 : (warp - 12) >> 1;
+    const bool spare = FEW && warp >= 6 && warp < 10;
     uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + L::BAR) + pipe * L::NBARS;
     uint64_t *const u_full = bars, *const u_empty = u_full + NU, *const q_full = u_empty + NU, *const q_empty = q_full + 1,
-                    *const qc_full = q_empty + 1, *const k_full = qc_full + 1, *const k_empty = k_full + KN,
-                    *const v_full = k_empty + KN, *const v_empty = v_full + 1, *const c_full = v_empty + 1,
+                    *const qc_full = q_empty + 1, *const t_full = qc_full + 1, *const t_empty = t_full + NS,
+                    *const c_full = t_empty + NS,
                     *const c_empty = c_full + (NC ? NC : 1), *const s_full = c_empty + (NC ? NC : 1), *const p_full = s_full + 1,
                     *const o_full = p_full + 1, *const o_free = o_full + 1, *const fin = o_free + 1;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC);
@@ -151,28 +157,26 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
     int8_t *const q_exp = reinterpret_cast<int8_t *>(smem + L::EXP) + pipe * 2 * BM;
     uint8_t *const q_tile = smem + L::Q + (FEW ? 0 : pipe * L::Q_TILE); // as the MMA reads it
     const int row_off = FEW ? pipe * 64 : 0;                            // the pipeline's first row in it
-    uint8_t *const k_ring = smem + L::K0 + pipe * KN * L::TILE, *const v_tile = smem + L::V0 + pipe * L::TILE;
+    uint8_t *const ring = smem + L::T0 + pipe * NS * L::TILE;
     uint8_t *const codes = smem + L::C0 + pipe * NC * L::CODE;
 
     if (threadIdx.x == 0) {
         for (int p = 0; p < 2; ++p) {
             uint64_t *b = reinterpret_cast<uint64_t *>(smem + L::BAR) + p * L::NBARS;
             for (int s = 0; s < NU; ++s) mbar_init(b++, 1);
-            for (int s = 0; s < NU; ++s) mbar_init(b++, KV8 ? 7 : 5); // issuer, four softmax warps, two that widen
-            mbar_init(b++, 1);                                        // Q full
-            mbar_init(b++, 1);                                        // Q empty
-            mbar_init(b++, 2);                                        // Q as fp16
-            for (int s = 0; s < KN; ++s) mbar_init(b++, KV8 ? 2 : 1); // K full: landed, or widened by two warps
-            for (int s = 0; s < KN; ++s) mbar_init(b++, 1);
-            mbar_init(b++, KV8 ? 2 : 1); // V full
-            mbar_init(b++, 1);
-            for (int s = 0; s < (NC ? NC : 1); ++s) mbar_init(b++, 1); // codes landed
-            for (int s = 0; s < (NC ? NC : 1); ++s) mbar_init(b++, 2); // codes read
-            mbar_init(b++, 1);                                         // S full
-            mbar_init(b++, 4);                                         // P full
-            mbar_init(b++, 1);                                         // O full
-            mbar_init(b++, 4);                                         // O free
-            mbar_init(b++, 1);                                         // end
+            for (int s = 0; s < NU; ++s) mbar_init(b++, 1 + L::kSoftmax + L::kWiden); // the issuer's, too
+            mbar_init(b++, 1);                                                        // Q full
+            mbar_init(b++, 1);                                                        // Q empty
+            mbar_init(b++, KV8 ? L::kWiden : 1);                                      // Q as fp16
+            for (int s = 0; s < NS; ++s) mbar_init(b++, KV8 ? L::kWiden : 1);         // tile landed, or widened
+            for (int s = 0; s < NS; ++s) mbar_init(b++, 1);
+            for (int s = 0; s < (NC ? NC : 1); ++s) mbar_init(b++, 1);                // codes landed
+            for (int s = 0; s < (NC ? NC : 1); ++s) mbar_init(b++, KV8 ? L::kWiden : 1); // codes read
+            mbar_init(b++, 1);                                                        // S full
+            mbar_init(b++, L::kSoftmax);                                              // P full
+            mbar_init(b++, 1);                                                        // O full
+            mbar_init(b++, L::kSoftmax);                                              // O free
+            mbar_init(b++, 1);                                                        // end
         }
         *abort_flag = 0;
         fence_mbarrier_init();
@@ -198,9 +202,59 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
         if (lane == 0) mbar_arrive(u_empty + n % NU);
     };
 
+    // ---------------------------------------------------------------- widening (E4M3)
+    // A row of every tile a thread (two, where there are two warps), K and V in turn as they are loaded, and of every bf16 Q tile.
+    auto widen_tiles = [&]() {
+        if constexpr (KV8) {
+            constexpr int kThreads = L::kWiden * 32;
+            const int r = ((warp & 1) + (spare ? 2 : 0)) * 32 + lane;
+            bool ok = true;
+            int nt = 0, nq = 0; // tiles, Q tiles so far
+            auto widen = [&]() -> bool {
+                const int cs = nt % NC, st = nt % NS;
+                bool w = mbar_wait_hint(c_full + cs, (nt / NC) & 1);
+                if (w && nt >= NS) w = mbar_wait_hint(t_empty + st, (nt / NS - 1) & 1);
+                if (!__all_sync(0xffffffffu, w)) return false;
+#pragma unroll 1
+                for (int x = r; x < BN; x += kThreads) widen_codes<D>(codes + cs * L::CODE, ring + st * L::TILE, x);
+                fence_proxy_async_smem(); // the MMAs read the tile through the async proxy
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(c_empty + cs);
+                    mbar_arrive(t_full + st);
+                }
+                ++nt;
+                return true;
+            };
+            for (int n = 0; ok; ++n) {
+                ok = take(n);
+                if (!ok) break;
+                const int tiles = slots[n % NU].n;
+                if (tiles < 0) break;
+                for (int j = 0; j < tiles && ok; ++j) {
+                    ok = widen();
+                    if (SCALE_Q && ok && j == 0) {
+                        ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full, nq & 1));
+                        if (!ok) break;
+#pragma unroll 1
+                        for (int x = r; x < kRows; x += kThreads) q_exp[(nq & 1) * BM + row_off + x] = (int8_t)q_to_f16<D>(q_tile, row_off + x);
+                        ++nq;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(qc_full);
+                    }
+                    ok = ok && widen();
+                }
+                give(n);
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            }
+            if (!ok && lane == 0) fail();
+        }
+    };
+
     if constexpr (KV8) { // 128 x (80 + 2 x 176 + 80) = 512 x 128 registers
         if (warp < 4 || warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    } else {
+    } else { // 128 x (104 + 2 x 200) <= 384 x 168
         if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     }
     if (warp == 0 || warp == 2) {
@@ -217,7 +271,7 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
         const bool direct = a.plan == nullptr;
         const int total = direct ? a.rect : a.plan[0] * a.hkv;
         int at = blockIdx.x + pipe * gridDim.x; // direct: the next place to look at
-        int nk = 0, nv = 0, nc = 0, nq = 0;     // loads so far: K, V (codes: both), Q
+        int nt = 0, nq = 0;                     // tiles (or their codes) and Q tiles loaded so far
         bool ok = true;
         auto publish = [&](int n) {
             if (n >= NU && !__all_sync(0xffffffffu, mbar_wait_hint(u_empty + n % NU, (n / NU - 1) & 1))) {
@@ -263,38 +317,16 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
                 return lane < nbt && (lb << a.lg_bs) < kend ? trow[lb + (lb >= from ? skip : 0)] : -1;
             };
             auto load = [&](bool isV, int j, int b) {
-                uint64_t *full, *empty;
-                uint8_t *stage;
-                int round;
-                if constexpr (KV8) {
-                    const int st = nc % NC;
-                    round = nc / NC;
-                    ++nc;
-                    full = c_full + st;
-                    empty = c_empty + st;
-                    stage = codes + st * L::CODE;
-                } else if (isV) {
-                    round = nv++;
-                    full = v_full;
-                    empty = v_empty;
-                    stage = v_tile;
-                } else {
-                    const int st = nk % KN;
-                    round = nk / KN;
-                    ++nk;
-                    full = k_full + st;
-                    empty = k_empty + st;
-                    stage = k_ring + st * L::TILE;
-                }
+                constexpr int N = KV8 ? NC : NS;
+                const int st = nt % N, round = nt / N;
+                uint64_t *const full = (KV8 ? c_full : t_full) + st, *const empty = (KV8 ? c_empty : t_empty) + st;
+                uint8_t *const stage = KV8 ? codes + st * L::CODE : ring + st * L::TILE;
                 if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait_hint(empty, (round - 1) & 1));
                 if (!ok || __any_sync(0xffffffffu, *abort_flag != 0)) {
-                    // (not issued: nothing to wait for at the end)
-                    if constexpr (KV8) --nc;
-                    else if (isV) --nv;
-                    else --nk;
                     ok = false;
                     return;
                 }
+                ++nt;
                 const int kbase = k0 + j * BN, lb = (kbase >> a.lg_bs) + lane;
                 const bool has = lane < nbt && (lb << a.lg_bs) < kend;
                 const bool good = has && b >= 0 && b < a.num_blocks;
@@ -347,25 +379,23 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
                 __syncwarp();
                 ++nq;
             };
-            // K of tile j, then V of tile j - (KN - 1); Q behind the first K tile; the next unit published behind the second
-            // round of loads (the ones in flight hide the reads that it takes)
-            int e_k = tiles > 0 ? entry(0) : -1, e_v = e_k;
-            const int rounds = tiles > 0 ? tiles + KN - 1 : 0;
+            // K and V of tile j; Q behind the first K tile; the next unit published behind the second tile (the loads in flight
+            // hide the reads that it takes)
+            int e = tiles > 0 ? entry(0) : -1;
             for (int j = 0; ok; ++j) {
-                if (j == min(rounds, 2)) {
+                if (j == min(tiles, 2)) {
                     publish(n + 1);
                     if (!ok) break;
                 }
-                if (j >= rounds) {
+                if (j >= tiles) {
                     if (j >= 2) break;
                     continue;
                 }
                 const int e_next = j + 1 < tiles ? entry(j + 1) : -1;
-                if (j < tiles) load(false, j, e_k);
+                load(false, j, e);
                 if (j == 0 && ok) load_q();
-                if (ok && j >= KN - 1) load(true, j - (KN - 1), KN == 2 ? e_v : e_k);
-                e_v = e_k;
-                e_k = e_next;
+                if (ok) load(true, j, e);
+                e = e_next;
             }
             if (!ok || __any_sync(0xffffffffu, *abort_flag != 0)) {
                 if (!ok && lane == 0) fail();
@@ -374,13 +404,9 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
         }
         // the last loads must land before this CTA's shared memory goes away
         if (lane == 0) {
+            constexpr int N = KV8 ? NC : NS;
             bool w = true;
-            if constexpr (KV8) {
-                for (int c = max(nc - NC, 0); c < nc; ++c) w = w && mbar_wait_hint(c_full + c % NC, (c / NC) & 1);
-            } else {
-                for (int c = max(nk - KN, 0); c < nk; ++c) w = w && mbar_wait_hint(k_full + c % KN, (c / KN) & 1);
-                if (nv > 0) w = w && mbar_wait_hint(v_full, (nv - 1) & 1);
-            }
+            for (int c = max(nt - N, 0); c < nt; ++c) w = w && mbar_wait_hint((KV8 ? c_full : t_full) + c % N, (c / N) & 1);
             if (nq > 0) w = w && mbar_wait_hint(q_full, (nq - 1) & 1);
             if (!w) set_error(a.err, PKV_DEVERR_TIMEOUT);
         }
@@ -391,68 +417,71 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
         constexpr uint32_t IQK = tc::idesc_f16(OT == PKV_BF16 ? 1u : 0u, 0u, BM, BN);
         constexpr uint32_t IPV = tc::idesc_f16(OT == PKV_BF16 ? 1u : 0u, 1u, BM, D);
         const uint64_t dQ = tc::smem_desc(smem_u32(q_tile), 16, 1024);
-        const uint64_t dK = tc::smem_desc(smem_u32(k_ring), 16, GROUPED ? 2048 : 1024);
-        const uint64_t dV = GROUPED ? tc::smem_desc(smem_u32(v_tile), 1024, 2048) : tc::smem_desc(smem_u32(v_tile), BN * 128, 1024);
+        const uint64_t dK = tc::smem_desc(smem_u32(ring), 16, GROUPED ? 2048 : 1024);
+        const uint64_t dV = GROUPED ? tc::smem_desc(smem_u32(ring), 1024, 2048) : tc::smem_desc(smem_u32(ring), BN * 128, 1024);
         constexpr int kHalf = GROUPED ? 1024 : BN * 128, kKeys16 = GROUPED ? 4096 : 2048;
         const uint32_t tS = tmem + (uint32_t)(pipe * BN), tO = tmem + (uint32_t)(2 * BN + pipe * D);
         uint64_t *const q_ready = SCALE_Q ? qc_full : q_full;
         bool any_mma = false, ok = true;
-        int nk = 0, nv = 0, nq = 0, no = 0, np = 0; // phases so far
+        int nt = 0, nq = 0, no = 0, np = 0; // tiles before the unit's; Q tiles, O tiles, P tiles so far
         for (int n = 0; ok; ++n) {
             ok = take(n);
             if (!ok) break;
             const int tiles = slots[n % NU].n;
             if (tiles < 0) break;
-            auto wait_k = [&]() { return mbar_wait(k_full + nk % KN, (nk / KN) & 1); };
-            auto issue_s = [&](bool last) {
-                const int st = nk % KN;
+            // K(j) is tile nt + 2 j of the ring, V(j) the next one
+            auto landed = [&](int c) { return mbar_wait(t_full + c % NS, (c / NS) & 1); };
+            auto issue_s = [&](int j) {
+                const int st = (nt + 2 * j) % NS;
                 const uint64_t b0 = dK + (uint64_t)((st * L::TILE) >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     tc::mma_f16_warp(tS, dQ + (uint64_t)(((k >> 2) * BM * 128 + (k & 3) * 32) >> 4),
                                      b0 + (uint64_t)(((k >> 2) * kHalf + (k & 3) * 32) >> 4), IQK, k > 0 ? 1u : 0u);
                 tc::commit_warp(s_full);
-                tc::commit_warp(k_empty + st);
-                if (last) tc::commit_warp(q_empty);
-                ++nk;
+                tc::commit_warp(t_empty + st);
+                if (j + 1 == tiles) tc::commit_warp(q_empty);
             };
             if (tiles > 0) {
-                ok = __all_sync(0xffffffffu, wait_k() && mbar_wait(q_ready, nq & 1));
+                ok = __all_sync(0xffffffffu, landed(nt) && mbar_wait(q_ready, nq & 1));
                 ++nq;
                 if (!ok) break;
                 tc::fence_after_sync();
                 any_mma = true;
-                issue_s(tiles == 1);
+                issue_s(0);
             }
             for (int j = 0; j < tiles && ok; ++j) {
                 const bool more = j + 1 < tiles;
-                bool w = (KN == 1 || !more || wait_k()) && mbar_wait(v_full, nv & 1) && mbar_wait(p_full, np & 1);
+                // (three stages: the next K tile is normally in place already, and S(j + 1) goes out right behind P V(j); two: its
+                // stage may still be this S's)
+                bool w = (NS == 2 || !more || landed(nt + 2 * j + 2)) && landed(nt + 2 * j + 1) && mbar_wait(p_full, np & 1);
                 if (j == 0 && no > 0) w = w && mbar_wait(o_free, (no - 1) & 1); // the unit before has been read out of O
                 ok = __all_sync(0xffffffffu, w);
                 if (!ok) break;
                 ++np;
-                ++nv;
                 tc::fence_after_sync();
+                const int st = (nt + 2 * j + 1) % NS;
+                const uint64_t b0 = dV + (uint64_t)((st * L::TILE) >> 4);
 #pragma unroll
                 for (int part = 0; part < NP; ++part)
 #pragma unroll
                     for (int k = 0; k < BN / 16; ++k)
-                        tc::mma_f16_ts_warp(tO, tS + (uint32_t)(part * (BN / 2) + k * 8), dV + (uint64_t)((k * kKeys16) >> 4), IPV,
+                        tc::mma_f16_ts_warp(tO, tS + (uint32_t)(part * (BN / 2) + k * 8), b0 + (uint64_t)((k * kKeys16) >> 4), IPV,
                                             (j > 0 || k > 0 || part > 0) ? 1u : 0u);
-                tc::commit_warp(v_empty);
+                tc::commit_warp(t_empty + st);
                 if (!more) {
                     tc::commit_warp(o_full);
                     ++no;
                 } else {
-                    // (one K stage: its next tile may only now have landed)
-                    if (KN == 1) {
-                        ok = __all_sync(0xffffffffu, wait_k());
+                    if (NS == 2) {
+                        ok = __all_sync(0xffffffffu, landed(nt + 2 * j + 2));
                         if (!ok) break;
                         tc::fence_after_sync();
                     }
-                    issue_s(j + 2 == tiles);
+                    issue_s(j + 1);
                 }
             }
+            nt += 2 * tiles;
             give(n);
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         }
@@ -463,59 +492,16 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
             if (!__all_sync(0xffffffffu, mbar_wait_hint(fin, 0)) && lane == 0) set_error(a.err, PKV_DEVERR_TIMEOUT);
         }
     } else if (warp >= 12) {
-        // ---------------------------------------------------------------- widening (E4M3)
-        // 64 threads, rows r and r + 64 of every tile, K and V in turn as they are loaded, and every bf16 Q tile.
-        if constexpr (KV8) {
-            const int r = (warp & 1) * 32 + lane;
-            bool ok = true;
-            int nc = 0, nt = 0, nq = 0; // code stages, tiles (K and V each), Q tiles so far
-            auto widen = [&](uint8_t *tile, uint64_t *free, uint64_t *done) -> bool {
-                const int st = nc % NC;
-                bool w = mbar_wait_hint(c_full + st, (nc / NC) & 1);
-                ++nc;
-                if (w && nt > 0) w = mbar_wait_hint(free, (nt - 1) & 1);
-                if (!__all_sync(0xffffffffu, w)) return false;
-                widen_codes<D>(codes + st * L::CODE, tile, r);
-                widen_codes<D>(codes + st * L::CODE, tile, r + 64);
-                fence_proxy_async_smem(); // the MMAs read the tile through the async proxy
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(c_empty + st);
-                    mbar_arrive(done);
-                }
-                return true;
-            };
-            for (int n = 0; ok; ++n) {
-                ok = take(n);
-                if (!ok) break;
-                const int tiles = slots[n % NU].n;
-                if (tiles < 0) break;
-                for (int j = 0; j < tiles && ok; ++j) {
-                    ok = widen(k_ring, k_empty, k_full);
-                    if (SCALE_Q && ok && j == 0) {
-                        ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full, nq & 1));
-                        if (!ok) break;
-#pragma unroll 1
-                        for (int x = r; x < kRows; x += 64) q_exp[(nq & 1) * BM + row_off + x] = (int8_t)q_to_f16<D>(q_tile, row_off + x);
-                        ++nq;
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(qc_full);
-                    }
-                    ok = ok && widen(v_tile, v_empty, v_full);
-                    ++nt;
-                }
-                give(n);
-                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-            }
-            if (!ok && lane == 0) fail();
-        }
+        widen_tiles();
     } else {
-        // ---------------------------------------------------------------- softmax, one thread per row
         if constexpr (KV8)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ---------------------------------------------------------------- softmax, one thread per row
+        if (spare) { // (registers go to a warpgroup's warps alike, hence only here)
+            widen_tiles();
+        } else {
         const int tile_row = (warp & 3) * 32 + lane, r = tile_row - row_off; // row of the tile = tensor-memory lane; of the unit
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + (uint32_t)(pipe * BN), tO = tmem + lane_off + (uint32_t)(2 * BN + pipe * D);
@@ -677,6 +663,7 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         }
         if (!ok && lane == 0) fail();
+        }
     }
 
     tc::fence_before_sync();

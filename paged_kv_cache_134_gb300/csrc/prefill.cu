@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
     }
 }
 
-// The work list of a chunk call: every (sequence, row tile or pair of them, split), heaviest first as above.  A warp takes a
-// sequence, its lanes the row tiles (long chunks have hundreds).
+// The work list of a chunk call: every (sequence, row tile or pair of them, split), heaviest first as above.  As many
+// lanes take a sequence as it can have row tiles (or pairs), up to a warp.
 template <bool STREAM>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Args a) {
     extern __shared__ int sh[];
@@ -113,12 +113,13 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const Args a) 
     pdl_wait();
     for (int x = threadIdx.x; x < R; x += kPlanThreads) hist[x] = cnt[x] = 0;
     __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wide = a.max_groups >= 32 ? 32 : a.max_groups <= 1 ? 1 : 2 << (31 - __clz(a.max_groups - 1)); // lanes of a sequence
+    const int lane = threadIdx.x & (wide - 1);
     int4 *list = reinterpret_cast<int4 *>(a.plan + 4);
     auto visit = [&](bool report, auto &&entry) {
-        for (int i = warp; i < a.num_seqs; i += kPlanThreads / 32) {
+        for (int i = threadIdx.x / wide; i < a.num_seqs; i += kPlanThreads / wide) {
             const int n = chunk_groups<!STREAM>(a, i, report && lane == 0);
-            for (int g = lane; g < n; g += 32) {
+            for (int g = lane; g < n; g += wide) {
                 // (splits are of equal size but for the last one)
                 const int parts = STREAM ? max(1, stream_unit(a, i, g, 0, 0).nsplit) : chunk_parts(chunk_item(a, i, g, 0, 0));
                 for (int k = 0; k < parts; ++k) {
@@ -658,8 +659,8 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     if (int r = pkv_stream_workspace(c, st, s.floats(c, p.total_tokens, hq), &ws)) return r;
     const bool direct = s.direct(c, p.num_seqs);
     a.plan = direct ? nullptr : reinterpret_cast<int *>(ws.p);
+    a.max_groups = s.max_groups;
     if (direct) {
-        a.max_groups = s.max_groups;
         a.max_parts = s.max_splits;
         a.rect = (int)s.rect(c, p.num_seqs);
     }
