@@ -113,7 +113,7 @@ PKV_DEV int4 direct_unit(const Args &a, int &at, int stride) {
     for (; at < a.rect; at += stride) {
         const int h = at % a.hkv, r = at / a.hkv, part = r % a.max_parts, g = r / a.max_parts % a.max_groups;
         const int seq = r / a.max_parts / a.max_groups;
-        if (g >= chunk_groups<true>(a, seq, h == 0 && part == 0 && g == 0)) continue;
+        if (g >= chunk_groups<false>(a, seq, h == 0 && part == 0 && g == 0)) continue;
         if (part > 0 && part >= stream_unit(a, seq, g, 0, 0).nsplit) continue;
         at += stride;
         return make_int4(seq, g, part, h);

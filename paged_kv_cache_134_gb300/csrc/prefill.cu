@@ -159,6 +159,10 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const Args a) {
     const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5);
     const int tok = blockIdx.x;
     if (h >= a.hq) return;
+    const int64_t base = ((int64_t)tok * a.hq + h) * a.max_splits;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + base;
+    // (read while the row's sequence is looked for; what lies behind its splits is left aside below)
+    const float2 early = lane < a.max_splits ? ml[lane] : make_float2(0.f, 0.f);
     // the sequence of the token: the last one that starts at or before it (the whole warp searches)
     int lo = 0, hi = a.num_seqs;
     while (hi - lo > 1) {
@@ -175,11 +179,9 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const Args a) {
     const int tile = (tok - st) / (BM >> a.lg_group);
     const int n = STREAM ? stream_unit(a, lo, tile, 0, 0).nsplit : chunk_splits(chunk_item(a, lo, tile / 2, 0, 0), tile & 1);
     if (n <= 1) return;
-    const int64_t base = ((int64_t)tok * a.hq + h) * a.max_splits;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + base;
     float top = -INFINITY;
     for (int j = lane; j < n; j += 32) {
-        const float2 v = ml[j];
+        const float2 v = j < 32 ? early : ml[j];
         if (v.y != 0.f) top = fmaxf(top, v.x);
     }
 #pragma unroll
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const Args a) {
     float num[PER], den = 0.f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) num[e] = 0.f;
-    constexpr int U = 4; // splits whose loads go out together
+    constexpr int U = 8; // splits whose loads go out together
     for (int j0 = 0; j0 < n; j0 += U) {
         float2 w[U];
         float v[U][PER];
@@ -556,8 +558,12 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
     ChunkShape s;
     const int G = hq / c->num_kv_heads, bs = c->block_size;
     const int per = BM / G; // tokens of a row tile
-    // one row tile: units by themselves, two at a time on an SM (chunk_stream.cuh); more: tiles in pairs that share their keys
-    s.stream = max_seqlen <= per;
+    // One row tile a sequence: units by themselves, two at a time on an SM (chunk_stream.cuh).  More: tiles in pairs that share
+    // their keys (prefill_impl.cuh), unless a sequence has two on average, so that most pairs would be half empty (64
+    // sequences of 1 to 347 new tokens under a window, 2497 in all, G = 4: 137 us by themselves, 158 in pairs; 4 of 100 tokens
+    // 164 and 123; one of 512 1185 and 1069).  Over E4M3 caches a pair's codes are widened once for both (512 tokens: 514
+    // and 301).
+    s.stream = max_seqlen <= per || (c->kv_dtype != PKV_FP8_E4M3 && tokens * G <= 2 * BM * (int64_t)num_seqs);
     const int group = s.stream ? per : 2 * per;
     s.groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + group - 1) / group), tokens / group + num_seqs);
     int64_t keys = (int64_t)max_blocks * bs;
@@ -650,7 +656,8 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     Maps m;
     const int G = hq / c->num_kv_heads, tile = s.stream && p.max_seqlen * G <= 64 ? 64 : BM;
     if (!make_group_map(&m.q, p.q, mt, p.total_tokens, hq, D, G, tile) ||
-        !make_group_map(&m.out, p.out, mt, p.total_tokens, hq, D, G) || !(D == 128 && c->kv_dtype != PKV_FP8_E4M3 ? pkv_tmap_rows128_grouped(&m.pool, c->pool, mt, pool_rows, c->block_size)
+        (!s.stream && !make_group_map(&m.out, p.out, mt, p.total_tokens, hq, D, G)) || // (TMA stores of whole tiles)
+        !(D == 128 && c->kv_dtype != PKV_FP8_E4M3 ? pkv_tmap_rows128_grouped(&m.pool, c->pool, mt, pool_rows, c->block_size)
                                                   : pool_map(&m.pool, c)))
         return pkv_fail(PKV_ECUDA, "tensor map");
     m.k = m.v = m.pool;

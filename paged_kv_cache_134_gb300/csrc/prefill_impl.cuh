@@ -213,7 +213,7 @@ constexpr int threads_of() {
 template <int D>
 PKV_DEV void widen_codes(const uint8_t *codes, uint8_t *tile, int r) {
     constexpr int NC = D / 16;
-#pragma unroll 2
+#pragma unroll 1 // (unrolled by four 8 % slower: the roles' code together outgrows the instruction cache)
     for (int i = 0; i < NC; ++i) {
         const int c = (i + r) & (NC - 1);
         const uint4 w = *reinterpret_cast<const uint4 *>(codes + r * D + c * 16);
