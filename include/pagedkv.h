@@ -114,9 +114,9 @@ int kv_cache_reserve_chunk(pkv_cache_t cache, int max_seqs, int64_t max_tokens, 
                            int max_blocks_per_seq);
 
 /* Synchronise the device and free the workspaces that paged_decode_attention_mass, paged_decode_attention_window,
- * paged_chunk_attention and the decode of PKV_INT4 caches keep for streams, whether reserved or grown on demand; with graphs != 0 also those of
- * captures, whose graphs must not be launched again.  Later calls allocate anew.  Not to be called while a
- * stream is being captured. */
+ * paged_chunk_attention and the decode of PKV_INT4 caches keep for streams, whether reserved or grown on demand;
+ * with graphs != 0 also those of captures, whose graphs must not be launched again.  Later calls allocate anew.
+ * Not to be called while a stream is being captured. */
 int kv_cache_release_workspaces(pkv_cache_t cache, int graphs);
 
 /* Synchronise the device, return the device error word's bits in *device_code and clear
@@ -231,8 +231,8 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
  * (t >= L_s - window) and the first `sinks` (t < sinks), window >= 1, sinks >= 0; blocks that hold none of them
  * are not read, and their table entries may be -1.  A window that reaches the sinks, or the first token, is
  * paged_decode_attention to its tolerance.  Lengths above the tables' tokens are cut to them and set PKV_DEVERR_LENGTH.
- * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4).  Split boundaries depend on L_s, window, sinks, num_seqs
- * and max_blocks_per_seq.  Workspace: as for paged_decode_attention_mass, one per stream and per capture. */
+ * Every cache type.  Split boundaries depend on L_s, window, sinks, num_seqs and max_blocks_per_seq.  Workspace: as
+ * for paged_decode_attention_mass, one per stream and per capture. */
 int paged_decode_attention_window(const void *q, pkv_cache_t cache, const int32_t *block_tables,
                                   int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_q_heads,
                                   float scale, int window, int sinks, void *out, void *stream);

@@ -229,8 +229,9 @@ class KVCache:
                                             int(max_q_heads), int(max_blocks_per_seq)))
 
     def release_workspaces(self, graphs: bool = False):
-        """Synchronise and free the workspaces that the mass decode and the decode of 4-bit caches keep for streams; with
-        ``graphs`` also those of stream captures, whose graphs must not be replayed again."""
+        """Synchronise and free the workspaces that the mass and windowed decodes, the chunk attention and the
+        decode of 4-bit caches keep for streams; with ``graphs`` also those of stream captures, whose graphs must not be
+        replayed again."""
         _check(lib().kv_cache_release_workspaces(self.handle, int(graphs)))
 
     def check_error(self) -> int:

@@ -18,7 +18,7 @@ LIB = os.path.join(LIBDIR, "libpagedkv.so")
 
 SOURCES = ["api.cu", "append.cu", "rotary.cu", "decode.cu", "decode_f16.cu", "decode_bf16.cu", "decode_fp8_f16.cu",
            "decode_fp8_bf16.cu", "decode_tc.cu", "decode_tc_window.cu", "decode_window_f16.cu",
-           "decode_window_bf16.cu", "decode_window_fp8_f16.cu", "decode_window_fp8_bf16.cu", "decode_mma.cu", "decode_mma_int4.cu",
+           "decode_window_bf16.cu", "decode_mma_int4_window.cu", "decode_mma_fp8_window.cu", "decode_mma.cu", "decode_mma_int4.cu",
            "decode_mma_int4_mass.cu", "decode_mma_fp8_mass.cu", "decode_mma_16bit_mass.cu",
            "decode_short.cu", "decode_short_fp8.cu", "decode_short_int4.cu", "evict.cu",
            "prefill.cu", "prefill_packed.cu", "prefill_paged.cu",

@@ -648,11 +648,16 @@ int paged_decode_attention_window(const void *q, pkv_cache_t c, const int32_t *b
     if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
     if (num_seqs < 0 || max_blocks_per_seq < 0) return pkv_fail(PKV_EINVAL, "negative size");
     if (window < 1 || sinks < 0) return pkv_fail(PKV_EINVAL, "window %d and sinks %d: window >= 1, sinks >= 0", window, sinks);
-    if (c->kv_dtype == PKV_INT4) return pkv_fail(PKV_EUNSUPPORTED, "the windowed decode does not read 4-bit caches");
     if (num_seqs == 0) return PKV_OK;
     if (int r = check_decode(c, q, block_tables, max_blocks_per_seq, context_lens, num_q_heads, scale, out)) return r;
     if (int r = check_device(c)) return r;
     const int G = num_q_heads / c->num_kv_heads;
+    sinks = std::min(sinks, 1 << 30); // (a block's rounding stays within 32 bits)
+    if (c->kv_dtype == PKV_INT4 || c->kv_dtype == PKV_FP8_E4M3) {
+        MmaDecodeLaunch d{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale,
+                          nullptr, -1, 1.f, window, sinks};
+        return decode_mma_entry(c, d, nullptr, static_cast<cudaStream_t>(stream));
+    }
     const int per_launch = std::min(num_seqs, decode_seqs_per_launch(c, G, true));
     DecodeLaunch d;
     d.q = q;
@@ -664,7 +669,7 @@ int paged_decode_attention_window(const void *q, pkv_cache_t c, const int32_t *b
     d.num_q_heads = num_q_heads;
     d.scale = scale;
     d.window = window;
-    d.sinks = std::min(sinks, 1 << 30); // (a block's rounding stays within 32 bits)
+    d.sinks = sinks;
     const int64_t seen = window_seen_blocks(c, max_blocks_per_seq, window, d.sinks);
     d.split_blocks = window_split_blocks(c, G, per_launch, seen);
     d.max_splits = (int)((seen + d.split_blocks - 1) / d.split_blocks);

@@ -21,11 +21,8 @@ using OccFn = int (*)(int, int, size_t);
 
 void pick(const pkv_cache *c, bool window, DecodeFn *fn, OccFn *occ) {
     if (window) {
-        const bool f8 = c->kv_dtype == PKV_FP8_E4M3, h = c->model_dtype == PKV_F16;
-        *fn = f8 ? (h ? pkv_decode_window_fp8_f16 : pkv_decode_window_fp8_bf16)
-                 : (h ? pkv_decode_window_f16 : pkv_decode_window_bf16);
-        *occ = f8 ? (h ? pkv_decode_window_occupancy_fp8_f16 : pkv_decode_window_occupancy_fp8_bf16)
-                  : (h ? pkv_decode_window_occupancy_f16 : pkv_decode_window_occupancy_bf16);
+        *fn = c->kv_dtype == PKV_F16 ? pkv_decode_window_f16 : pkv_decode_window_bf16;
+        *occ = c->kv_dtype == PKV_F16 ? pkv_decode_window_occupancy_f16 : pkv_decode_window_occupancy_bf16;
         return;
     }
     if (c->kv_dtype == PKV_F16) {

@@ -72,20 +72,6 @@ struct Args {
     int window = 0, sinks = 0;
 };
 
-// What a sequence of L tokens shows to a query at its end under a window with sinks: the blocks that hold a visible token,
-// taken one after the other ("seen" order: the sinks' blocks, then the window's), as if the sequence were
-// `len` tokens long.  Seen block i is logical block i, or i + skip from block `from` on.  Of the seen tokens only
-// [lo, hi) are not visible: the rest of the sinks' last block and what lies before the window in its first.
-// Every seen block holds a visible token.
-struct Reach {
-    int len, from, skip, lo, hi;
-};
-PKV_DEV Reach reach_of(int L, int window, int sinks, int bs) {
-    const int first = L - window; // (L >= 0, window >= 1)
-    if (first <= sinks) return {L, 0, 0, 0, 0};
-    const int from = (sinks + bs - 1) / bs, skip = max(first / bs - from, 0);
-    return {L - skip * bs, from, skip, sinks, first - skip * bs};
-}
 // a length cut to what the table's row can name
 PKV_DEV int length_in(const Args &a, int s) {
     const int64_t most = (int64_t)a.max_blocks * a.bs;
@@ -846,14 +832,8 @@ int pkv_decode_occupancy_f16(int D, int G, size_t smem);
 int pkv_decode_occupancy_bf16(int D, int G, size_t smem);
 int pkv_decode_occupancy_fp8_f16(int D, int G, size_t smem);
 int pkv_decode_occupancy_fp8_bf16(int D, int G, size_t smem);
-// the same with a sliding window and sinks (decode_window_*.cu)
+// 16-bit caches with a sliding window and sinks (decode_window_*.cu); E4M3 and 4-bit caches: decode_mma.cu
 cudaError_t pkv_decode_window_f16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t, bool merge);
 cudaError_t pkv_decode_window_bf16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t, bool merge);
-cudaError_t pkv_decode_window_fp8_f16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t,
-                                      bool merge);
-cudaError_t pkv_decode_window_fp8_bf16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t,
-                                       bool merge);
 int pkv_decode_window_occupancy_f16(int D, int G, size_t smem);
 int pkv_decode_window_occupancy_bf16(int D, int G, size_t smem);
-int pkv_decode_window_occupancy_fp8_f16(int D, int G, size_t smem);
-int pkv_decode_window_occupancy_fp8_bf16(int D, int G, size_t smem);

@@ -77,7 +77,7 @@ PKV_DEV int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; } 
 PKV_DEV float power_of_two(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + e) << 23); } // e < 128
 
 // GC: 1 query head per KV head, 4 (two or four), 8
-template <int D, int MT, int GC, bool MASS>
+template <int D, int MT, int GC, bool MASS, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kernel(const Args a) {
     using G_ = Geo4<D, GC>;
     constexpr int KS = D / 16;             // k steps of the first product = m tiles of the second
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
     __shared__ Join J;
     __shared__ int sm_tmp[2 * kWarps];
     __shared__ uint64_t sm_bars[kWarps * ST];
-    __shared__ Unit sm_unit[2];
+    __shared__ UnitOf<WIN> sm_unit[2];
     __shared__ float sm_Q[2][8], sm_SQ[2][8]; // per column: the score's scale, sum(q) times it
     __shared__ int sm_bad[2];
     float *oacc = reinterpret_cast<float *>(smem + kWarps * ST * G_::kBytes); // [warp][COLS][LD]
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
     fence_mbarrier_init();
     const uint64_t policy = l2_policy_evict_first();
     pdl_wait();
-    list_units(a, full, part, sm_tmp);
+    list_units<WIN>(a, full, part, sm_tmp);
     const int nfull = full[a.num_seqs] * a.hkv, nunits = nfull + part[a.num_seqs] * a.hkv;
     if ((int)blockIdx.x >= nunits) return;
 
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
     };
     // One warp's work for a unit of buffer `par`: find it and start its copies ...
     auto fetch = [&](int ui, int par) {
-        const Unit v = unit_of(a, full, part, nfull, ui);
+        const UnitOf<WIN> v = unit_of<WIN>(a, full, part, nfull, ui);
         if (lane == 0) sm_unit[par] = v;
         stage_unit<D>(a, v, tb + par * tb_len, qraw, lane, 32);
         cp_commit();
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
         prepare(0);
     }
     __syncthreads();
-    Unit u = sm_unit[0];
+    UnitOf<WIN> u = sm_unit[0];
     int *table = tb;
     bool bad = sm_bad[0] != 0;
     int turn = 1; // the warp that prepares the next unit
@@ -325,6 +325,18 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
                         for (int k = 0; k < NC; ++k) x[r][k] = -INFINITY;
                         vs[r] = vz[r] = 0.f;
                     }
+            }
+            if constexpr (WIN) { // tokens out of sight among those in it
+                const int lo = u.lo - u.t0 - t0, hi = u.hi - u.t0 - t0;
+                if (lo < T && hi > 0 && lo < hi) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (g + 8 * r >= lo && g + 8 * r < hi) {
+#pragma unroll
+                            for (int k = 0; k < NC; ++k) x[r][k] = -INFINITY;
+                            vs[r] = vz[r] = 0.f;
+                        }
+                }
             }
             if constexpr (MASS) {
                 float *dst = a.ws_x + (((int64_t)u.s * a.hkv + u.kvh) * a.cap + u.t0 + t0 + g) * G;
@@ -544,11 +556,11 @@ __global__ void __launch_bounds__(kThreads, Geo4<D, GC>::kCtas) decode_int4_kern
     pdl_trigger();
 }
 
-template <int D, int MT, int GC, bool MASS>
+template <int D, int MT, int GC, bool MASS, bool WIN>
 cudaError_t launch_int4_t(const Args &a, int sms, cudaStream_t st) {
     using G_ = Geo4<D, GC>;
     static std::atomic<bool> have[64];
-    auto kern = decode_int4_kernel<D, MT, GC, MASS>;
+    auto kern = decode_int4_kernel<D, MT, GC, MASS, WIN>;
     const size_t smem = (size_t)kWarps * G_::kStages * G_::kBytes + kWarps * GC * (D + 4) * sizeof(float) +
                         2 * (D / 32) * 32 * 16 + GC * D * 2 + (3 * (a.num_seqs + 1) + 2 * (a.split_tokens >> a.bs_log2)) * sizeof(int);
     cudaError_t e = pkv_allow_smem(reinterpret_cast<const void *>(kern), have);
@@ -556,12 +568,12 @@ cudaError_t launch_int4_t(const Args &a, int sms, cudaStream_t st) {
     return pdl_launch(kern, dim3(grid_of(a, sms * ctas_of(G_::kCtas, smem))), dim3(kThreads), smem, st, a);
 }
 
-template <int MT, bool MASS>
+template <int MT, bool MASS, bool WIN = false>
 cudaError_t dispatch_int4(const Args &a, int D, int sms, bool merge, cudaStream_t st) {
-    if (merge) return D == 64 ? launch_merge_t<64, MT, MASS>(a, sms, st) : launch_merge_t<128, MT, MASS>(a, sms, st);
+    if (merge) return D == 64 ? launch_merge_t<64, MT, MASS, WIN>(a, sms, st) : launch_merge_t<128, MT, MASS, WIN>(a, sms, st);
 #define PKV_INT4_CASE(DD, GC)                                                                                          \
     if (D == DD && (GC == 4 ? a.group == 2 || a.group == 4 : a.group == GC))                                           \
-        return launch_int4_t<DD, MT, GC, MASS>(a, sms, st);
+        return launch_int4_t<DD, MT, GC, MASS, WIN>(a, sms, st);
     PKV_INT4_CASE(64, 1)
     PKV_INT4_CASE(64, 4)
     PKV_INT4_CASE(64, 8)

@@ -28,7 +28,8 @@ struct Plan {
     bool is_short;  // a warp a row
 };
 
-bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len, Plan *p) {
+// (window: max_blocks are those that a window shows)
+bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len, bool window, Plan *p) {
     const bool mass = mass_len >= 0;
     p->cap = (int64_t)max_blocks * c->block_size;
     if (mass) p->cap = std::min(p->cap, mass_len);
@@ -40,7 +41,7 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     // warp's work), more rows than CTAs.  4-bit, D = 128: 8 rows of four heads and 16 tokens, 5.4 us with mass
     // (units: 8.0), 5.7 without (5.1); 256 rows of eight heads and 32 tokens, 15.7 us with mass (9.4); many rows see
     // decode_short.cuh.
-    p->is_short = p->cap <= pkv_mma::kShortTokens &&
+    p->is_short = !window && p->cap <= pkv_mma::kShortTokens &&
                   (int)mass + (hq / c->num_kv_heads <= 4) + (rows > workers) >= 2;
     if (p->is_short) {
         p->split = p->max_splits = 1;
@@ -105,6 +106,8 @@ __global__ void clear_kernel(int *done, int n) {
 
 cudaError_t run(const pkv_cache *c, const pkv_mma::Args &a, bool mass, bool merge, cudaStream_t st) {
     const int mt = c->model_dtype, D = c->head_dim, sms = c->num_sms;
+    if (a.window > 0)
+        return c->kv_dtype == PKV_INT4 ? pkv_mma_int4_window(a, mt, D, sms, merge, st) : pkv_mma_fp8_window(a, mt, D, sms, merge, st);
     if (!mass) return pkv_mma_int4(a, mt, D, sms, merge, st);
     if (c->kv_dtype == PKV_INT4) return pkv_mma_int4_mass(a, mt, D, sms, merge, st);
     if (c->kv_dtype == PKV_FP8_E4M3) return pkv_mma_fp8_mass(a, mt, D, sms, merge, st);
@@ -131,7 +134,8 @@ int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, in
 
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st) {
     Plan p;
-    if (!plan_for(c, d.num_seqs, d.num_q_heads, d.max_blocks, d.mass_len, &p))
+    const int seen = d.window > 0 ? (int)window_seen_blocks(c, d.max_blocks, d.window, d.sinks) : d.max_blocks;
+    if (!plan_for(c, d.num_seqs, d.num_q_heads, seen, d.mass_len, d.window > 0, &p))
         return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this decode takes", d.max_blocks);
     // a batch larger than one launch takes runs in consecutive launches that share the workspace: each
     // waits for the one before it.  Another host thread's call on this stream may use the same workspace, or replace
@@ -161,7 +165,9 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace 
     if (a.blk_stride > 0xFFFFFFFFll)
         return pkv_fail(PKV_EUNSUPPORTED, "blocks of %lld bytes are larger than this decode takes", (long long)a.blk_stride);
     a.mass_len = d.mass_len;
-    a.cap = p.cap;
+    a.cap = d.window > 0 ? (int64_t)d.max_blocks * c->block_size : p.cap;
+    a.window = d.window;
+    a.sinks = d.sinks;
     a.max_blocks = d.max_blocks;
     a.hq = d.num_q_heads;
     a.hkv = c->num_kv_heads;

@@ -52,7 +52,11 @@ PKV_DEV int place_v(int r, int c) {
     return p * R + ((c ^ (p & 2)) << 4);
 }
 
-template <int D, int KV, int MT, bool G8>
+// MASS false, WIN: without the mass, under a sliding window with sinks (see Reach); a row's splits are joined as in
+// decode_int4.cuh.  Bound by the bytes of the cache where a window is long; 256 log-normal sequences over E4M3, 32/8
+// heads, D = 128: a window of 1024 73 us (305 MB, 4.2 TB/s), 511 and a sink 47 (95 by the tensor-core kernel of the
+// plain decode, whose units of 128 tokens at least leave a window's edges empty), 256 36 (83); D = 64, 511: 34 (94).
+template <int D, int KV, int MT, bool G8, bool MASS = true, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kernel(const Args a) {
     using G_ = Geo<D, KV, G8>;
     using M = ModelT<MT>;
@@ -75,11 +79,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
     const int G = a.group, bl = a.bs_log2, bs = 1 << bl;
     const uint32_t ring_u = smem_u32(smem + warp * ST * G_::kBytes);
     pdl_wait();
-    list_units(a, full, part, sm_tmp);
+    list_units<WIN>(a, full, part, sm_tmp);
     const int nfull = full[a.num_seqs] * a.hkv, nunits = nfull + part[a.num_seqs] * a.hkv;
     if ((int)blockIdx.x >= nunits) return;
 
-    Unit u = unit_of(a, full, part, nfull, blockIdx.x);
+    UnitOf<WIN> u = unit_of<WIN>(a, full, part, nfull, blockIdx.x);
     int par = 0; // which of the two buffers is this unit's
     int *tb = tbuf;
     stage_unit<D>(a, u, tb, qbuf, threadIdx.x, kThreads);
@@ -109,7 +113,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
         for (int i = 0; i < kTile * G_::kChunks / 32; ++i) {
             const int c = i * 32 + lane, r = c / G_::kChunks, p = c % G_::kChunks, o = r >> 3;
             const char *src = (o ? base[1] : base[0]) + ((o ? off[1] : off[0]) + (r & 7)) * G_::kRow + p * 16;
-            const int sz = (r & 7) < (o ? lim[1] : lim[0]) ? 16 : 0;
+            int sz = (r & 7) < (o ? lim[1] : lim[0]) ? 16 : 0;
+            if constexpr (WIN) // (out of sight: zeros, as V is multiplied by the weight 0 there)
+                if (u.t0 + t0 + r >= u.lo && u.t0 + t0 + r < u.hi) sz = 0;
             cp16(dst + place_k<D, KV>(r, p), src, sz);
             cp16(dst + G_::kV + place_v<D, KV>(r, p), src + a.v_off, sz);
         }
@@ -128,13 +134,17 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
     };
     start();
 
+    Unit prev = u;        // the last unit, if it still has to be counted (without mass)
+    bool pending = false;
     for (int ui = blockIdx.x;;) {
+        int before = 0;
+        if (!MASS && pending && threadIdx.x == 0) before = count_unit(a, prev);
         const int un = ui + gridDim.x;
         const bool more = un < nunits;
-        Unit next = u;
+        UnitOf<WIN> next = u;
         int *next_tb = tbuf + (par ^ 1) * tb_len;
         if (more) { // its needs ride in this unit's first group: they have landed with the last tile
-            next = unit_of(a, full, part, nfull, un);
+            next = unit_of<WIN>(a, full, part, nfull, un);
             stage_unit<D>(a, next, next_tb, qbuf + (par ^ 1) * COLS * D * 2, threadIdx.x, kThreads);
         }
         const int n = u.n, s = u.s, kvh = u.kvh;
@@ -246,7 +256,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
                 if (g >= left || (bad && tb[(t0 + g) >> bl] < 0)) x[0] = x[1] = -INFINITY;
                 if (g + 8 >= left || (bad && tb[(t0 + g + 8) >> bl] < 0)) x[2] = x[3] = -INFINITY;
             }
-            {
+            if constexpr (WIN) { // tokens out of sight among those in it
+                const int lo = u.lo - u.t0 - t0, hi = u.hi - u.t0 - t0;
+                if (g >= lo && g < hi) x[0] = x[1] = -INFINITY;
+                if (g + 8 >= lo && g + 8 < hi) x[2] = x[3] = -INFINITY;
+            }
+            if constexpr (MASS) {
                 float *dst = a.ws_x + (((int64_t)s * a.hkv + kvh) * a.cap + u.t0 + t0 + g) * G;
                 if (G == 1) {
                     if (t4 == 0) {
@@ -353,11 +368,18 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
             J.m[warp][2 * t4 + 1] = m1 - kUp;
         }
         const Unit cur = u;
+        if (!MASS && threadIdx.x == 0) J.last = pending && before == prev.nsplit - 1;
         bad = __syncthreads_or(more && check_table(a, next, next_tb, threadIdx.x, kThreads)); // (each its own copies)
         u = next;
         tb = next_tb;
         par ^= 1;
         if (more) start();
+        if constexpr (!MASS) {
+            if (J.last) {
+                __threadfence();
+                join_row<D, MT>(a, prev, J);
+            }
+        }
         {
             const Weight w0 = warp_weight(J, warp, 2 * t4), w1 = warp_weight(J, warp, 2 * t4 + 1);
             l0 = row_sum(l0);
@@ -389,18 +411,30 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
                 }
             }
         }
-        join_unit<D, COLS, MT, true, false>(a, cur, J, oacc);
+        join_unit<D, COLS, MT, MASS, false>(a, cur, J, oacc);
+        prev = cur;
+        pending = !MASS && cur.nsplit > 1 && a.done;
         if (!more) break;
         ui = un;
+    }
+    if constexpr (!MASS) {
+        if (pending) {
+            if (threadIdx.x == 0) J.last = count_unit(a, prev) == prev.nsplit - 1;
+            __syncthreads();
+            if (J.last) {
+                __threadfence();
+                join_row<D, MT>(a, prev, J);
+            }
+        }
     }
     pdl_trigger();
 }
 
-template <int D, int KV, int MT, bool G8>
+template <int D, int KV, int MT, bool G8, bool MASS, bool WIN>
 cudaError_t launch_mass_t(const Args &a, int sms, cudaStream_t st) {
     using G_ = Geo<D, KV, G8>;
     static std::atomic<bool> have[64];
-    auto kern = decode_mass_kernel<D, KV, MT, G8>;
+    auto kern = decode_mass_kernel<D, KV, MT, G8, MASS, WIN>;
     constexpr int cols = G8 ? 8 : 4;
     const size_t smem = (size_t)kWarps * G_::kStages * G_::kBytes + kWarps * cols * (D + 4) * sizeof(float) +
                         2 * cols * D * 2 + (3 * (a.num_seqs + 1) + 2 * (a.split_tokens >> a.bs_log2)) * sizeof(int);
@@ -410,12 +444,14 @@ cudaError_t launch_mass_t(const Args &a, int sms, cudaStream_t st) {
 }
 
 // one cache type's kernels (one translation unit each)
-template <int KV, int MT>
+template <int KV, int MT, bool MASS = true, bool WIN = false>
 cudaError_t dispatch_mass(const Args &a, int D, int sms, bool merge, cudaStream_t st) {
-    if (merge) return D == 64 ? launch_merge_t<64, MT, true>(a, sms, st) : launch_merge_t<128, MT, true>(a, sms, st);
+    if (merge) return D == 64 ? launch_merge_t<64, MT, MASS, WIN>(a, sms, st) : launch_merge_t<128, MT, MASS, WIN>(a, sms, st);
     if (D == 64)
-        return a.group == 8 ? launch_mass_t<64, KV, MT, true>(a, sms, st) : launch_mass_t<64, KV, MT, false>(a, sms, st);
-    return a.group == 8 ? launch_mass_t<128, KV, MT, true>(a, sms, st) : launch_mass_t<128, KV, MT, false>(a, sms, st);
+        return a.group == 8 ? launch_mass_t<64, KV, MT, true, MASS, WIN>(a, sms, st)
+                            : launch_mass_t<64, KV, MT, false, MASS, WIN>(a, sms, st);
+    return a.group == 8 ? launch_mass_t<128, KV, MT, true, MASS, WIN>(a, sms, st)
+                        : launch_mass_t<128, KV, MT, false, MASS, WIN>(a, sms, st);
 }
 
 } // namespace pkv_mma

@@ -6,7 +6,7 @@
 
 // with a sliding window and sinks (decode_tc_window.cu)
 cudaError_t pkv_decode_tc_window(const CUtensorMap &tkv, const CUtensorMap &tq, const pkv_decode::Args &a, int G, int mt,
-                                 bool f8, int grid, size_t smem, cudaStream_t st);
+                                 int grid, size_t smem, cudaStream_t st);
 
 namespace {
 
@@ -49,7 +49,7 @@ cudaError_t pkv_decode_tc_launch(const pkv_cache *c, const pkv_decode::Args &a, 
         return cudaErrorInvalidValue;
     const size_t smem = smem_bytes(operand_dtype(c), f8, a.num_seqs, a.window > 0);
     const int grid = c->num_sms;
-    if (a.window > 0) return pkv_decode_tc_window(tkv, tq, a, G, mt, f8, grid, smem, st);
+    if (a.window > 0) return pkv_decode_tc_window(tkv, tq, a, G, mt, grid, smem, st);
 #define PKV_TC_CASE(GG)                                                                                                \
     if (G == GG) {                                                                                                     \
         if (f8)                                                                                                        \

@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
     const int bps = a.split_blocks;
     pkv_decode::build_unit_list<WIN>(a, pf, pp, nb, warp, lane, ln);
     // what the sequence shows (without a window: all of it)
-    auto reach = [&](int s) -> pkv_decode::Reach {
-        if constexpr (WIN) return pkv_decode::reach_of(ln[s], a.window, a.sinks, a.bs);
+    auto reach = [&](int s) -> Reach {
+        if constexpr (WIN) return reach_of(ln[s], a.window, a.sinks, a.bs);
         return {};
     };
     auto length = [&](int s) -> int {
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
         constexpr int kER = 4;
         int ecur[kER], enx[kER];
         auto load_entries = [&](const Unit &x, int (&e)[kER]) {
-            pkv_decode::Reach rc{};
+            Reach rc{};
             if constexpr (WIN) rc = reach(x.s);
 #pragma unroll
             for (int k = 0; k < kER; ++k) {
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
             if (idx >= kER * 32 && idx < x.ntiles) {
                 int at = x.blk0 + idx;
                 if constexpr (WIN) {
-                    const pkv_decode::Reach rc = reach(x.s);
+                    const Reach rc = reach(x.s);
                     if (at >= rc.from) at += rc.skip;
                 }
                 v = a.tables[(int64_t)x.s * a.max_blocks + at];
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
         auto blk_read = [&](const Unit &x, int i) -> int {
             int idx = x.blk0 + i * bpstep + jb;
             if constexpr (WIN) {
-                const pkv_decode::Reach rc = reach(x.s);
+                const Reach rc = reach(x.s);
                 if (idx >= rc.from) idx += rc.skip;
             }
             idx = min(idx, a.max_blocks - 1);
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
             int tok_end2 = 0;
             float ksc2 = 1.f;
             const int tok0 = un.blk0 * a.bs;
-            pkv_decode::Reach rc{};
+            Reach rc{};
             if constexpr (WIN) rc = reach(un.s);
             // scores in log2 units: scale * log2(e), times the K scale of the head and the power of two
             // taken out of q by the converters (FP8 caches)

@@ -1,14 +1,11 @@
-// Instantiations of the tensor-core decode (decode_tc.cuh) with a sliding window and sinks.
+// Instantiations of the tensor-core decode (decode_tc.cuh) with a sliding window and sinks, 16-bit caches.
 #include "decode_tc.cuh"
 
 cudaError_t pkv_decode_tc_window(const CUtensorMap &tkv, const CUtensorMap &tq, const pkv_decode::Args &a, int G, int mt,
-                                 bool f8, int grid, size_t smem, cudaStream_t st) {
+                                 int grid, size_t smem, cudaStream_t st) {
     using namespace pkv_decode_tc;
 #define PKV_TC_CASE(GG)                                                                                                \
     if (G == GG) {                                                                                                     \
-        if (f8)                                                                                                        \
-            return mt == PKV_BF16 ? launch<GG, PKV_BF16, PKV_FP8_E4M3, true>(tkv, tq, a, grid, smem, st)               \
-                                  : launch<GG, PKV_F16, PKV_FP8_E4M3, true>(tkv, tq, a, grid, smem, st);               \
         return mt == PKV_BF16 ? launch<GG, PKV_BF16, PKV_BF16, true>(tkv, tq, a, grid, smem, st)                       \
                               : launch<GG, PKV_F16, PKV_F16, true>(tkv, tq, a, grid, smem, st);                        \
     }

@@ -43,6 +43,20 @@ PKV_DEV int64_t slot_of(const int32_t *__restrict__ tables, int rows, int max_bl
     return b < 0 ? -1 : (int64_t)b * bs + p % bs;
 }
 
+// What a sequence of L tokens shows to a query at its end under a window with sinks: the blocks that hold a visible token,
+// taken one after the other ("seen" order: the sinks' blocks, then the window's), as if the sequence were
+// `len` tokens long.  Seen block i is logical block i, or i + skip from block `from` on.  Of the seen tokens only
+// [lo, hi) are not visible: the rest of the sinks' last block and what lies before the window in its first.
+// Every seen block holds a visible token.
+struct Reach {
+    int len, from, skip, lo, hi;
+};
+PKV_DEV Reach reach_of(int L, int window, int sinks, int bs) {
+    const int first = L - window; // (L >= 0, window >= 1)
+    if (first <= sinks) return {L, 0, 0, 0, 0};
+    const int from = (sinks + bs - 1) / bs, skip = max(first / bs - from, 0);
+    return {L - skip * bs, from, skip, sinks, first - skip * bs};
+}
 // ------------------------------------------------------------------ mbarrier
 
 PKV_DEV void mbar_init(uint64_t *bar, uint32_t count) {

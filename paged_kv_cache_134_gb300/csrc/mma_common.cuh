@@ -13,6 +13,8 @@
 // 65 us more on 32 fp16 sequences of up to 4096 tokens, 32 heads.)
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "int4.cuh"
 #include "pkv_internal.h"
@@ -45,6 +47,7 @@ struct Args {
     int hkv_shift;
     float qk_scale_log2; // scale * log2(e)
     float decay;
+    int window, sinks; // WIN kernels: what is attended to (see Reach)
 };
 
 // (the offset rides in the instruction: no address to compute)
@@ -149,7 +152,8 @@ PKV_DEV int row_len(const Args &a, int s) {
 
 // Block scan of the sequences' unit counts: full[s + 1], part[s + 1] hold the inclusive sums of whole
 // splits and of partial ones (a sequence of length 0 has one partial unit, which writes its zero row); the lengths lie
-// behind part.
+// behind part.  WIN: units of what is in sight (see Reach).
+template <bool WIN = false>
 PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
     const int S = a.num_seqs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *len = part + S + 1;
@@ -162,8 +166,9 @@ PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
             const int L = row_len(a, s);
             if (blockIdx.x == 0 && (int64_t)a.lens[s] > a.cap) set_error(a.err, PKV_DEVERR_LENGTH);
             len[s] = L;
-            f = L / a.split_tokens;
-            p = (L % a.split_tokens != 0 || L == 0) ? 1 : 0;
+            const int n = WIN ? reach_of(L, a.window, a.sinks, 1 << a.bs_log2).len : L;
+            f = n / a.split_tokens;
+            p = (n % a.split_tokens != 0 || n == 0) ? 1 : 0;
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -197,16 +202,33 @@ struct Unit {
     int t0, n; // first token, tokens
 };
 
+// WIN: t0 counts the tokens in sight; block i of them is logical block i, or i + skip from block `from` on, and [lo, hi) are
+// hidden.
+struct SeenUnit : Unit {
+    int from, skip, lo, hi;
+};
+template <bool WIN>
+using UnitOf = std::conditional_t<WIN, SeenUnit, Unit>;
+
 // Unit u of the list (all lanes of a warp together, u the same for all).
-PKV_DEV Unit unit_of(const Args &a, const int *full, const int *part, int nfull, int u) {
-    Unit r;
+template <bool WIN = false>
+PKV_DEV UnitOf<WIN> unit_of(const Args &a, const int *full, const int *part, int nfull, int u) {
+    UnitOf<WIN> r;
     const bool whole = u < nfull;
     const int v = whole ? u : u - nfull;
     const int k = (int)(((uint64_t)(uint32_t)v * a.hkv_magic) >> a.hkv_shift); // v / hkv
     r.kvh = v - k * a.hkv;
     r.s = find_row(whole ? full : part, a.num_seqs, k);
     r.j = whole ? k - full[r.s] : full[r.s + 1] - full[r.s];
-    const int L = part[a.num_seqs + 1 + r.s];
+    int L = part[a.num_seqs + 1 + r.s];
+    if constexpr (WIN) {
+        const Reach rc = reach_of(L, a.window, a.sinks, 1 << a.bs_log2);
+        L = rc.len;
+        r.from = rc.from;
+        r.skip = rc.skip;
+        r.lo = rc.lo;
+        r.hi = rc.hi;
+    }
     r.nsplit = (full[r.s + 1] - full[r.s]) + (part[r.s + 1] - part[r.s]);
     r.t0 = r.j * a.split_tokens;
     r.n = min(L - r.t0, a.split_tokens);
@@ -246,11 +268,15 @@ PKV_DEV void cp_wait() {
 }
 
 // issue only: the caller commits and waits
-template <int D>
-PKV_DEV void stage_unit(const Args &a, const Unit &u, int *tb, char *qs, int i0, int step) {
+template <int D, typename U>
+PKV_DEV void stage_unit(const Args &a, const U &u, int *tb, char *qs, int i0, int step) {
     const int nblk = blocks_of(a, u);
     const int32_t *row = a.tables + (int64_t)u.s * a.max_blocks + (u.t0 >> a.bs_log2);
-    for (int i = i0; i < nblk; i += step) cp4(smem_u32(tb + i), row + i);
+    for (int i = i0; i < nblk; i += step) {
+        int at = i;
+        if constexpr (std::is_same_v<U, SeenUnit>) at += (u.t0 >> a.bs_log2) + i >= u.from ? u.skip : 0;
+        cp4(smem_u32(tb + i), row + at);
+    }
     const char *q = static_cast<const char *>(a.q) + ((int64_t)u.s * a.hq + u.kvh * a.group) * (D * 2);
     for (int i = i0; i < a.group * (D / 8); i += step) cp16(smem_u32(qs) + i * 16, q + i * 16, 16);
 }
@@ -395,7 +421,7 @@ PKV_DEV float row_sum(float x) {
 constexpr int kMergeWarps = 16;
 constexpr int kMassCtas = 8;
 
-template <int D, int MT>
+template <int D, int MT, bool WIN = false>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
     using M = ModelT<MT>;
     __shared__ float sm_M[8], sm_inv[8], sum[kMergeWarps][32];
@@ -403,7 +429,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const int row = blockIdx.x, s = row / a.hkv, kvh = row - s * a.hkv;
-    const int nsplit = (row_len(a, s) + a.split_tokens - 1) / a.split_tokens;
+    const int n = WIN ? reach_of(row_len(a, s), a.window, a.sinks, 1 << a.bs_log2).len : row_len(a, s);
+    const int nsplit = (n + a.split_tokens - 1) / a.split_tokens;
     if (nsplit <= 1) return;
     split_weights(a, s, kvh, nsplit, wj, a.max_splits, sm_M, sm_inv);
     __syncthreads();
@@ -568,14 +595,14 @@ inline unsigned grid_of(const Args &a, int slots) {
 }
 
 // the launch after the decode: merge_kernel, or mass_kernel
-template <int D, int MT, bool MASS>
+template <int D, int MT, bool MASS, bool WIN = false>
 cudaError_t launch_merge_t(const Args &a, int sms, cudaStream_t st) {
     const size_t smem = (size_t)a.group * a.max_splits * sizeof(float);
     if constexpr (MASS) {
         return pdl_launch(mass_kernel<D, MT>, dim3(grid_of(a, kMassCtas * sms)), dim3(kThreads),
                           smem + 3 * (a.num_seqs + 1) * sizeof(int), st, a);
     } else {
-        return pdl_launch(merge_kernel<D, MT>, dim3((unsigned)(a.num_seqs * a.hkv), a.group * D / 32),
+        return pdl_launch(merge_kernel<D, MT, WIN>, dim3((unsigned)(a.num_seqs * a.hkv), a.group * D / 32),
                           dim3(kMergeWarps * 32),
                           smem, st, a);
     }
@@ -584,6 +611,8 @@ cudaError_t launch_merge_t(const Args &a, int sms, cudaStream_t st) {
 } // namespace pkv_mma
 
 cudaError_t pkv_mma_int4(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_mma_int4_window(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_mma_fp8_window(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_int4_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_fp8_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_16bit_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);

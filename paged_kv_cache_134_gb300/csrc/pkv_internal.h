@@ -155,7 +155,7 @@ inline void pkv_row_strides(const pkv_cache *c, int64_t *block, int64_t *head, i
     }
 }
 
-// decode of 4-bit caches, and decode with attention mass of every cache (decode_mma.cu)
+// decode of 4-bit caches, decode with attention mass of every cache, windowed decode of E4M3 caches (decode_mma.cu)
 struct MmaDecodeLaunch {
     const void *q;
     void *out;
@@ -165,6 +165,7 @@ struct MmaDecodeLaunch {
     float *mass;
     int64_t mass_len; // -1: no mass
     float decay;
+    int window = 0, sinks = 0; // window > 0 (4-bit and E4M3 caches): the last `window` tokens and the first `sinks`
 };
 struct PkvWorkspace {
     float *p = nullptr;

@@ -4,6 +4,7 @@ The pool is filled with NaN first, so that a read of a slot that no token owns s
 import numpy as np
 import torch
 
+import compress_ref
 import paged_kv_cache_134_gb300 as P
 
 MODEL = {"f16": torch.float16, "bf16": torch.bfloat16}
@@ -33,13 +34,19 @@ class Setup:
         self.cache.view()[0].fill_(255)
         if kv == "fp8":
             s = [(x.float().abs().amax(dim=(0, 2)) / 448).clamp(min=1e-6) if n else torch.ones(hkv) for x in (k, v)]
-            self.cache.set_scales(s[0].cuda(), s[1].cuda())
+            self.scales = tuple(x.cuda() for x in s)
+            self.cache.set_scales(*self.scales)
             codes = [(x.float() / f[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn) for x, f in zip((k, v), s)]
             self.k64, self.v64 = ((c.double() * f[:, None].double()).numpy() for c, f in zip(codes, s))
         else:
             self.k64, self.v64 = k.double().numpy(), v.double().numpy()
+        if kv == "int4" and n:
+            rows = [compress_ref.quantise4(x, model) for x in (self.k64, self.v64)]
+            self.k64, self.v64 = (compress_ref.values4(*r) for r in rows)
+            self.steps = tuple(float(r[1].max()) for r in rows)
+        self.given = k.cuda(), v.cuda()
         if n:
-            P.paged_kv_append(self.cache, k.cuda(), v.cuda(), self.slots)
+            P.paged_kv_append(self.cache, *self.given, self.slots)
         self.at = np.concatenate([[0], np.cumsum(self.lens)])
         self.gen = g
 
@@ -57,6 +64,10 @@ class Setup:
         if not len(positions):
             return
         slots = self.slots[self.at[i] + torch.as_tensor(np.asarray(positions)).long().cuda()]
+        if self.kv == "int4":  # steps and offsets NaN
+            row = torch.full((len(slots), self.hkv, self.d), float("nan"), dtype=MODEL[self.model], device="cuda")
+            P.paged_kv_append(self.cache, row, row, slots)
+            return
         if self.kv == "fp8":
             pool = self.cache.view()[0].view(self.nb, 2, self.hkv, self.bs, self.d)
             pool[slots // self.bs, :, :, slots % self.bs] = 0x7F

@@ -271,15 +271,15 @@ def test_a_conversation_as_it_runs(kv, model, norm):
                                       k_weight=w)
         assert torch.equal(qr, q_all[at:e])
         lens = torch.tensor([e], dtype=torch.int32).cuda()
-        p, terms = "pair" if kv == "bf16" else "f16", False
+        p = "pair" if kv == "bf16" else "f16"
         if n == 1:
             out = P.paged_decode_attention_window(qr, cache, tables, lens, s, window, sinks=sinks)
-            p, terms = "pair" if kv == "bf16" else "f16", kv == "fp8"
+            p = {"bf16": "pair", "f16": "f16", "fp8": "f32"}[kv]
         else:
             cu = torch.tensor([0, n], dtype=torch.int32).cuda()
             out = P.paged_chunk_attention(qr, cache, tables, lens, cu, n, s, window=window, sinks=sinks)
         ref = R.attend(qr.double().cpu().numpy(), k64[:e], v64[:e], s, positions(e, n), window, sinks)
-        R.check(out.double().cpu().numpy(), ref, model, p, terms)
+        R.check(out.double().cpu().numpy(), ref, model, p)
         at = e
     assert at == total and cache.check_error() == 0
 
