@@ -17,14 +17,14 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libpagedkv.so")
 
 SOURCES = ["api.cu", "append.cu", "rotary.cu", "decode.cu", "decode_f16.cu", "decode_bf16.cu", "decode_fp8_f16.cu",
-           "decode_fp8_bf16.cu", "decode_tc.cu", "decode_tc_window.cu", "decode_window_f16.cu",
-           "decode_window_bf16.cu", "decode_mma_int4_window.cu", "decode_mma_fp8_window.cu", "decode_mma.cu", "decode_mma_int4.cu",
+           "decode_fp8_bf16.cu", "decode_tc.cu", "decode_mma.cu", "decode_mma_int4.cu",
            "decode_mma_int4_mass.cu", "decode_mma_fp8_mass.cu", "decode_mma_16bit_mass.cu",
+           "decode_mma_int4_window.cu", "decode_mma_fp8_window.cu", "decode_mma_16bit_window.cu",
            "decode_short.cu", "decode_short_fp8.cu", "decode_short_int4.cu", "evict.cu",
            "prefill.cu", "prefill_packed.cu", "prefill_paged.cu",
            "prefill_cascade.cu", "prefill_chunk.cu", "chunk_stream_16bit_few.cu",
-           "chunk_stream_16bit_rows.cu", "chunk_stream_e4m3_few.cu", "chunk_stream_e4m3_rows.cu", "noalloc.cu", "blocks.cu", "selftest.cu",
-           "prefix_cache.cpp"]
+           "chunk_stream_16bit_rows.cu", "chunk_stream_e4m3_few.cu", "chunk_stream_e4m3_rows.cu",
+           "noalloc.cu", "blocks.cu", "selftest.cu", "prefix_cache.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -208,7 +208,7 @@ int pkv_cuda_fail(cudaError_t e, const char *what) {
 
 cudaError_t launch_decode_chunked(pkv_cache *c, DecodeLaunch d, cudaStream_t st) {
     const int G = d.num_q_heads / c->num_kv_heads;
-    const int per = decode_seqs_per_launch(c, G, d.window > 0);
+    const int per = decode_seqs_per_launch(c, G);
     const int total = d.num_seqs;
     const int64_t row_bytes = (int64_t)d.num_q_heads * c->head_dim * 2; // q and out rows, 16-bit model dtype
     const char *q0 = static_cast<const char *>(d.q);
@@ -651,37 +651,10 @@ int paged_decode_attention_window(const void *q, pkv_cache_t c, const int32_t *b
     if (num_seqs == 0) return PKV_OK;
     if (int r = check_decode(c, q, block_tables, max_blocks_per_seq, context_lens, num_q_heads, scale, out)) return r;
     if (int r = check_device(c)) return r;
-    const int G = num_q_heads / c->num_kv_heads;
     sinks = std::min(sinks, 1 << 30); // (a block's rounding stays within 32 bits)
-    if (c->kv_dtype == PKV_INT4 || c->kv_dtype == PKV_FP8_E4M3) {
-        MmaDecodeLaunch d{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale,
-                          nullptr, -1, 1.f, window, sinks};
-        return decode_mma_entry(c, d, nullptr, static_cast<cudaStream_t>(stream));
-    }
-    const int per_launch = std::min(num_seqs, decode_seqs_per_launch(c, G, true));
-    DecodeLaunch d;
-    d.q = q;
-    d.out = out;
-    d.tables = block_tables;
-    d.lens = context_lens;
-    d.max_blocks = max_blocks_per_seq;
-    d.num_seqs = num_seqs;
-    d.num_q_heads = num_q_heads;
-    d.scale = scale;
-    d.window = window;
-    d.sinks = sinks;
-    const int64_t seen = window_seen_blocks(c, max_blocks_per_seq, window, d.sinks);
-    d.split_blocks = window_split_blocks(c, G, per_launch, seen);
-    d.max_splits = (int)((seen + d.split_blocks - 1) / d.split_blocks);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    std::lock_guard<std::mutex> lk(c->ws_mu);
-    PkvWorkspace ws;
-    if (int r = pkv_stream_workspace(c, st, decode_workspace_floats(c, per_launch, num_q_heads, d.max_splits), &ws)) return r;
-    d.ws_o = ws.p;
-    d.ws_ml = nullptr;
-    cudaError_t e = launch_decode_chunked(c, d, st);
-    if (e != cudaSuccess) return pkv_cuda_fail(e, "decode launch");
-    return PKV_OK;
+    MmaDecodeLaunch d{q, out, block_tables, context_lens, max_blocks_per_seq, num_seqs, num_q_heads, scale, nullptr, -1, 1.f,
+                      window, sinks};
+    return decode_mma_entry(c, d, nullptr, static_cast<cudaStream_t>(stream));
 }
 
 int paged_chunk_attention(const void *q, pkv_cache_t c, const int32_t *block_tables, int max_blocks_per_seq,

@@ -1,5 +1,4 @@
 // Host side of the paged decode: split size, stage count, grid, workspace, launches.
-#include <algorithm>
 #include <cstdlib>
 
 #include "decode_impl.cuh"
@@ -19,12 +18,7 @@ int ctas_per_sm() { return env_int("PAGEDKV_DECODE_CTAS", 4); }
 using DecodeFn = cudaError_t (*)(const pkv_decode::Args &, int, int, int, size_t, cudaStream_t, bool);
 using OccFn = int (*)(int, int, size_t);
 
-void pick(const pkv_cache *c, bool window, DecodeFn *fn, OccFn *occ) {
-    if (window) {
-        *fn = c->kv_dtype == PKV_F16 ? pkv_decode_window_f16 : pkv_decode_window_bf16;
-        *occ = c->kv_dtype == PKV_F16 ? pkv_decode_window_occupancy_f16 : pkv_decode_window_occupancy_bf16;
-        return;
-    }
+void pick(const pkv_cache *c, DecodeFn *fn, OccFn *occ) {
     if (c->kv_dtype == PKV_F16) {
         *fn = pkv_decode_f16;
         *occ = pkv_decode_occupancy_f16;
@@ -65,47 +59,14 @@ int cascade_suffix_split_blocks(const pkv_cache *c) {
     return b > 0 ? b : 1;
 }
 
-int decode_seqs_per_launch(const pkv_cache *c, int G, bool window) {
+int decode_seqs_per_launch(const pkv_cache *c, int G) {
     // Both decode kernels keep a per-sequence unit table (3 ints a sequence) in shared memory: the
     // CUDA-core kernel takes up to kMaxSeqs sequences a launch; the tensor-core kernel, whose stage
     // rings fill nearly all of shared memory, fewer (the largest multiple of 64 that still fits).
     int n = pkv_decode::kMaxSeqs;
-    if (pkv_decode_tc_eligible(c, G, 64, window))
-        while (n > 64 && !pkv_decode_tc_eligible(c, G, n, window)) n -= 64;
+    if (pkv_decode_tc_eligible(c, G, 64))
+        while (n > 64 && !pkv_decode_tc_eligible(c, G, n)) n -= 64;
     return n;
-}
-
-int64_t window_seen_blocks(const pkv_cache *c, int max_blocks, int window, int sinks) {
-    const int64_t bs = c->block_size, w = ((int64_t)window - 1 + bs - 1) / bs + 1, s = ((int64_t)sinks + bs - 1) / bs;
-    return std::min<int64_t>(max_blocks, w + s);
-}
-
-int window_split_blocks(const pkv_cache *c, int G, int num_seqs, int64_t seen_blocks) {
-    const int bs = c->block_size;
-    if (!pkv_decode_tc_eligible(c, G, num_seqs, true)) {
-        // about the splits of the plain decode, of equal size (a last one of a block or two would be a unit like any other);
-        // nothing is cut that is not longer than two of them, as a short call's second launch costs more than it saves
-        const int64_t per = std::max(1, 256 / bs);
-        const int64_t k = seen_blocks <= 2 * per ? 1 : (seen_blocks + per / 2) / per;
-        return (int)std::max<int64_t>(1, (seen_blocks + k - 1) / k);
-    }
-    // Under a window most sequences show the same number of blocks, so that units of work come in equal sizes and rounds
-    // over the SMs show: of the splits of whole steps of 128 tokens, the one whose rounds take the fewest steps, a unit's own
-    // cost counted as 0.7 of a step and the merge's launch as two.  (Four sequences under 8192 + 64 tokens, 32/8 heads: 16
-    // splits of 17 blocks, 4 rounds of 5 steps, 36.2 us; 4 splits, one round of 17 steps, 30.7 us.)
-    const int64_t step = 128 / bs, steps = std::max<int64_t>(1, (seen_blocks + step - 1) / step);
-    const int64_t rows = (int64_t)num_seqs * c->num_kv_heads;
-    int64_t best = steps;
-    double least = 1e300;
-    for (int64_t k = 1; k <= std::min<int64_t>(steps, 128); ++k) {
-        const int64_t s = (steps + k - 1) / k, units = rows * ((steps + s - 1) / s);
-        const double cost = (double)((units + c->num_sms - 1) / c->num_sms) * ((double)s + 0.7) + (k > 1 ? 2.0 : 0.0);
-        if (cost < least) {
-            least = cost;
-            best = s;
-        }
-    }
-    return (int)std::max<int64_t>(1, std::min(best * step, seen_blocks));
 }
 
 int64_t decode_workspace_floats(const pkv_cache *c, int num_seqs, int num_q_heads, int max_splits) {
@@ -153,14 +114,12 @@ cudaError_t launch_decode(pkv_cache *c, const DecodeLaunch &d, cudaStream_t st) 
     a.qk_scale_log2 = d.scale * 1.4426950408889634f;
     a.start_block = d.start_block;
     a.slot0 = d.slot0;
-    a.window = d.window;
-    a.sinks = d.sinks;
 
     DecodeFn fn;
     OccFn occ;
-    pick(c, d.window > 0, &fn, &occ);
+    pick(c, &fn, &occ);
     cudaError_t e;
-    if (pkv_decode_tc_eligible(c, G, d.num_seqs, d.window > 0)) {
+    if (pkv_decode_tc_eligible(c, G, d.num_seqs)) {
         a.nstages = 0;
         // longer splits than the CUDA-core kernel's: a unit then spans several 128-token MMA steps,
         // which spreads the per-unit work (Q load, epilogue, partial write) over more bytes; the
@@ -170,13 +129,13 @@ cudaError_t launch_decode(pkv_cache *c, const DecodeLaunch &d, cudaStream_t st) 
         // ~5 % faster than 512-token ones for E4M3 and ~4 % slower for bf16)
         const int tc_default = c->kv_dtype == PKV_FP8_E4M3 ? 1024 : 512;
         const int tc_blocks = env_int("PAGEDKV_SPLIT_TOKENS_TC", tc_default) / c->block_size;
-        if (tc_blocks > a.split_blocks && d.window == 0) a.split_blocks = tc_blocks;
+        if (tc_blocks > a.split_blocks) a.split_blocks = tc_blocks;
         {
             PkvTimer timer(c, PKV_KIND_DECODE, st);
             e = pkv_decode_tc_launch(c, a, d.q, G, st);
             g_pkv_launches++;
         }
-        if (e != cudaSuccess || (d.window > 0 && d.max_splits <= 1)) return e;
+        if (e != cudaSuccess) return e;
         if ((e = launch_prefix_between(c, d, st)) != cudaSuccess) return e;
         PkvTimer timer(c, PKV_KIND_MERGE, st);
         e = fn(a, c->head_dim, G, 0, 0, st, true);
@@ -210,8 +169,7 @@ cudaError_t launch_decode(pkv_cache *c, const DecodeLaunch &d, cudaStream_t st) 
         e = fn(a, c->head_dim, G, grid, smem, st, false);
         g_pkv_launches++;
     }
-    // (a window that needs no split needs no merge: its kernels write the rows without tokens, too)
-    if (e != cudaSuccess || (d.window > 0 && d.max_splits <= 1)) return e;
+    if (e != cudaSuccess) return e;
     if ((e = launch_prefix_between(c, d, st)) != cudaSuccess) return e;
     {
         PkvTimer timer(c, PKV_KIND_MERGE, st);

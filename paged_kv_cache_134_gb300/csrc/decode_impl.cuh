@@ -68,15 +68,7 @@ struct Args {
     // attention another kernel computed into workspace slots [0, slot0); this kernel then covers the
     // blocks from start_block on and writes its splits from slot slot0 on (both 0 otherwise)
     int start_block = 0, slot0 = 0;
-    // sliding window (WIN kernels): the last `window` tokens and the first `sinks` ones are attended to
-    int window = 0, sinks = 0;
 };
-
-// a length cut to what the table's row can name
-PKV_DEV int length_in(const Args &a, int s) {
-    const int64_t most = (int64_t)a.max_blocks * a.bs;
-    return (int)max((int64_t)0, min((int64_t)a.lens[s], most));
-}
 
 template <int KVT>
 PKV_DEV void load8(const char *p, float *f) {
@@ -152,12 +144,10 @@ PKV_DEV void loadN(const char *p, float *f) {
 }
 
 // One tile of `bs` tokens, `valid` of them real, for this lane's query head.
-// WIN: tokens [lo, hi) of the tile are not attended to.
-template <int D, int G, int KVT, bool WIN>
+template <int D, int G, int KVT>
 PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
                           const float (&qf)[Lanes<D, G>::DL], float &m, float &l, float (&acc)[Lanes<D, G>::DL],
-                          int lane, int lo, int hi) {
-    auto live = [&](int t) { return t < valid && !(WIN && t >= lo && t < hi); };
+                          int lane) {
     using LY = Lanes<D, G>;
     constexpr int DL = LY::DL, LH = LY::LH, LT = LY::LT, TPP = LY::TPP, MAXP = LY::MAXP;
     constexpr int EB = (KVT == PKV_FP8_E4M3) ? 1 : 2;
@@ -166,7 +156,6 @@ PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
     const int npc = ch / TPP;
     for (int c0 = 0; c0 < bs; c0 += ch) {
         if (c0 >= valid) break;
-        if (WIN && c0 >= lo && c0 + ch <= hi) continue;
         float sc[MAXP];
 #pragma unroll
         for (int p = 0; p < MAXP; ++p) {
@@ -189,7 +178,7 @@ PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
                 float v = sc[p];
 #pragma unroll
                 for (int o = LH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                sc[p] = live(c0 + p * TPP + tg) ? v : -INFINITY;
+                sc[p] = (c0 + p * TPP + tg) < valid ? v : -INFINITY;
             }
         }
         float mx = -INFINITY;
@@ -216,7 +205,7 @@ PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
         for (int p = 0; p < MAXP; ++p) {
             if (p < npc) {
                 const int t = c0 + p * TPP + tg;
-                if (live(t)) {
+                if (t < valid) {
                     float vf[DL];
                     loadN<KVT, DL>(vs + (t * D + sub * DL) * EB, vf);
 #pragma unroll
@@ -234,10 +223,9 @@ PKV_DEV void process_tile(const char *ks, const char *vs, int bs, int valid,
 // lanes by a reduce-scatter: after log2 steps every lane holds the full score of one pass, so the
 // softmax of a head costs one exp2 per lane, and each pass's weight is then fetched back by a
 // shuffle from the lane that owns it.
-template <int D, int G, int KVT, bool WIN>
+template <int D, int G, int KVT>
 PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, const float (&qf)[G][8],
-                             float (&m)[G], float (&l)[G], float (&acc)[G][8], int lane, int lo, int hi) {
-    auto live = [&](int t) { return t < valid && !(WIN && t >= lo && t < hi); };
+                             float (&m)[G], float (&l)[G], float (&acc)[G][8], int lane) {
     constexpr int LPT = D / 8;     // lanes per token
     constexpr int TPP = 32 / LPT;  // tokens per pass
     constexpr int MAXP = 16 / TPP; // passes per 16-token chunk (8 for D=128, 4 for D=64)
@@ -254,7 +242,6 @@ PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, 
     const int npc = ch / TPP;
     for (int c0 = 0; c0 < bs; c0 += ch) {
         if (c0 >= valid) break;
-        if (WIN && c0 >= lo && c0 + ch <= hi) continue;
         float part[G][MAXP];
 #pragma unroll
         for (int p = 0; p < MAXP; ++p) {
@@ -293,7 +280,7 @@ PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, 
             float v = part[g][0];
 #pragma unroll
             for (int o = (1 << DUP) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            sc[g] = live(c0 + mypass * TPP + grp) ? v : -INFINITY;
+            sc[g] = (c0 + mypass * TPP + grp) < valid ? v : -INFINITY;
         }
         // online softmax per head; the chunk's scores are spread one per lane
 #pragma unroll
@@ -318,7 +305,7 @@ PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, 
                 float w[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g) w[g] = __shfl_sync(0xffffffffu, sc[g], src);
-                if (live(t)) {
+                if (t < valid) {
                     float vf[8];
                     load8<KVT>(vs + (t * D + sub * 8) * EB, vf);
 #pragma unroll
@@ -334,10 +321,8 @@ PKV_DEV void process_tile_tp(const char *ks, const char *vs, int bs, int valid, 
 // Unit list, built by the whole CTA into shared memory: per sequence its block count nb[s], and
 // prefix counts of full splits (pf) and of partial tail splits (pp, 0 or 1 per sequence), so that
 // unit u resolves to (sequence, KV head, split) with two binary searches (unit_info).  Sequences
-// longer than the table allows are clamped and reported.  WIN: the blocks in sight (see Reach); `ln`, when given,
-// receives the lengths.
-template <bool WIN = false>
-PKV_DEV void build_unit_list(const Args &a, int *pf, int *pp, int *nb, int warp, int lane, int *ln = nullptr) {
+// longer than the table allows are clamped and reported.
+PKV_DEV void build_unit_list(const Args &a, int *pf, int *pp, int *nb, int warp, int lane) {
     const int S = a.num_seqs, bps = a.split_blocks;
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
         const int L = a.lens[s];
@@ -345,11 +330,6 @@ PKV_DEV void build_unit_list(const Args &a, int *pf, int *pp, int *nb, int warp,
         if (n > a.max_blocks) {
             if (blockIdx.x == 0) set_error(a.err, PKV_DEVERR_LENGTH);
             n = a.max_blocks;
-        }
-        if constexpr (WIN) {
-            const int cut = length_in(a, s);
-            if (ln) ln[s] = cut;
-            n = (reach_of(cut, a.window, a.sinks, a.bs).len + a.bs - 1) / a.bs;
         }
         nb[s] = n;
         const int m = n > a.start_block ? n - a.start_block : 0; // blocks this kernel covers
@@ -385,15 +365,6 @@ PKV_DEV void build_unit_list(const Args &a, int *pf, int *pp, int *nb, int warp,
     __syncthreads();
 }
 
-// WIN, no split anywhere (no merge follows): rows of sequences without tokens, by `n` threads of each CTA
-template <typename T, int D>
-PKV_DEV void zero_empty_rows(const Args &a, const int *nb, int i, int n) {
-    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x)
-        if (nb[s] == 0)
-            for (int e = i; e < a.hq * D / 8; e += n)
-                reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + (int64_t)s * a.hq * D)[e] = make_uint4(0u, 0u, 0u, 0u);
-}
-
 // wait (bounded) until a shared-memory counter reaches n or the CTA aborts; false after the limit
 PKV_DEV bool wait_at_least(const int *x, int n, const int *abort_flag) {
     const volatile int *v = x;
@@ -406,7 +377,7 @@ PKV_DEV bool wait_at_least(const int *x, int n, const int *abort_flag) {
     return true;
 }
 
-template <int D, int G, int MT, int KVT, bool WIN = false>
+template <int D, int G, int MT, int KVT>
 __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
     using M = ModelT<MT>;
     using T = typename M::T;
@@ -440,11 +411,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
     // it may launch now and take the SMs this grid's CTAs leave
     if (a.slot0 > 0) pdl_trigger();
     const int bps = a.split_blocks;
-    build_unit_list<WIN>(a, pf, pp, nb, warp, lane);
-    auto reach = [&](int s) -> Reach {
-        if constexpr (WIN) return reach_of(length_in(a, s), a.window, a.sinks, a.bs);
-        return {a.lens[s], 0, 0, 0, 0};
-    };
+    build_unit_list(a, pf, pp, nb, warp, lane);
     const int U = (pf[S] + pp[S]) * a.hkv;
     const int ST = a.sub_tokens, spb = a.bs / a.sub_tokens; // stage tokens, stages per block
 
@@ -455,16 +422,13 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
         bool ok = true;
         for (int u = blockIdx.x; u < U && ok; u += gridDim.x) {
             const Unit un = unit_info(u, pf, pp, nb, S, a.hkv, bps, a.start_block);
-            Reach rc{};
-            if constexpr (WIN) rc = reach(un.s);
             const int32_t *trow = a.tables + (int64_t)un.s * a.max_blocks + un.blk0;
             const char *head_base = a.pool + (int64_t)un.kvh * a.tile_bytes;
             // stages of this unit: spb per block, less the parts wholly past the sequence's end
-            const int nt = spb > 1 ? min(un.ntiles * spb, ((WIN ? rc.len : a.lens[un.s]) - un.blk0 * a.bs + ST - 1) / ST) : un.ntiles;
+            const int nt = spb > 1 ? min(un.ntiles * spb, (a.lens[un.s] - un.blk0 * a.bs + ST - 1) / ST) : un.ntiles;
             for (int i0 = 0; i0 < un.ntiles && ok; i0 += 32) {
                 const int cnt = min(32, un.ntiles - i0);
-                const int at = i0 + lane + (WIN && un.blk0 + i0 + lane >= rc.from ? rc.skip : 0);
-                const int myb = lane < cnt ? trow[at] : 0;
+                const int myb = lane < cnt ? trow[i0 + lane] : 0;
                 for (int i = 0; i < cnt && ok; ++i) {
                     const int b = __shfl_sync(0xffffffffu, myb, i);
                     for (int h = 0, k = (i0 + i) * spb; h < spb && k < nt; ++h, ++k) {
@@ -516,12 +480,9 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
     const int sub = lane % LH, gl = (G == 1) ? 0 : 0, tg = lane / LT;
     uint32_t tau = 0;
     int nu = 0; // this CTA's units so far
-    if constexpr (WIN)
-        if (a.max_splits <= 1) zero_empty_rows<T, D>(a, nb, threadIdx.x, NCW * 32);
     for (int u = blockIdx.x; u < U; u += gridDim.x, ++nu) {
         const Unit un = unit_info(u, pf, pp, nb, S, a.hkv, bps, a.start_block);
-        const Reach rc = reach(un.s);
-        const int L = rc.len;
+        const int L = a.lens[un.s];
         float qs = a.qk_scale_log2;
         if constexpr (KVT == PKV_FP8_E4M3) qs *= a.k_scale[un.kvh];
         float qf[GS][DL];
@@ -559,11 +520,10 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
             if (!flags[stage]) {
                 const char *ks = ring + (size_t)stage * 2 * a.sub_bytes;
                 const int valid = min(ST, L - un.blk0 * a.bs - i * ST);
-                const int lo = rc.lo - un.blk0 * a.bs - i * ST, hi = rc.hi - un.blk0 * a.bs - i * ST;
                 if constexpr (G == 1)
-                    process_tile<D, 1, KVT, WIN>(ks, ks + a.sub_bytes, ST, valid, qf[0], m[0], l[0], acc[0], lane, lo, hi);
+                    process_tile<D, 1, KVT>(ks, ks + a.sub_bytes, ST, valid, qf[0], m[0], l[0], acc[0], lane);
                 else
-                    process_tile_tp<D, G, KVT, WIN>(ks, ks + a.sub_bytes, ST, valid, qf, m, l, acc, lane, lo, hi);
+                    process_tile_tp<D, G, KVT>(ks, ks + a.sub_bytes, ST, valid, qf, m, l, acc, lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[stage]);
@@ -665,7 +625,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const Args a) {
 // max M from all splits' (m, l), then accumulates the splits j = warp, warp + 4, ... (lane = D/32
 // dims, vector loads; the first 16 splits' loads go out with those of the maxima); the four warp
 // sums are added in warp order through shared memory, so the result is deterministic.
-template <int D, int MT, bool WIN = false>
+template <int D, int MT>
 __global__ void __launch_bounds__(128) merge_kernel(const Args a) {
     using M = ModelT<MT>;
     using T = typename M::T;
@@ -678,7 +638,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const Args a) {
     pdl_wait();
     const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = row / a.hq;
-    const int L = WIN ? reach_of(length_in(a, s), a.window, a.sinks, a.bs).len : a.lens[s];
+    const int L = a.lens[s];
     int n = L > 0 ? (L + a.bs - 1) / a.bs : 0;
     if (n > a.max_blocks) n = a.max_blocks;
     if (a.slot0 > 0 && L < a.start_block * a.bs) {
@@ -763,26 +723,26 @@ inline size_t smem_bytes(int D, int G, int nst, int stage_part_bytes, int S) {
            (size_t)(3 * S + 2) * 4;
 }
 
-template <int D, int G, int MT, int KVT, bool WIN>
+template <int D, int G, int MT, int KVT>
 cudaError_t launch_t(const Args &a, int grid, size_t smem, cudaStream_t st) {
-    auto kern = decode_kernel<D, G, MT, KVT, WIN>;
+    auto kern = decode_kernel<D, G, MT, KVT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return pdl_launch(kern, dim3(grid), dim3(kThreads), smem, st, a);
 }
 
-template <int D, int MT, bool WIN>
+template <int D, int MT>
 cudaError_t launch_merge_t(const Args &a, cudaStream_t st) {
     const int rows = a.num_seqs * a.hq;
     if (rows == 0) return cudaSuccess;
-    return pdl_launch(merge_kernel<D, MT, WIN>, dim3(rows), dim3(128), 0, st, a);
+    return pdl_launch(merge_kernel<D, MT>, dim3(rows), dim3(128), 0, st, a);
 }
 
 // Dispatch over head_dim and group size for one (model dtype, KV dtype) pair.
-template <int MT, int KVT, bool WIN = false>
+template <int MT, int KVT>
 cudaError_t dispatch(const Args &a, int D, int G, int grid, size_t smem, cudaStream_t st, bool merge) {
 #define PKV_CASE(DD, GG)                                                                                               \
-    if (D == DD && G == GG) return merge ? launch_merge_t<DD, MT, WIN>(a, st) : launch_t<DD, GG, MT, KVT, WIN>(a, grid, smem, st);
+    if (D == DD && G == GG) return merge ? launch_merge_t<DD, MT>(a, st) : launch_t<DD, GG, MT, KVT>(a, grid, smem, st);
     PKV_CASE(64, 1)
     PKV_CASE(64, 2)
     PKV_CASE(64, 4)
@@ -795,18 +755,18 @@ cudaError_t dispatch(const Args &a, int D, int G, int grid, size_t smem, cudaStr
     return cudaErrorInvalidValue;
 }
 
-template <int D, int G, int MT, int KVT, bool WIN>
+template <int D, int G, int MT, int KVT>
 int occupancy(size_t smem) {
     int n = 0;
-    cudaFuncSetAttribute(decode_kernel<D, G, MT, KVT, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, MT, KVT, WIN>, kThreads, smem);
+    cudaFuncSetAttribute(decode_kernel<D, G, MT, KVT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, MT, KVT>, kThreads, smem);
     return n;
 }
 
-template <int MT, int KVT, bool WIN = false>
+template <int MT, int KVT>
 int occupancy_dispatch(int D, int G, size_t smem) {
 #define PKV_CASE(DD, GG)                                                                                               \
-    if (D == DD && G == GG) return occupancy<DD, GG, MT, KVT, WIN>(smem);
+    if (D == DD && G == GG) return occupancy<DD, GG, MT, KVT>(smem);
     PKV_CASE(64, 1)
     PKV_CASE(64, 2)
     PKV_CASE(64, 4)
@@ -832,8 +792,3 @@ int pkv_decode_occupancy_f16(int D, int G, size_t smem);
 int pkv_decode_occupancy_bf16(int D, int G, size_t smem);
 int pkv_decode_occupancy_fp8_f16(int D, int G, size_t smem);
 int pkv_decode_occupancy_fp8_bf16(int D, int G, size_t smem);
-// 16-bit caches with a sliding window and sinks (decode_window_*.cu); E4M3 and 4-bit caches: decode_mma.cu
-cudaError_t pkv_decode_window_f16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t, bool merge);
-cudaError_t pkv_decode_window_bf16(const pkv_decode::Args &, int D, int G, int grid, size_t smem, cudaStream_t, bool merge);
-int pkv_decode_window_occupancy_f16(int D, int G, size_t smem);
-int pkv_decode_window_occupancy_bf16(int D, int G, size_t smem);

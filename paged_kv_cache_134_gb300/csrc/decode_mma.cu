@@ -15,9 +15,10 @@ int64_t workers_of(const pkv_cache *c, int group) {
     return (int64_t)c->num_sms * (c->kv_dtype == PKV_INT4 ? (few ? 3 : 4) : c->kv_dtype == PKV_FP8_E4M3 ? 3 : 2);
 }
 
-// sequences of a launch: over 16-bit caches the list of more would leave room for one CTA an SM instead of two
-int most_seqs(const pkv_cache *c) {
-    return c->kv_dtype == PKV_INT4 || c->kv_dtype == PKV_FP8_E4M3 ? pkv_mma::kMaxSeqs : 384;
+// sequences of a launch: over 16-bit caches the list of more would leave room for one CTA an SM instead of two (under a
+// window, whose splits may be half as long again, of fewer)
+int most_seqs(const pkv_cache *c, bool window = false) {
+    return c->kv_dtype == PKV_INT4 || c->kv_dtype == PKV_FP8_E4M3 ? pkv_mma::kMaxSeqs : window ? 312 : 384;
 }
 
 // What one launch of at most `seqs` sequences looks like.
@@ -28,6 +29,12 @@ struct Plan {
     bool is_short;  // a warp a row
 };
 
+// blocks of a sequence that a windowed query can see at most
+int window_blocks(const pkv_cache *c, const MmaDecodeLaunch &d) {
+    const int64_t bs = c->block_size, w = ((int64_t)d.window - 1 + bs - 1) / bs + 1, s = ((int64_t)d.sinks + bs - 1) / bs;
+    return (int)std::min<int64_t>(d.max_blocks, w + s);
+}
+
 // (window: max_blocks are those that a window shows)
 bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len, bool window, Plan *p) {
     const bool mass = mass_len >= 0;
@@ -35,7 +42,7 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     if (mass) p->cap = std::min(p->cap, mass_len);
     const bool i4 = c->kv_dtype == PKV_INT4;
     const int64_t workers = workers_of(c, hq / c->num_kv_heads);
-    const int most = most_seqs(c);
+    const int most = most_seqs(c, window);
     const int64_t rows = (int64_t)std::min(num_seqs, most) * c->num_kv_heads;
     // Short rows by a warp each, where two of three speak for it: the mass (which saves a launch), up to four heads (a
     // warp's work), more rows than CTAs.  4-bit, D = 128: 8 rows of four heads and 16 tokens, 5.4 us with mass
@@ -57,11 +64,16 @@ bool plan_for(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t 
     // unit, 3 for the last CTA's join, 5 for a merge launch; where a CTA has several units one warp prepares the next and
     // takes a tile less.  (Against two units per CTA, at least 64 tokens, over a hundred batches of 1 to 256
     // sequences: 0.5 to 1.1 of the time, 6 % less on average; one sequence of 131071 tokens 38.0 -> 37.1 us.)
+    // Under a window the sequences' sight is mostly of one length, a little above a round number: splits of equal
+    // size, and longer ones rather than one with a small rest (a window of 1024 and 4 sinks, 32 sequences of 32 fp16
+    // heads: one split of 1056 74.0 us, two of 528 85.1, one of 1024 and a rest 83.2).
     const int tile = i4 ? 32 : 16, round = 4 * tile;
-    int64_t split = kMaxSplit;
-    if (rows * ((p->cap + kMaxSplit - 1) / kMaxSplit) <= 4 * workers) {
+    const int64_t longest = window ? kMaxSplit + kMaxSplit / 2 : kMaxSplit;
+    const int64_t parts = std::max<int64_t>(1, (p->cap + longest - 1) / longest);
+    int64_t split = window ? round_up(std::max<int64_t>(1, (p->cap + parts - 1) / parts), 32) : kMaxSplit;
+    if (rows * parts <= 4 * workers) {
         double least = 0.;
-        for (int64_t k = i4 ? 1 : 2; k <= 2 * kMaxSplit / round; k += i4 ? 1 : 2) { // whole rounds, or a tile less
+        for (int64_t k = i4 ? 1 : 2; k <= 2 * longest / round; k += i4 ? 1 : 2) { // whole rounds, or a tile less
             const int64_t t = (k + 1) / 2 * round - (k % 2 ? tile : 0);
             const int64_t splits = std::max<int64_t>(1, (p->cap + t - 1) / t), units = rows * splits;
             if (units > 2 * workers + rows) continue; // (keeps the workspace within decode_mma_workspace_floats)
@@ -106,8 +118,11 @@ __global__ void clear_kernel(int *done, int n) {
 
 cudaError_t run(const pkv_cache *c, const pkv_mma::Args &a, bool mass, bool merge, cudaStream_t st) {
     const int mt = c->model_dtype, D = c->head_dim, sms = c->num_sms;
-    if (a.window > 0)
-        return c->kv_dtype == PKV_INT4 ? pkv_mma_int4_window(a, mt, D, sms, merge, st) : pkv_mma_fp8_window(a, mt, D, sms, merge, st);
+    if (a.window > 0) {
+        if (c->kv_dtype == PKV_INT4) return pkv_mma_int4_window(a, mt, D, sms, merge, st);
+        if (c->kv_dtype == PKV_FP8_E4M3) return pkv_mma_fp8_window(a, mt, D, sms, merge, st);
+        return pkv_mma_16bit_window(a, mt, D, sms, merge, st);
+    }
     if (!mass) return pkv_mma_int4(a, mt, D, sms, merge, st);
     if (c->kv_dtype == PKV_INT4) return pkv_mma_int4_mass(a, mt, D, sms, merge, st);
     if (c->kv_dtype == PKV_FP8_E4M3) return pkv_mma_fp8_mass(a, mt, D, sms, merge, st);
@@ -134,7 +149,7 @@ int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, in
 
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st) {
     Plan p;
-    const int seen = d.window > 0 ? (int)window_seen_blocks(c, d.max_blocks, d.window, d.sinks) : d.max_blocks;
+    const int seen = d.window > 0 ? window_blocks(c, d) : d.max_blocks;
     if (!plan_for(c, d.num_seqs, d.num_q_heads, seen, d.mass_len, d.window > 0, &p))
         return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this decode takes", d.max_blocks);
     // a batch larger than one launch takes runs in consecutive launches that share the workspace: each

@@ -1,4 +1,4 @@
-// Decode attention with attention mass over 16-bit and E4M3 caches.
+// Decode attention over 16-bit and E4M3 caches, with attention mass or under a sliding window with sinks.
 //
 // out[s][h] = sum_t p_t V_t with p_t = softmax_t(scale * q[s][h] . K_t), and
 // mass[s][g][t] := decay * mass[s][g][t] + sum_{h in group g} p[s][h][t].
@@ -53,9 +53,12 @@ PKV_DEV int place_v(int r, int c) {
 }
 
 // MASS false, WIN: without the mass, under a sliding window with sinks (see Reach); a row's splits are joined as in
-// decode_int4.cuh.  Bound by the bytes of the cache where a window is long; 256 log-normal sequences over E4M3, 32/8
-// heads, D = 128: a window of 1024 73 us (305 MB, 4.2 TB/s), 511 and a sink 47 (95 by the tensor-core kernel of the
-// plain decode, whose units of 128 tokens at least leave a window's edges empty), 256 36 (83); D = 64, 511: 34 (94).
+// decode_int4.cuh.  Bound by the bytes of the cache where windows are long, by a unit's fixed parts (finding it, the
+// queries, the join: about 3 us) where they are not.  A window wants units of few tokens: against the plain decode's
+// kernels under the same windows (CUDA cores for one head a KV head or D = 64, steps of 128 tokens on tcgen05 else)
+// 32 sequences of 32 fp16 heads, window 1024, 474 MB: 73 us (80); 256 log-normal sequences, 32/8 heads, window 511, E4M3:
+// 47 us (95), bf16 69 (89), of 64 dimensions 44 (90); one of 8192 tokens, bf16: 11 (13).  Only long windows of one head
+// a KV head went as fast there (32 of 3000 tokens: 151 and 149).
 template <int D, int KV, int MT, bool G8, bool MASS = true, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kernel(const Args a) {
     using G_ = Geo<D, KV, G8>;

@@ -4,10 +4,6 @@
 
 #include "decode_tc.cuh"
 
-// with a sliding window and sinks (decode_tc_window.cu)
-cudaError_t pkv_decode_tc_window(const CUtensorMap &tkv, const CUtensorMap &tq, const pkv_decode::Args &a, int G, int mt,
-                                 int grid, size_t smem, cudaStream_t st);
-
 namespace {
 
 bool tc_enabled() {
@@ -22,7 +18,7 @@ int operand_dtype(const pkv_cache *c) {
 
 } // namespace
 
-bool pkv_decode_tc_eligible(const pkv_cache *c, int G, int num_seqs, bool window) {
+bool pkv_decode_tc_eligible(const pkv_cache *c, int G, int num_seqs) {
     using namespace pkv_decode_tc;
     if (!tc_enabled()) return false;
     if (c->head_dim != D) return false;
@@ -30,7 +26,7 @@ bool pkv_decode_tc_eligible(const pkv_cache *c, int G, int num_seqs, bool window
     // TMA row coordinates are 32-bit
     if ((int64_t)c->num_blocks * 2 * c->num_kv_heads * c->block_size > 0x7FFFFFFFLL) return false;
     if ((int64_t)num_seqs * 16 > 0x7FFFFFFFLL) return false;
-    return smem_bytes(operand_dtype(c), c->kv_dtype == PKV_FP8_E4M3, num_seqs, window) <= 232448;
+    return smem_bytes(operand_dtype(c), c->kv_dtype == PKV_FP8_E4M3, num_seqs) <= 232448;
 }
 
 cudaError_t pkv_decode_tc_launch(const pkv_cache *c, const pkv_decode::Args &a, const void *q, int G,
@@ -47,9 +43,8 @@ cudaError_t pkv_decode_tc_launch(const pkv_cache *c, const pkv_decode::Args &a, 
     if (!(f8 ? pkv_tmap_kv_pairs_e4m3(&tkv, c->pool, c->num_blocks, c->num_kv_heads, c->block_size)
              : pkv_tmap_rows128_grouped(&tkv, c->pool, mt, pool_rows, c->block_size)))
         return cudaErrorInvalidValue;
-    const size_t smem = smem_bytes(operand_dtype(c), f8, a.num_seqs, a.window > 0);
+    const size_t smem = smem_bytes(operand_dtype(c), f8, a.num_seqs);
     const int grid = c->num_sms;
-    if (a.window > 0) return pkv_decode_tc_window(tkv, tq, a, G, mt, grid, smem, st);
 #define PKV_TC_CASE(GG)                                                                                                \
     if (G == GG) {                                                                                                     \
         if (f8)                                                                                                        \

@@ -98,10 +98,10 @@ struct Layout {
     static constexpr int FIXED = UNITS + kUnitRing * 64;   // + unit tables, 3 (S + 1) ints
 };
 
-inline size_t smem_bytes(int mt, bool f8, int num_seqs, bool window = false) {
+inline size_t smem_bytes(int mt, bool f8, int num_seqs) {
     const size_t fixed = f8 ? Layout<PKV_F16, true>::FIXED
                             : (mt == PKV_BF16 ? Layout<PKV_BF16>::FIXED : Layout<PKV_F16>::FIXED);
-    return fixed + (size_t)(window ? 4 : 3) * (num_seqs + 1) * sizeof(int); // (windows: the lengths too)
+    return fixed + (size_t)3 * (num_seqs + 1) * sizeof(int);
 }
 
 // one packed pair of the model dtype from two floats (round-to-nearest-even), `lo` in the low half
@@ -171,7 +171,7 @@ PKV_DEV int p_offset(int g, int t) {
     return (t >> 6) * (NPR * 128) + (g >> 3) * 1024 + (g & 7) * 128 + ((((e >> 3) ^ (g & 7))) << 4) + ((e & 7) << 1);
 }
 
-template <int G, int MT, int KVT, bool WIN = false>
+template <int G, int MT, int KVT>
 __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tkv, const __grid_constant__ CUtensorMap tq, const Args a) {
     // FP8 caches: S^T = K q^T is an E4M3 x E4M3 MMA (K as stored, q as three E4M3 terms with a
@@ -213,7 +213,6 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
     int *pf = reinterpret_cast<int *>(smem + LY::FIXED);
     int *pp = pf + (S + 1);
     int *nb = pp + (S + 1);
-    int *ln = WIN ? nb + (S + 1) : nullptr; // lengths
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -267,16 +266,7 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
     const uint32_t tmem = *tmem_slot;
     pdl_wait(); // the previous kernel (e.g. the append of this step) has finished
     const int bps = a.split_blocks;
-    pkv_decode::build_unit_list<WIN>(a, pf, pp, nb, warp, lane, ln);
-    // what the sequence shows (without a window: all of it)
-    auto reach = [&](int s) -> Reach {
-        if constexpr (WIN) return reach_of(ln[s], a.window, a.sinks, a.bs);
-        return {};
-    };
-    auto length = [&](int s) -> int {
-        if constexpr (WIN) return reach(s).len;
-        return a.lens[s];
-    };
+    pkv_decode::build_unit_list(a, pf, pp, nb, warp, lane);
     const int U = (pf[S] + pp[S]) * a.hkv;
     const int bpstep = TOK / a.bs; // blocks per step
     auto fail = [&]() {
@@ -339,13 +329,10 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
         constexpr int kER = 4;
         int ecur[kER], enx[kER];
         auto load_entries = [&](const Unit &x, int (&e)[kER]) {
-            Reach rc{};
-            if constexpr (WIN) rc = reach(x.s);
 #pragma unroll
             for (int k = 0; k < kER; ++k) {
                 const int idx = k * 32 + lane;
-                const int at = x.blk0 + idx + (WIN && x.blk0 + idx >= rc.from ? rc.skip : 0);
-                e[k] = idx < x.ntiles ? a.tables[(int64_t)x.s * a.max_blocks + at] : 0;
+                e[k] = idx < x.ntiles ? a.tables[(int64_t)x.s * a.max_blocks + x.blk0 + idx] : 0;
             }
         };
         // table entry of this lane's block in step i of unit `x` (0 for lanes past the step's blocks)
@@ -357,14 +344,7 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
                 const int t = __shfl_sync(0xffffffffu, e[k], idx & 31);
                 if ((idx >> 5) == k) v = t;
             }
-            if (idx >= kER * 32 && idx < x.ntiles) {
-                int at = x.blk0 + idx;
-                if constexpr (WIN) {
-                    const Reach rc = reach(x.s);
-                    if (at >= rc.from) at += rc.skip;
-                }
-                v = a.tables[(int64_t)x.s * a.max_blocks + at];
-            }
+            if (idx >= kER * 32 && idx < x.ntiles) v = a.tables[(int64_t)x.s * a.max_blocks + x.blk0 + idx];
             return lane < min(bpstep, x.ntiles - i * bpstep) ? v : 0;
         };
         int64_t gs = 0; // steps issued so far, all units
@@ -388,14 +368,14 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
         auto look_ahead = [&](int uu) {
             if (uu < U) {
                 nx = unit_at(uu);
-                nx_len = length(nx.s);
+                nx_len = a.lens[nx.s];
                 if constexpr (F8) nx_ks = a.k_scale[nx.kvh];
             }
         };
         if (u < U) {
             if (boss) {
                 un = unit_at(u);
-                if (lane == 0) write_rec(0, un, length(un.s), F8 ? a.k_scale[un.kvh] : 1.f);
+                if (lane == 0) write_rec(0, un, a.lens[un.s], F8 ? a.k_scale[un.kvh] : 1.f);
                 look_ahead(u + (int)gridDim.x);
                 if (u + (int)gridDim.x < U) load_entries(nx, enx);
             } else {
@@ -645,12 +625,7 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
         // belongs to the unit is kept apart: a select between the loaded value and -1 would wait for
         // the load on the spot, while here the value is first used a step later)
         auto blk_read = [&](const Unit &x, int i) -> int {
-            int idx = x.blk0 + i * bpstep + jb;
-            if constexpr (WIN) {
-                const Reach rc = reach(x.s);
-                if (idx >= rc.from) idx += rc.skip;
-            }
-            idx = min(idx, a.max_blocks - 1);
+            const int idx = min(x.blk0 + i * bpstep + jb, a.max_blocks - 1);
             return a.tables[(int64_t)x.s * a.max_blocks + max(idx, 0)];
         };
         auto blk_in = [&](const Unit &x, int i) -> bool { return i * bpstep + jb < x.ntiles; };
@@ -675,8 +650,6 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
             int tok_end2 = 0;
             float ksc2 = 1.f;
             const int tok0 = un.blk0 * a.bs;
-            Reach rc{};
-            if constexpr (WIN) rc = reach(un.s);
             // scores in log2 units: scale * log2(e), times the K scale of the head and the power of two
             // taken out of q by the converters (FP8 caches)
             float qsc = a.qk_scale_log2;
@@ -708,8 +681,7 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
                 const int step0 = tok0 + i * TOK;
                 // a row holds a token of the unit if it lies before the unit's end and in a block whose
                 // table entry names a block of the pool (the loaders skip the others)
-                const bool valid = step0 + r < tok_end && ent_in && ent >= 0 && ent < a.num_blocks &&
-                                   !(WIN && step0 + r >= rc.lo && step0 + r < rc.hi);
+                const bool valid = step0 + r < tok_end && ent_in && ent >= 0 && ent < a.num_blocks;
                 ent = ent_nx;
                 ent_in = ent_nx_in;
                 float sc[G];
@@ -876,8 +848,6 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
         const uint32_t lane_off = static_cast<uint32_t>(lw * 32) << 16;
         bool ok = true;
         int nu = 0;
-        if constexpr (WIN)
-            if (a.max_splits <= 1) pkv_decode::zero_empty_rows<T, D>(a, nb, r, 128);
         for (int u = blockIdx.x; u < U && ok; u += gridDim.x, ++nu) {
             Unit un;
             int te;
@@ -1083,10 +1053,10 @@ __global__ void __launch_bounds__(threads_for<KVT == PKV_FP8_E4M3>(), 1)
     }
 }
 
-template <int G, int MT, int KVT, bool WIN = false>
+template <int G, int MT, int KVT>
 cudaError_t launch(const CUtensorMap &tkv, const CUtensorMap &tq, const Args &a, int grid, size_t smem,
                    cudaStream_t st) {
-    auto kern = decode_tc_kernel<G, MT, KVT, WIN>;
+    auto kern = decode_tc_kernel<G, MT, KVT>;
     constexpr int kThreads = threads_for<KVT == PKV_FP8_E4M3>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -612,6 +612,7 @@ cudaError_t launch_merge_t(const Args &a, int sms, cudaStream_t st) {
 
 cudaError_t pkv_mma_int4(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_int4_window(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_mma_16bit_window(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_fp8_window(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_int4_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_fp8_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);

@@ -155,7 +155,7 @@ inline void pkv_row_strides(const pkv_cache *c, int64_t *block, int64_t *head, i
     }
 }
 
-// decode of 4-bit caches, decode with attention mass of every cache, windowed decode of E4M3 caches (decode_mma.cu)
+// decode of 4-bit caches, and decode with attention mass or under a window of every cache (decode_mma.cu)
 struct MmaDecodeLaunch {
     const void *q;
     void *out;
@@ -165,7 +165,7 @@ struct MmaDecodeLaunch {
     float *mass;
     int64_t mass_len; // -1: no mass
     float decay;
-    int window = 0, sinks = 0; // window > 0 (4-bit and E4M3 caches): the last `window` tokens and the first `sinks`
+    int window = 0, sinks = 0; // window > 0 (without mass): the last `window` tokens and the first `sinks` are attended to
 };
 struct PkvWorkspace {
     float *p = nullptr;
@@ -215,7 +215,6 @@ struct DecodeLaunch {
     // cascade decode: the prefix kernel, launched after the decode kernel and before the merge (its
     // plan kernel went before the decode)
     const CascadePrefixLaunch *prefix = nullptr;
-    int window = 0, sinks = 0; // window > 0: the last `window` tokens and the first `sinks` are attended to
 };
 
 // One NVTX range per C-ABI call that launches GPU work, named after the call: a profiler attached
@@ -249,10 +248,7 @@ int64_t decode_workspace_floats(const pkv_cache *c, int num_seqs, int num_q_head
 // Sequences one decode launch takes at most (its kernels hold a per-sequence table in shared memory);
 // a call with more runs its sequences in consecutive launches of this many, which reuse one workspace
 // (stream order: each launch waits for the previous launch's merge before it writes partials).
-int decode_seqs_per_launch(const pkv_cache *c, int G, bool window = false);
-// windowed decode: blocks of a sequence that a query can see at most, and the blocks of a split of them
-int64_t window_seen_blocks(const pkv_cache *c, int max_blocks, int window, int sinks);
-int window_split_blocks(const pkv_cache *c, int G, int num_seqs, int64_t seen_blocks);
+int decode_seqs_per_launch(const pkv_cache *c, int G);
 // Runs the decode described by d (d.ws_o sized for min(num_seqs, decode_seqs_per_launch) sequences)
 // as consecutive launches of at most decode_seqs_per_launch sequences each (api.cu).
 cudaError_t launch_decode_chunked(pkv_cache *c, DecodeLaunch d, cudaStream_t st);
@@ -267,7 +263,7 @@ cudaError_t launch_decode(pkv_cache *c, const DecodeLaunch &d, cudaStream_t st);
 namespace pkv_decode {
 struct Args;
 }
-bool pkv_decode_tc_eligible(const pkv_cache *c, int G, int num_seqs, bool window = false);
+bool pkv_decode_tc_eligible(const pkv_cache *c, int G, int num_seqs);
 cudaError_t pkv_decode_tc_launch(const pkv_cache *c, const pkv_decode::Args &a, const void *q, int G, cudaStream_t st);
 
 struct PrefillLaunch {

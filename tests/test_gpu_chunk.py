@@ -274,7 +274,7 @@ def test_a_conversation_as_it_runs(kv, model, norm):
         p = "pair" if kv == "bf16" else "f16"
         if n == 1:
             out = P.paged_decode_attention_window(qr, cache, tables, lens, s, window, sinks=sinks)
-            p = {"bf16": "pair", "f16": "f16", "fp8": "f32"}[kv]
+            p = {"bf16": "pair", "f16": "f32", "fp8": "f32"}[kv]
         else:
             cu = torch.tensor([0, n], dtype=torch.int32).cuda()
             out = P.paged_chunk_attention(qr, cache, tables, lens, cu, n, s, window=window, sinks=sinks)

@@ -17,14 +17,15 @@ if not torch.cuda.is_available():
 
 
 def weights(x, plain=False):
-    """How the weights enter the second product: 16-bit caches' grouped heads of 128 go to the tensor cores, E4M3's in the
-    plain decode; under a window E4M3's weights are fp16 pairs (2^-22) and the queries fp16 scaled to the range."""
+    """How the weights enter the second product: as pairs, bf16 (2^-16) or fp16 (2^-22, as good as fp32 here); in the
+    plain decode grouped heads of 128 go to the tensor cores, where fp16 weights are single and E4M3 queries terms."""
     if x.kv == "int4":
         return dict(p="f32", steps=x.steps)
-    tensor = x.d == 128 and x.hq > x.hkv and (plain or x.kv != "fp8")
-    if not tensor:
-        return dict(p="f32")
-    return dict(p="pair" if x.kv == "bf16" else "f16", terms=x.kv == "fp8")
+    if x.kv == "bf16":
+        return dict(p="pair")
+    if plain and x.d == 128 and x.hq > x.hkv:
+        return dict(p="f16", terms=x.kv == "fp8")
+    return dict(p="f32")
 
 
 def reference(x, q64, window, sinks):
