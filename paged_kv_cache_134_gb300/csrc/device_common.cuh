@@ -54,7 +54,8 @@ struct Reach {
 PKV_DEV Reach reach_of(int L, int window, int sinks, int bs) {
     const int first = L - window; // (L >= 0, window >= 1)
     if (first <= sinks) return {L, 0, 0, 0, 0};
-    const int from = (sinks + bs - 1) / bs, skip = max(first / bs - from, 0);
+    const int log2 = 31 - __clz(bs); // (blocks hold 8, 16 or 32 tokens)
+    const int from = (sinks + bs - 1) >> log2, skip = max((first >> log2) - from, 0);
     return {L - skip * bs, from, skip, sinks, first - skip * bs};
 }
 // ------------------------------------------------------------------ mbarrier

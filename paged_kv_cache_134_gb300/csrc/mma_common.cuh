@@ -150,11 +150,73 @@ PKV_DEV int row_len(const Args &a, int s) {
     return L <= 0 ? 0 : (int64_t)L > a.cap ? (int)a.cap : L;
 }
 
+// Windows without splits, more units than CTAs: sequences of most tokens first, in eight classes, so that the CTAs, which take
+// every gridDim-th unit, end together.  full[0 .. S) is then the order, full[S] = 0, part[S] = S.  (256 log-normal
+// sequences over E4M3, window 511: SORTED_FIGURES.)
+PKV_DEV bool by_length(const Args &a) {
+    return a.max_splits == 1 && a.num_seqs >= 31 && (int64_t)a.num_seqs * a.hkv > (int64_t)gridDim.x;
+}
+PKV_DEV void list_by_length(const Args &a, int *full, int *part) {
+    const int S = a.num_seqs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = (S + 31) >> 5;
+    int *len = part + S + 1, *count = part; // [class][chunk of 32 sequences]: 8 chunks <= S + 1 for S >= 31
+    uint32_t classes = 0; // this lane's sequences', four bits each (at most 1024 sequences: 8 chunks a warp)
+    for (int k = warp; k < chunks; k += kWarps) {
+        const int s = k * 32 + lane;
+        int cls = 8;
+        if (s < S) {
+            const int L = row_len(a, s), n = reach_of(L, a.window, a.sinks, 1 << a.bs_log2).len;
+            if (blockIdx.x == 0 && (int64_t)a.lens[s] > a.cap) set_error(a.err, PKV_DEVERR_LENGTH);
+            len[s] = L;
+            cls = 7;
+#pragma unroll
+            for (int i = 1; i < 8; ++i) cls -= 8 * (int64_t)n >= (int64_t)i * a.split_tokens;
+        }
+        classes = classes << 4 | cls;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = __popc(__ballot_sync(0xffffffffu, cls == i));
+            if (lane == i) count[i * chunks + k] = n;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int sum = 0;
+        for (int i = 0; i < 8 * chunks; i += 32) {
+            const int n = i + lane < 8 * chunks ? count[i + lane] : 0;
+            int v = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int w = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += w;
+            }
+            if (i + lane < 8 * chunks) count[i + lane] = sum + v - n;
+            sum += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+    for (int k = warp; k < chunks; k += kWarps) {
+        const int s = k * 32 + lane, cls = classes >> (4 * ((chunks - 1 - k) / kWarps)) & 15;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned same = __ballot_sync(0xffffffffu, cls == i);
+            if (cls == i) full[count[i * chunks + k] + __popc(same & ((1u << lane) - 1))] = s;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        full[S] = 0;
+        part[S] = S;
+    }
+    __syncthreads();
+}
+
 // Block scan of the sequences' unit counts: full[s + 1], part[s + 1] hold the inclusive sums of whole
 // splits and of partial ones (a sequence of length 0 has one partial unit, which writes its zero row); the lengths lie
 // behind part.  WIN: units of what is in sight (see Reach).
 template <bool WIN = false>
 PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
+    if constexpr (WIN)
+        if (by_length(a)) return list_by_length(a, full, part);
     const int S = a.num_seqs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *len = part + S + 1;
     int cf = 0, cp = 0; // sums of the sequences before this pass
@@ -218,8 +280,14 @@ PKV_DEV UnitOf<WIN> unit_of(const Args &a, const int *full, const int *part, int
     const int v = whole ? u : u - nfull;
     const int k = (int)(((uint64_t)(uint32_t)v * a.hkv_magic) >> a.hkv_shift); // v / hkv
     r.kvh = v - k * a.hkv;
-    r.s = find_row(whole ? full : part, a.num_seqs, k);
-    r.j = whole ? k - full[r.s] : full[r.s + 1] - full[r.s];
+    const bool ordered = WIN && by_length(a);
+    if (ordered) {
+        r.s = full[k];
+        r.j = 0;
+    } else {
+        r.s = find_row(whole ? full : part, a.num_seqs, k);
+        r.j = whole ? k - full[r.s] : full[r.s + 1] - full[r.s];
+    }
     int L = part[a.num_seqs + 1 + r.s];
     if constexpr (WIN) {
         const Reach rc = reach_of(L, a.window, a.sinks, 1 << a.bs_log2);
@@ -229,7 +297,7 @@ PKV_DEV UnitOf<WIN> unit_of(const Args &a, const int *full, const int *part, int
         r.lo = rc.lo;
         r.hi = rc.hi;
     }
-    r.nsplit = (full[r.s + 1] - full[r.s]) + (part[r.s + 1] - part[r.s]);
+    r.nsplit = ordered ? 1 : (full[r.s + 1] - full[r.s]) + (part[r.s + 1] - part[r.s]);
     r.t0 = r.j * a.split_tokens;
     r.n = min(L - r.t0, a.split_tokens);
     return r;

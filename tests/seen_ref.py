@@ -7,7 +7,8 @@ Tolerance of an output o = sum p v / sum p, S = sum p |v| / sum p:
   * scores: a sum of D products in fp32, D 2^-24 of sum |q||k| scale, twice in a weight (its own and the maximum's
     part in the denominator);
   * exp2, the sums and the quotient: 2^-18 (ex2.approx 2^-22, sums of up to a few thousand rounded terms in blocks);
-  * weights enter the second product as fp16 (2^-11) or as a bf16 pair (2^-16), or in fp32 or an fp16 pair (2^-22); as fp16 a weight below
+  * weights enter the second product as fp16 (2^-11), as a bf16 pair (2^-16), or in fp32 or an fp16 pair (2^-22); as
+    fp16 a weight below
     2^-14 of the base is held to 2^-25, which a row of L tokens meets at most L times (the base's own weight is at
     least 1): L 2^-25 max |v|;
   * grouped heads over an E4M3 cache at D = 128, single tokens: q goes in as three E4M3 terms, each to 2^-4 of what
