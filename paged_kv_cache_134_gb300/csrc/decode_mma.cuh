@@ -57,8 +57,9 @@ PKV_DEV int place_v(int r, int c) {
 // queries, the join: about 3 us) where they are not.  A window wants units of few tokens: against the plain decode's
 // kernels under the same windows (CUDA cores for one head a KV head or D = 64, steps of 128 tokens on tcgen05 else)
 // 32 sequences of 32 fp16 heads, window 1024, 474 MB: 73 us (80); 256 log-normal sequences, 32/8 heads, window 511, E4M3:
-// 47 us (95), bf16 69 (89), of 64 dimensions 44 (90); one of 8192 tokens, bf16: 11 (13).  Only long windows of one head
-// a KV head went as fast there (32 of 3000 tokens: 151 and 149).
+// 47 us (95), bf16 70 (89), of 64 dimensions 44 (90); one of 8192 tokens, bf16: 11 (13).  Only long windows of one head
+// a KV head went as fast there (32 of 3000 tokens: 151 and 149).  The next unit's first tiles behind this one's last in the
+// ring, its table checked at a barrier of its own, changed nothing (47.2; three CTAs an SM hide one another's joins).
 template <int D, int KV, int MT, bool G8, bool MASS = true, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kernel(const Args a) {
     using G_ = Geo<D, KV, G8>;

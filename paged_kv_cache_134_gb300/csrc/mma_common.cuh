@@ -152,7 +152,8 @@ PKV_DEV int row_len(const Args &a, int s) {
 
 // Windows without splits, more units than CTAs: sequences of most tokens first, in eight classes, so that the CTAs, which take
 // every gridDim-th unit, end together.  full[0 .. S) is then the order, full[S] = 0, part[S] = S.  (256 log-normal
-// sequences over E4M3, window 511: SORTED_FIGURES.)
+// sequences, 32/8 heads, by order of the batch and by length: window 1024 over E4M3 64.7 and 59.6 us, bf16 101.0 and 96.4,
+// of 64 dimensions 63.0 and 58.5; 511 over E4M3 46.7 and 46.5, bf16, where all SMs wait for memory anyway, 68.7 and 70.0.)
 PKV_DEV bool by_length(const Args &a) {
     return a.max_splits == 1 && a.num_seqs >= 31 && (int64_t)a.num_seqs * a.hkv > (int64_t)gridDim.x;
 }
