@@ -374,15 +374,16 @@ int paged_prefill_attention(const void *q, const void *k, const void *v, const i
  *   out[cu_i + r][h] = sum_t softmax_t(scale * q[cu_i + r][h] . K_t[g]) V_t[g],
  *   t <= p, and with window > 0 also t > p - window or t < sinks (window 0: no window, sinks 0),
  * g = h / group.  A row that sees nothing (p < 0) is zero.  q, out: [total_tokens][num_q_heads][head_dim], not
- * overlapping; rows behind cu_seqlens[num_seqs] are left as they were.  Blocks that no row of a tile (128 / group tokens) sees are
- * not read.  scale finite and > 0.  cu_seqlens as for packed_prefill_attention; L_i above the tables' tokens sets
- * PKV_DEVERR_LENGTH.  The rows of a sequence with such numbers are left as they were.
- * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4), arithmetic as in paged_prefill_attention, whose results for the
- * same rows agree to its tolerance.  The query heads of a KV head share its keys, which are cut into splits where the
- * rows are few: boundaries depend on L_i, n_i, num_seqs, total_tokens, max_seqlen, max_blocks_per_seq, window and
- * sinks.  A NaN or infinity in V reaches the rows of its sequence whose tile of rows sees that token, also the earlier ones among
- * them; one in K only the rows that see it.  Three launches (two where no row's keys are split).  Workspace: as
- * for paged_decode_attention_mass, one per stream and per capture. */
+ * overlapping; rows behind cu_seqlens[num_seqs] are left as they were.  Blocks that no row of a tile (128 / group
+ * tokens) sees are not read.  scale finite and > 0.  cu_seqlens as for packed_prefill_attention; L_i above the tables'
+ * tokens sets PKV_DEVERR_LENGTH.  The rows of a sequence with such numbers are left as they were.
+ * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4), arithmetic as in paged_prefill_attention, or, for up to 24 rows
+ * (max_seqlen times group), as in paged_decode_attention_mass; results agree with paged_prefill_attention's for the same
+ * rows to its tolerance.  The query heads of a KV head share its keys, which are cut into splits where the rows are few:
+ * boundaries depend on L_i, n_i, num_seqs, total_tokens, max_seqlen, max_blocks_per_seq, window and sinks.  A NaN or
+ * infinity in V reaches the rows of its sequence whose tile of rows sees that token, also the earlier ones among them;
+ * one in K only the rows that see it.  One to three launches.  Workspace: as for paged_decode_attention_mass, one per
+ * stream and per capture. */
 int paged_chunk_attention(const void *q, pkv_cache_t cache, const int32_t *block_tables, int max_blocks_per_seq,
                           const int32_t *context_lens, const int32_t *cu_seqlens, int num_seqs, int max_seqlen,
                           int64_t total_tokens, int num_q_heads, float scale, int window, int sinks, void *out,

@@ -24,7 +24,7 @@ SOURCES = ["api.cu", "append.cu", "rotary.cu", "decode.cu", "decode_f16.cu", "de
            "prefill.cu", "prefill_packed.cu", "prefill_paged.cu",
            "prefill_cascade.cu", "prefill_chunk.cu", "chunk_stream_16bit_few.cu",
            "chunk_stream_16bit_rows.cu", "chunk_stream_e4m3_few.cu", "chunk_stream_e4m3_rows.cu",
-           "noalloc.cu", "blocks.cu", "selftest.cu", "prefix_cache.cpp"]
+           "chunk_few_16bit.cu", "chunk_few_e4m3.cu", "noalloc.cu", "blocks.cu", "selftest.cu", "prefix_cache.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,6 @@
+#include "chunk_few.cuh"
+
+cudaError_t pkv_few_16bit(const pkv_mma::FewArgs &a, int mt, int D, int sms, bool merge, cudaStream_t st) {
+    return mt == PKV_F16 ? pkv_mma::launch_few<PKV_F16, PKV_F16>(a, D, sms, merge, st)
+                         : pkv_mma::launch_few<PKV_BF16, PKV_BF16>(a, D, sms, merge, st);
+}

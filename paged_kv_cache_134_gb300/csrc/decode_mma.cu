@@ -6,6 +6,7 @@
 namespace {
 
 constexpr int kMaxSplit = 1024; // tokens
+constexpr int kFewSplit = 1536; // of the chunk attention of few rows
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -129,7 +130,134 @@ cudaError_t run(const pkv_cache *c, const pkv_mma::Args &a, bool mass, bool merg
     return pkv_mma_16bit_mass(a, mt, D, sms, merge, st);
 }
 
+// what follows from the cache and the heads alone
+int pool_args(const pkv_cache *c, int hq, pkv_mma::Args *a) {
+    a->pool = static_cast<const char *>(c->pool);
+    a->k_scale = c->k_scale;
+    a->v_scale = c->v_scale;
+    a->err = c->err;
+    a->num_blocks = c->num_blocks;
+    pkv_row_strides(c, &a->blk_stride, &a->head_stride, &a->v_off);
+    if (a->blk_stride > 0xFFFFFFFFll)
+        return pkv_fail(PKV_EUNSUPPORTED, "blocks of %lld bytes are larger than this decode takes", (long long)a->blk_stride);
+    a->hq = hq;
+    a->hkv = c->num_kv_heads;
+    a->group = hq / c->num_kv_heads;
+    int s = 0;
+    while (((int64_t)1 << s) < a->hkv) ++s;
+    a->hkv_shift = 31 + s;
+    a->hkv_magic = (uint32_t)((((uint64_t)1 << a->hkv_shift) + a->hkv - 1) / a->hkv);
+    a->bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
+    return PKV_OK;
+}
+
+// Splits of the chunk attention of few rows: tokens of one, for `units` = sequences times KV heads.  At least 128 tokens (a
+// unit's fixed part costs about 100) and so few that the units fill the SMs twice; where there are more units than that,
+// splits of equal size up to kFewSplit tokens.
+int few_split(const pkv_cache *c, int64_t units, int64_t cap, int ctas) {
+    const int64_t workers = (int64_t)c->num_sms * ctas, longest = kFewSplit;
+    const int64_t parts = std::max<int64_t>(1, (cap + longest - 1) / longest);
+    int64_t split = round_up(std::max<int64_t>(1, (cap + parts - 1) / parts), 32);
+    if (units * parts <= 4 * workers) {
+        double least = 0.;
+        for (int64_t t = 128; t <= longest; t += 64) {
+            const int64_t splits = std::max<int64_t>(1, (cap + t - 1) / t);
+            if (units * splits > 2 * workers + units) continue; // (keeps the workspace within few_workspace_floats)
+            const double join = splits == 1 ? 0. : 4.;
+            const double time = (double)((units * splits + workers - 1) / workers) *
+                                    (1.4 * (double)((std::min(t, cap) + 63) / 64) + 3.) + join;
+            if (least == 0. || time < least) {
+                least = time;
+                split = t;
+            }
+            if (splits == 1) break;
+        }
+    }
+    return (int)std::max(split, round_up((cap + 1023) / 1024, 64));
+}
+
 } // namespace
+
+// tokens that the new ones of a sequence can see together, at most
+static int64_t few_seen(const pkv_cache *c, const ChunkLaunch &p) {
+    const int64_t bs = c->block_size, cap = p.max_blocks * bs;
+    if (p.window == 0) return cap;
+    return std::min<int64_t>(cap, (((int64_t)p.window + p.max_seqlen - 2 + bs - 1) / bs + 1 + ((int64_t)p.sinks + bs - 1) / bs) * bs);
+}
+static int few_seqs(const pkv_cache *c, int num_seqs) { // of a launch (the list of more would leave room for one CTA an SM less)
+    return std::min(num_seqs, c->kv_dtype == PKV_FP8_E4M3 ? pkv_mma::kMaxSeqs : 256);
+}
+
+// Up to 24 rows of a KV head: by chunk_few.cuh, but where long sequences fill the SMs many times over only up to 16 (E4M3)
+// and 8; tcgen05 takes 64 rows in the time of one there.  (256 log-normal sequences of up to 8192 tokens, 32/8 heads, E4M3:
+// 8 rows 95 us, tcgen05 168, 16 rows 148 and 174, 24 rows 190 and 178; bf16 8 rows 159 and 191, 16 rows 203 and 197.  The
+// same under a window of 511: E4M3 16 rows 78 and 121, 24 rows 104 and 123, bf16 16 rows 99 and 154; 8 sequences of 4096,
+// 24 rows: E4M3 30 and 46, bf16 35 and 50.)
+bool chunk_is_few(const pkv_cache *c, const ChunkLaunch &p) {
+    const int64_t rows = (int64_t)p.max_seqlen * (p.num_q_heads / c->num_kv_heads);
+    if (rows > 24) return false;
+    const int64_t parts = (few_seen(c, p) + kFewSplit - 1) / kFewSplit;
+    return rows <= (c->kv_dtype == PKV_FP8_E4M3 ? 16 : 8) || parts <= 1 ||
+           (int64_t)few_seqs(c, p.num_seqs) * c->num_kv_heads * parts <= 8 * (int64_t)c->num_sms;
+}
+
+int64_t few_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens, int hq, int max_blocks) {
+    // Rows of at most 24 a (sequence, KV head).  Splits: of at least 1024 tokens, or of at least 128 and so that a launch (of
+    // 256 sequences at least, unless it is the only one) has two waves of units (3 CTAs an SM) and one a row more.
+    const int64_t cap = (int64_t)max_blocks * c->block_size;
+    const int64_t rows = std::min<int64_t>(tokens * hq, (int64_t)num_seqs * c->num_kv_heads * 24);
+    const int64_t waves = 24 * 2 * 3 * (int64_t)c->num_sms * ((num_seqs + 255) / 256);
+    const int64_t most = std::min<int64_t>(rows * ((cap + 127) / 128), rows + waves);
+    return std::max(most, rows * ((cap + 1023) / 1024)) * (c->head_dim + 2);
+}
+
+int chunk_few_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
+    const int G = p.num_q_heads / c->num_kv_heads, rows = p.max_seqlen * G;
+    const int64_t bs = c->block_size, cap = (int64_t)p.max_blocks * bs, seen = few_seen(c, p);
+    const bool fp8 = c->kv_dtype == PKV_FP8_E4M3;
+    const int per = few_seqs(c, p.num_seqs);
+    pkv_mma::FewArgs a;
+    if (int r = pool_args(c, p.num_q_heads, &a)) return r;
+    a.split_tokens = few_split(c, (int64_t)per * c->num_kv_heads, seen, fp8 && rows <= 8 ? 3 : 2);
+    if (a.split_tokens / bs > 8192) return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this call takes", p.max_blocks);
+    a.max_splits = (int)std::max<int64_t>(1, (seen + a.split_tokens - 1) / a.split_tokens);
+    std::lock_guard<std::mutex> lk(c->ws_mu);
+    PkvWorkspace ws;
+    const int64_t partials = a.max_splits > 1 ? p.total_tokens * p.num_q_heads * a.max_splits : 0;
+    if (int r = pkv_stream_workspace(c, st, partials * (c->head_dim + 2), &ws)) return r;
+    a.q = p.q;
+    a.out = p.out;
+    a.ws_o = ws.p;
+    a.ws_ml = ws.p + partials * c->head_dim;
+    a.ws_x = nullptr;
+    a.mass = nullptr;
+    a.mass_len = -1;
+    a.decay = 1.f;
+    a.done = nullptr;
+    a.cap = cap;
+    a.max_blocks = p.max_blocks;
+    a.qk_scale_log2 = p.scale * 1.4426950408889634f;
+    a.window = std::min(p.window, 1 << 30);
+    a.sinks = p.sinks;
+    a.total = p.total_tokens;
+    a.max_seqlen = p.max_seqlen;
+    a.lg_group = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
+    PkvTimer timer(c, PKV_KIND_PREFILL, st);
+    for (int s0 = 0; s0 < p.num_seqs; s0 += per) {
+        a.num_seqs = std::min(per, p.num_seqs - s0);
+        a.tables = p.tables ? p.tables + (int64_t)s0 * p.max_blocks : nullptr;
+        a.lens = p.lens + s0;
+        a.cu = p.cu + s0;
+        for (const bool merge : {false, true}) {
+            if (merge && a.max_splits == 1) break;
+            g_pkv_launches++;
+            const cudaError_t e = fp8 ? pkv_few_e4m3(a, c->model_dtype, c->head_dim, c->num_sms, merge, st)
+                                      : pkv_few_16bit(a, c->model_dtype, c->head_dim, c->num_sms, merge, st);
+            if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
+        }
+    }
+    return PKV_OK;
+}
 
 int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len) {
     // units of one launch: at most two waves and one more a row, or those of the largest split; with mass the scores
@@ -171,29 +299,12 @@ int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace 
     const bool mass = d.mass_len >= 0;
     const bool join = !mass && p.max_splits <= pkv_mma::kJoinSplits && (int64_t)p.seqs * c->num_kv_heads <= ws.counters;
     pkv_mma::Args a;
-    a.pool = static_cast<const char *>(c->pool);
-    a.k_scale = c->k_scale;
-    a.v_scale = c->v_scale;
-    a.err = c->err;
-    a.num_blocks = c->num_blocks;
-    pkv_row_strides(c, &a.blk_stride, &a.head_stride, &a.v_off);
-    if (a.blk_stride > 0xFFFFFFFFll)
-        return pkv_fail(PKV_EUNSUPPORTED, "blocks of %lld bytes are larger than this decode takes", (long long)a.blk_stride);
+    if (int r = pool_args(c, d.num_q_heads, &a)) return r;
     a.mass_len = d.mass_len;
     a.cap = d.window > 0 ? (int64_t)d.max_blocks * c->block_size : p.cap;
     a.window = d.window;
     a.sinks = d.sinks;
     a.max_blocks = d.max_blocks;
-    a.hq = d.num_q_heads;
-    a.hkv = c->num_kv_heads;
-    a.group = d.num_q_heads / c->num_kv_heads;
-    {
-        int s = 0;
-        while (((int64_t)1 << s) < a.hkv) ++s;
-        a.hkv_shift = 31 + s;
-        a.hkv_magic = (uint32_t)((((uint64_t)1 << a.hkv_shift) + a.hkv - 1) / a.hkv);
-    }
-    a.bs_log2 = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
     a.split_tokens = p.split;
     a.max_splits = p.max_splits;
     a.qk_scale_log2 = d.scale * 1.4426950408889634f;

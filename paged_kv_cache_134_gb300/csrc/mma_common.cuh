@@ -50,6 +50,13 @@ struct Args {
     int window, sinks; // WIN kernels: what is attended to (see Reach)
 };
 
+// attention of several new tokens a sequence (chunk_few.cuh)
+struct FewArgs : Args {
+    const int32_t *cu; // rows of sequence s: [cu[s], cu[s + 1])
+    int64_t total;     // rows of q
+    int max_seqlen, lg_group;
+};
+
 // (the offset rides in the instruction: no address to compute)
 template <int OFF = 0>
 PKV_DEV void lds64(uint32_t *w, uint32_t a) {
@@ -150,6 +157,17 @@ PKV_DEV int row_len(const Args &a, int s) {
     return L <= 0 ? 0 : (int64_t)L > a.cap ? (int)a.cap : L;
 }
 
+// what sequence s shows, if it holds L tokens
+template <bool WIN>
+PKV_DEV Reach sight_of(const Args &a, int s, int L) {
+    if constexpr (WIN) return reach_of(L, a.window, a.sinks, 1 << a.bs_log2);
+    return {L, 0, 0, 0, 0};
+}
+PKV_DEV void report_row(const Args &a, int s) {
+    if ((int64_t)a.lens[s] > a.cap) set_error(a.err, PKV_DEVERR_LENGTH);
+}
+PKV_DEV bool has_rows(const Args &, int) { return true; }
+
 // Windows without splits, more units than CTAs: sequences of most tokens first, in eight classes, so that the CTAs, which take
 // every gridDim-th unit, end together.  full[0 .. S) is then the order, full[S] = 0, part[S] = S.  (256 log-normal
 // sequences, 32/8 heads, by order of the batch and by length: window 1024 over E4M3 64.7 and 59.6 us, bf16 101.0 and 96.4,
@@ -157,7 +175,8 @@ PKV_DEV int row_len(const Args &a, int s) {
 PKV_DEV bool by_length(const Args &a) {
     return a.max_splits == 1 && a.num_seqs >= 31 && (int64_t)a.num_seqs * a.hkv > (int64_t)gridDim.x;
 }
-PKV_DEV void list_by_length(const Args &a, int *full, int *part) {
+template <typename A>
+PKV_DEV void list_by_length(const A &a, int *full, int *part) {
     const int S = a.num_seqs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = (S + 31) >> 5;
     int *len = part + S + 1, *count = part; // [class][chunk of 32 sequences]: 8 chunks <= S + 1 for S >= 31
     uint32_t classes = 0; // this lane's sequences', four bits each (at most 1024 sequences: 8 chunks a warp)
@@ -165,8 +184,8 @@ PKV_DEV void list_by_length(const Args &a, int *full, int *part) {
         const int s = k * 32 + lane;
         int cls = 8;
         if (s < S) {
-            const int L = row_len(a, s), n = reach_of(L, a.window, a.sinks, 1 << a.bs_log2).len;
-            if (blockIdx.x == 0 && (int64_t)a.lens[s] > a.cap) set_error(a.err, PKV_DEVERR_LENGTH);
+            const int L = row_len(a, s), n = sight_of<true>(a, s, L).len;
+            if (blockIdx.x == 0) report_row(a, s);
             len[s] = L;
             cls = 7;
 #pragma unroll
@@ -214,8 +233,8 @@ PKV_DEV void list_by_length(const Args &a, int *full, int *part) {
 // Block scan of the sequences' unit counts: full[s + 1], part[s + 1] hold the inclusive sums of whole
 // splits and of partial ones (a sequence of length 0 has one partial unit, which writes its zero row); the lengths lie
 // behind part.  WIN: units of what is in sight (see Reach).
-template <bool WIN = false>
-PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
+template <bool WIN = false, typename A = Args>
+PKV_DEV void list_units(const A &a, int *full, int *part, int *tmp) {
     if constexpr (WIN)
         if (by_length(a)) return list_by_length(a, full, part);
     const int S = a.num_seqs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -227,11 +246,13 @@ PKV_DEV void list_units(const Args &a, int *full, int *part, int *tmp) {
         int f = 0, p = 0;
         if (s < S) {
             const int L = row_len(a, s);
-            if (blockIdx.x == 0 && (int64_t)a.lens[s] > a.cap) set_error(a.err, PKV_DEVERR_LENGTH);
+            if (blockIdx.x == 0) report_row(a, s);
             len[s] = L;
-            const int n = WIN ? reach_of(L, a.window, a.sinks, 1 << a.bs_log2).len : L;
-            f = n / a.split_tokens;
-            p = (n % a.split_tokens != 0 || n == 0) ? 1 : 0;
+            if (has_rows(a, s)) {
+                const int n = sight_of<WIN>(a, s, L).len;
+                f = n / a.split_tokens;
+                p = (n % a.split_tokens != 0 || n == 0) ? 1 : 0;
+            }
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -274,8 +295,8 @@ template <bool WIN>
 using UnitOf = std::conditional_t<WIN, SeenUnit, Unit>;
 
 // Unit u of the list (all lanes of a warp together, u the same for all).
-template <bool WIN = false>
-PKV_DEV UnitOf<WIN> unit_of(const Args &a, const int *full, const int *part, int nfull, int u) {
+template <bool WIN = false, typename A = Args>
+PKV_DEV UnitOf<WIN> unit_of(const A &a, const int *full, const int *part, int nfull, int u) {
     UnitOf<WIN> r;
     const bool whole = u < nfull;
     const int v = whole ? u : u - nfull;
@@ -291,7 +312,7 @@ PKV_DEV UnitOf<WIN> unit_of(const Args &a, const int *full, const int *part, int
     }
     int L = part[a.num_seqs + 1 + r.s];
     if constexpr (WIN) {
-        const Reach rc = reach_of(L, a.window, a.sinks, 1 << a.bs_log2);
+        const Reach rc = sight_of<true>(a, r.s, L);
         L = rc.len;
         r.from = rc.from;
         r.skip = rc.skip;
@@ -498,7 +519,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const int row = blockIdx.x, s = row / a.hkv, kvh = row - s * a.hkv;
-    const int n = WIN ? reach_of(row_len(a, s), a.window, a.sinks, 1 << a.bs_log2).len : row_len(a, s);
+    const int n = sight_of<WIN>(a, s, row_len(a, s)).len;
     const int nsplit = (n + a.split_tokens - 1) / a.split_tokens;
     if (nsplit <= 1) return;
     split_weights(a, s, kvh, nsplit, wj, a.max_splits, sm_M, sm_inv);
@@ -686,6 +707,8 @@ cudaError_t pkv_mma_fp8_window(const pkv_mma::Args &, int mt, int D, int sms, bo
 cudaError_t pkv_mma_int4_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_fp8_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_mma_16bit_mass(const pkv_mma::Args &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_few_16bit(const pkv_mma::FewArgs &, int mt, int D, int sms, bool merge, cudaStream_t);
+cudaError_t pkv_few_e4m3(const pkv_mma::FewArgs &, int mt, int D, int sms, bool merge, cudaStream_t);
 cudaError_t pkv_short_int4(const pkv_mma::Args &, int mt, int D, cudaStream_t);
 cudaError_t pkv_short_fp8(const pkv_mma::Args &, int mt, int D, cudaStream_t);
 cudaError_t pkv_short_16bit(const pkv_mma::Args &, int mt, int D, cudaStream_t);

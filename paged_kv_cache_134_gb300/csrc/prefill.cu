@@ -626,10 +626,12 @@ int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens,
     const int64_t partials = rows * splits + std::min<int64_t>(rows * steps, 2 * 256 * (int64_t)c->num_sms);
     const int64_t groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + 15) / 16), tokens / 16 + num_seqs);
     const int64_t items = groups * splits + std::min<int64_t>(groups * steps, 2 * (int64_t)c->num_sms);
-    return (4 + 4 * items + 63) / 64 * 64 + partials * (c->head_dim + 2);
+    const int64_t few = few_workspace_floats(c, num_seqs, tokens, hq, max_blocks);
+    return std::max((4 + 4 * items + 63) / 64 * 64 + partials * (c->head_dim + 2), few);
 }
 
 int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
+    if (chunk_is_few(c, p)) return chunk_few_entry(c, p, st);
     const int hq = p.num_q_heads, D = c->head_dim, mt = c->model_dtype;
     const ChunkShape s = chunk_shape(c, p.num_seqs, p.total_tokens, p.max_seqlen, hq, p.max_blocks, p.window, p.sinks);
     if (s.items * c->num_kv_heads > 0x7FFFFFFF || p.total_tokens > 0x7FFFFFFF)

@@ -14,8 +14,10 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 
-def weights(x):
+def weights(x, few=False):
     # (over an E4M3 cache the products run on fp16 whatever the model's type: codes and a scaled q are exact in it)
+    if few and x.model == "f16":  # a pair of fp16: 2^-22, as good as fp32 here
+        return dict(p="f32")
     return dict(p="pair" if x.kv == "bf16" else "f16")
 
 
@@ -29,7 +31,7 @@ def chunks(x, new):
     return cu, q, q64
 
 
-def run(x, new, window=0, sinks=0, most=None, hidden=True):
+def run(x, new, window=0, sinks=0, most=None, hidden=True, few=False):
     """The call on sequences whose last new[i] tokens are the queries, checked row by row; what no row of a
     sequence sees is taken off the tables or spoilt first."""
     cu, q, q64 = chunks(x, new)
@@ -51,7 +53,7 @@ def run(x, new, window=0, sinks=0, most=None, hidden=True):
     at = 0
     for i, (n, m) in enumerate(zip(x.lens, new)):
         r = R.attend(q64[at:at + m], *x.rows(i), R.scale_of(x.d), positions(n, m), window, sinks)
-        R.check(g[at:at + m], r, x.model, **weights(x))
+        R.check(g[at:at + m], r, x.model, **weights(x, few))
         at += m
     return got
 
@@ -301,3 +303,86 @@ def test_many_items_of_unequal_lengths(hq, hkv, d, bs, kv, model, longest):
     assert got.shape == first.shape
     for _ in range(6):
         assert torch.equal(first, P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, longest, 0.1))
+
+
+FEW_LENS = [1, 2, 3, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 200, 257, 300, 511, 700, 0, 40]
+
+
+@pytest.mark.parametrize("rows", [8, 16, 24])
+@pytest.mark.parametrize("hq,hkv,d,bs,kv,model,window,sinks", [
+    (3, 3, 128, 16, "f16", "f16", 0, 0), (4, 2, 64, 8, "bf16", "bf16", 0, 0), (8, 2, 128, 16, "fp8", "bf16", 0, 0),
+    (8, 1, 128, 32, "fp8", "f16", 0, 0), (8, 1, 64, 32, "f16", "f16", 0, 0), (2, 2, 64, 16, "fp8", "bf16", 0, 0),
+    (8, 2, 128, 8, "bf16", "bf16", 1, 0), (2, 2, 128, 16, "f16", "f16", 16, 4), (8, 2, 128, 32, "fp8", "bf16", 33, 40),
+    (8, 1, 64, 8, "fp8", "f16", 7, 9), (4, 2, 128, 8, "bf16", "bf16", 100, 1), (8, 4, 128, 16, "fp8", "f16", 2, 200),
+    (4, 1, 128, 16, "f16", "f16", 2 ** 31 - 1, 2 ** 31 - 1), (1, 1, 64, 8, "bf16", "bf16", 64, 64)])
+def test_up_to_three_groups_of_eight_rows(rows, hq, hkv, d, bs, kv, model, window, sinks):
+    most = rows * hkv // hq
+    new = [min(n, i % (most + 1)) for i, n in enumerate(FEW_LENS, 1)]
+    new[-1] = most
+    run(Setup(FEW_LENS, hq, hkv, d, bs, kv, model, seed=rows + window % 89), new, window, sinks, most=most, few=True)
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,kv,model,lens,new,window,sinks", [
+    (8, 1, 128, 16, "fp8", "bf16", [40000, 77, 1], [2, 1, 1], 0, 0), (4, 4, 128, 8, "f16", "f16", [9000, 2049, 3], [8, 3, 1], 0, 0),
+    (8, 2, 64, 32, "bf16", "bf16", [20000, 19999], [6, 0], 0, 0), (8, 2, 128, 16, "fp8", "f16", [9001, 9000, 6100], [4, 1, 3], 5000, 70),
+    (2, 1, 128, 32, "bf16", "bf16", [8000, 3000], [12, 5], 2900, 1), (8, 1, 64, 8, "fp8", "bf16", [33333], [3], 0, 0)])
+def test_few_rows_over_many_splits(hq, hkv, d, bs, kv, model, lens, new, window, sinks):
+    run(Setup(lens, hq, hkv, d, bs, kv, model), new, window, sinks, few=True)
+
+
+@pytest.mark.parametrize("hq,hkv,kv,model,count", [(4, 1, "fp8", "bf16", 1100), (2, 2, "f16", "f16", 530), (8, 1, "bf16", "bf16", 257)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_few_rows_of_more_sequences_than_a_launch_takes(hq, hkv, kv, model, count, window):
+    lens = [(i * 37) % 90 for i in range(count)]
+    new = [min(n, (i * 5) % 3) for i, n in enumerate(lens)]
+    run(Setup(lens, hq, hkv, 64, 8, kv, model), new, window, 2 if window else 0, most=2, few=True)
+
+
+@pytest.mark.parametrize("hq,hkv,kv", [(8, 2, "fp8"), (4, 4, "f16")])
+def test_few_rows_on_streams_in_graphs_and_among_others(hq, hkv, kv):
+    lens, new = [5000, 4000, 3001], [2, 1, 2]
+    x, y = Setup(lens, hq, hkv, kv=kv), Setup([lens[0], 100, 2500], hq, hkv, kv=kv, width=313)
+    if kv == "fp8":
+        y.cache.set_scales(*x.scales)
+    P.paged_kv_append(y.cache, *(t[:5000] for t in x.given), y.slots[:5000])
+    cu, q, _ = chunks(x, new)
+    call = lambda z, q, out=None: P.paged_chunk_attention(q, z.cache, z.tables, z.context, cu, 2, 0.1, out=out)
+    assert x.tables.shape == y.tables.shape
+    assert torch.equal(call(x, q)[:2], call(y, q)[:2])  # the first sequence's rows do not depend on the others' lengths
+    qs = [torch.randn_like(q) for _ in range(4)]
+    want = [call(x, a) for a in qs]
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(q) for q in qs]
+    graphs = []
+    for a, o in zip(qs[2:], outs[2:]):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(x, a, o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                call(x, qs[i], outs[i]) if i < 2 else graphs[i - 2].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want)) and x.cache.check_error() == 0
+
+
+@pytest.mark.parametrize("kv", ["f16", "fp8"])
+def test_few_rows_pass_over_blocks_that_are_none(kv):
+    """A bad entry in sight is reported and its tokens count for nothing; NaN keys reach the rows that see them."""
+    x = Setup([100, 64], 4, 2, kv=kv)
+    cu, q, q64 = chunks(x, [3, 2])
+    x.tables[0, 2] = x.nb + 3
+    out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, 3, R.scale_of(128))
+    assert x.cache.check_error() == 1
+    k, v = x.rows(0)
+    keep = np.r_[0:32, 48:100]
+    for r in range(3):
+        e = np.searchsorted(keep, 97 + r, side="right")
+        ref = R.attend(q64[r:r + 1], k[keep[:e]], v[keep[:e]], R.scale_of(128), [e - 1])
+        R.check(out[r:r + 1].double().cpu().numpy(), ref, "f16", p="f32")
+    x.tables[0, 2] = 0
+    x.spoil(1, [63])  # the last token: seen by the last row alone, and by its own tile's rows through V
+    out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, 3, R.scale_of(128))
+    assert out[4].isnan().all()
