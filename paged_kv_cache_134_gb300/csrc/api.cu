@@ -43,6 +43,15 @@ bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
     return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+// do n rows of na bytes, sa apart, share a byte with n rows of nb bytes, sb apart?  (Slices of one matrix do not; rows of
+// different strides whose extents meet count as if they did.)
+bool rows_overlap(const void *a, int64_t na, int64_t sa, const void *b, int64_t nb, int64_t sb, int64_t n) {
+    if (na == 0 || nb == 0 || !overlap(a, (n - 1) * sa + na, b, (n - 1) * sb + nb)) return false;
+    if (n == 1 || sa != sb || sa <= 0) return true;
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)), m = (d % sa + sa) % sa;
+    return m < na || m + nb > sa;
+}
+
 int check_device(const pkv_cache *c) {
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
@@ -529,6 +538,15 @@ int paged_kv_append_rotary(pkv_cache_t c, const void *q, int64_t q_stride, const
         return pkv_fail(PKV_EINVAL, "strides must be multiples of 8 elements");
     if (num_q_heads > 0 && num_tokens > 1 && q_out_stride < (int64_t)num_q_heads * c->head_dim)
         return pkv_fail(PKV_EINVAL, "q_out rows overlap");
+    if (num_q_heads > 0) {
+        const int64_t wq = (int64_t)num_q_heads * c->head_dim * 2, wk = (int64_t)c->num_kv_heads * c->head_dim * 2;
+        const int64_t so = q_out_stride * 2;
+        if ((!(q_out == q && (q_stride == q_out_stride || num_tokens == 1)) &&
+             rows_overlap(q_out, wq, so, q, wq, q_stride * 2, num_tokens)) ||
+            rows_overlap(q_out, wq, so, k, wk, k_stride * 2, num_tokens) ||
+            rows_overlap(q_out, wq, so, v, wk, v_stride * 2, num_tokens))
+            return pkv_fail(PKV_EINVAL, "q_out overlaps the inputs and is not q with q's stride");
+    }
     if (int r = check_device(c)) return r;
     RotaryLaunch r{q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, num_q_heads, block_tables, num_rows,
                    max_blocks_per_seq, seq_ids, positions, rotary_positions, num_tokens, rotary,

@@ -386,3 +386,43 @@ def test_few_rows_pass_over_blocks_that_are_none(kv):
     x.spoil(1, [63])  # the last token: seen by the last row alone, and by its own tile's rows through V
     out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, 3, R.scale_of(128))
     assert out[4].isnan().all()
+
+
+@pytest.mark.parametrize("kv", ["f16", "fp8", "int4"])
+def test_a_pool_of_more_than_four_gigabytes(kv):
+    """Blocks behind byte 2^32 of the pool: the appended rows and every path's output are those of a small pool."""
+    hq, hkv, d, bs = 16, 8, 128, 32
+    elem = {"f16": 2.0, "fp8": 1.0, "int4": (d + 8) / 2 / d}[kv]
+    block = int(2 * hkv * bs * d * elem)
+    count = (1 << 32) // block + 200
+    lens, new = [1500, 1000, 300], [200, 3, 1]
+    need = [(n + bs - 1) // bs for n in lens]
+    tables = torch.full((3, max(need)), -1, dtype=torch.int32)
+    order, at = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)), 0
+    for i, n in enumerate(need):
+        tables[i, :n] = order[at:at + n]
+        at += n
+    seq = torch.repeat_interleave(torch.arange(3), torch.tensor(lens)).to(torch.int32).cuda()
+    pos = torch.cat([torch.arange(n) for n in lens]).to(torch.int32).cuda()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = [torch.randn(sum(lens), h, d, generator=g, device="cuda").half() for h in (hq, hkv, hkv)]
+    q = torch.randn(sum(new), hq, d, generator=g, device="cuda").half()
+    context = torch.tensor(lens, dtype=torch.int32).cuda()
+    outs = []
+    for blocks, shift in ((200, 0), (count, count - 120)):
+        t = torch.where(tables >= 0, tables + shift, tables).to(torch.int32).cuda()
+        cache = P.KVCache(blocks, bs, hkv, d, kv_dtype=kv, model_dtype="f16")
+        if kv == "fp8":
+            cache.set_scales(torch.full((hkv,), 0.01).cuda(), torch.full((hkv,), 0.01).cuda())
+        o = [P.paged_kv_append_rotary(cache, *rows, t, seq, pos, P.Rotary(d))]
+        for w, s in ((400, 5), (5000, 0)):
+            o.append(P.paged_decode_attention_window(q[:3], cache, t, context, 0.1, w, sinks=s))
+            if kv == "int4":
+                continue
+            for n in (new, [3, 2, 1]):
+                cu = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32).cuda()
+                o.append(P.paged_chunk_attention(q[:sum(n)], cache, t, context, cu, max(n), 0.1, window=w, sinks=s))
+        assert cache.check_error() == 0
+        outs.append(o)
+        cache.close()
+    assert all(torch.equal(a, b) and a.isfinite().all() for a, b in zip(*outs))

@@ -246,3 +246,20 @@ def test_refusals():
     with pytest.raises(P.PagedKVError) as e:  # more rotated elements than the head has
         P.paged_kv_append_rotary(small, z, z, z, x.tables, x.seq, x.pos, r)
     assert e.value.status == -4
+
+
+@pytest.mark.parametrize("n", [1, 5])
+def test_outputs_over_the_inputs_are_refused_and_slices_of_one_matrix_are_not(n):
+    x, r = Case(n, 4, 2), P.Rotary(128)
+    wide = torch.zeros(n, 16, 128, dtype=torch.float16, device="cuda")  # q, k, v and the output side by side
+    wide[:, :4], wide[:, 4:6], wide[:, 6:8] = x.q, x.k, x.v
+    q, k, v = wide[:, :4], wide[:, 4:6], wide[:, 6:8]
+    call = lambda o, q=q: P.paged_kv_append_rotary(x.cache, q, k, v, x.tables, x.seq, x.pos, r, q_out=o)
+    want = call(None).clone()
+    for out in (wide[:, 2:6], wide[:, 3:7], wide[:, 5:9], wide[:, 1:5], wide.view(-1)[128:128 + n * 512].view(n, 4, 128)):
+        with pytest.raises(P.PagedKVError) as e:
+            call(out)
+        assert e.value.status == -1
+    assert torch.equal(call(wide[:, 8:12]), want) and torch.equal(call(wide[:, 12:]), want)
+    assert torch.equal(call(q), want)  # in place
+    assert x.cache.check_error() == 0

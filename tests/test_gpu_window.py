@@ -56,7 +56,8 @@ CASES = [
     (2, 2, 128, 16, "int4", "f16", 16, 4), (4, 2, 128, 8, "int4", "bf16", 1, 0), (8, 2, 64, 32, "int4", "f16", 33, 40),
     (8, 1, 128, 32, "int4", "bf16", 150, 1), (1, 1, 64, 8, "int4", "bf16", 7, 9), (8, 1, 64, 16, "int4", "f16", 64, 64),
     (8, 1, 128, 32, "fp8", "f16", 2 ** 31 - 1, 5), (4, 1, 128, 16, "int4", "f16", 2, 2 ** 31 - 1),
-    (8, 1, 128, 8, "fp8", "f16", 100, 70),
+    (8, 1, 128, 8, "fp8", "f16", 100, 70), (8, 1, 128, 16, "bf16", "bf16", 40, 3), (8, 1, 64, 8, "bf16", "bf16", 9, 0),
+    (8, 1, 128, 16, "fp8", "bf16", 77, 20),
 ]
 
 
@@ -76,7 +77,7 @@ def test_what_is_in_sight(hq, hkv, d, bs, kv, model, window, sinks):
 @pytest.mark.parametrize("hq,hkv,d,bs,kv,model,window,sinks", [
     (4, 4, 128, 16, "f16", "f16", 1500, 4), (8, 2, 128, 16, "bf16", "bf16", 2100, 100), (8, 1, 128, 32, "fp8", "bf16", 3001, 7),
     (2, 2, 64, 8, "bf16", "bf16", 999, 0), (2, 1, 64, 16, "f16", "f16", 4000, 1), (2, 2, 128, 16, "int4", "f16", 1500, 33),
-    (8, 1, 64, 32, "int4", "bf16", 4000, 0), (4, 2, 64, 8, "fp8", "f16", 2222, 9), (1, 1, 128, 16, "fp8", "bf16", 4096, 1)])
+    (8, 1, 64, 32, "int4", "bf16", 4000, 0), (4, 2, 64, 8, "fp8", "f16", 2222, 9), (1, 1, 128, 16, "fp8", "bf16", 4096, 1), (8, 1, 128, 8, "bf16", "bf16", 1800, 2)])
 def test_windows_of_several_splits(hq, hkv, d, bs, kv, model, window, sinks):
     x = Setup([5000, 1, window - 1, window, window + sinks, window + sinks + 1, 4097], hq, hkv, d, bs, kv, model)
     q, q64 = x.queries(len(x.lens))
