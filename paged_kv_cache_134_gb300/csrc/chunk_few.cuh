@@ -5,7 +5,9 @@
 //
 // decode_mma.cuh's kernel with C groups of eight columns: K and V tiles travel global -> shared -> register once and meet
 // every group there (an E4M3 code is widened once for all rows).  Bound by the bytes of the cache for one group and by the
-// tiles' chains beside it (scores, exponentials, products: eight to twelve warps an SM) for more.  P goes into the second
+// tiles' chains beside it (scores, exponentials, products: eight to twelve warps an SM) for more: 32 sequences of up to
+// 4096 tokens, 5 new ones, 32 fp16 heads 163 us (1.01 GB, 6.2 TB/s); 256 log-normal ones of up to 8192, 32/8 heads,
+// E4M3, 2 new tokens (one group) 101 us, 4 (two) 143 (455 MB).  P goes into the second
 // product as a pair hi + lo, of fp16 (2^-22; the largest weight at 2^14, so that weights stay normal numbers down to 2^-28
 // of it) or bf16 (2^-16), or as one fp16 (2^-11) where an E4M3 cache's outputs are bf16 (2^-8); scores, statistics, sums
 // and accumulators are fp32.  A tile is masked only where a row's end or its window's begin
@@ -16,7 +18,7 @@
 
 namespace pkv_mma {
 
-// new tokens of sequence s; 0 where its numbers make no sense
+// new tokens of sequence s; 0 where its numbers make no sense, or where it has more rows than this kernel's share
 PKV_DEV int new_tokens(const FewArgs &a, int s, bool report = false) {
     const int64_t st = a.cu[s], n = a.cu[s + 1] - st;
     if (st < 0 || n < 0 || st + n > a.total || n > a.max_seqlen) {
@@ -27,7 +29,7 @@ PKV_DEV int new_tokens(const FewArgs &a, int s, bool report = false) {
         if (report) set_error(a.err, PKV_DEVERR_LENGTH);
         return 0;
     }
-    return (int)n;
+    return n > a.most_rows >> a.lg_group ? 0 : (int)n;
 }
 PKV_DEV void report_row(const FewArgs &a, int s) { new_tokens(a, s, true); }
 PKV_DEV bool has_rows(const FewArgs &a, int s) { return new_tokens(a, s) > 0; }
@@ -57,19 +59,26 @@ PKV_DEV int64_t few_row(const FewArgs &a, int start, int kvh, int r) {
     return (int64_t)(start + (r >> a.lg_group)) * a.hq + (kvh << a.lg_group) + (r & (a.group - 1));
 }
 
+// A split's first partial row.  (A split's rows side by side, as its unit writes them; a row's splits side by side
+// instead: one sequence of 32768 tokens 29.4 us for 23.9, of 2047 15.2 for 12.8.)
+PKV_DEV int64_t few_room(const FewArgs &a, int s, int kvh, int j) {
+    return (((int64_t)s * a.hkv + kvh) * a.max_splits + j) * a.row_room;
+}
+
 // Joins one row's splits, 32 at a time in their order; a warp.  The partial rows of eight splits are on their way at once.
 template <int D, int MT>
-PKV_DEV void few_join(const FewArgs &a, int64_t row, int nsplit) {
+PKV_DEV void few_join(const FewArgs &a, int64_t room, int64_t row, int nsplit) {
     using M_ = ModelT<MT>;
     constexpr int N = D / 32, U = 8;
     using Vec = std::conditional_t<N == 4, float4, float2>;
     const int lane = threadIdx.x & 31;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + row * a.max_splits;
-    const float *o = a.ws_o + row * a.max_splits * D + lane * N;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml) + room;
+    const float *o = a.ws_o + room * D + lane * N;
+    const int64_t step = (int64_t)a.row_room * D;
     float M = -INFINITY, den = 0.f, acc[N] = {};
     for (int j0 = 0; j0 < nsplit; j0 += 32) {
         const int n = min(32, nsplit - j0);
-        const float2 v = lane < n ? __ldcg(ml + j0 + lane) : make_float2(-INFINITY, 0.f);
+        const float2 v = lane < n ? __ldcg(ml + (int64_t)(j0 + lane) * a.row_room) : make_float2(-INFINITY, 0.f);
         float top = v.x;
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -89,7 +98,7 @@ PKV_DEV void few_join(const FewArgs &a, int64_t row, int nsplit) {
             Vec x[U];
 #pragma unroll
             for (int i = 0; i < U; ++i)
-                if (j + i < n) x[i] = __ldcg(reinterpret_cast<const Vec *>(o + (int64_t)(j0 + j + i) * D));
+                if (j + i < n) x[i] = __ldcg(reinterpret_cast<const Vec *>(o + (j0 + j + i) * step));
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const float f = __shfl_sync(0xffffffffu, w, (j + i) & 31);
@@ -120,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) few_merge_kernel(const FewArgs a) {
     const int n = new_tokens(a, s), start = a.cu[s]; // (complete before the launch that this one follows began)
     const int nsplit = (sight_of<true>(a, s, row_len(a, s)).len + a.split_tokens - 1) / a.split_tokens;
     pdl_wait();
-    if (r < n << a.lg_group && nsplit > 1) few_join<D, MT>(a, few_row(a, start, kvh, r), nsplit);
+    if (r < n << a.lg_group && nsplit > 1) few_join<D, MT>(a, few_room(a, s, kvh, 0) + r, few_row(a, start, kvh, r), nsplit);
 }
 
 template <int D, int KV, int C>
@@ -152,10 +161,15 @@ __global__ void __launch_bounds__(kThreads, few_ctas<D, KV, C>()) few_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int bl = a.bs_log2, bs = 1 << bl;
     const uint32_t ring_u = smem_u32(smem + warp * ST * G_::kBytes);
-    pdl_wait();
+    // late: beside the kernel of the sequences of more rows, which lets this one in once it has itself waited for what came
+    // before; it fills the SMs as that one's CTAs leave them, and waits for it only before it exits.
+    if (!a.late) pdl_wait();
     list_units<true>(a, full, part, sm_tmp);
     const int nfull = full[a.num_seqs] * a.hkv, nunits = nfull + part[a.num_seqs] * a.hkv;
-    if ((int)blockIdx.x >= nunits) return;
+    if ((int)blockIdx.x >= nunits) {
+        if (a.late) pdl_wait();
+        return;
+    }
 
     // a unit's table entries and q rows on their way (rows without a query keep what was there: their columns are nobody's)
     auto stage = [&](const FewUnit &u, int *tb, char *qs) {
@@ -498,11 +512,12 @@ __global__ void __launch_bounds__(kThreads, few_ctas<D, KV, C>()) few_kernel(con
             const int r = i / (D / 4), d = i % (D / 4) * 4;
             const float4 v = *reinterpret_cast<const float4 *>(oacc + r * LD + d);
             const float den = ((J.l[0][r] + J.l[1][r]) + J.l[2][r]) + J.l[3][r];
-            const int64_t row = few_row(a, cur.start, cur.kvh, r);
             if (cur.nsplit > 1) {
-                if (d == 0) reinterpret_cast<float2 *>(a.ws_ml)[row * a.max_splits + cur.j] = make_float2(J.M[r], den);
-                *reinterpret_cast<float4 *>(a.ws_o + (row * a.max_splits + cur.j) * D + d) = v;
+                const int64_t part_row = few_room(a, cur.s, cur.kvh, cur.j) + r;
+                if (d == 0) reinterpret_cast<float2 *>(a.ws_ml)[part_row] = make_float2(J.M[r], den);
+                *reinterpret_cast<float4 *>(a.ws_o + part_row * D + d) = v;
             } else {
+                const int64_t row = few_row(a, cur.start, cur.kvh, r);
                 const float inv = den == 0.f ? 0.f : 1.f / den;
                 *reinterpret_cast<uint2 *>(static_cast<char *>(a.out) + (row * D + d) * 2) =
                     den == 0.f ? make_uint2(0u, 0u) : make_uint2(M_::pack(v.x * inv, v.y * inv), M_::pack(v.z * inv, v.w * inv));
@@ -512,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, few_ctas<D, KV, C>()) few_kernel(con
         if (!more) break;
         ui = un;
     }
+    if (a.late) pdl_wait();
     pdl_trigger();
 }
 
@@ -533,7 +549,7 @@ cudaError_t launch_few_t(const FewArgs &a, int sms, cudaStream_t st) {
 }
 template <int D, int KV, int MT>
 cudaError_t launch_few_d(const FewArgs &a, int sms, bool merge, cudaStream_t st) {
-    const int rows = a.max_seqlen << a.lg_group;
+    const int rows = min(a.most_rows >> a.lg_group, a.max_seqlen) << a.lg_group;
     if (merge)
         return pdl_launch(few_merge_kernel<D, MT>, dim3((unsigned)(a.num_seqs * a.hkv), (rows + kWarps - 1) / kWarps),
                           dim3(kThreads), 0, st, a);

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
     constexpr int kRows = FEW ? 64 : 128;        // rows of a pipeline in the Q tile
     extern __shared__ __align__(1024) uint8_t smem[];
 
-    pdl_trigger();
+    if (a.few_rows == 0) pdl_trigger();
     if (smem_u32(smem) & 1023u) return; // the swizzled tiles need 1024-byte alignment (always true)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // loaders 0 and 2, issuers 1 and 3, softmax 4-7 and 8-11 (FEW: 4-5 and 10-11), widening 12-13 and 14-15 (FEW: and 6-7, 8-9)
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     pdl_wait(); // from here on global memory that the stream's earlier kernels wrote is read
+    if (a.few_rows > 0) pdl_trigger(); // (few_kernel reads what the list's launch, too, had waited for)
 
     const int G = 1 << a.lg_group;
     auto fail = [&]() {

@@ -178,11 +178,12 @@ int few_split(const pkv_cache *c, int64_t units, int64_t cap, int ctas) {
 
 } // namespace
 
-// tokens that the new ones of a sequence can see together, at most
-static int64_t few_seen(const pkv_cache *c, const ChunkLaunch &p) {
+// tokens that the new ones of a sequence (rows at most) can see together, at most
+static int64_t few_seen(const pkv_cache *c, const ChunkLaunch &p, int rows) {
     const int64_t bs = c->block_size, cap = p.max_blocks * bs;
     if (p.window == 0) return cap;
-    return std::min<int64_t>(cap, (((int64_t)p.window + p.max_seqlen - 2 + bs - 1) / bs + 1 + ((int64_t)p.sinks + bs - 1) / bs) * bs);
+    const int64_t n = std::min(p.max_seqlen, rows / (p.num_q_heads / c->num_kv_heads));
+    return std::min<int64_t>(cap, ((p.window + n - 2 + bs - 1) / bs + 1 + ((int64_t)p.sinks + bs - 1) / bs) * bs);
 }
 static int few_seqs(const pkv_cache *c, int num_seqs) { // of a launch (the list of more would leave room for one CTA an SM less)
     return std::min(num_seqs, c->kv_dtype == PKV_FP8_E4M3 ? pkv_mma::kMaxSeqs : 256);
@@ -193,48 +194,55 @@ static int few_seqs(const pkv_cache *c, int num_seqs) { // of a launch (the list
 // 8 rows 95 us, tcgen05 168, 16 rows 148 and 174, 24 rows 190 and 178; bf16 8 rows 159 and 191, 16 rows 203 and 197.  The
 // same under a window of 511: E4M3 16 rows 78 and 121, 24 rows 104 and 123, bf16 16 rows 99 and 154; 8 sequences of 4096,
 // 24 rows: E4M3 30 and 46, bf16 35 and 50.)
-bool chunk_is_few(const pkv_cache *c, const ChunkLaunch &p) {
-    const int64_t rows = (int64_t)p.max_seqlen * (p.num_q_heads / c->num_kv_heads);
-    if (rows > 24) return false;
-    const int64_t parts = (few_seen(c, p) + kFewSplit - 1) / kFewSplit;
-    return rows <= (c->kv_dtype == PKV_FP8_E4M3 ? 16 : 8) || parts <= 1 ||
-           (int64_t)few_seqs(c, p.num_seqs) * c->num_kv_heads * parts <= 8 * (int64_t)c->num_sms;
+int chunk_few_rows(const pkv_cache *c, const ChunkLaunch &p) {
+    const int64_t parts = (few_seen(c, p, 24) + kFewSplit - 1) / kFewSplit;
+    const bool some = parts <= 1 || (int64_t)few_seqs(c, p.num_seqs) * c->num_kv_heads * parts <= 8 * (int64_t)c->num_sms;
+    return some ? 24 : c->kv_dtype == PKV_FP8_E4M3 ? 16 : 8;
 }
 
-int64_t few_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens, int hq, int max_blocks) {
+static int few_plan(const pkv_cache *c, const ChunkLaunch &p, int rows, pkv_mma::FewArgs *a) {
+    const int G = p.num_q_heads / c->num_kv_heads;
+    const int64_t seen = few_seen(c, p, rows);
+    a->most_rows = rows;
+    a->row_room = std::min(p.max_seqlen, rows / G) * G;
+    a->split_tokens = few_split(c, (int64_t)few_seqs(c, p.num_seqs) * c->num_kv_heads, seen,
+                                c->kv_dtype == PKV_FP8_E4M3 && std::min<int64_t>(rows, (int64_t)p.max_seqlen * G) <= 8 ? 3 : 2);
+    a->max_splits = (int)std::max<int64_t>(1, (seen + a->split_tokens - 1) / a->split_tokens);
+    if (a->split_tokens / c->block_size > 8192)
+        return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this call takes", p.max_blocks);
+    return PKV_OK;
+}
+
+int64_t chunk_few_floats(const pkv_cache *c, const ChunkLaunch &p, int rows) {
+    pkv_mma::FewArgs a;
+    if (few_plan(c, p, rows, &a)) return 0;
+    return a.max_splits > 1 ? (int64_t)p.num_seqs * c->num_kv_heads * a.row_room * a.max_splits * (c->head_dim + 2) : 0;
+}
+
+int64_t few_workspace_floats(const pkv_cache *c, int num_seqs, int max_blocks) {
     // Rows of at most 24 a (sequence, KV head).  Splits: of at least 1024 tokens, or of at least 128 and so that a launch (of
     // 256 sequences at least, unless it is the only one) has two waves of units (3 CTAs an SM) and one a row more.
     const int64_t cap = (int64_t)max_blocks * c->block_size;
-    const int64_t rows = std::min<int64_t>(tokens * hq, (int64_t)num_seqs * c->num_kv_heads * 24);
+    const int64_t rows = (int64_t)num_seqs * c->num_kv_heads * 24;
     const int64_t waves = 24 * 2 * 3 * (int64_t)c->num_sms * ((num_seqs + 255) / 256);
     const int64_t most = std::min<int64_t>(rows * ((cap + 127) / 128), rows + waves);
     return std::max(most, rows * ((cap + 1023) / 1024)) * (c->head_dim + 2);
 }
 
-int chunk_few_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
-    const int G = p.num_q_heads / c->num_kv_heads, rows = p.max_seqlen * G;
-    const int64_t bs = c->block_size, cap = (int64_t)p.max_blocks * bs, seen = few_seen(c, p);
-    const bool fp8 = c->kv_dtype == PKV_FP8_E4M3;
-    const int per = few_seqs(c, p.num_seqs);
+int chunk_few_launch(pkv_cache *c, const ChunkLaunch &p, int rows, bool late, float *ws, bool merge, cudaStream_t st) {
+    const int G = p.num_q_heads / c->num_kv_heads, per = few_seqs(c, p.num_seqs);
     pkv_mma::FewArgs a;
     if (int r = pool_args(c, p.num_q_heads, &a)) return r;
-    a.split_tokens = few_split(c, (int64_t)per * c->num_kv_heads, seen, fp8 && rows <= 8 ? 3 : 2);
-    if (a.split_tokens / bs > 8192) return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this call takes", p.max_blocks);
-    a.max_splits = (int)std::max<int64_t>(1, (seen + a.split_tokens - 1) / a.split_tokens);
-    std::lock_guard<std::mutex> lk(c->ws_mu);
-    PkvWorkspace ws;
-    const int64_t partials = a.max_splits > 1 ? p.total_tokens * p.num_q_heads * a.max_splits : 0;
-    if (int r = pkv_stream_workspace(c, st, partials * (c->head_dim + 2), &ws)) return r;
+    if (int r = few_plan(c, p, rows, &a)) return r;
+    if (merge && a.max_splits == 1) return PKV_OK;
     a.q = p.q;
     a.out = p.out;
-    a.ws_o = ws.p;
-    a.ws_ml = ws.p + partials * c->head_dim;
     a.ws_x = nullptr;
     a.mass = nullptr;
     a.mass_len = -1;
     a.decay = 1.f;
     a.done = nullptr;
-    a.cap = cap;
+    a.cap = (int64_t)p.max_blocks * c->block_size;
     a.max_blocks = p.max_blocks;
     a.qk_scale_log2 = p.scale * 1.4426950408889634f;
     a.window = std::min(p.window, 1 << 30);
@@ -242,19 +250,23 @@ int chunk_few_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     a.total = p.total_tokens;
     a.max_seqlen = p.max_seqlen;
     a.lg_group = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
-    PkvTimer timer(c, PKV_KIND_PREFILL, st);
+    a.late = late;
     for (int s0 = 0; s0 < p.num_seqs; s0 += per) {
         a.num_seqs = std::min(per, p.num_seqs - s0);
         a.tables = p.tables ? p.tables + (int64_t)s0 * p.max_blocks : nullptr;
         a.lens = p.lens + s0;
         a.cu = p.cu + s0;
-        for (const bool merge : {false, true}) {
-            if (merge && a.max_splits == 1) break;
-            g_pkv_launches++;
-            const cudaError_t e = fp8 ? pkv_few_e4m3(a, c->model_dtype, c->head_dim, c->num_sms, merge, st)
-                                      : pkv_few_16bit(a, c->model_dtype, c->head_dim, c->num_sms, merge, st);
-            if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
+        if (a.max_splits > 1) { // (each launch has room of its own: none waits for the one before it)
+            const int64_t row = (int64_t)c->num_kv_heads * a.row_room * a.max_splits;
+            a.ws_o = ws + s0 * row * c->head_dim;
+            a.ws_ml = ws + p.num_seqs * row * c->head_dim + s0 * row * 2;
+        } else {
+            a.ws_o = a.ws_ml = nullptr;
         }
+        g_pkv_launches++;
+        const cudaError_t e = c->kv_dtype == PKV_FP8_E4M3 ? pkv_few_e4m3(a, c->model_dtype, c->head_dim, c->num_sms, merge, st)
+                                                          : pkv_few_16bit(a, c->model_dtype, c->head_dim, c->num_sms, merge, st);
+        if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
     }
     return PKV_OK;
 }

@@ -55,6 +55,9 @@ struct FewArgs : Args {
     const int32_t *cu; // rows of sequence s: [cu[s], cu[s + 1])
     int64_t total;     // rows of q
     int max_seqlen, lg_group;
+    int most_rows; // sequences of more rows a KV head are left aside
+    int row_room;  // rows that a (sequence, KV head) has room for in the workspace: ws_o, ws_ml by (s, kvh, split, row)
+    bool late;     // see few_kernel
 };
 
 // (the offset rides in the instruction: no address to compute)

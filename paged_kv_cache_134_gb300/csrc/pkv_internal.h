@@ -289,10 +289,11 @@ struct ChunkLaunch {
     float scale;
 };
 int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st);
-// few new tokens (decode_mma.cu)
-bool chunk_is_few(const pkv_cache *c, const ChunkLaunch &p);
-int chunk_few_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st);
-int64_t few_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens, int hq, int max_blocks);
+// few new tokens (decode_mma.cu): the most rows a KV head that chunk_few.cuh takes in a call, its workspace, its launches
+int chunk_few_rows(const pkv_cache *c, const ChunkLaunch &p);
+int64_t chunk_few_floats(const pkv_cache *c, const ChunkLaunch &p, int rows);
+int chunk_few_launch(pkv_cache *c, const ChunkLaunch &p, int rows, bool late, float *ws, bool merge, cudaStream_t st);
+int64_t few_workspace_floats(const pkv_cache *c, int num_seqs, int max_blocks); // no call of such sizes needs more
 int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens, int max_seqlen, int hq, int max_blocks);
 
 // Tiled-TMA map of a row-major fp16/bf16 matrix [rows][cols]: box = 64 columns x box_rows rows,

@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const Args a) {
     if (tok < st || tok >= en || st < 0 || en > a.total_tokens || en - st > a.max_seqlen ||
         (int64_t)a.lens[lo] > (int64_t)a.max_blocks * a.bs)
         return;
+    if (en - st <= a.few_rows >> a.lg_group) return;
     const int tile = (tok - st) / (BM >> a.lg_group);
     const int n = STREAM ? stream_unit(a, lo, tile, 0, 0).nsplit : chunk_splits(chunk_item(a, lo, tile / 2, 0, 0), tile & 1);
     if (n <= 1) return;
@@ -583,9 +584,18 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
 }
 
 template <bool STREAM>
-cudaError_t launch_chunk_t(pkv_cache *c, const Args &a, const Maps &m, int64_t ctas, cudaStream_t st) {
+cudaError_t launch_chunk_t(pkv_cache *c, const Args &a, const Maps &m, int64_t ctas, bool merge, cudaStream_t st) {
     const int D = c->head_dim, mt = c->model_dtype, smem = (2 * a.cost_bins + 32) * (int)sizeof(int);
     cudaError_t e;
+    if (merge) {
+        if (a.max_splits <= 1) return cudaSuccess;
+        const dim3 grid((unsigned)a.total_tokens, (unsigned)((a.hq + 3) / 4));
+        auto kern = D == 128 ? (mt == PKV_F16 ? chunk_merge_kernel<128, PKV_F16, STREAM> : chunk_merge_kernel<128, PKV_BF16, STREAM>)
+                             : (mt == PKV_F16 ? chunk_merge_kernel<64, PKV_F16, STREAM> : chunk_merge_kernel<64, PKV_BF16, STREAM>);
+        e = pdl_launch(kern, grid, dim3(128), 0, st, a);
+        g_pkv_launches++;
+        return e;
+    }
     if (a.plan) {
         static std::atomic<bool> allowed[64] = {};
         e = pkv_allow_smem(reinterpret_cast<const void *>(chunk_plan_kernel<STREAM>), allowed);
@@ -607,13 +617,18 @@ cudaError_t launch_chunk_t(pkv_cache *c, const Args &a, const Maps &m, int64_t c
                 : dispatch<MODE_CHUNK, false>(D, mt, m, a, ctas, c->num_sms, st);
     }
     g_pkv_launches++;
-    if (e != cudaSuccess || a.max_splits <= 1) return e;
-    const dim3 grid((unsigned)a.total_tokens, (unsigned)((a.hq + 3) / 4));
-    auto merge = D == 128 ? (mt == PKV_F16 ? chunk_merge_kernel<128, PKV_F16, STREAM> : chunk_merge_kernel<128, PKV_BF16, STREAM>)
-                          : (mt == PKV_F16 ? chunk_merge_kernel<64, PKV_F16, STREAM> : chunk_merge_kernel<64, PKV_BF16, STREAM>);
-    e = pdl_launch(merge, grid, dim3(128), 0, st, a);
-    g_pkv_launches++;
     return e;
+}
+
+// Sequences of up to so many rows a KV head are taken apart from the others, by chunk_few.cuh beside the tcgen05 kernel; 0:
+// none.  Where the longest piece is four times the mean one or more, as a batch of single tokens with a few pieces of prompts
+// has it.  (Window 1024, 32/8 heads, 64 sequences of 1 to 347 new tokens: bf16 140 us by one kernel, 134 by two,
+// 16 rows 136; one head a KV head 96 and 79; E4M3 133 and 107, 8 rows 115; 255 single tokens after 2048 and a piece of 128:
+// bf16 391 and 344, E4M3 539 and 264.  16 bf16 sequences of that window 51 and 56.)
+int rows_apart(const pkv_cache *c, const ChunkLaunch &p) {
+    const bool fp8 = c->kv_dtype == PKV_FP8_E4M3;
+    if (p.num_seqs < (fp8 ? 8 : 32) || (int64_t)p.num_seqs * p.max_seqlen < 4 * p.total_tokens) return 0;
+    return fp8 ? 16 : 8;
 }
 } // namespace
 
@@ -626,13 +641,24 @@ int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens,
     const int64_t partials = rows * splits + std::min<int64_t>(rows * steps, 2 * 256 * (int64_t)c->num_sms);
     const int64_t groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + 15) / 16), tokens / 16 + num_seqs);
     const int64_t items = groups * splits + std::min<int64_t>(groups * steps, 2 * (int64_t)c->num_sms);
-    const int64_t few = few_workspace_floats(c, num_seqs, tokens, hq, max_blocks);
-    return std::max((4 + 4 * items + 63) / 64 * 64 + partials * (c->head_dim + 2), few);
+    // (a call may take the sequences of few rows apart from the others)
+    return (4 + 4 * items + 63) / 64 * 64 + (partials * (c->head_dim + 2) + 63) / 64 * 64 +
+           few_workspace_floats(c, num_seqs, max_blocks);
 }
 
 int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
-    if (chunk_is_few(c, p)) return chunk_few_entry(c, p, st);
     const int hq = p.num_q_heads, D = c->head_dim, mt = c->model_dtype;
+    int few = chunk_few_rows(c, p);
+    if ((int64_t)p.max_seqlen * (hq / c->num_kv_heads) <= few) { // every sequence
+        std::lock_guard<std::mutex> lk(c->ws_mu);
+        PkvWorkspace ws;
+        if (int r = pkv_stream_workspace(c, st, chunk_few_floats(c, p, few), &ws)) return r;
+        PkvTimer timer(c, PKV_KIND_PREFILL, st);
+        for (const bool merge : {false, true})
+            if (int r = chunk_few_launch(c, p, few, false, ws.p, merge, st)) return r;
+        return PKV_OK;
+    }
+    few = rows_apart(c, p);
     const ChunkShape s = chunk_shape(c, p.num_seqs, p.total_tokens, p.max_seqlen, hq, p.max_blocks, p.window, p.sinks);
     if (s.items * c->num_kv_heads > 0x7FFFFFFF || p.total_tokens > 0x7FFFFFFF)
         return pkv_fail(PKV_EUNSUPPORTED, "too many rows for one call");
@@ -665,7 +691,8 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     m.k = m.v = m.pool;
     std::lock_guard<std::mutex> lk(c->ws_mu);
     PkvWorkspace ws;
-    if (int r = pkv_stream_workspace(c, st, s.floats(c, p.total_tokens, hq), &ws)) return r;
+    const int64_t floats = (s.floats(c, p.total_tokens, hq) + 63) / 64 * 64;
+    if (int r = pkv_stream_workspace(c, st, floats + (few ? chunk_few_floats(c, p, few) : 0), &ws)) return r;
     const bool direct = s.direct(c, p.num_seqs);
     a.plan = direct ? nullptr : reinterpret_cast<int *>(ws.p);
     a.max_groups = s.max_groups;
@@ -677,7 +704,12 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     a.ws_ml = a.ws_o + p.total_tokens * hq * s.max_splits * D;
     PkvTimer timer(c, PKV_KIND_PREFILL, st);
     const int64_t ctas = direct ? a.rect : s.items * c->num_kv_heads;
-    const cudaError_t e = s.stream ? launch_chunk_t<true>(c, a, m, ctas, st) : launch_chunk_t<false>(c, a, m, ctas, st);
-    if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
+    a.few_rows = few;
+    for (const bool merge : {false, true}) {
+        const cudaError_t e = s.stream ? launch_chunk_t<true>(c, a, m, ctas, merge, st) : launch_chunk_t<false>(c, a, m, ctas, merge, st);
+        if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
+        if (few)
+            if (int r = chunk_few_launch(c, p, few, true, ws.p + floats, merge, st)) return r;
+    }
     return PKV_OK;
 }

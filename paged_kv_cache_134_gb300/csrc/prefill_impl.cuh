@@ -82,6 +82,7 @@ struct Args {
     // `sinks` are attended to; log2 of the query heads per KV head; key tiles of a split, about
     const int32_t *lens = nullptr;
     int window = 0, sinks = 0, lg_group = 0, split_steps = 0;
+    int few_rows = 0; // sequences of at most so many rows a KV head are another kernel's (chunk_few.cuh)
     // without a list (plan NULL): row tiles (or pairs) of a sequence and splits (or pairs) of their keys, at most, and
     // sequences x those x KV heads
     int max_groups = 0, max_parts = 0, rect = 0;
@@ -410,6 +411,7 @@ PKV_DEV int chunk_groups(const Args &a, int i, bool report) {
         if (report) set_error(a.err, PKV_DEVERR_LENGTH);
         return 0;
     }
+    if (en - st <= a.few_rows >> a.lg_group) return 0;
     const int per = (PAIRS ? 2 : 1) * (BM >> a.lg_group);
     return (en - st + per - 1) / per;
 }
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
     constexpr int NKS = L::NKS, NVS = L::NVS;
     extern __shared__ __align__(1024) uint8_t smem[];
 
-    pdl_trigger();
+    if (!CHUNKED || a.few_rows == 0) pdl_trigger();
     if (smem_u32(smem) & 1023u) return; // the swizzled tiles need 1024-byte alignment (always true)
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::BAR);
@@ -570,6 +572,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
     // so it starts at once and fills the SMs the decode's CTAs leave, and waits for the decode only
     // before it exits (the merge after it then sees both).
     if constexpr (!CASCADE) pdl_wait();
+    if (CHUNKED && a.few_rows > 0) pdl_trigger(); // (few_kernel reads what the list's launch, too, had waited for)
 
     const int G = a.hq / a.hkv;
     auto make_item = [&](int seq, int pr, int h, int split) -> It {

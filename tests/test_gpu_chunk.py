@@ -426,3 +426,49 @@ def test_a_pool_of_more_than_four_gigabytes(kv):
         outs.append(o)
         cache.close()
     assert all(torch.equal(a, b) and a.isfinite().all() for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,kv,model,window,sinks,longest", [
+    (8, 2, 128, 16, "fp8", "bf16", 0, 0, 300), (8, 1, 128, 8, "fp8", "f16", 50, 7, 200), (4, 4, 64, 16, "f16", "f16", 0, 0, 400),
+    (8, 2, 128, 16, "bf16", "bf16", 333, 3, 300), (2, 2, 64, 8, "fp8", "bf16", 0, 0, 500), (8, 2, 128, 32, "bf16", "bf16", 0, 0, 130)])
+def test_few_rows_beside_many(hq, hkv, d, bs, kv, model, window, sinks, longest):
+    """Single tokens, drafted tokens and empty rows beside a few pieces of prompts: two kernels share the call."""
+    new = [longest, 1, 1, 0, 2, 1, 3, 4, 1, 8, 9, 1, 16, 17, 1, 2, 24, 25, 1, 1, 60, 1, 5, 1, 1, 1, 0, 1, 2, 1, 1, 33, 1, 1, 1, 1]
+    lens = [n + (i * 277) % 1900 for i, n in enumerate(new)]
+    lens[1], lens[10] = 1, 9
+    x = Setup(lens, hq, hkv, d, bs, kv, model, seed=longest)
+    assert len(new) * longest >= 4 * sum(new)
+    run(x, new, window, sinks)
+
+
+def test_few_rows_beside_many_on_streams_in_graphs_and_in_reserved_memory():
+    new = [200] + [1, 2, 3, 4, 1, 1, 2, 1] * 4
+    x = Setup([n + 3000 * (i % 3 == 0) for i, n in enumerate(new)], 8, 2, kv="fp8")
+    cu, q, _ = chunks(x, new)
+    call = lambda q, out: P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, 200, 0.1, out=out)
+    qs = [torch.randn_like(q) for _ in range(4)]
+    outs = [torch.empty_like(q) for _ in qs]
+    x.cache.reserve_chunk(len(new), sum(new), 200, 8, x.tables.shape[1])
+    free = torch.cuda.mem_get_info()[0]
+    call(qs[0], outs[0])
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] == free
+    want = []
+    for a, o in zip(qs, outs):
+        want.append(call(a, o).clone())
+    torch.cuda.synchronize()
+    graphs = []
+    for a, o in zip(qs[2:], outs[2:]):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(a, o)
+            o.mul_(1.0)  # (an ordinary kernel behind the call sees all of its rows)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].zero_()
+                call(qs[i], outs[i]).mul_(1.0) if i < 2 else graphs[i - 2].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want)) and x.cache.check_error() == 0
