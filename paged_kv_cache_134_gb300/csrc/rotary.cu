@@ -242,7 +242,7 @@ cudaError_t launch_t(const RotaryArgs &a, bool norm, bool interleaved, dim3 grid
 uint64_t turn_bits(double radians) {
     const double turns = radians * 0.15915494309189533577; // 1 / (2 pi)
     const double part = turns - std::floor(turns);
-    return part >= 1.0 ? 0 : (uint64_t)std::ldexp(part, 64);
+    return part >= 1.0 ? 0 : (uint64_t)(part * 18446744073709551616.0);
 }
 
 } // namespace
