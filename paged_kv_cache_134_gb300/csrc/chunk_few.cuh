@@ -7,9 +7,9 @@
 // every group there (an E4M3 code is widened once for all rows).  Bound by the bytes of the cache for one group and by the
 // tiles' chains beside it (scores, exponentials, products: eight to twelve warps an SM) for more: 32 sequences of up to
 // 4096 tokens, 5 new ones, 32 fp16 heads 163 us (1.01 GB, 6.2 TB/s); 256 log-normal ones of up to 8192, 32/8 heads,
-// E4M3, 2 new tokens (one group) 101 us, 4 (two) 143 (455 MB).  P goes into the second
-// product as a pair hi + lo, of fp16 (2^-22; the largest weight at 2^14, so that weights stay normal numbers down to 2^-28
-// of it) or bf16 (2^-16), or as one fp16 (2^-11) where an E4M3 cache's outputs are bf16 (2^-8); scores, statistics, sums
+// E4M3, 2 new tokens (one group) 99 us, 4 (two) 131 (455 MB).  P goes into the second
+// product as a pair hi + lo, of fp16 (2^-22; weights of the base at 2^6 and at most at 2^14, so that they stay normal numbers down to
+// 2^-20 of it) or bf16 (2^-16), or as one fp16 (2^-11) where an E4M3 cache's outputs are bf16 (2^-8); scores, statistics, sums
 // and accumulators are fp32.  A tile is masked only where a row's end or its window's begin
 // crosses it.  The four warps' sums meet in one buffer, added in turn (four barriers for four times the memory).
 #pragma once
@@ -146,7 +146,10 @@ __global__ void __launch_bounds__(kThreads, few_ctas<D, KV, C>()) few_kernel(con
     constexpr int KS = D / 16; // k steps of the first product = m tiles of the second
     constexpr int ST = G_::kStages, R = 8 * C, LD = D + 4;
     constexpr bool PAIR = OT == PKV_BF16 || MT == PKV_F16; // (one fp16 weight would add 2^-11 to fp16 outputs' own)
-    constexpr float kUp = OT == PKV_BF16 ? 0.f : 14.f; // log2 of the largest weight
+    // A row's weights stand against a base that moves only when a score passes it by 2^kPast, to 2^kUp: few tiles move it,
+    // and with it every sum, though sixteen rows have a new maximum in most (moving with every maximum: 143 us for 131 of
+    // the E4M3 batch above).
+    constexpr float kPast = 8.f, kUp = OT == PKV_BF16 ? 0.f : 14.f - kPast;
     extern __shared__ __align__(128) char smem[];
     __shared__ struct {
         float m[kWarps][R], l[kWarps][R], M[R];
@@ -298,11 +301,11 @@ __global__ void __launch_bounds__(kThreads, few_ctas<D, KV, C>()) few_kernel(con
             qs[c][1] = __shfl_sync(0xffffffffu, s, 8 * t4 + 4);
         }
 
-        float m[C][2], mu[C][2], l[C][2]; // running maxima; the finite numbers to subtract; sums
+        float m[C][2], mu[C][2], lim[C][2], l[C][2]; // bases; the finite numbers to subtract; where they move; sums
         float acc[C][KS][4];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            m[c][0] = m[c][1] = -INFINITY;
+            m[c][0] = m[c][1] = lim[c][0] = lim[c][1] = -INFINITY;
             mu[c][0] = mu[c][1] = l[c][0] = l[c][1] = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) acc[c][k][0] = acc[c][k][1] = acc[c][k][2] = acc[c][k][3] = 0.f;
@@ -371,10 +374,10 @@ __global__ void __launch_bounds__(kThreads, few_ctas<D, KV, C>()) few_kernel(con
                     }
             }
 
-            // ---- running maxima (move rarely: one vote a tile)
+            // ---- bases (one vote a tile)
             bool up = false;
 #pragma unroll
-            for (int c = 0; c < C; ++c) up = up || fmaxf(x[c][0], x[c][2]) > m[c][0] || fmaxf(x[c][1], x[c][3]) > m[c][1];
+            for (int c = 0; c < C; ++c) up = up || fmaxf(x[c][0], x[c][2]) > lim[c][0] || fmaxf(x[c][1], x[c][3]) > lim[c][1];
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
@@ -384,10 +387,11 @@ __global__ void __launch_bounds__(kThreads, few_ctas<D, KV, C>()) few_kernel(con
                         float n = fmaxf(x[c][e], x[c][e + 2]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
-                        n = fmaxf(n, m[c][e]);
+                        n = n > lim[c][e] ? n : m[c][e]; // (whatever the other rows do, which may be nobody's)
                         f[e] = m[c][e] == n ? 1.f : fast_exp2(m[c][e] - n);
                         m[c][e] = n;
                         mu[c][e] = n == -INFINITY ? 0.f : n - kUp;
+                        lim[c][e] = n + kPast;
                         l[c][e] *= f[e];
                     }
 #pragma unroll

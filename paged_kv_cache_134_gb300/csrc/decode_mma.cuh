@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
     using O = ModelT<OT>;
     constexpr int KS = D / 16; // k steps of the first product = m tiles of the second
     constexpr int ST = G_::kStages;
-    constexpr float kUp = OT == PKV_F16 ? 14.f : 0.f; // log2 of the largest weight
+    // Without mass the base moves only when a score passes it by 2^kPast, and with it every sum (see chunk_few.cuh).
+    constexpr float kPast = MASS ? 0.f : 8.f;
+    constexpr float kUp = OT == PKV_F16 ? 14.f - kPast : 0.f; // log2 of the base's weight (the largest: 2^14)
     extern __shared__ __align__(128) char smem[];
     __shared__ Join J;
     __shared__ int sm_tmp[2 * kWarps];
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, KV>::kCtas) decode_mass_kerne
             }
 
             // ---- running maximum (moves rarely: one vote a tile)
-            if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > m0 || fmaxf(x[1], x[3]) > m1)) {
+            if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > m0 + kPast || fmaxf(x[1], x[3]) > m1 + kPast)) {
                 float n0 = fmaxf(x[0], x[2]), n1 = fmaxf(x[1], x[3]);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
