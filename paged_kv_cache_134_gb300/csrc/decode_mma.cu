@@ -191,9 +191,9 @@ static int few_seqs(const pkv_cache *c, int num_seqs) { // of a launch (the list
 
 // Up to 24 rows of a KV head: by chunk_few.cuh, but where long sequences fill the SMs many times over only up to 16 (E4M3)
 // and 8; tcgen05 takes 64 rows in the time of one there.  (256 log-normal sequences of up to 8192 tokens, 32/8 heads, E4M3:
-// 8 rows 95 us, tcgen05 168, 16 rows 148 and 174, 24 rows 190 and 178; bf16 8 rows 159 and 191, 16 rows 203 and 197.  The
-// same under a window of 511: E4M3 16 rows 78 and 121, 24 rows 104 and 123, bf16 16 rows 99 and 154; 8 sequences of 4096,
-// 24 rows: E4M3 30 and 46, bf16 35 and 50.)
+// 8 rows 99 us, tcgen05 168, 16 rows 131 and 174, 24 rows 172 and 179, 4 to 24 of them 172 and 167; bf16 8 rows 157 and
+// 191, 16 rows 198 and 196, 24 rows 224 and 201.  The same under a window of 511: E4M3 16 rows 70 and 121, 24 rows 93 and
+// 123, bf16 16 rows 96 and 154; 8 sequences of 4096, 24 rows: E4M3 26 and 46, bf16 34 and 50.)
 int chunk_few_rows(const pkv_cache *c, const ChunkLaunch &p) {
     const int64_t parts = (few_seen(c, p, 24) + kFewSplit - 1) / kFewSplit;
     const bool some = parts <= 1 || (int64_t)few_seqs(c, p.num_seqs) * c->num_kv_heads * parts <= 8 * (int64_t)c->num_sms;
