@@ -7,6 +7,7 @@ namespace {
 
 constexpr int kMaxSplit = 1024; // tokens
 constexpr int kFewSplit = 1536; // of the chunk attention of few rows
+constexpr int64_t kFewFloats = (int64_t)1 << 29; // partial rows of a launch of it
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -200,7 +201,8 @@ int chunk_few_rows(const pkv_cache *c, const ChunkLaunch &p) {
     return some ? 24 : c->kv_dtype == PKV_FP8_E4M3 ? 16 : 8;
 }
 
-static int few_plan(const pkv_cache *c, const ChunkLaunch &p, int rows, pkv_mma::FewArgs *a) {
+// (seqs: of a launch, whose partial rows take at most 2 GB unless one sequence's need more)
+static int few_plan(const pkv_cache *c, const ChunkLaunch &p, int rows, pkv_mma::FewArgs *a, int *seqs) {
     const int G = p.num_q_heads / c->num_kv_heads;
     const int64_t seen = few_seen(c, p, rows);
     a->most_rows = rows;
@@ -210,31 +212,35 @@ static int few_plan(const pkv_cache *c, const ChunkLaunch &p, int rows, pkv_mma:
     a->max_splits = (int)std::max<int64_t>(1, (seen + a->split_tokens - 1) / a->split_tokens);
     if (a->split_tokens / c->block_size > 8192)
         return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this call takes", p.max_blocks);
+    const int64_t floats = (int64_t)c->num_kv_heads * a->row_room * a->max_splits * (c->head_dim + 2);
+    *seqs = few_seqs(c, p.num_seqs);
+    if (a->max_splits > 1) *seqs = (int)std::max<int64_t>(1, std::min<int64_t>(*seqs, kFewFloats / floats));
     return PKV_OK;
 }
 
 int64_t chunk_few_floats(const pkv_cache *c, const ChunkLaunch &p, int rows) {
     pkv_mma::FewArgs a;
-    if (few_plan(c, p, rows, &a)) return 0;
-    return a.max_splits > 1 ? (int64_t)p.num_seqs * c->num_kv_heads * a.row_room * a.max_splits * (c->head_dim + 2) : 0;
+    int seqs;
+    if (few_plan(c, p, rows, &a, &seqs) || a.max_splits <= 1) return 0;
+    return (int64_t)seqs * c->num_kv_heads * a.row_room * a.max_splits * (c->head_dim + 2);
 }
 
 int64_t few_workspace_floats(const pkv_cache *c, int num_seqs, int max_blocks) {
-    // Rows of at most 24 a (sequence, KV head).  Splits: of at least 1024 tokens, or of at least 128 and so that a launch (of
-    // 256 sequences at least, unless it is the only one) has two waves of units (3 CTAs an SM) and one a row more.
-    const int64_t cap = (int64_t)max_blocks * c->block_size;
-    const int64_t rows = (int64_t)num_seqs * c->num_kv_heads * 24;
-    const int64_t waves = 24 * 2 * 3 * (int64_t)c->num_sms * ((num_seqs + 255) / 256);
-    const int64_t most = std::min<int64_t>(rows * ((cap + 127) / 128), rows + waves);
-    return std::max(most, rows * ((cap + 1023) / 1024)) * (c->head_dim + 2);
+    // Rows of at most 24 a (sequence, KV head).  Splits: of at least 1024 tokens, or of at least 128 and so that a launch
+    // has two waves of units (3 CTAs an SM) and one a row more.
+    const int64_t cap = (int64_t)max_blocks * c->block_size, per_seq = (int64_t)c->num_kv_heads * 24;
+    const int64_t rows = few_seqs(c, num_seqs) * per_seq;
+    const int64_t most = std::min<int64_t>(rows * ((cap + 127) / 128), rows + 24 * 2 * 3 * (int64_t)c->num_sms);
+    const int64_t floats = std::max(most, rows * ((cap + 1023) / 1024)) * (c->head_dim + 2);
+    return std::min(floats, std::max(kFewFloats, per_seq * ((cap + 127) / 128) * (c->head_dim + 2)));
 }
 
-int chunk_few_launch(pkv_cache *c, const ChunkLaunch &p, int rows, bool late, float *ws, bool merge, cudaStream_t st) {
-    const int G = p.num_q_heads / c->num_kv_heads, per = few_seqs(c, p.num_seqs);
+int chunk_few_launch(pkv_cache *c, const ChunkLaunch &p, int rows, bool late, float *ws, cudaStream_t st) {
+    const int G = p.num_q_heads / c->num_kv_heads;
+    int per;
     pkv_mma::FewArgs a;
     if (int r = pool_args(c, p.num_q_heads, &a)) return r;
-    if (int r = few_plan(c, p, rows, &a)) return r;
-    if (merge && a.max_splits == 1) return PKV_OK;
+    if (int r = few_plan(c, p, rows, &a, &per)) return r;
     a.q = p.q;
     a.out = p.out;
     a.ws_x = nullptr;
@@ -250,23 +256,21 @@ int chunk_few_launch(pkv_cache *c, const ChunkLaunch &p, int rows, bool late, fl
     a.total = p.total_tokens;
     a.max_seqlen = p.max_seqlen;
     a.lg_group = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
-    a.late = late;
+    const bool split = a.max_splits > 1;
+    a.ws_o = split ? ws : nullptr;
+    a.ws_ml = split ? ws + (int64_t)per * c->num_kv_heads * a.row_room * a.max_splits * c->head_dim : nullptr;
     for (int s0 = 0; s0 < p.num_seqs; s0 += per) {
         a.num_seqs = std::min(per, p.num_seqs - s0);
         a.tables = p.tables ? p.tables + (int64_t)s0 * p.max_blocks : nullptr;
         a.lens = p.lens + s0;
         a.cu = p.cu + s0;
-        if (a.max_splits > 1) { // (each launch has room of its own: none waits for the one before it)
-            const int64_t row = (int64_t)c->num_kv_heads * a.row_room * a.max_splits;
-            a.ws_o = ws + s0 * row * c->head_dim;
-            a.ws_ml = ws + p.num_seqs * row * c->head_dim + s0 * row * 2;
-        } else {
-            a.ws_o = a.ws_ml = nullptr;
+        a.late = late && s0 == 0; // (later launches wait for the merge before them, whose room they use)
+        for (int merge = 0; merge <= (split ? 1 : 0); ++merge) {
+            g_pkv_launches++;
+            const cudaError_t e = c->kv_dtype == PKV_FP8_E4M3 ? pkv_few_e4m3(a, c->model_dtype, c->head_dim, c->num_sms, merge, st)
+                                                              : pkv_few_16bit(a, c->model_dtype, c->head_dim, c->num_sms, merge, st);
+            if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
         }
-        g_pkv_launches++;
-        const cudaError_t e = c->kv_dtype == PKV_FP8_E4M3 ? pkv_few_e4m3(a, c->model_dtype, c->head_dim, c->num_sms, merge, st)
-                                                          : pkv_few_16bit(a, c->model_dtype, c->head_dim, c->num_sms, merge, st);
-        if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
     }
     return PKV_OK;
 }

@@ -292,7 +292,7 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st);
 // few new tokens (decode_mma.cu): the most rows a KV head that chunk_few.cuh takes in a call, its workspace, its launches
 int chunk_few_rows(const pkv_cache *c, const ChunkLaunch &p);
 int64_t chunk_few_floats(const pkv_cache *c, const ChunkLaunch &p, int rows);
-int chunk_few_launch(pkv_cache *c, const ChunkLaunch &p, int rows, bool late, float *ws, bool merge, cudaStream_t st);
+int chunk_few_launch(pkv_cache *c, const ChunkLaunch &p, int rows, bool late, float *ws, cudaStream_t st);
 int64_t few_workspace_floats(const pkv_cache *c, int num_seqs, int max_blocks); // no call of such sizes needs more
 int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens, int max_seqlen, int hq, int max_blocks);
 

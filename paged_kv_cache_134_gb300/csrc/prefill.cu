@@ -654,9 +654,7 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
         PkvWorkspace ws;
         if (int r = pkv_stream_workspace(c, st, chunk_few_floats(c, p, few), &ws)) return r;
         PkvTimer timer(c, PKV_KIND_PREFILL, st);
-        for (const bool merge : {false, true})
-            if (int r = chunk_few_launch(c, p, few, false, ws.p, merge, st)) return r;
-        return PKV_OK;
+        return chunk_few_launch(c, p, few, false, ws.p, st);
     }
     few = rows_apart(c, p);
     const ChunkShape s = chunk_shape(c, p.num_seqs, p.total_tokens, p.max_seqlen, hq, p.max_blocks, p.window, p.sinks);
@@ -708,8 +706,8 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     for (const bool merge : {false, true}) {
         const cudaError_t e = s.stream ? launch_chunk_t<true>(c, a, m, ctas, merge, st) : launch_chunk_t<false>(c, a, m, ctas, merge, st);
         if (e != cudaSuccess) return pkv_cuda_fail(e, "chunk attention launch");
-        if (few)
-            if (int r = chunk_few_launch(c, p, few, true, ws.p + floats, merge, st)) return r;
+        if (few && !merge)
+            if (int r = chunk_few_launch(c, p, few, true, ws.p + floats, st)) return r;
     }
     return PKV_OK;
 }

@@ -472,3 +472,13 @@ def test_few_rows_beside_many_on_streams_in_graphs_and_in_reserved_memory():
                 call(qs[i], outs[i]).mul_(1.0) if i < 2 else graphs[i - 2].replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want)) and x.cache.check_error() == 0
+
+
+@pytest.mark.parametrize("piece", [2, 260])
+def test_few_rows_in_several_launches_with_splits(piece):
+    """Launches that use the same room for their partial rows one after the other, alone and beside a piece of a prompt."""
+    lens = [(i * 37) % 90 + (3100 if i in (3, 250, 256, 299) else 0) for i in range(300)]
+    lens[7] = 4000
+    new = [min(n, (i * 5) % 3) for i, n in enumerate(lens)]
+    new[7] = piece
+    run(Setup(lens, 4, 4, 64, 8, "f16", "f16", width=700), new, few=piece == 2)
