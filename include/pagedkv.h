@@ -377,13 +377,14 @@ int paged_prefill_attention(const void *q, const void *k, const void *v, const i
  * overlapping; rows behind cu_seqlens[num_seqs] are left as they were.  Blocks that no row of a tile (128 / group
  * tokens) sees are not read.  scale finite and > 0.  cu_seqlens as for packed_prefill_attention; L_i above the tables'
  * tokens sets PKV_DEVERR_LENGTH.  The rows of a sequence with such numbers are left as they were.
- * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4), arithmetic as in paged_prefill_attention, or, for sequences of
- * up to 24 rows (n_i times group), as in paged_decode_attention_mass (an E4M3 cache's bf16 outputs: weights as one
- * fp16); results agree with paged_prefill_attention's for the same rows to its tolerance.  The query heads of a KV head share its keys, which are cut into splits where the rows are few:
- * boundaries depend on L_i, n_i, num_seqs, total_tokens, max_seqlen, max_blocks_per_seq, window and sinks.  A NaN or
- * infinity in V reaches the rows of its sequence whose tile of rows sees that token, also the earlier ones among them;
- * one in K only the rows that see it.  One to five launches.  Workspace: as for paged_decode_attention_mass, one per
- * stream and per capture. */
+ * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4), arithmetic as in paged_prefill_attention, or, for sequences
+ * of up to 24 rows (n_i times group), as in paged_decode_attention_mass (an E4M3 cache's bf16 outputs: weights as
+ * one fp16); results agree with paged_prefill_attention's for the same rows to its tolerance.  The query heads of a
+ * KV head share its keys, which are cut into splits where the rows are few: boundaries depend on L_i, n_i, num_seqs,
+ * total_tokens, max_seqlen, max_blocks_per_seq, window and sinks.  A NaN or infinity in V reaches the rows of its
+ * sequence whose tile of rows sees that token, also the earlier ones among them; one in K only the rows that see it.
+ * One to five launches, more for batches that one does not take.  Workspace: as for paged_decode_attention_mass, one
+ * per stream and per capture. */
 int paged_chunk_attention(const void *q, pkv_cache_t cache, const int32_t *block_tables, int max_blocks_per_seq,
                           const int32_t *context_lens, const int32_t *cu_seqlens, int num_seqs, int max_seqlen,
                           int64_t total_tokens, int num_q_heads, float scale, int window, int sinks, void *out,

@@ -3,15 +3,15 @@
 // out[r] = sum_t p_t V_t with p_t = softmax_t(scale * q_r . K_t) over the tokens t that row r sees: t <= p_r, and under a
 // window t > p_r - window or t < sinks; rows r = (new token r / G, head r % G) of a sequence's KV head.
 //
-// decode_mma.cuh's kernel with C groups of eight columns: K and V tiles travel global -> shared -> register once and meet
-// every group there (an E4M3 code is widened once for all rows).  Bound by the bytes of the cache for one group and by the
-// tiles' chains beside it (scores, exponentials, products: eight to twelve warps an SM) for more: 32 sequences of up to
-// 4096 tokens, 5 new ones, 32 fp16 heads 163 us (1.01 GB, 6.2 TB/s); 256 log-normal ones of up to 8192, 32/8 heads,
-// E4M3, 2 new tokens (one group) 99 us, 4 (two) 131 (455 MB).  P goes into the second
-// product as a pair hi + lo, of fp16 (2^-22; weights of the base at 2^6 and at most at 2^14, so that they stay normal numbers down to
-// 2^-20 of it) or bf16 (2^-16), or as one fp16 (2^-11) where an E4M3 cache's outputs are bf16 (2^-8); scores, statistics, sums
-// and accumulators are fp32.  A tile is masked only where a row's end or its window's begin
-// crosses it.  The four warps' sums meet in one buffer, added in turn (four barriers for four times the memory).
+// decode_mma.cuh's kernel with C groups of eight columns: K and V tiles travel global -> shared -> register once and
+// meet every group there (an E4M3 code is widened once for all rows).  Bound by the bytes of the cache for one group
+// and by the tiles' chains beside it (scores, exponentials, products: eight to twelve warps an SM) for more: 32
+// sequences of up to 4096 tokens, 5 new ones, 32 fp16 heads 163 us (1.01 GB, 6.2 TB/s); 256 log-normal ones of up to
+// 8192, 32/8 heads, E4M3, 2 new tokens (one group) 99 us, 4 (two) 131 (455 MB).  P goes into the second product as a
+// pair hi + lo, of fp16 (2^-22; weights of the base at 2^6 and at most at 2^14, so that they stay normal numbers down
+// to 2^-20 of it) or bf16 (2^-16), or as one fp16 (2^-11) where an E4M3 cache's outputs are bf16 (2^-8); scores,
+// statistics, sums and accumulators are fp32.  A tile is masked only where a row's end or its window's begin crosses
+// it.  The four warps' sums meet in one buffer, added in turn (four barriers for four times the memory).
 #pragma once
 
 #include "decode_mma.cuh"
