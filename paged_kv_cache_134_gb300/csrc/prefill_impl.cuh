@@ -368,7 +368,8 @@ PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
     it.trow = seq;
     const int before = max(a.lens[seq], 0) - it.n; // position of the first new token (negative: those rows see nothing)
     const int tok0 = 2 * pr * per_tile;
-    const int low = a.window > 0 ? max(before + tok0 - a.window + 1, 0) : 0; // first key of the first row's window
+    // first key of the first row's window (whose position less the window may leave 32 bits)
+    const int low = a.window > 0 && before + tok0 >= a.window ? before + tok0 - a.window + 1 : 0;
     it.from = it.skip = it.lo = it.hi = 0;
     if (low > a.sinks) {
         it.from = (a.sinks + a.bs - 1) >> a.lg_bs;
@@ -1270,10 +1271,10 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                         const int hidden = it.skip << a.lg_bs; // tokens between the sinks' blocks and the window's
                         const int plast = x.qpos0 + x.qlast - x.q0; // position of the tile's last row
                         const bool late = kbase + BN - 1 + hidden > x.qpos0;
-                        const bool early = a.window > 0 && plast - a.window + 1 - hidden > kbase;
+                        const bool early = a.window > 0 && plast >= a.window && plast - a.window + 1 - hidden > kbase;
                         if (late || early) {
                             const int upto = qpos + 1 - hidden - kbase;
-                            const int since = a.window > 0 ? qpos - a.window + 1 - hidden - kbase : 0;
+                            const int since = a.window > 0 && qpos >= a.window ? qpos - a.window + 1 - hidden - kbase : 0;
                             const int first = min(a.sinks, qpos + 1) - kbase;
                             // (a word of seen keys at a time: tested one by one against three bounds they cost 70 registers)
 #pragma unroll

@@ -1,0 +1,45 @@
+"""GPU tests at the edges of a step's operators (rotation with append, windowed decode, chunk attention): numbers at the
+ends of their types, workspaces, reservations, against 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_134_gb300 as P
+import seen_ref as R
+from seen_setup import MODEL, Setup
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+WIDEST = 2 ** 31 - 1
+
+
+def packed(new):
+    return torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32).cuda()
+
+
+def weights(x):
+    """How the weights enter the second product where a sequence has more than 24 rows a KV head."""
+    return dict(p="pair" if x.kv == "bf16" else "f16")
+
+
+@pytest.mark.parametrize("window", [WIDEST, WIDEST - 3, 2 ** 30, 10 ** 6])
+@pytest.mark.parametrize("hq,hkv,kv,model,lens,new", [
+    (4, 2, "f16", "f16", [40, 3, 20], [60, 40, 20]), (8, 1, "bf16", "bf16", [5, 1, 8], [12, 6, 8]),
+    (4, 2, "fp8", "bf16", [40, 3, 20], [60, 40, 20]), (4, 4, "f16", "f16", [300, 3, 200], [500, 140, 200]),
+    (8, 1, "bf16", "bf16", [150, 40, 100], [250, 90, 100]), (2, 2, "fp8", "f16", [300, 3, 200], [500, 140, 200])])
+def test_windows_of_any_length_over_sequences_shorter_than_their_chunk(hq, hkv, kv, model, lens, new, window):
+    """Rows before the first token see nothing; the others see all up to their own: position less window has 33 bits."""
+    x = Setup(lens, hq, hkv, kv=kv, model=model, seed=3)
+    q, q64 = x.queries(sum(new))
+    out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, packed(new), max(new), R.scale_of(x.d), window=window,
+                                  sinks=2)
+    assert x.cache.check_error() == 0
+    got, at = out.double().cpu().numpy(), 0
+    for i, (length, n) in enumerate(zip(lens, new)):
+        r = R.attend(q64[at:at + n], *x.rows(i), R.scale_of(x.d), list(range(length - n, length)), window, 2)
+        R.check(got[at:at + n], r, model, **weights(x))
+        assert (got[at:at + max(n - length, 0)] == 0).all()
+        at += n
