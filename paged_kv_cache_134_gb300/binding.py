@@ -225,7 +225,7 @@ class KVCache:
 
     def reserve_chunk(self, max_seqs: int, max_tokens: int, max_seqlen: int, max_q_heads: int, max_blocks_per_seq: int):
         """Allocate a workspace for paged_chunk_attention calls of at most these sizes, for one stream or stream capture."""
-        _check(lib().kv_cache_reserve_chunk(self.handle, int(max_seqs), int(max_tokens), int(max_seqlen),
+        _check(lib().kv_cache_reserve_chunk(self.handle, int(max_seqs), int(max_tokens), _c_int(max_seqlen),
                                             int(max_q_heads), int(max_blocks_per_seq)))
 
     def release_workspaces(self, graphs: bool = False):
@@ -541,6 +541,11 @@ def paged_decode_attention_window(q: torch.Tensor, cache: KVCache, block_tables:
     return out
 
 
+def _c_int(n):
+    """The nearest number a C int holds (ctypes would take its low 32 bits): for sizes that may be larger than need be."""
+    return min(max(int(n), -2 ** 31), 2 ** 31 - 1)
+
+
 def _window(window, sinks, least):
     window, sinks = int(window), int(sinks)
     if window < least or sinks < 0 or (window == 0 and sinks):
@@ -635,7 +640,7 @@ def paged_chunk_attention(q: torch.Tensor, cache: KVCache, block_tables: torch.T
         _take(cache, out, "out", cache.torch_dtype, 3)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    _check(lib().paged_chunk_attention(qp, cache.handle, tables, width, lens, cu, nseq, int(max_seqlen), T, hq,
+    _check(lib().paged_chunk_attention(qp, cache.handle, tables, width, lens, cu, nseq, _c_int(max_seqlen), T, hq,
                                        float(scale), window, sinks, out.data_ptr(), _stream()))
     return out
 

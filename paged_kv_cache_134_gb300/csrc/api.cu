@@ -430,6 +430,7 @@ int kv_cache_reserve_chunk(pkv_cache_t c, int max_seqs, int64_t max_tokens, int 
         return pkv_fail(PKV_EUNSUPPORTED, "num_q_heads / num_kv_heads not in {1, 2, 4, 8}");
     if (int r = check_device(c)) return r;
     if (!max_seqs || !max_tokens || !max_seqlen || !max_q_heads) return PKV_OK;
+    max_seqlen = (int)std::min<int64_t>(max_seqlen, max_tokens);
     return add_spare(c, chunk_workspace_floats(c, max_seqs, max_tokens, max_seqlen, max_q_heads, max_blocks_per_seq));
 }
 
@@ -689,6 +690,7 @@ int paged_chunk_attention(const void *q, pkv_cache_t c, const int32_t *block_tab
     if (c->kv_dtype == PKV_INT4) return pkv_fail(PKV_EUNSUPPORTED, "the chunk attention does not read 4-bit caches");
     if (!(scale > 0.f) || !std::isfinite(scale)) return pkv_fail(PKV_EINVAL, "scale must be finite and > 0");
     if (num_seqs == 0 || max_seqlen == 0 || total_tokens == 0) return PKV_OK;
+    max_seqlen = (int)std::min<int64_t>(max_seqlen, total_tokens); // (no piece of the call is longer)
     if (int r = check_decode(c, q, block_tables, max_blocks_per_seq, context_lens, num_q_heads, scale, out)) return r;
     if (!cu_seqlens) return pkv_fail(PKV_EINVAL, "NULL pointer");
     if (overlap(q, total_tokens * num_q_heads * c->head_dim * 2, out, total_tokens * num_q_heads * c->head_dim * 2))

@@ -566,7 +566,8 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
     // and 301).
     s.stream = max_seqlen <= per || (c->kv_dtype != PKV_FP8_E4M3 && tokens * G <= 2 * BM * (int64_t)num_seqs);
     const int group = s.stream ? per : 2 * per;
-    s.groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + group - 1) / group), tokens / group + num_seqs);
+    const int64_t most = ((int64_t)max_seqlen + group - 1) / group; // of a sequence
+    s.groups = std::min<int64_t>(num_seqs * most, tokens / group + num_seqs);
     int64_t keys = (int64_t)max_blocks * bs;
     if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + std::min(max_seqlen, group) + sinks + 2 * bs);
     const int64_t steps = std::max<int64_t>(1, (keys + BN - 1) / BN);
@@ -578,7 +579,7 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
     const int64_t share = (s.groups * c->num_kv_heads * steps + places - 1) / places;
     s.split_steps = (int)std::min(kMost, std::max(kLeast, share));
     s.max_splits = (int)((steps + s.split_steps - 1) / s.split_steps);
-    s.max_groups = (max_seqlen + group - 1) / group;
+    s.max_groups = (int)most;
     s.items = s.groups * s.max_splits;
     return s;
 }
@@ -606,7 +607,7 @@ cudaError_t launch_chunk_t(pkv_cache *c, const Args &a, const Maps &m, int64_t c
     }
     const bool kv8 = c->kv_dtype == PKV_FP8_E4M3;
     if constexpr (STREAM) {
-        const bool few = (a.max_seqlen << a.lg_group) <= 64;
+        const bool few = (int64_t)a.max_seqlen << a.lg_group <= 64;
         const int grid = (int)std::min<int64_t>(ctas, c->num_sms);
         e = kv8 ? (few ? launch_stream_any<true, true>(D, mt, m.q, m.pool, a, grid, st)
                        : launch_stream_any<true, false>(D, mt, m.q, m.pool, a, grid, st))
@@ -639,7 +640,7 @@ int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens,
     const int64_t steps = ((int64_t)max_blocks * c->block_size + BN - 1) / BN, splits = steps / 32 + 3;
     const int64_t rows = tokens * hq;
     const int64_t partials = rows * splits + std::min<int64_t>(rows * steps, 2 * 256 * (int64_t)c->num_sms);
-    const int64_t groups = std::min<int64_t>((int64_t)num_seqs * ((max_seqlen + 15) / 16), tokens / 16 + num_seqs);
+    const int64_t groups = std::min<int64_t>(num_seqs * (((int64_t)max_seqlen + 15) / 16), tokens / 16 + num_seqs);
     const int64_t items = groups * splits + std::min<int64_t>(groups * steps, 2 * (int64_t)c->num_sms);
     // (a call may take the sequences of few rows apart from the others)
     return (4 + 4 * items + 63) / 64 * 64 + (partials * (c->head_dim + 2) + 63) / 64 * 64 +
@@ -680,7 +681,7 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     a.plan_cap = s.items;
     a.cost_bins = 2 * std::max(s.split_steps, 1) + 2;
     Maps m;
-    const int G = hq / c->num_kv_heads, tile = s.stream && p.max_seqlen * G <= 64 ? 64 : BM;
+    const int G = hq / c->num_kv_heads, tile = s.stream && (int64_t)p.max_seqlen * G <= 64 ? 64 : BM;
     if (!make_group_map(&m.q, p.q, mt, p.total_tokens, hq, D, G, tile) ||
         (!s.stream && !make_group_map(&m.out, p.out, mt, p.total_tokens, hq, D, G)) || // (TMA stores of whole tiles)
         !(D == 128 && c->kv_dtype != PKV_FP8_E4M3 ? pkv_tmap_rows128_grouped(&m.pool, c->pool, mt, pool_rows, c->block_size)

@@ -43,3 +43,31 @@ def test_windows_of_any_length_over_sequences_shorter_than_their_chunk(hq, hkv, 
         R.check(got[at:at + n], r, model, **weights(x))
         assert (got[at:at + max(n - length, 0)] == 0).all()
         at += n
+
+
+@pytest.mark.parametrize("most", [2 ** 29, 2 ** 30, WIDEST, 2 ** 32, 2 ** 32 + 1])
+@pytest.mark.parametrize("hq,hkv,kv,new", [(8, 1, "f16", [20]), (4, 1, "bf16", [30, 2]), (2, 1, "f16", [100, 1, 40]),
+                                           (8, 1, "fp8", [20, 300]), (8, 2, "bf16", [3, 1]), (4, 4, "fp8", [1, 9])])
+def test_longest_piece_may_be_overstated(hq, hkv, kv, new, most):
+    """Any max_seqlen from the longest piece on, to the ends of its type and past it, gives the same rows."""
+    model = "bf16" if kv == "bf16" else "f16"
+    x = Setup([n + 77 * i for i, n in enumerate(new, 1)], hq, hkv, kv=kv, model=model)
+    q, q64 = x.queries(sum(new))
+    s = R.scale_of(x.d)
+    out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, packed(new), most, s)
+    assert x.cache.check_error() == 0
+    assert torch.equal(out, P.paged_chunk_attention(q, x.cache, x.tables, x.context, packed(new), sum(new), s))
+    got, at = out.double().cpu().numpy(), 0
+    for i, n in enumerate(new):
+        r = R.attend(q64[at:at + n], *x.rows(i), s, list(range(x.lens[i] - n, x.lens[i])))
+        R.check(got[at:at + n], r, model, **weights(x))
+        at += n
+
+
+def test_reservations_of_the_longest_pieces():
+    x = Setup([300], 8, 1)
+    for most in (WIDEST, 2 ** 40):
+        x.cache.reserve_chunk(1, 100, most, 8, x.tables.shape[1])
+    with pytest.raises(P.PagedKVError) as e:
+        x.cache.reserve_chunk(1, 100, -2 ** 40, 8, x.tables.shape[1])
+    assert e.value.status == -1
