@@ -377,7 +377,8 @@ int paged_prefill_attention(const void *q, const void *k, const void *v, const i
  * overlapping; rows behind cu_seqlens[num_seqs] are left as they were.  Blocks that no row of a tile (128 / group
  * tokens) sees are not read.  scale finite and > 0.  cu_seqlens as for packed_prefill_attention; L_i above the tables'
  * tokens sets PKV_DEVERR_LENGTH.  The rows of a sequence with such numbers are left as they were.
- * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4), arithmetic as in paged_prefill_attention, or, for sequences
+ * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4), arithmetic as in paged_prefill_attention (weights that are
+ * one fp16 to 2^-11, and to 2^-31 of the largest where they are less than 2^-20 of it), or, for sequences
  * of up to 24 rows (n_i times group), as in paged_decode_attention_mass (an E4M3 cache's bf16 outputs: weights as
  * one fp16); results agree with paged_prefill_attention's for the same rows to its tolerance.  The query heads of a
  * KV head share its keys, which are cut into splits where the rows are few: boundaries depend on L_i, n_i, num_seqs,

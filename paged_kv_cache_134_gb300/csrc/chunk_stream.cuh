@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
     using L = StreamLayout<D, KV8, FEW>;
     constexpr int OT = KV8 ? (int)PKV_F16 : MT;  // the products' operands
     constexpr int NP = OT == PKV_BF16 ? 2 : 1;   // P parts (bf16: hi + lo)
+    constexpr float kUp = OT == PKV_F16 ? kChunkUp : 0.f;
     constexpr int EB = KV8 ? 1 : 2;              // pool bytes per element
     constexpr bool GROUPED = D == 128 && !KV8;   // one box a block, [8 rows][half][8 rows][128 bytes] (see attn_kernel)
     constexpr bool SCALE_Q = KV8 && MT == PKV_BF16;
@@ -580,8 +581,8 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
                     }
                     const float mx = fmaxf(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], max3(mc[5], mc[6], mc[7]))) *
                                      sl; // scale > 0 keeps the order
-                    const bool up = mx > m_use + kRescale;
-                    const float m_new = up ? mx : m_use;
+                    const bool up = mx > m_use + (kRescale + kUp);
+                    const float m_new = up ? mx - kUp : m_use;
                     const float alpha = up ? fast_exp2(m_use - m_new) : 1.f;
                     m_use = m_new;
                     const float nbase = m_use == -INFINITY ? 0.f : -m_use; // a row with no live key yet keeps p = 0

@@ -55,6 +55,10 @@ constexpr int BN = 128;          // keys per tile (MMA N of Q K^T, K of P V)
 constexpr int kThreads = 384;    // 12 warps
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f; // log2 units
+// Chunks whose weights are fp16: a new base's weight is 2^kChunkUp and the largest 2^14, so that a weight stays a normal
+// number down to 2^-20 of the base's and is nothing only below 2^-31.  (With the base at 1 those of 4000 tokens at 2^-25.2 of
+// one token's came out as nothing, an output of 1e-4 as 0; over a long split that would be 2^-8 of the sum.)
+constexpr float kChunkUp = 14.f - kRescale;
 constexpr int kCodeOff = 16384;  // E4M3 codes of a stage: row r at stage + kCodeOff + r * D
 
 enum { MODE_PACKED = 0, MODE_PAGED = 1, MODE_CASCADE = 2, MODE_CHUNK = 3 };
@@ -480,6 +484,7 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
     constexpr bool CODES = KV8 && CHUNKED;         // widened by warps of their own (CodeLayout)
     constexpr int OT = CODES ? (int)PKV_F16 : MT;  // the products' operands
     constexpr int NP = OT == PKV_BF16 ? 2 : 1;     // P parts (bf16: hi + lo)
+    constexpr float kUp = CHUNKED && OT == PKV_F16 ? kChunkUp : 0.f;
     constexpr int EB = KV8 ? 1 : 2;                // pool bytes per element
     constexpr int NKS = L::NKS, NVS = L::NVS;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -1303,8 +1308,8 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                     }
                     const float mx = fmaxf(max3(mc[0], mc[1], mc[2]), max3(mc[3], mc[4], max3(mc[5], mc[6], mc[7]))) *
                                      sl; // scale > 0 keeps the order
-                    const bool up = mx > m_use + kRescale;
-                    const float m_new = up ? mx : m_use;
+                    const bool up = mx > m_use + (kRescale + kUp);
+                    const float m_new = up ? mx - kUp : m_use;
                     const float alpha = up ? fast_exp2(m_use - m_new) : 1.f;
                     m_use = m_new;
                     const float nbase = m_use == -INFINITY ? 0.f : -m_use; // a row with no live key yet keeps p = 0

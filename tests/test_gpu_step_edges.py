@@ -71,3 +71,44 @@ def test_reservations_of_the_longest_pieces():
     with pytest.raises(P.PagedKVError) as e:
         x.cache.reserve_chunk(1, 100, -2 ** 40, 8, x.tables.shape[1])
     assert e.value.status == -1
+
+
+@pytest.mark.parametrize("kv,model", [("f16", "f16"), ("fp8", "f16"), ("fp8", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("seqs,new,bits", [(10, 40, 25.2), (10, 100, 30.0), (3, 300, 25.2), (3, 300, 30.0), (16, 24, 30.0)])
+def test_many_small_weights_beside_a_large_one(seqs, new, bits, kv, model):
+    """One token of weight 1 whose value is 0, thousands of weight 2^-bits whose value is 1: the sum of the small ones is
+    the output.  Keys are not split (32 key tiles, as many row tiles as fill the SMs).
+
+    Tolerance: half a step of the output type; a weight as one fp16 2^-11 where it is a normal number, and an error of at
+    most 2^-31 of the base's where it is not (the base's own weight is 2^6 or more, and half a step of an fp16
+    subnormal 2^-25), as a bf16 pair 2^-16; exp2, sums and quotient 2^-18; the scores are exact but for a product of three
+    fp32 factors of about 25, 2 * 25 * 2^-23 in the exponent."""
+    d, bs, hkv, length = 64, 16, 32, 4000
+    md = MODEL[model]
+    blocks = length // bs
+    k = torch.zeros(length, hkv, d, dtype=md)
+    k[0, :, 0] = 32.0
+    v = torch.ones(length, hkv, d, dtype=md)
+    v[0] = 0
+    cache = P.KVCache(blocks, bs, hkv, d, kv_dtype=kv, model_dtype=model)
+    table = torch.randperm(blocks, generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    pos = torch.arange(length)
+    slots = table[pos // bs].long() * bs + pos % bs
+    P.paged_kv_append(cache, k.cuda(), v.cuda(), slots.cuda())
+    q = torch.zeros(seqs * new, hkv, d, dtype=md)
+    q[..., 0] = 1.0
+    scale = bits * np.log(2) / 32  # the first token's score, in log2 units: bits
+    tables = table[None].repeat(seqs, 1).contiguous().cuda()
+    lens = torch.full((seqs,), length, dtype=torch.int32).cuda()
+    out = P.paged_chunk_attention(q.cuda(), cache, tables, lens, packed([new] * seqs), new, scale)
+    assert cache.check_error() == 0
+    seen = np.tile(np.arange(length - new, length), seqs).astype(np.float64)  # tokens but the first that a row sees
+    small = 2.0 ** -(np.float64(np.float32(scale)) * 32 / np.log(2))
+    want = seen * small / (1 + seen * small)
+    lost = want * ((2.0 ** -16 if kv == "bf16" else 2.0 ** -11) + 2.0 ** -18 + 2 * 25 * 2.0 ** -23)
+    if kv != "bf16":
+        lost = lost + seen * 2.0 ** -31
+    half = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}[model]
+    tol = half * (want + lost) + lost + 2.0 ** -25
+    err = np.abs(out.double().cpu().numpy() - want[:, None, None]).max((1, 2))
+    assert (err <= tol).all(), (err / tol).max()
