@@ -554,6 +554,9 @@ struct ChunkShape {
     }
 };
 
+// Partial rows of a call: at most 2 GB of them.
+int64_t most_partials(const pkv_cache *c) { return ((int64_t)1 << 29) / (c->head_dim + 2); }
+
 ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max_seqlen, int hq, int max_blocks, int window,
                        int sinks) {
     ChunkShape s;
@@ -579,6 +582,13 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
     const int64_t share = (s.groups * c->num_kv_heads * steps + places - 1) / places;
     s.split_steps = (int)std::min(kMost, std::max(kLeast, share));
     s.max_splits = (int)((steps + s.split_steps - 1) / s.split_steps);
+    // Longer ones where the partial rows of so many would be more than a call may have: their room follows from the
+    // table's width, whatever the sequences hold (a piece of 8192 tokens, 64 heads, a table of 131072: 8.7 GB at 32).
+    const int64_t fit = std::max<int64_t>(1, most_partials(c) / (tokens * hq));
+    if (s.max_splits > fit) {
+        s.split_steps = (int)((steps + fit - 1) / fit);
+        s.max_splits = (int)((steps + s.split_steps - 1) / s.split_steps);
+    }
     s.max_groups = (int)most;
     s.items = s.groups * s.max_splits;
     return s;
@@ -638,8 +648,9 @@ int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens,
     // at most steps / 32 + 3, or as many more as fill the SMs: 2 SMs / (row tiles KV heads) of them, so that rows times
     // those stay below 2 SMs tiles of 256 rows.
     const int64_t steps = ((int64_t)max_blocks * c->block_size + BN - 1) / BN, splits = steps / 32 + 3;
-    const int64_t rows = tokens * hq;
-    const int64_t partials = rows * splits + std::min<int64_t>(rows * steps, 2 * 256 * (int64_t)c->num_sms);
+    // (and of at most most_partials)
+    const int64_t most = most_partials(c), rows = tokens > most ? most : std::min(tokens * hq, most);
+    const int64_t partials = std::min(most, rows * splits + std::min<int64_t>(rows * steps, 2 * 256 * (int64_t)c->num_sms));
     const int64_t groups = std::min<int64_t>(num_seqs * (((int64_t)max_seqlen + 15) / 16), tokens / 16 + num_seqs);
     const int64_t items = groups * splits + std::min<int64_t>(groups * steps, 2 * (int64_t)c->num_sms);
     // (a call may take the sequences of few rows apart from the others)
@@ -679,7 +690,7 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     a.split_steps = s.split_steps;
     a.max_splits = s.max_splits;
     a.plan_cap = s.items;
-    a.cost_bins = 2 * std::max(s.split_steps, 1) + 2;
+    a.cost_bins = std::min(2 * s.split_steps + 2, 16384); // (the longest splits of the widest tables count alike)
     Maps m;
     const int G = hq / c->num_kv_heads, tile = s.stream && (int64_t)p.max_seqlen * G <= 64 ? 64 : BM;
     if (!make_group_map(&m.q, p.q, mt, p.total_tokens, hq, D, G, tile) ||

@@ -112,3 +112,34 @@ def test_many_small_weights_beside_a_large_one(seqs, new, bits, kv, model):
     tol = half * (want + lost) + lost + 2.0 ** -25
     err = np.abs(out.double().cpu().numpy() - want[:, None, None]).max((1, 2))
     assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("kv,length", [("f16", 5000), ("f16", 70000), ("fp8", 30000)])
+def test_room_for_partial_rows_is_bounded_under_wide_tables(kv, length):
+    """A piece of 5000 tokens, a table for a million: the splits follow the table's width, their room stays at 2 GB."""
+    n, hq, hkv = 5000, 8, 1
+    x = Setup([length], hq, hkv, kv=kv, width=65536)
+    q, q64 = x.queries(n)
+    out = torch.empty_like(q)
+    cu = packed([n])
+    warm = Setup([300], hq, hkv, kv=kv)  # (loads the kernels)
+    P.paged_chunk_attention(q[:300], warm.cache, warm.tables, warm.context, packed([300]), 300, 0.1)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, n, R.scale_of(128), out=out)
+    torch.cuda.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] <= (2 << 30) + (64 << 20)
+    assert x.cache.check_error() == 0
+    rows = np.arange(3, n, 97)
+    r = R.attend(q64[rows], *x.rows(0), R.scale_of(128), length - n + rows)
+    R.check(out.double().cpu().numpy()[rows], r, "f16", **weights(x))
+
+
+@pytest.mark.parametrize("tokens,most", [(5000, 5000), (5000, 64), (2 ** 40, 5000)])
+def test_reservations_are_bounded_too(tokens, most):
+    x = Setup([300], 8, 1, width=65536)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    x.cache.reserve_chunk(1, tokens, most, 8, 65536)
+    assert free - torch.cuda.mem_get_info()[0] <= (2 << 30) + (64 << 20)
+    x.cache.close()
