@@ -554,8 +554,16 @@ struct ChunkShape {
     }
 };
 
-// Partial rows of a call: at most 2 GB of them.
-int64_t most_partials(const pkv_cache *c) { return ((int64_t)1 << 29) / (c->head_dim + 2); }
+// Partial rows of a call of so many (token, head) rows over tables of so many key tiles, at most: what splits of 32 tiles
+// need, or as many as fill the SMs (2 SMs / (row tiles KV heads) splits of tiles of at most 256 rows), and 2 GB.  A call
+// whose q has more rows than its sequences can take (rows behind the last one, that nobody asks for) would be
+// cut into more: it has few row tiles, but each split has room for all its rows.
+int64_t most_partials(const pkv_cache *c, int64_t rows, int64_t steps) {
+    const int64_t most = ((int64_t)1 << 29) / (c->head_dim + 2);
+    if (rows >= most) return most;
+    return std::min(most, rows * (steps / 32 + 3) + std::min<int64_t>(rows * steps, 2 * 256 * (int64_t)c->num_sms));
+}
+int64_t table_steps(const pkv_cache *c, int max_blocks) { return ((int64_t)max_blocks * c->block_size + BN - 1) / BN; }
 
 ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max_seqlen, int hq, int max_blocks, int window,
                        int sinks) {
@@ -584,7 +592,7 @@ ChunkShape chunk_shape(const pkv_cache *c, int num_seqs, int64_t tokens, int max
     s.max_splits = (int)((steps + s.split_steps - 1) / s.split_steps);
     // Longer ones where the partial rows of so many would be more than a call may have: their room follows from the
     // table's width, whatever the sequences hold (a piece of 8192 tokens, 64 heads, a table of 131072: 8.7 GB at 32).
-    const int64_t fit = std::max<int64_t>(1, most_partials(c) / (tokens * hq));
+    const int64_t fit = std::max<int64_t>(1, most_partials(c, tokens * hq, table_steps(c, max_blocks)) / (tokens * hq));
     if (s.max_splits > fit) {
         s.split_steps = (int)((steps + fit - 1) / fit);
         s.max_splits = (int)((steps + s.split_steps - 1) / s.split_steps);
@@ -644,13 +652,9 @@ int rows_apart(const pkv_cache *c, const ChunkLaunch &p) {
 } // namespace
 
 int64_t chunk_workspace_floats(const pkv_cache *c, int num_seqs, int64_t tokens, int max_seqlen, int hq, int max_blocks) {
-    // A call of fewer rows may be cut into more splits: what chunk_shape can make of any sizes up to these.  Splits are
-    // at most steps / 32 + 3, or as many more as fill the SMs: 2 SMs / (row tiles KV heads) of them, so that rows times
-    // those stay below 2 SMs tiles of 256 rows.
-    const int64_t steps = ((int64_t)max_blocks * c->block_size + BN - 1) / BN, splits = steps / 32 + 3;
-    // (and of at most most_partials)
-    const int64_t most = most_partials(c), rows = tokens > most ? most : std::min(tokens * hq, most);
-    const int64_t partials = std::min(most, rows * splits + std::min<int64_t>(rows * steps, 2 * 256 * (int64_t)c->num_sms));
+    // A call of fewer rows may be cut into more splits: what chunk_shape can make of any sizes up to these.
+    const int64_t steps = table_steps(c, max_blocks), splits = steps / 32 + 3;
+    const int64_t partials = most_partials(c, tokens > INT64_MAX / hq ? INT64_MAX : tokens * hq, steps);
     const int64_t groups = std::min<int64_t>(num_seqs * (((int64_t)max_seqlen + 15) / 16), tokens / 16 + num_seqs);
     const int64_t items = groups * splits + std::min<int64_t>(groups * steps, 2 * (int64_t)c->num_sms);
     // (a call may take the sequences of few rows apart from the others)

@@ -143,3 +143,25 @@ def test_reservations_are_bounded_too(tokens, most):
     x.cache.reserve_chunk(1, tokens, most, 8, 65536)
     assert free - torch.cuda.mem_get_info()[0] <= (2 << 30) + (64 << 20)
     x.cache.close()
+
+
+@pytest.mark.parametrize("hq,hkv,new,tokens,width", [(8, 1, [40], 1024, 8192), (8, 1, [40, 30], 3000, 4096), (4, 1, [200], 2000, 8192),
+                                                     (8, 2, [3, 2], 5000, 8192)])
+def test_a_padded_q_stays_within_its_reservation(hq, hkv, new, tokens, width):
+    """Rows of q behind the last sequence count for the workspace, not for the number of splits."""
+    x = Setup([3000 + 400 * i for i in range(len(new))], hq, hkv, width=width)
+    q, q64 = x.queries(tokens)
+    out, cu = torch.full_like(q, 9.0), packed(new)
+    P.paged_chunk_attention(q, Setup([20] * len(new), hq, hkv).cache, x.tables, x.context * 0, cu, max(new), 0.1)  # loads the kernels
+    x.cache.reserve_chunk(len(new), tokens, max(new), hq, width)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    P.paged_chunk_attention(q, x.cache, x.tables, x.context, cu, max(new), R.scale_of(128), out=out)
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] == free and x.cache.check_error() == 0
+    got, at = out.double().cpu().numpy(), 0
+    for i, n in enumerate(new):
+        r = R.attend(q64[at:at + n], *x.rows(i), R.scale_of(128), list(range(x.lens[i] - n, x.lens[i])))
+        R.check(got[at:at + n], r, "f16", **weights(x))
+        at += n
+    assert (got[at:] == 9).all()
