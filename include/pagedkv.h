@@ -192,8 +192,8 @@ typedef struct {
 
 /* paged_kv_append_at for the rows as the projections leave them: for each token j, q and k head rows are normed
  * (x * rsqrt(mean(x^2) + eps) * weight, where the weight, [head_dim] in the model dtype, is not NULL), rotated, and
- * rounded once to the model dtype; fp32 in between, angles exact to 2^-25 of a turn at every position.  q goes to q_out;
- * k and v to the slot of (block_tables, seq_ids[j], positions[j]) as paged_kv_append stores the rounded rows.
+ * rounded once to the model dtype; fp32 in between, angles to 2^-25 of a turn at every position (of frequencies up to
+ * 2^40 radians).  q goes to q_out; k and v to the slot of (block_tables, seq_ids[j], positions[j]) as paged_kv_append stores the rounded rows.
  * rotary_positions, when not NULL, are the positions of the rotation (after paged_kv_evict a token's place in the cache
  * and its position differ); may be negative.  A token without a slot is not stored, but its q_out is written.
  * q: [num_tokens][num_q_heads][head_dim], k, v: [num_tokens][num_kv_heads][head_dim], model dtype, tokens the

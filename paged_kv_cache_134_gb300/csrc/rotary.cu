@@ -7,7 +7,7 @@
 // fp32, rounded once to the model's type: q goes to q_out, k and v to their slots as paged_kv_append stores them (so
 // that a cache of few bits holds the codes of the k that the model's type holds, as the prefill that is given that k).
 //
-// The angle.  f_i comes as a 64-bit fraction of a turn, so p f_i modulo 2^64 is the angle modulo a turn, exactly:
+// The angle.  f_i comes as a 64-bit fraction of a turn, so p f_i modulo 2^64 is the angle modulo a turn (to 2^-31):
 // two integer multiplications, no reduction of large arguments, the same error at position 100000 as at 1 (the leading 32 bits
 // as a float, 2^-25 of a turn, then sincospif's own).  Nothing is read for it but the position, and a table of
 // cosines for 131072 positions would be 64 MB.
@@ -238,11 +238,19 @@ cudaError_t launch_t(const RotaryArgs &a, bool norm, bool interleaved, dim3 grid
     return pdl_launch(kern, grid, dim3(kThreads), 0, st, a);
 }
 
-// a fraction of a turn, modulo one, times 2^64
+// x modulo one, times 2^64, cut
+uint64_t part_bits(double x) {
+    const double part = std::fmod(x, 1.0); // (exact, of x's sign)
+    const uint64_t bits = (uint64_t)(std::fabs(part) * 18446744073709551616.0);
+    return part < 0 ? 0 - bits : bits;
+}
+// radians as a fraction of a turn, modulo one, times 2^64: 1 / (2 pi) is two doubles and the product keeps its rounding
+// error, so that 2^31 positions of it are right to 2^-31 of a turn for frequencies of up to 2^40.  (As one double product,
+// right to 2^-53 of the turns of a position, position 2^31 - 1 was off by 2^-25 of a turn at a frequency of 1 and by a whole one at 1e8.)
 uint64_t turn_bits(double radians) {
-    const double turns = radians * 0.15915494309189533577; // 1 / (2 pi)
-    const double part = turns - std::floor(turns);
-    return part >= 1.0 ? 0 : (uint64_t)(part * 18446744073709551616.0);
+    constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+    const double turns = radians * hi, rest = std::fma(radians, hi, -turns) + radians * lo;
+    return part_bits(turns) + part_bits(rest);
 }
 
 } // namespace

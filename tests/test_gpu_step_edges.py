@@ -1,5 +1,8 @@
 """GPU tests at the edges of a step's operators (rotation with append, windowed decode, chunk attention): numbers at the
 ends of their types, workspaces, reservations, against 64 bits."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -165,3 +168,42 @@ def test_a_padded_q_stays_within_its_reservation(hq, hkv, new, tokens, width):
         R.check(got[at:at + n], r, "f16", **weights(x))
         at += n
     assert (got[at:] == 9).all()
+
+
+TWO_PI = Fraction(2 * 3141592653589793238462643383279502884197169399375105820974944, 10 ** 60)
+
+
+def reduced(position, freq):
+    """position * freq radians, less whole turns, in [-pi, pi], rounded once."""
+    angle = position * Fraction(freq)
+    return float(angle - round(angle / TWO_PI) * TWO_PI)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_angles_of_far_positions(interleaved, sign):
+    """Angles against a product without rounding, at positions near 2^31 where the sine is small, so that its own rounding
+    does not hide them.
+
+    Tolerance: as in test_gpu_rotary.py, relative to |y_a| + |y_b| = 2: half a step of fp16 and 2^-20."""
+    freqs = [1.0, 0.1, 3.7, 100.7, 12345.678, 1e6 + 0.25, 7.3e9, 1.1e11]
+    pos = [WIDEST]
+    for f in freqs:  # for each frequency the four positions of the smallest sines, of two thousand
+        some = range(WIDEST - 2000, WIDEST)
+        pos += sorted(some, key=lambda p: abs(math.sin(reduced(p, f))))[:4]
+    n = len(pos)
+    x = torch.ones(n, 1, 64, dtype=torch.float16, device="cuda")
+    cache = P.KVCache(4, 16, 1, 64, kv_dtype="f16", model_dtype="f16")
+    seq, place = torch.zeros(n, dtype=torch.int32).cuda(), torch.arange(n, dtype=torch.int32).cuda()
+    tables = torch.arange(4, dtype=torch.int32)[None].cuda()
+    x[..., 8:16] = 0  # (pairs of halves: (1, 0) turns to (cos, sin))
+    if interleaved:
+        x[..., 0:16:2], x[..., 1:16:2] = 1, 0
+    r = P.Rotary.from_frequencies([sign * f for f in freqs], interleaved=interleaved)
+    got = P.paged_kv_append_rotary(cache, x, x, x, tables, seq, place, r,
+                                   rotary_positions=torch.tensor(pos, dtype=torch.int32).cuda()).double().cpu().numpy()[:, 0]
+    angle = np.array([[reduced(p, sign * f) for f in freqs] for p in pos])
+    a, b = (slice(0, 16, 2), slice(1, 16, 2)) if interleaved else (slice(0, 8), slice(8, 16))
+    for y, w in ((got[:, a], np.cos(angle)), (got[:, b], np.sin(angle))):
+        assert (np.abs(y - w) <= 2.0 ** -11 * (np.abs(w) + 2.0 ** -19) + 2.0 ** -19 + 2.0 ** -25).all(), np.abs(y - w).max(0)
+    assert (got[:, 16:] == 1).all()
