@@ -108,6 +108,12 @@ int kv_cache_reserve(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_b
 int kv_cache_reserve_mass(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq,
                           int64_t max_mass_len);
 
+/* Add a workspace for paged_decode_attention_window calls (any cache type) of at most max_seqs sequences,
+ * max_q_heads query heads, tables of max_blocks_per_seq entries, windows of max_window tokens and max_sinks
+ * sinks, as above. */
+int kv_cache_reserve_window(pkv_cache_t cache, int max_seqs, int max_q_heads, int max_blocks_per_seq, int max_window,
+                            int max_sinks);
+
 /* Add a workspace for paged_chunk_attention calls of at most max_seqs sequences, max_tokens new tokens in all,
  * max_seqlen of one sequence, max_q_heads query heads and tables of max_blocks_per_seq entries, as above. */
 int kv_cache_reserve_chunk(pkv_cache_t cache, int max_seqs, int64_t max_tokens, int max_seqlen, int max_q_heads,
@@ -232,7 +238,7 @@ int paged_decode_attention(const void *q, pkv_cache_t cache, const int32_t *bloc
  * are not read, and their table entries may be -1.  A window that reaches the sinks, or the first token, is
  * paged_decode_attention to its tolerance.  Lengths above the tables' tokens are cut to them and set PKV_DEVERR_LENGTH.
  * Every cache type.  Split boundaries depend on L_s, window, sinks, num_seqs and max_blocks_per_seq.  Workspace: as
- * for paged_decode_attention_mass, one per stream and per capture. */
+ * for paged_decode_attention_mass, one per stream and per capture (kv_cache_reserve_window). */
 int paged_decode_attention_window(const void *q, pkv_cache_t cache, const int32_t *block_tables,
                                   int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_q_heads,
                                   float scale, int window, int sinks, void *out, void *stream);
@@ -385,7 +391,7 @@ int paged_prefill_attention(const void *q, const void *k, const void *v, const i
  * total_tokens, max_seqlen, max_blocks_per_seq, window and sinks.  A NaN or infinity in V reaches the rows of its
  * sequence whose tile of rows sees that token, also the earlier ones among them; one in K only the rows that see it.
  * One to five launches, more for batches that one does not take.  Workspace: as for paged_decode_attention_mass, one
- * per stream and per capture. */
+ * per stream and per capture (kv_cache_reserve_chunk). */
 int paged_chunk_attention(const void *q, pkv_cache_t cache, const int32_t *block_tables, int max_blocks_per_seq,
                           const int32_t *context_lens, const int32_t *cu_seqlens, int num_seqs, int max_seqlen,
                           int64_t total_tokens, int num_q_heads, float scale, int window, int sinks, void *out,

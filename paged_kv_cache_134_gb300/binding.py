@@ -53,6 +53,7 @@ def lib() -> ctypes.CDLL:
         L.kv_cache_view.argtypes = [vp, ctypes.POINTER(vp), ctypes.POINTER(i64), ctypes.POINTER(i64)]
         L.kv_cache_reserve.argtypes = [vp, i32, i32, i32]
         L.kv_cache_reserve_mass.argtypes = [vp, i32, i32, i32, i64]
+        L.kv_cache_reserve_window.argtypes = [vp, i32, i32, i32, i32, i32]
         L.kv_cache_reserve_chunk.argtypes = [vp, i32, i64, i32, i32, i32]
         L.kv_cache_release_workspaces.argtypes = [vp, i32]
         L.kv_cache_check_error.argtypes = [vp, ctypes.POINTER(i32)]
@@ -222,6 +223,13 @@ class KVCache:
         stream or stream capture."""
         _check(lib().kv_cache_reserve_mass(self.handle, int(max_seqs), int(max_q_heads), int(max_blocks_per_seq),
                                            int(max_mass_len)))
+
+    def reserve_window(self, max_seqs: int, max_q_heads: int, max_blocks_per_seq: int, max_window: int, max_sinks: int = 0):
+        """Allocate a workspace for paged_decode_attention_window calls of at most these sizes, for one stream or stream
+        capture."""
+        window, sinks = _window(max_window, max_sinks, 1)
+        _check(lib().kv_cache_reserve_window(self.handle, int(max_seqs), int(max_q_heads), int(max_blocks_per_seq), window,
+                                             sinks))
 
     def reserve_chunk(self, max_seqs: int, max_tokens: int, max_seqlen: int, max_q_heads: int, max_blocks_per_seq: int):
         """Allocate a workspace for paged_chunk_attention calls of at most these sizes, for one stream or stream capture."""

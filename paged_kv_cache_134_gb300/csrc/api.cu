@@ -421,6 +421,18 @@ int kv_cache_reserve_mass(pkv_cache_t c, int max_seqs, int max_q_heads, int max_
     return add_spare(c, decode_mma_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq, max_mass_len));
 }
 
+int kv_cache_reserve_window(pkv_cache_t c, int max_seqs, int max_q_heads, int max_blocks_per_seq, int max_window,
+                            int max_sinks) {
+    if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");
+    if (max_seqs < 0 || max_q_heads < 0 || max_blocks_per_seq < 0 || max_sinks < 0)
+        return pkv_fail(PKV_EINVAL, "negative size");
+    if (max_window < 1) return pkv_fail(PKV_EINVAL, "window %d: window >= 1", max_window);
+    if (max_q_heads % c->num_kv_heads || (max_q_heads > 0 && !supported_group(max_q_heads / c->num_kv_heads)))
+        return pkv_fail(PKV_EUNSUPPORTED, "num_q_heads / num_kv_heads not in {1, 2, 4, 8}");
+    if (int r = check_device(c)) return r;
+    return add_spare(c, decode_window_workspace_floats(c, max_seqs, max_q_heads, max_blocks_per_seq, max_window, max_sinks));
+}
+
 int kv_cache_reserve_chunk(pkv_cache_t c, int max_seqs, int64_t max_tokens, int max_seqlen, int max_q_heads,
                            int max_blocks_per_seq) {
     if (!c) return pkv_fail(PKV_EINVAL, "cache is NULL");

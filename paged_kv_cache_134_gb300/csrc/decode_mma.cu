@@ -32,9 +32,9 @@ struct Plan {
 };
 
 // blocks of a sequence that a windowed query can see at most
-int window_blocks(const pkv_cache *c, const MmaDecodeLaunch &d) {
-    const int64_t bs = c->block_size, w = ((int64_t)d.window - 1 + bs - 1) / bs + 1, s = ((int64_t)d.sinks + bs - 1) / bs;
-    return (int)std::min<int64_t>(d.max_blocks, w + s);
+int window_blocks(const pkv_cache *c, int max_blocks, int window, int sinks) {
+    const int64_t bs = c->block_size, w = ((int64_t)window - 1 + bs - 1) / bs + 1, s = ((int64_t)sinks + bs - 1) / bs;
+    return (int)std::min<int64_t>(max_blocks, w + s);
 }
 
 // (window: max_blocks are those that a window shows)
@@ -291,9 +291,14 @@ int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, in
                     std::max<int64_t>((int64_t)1 << 29, 1024 * row * c->num_kv_heads + scores));
 }
 
+int64_t decode_window_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int window, int sinks) {
+    // (the decode's, of tables that hold what a window shows: its splits are no shorter and its launches of no more rows)
+    return decode_mma_workspace_floats(c, num_seqs, hq, window_blocks(c, max_blocks, window, sinks), -1);
+}
+
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st) {
     Plan p;
-    const int seen = d.window > 0 ? window_blocks(c, d) : d.max_blocks;
+    const int seen = d.window > 0 ? window_blocks(c, d.max_blocks, d.window, d.sinks) : d.max_blocks;
     if (!plan_for(c, d.num_seqs, d.num_q_heads, seen, d.mass_len, d.window > 0, &p))
         return pkv_fail(PKV_EUNSUPPORTED, "tables of %d blocks are wider than this decode takes", d.max_blocks);
     // a batch larger than one launch takes runs in consecutive launches that share the workspace: each

@@ -178,6 +178,7 @@ struct PkvWorkspace {
 int decode_mma_entry(pkv_cache *c, const MmaDecodeLaunch &d, const PkvWorkspace *fixed, cudaStream_t st);
 // the most that a call of at most these sizes asks for (mass_len -1: without mass)
 int64_t decode_mma_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int64_t mass_len);
+int64_t decode_window_workspace_floats(const pkv_cache *c, int num_seqs, int hq, int max_blocks, int window, int sinks);
 // The caller holds ws_mu until it has launched what uses the workspace (another thread's call on the stream may replace
 // it) (api.cu).
 int pkv_stream_workspace(pkv_cache *c, cudaStream_t st, int64_t floats, PkvWorkspace *ws);

@@ -207,3 +207,101 @@ def test_angles_of_far_positions(interleaved, sign):
     for y, w in ((got[:, a], np.cos(angle)), (got[:, b], np.sin(angle))):
         assert (np.abs(y - w) <= 2.0 ** -11 * (np.abs(w) + 2.0 ** -19) + 2.0 ** -19 + 2.0 ** -25).all(), np.abs(y - w).max(0)
     assert (got[:, 16:] == 1).all()
+
+
+def taken():
+    torch.cuda.synchronize()
+    free, total = torch.cuda.mem_get_info()
+    return total - free
+
+
+@pytest.mark.parametrize("kv", ["f16", "fp8", "int4"])
+def test_reserved_window_workspace_covers_smaller_calls(kv):
+    """No windowed call of at most the reserved sizes allocates, however its sight is split; graphs take one of their own."""
+    seqs, width, hkv, d, bs = 450, 3000, 2, 128, 8
+    q = torch.randn(seqs, 16, d, device="cuda").half()
+    tables = torch.zeros(seqs, width, dtype=torch.int32, device="cuda")
+    lens = torch.ones(seqs, dtype=torch.int32, device="cuda")
+    for reserved in (False, True):  # (the first cache's calls load the kernels)
+        cache = P.KVCache(1, bs, hkv, d, kv_dtype=kv, model_dtype="f16")
+        if reserved:
+            cache.reserve_window(seqs, 16, width, 9000, 300)
+        before = taken()
+        for n in (450, 1, 2, 3, 20, 101, 313):
+            for w in (3000, 5, 62, 333, 1200):
+                for hq in (16, 2, 4):
+                    for window, sinks in ((9000, 300), (1, 0), (100, 4), (1500, 0), (3100, 33), (5000, 300)):
+                        P.paged_decode_attention_window(q[:n, :hq].contiguous(), cache, tables[:n, :w].contiguous(),
+                                                        lens[:n].contiguous(), 1.0, window, sinks=sinks)
+        grown = taken() - before
+        assert grown == 0 if reserved else grown > 0
+        assert cache.check_error() == 0
+        cache.close()
+
+
+def test_reserved_window_workspace_is_used_and_small():
+    x = Setup([9000] * 7 + [1], 8, 2, width=8192)
+    q, _ = x.queries(8)
+    call = lambda out=None: P.paged_decode_attention_window(q, x.cache, x.tables, x.context, 0.1, 5000, sinks=3, out=out)
+    want, out = call(), torch.empty_like(q)
+    first = torch.cuda.CUDAGraph()  # (the process's first graph takes memory of the driver's)
+    with torch.cuda.graph(first):
+        call(out)
+    first.replay()
+    before = taken()
+    for _ in range(2):
+        x.cache.reserve_window(8, 8, 8192, 5000, 3)
+    reserved = taken()
+    assert reserved - before <= 32 << 20  # (what a window shows, not what the tables hold)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert torch.equal(call(out), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    out.zero_()
+    graph.replay()
+    assert taken() - reserved <= 2 << 20 and torch.equal(out, want)  # (a graph's own nodes)
+
+
+def test_window_reservations_refused():
+    cache = P.KVCache(4, 16, 2, 64, kv_dtype="f16", model_dtype="f16")
+    for bad in ((1, 2, 4, 0), (1, 2, 4, -5), (1, 2, 4, 8, -1)):
+        with pytest.raises(ValueError):
+            cache.reserve_window(*bad)
+    for bad, status in (((-1, 2, 4, 8), -1), ((1, -2, 4, 8), -1), ((1, 2, -4, 8), -1), ((1, 3, 4, 8), -4), ((1, 12, 4, 8), -4)):
+        with pytest.raises(P.PagedKVError) as e:
+            cache.reserve_window(*bad)
+        assert e.value.status == status
+    lib = P.lib()
+    assert lib.kv_cache_reserve_window(cache.handle, 1, 2, 4, 0, 0) == -1
+    assert lib.kv_cache_reserve_window(None, 1, 2, 4, 1, 0) == -1
+    before = taken()
+    cache.reserve_window(0, 2, 4, 8)
+    cache.reserve_window(1, 0, 4, 8)
+    assert taken() == before
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_reserved_chunk_workspace_covers_smaller_calls(kv):
+    """No chunk call of at most the reserved sizes allocates, whichever kernels take it, with padded rows or without."""
+    seqs, tokens, width, hkv, d, bs = 70, 700, 3000, 2, 128, 8
+    q = torch.randn(tokens, 16, d, device="cuda").to(torch.bfloat16)
+    tables = torch.zeros(seqs, width, dtype=torch.int32, device="cuda")
+    lens = torch.ones(seqs, dtype=torch.int32, device="cuda")
+    for reserved in (False, True):
+        cache = P.KVCache(1, bs, hkv, d, kv_dtype=kv, model_dtype="bf16")
+        if reserved:
+            cache.reserve_chunk(seqs, tokens, 300, 16, width)
+        before = taken()
+        for n in (70, 1, 2, 9, 33):
+            for new in ([1] * n, [300] + [1] * (n - 1), [24] + [2] * (n - 1), [40] * min(n, 9) + [0] * max(0, n - 9)):
+                for t in {sum(new), tokens}:
+                    for w in (3000, 17, 333):
+                        for hq in (16, 2, 8):
+                            for window in (0, 4000):
+                                P.paged_chunk_attention(q[:t, :hq].contiguous(), cache, tables[:n, :w].contiguous(),
+                                                        lens[:n].contiguous(), packed(new), max(new), 1.0, window=window)
+        grown = taken() - before
+        assert grown == 0 if reserved else grown > 0
+        assert cache.check_error() == 0
+        cache.close()
