@@ -378,7 +378,8 @@ int paged_prefill_attention(const void *q, const void *k, const void *v, const i
  * first: paged_kv_append_at, paged_kv_append_rotary); rows [cu_seqlens[i], cu_seqlens[i+1]) of q, n_i of them, are the
  * queries of its last n_i tokens.  Row r sits at position p = L_i - n_i + r:
  *   out[cu_i + r][h] = sum_t softmax_t(scale * q[cu_i + r][h] . K_t[g]) V_t[g],
- *   t <= p, and with window > 0 also t > p - window or t < sinks (window 0: no window, sinks 0),
+ *   t <= p, and with window > 0 also t > p - window or t < sinks (window 0: no window, sinks 0; at most 2^30 where tables
+ *   hold more),
  * g = h / group.  A row that sees nothing (p < 0) is zero.  q, out: [total_tokens][num_q_heads][head_dim], not
  * overlapping; rows behind cu_seqlens[num_seqs] are left as they were.  Blocks that no row of a tile (128 / group
  * tokens) sees are not read.  scale finite and > 0.  cu_seqlens as for packed_prefill_attention; L_i above the tables'

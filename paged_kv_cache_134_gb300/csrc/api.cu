@@ -703,6 +703,7 @@ int paged_chunk_attention(const void *q, pkv_cache_t c, const int32_t *block_tab
     if (!(scale > 0.f) || !std::isfinite(scale)) return pkv_fail(PKV_EINVAL, "scale must be finite and > 0");
     if (num_seqs == 0 || max_seqlen == 0 || total_tokens == 0) return PKV_OK;
     max_seqlen = (int)std::min<int64_t>(max_seqlen, total_tokens); // (no piece of the call is longer)
+    if (window >= (int64_t)max_blocks_per_seq * c->block_size) window = sinks = 0; // (no row has so many tokens before it)
     if (int r = check_decode(c, q, block_tables, max_blocks_per_seq, context_lens, num_q_heads, scale, out)) return r;
     if (!cu_seqlens) return pkv_fail(PKV_EINVAL, "NULL pointer");
     if (overlap(q, total_tokens * num_q_heads * c->head_dim * 2, out, total_tokens * num_q_heads * c->head_dim * 2))

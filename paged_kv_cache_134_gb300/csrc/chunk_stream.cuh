@@ -85,7 +85,7 @@ PKV_DEV StreamUnit stream_unit(const Args &a, int seq, int g, int split, int h) 
     const int per_tile = BM >> a.lg_group, start = a.cu[seq], n = a.cu[seq + 1] - start, q0 = g * per_tile;
     const int before = max(a.lens[seq], 0) - n; // position of the first new token (negative: those rows see nothing)
     const int p0 = before + q0;                 // of the tile's first row
-    const int low = a.window > 0 && p0 >= a.window ? p0 - a.window + 1 : 0; // (p0 - window may leave 32 bits)
+    const int low = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
     int skip = 0;
     u.from = u.lo = u.hi = 0;
     if (low > a.sinks) {
@@ -559,9 +559,9 @@ __global__ void __launch_bounds__(stream_threads<KV8>(), 1)
                     tc::wait_ld();
                     // seen key kbase + c is at most this row's position up to c = upto - 1, inside its window from c = since on,
                     // a sink below c = sink; only tiles on either edge of some row's sight
-                    if (kbase + BN - 1 + hidden > qfirst || (a.window > 0 && plast >= a.window && plast - a.window + 1 - hidden > kbase)) {
+                    if (kbase + BN - 1 + hidden > qfirst || (a.window > 0 && plast - a.window + 1 - hidden > kbase)) {
                         const int upto = qpos + 1 - hidden - kbase;
-                        const int since = a.window > 0 && qpos >= a.window ? qpos - a.window + 1 - hidden - kbase : 0;
+                        const int since = a.window > 0 ? qpos - a.window + 1 - hidden - kbase : 0;
                         const int sink = min(a.sinks, qpos + 1) - kbase;
 #pragma unroll
                         for (int w = 0; w < BN / 32; ++w) {

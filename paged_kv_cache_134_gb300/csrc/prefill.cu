@@ -674,8 +674,9 @@ int chunk_entry(pkv_cache *c, const ChunkLaunch &p, cudaStream_t st) {
     }
     few = rows_apart(c, p);
     const ChunkShape s = chunk_shape(c, p.num_seqs, p.total_tokens, p.max_seqlen, hq, p.max_blocks, p.window, p.sinks);
-    if (s.items * c->num_kv_heads > 0x7FFFFFFF || p.total_tokens > 0x7FFFFFFF)
+    if (s.items * c->num_kv_heads > 0x7FFFFFFF || p.total_tokens > 1 << 30)
         return pkv_fail(PKV_EUNSUPPORTED, "too many rows for one call");
+    if (p.window > 1 << 30) return pkv_fail(PKV_EUNSUPPORTED, "a window of more than 2^30 tokens in wider tables");
     const int64_t pool_rows = c->num_blocks * 2 * c->num_kv_heads * c->block_size;
     if (pool_rows > 0x7FFFFFFFLL) return pkv_fail(PKV_EUNSUPPORTED, "pools of more than 2^31 - 1 rows");
     Args a = base_args(c, p.scale);

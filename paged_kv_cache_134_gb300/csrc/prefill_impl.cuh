@@ -83,7 +83,8 @@ struct Args {
     float *ws_o = nullptr, *ws_ml = nullptr;
     int max_splits = 0, prefix_tokens = 0, split_tokens = 0, nps = 0;
     // chunk mode and chunk_stream.cuh: tokens of each sequence, the new ones included; the last `window` keys (0: all) and the first
-    // `sinks` are attended to; log2 of the query heads per KV head; key tiles of a split, about
+    // `sinks` are attended to; log2 of the query heads per KV head; key tiles of a split, about.  The window and a
+    // call's rows are at most 2^30: a position less the window stays within 32 bits, also that of a row before the first token
     const int32_t *lens = nullptr;
     int window = 0, sinks = 0, lg_group = 0, split_steps = 0;
     int few_rows = 0; // sequences of at most so many rows a KV head are another kernel's (chunk_few.cuh)
@@ -372,8 +373,7 @@ PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
     it.trow = seq;
     const int before = max(a.lens[seq], 0) - it.n; // position of the first new token (negative: those rows see nothing)
     const int tok0 = 2 * pr * per_tile;
-    // first key of the first row's window (whose position less the window may leave 32 bits)
-    const int low = a.window > 0 && before + tok0 >= a.window ? before + tok0 - a.window + 1 : 0;
+    const int low = a.window > 0 ? max(before + tok0 - a.window + 1, 0) : 0; // first key of the first row's window
     it.from = it.skip = it.lo = it.hi = 0;
     if (low > a.sinks) {
         it.from = (a.sinks + a.bs - 1) >> a.lg_bs;
@@ -1276,10 +1276,10 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
                         const int hidden = it.skip << a.lg_bs; // tokens between the sinks' blocks and the window's
                         const int plast = x.qpos0 + x.qlast - x.q0; // position of the tile's last row
                         const bool late = kbase + BN - 1 + hidden > x.qpos0;
-                        const bool early = a.window > 0 && plast >= a.window && plast - a.window + 1 - hidden > kbase;
+                        const bool early = a.window > 0 && plast - a.window + 1 - hidden > kbase;
                         if (late || early) {
                             const int upto = qpos + 1 - hidden - kbase;
-                            const int since = a.window > 0 && qpos >= a.window ? qpos - a.window + 1 - hidden - kbase : 0;
+                            const int since = a.window > 0 ? qpos - a.window + 1 - hidden - kbase : 0;
                             const int first = min(a.sinks, qpos + 1) - kbase;
                             // (a word of seen keys at a time: tested one by one against three bounds they cost 70 registers)
 #pragma unroll

@@ -305,3 +305,15 @@ def test_reserved_chunk_workspace_covers_smaller_calls(kv):
         assert grown == 0 if reserved else grown > 0
         assert cache.check_error() == 0
         cache.close()
+
+
+def test_windows_that_tables_exceed_are_at_most_two_to_the_thirty():
+    """A window no shorter than the tables is none; longer ones than 2^30 tokens under wider tables are refused."""
+    x = Setup([100], 4, 2, bs=32)
+    q, _ = x.queries(40)
+    wide = torch.full((1, 2 ** 25 + 8), -1, dtype=torch.int32, device="cuda")
+    call = lambda tables, window: P.paged_chunk_attention(q, x.cache, tables, x.context, packed([40]), 40, 0.1, window=window)
+    with pytest.raises(P.PagedKVError) as e:
+        call(wide, 2 ** 30 + 1)
+    assert e.value.status == -4
+    assert torch.equal(call(x.tables, 2 ** 30 + 1), call(x.tables, 0)) and torch.equal(call(x.tables, 128), call(x.tables, 0))
