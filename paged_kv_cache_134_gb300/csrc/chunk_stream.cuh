@@ -71,12 +71,6 @@ struct StreamUnit {
 };
 static_assert(sizeof(StreamUnit) == 64, "a slot");
 
-// key tiles of a split, of n in all
-PKV_DEV int stream_steps(const Args &a, int n) {
-    const int k = (n + a.split_steps - 1) / a.split_steps;
-    return k > 1 ? (n + k - 1) / k : max(n, 1);
-}
-
 PKV_DEV StreamUnit stream_unit(const Args &a, int seq, int g, int split, int h) {
     StreamUnit u;
     u.n = -1;
@@ -85,22 +79,17 @@ PKV_DEV StreamUnit stream_unit(const Args &a, int seq, int g, int split, int h) 
     const int per_tile = BM >> a.lg_group, start = a.cu[seq], n = a.cu[seq + 1] - start, q0 = g * per_tile;
     const int before = max(a.lens[seq], 0) - n; // position of the first new token (negative: those rows see nothing)
     const int p0 = before + q0;                 // of the tile's first row
-    const int low = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
-    int skip = 0;
-    u.from = u.lo = u.hi = 0;
-    if (low > a.sinks) {
-        u.from = (a.sinks + a.bs - 1) >> a.lg_bs;
-        skip = max((low >> a.lg_bs) - u.from, 0);
-        u.lo = a.sinks;
-        u.hi = low - (skip << a.lg_bs);
-    }
+    const Hidden hid = hidden_from(a, p0);
+    u.from = hid.from;
+    u.lo = hid.lo;
+    u.hi = hid.hi;
     u.h = h;
-    u.hidden = skip << a.lg_bs;
+    u.hidden = hid.skip << a.lg_bs;
     u.trow = seq;
     u.qpos0 = p0;
     u.row0 = start + q0;
     u.ntok = min(per_tile, n - q0);
-    const int end = max(p0 + u.ntok - u.hidden, 0), tiles = (end + BN - 1) / BN, per = stream_steps(a, tiles);
+    const int end = max(p0 + u.ntok - u.hidden, 0), tiles = (end + BN - 1) / BN, per = steps_per_split(a, tiles);
     u.split = split;
     u.nsplit = (tiles + per - 1) / per;
     u.k0 = split * per * BN;

@@ -360,6 +360,18 @@ PKV_DEV int steps_per_split(const Args &a, int n) {
     return k > 1 ? (n + k - 1) / k : max(n, 1);
 }
 
+// What the window hides from every row from position p0 on, of a chunk: seen block i is logical block i, or i + skip from
+// block `from` on, and of the seen keys [lo, hi) are hidden.
+struct Hidden {
+    int from, skip, lo, hi;
+};
+PKV_DEV Hidden hidden_from(const Args &a, int p0) {
+    const int low = a.window > 0 ? max(p0 - a.window + 1, 0) : 0; // first key of the first row's window
+    if (low <= a.sinks) return {0, 0, 0, 0};
+    const int from = (a.sinks + a.bs - 1) >> a.lg_bs, skip = max((low >> a.lg_bs) - from, 0);
+    return {from, skip, a.sinks, low - (skip << a.lg_bs)};
+}
+
 PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
     ChunkItem it;
     it.seq = seq;
@@ -373,14 +385,11 @@ PKV_DEV ChunkItem chunk_item(const Args &a, int seq, int pr, int split, int h) {
     it.trow = seq;
     const int before = max(a.lens[seq], 0) - it.n; // position of the first new token (negative: those rows see nothing)
     const int tok0 = 2 * pr * per_tile;
-    const int low = a.window > 0 ? max(before + tok0 - a.window + 1, 0) : 0; // first key of the first row's window
-    it.from = it.skip = it.lo = it.hi = 0;
-    if (low > a.sinks) {
-        it.from = (a.sinks + a.bs - 1) >> a.lg_bs;
-        it.skip = max((low >> a.lg_bs) - it.from, 0);
-        it.lo = a.sinks;
-        it.hi = low - (it.skip << a.lg_bs);
-    }
+    const Hidden hid = hidden_from(a, before + tok0);
+    it.from = hid.from;
+    it.skip = hid.skip;
+    it.lo = hid.lo;
+    it.hi = hid.hi;
     int end[2], n[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -630,8 +639,6 @@ __global__ void __launch_bounds__(threads_of<MODE, KV8>(), 1) attn_kernel(const 
         // the rows of a partly filled last block as plain 16-byte stores, so no slot past the sequence
         // is touched), or at the end.
         const bool isK = warp == 0;
-        constexpr int NS = 0; // (stage counts differ per ring; see ns below)
-        (void)NS;
         int ns = isK ? NKS : NVS, stage_bytes = L::STAGE, code_off = kCodeOff;
         uint8_t *ring = smem + (isK ? L::K0 : L::V0);
         uint64_t *const full = isK ? k_full : v_full;

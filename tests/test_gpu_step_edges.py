@@ -317,3 +317,20 @@ def test_windows_that_tables_exceed_are_at_most_two_to_the_thirty():
         call(wide, 2 ** 30 + 1)
     assert e.value.status == -4
     assert torch.equal(call(x.tables, 2 ** 30 + 1), call(x.tables, 0)) and torch.equal(call(x.tables, 128), call(x.tables, 0))
+
+
+@pytest.mark.parametrize("window,sinks", [(10 ** 6, 2), (200, 40)])
+@pytest.mark.parametrize("hq,hkv,kv,model,lens,new", [
+    (4, 2, "f16", "f16", [40, 3, 420], [60, 40, 20]), (8, 1, "fp8", "bf16", [700, 40, 100], [250, 90, 100]),
+    (8, 2, "bf16", "bf16", [300, 3, 900], [500, 140, 200])])
+def test_windows_under_tables_that_hold_more(hq, hkv, kv, model, lens, new, window, sinks):
+    x = Setup(lens, hq, hkv, kv=kv, model=model, seed=5, width=1 << 17)
+    q, q64 = x.queries(sum(new))
+    out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, packed(new), max(new), R.scale_of(x.d), window=window,
+                                  sinks=sinks)
+    assert x.cache.check_error() == 0
+    got, at = out.double().cpu().numpy(), 0
+    for i, (length, n) in enumerate(zip(lens, new)):
+        r = R.attend(q64[at:at + n], *x.rows(i), R.scale_of(x.d), list(range(length - n, length)), window, sinks)
+        R.check(got[at:at + n], r, model, **weights(x))
+        at += n
