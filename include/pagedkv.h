@@ -385,9 +385,9 @@ int paged_prefill_attention(const void *q, const void *k, const void *v, const i
  * tokens) sees are not read.  scale finite and > 0.  cu_seqlens as for packed_prefill_attention; L_i above the tables'
  * tokens sets PKV_DEVERR_LENGTH.  The rows of a sequence with such numbers are left as they were.
  * 16-bit and FP8 caches (PKV_EUNSUPPORTED for PKV_INT4), arithmetic as in paged_prefill_attention (weights that are
- * one fp16 to 2^-11, and to 2^-31 of the largest where they are less than 2^-20 of it), or, for sequences
- * of up to 24 rows (n_i times group), as in paged_decode_attention_mass (an E4M3 cache's bf16 outputs: weights as
- * one fp16); results agree with paged_prefill_attention's for the same rows to its tolerance.  The query heads of a
+ * one fp16 to 2^-11, and to 2^-31 of the largest where they are less than 2^-20 of it), or, for sequences of few
+ * rows (n_i times group: up to 24, 16 or 8 by the call's sizes), as in paged_decode_attention_mass (an E4M3 cache's
+ * bf16 outputs: weights as one fp16); results agree with paged_prefill_attention's for the same rows to its tolerance.  The query heads of a
  * KV head share its keys, which are cut into splits where the rows are few: boundaries depend on L_i, n_i, num_seqs,
  * total_tokens, max_seqlen, max_blocks_per_seq, window and sinks.  A NaN or infinity in V reaches the rows of its
  * sequence whose tile of rows sees that token, also the earlier ones among them; one in K only the rows that see it.

@@ -6,7 +6,7 @@
 // decode_mma.cuh's kernel with C groups of eight columns: K and V tiles travel global -> shared -> register once and
 // meet every group there (an E4M3 code is widened once for all rows).  Bound by the bytes of the cache for one group
 // and by the tiles' chains beside it (scores, exponentials, products: eight to twelve warps an SM) for more: 32
-// sequences of up to 4096 tokens, 5 new ones, 32 fp16 heads 163 us (1.01 GB, 6.2 TB/s); 256 log-normal ones of up to
+// sequences of up to 4096 tokens, 5 new ones, 32 fp16 heads 161 us (1.01 GB, 6.3 TB/s); 256 log-normal ones of up to
 // 8192, 32/8 heads, E4M3, 2 new tokens (one group) 99 us, 4 (two) 131 (455 MB).  P goes into the second product as a
 // pair hi + lo, of fp16 (2^-22; weights of the base at 2^6 and at most at 2^14, so that they stay normal numbers down
 // to 2^-20 of it) or bf16 (2^-16), or as one fp16 (2^-11) where an E4M3 cache's outputs are bf16 (2^-8); scores,

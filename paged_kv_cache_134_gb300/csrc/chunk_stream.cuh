@@ -4,6 +4,8 @@
 // The mathematics are those of prefill_impl.cuh: S = Q K^T and O += P V on tcgen05 with accumulators in tensor memory, an
 // online softmax with a base that moves only when a row's maximum passes it by more than 2^8, one thread a row.
 //
+// (Weights of one fp16, or a pair of bf16: see kChunkUp.)
+//
 // A unit is (sequence, KV head, tile of rows, split of its keys): row r is token q0 + r / G, query head h G + r % G, so a
 // KV head's keys are read once for all its query heads and all new tokens.  What bounds it is HBM (K and V once, 2 rows
 // flops a byte), as long as copies stay in flight.  One unit's chain of products and softmax (S, exponentials, P V: about

@@ -42,7 +42,8 @@
 //
 // Measured: 32 sequences of up to 4096 tokens, 32 heads (7B batch), 268 MB in 59 us, 4.5 TB/s; 256 ragged ones of up to
 // 8192, four heads to a KV head, 237 MB in 61 us, 3.9 TB/s; one of 131071 tokens, 143 MB in 37 us; 64 of up to 4096, eight
-// heads to a KV head, 40 us.  Copies alone take 48 us of the first, arithmetic on data in L2 nearly all of it: four warps a
+// heads to a KV head, 40 us.  Under a window (WIN, see Reach): of 1024 tokens and 4 sinks, the first of these 30.2 us (126 MB,
+// floor 18.9); of 511 and 1, the second 35.5 (17.2).  Copies alone take 48 us of the first, arithmetic on data in L2 nearly all of it: four warps a
 // scheduler, as many as 128 registers allow, hide the two and the dependent chain of a tile behind one another only in part.
 #pragma once
 

@@ -11,9 +11,11 @@
 // with up to four heads the lo part uses the four columns of B that are free anyway, with eight it takes a
 // second product.  For fp16 operands the largest weight so far stands at 2^14, so that weights down to 2^-28 of it
 // stay normal numbers and smaller ones lose 2^-39 of it at most (at 1, 20000 tokens beside one of e^16 times their
-// weight lost 4e-4 of their sum).  E4M3 codes widen to fp16 in registers; bf16 queries are then scaled by a power of two
-// per head so that their largest element is in [2^10, 2^11).  Each warp has its own ring of 16-token tiles,
-// filled by cp.async and swizzled on the way (no barrier between warps, no wait that could hang).
+// weight lost 4e-4 of their sum); without mass, where the base stays while scores pass it by up to 2^8, it
+// stands at 2^6: normal down to 2^-20 of it, smaller ones lose 2^-30.  E4M3 codes widen to fp16 in registers; bf16
+// queries are then scaled by a power of two per head so that their largest element is in [2^10, 2^11).  Each warp
+// has its own ring of 16-token tiles, filled by cp.async and swizzled on the way (no barrier between warps, no
+// wait that could hang).
 //
 // Measured with mass_kernel: 32 fp16 sequences of up to 4096 tokens, 32 heads, 1.02 GB in 161 us, 6.4 TB/s.
 #pragma once

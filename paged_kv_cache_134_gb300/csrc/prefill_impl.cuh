@@ -14,7 +14,10 @@
 // a prefix shared by every table (section 3.3), cut into splits whose fp32 partials a merge combines.
 // In chunk mode (paged_chunk_attention, pieces of prompts) the last n_i of a sequence's L_i cached tokens are its queries, the
 // group's query heads of a token lie side by side in a tile's rows (a KV head's keys are read once for all of them), the
-// keys may be cut into splits, and a window with sinks may hide keys: see ChunkItem.
+// keys may be cut into splits, and a window with sinks may hide keys: see ChunkItem.  512 tokens after 131071, 32/8 heads of
+// 128 (1097 GFLOP, 575 us at the measured rate): bf16 1.11 ms (the pair makes 862 us of work; tensor pipe 72 % busy), fp16
+// 0.91 (59 %), E4M3 1.04 (49 %; codes go through shared memory twice).  8 prompts of 4096 tokens, 577 us:
+// 1.17, 0.92 and 1.06; under a window of 1024, 253 us: 728, 609 and 618.
 //
 // Design (one persistent CTA per SM, items taken from an atomic counter, heaviest first):
 //  * An item is two 128-row query tiles A and B.  Packed and paged modes: consecutive tiles of one
@@ -55,7 +58,12 @@ constexpr int BN = 128;          // keys per tile (MMA N of Q K^T, K of P V)
 constexpr int kThreads = 384;    // 12 warps
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f; // log2 units
-// Chunks whose weights are fp16: a new base's weight is 2^kChunkUp and the largest 2^14, so that a weight stays a normal
+// Chunks over fp16 and E4M3 caches give their weights to P V as one fp16, as the prefill does over fp16 caches: fp16 outputs
+// come to 1.35 times their own rounding (rms; 1.00 where chunk_few.cuh takes the rows, whose weights are pairs), bf16
+// outputs to 1.006.  Pairs here: 1.00, and 28 % more time for 512 fp16 tokens after 131071 (894 us, 1145), 23 to 35 % for
+// prompts of 4096, 6 to 11 % for tiles of 25 to 128 rows (44 over E4M3).  bf16 caches' weights are pairs: one bf16
+// would cost outputs that have 2^-8 as much again.
+// Of one fp16 a new base's weight is 2^kChunkUp and the largest 2^14, so that a weight stays a normal
 // number down to 2^-20 of the base's and is nothing only below 2^-31.  (With the base at 1 those of 4000 tokens at 2^-25.2 of
 // one token's came out as nothing, an output of 1e-4 as 0; over a long split that would be 2^-8 of the sum.)
 constexpr float kChunkUp = 14.f - kRescale;

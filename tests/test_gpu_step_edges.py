@@ -334,3 +334,15 @@ def test_windows_under_tables_that_hold_more(hq, hkv, kv, model, lens, new, wind
         r = R.attend(q64[at:at + n], *x.rows(i), R.scale_of(x.d), list(range(length - n, length)), window, sinks)
         R.check(got[at:at + n], r, model, **weights(x))
         at += n
+
+
+def test_splits_of_a_million_tokens():
+    """A table for 134 million tokens: more key tiles a split than the list's classes of cost."""
+    n, hq = 2300, 16
+    x = Setup([3000], hq, 2, bs=32, width=1 << 22)
+    q, q64 = x.queries(n)
+    out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, packed([n]), n, R.scale_of(128), window=1 << 26, sinks=3)
+    assert x.cache.check_error() == 0
+    rows = np.arange(3, n, 101)
+    r = R.attend(q64[rows], *x.rows(0), R.scale_of(128), 3000 - n + rows)
+    R.check(out.double().cpu().numpy()[rows], r, "f16", **weights(x))
