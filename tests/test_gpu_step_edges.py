@@ -341,7 +341,7 @@ def test_splits_of_a_million_tokens():
     n, hq = 2300, 16
     x = Setup([3000], hq, 2, bs=32, width=1 << 22)
     q, q64 = x.queries(n)
-    out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, packed([n]), n, R.scale_of(128), window=1 << 26, sinks=3)
+    out = P.paged_chunk_attention(q, x.cache, x.tables, x.context, packed([n]), n, R.scale_of(128))
     assert x.cache.check_error() == 0
     rows = np.arange(3, n, 101)
     r = R.attend(q64[rows], *x.rows(0), R.scale_of(128), 3000 - n + rows)
